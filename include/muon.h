@@ -248,6 +248,124 @@ typedef struct muon_adamw_param {
 int muon_adamw_step(const muon_adamw_param* params, int n, int64_t t, float lr, double beta1,
                     double beta2, float eps, float weight_decay, muon_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators at a model's head: the parameters that Muon leaves to AdamW are
+ * mostly the norms and the vocabulary matrix.  These entry points compute the last
+ * part of a training step around them -- layer norm, the vocabulary projection with
+ * its loss, and an AdamW step with 8-bit moments.  The conventions above hold for
+ * them too; the pages have no counterpart for them.
+ * Strides (ld*) are in elements between rows; columns are contiguous. */
+
+/* Layer norm over the last dimension, for rows r = 0 .. rows-1:
+ *   mean = sum(x)/dim;  rstd = 1/sqrt(sum((x - mean)^2)/dim + eps);
+ *   y = (x - mean)*rstd*weight + bias.
+ * x and y are x_dtype, weight and bias w_dtype (either may be NULL: 1 and 0).  mean
+ * and rstd are fp32, one a row, and may be NULL when no backward pass follows.
+ * Arithmetic is fp32 with one rounding of y; the variance is summed from the centred
+ * values.  y may be x itself (same ld); other overlaps are not allowed.
+ * eps >= 0; dim >= 1 (below 2^31); rows == 0 is a no-op. */
+int muon_layernorm_forward(const void* x, int64_t ldx, const void* weight, const void* bias,
+                           int64_t rows, int64_t dim, int x_dtype, int w_dtype, float eps,
+                           void* y, int64_t ldy, float* mean, float* rstd, muon_stream_t stream);
+
+/* Bytes of workspace muon_layernorm_backward needs to reduce the weight's and bias's
+ * gradients; (size_t)-1 for invalid sizes. */
+size_t muon_layernorm_workspace_size(int64_t rows, int64_t dim);
+
+/* Gradient of the above.  With xh = (x - mean)*rstd and g = dy*weight:
+ *   dx = rstd*(g - sum(g)/dim - xh*sum(g*xh)/dim);
+ *   dweight = sum over rows of dy*xh;  dbias = sum over rows of dy.
+ * mean and rstd are the forward pass's.  dy and dx are x_dtype; dweight and dbias are
+ * w_dtype, overwritten, and may each be NULL; rows == 0 writes zeros to them.  The
+ * sums over rows are fp32 in a fixed order.  dx may be dy itself (same ld).  ws may
+ * be NULL when dweight and dbias both are. */
+int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                            const float* mean, const float* rstd, int64_t rows, int64_t dim,
+                            int x_dtype, int w_dtype, void* dx, int64_t lddx, void* dweight, void* dbias,
+                            void* ws, size_t ws_bytes, muon_stream_t stream);
+
+/* Softmax cross entropy of the logits z = H W^T over a vocabulary, computed in pieces
+ * so that the rows x vocab logits are never kept. */
+typedef struct muon_linear_ce {
+  const void* H;          /* device, rows x dim, dtype; the hidden states                      */
+  const void* W;          /* device, vocab x dim, dtype; the vocabulary matrix                 */
+  const int64_t* labels;  /* device, rows                                                      */
+  int64_t rows, vocab, dim; /* rows >= 0, vocab >= 1, dim >= 1, each below 2^31                */
+  int64_t ldh, ldw;       /* elements between rows of H and of W (>= dim)                      */
+  int32_t dtype;          /* of H, W and their gradients: MUON_DTYPE_F32 or MUON_DTYPE_BF16    */
+  int64_t ignore_index;   /* rows with this label carry no loss and no gradient                */
+} muon_linear_ce;
+
+/* Bytes of workspace for muon_linear_ce_forward (backward == 0) or for both passes
+ * (backward != 0) of these sizes, strides, dtype and pointers (NULL pointers count as
+ * aligned).  H or W whose rows do not start on 16-byte boundaries need room for an
+ * aligned copy.  (size_t)-1 for invalid sizes. */
+size_t muon_linear_ce_workspace_size(const muon_linear_ce* a, int backward);
+
+/* loss[r] = lse[r] - z[r, label_r] with lse[r] = log(sum_v exp(z[r, v])); loss is 0 for
+ * an ignored row, whose lse is computed all the same.  A label outside [0, vocab) that
+ * is not ignore_index makes that row's loss NaN.  stats, if not NULL: stats[0] the mean
+ * loss over the rows that are not ignored (0 if there is none), stats[1] their count.
+ * loss, lse and stats are device fp32.  Products of bf16 values are exact and summed in
+ * fp32; a NaN or +Inf logit makes the row's lse and loss NaN.  Call muon_workspace_init
+ * once on a fresh workspace; muon_check_status reports an expired wait. */
+int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, float* lse, float* stats,
+                           void* ws, size_t ws_bytes, muon_stream_t stream);
+
+/* Gradient of sum_r c_r*loss[r]:  g[r, v] = c_r*(exp(z[r, v] - lse[r]) - [v == label_r]),
+ *   dH = g W  (rows x dim, leading dimension dim),  dW = g^T H  (vocab x dim, likewise),
+ * both of a->dtype and overwritten; either may be NULL.  c_r = grad_scale * (row_grad ?
+ * row_grad[r] : 1) * (stats ? 1/max(stats[1], 1) : 1), and 0 for an ignored row and for
+ * one whose label is out of range: with the forward pass's stats this is the gradient of
+ * grad_scale times the mean loss.  The logits are computed again, by pieces of the
+ * vocabulary.  In bf16, g is rounded to bf16 before the two products, which are summed
+ * in fp32. */
+int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse, const float* row_grad,
+                            const float* stats, float grad_scale, void* dH, void* dW,
+                            void* ws, size_t ws_bytes, muon_stream_t stream);
+
+/* AdamW with both moments held in 8 bits.  Blocks of MUON_ADAMW8_BLOCK consecutive
+ * elements share one scale byte s per moment.  A code c stands for the fp32 number
+ * whose bits are (c + base) << 20, so for a float with 3 bits of mantissa:
+ *   first moment   1 sign bit and 7 bits c, base = 8*max(s - 16, 0): 15.9 binades a block;
+ *   second moment  8 bits c,                base = 8*max(s - 32, 0): 31.9 binades a block;
+ * c = 0 stands for 0, whatever s; the first moment's byte 0x80 stands for NaN.  s is the
+ * smallest that holds the block's largest value.  New moments are rounded
+ * stochastically, up with a probability equal to the remainder (16 bits), because one
+ * step moves the second moment by 1 - beta2, far less than the grid's spacing, and
+ * rounding to nearest would hold it still.  A nonzero second moment never rounds to 0
+ * (it would turn the update into m/eps): it takes code 1 at least.  The random bits
+ * depend only on (seed, t, index of the element), so a step is reproducible bit for bit.
+ * A fresh state is all zero bytes. */
+#define MUON_ADAMW8_BLOCK 128
+typedef struct muon_adamw8_param {
+  void* P;           /* device, numel elements of p_dtype; updated in place                    */
+  const void* G;     /* device, numel elements of g_dtype                                      */
+  uint8_t* m;        /* device, 16-byte aligned, ceil(numel/128)*128 codes of the first moment */
+  uint8_t* v;        /* the same for the second moment                                         */
+  uint8_t* m_scale;  /* device, ceil(numel/128) scale bytes                                    */
+  uint8_t* v_scale;
+  int64_t numel;
+  int64_t first;     /* index of the first element for the random bits: a multiple of 128; give
+                        every parameter a range of its own                                     */
+  int32_t p_dtype;   /* MUON_DTYPE_F32 or MUON_DTYPE_BF16                                      */
+  int32_t g_dtype;   /* MUON_DTYPE_F32 or MUON_DTYPE_BF16                                      */
+} muon_adamw8_param;
+
+/* The update of muon_adamw_step, from the new moments before they are rounded to 8 bits,
+ * fp32 arithmetic and one rounding to p_dtype.  Codes past numel in the last block are
+ * set to 0.  A NaN or Inf gradient makes that element's m and P NaN and leaves its
+ * block's other elements as they would be; a second moment beyond fp32 is held at its
+ * largest code.  One launch per 256 parameters; every entry uses the same dtype pair. */
+int muon_adamw8_step(const muon_adamw8_param* params, int n, int64_t t, float lr, double beta1,
+                     double beta2, float eps, float weight_decay, uint32_t seed, muon_stream_t stream);
+
+/* The values that codes stand for, as bf16 (exact): numel codes, a multiple of
+ * MUON_ADAMW8_BLOCK.  m and v 16-byte aligned, m_out and v_out 32-byte aligned; m with
+ * m_scale and m_out, or v with v_scale and v_out, may be NULL. */
+int muon_adamw8_unpack(const uint8_t* m, const uint8_t* m_scale, const uint8_t* v, const uint8_t* v_scale,
+                       int64_t numel, void* m_out, void* v_out, muon_stream_t stream);
+
 /* Synchronises `stream`, reads and clears the device status word in `ws`, and
  * returns MUON_OK or the recorded error: MUON_ERR_TIMEOUT when a bounded wait
  * expired (it takes precedence), else MUON_ERR_NONFINITE when the finite check saw

@@ -103,6 +103,16 @@ def load_library(path: Optional[str] = None):
         "muon_profile_events": (i32, [ptrs, i32]),
         "muon_adamw_step": (i32, [ctypes.POINTER(MuonAdamwParam), i32, i64, f32, ctypes.c_double, ctypes.c_double,
                                   f32, f32, vp]),
+        "muon_layernorm_forward": (i32, [vp, i64, vp, vp, i64, i64, i32, i32, f32, vp, i64, vp, vp, vp]),
+        "muon_layernorm_workspace_size": (sz, [i64, i64]),
+        "muon_layernorm_backward": (i32, [vp, i64, vp, i64, vp, vp, vp, i64, i64, i32, i32, vp, i64, vp, vp, vp, sz,
+                                          vp]),
+        "muon_linear_ce_workspace_size": (sz, [vp, i32]),
+        "muon_linear_ce_forward": (i32, [vp, vp, vp, vp, vp, sz, vp]),
+        "muon_linear_ce_backward": (i32, [vp, vp, vp, vp, f32, vp, vp, vp, sz, vp]),
+        "muon_adamw8_step": (i32, [vp, i32, i64, f32, ctypes.c_double, ctypes.c_double, f32, f32, ctypes.c_uint32,
+                                   vp]),
+        "muon_adamw8_unpack": (i32, [vp, vp, vp, vp, i64, vp, vp, vp]),
         "muon_launch_count": (i32, []),
     }
     for name, (res, args) in sig.items():

@@ -587,6 +587,19 @@ int common_checks(int n, DevInfo* di) {
 // ===========================================================================
 // exported entry points
 // ===========================================================================
+namespace muon {
+int require_device(int* num_sms) {
+  DevInfo d;
+  const int rc = device_info(&d);
+  if (rc == MUON_OK) *num_sms = d.sms;
+  return rc;
+}
+void begin_launches() { t_launches = 0; }
+void count_launch() { ++t_launches; }
+unsigned long long wait_limit_ns() { return (unsigned long long)g_timeout_ms.load() * 1000000ull; }
+int test_flags() { return g_debug_flags.load(); }
+}  // namespace muon
+
 extern "C" {
 
 int muon_abi_version(void) { return MUON_ABI_VERSION; }

@@ -373,6 +373,15 @@ cudaError_t launch_apply_ws(int w_dt, int o_dt, const ApplyWsParams& p, cudaStre
 cudaError_t launch_ns_simt(const NsParams& p, cudaStream_t s);
 cudaError_t launch_ns_tc(const NsParams& p, cudaStream_t s, int num_sms);
 
+// api.cu, for the entry points of other files: the current device's checks (a muon_status)
+// and SM count, the launch count of the calling thread's entry point, the wait limit and
+// test flags.
+int require_device(int* num_sms);
+void begin_launches();
+void count_launch();
+unsigned long long wait_limit_ns();
+int test_flags();
+
 // tensor map encoding (driver entry point obtained through the runtime)
 bool encode_tmap_bf16(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
                       uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0, uint32_t box1);

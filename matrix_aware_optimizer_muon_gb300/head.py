@@ -1,0 +1,272 @@
+"""The operators at a model's head: layer norm, linear cross entropy and AdamW with
+8-bit moments.
+
+Muon takes the blocks' matrices; the norms and the vocabulary matrix stay on AdamW.  The
+functions here (same names as the C ABI in include/muon.h) compute the part of a training
+step those parameters belong to: the norm before the vocabulary matrix, the loss over the
+vocabulary without keeping its logits, their gradients, and the update.  Like the rest of
+the package they only marshal arguments: every computation runs in the library's kernels.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Dict, List, Optional, Sequence, Tuple
+
+import numpy as np
+import torch
+
+from . import _lib
+from ._lib import _check, _dt, _stream, load_library
+
+ADAMW8_BLOCK = 128
+
+
+def _on(stream):
+    """Outputs are allocated on the stream they are written on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
+def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    """(pointer, elements between rows) of a 2-D tensor with contiguous columns."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    n, d = t.shape
+    ld, one = t.stride()
+    if d > 1 and one != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    if n > 1 and ld < d:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.data_ptr(), (ld if n > 1 else max(ld, d))
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype, name: str) -> Optional[int]:
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} elements")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    return t.data_ptr()
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+def muon_layernorm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                           bias: Optional[torch.Tensor] = None, eps: float = 1e-5, stream=None):
+    """y = (x - mean)*rstd*weight + bias over the last dimension of the 2-D x (rows may be
+    strided).  Returns (y, mean, rstd): y contiguous in x's dtype, mean and rstd fp32."""
+    px, ldx = _rows(x, "x")
+    n, d = x.shape
+    pw, pb = _vector(weight, d, None, "weight"), _vector(bias, d, weight.dtype if weight is not None else None, "bias")
+    wdt = _dt(weight if weight is not None else bias if bias is not None else x)
+    with _on(stream):
+        y = torch.empty((n, d), dtype=x.dtype, device=x.device)
+        mean = torch.empty(n, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(n, dtype=torch.float32, device=x.device)
+    _check("muon_layernorm_forward", load_library().muon_layernorm_forward(
+        px, ldx, pw, pb, n, d, _dt(x), wdt, eps, y.data_ptr(), d, mean.data_ptr(), rstd.data_ptr(), _stream(stream)))
+    return y, mean, rstd
+
+
+def alloc_layernorm_workspace(rows: int, dim: int, device=None) -> torch.Tensor:
+    """Workspace of muon_layernorm_backward for these sizes; one call at a time uses it."""
+    v = load_library().muon_layernorm_workspace_size(int(rows), int(dim))
+    if v == ctypes.c_size_t(-1).value:
+        raise _lib.MuonError("muon_layernorm_workspace_size", _lib.MUON_ERR_INVALID)
+    return torch.empty(int(v), dtype=torch.uint8, device=device or "cuda")
+
+
+def muon_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
+                            rstd: torch.Tensor, ws: Optional[torch.Tensor] = None, bias: bool = True, stream=None):
+    """Gradients of muon_layernorm_forward: (dx, dweight, dbias).  dweight is None without a
+    weight; dbias is None when bias is False."""
+    px, ldx = _rows(x, "x")
+    py, ldy = _rows(dy, "dy")
+    n, d = x.shape
+    if tuple(dy.shape) != (n, d) or dy.dtype != x.dtype:
+        raise ValueError("dy and x must have the same shape and dtype")
+    pw = _vector(weight, d, None, "weight")
+    pm, pr = _vector(mean, n, torch.float32, "mean"), _vector(rstd, n, torch.float32, "rstd")
+    wt = weight.dtype if weight is not None else x.dtype
+    with _on(stream):
+        dx = torch.empty((n, d), dtype=x.dtype, device=x.device)
+        dw = torch.empty(d, dtype=wt, device=x.device) if weight is not None else None
+        db = torch.empty(d, dtype=wt, device=x.device) if bias else None
+    _check("muon_layernorm_backward", load_library().muon_layernorm_backward(
+        py, ldy, px, ldx, pw, pm, pr, n, d, _dt(x), _dt(weight if weight is not None else x), dx.data_ptr(), d,
+        None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), _lib._ptr(ws),
+        0 if ws is None else ws.numel(), _stream(stream)))
+    return dx, dw, db
+
+
+# ---------------------------------------------------------------------------
+# linear cross entropy
+# ---------------------------------------------------------------------------
+class MuonLinearCe(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_void_p), ("W", ctypes.c_void_p), ("labels", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("ldh", ctypes.c_int64), ("ldw", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("ignore_index", ctypes.c_int64)]
+
+
+def _workspace(nbytes: int, device) -> torch.Tensor:
+    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
+    _lib.muon_workspace_init(ws)
+    return ws
+
+
+def _ce_args(h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, ignore_index: int) -> MuonLinearCe:
+    ph, ldh = _rows(h, "h")
+    pw, ldw = _rows(w, "w")
+    if h.dtype != w.dtype or h.shape[1] != w.shape[1]:
+        raise ValueError("h and w must have the same dtype and width")
+    pl = _vector(labels, h.shape[0], torch.int64, "labels")
+    return MuonLinearCe(ph, pw, pl, h.shape[0], w.shape[0], h.shape[1], ldh, ldw, _dt(h), ignore_index)
+
+
+def muon_linear_ce_workspace_size(rows: int, vocab: int, dim: int, dtype=torch.bfloat16, backward: bool = True,
+                                  ldh: Optional[int] = None, ldw: Optional[int] = None) -> int:
+    a = MuonLinearCe(None, None, None, rows, vocab, dim, ldh or dim, ldw or dim,
+                     _lib.MUON_DTYPE_F32 if dtype == torch.float32 else _lib.MUON_DTYPE_BF16, -100)
+    return _ce_workspace_size(a, backward)
+
+
+def _ce_workspace_size(a: MuonLinearCe, backward: bool) -> int:
+    v = load_library().muon_linear_ce_workspace_size(ctypes.byref(a), 1 if backward else 0)
+    if v == ctypes.c_size_t(-1).value:
+        raise _lib.MuonError("muon_linear_ce_workspace_size", _lib.MUON_ERR_INVALID)
+    return int(v)
+
+
+def linear_ce_workspace_for(h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, backward: bool = True) -> torch.Tensor:
+    """Workspace for these very tensors (their strides and alignment included)."""
+    return _workspace(_ce_workspace_size(_ce_args(h, w, labels, -100), backward), h.device)
+
+
+def alloc_linear_ce_workspace(rows: int, vocab: int, dim: int, dtype=torch.bfloat16, backward: bool = True,
+                              ldh: Optional[int] = None, ldw: Optional[int] = None, device=None) -> torch.Tensor:
+    """Workspace of muon_linear_ce_forward and, with backward, muon_linear_ce_backward.
+    ldh and ldw: elements between rows of h and w where they are not contiguous."""
+    return _workspace(muon_linear_ce_workspace_size(rows, vocab, dim, dtype, backward, ldh, ldw), device)
+
+
+def muon_linear_ce_forward(h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, ws: torch.Tensor,
+                           ignore_index: int = -100, stream=None):
+    """Cross entropy of the logits h w^T (h: rows x dim, w: vocab x dim) against int64 labels,
+    without keeping the logits.  Returns (loss, lse, stats), fp32: each row's loss (0 where
+    the label is ignore_index) and log-sum-exp, and [mean loss of the other rows, their count]."""
+    a = _ce_args(h, w, labels, ignore_index)
+    n = h.shape[0]
+    with _on(stream):
+        loss = torch.empty(n, dtype=torch.float32, device=h.device)
+        lse = torch.empty(n, dtype=torch.float32, device=h.device)
+        stats = torch.empty(2, dtype=torch.float32, device=h.device)
+    _check("muon_linear_ce_forward", load_library().muon_linear_ce_forward(
+        ctypes.byref(a), loss.data_ptr(), lse.data_ptr(), stats.data_ptr(), _lib._ptr(ws), ws.numel(), _stream(stream)))
+    return loss, lse, stats
+
+
+def muon_linear_ce_backward(h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor,
+                            ws: torch.Tensor, row_grad: Optional[torch.Tensor] = None,
+                            stats: Optional[torch.Tensor] = None, grad_scale: float = 1.0, ignore_index: int = -100,
+                            need_dh: bool = True, need_dw: bool = True, stream=None):
+    """(dh, dw) of sum_r c_r*loss[r], c_r = grad_scale * row_grad[r] / stats[1] (each factor 1
+    where it is None): with the forward pass's stats, the gradient of the mean loss."""
+    a = _ce_args(h, w, labels, ignore_index)
+    n = h.shape[0]
+    pl = _vector(lse, n, torch.float32, "lse")
+    pg, ps = _vector(row_grad, n, torch.float32, "row_grad"), _vector(stats, 2, torch.float32, "stats")
+    with _on(stream):
+        dh = torch.empty((n, h.shape[1]), dtype=h.dtype, device=h.device) if need_dh else None
+        dw = torch.empty(tuple(w.shape), dtype=w.dtype, device=h.device) if need_dw else None
+    _check("muon_linear_ce_backward", load_library().muon_linear_ce_backward(
+        ctypes.byref(a), pl, pg, ps, grad_scale, None if dh is None else dh.data_ptr(),
+        None if dw is None else dw.data_ptr(), _lib._ptr(ws), ws.numel(), _stream(stream)))
+    return dh, dw
+
+
+# ---------------------------------------------------------------------------
+# AdamW with 8-bit moments
+# ---------------------------------------------------------------------------
+_PARAM8 = np.dtype([("P", "u8"), ("G", "u8"), ("m", "u8"), ("v", "u8"), ("m_scale", "u8"), ("v_scale", "u8"),
+                    ("numel", "i8"), ("first", "i8"), ("p_dtype", "i4"), ("g_dtype", "i4")])
+
+
+class AdamW8:
+    """AdamW over a list of parameters, both moments in 8 bits (see muon_adamw8_step in
+    include/muon.h for the format).  The state is four flat byte buffers, 2 + 2/128 bytes a
+    parameter; parameter i's codes start at self.starts[i], a multiple of 128."""
+
+    def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-4, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.0, seed: int = 0):
+        self.params: List[torch.Tensor] = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        self.lr, self.betas, self.eps, self.weight_decay, self.seed = lr, betas, eps, weight_decay, int(seed) & 0xFFFFFFFF
+        self.numels = [p.numel() for p in self.params]
+        blocks = [-(-n // ADAMW8_BLOCK) for n in self.numels]
+        self.starts = [ADAMW8_BLOCK * b for b in np.concatenate([[0], np.cumsum(blocks)]).tolist()]
+        dev, total = self.params[0].device, self.starts[-1]
+        self.m, self.v = (torch.zeros(total, dtype=torch.uint8, device=dev) for _ in range(2))
+        self.m_scale, self.v_scale = (torch.zeros(total // ADAMW8_BLOCK, dtype=torch.uint8, device=dev) for _ in range(2))
+        self.step_count = 0
+        self._arr = np.zeros(len(self.params), dtype=_PARAM8)
+        at = np.array(self.starts[:-1], dtype=np.int64)
+        self._arr["m"], self._arr["v"] = self.m.data_ptr() + at, self.v.data_ptr() + at
+        self._arr["m_scale"] = self.m_scale.data_ptr() + at // ADAMW8_BLOCK
+        self._arr["v_scale"] = self.v_scale.data_ptr() + at // ADAMW8_BLOCK
+        self._arr["numel"], self._arr["first"] = self.numels, at
+        self._arr["p_dtype"] = self._pointers(self.params, "P")
+
+    def _pointers(self, tensors: Sequence[torch.Tensor], field: str) -> int:
+        """Fills one pointer column after checking the tensors; returns their dtype."""
+        if len(tensors) != len(self.numels):
+            raise ValueError("one gradient per parameter")
+        dt = tensors[0].dtype
+        for t, n in zip(tensors, self.numels):
+            if t.dtype != dt:
+                raise ValueError("all parameters, and all gradients, have one dtype")
+            if t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError("parameters and gradients are contiguous CUDA tensors of the same size")
+        self._arr[field] = [t.data_ptr() for t in tensors]
+        return _dt(tensors[0])
+
+    def step(self, grads: Sequence[torch.Tensor], stream=None) -> None:
+        """One asynchronous step."""
+        self._arr["g_dtype"] = self._pointers(grads, "G")
+        self._pointers(self.params, "P")
+        _check("muon_adamw8_step", load_library().muon_adamw8_step(
+            self._arr.ctypes.data, len(self.params), self.step_count + 1, self.lr, self.betas[0], self.betas[1],
+            self.eps, self.weight_decay, self.seed, _stream(stream)))
+        self.step_count += 1
+
+    def moments(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """The values the codes of both moments stand for, as flat bf16 tensors (exact)."""
+        with _on(stream):
+            out = torch.empty((2, self.m.numel()), dtype=torch.bfloat16, device=self.m.device)
+        m, v = out[0], out[1]
+        _check("muon_adamw8_unpack", load_library().muon_adamw8_unpack(
+            self.m.data_ptr(), self.m_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr(), self.m.numel(),
+            m.data_ptr(), v.data_ptr(), _stream(stream)))
+        return m, v
+
+    def state_dict(self) -> Dict:
+        return {"step": self.step_count, "seed": self.seed, "m": self.m.clone(), "v": self.v.clone(),
+                "m_scale": self.m_scale.clone(), "v_scale": self.v_scale.clone()}
+
+    def load_state_dict(self, sd: Dict) -> None:
+        mine = (self.m, self.v, self.m_scale, self.v_scale)
+        theirs = [sd[k] for k in ("m", "v", "m_scale", "v_scale")]
+        if any(a.shape != b.shape or b.dtype != torch.uint8 for a, b in zip(mine, theirs)):
+            raise ValueError("state was saved for other parameters")
+        for a, b in zip(mine, theirs):
+            a.copy_(b)
+        self.step_count, self.seed = int(sd["step"]), int(sd["seed"])

@@ -6,6 +6,7 @@ from typing import Dict, List, Sequence
 import torch
 
 from . import _lib
+from .head import AdamW8
 
 
 class PeriodicMuon:
@@ -18,14 +19,21 @@ class PeriodicMuon:
     def __init__(self, params: Sequence[torch.Tensor], K: int = 3, gamma: float = 0.15, mu: float = 0.95,
                  eta: float = 0.02, lam: float = 0.01, ns5_mode: str = "bf16",
                  aux_params: Sequence[torch.Tensor] = (), aux_lr: float = 1e-4, betas=(0.9, 0.999),
-                 eps: float = 1e-8):
+                 eps: float = 1e-8, aux_bits: int = 32, aux_seed: int = 0):
         """aux_params: parameters Muon does not take (biases, norms, out-of-block weights);
-        they are updated by AdamW with learning rate aux_lr and the shared weight decay lam."""
+        they are updated by AdamW with learning rate aux_lr and the shared weight decay lam.
+        aux_bits: 32, or 8 to hold AdamW's moments in 8 bits (aux_seed seeds their rounding)."""
         self.params: List[torch.Tensor] = list(params)
         self.aux = list(aux_params)
         self.aux_lr, self.betas, self.eps = aux_lr, betas, eps
-        self.aux_m = [torch.zeros(p.numel(), dtype=torch.float32, device=p.device) for p in self.aux]
-        self.aux_v = [torch.zeros(p.numel(), dtype=torch.float32, device=p.device) for p in self.aux]
+        if aux_bits not in (8, 32):
+            raise ValueError("aux_bits is 8 or 32")
+        self.aux8 = None
+        if aux_bits == 8 and self.aux:
+            self.aux8 = AdamW8(self.aux, aux_lr, betas, eps, lam, aux_seed)
+        wide = [] if aux_bits == 8 else self.aux
+        self.aux_m = [torch.zeros(p.numel(), dtype=torch.float32, device=p.device) for p in wide]
+        self.aux_v = [torch.zeros(p.numel(), dtype=torch.float32, device=p.device) for p in wide]
         if not self.params:
             raise ValueError("no parameters")
         self.K, self.gamma, self.mu, self.eta, self.lam, self.ns5_mode = K, gamma, mu, eta, lam, ns5_mode
@@ -51,6 +59,12 @@ class PeriodicMuon:
         if self.aux:
             if len(aux_grads) != len(self.aux):
                 raise ValueError("one gradient per auxiliary parameter")
+        if self.aux8 is not None:
+            # the schedule of learning rate and decay is the caller's, as for 32 bits
+            self.aux8.lr, self.aux8.betas, self.aux8.eps, self.aux8.weight_decay = self.aux_lr, self.betas, self.eps, self.lam
+            self.aux8.step_count = self.step_count
+            self.aux8.step([g.contiguous() for g in aux_grads], stream=stream)
+        elif self.aux:
             _lib.muon_adamw_step([p.view(-1) for p in self.aux], [g.reshape(-1) for g in aux_grads], self.aux_m,
                                  self.aux_v, self.step_count + 1, self.aux_lr, self.betas[0], self.betas[1],
                                  self.eps, self.lam, stream=stream)
@@ -63,6 +77,7 @@ class PeriodicMuon:
     def state_dict(self) -> Dict:
         return {"step": self.step_count, "M": [m.detach().clone() for m in self.M],
                 "aux_m": [m.detach().clone() for m in self.aux_m], "aux_v": [v.detach().clone() for v in self.aux_v],
+                "aux8": None if self.aux8 is None else self.aux8.state_dict(),
                 "hyper": dict(K=self.K, gamma=self.gamma, mu=self.mu, eta=self.eta, lam=self.lam,
                               ns5_mode=self.ns5_mode)}
 
@@ -79,8 +94,12 @@ class PeriodicMuon:
         aux_m, aux_v = sd.get("aux_m", []), sd.get("aux_v", [])
         if len(aux_m) != len(self.aux_m) or len(aux_v) != len(self.aux_v):
             raise ValueError("state has a different number of auxiliary parameters")
+        if (sd.get("aux8") is None) != (self.aux8 is None):
+            raise ValueError("state was saved with another aux_bits")
         for dst, src in zip(self.M + self.aux_m + self.aux_v, list(sd["M"]) + list(aux_m) + list(aux_v)):
             if tuple(dst.shape) != tuple(src.shape):
                 raise ValueError("state shape mismatch")
             dst.copy_(src)
+        if self.aux8 is not None:
+            self.aux8.load_state_dict(sd["aux8"])
         self.step_count = int(sd["step"])
