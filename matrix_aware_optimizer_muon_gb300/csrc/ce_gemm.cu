@@ -1,0 +1,472 @@
+// The products of the linear cross entropy on the sm_103a tensor cores (tcgen05, TMEM,
+// TMA), with the softmax fused into their epilogues.
+//
+// A 2-CTA cluster (cta_group::2) computes a 256 x 256 output tile; each CTA stages its
+// 128 rows of A and 128 rows of B (32 KB a K step of 64).  320 threads a CTA:
+//   warp 0      TMA producer (one lane), a ring of STAGES K steps;
+//   warp 1      tensor-memory allocation; in the even CTA one lane issues the MMAs;
+//   warps 2..9  epilogue, two per TMEM lane quarter, 128 of the 256 columns each: a
+//               thread owns one row, so a row's max and sum need no shuffles.
+// Two 256-column fp32 accumulators: the epilogue of a tile overlaps the next one's MMAs.
+//
+// One launch runs up to three products (jobs) over one list of tiles.  The backward
+// pass multiplies g of piece i twice (dH and dW) while it computes g of piece i+1, so
+// the short lists of dH tiles never leave SMs idle at the end of a launch of their own.
+//
+// The tensor cores add to the fp32 accumulator with truncation; its bias grows with the
+// number of K steps (measured: 2.3e-7 of a sum of 256 bf16 products, 1e-6 of 1024,
+// 9e-6 of 8192).  The kPromote form takes the accumulator over into registers every
+// seg_kb K steps and adds there with rounding to nearest.  It serves the logits of the
+// forward pass, whose loss is fp32, and every product of 32-bit operands; sums that
+// are rounded to bf16 (2e-3) do without.
+//
+// 32-bit operands come as three bf16 parts (24 bits of mantissa); the six products of
+// parts down to 2^-16 of the leading one are summed, smallest first.
+#include <map>
+#include <mutex>
+
+#include "ce.h"
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace muon {
+namespace ce {
+namespace {
+
+constexpr int HALF = TILE / 2;
+constexpr int OP_BYTES = HALF * BK * 2;        // one operand's 128 rows of a K step
+constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int STAGES = 6;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int CHUNKS = 4;                      // 32-column chunks of an epilogue warp
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 256;
+
+struct Tile {
+  int job, tm, tn, split;
+};
+
+__device__ __forceinline__ Tile decode(const Params& p, int t) {
+  Tile ti;
+  int j = 0;
+  while (j + 1 < p.njobs && p.job[j + 1].begin <= t) ++j;
+  const Job& J = p.job[j];
+  ti.job = j;
+  int r = t - J.begin;
+  const int per = J.mtiles * J.ntiles;
+  ti.split = r / per;
+  r -= ti.split * per;
+  const int g = r / (J.group * J.ntiles);
+  const int rows = min(J.group, J.mtiles - g * J.group);
+  r -= g * J.group * J.ntiles;
+  ti.tn = r / rows;
+  ti.tm = g * J.group + (r - ti.tn * rows);
+  return ti;
+}
+
+// The pair's k-th tile, or -1.
+__device__ __forceinline__ int tile_at(const Params& p, int pair, int npairs, int k) {
+  if (p.ordered) {
+    const int i = p.start[pair] + k;
+    return i < p.start[pair + 1] ? p.order[i] : -1;
+  }
+  const int t = pair + k * npairs;
+  return t < p.tiles ? t : -1;
+}
+
+__device__ __forceinline__ int segments(const Job& J, int nterms) {
+  return nterms * ((J.nkb + J.seg_kb - 1) / J.seg_kb);
+}
+
+// Bounded wait: on expiry the status word and the CTA's abort flag are set and every
+// role leaves its loop.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const Params& p,
+                                         bool honor_abort) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  while (true) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (honor_abort && *abort_flag) return false;
+    if (ptx::globaltimer() - t0 > p.timeout_ns) {
+      *abort_flag = 1;
+      atomicOr(p.status, DEV_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// 32 consecutive results of one row: cols of them are inside the matrix.
+template <typename T>
+__device__ __forceinline__ void store_row(T* dst, const float (&v)[32], int cols, int vec) {
+  if (cols >= 32 && vec) {
+    if (sizeof(T) == 2) {
+      uint32_t w[16];
+#pragma unroll
+      for (int h = 0; h < 16; ++h) w[h] = pack_bf16x2(v[2 * h], v[2 * h + 1]);
+      if (vec == 2) {
+        st_v8(dst, w);
+        st_v8(reinterpret_cast<uint8_t*>(dst) + 32, w + 8);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          reinterpret_cast<uint4*>(dst)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        reinterpret_cast<float4*>(dst)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < cols) st1(dst + j, v[j]);
+  }
+}
+
+// Row constants of a GRAD tile: c (0 for a row without gradient), lse and the label's
+// column inside the piece.
+struct RowIn {
+  float c, lse;
+  long long label;
+};
+__device__ __forceinline__ RowIn row_in(const Params& p, int r) {
+  const long long lab = p.labels[r];
+  RowIn x;
+  x.lse = p.lse[r];
+  x.label = lab - p.v0;
+  float c = p.scale;
+  if (p.row_grad) c *= p.row_grad[r];
+  if (p.stats) c /= fmaxf(p.stats[1], 1.f);
+  x.c = (lab == p.ignore || lab < 0 || lab >= p.vocab) ? 0.f : c;
+  // a row without gradient gives zeros even where its logits or lse are not finite
+  if (lab == p.ignore || lab < 0 || lab >= p.vocab) x.lse = INFINITY;
+  return x;
+}
+
+__device__ __forceinline__ void finish_grad(const Params& p, const Job& J, int r, int c0, float (&v)[32],
+                                            const RowIn& x) {
+  if (r >= J.m || c0 >= J.n) return;
+  const bool dead = x.lse == INFINITY && x.c == 0.f;
+  const int at = x.label >= c0 && x.label < c0 + 32 ? (int)(x.label - c0) : -1;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    float e = __expf(v[j] - x.lse);
+    if (j == at) e -= 1.f;
+    v[j] = dead ? 0.f : x.c * e;
+  }
+  bf16* dst = static_cast<bf16*>(J.out) + (size_t)r * J.ldo + c0;
+  store_row(dst, v, J.n - c0, 2);
+  for (int q = 1; q < p.parts; ++q) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+    store_row(dst + q * J.part_stride, v, J.n - c0, 2);
+  }
+}
+
+__device__ __forceinline__ void finish_sum(const Params& p, const Job& J, int split, int r, int c0, float (&v)[32]) {
+  if (r >= J.m || c0 >= J.n) return;
+  const int cols = J.n - c0;
+  if (J.kind == DH && J.acc) {
+    float* a = J.acc + ((size_t)split * J.m + r) * J.ldacc + c0;
+    if (!J.first) {
+      if (cols >= 32) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[8];
+          ld_v8(a + 8 * q, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[8 * q + j] += __uint_as_float(w[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j < cols) v[j] += a[j];
+      }
+    }
+    if (!J.last || !J.out) {
+      store_row(a, v, cols, 2);
+      return;
+    }
+  }
+  if (p.f32_out) store_row(static_cast<float*>(J.out) + (size_t)r * J.ldo + c0, v, cols, J.vec);
+  else store_row(static_cast<bf16*>(J.out) + (size_t)r * J.ldo + c0, v, cols, J.vec);
+}
+
+// Max, sum of exponentials and the label's logit over this thread's 128 columns.
+__device__ __forceinline__ void finish_logits(const Params& p, const Job& J, const Tile& ti, int half, int r, int cbase,
+                                              const float (&acc)[CHUNKS][32]) {
+  if (r >= J.m) return;
+  const int cols = J.n - cbase;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k)
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (k * 32 + j < cols) mx = fmaxf(mx, acc[k][j]);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k) {
+    float q = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (k * 32 + j < cols) q += __expf(acc[k][j] - ref);
+    s += q;
+  }
+  p.part[(size_t)r * (2 * J.ntiles) + 2 * ti.tn + half] = make_float2(mx, s);
+  const long long at = p.labels[r] - cbase;
+  if (at >= 0 && at < HALF && at < cols) {
+    float z = 0.f;
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k)
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (k * 32 + j == (int)at) z = acc[k][j];
+    p.zlabel[r] = z;
+  }
+}
+
+template <bool kPromote>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* mdone = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)ptx::cluster_ctarank();
+  const bool even = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&tfull[a], 1);
+      ptx::mbar_init(&tempty[a], 2 * EPI_WARPS);
+    }
+    ptx::mbar_init(mdone, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(tmem_slot, TMEM_COLS);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    if (lane == 0 && !(p.debug_flags & MUON_DEBUG_STALL_PRODUCER)) {
+      for (int j = 0; j < p.njobs; ++j) {
+        ptx::prefetch_tmap(&p.job[j].a);
+        ptx::prefetch_tmap(&p.job[j].b);
+      }
+      int stage = 0;
+      uint32_t phase = 0, pending = 0, pend_phase = 0;
+      bool stop = false;
+      for (int i = 0, t; !stop && (t = tile_at(p, pair, npairs, i)) >= 0; ++i) {
+        const Tile ti = decode(p, t);
+        const Job& J = p.job[ti.job];
+        const int m0 = ti.tm * TILE + rank * HALF;
+        const int n0 = ti.tn * TILE + rank * HALF + J.b_n0;
+        const int kbase = ti.split * J.nkb;
+        for (int term = 0; term < p.nterms && !stop; ++term) {
+          const int za = p.ta[term], zb = p.tb[term];
+          for (int kb = 0; kb < J.nkb; ++kb) {
+            if (!wait_for(&empty[stage], phase ^ 1u, abort_flag, p, true)) { stop = true; break; }
+            const uint32_t fb = ptx::mapa_shared(ptx::smem_addr(&full[stage]), 0);
+            if (even) ptx::mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
+            const uint32_t sa = ptx::smem_addr(smem + stage * STAGE_BYTES);
+            const uint32_t sb = sa + OP_BYTES;
+            const int ka = (kbase + kb) * BK, kbk = ka + J.b_k0;
+            if (J.a_mn) {
+              ptx::tma_load_3d_pair(sa, &J.a, fb, m0, ka, za);
+              ptx::tma_load_3d_pair(sa + OP_BYTES / 2, &J.a, fb, m0 + 64, ka, za);
+            } else {
+              ptx::tma_load_3d_pair(sa, &J.a, fb, ka, m0, za);
+            }
+            if (J.b_mn) {
+              ptx::tma_load_3d_pair(sb, &J.b, fb, n0, kbk, zb);
+              ptx::tma_load_3d_pair(sb + OP_BYTES / 2, &J.b, fb, n0 + 64, kbk, zb);
+            } else {
+              ptx::tma_load_3d_pair(sb, &J.b, fb, kbk, n0, zb);
+            }
+            pending |= 1u << stage;
+            pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          }
+        }
+      }
+      // Every issued copy lands before a CTA leaves.  The even CTA's barriers count both
+      // CTAs' copies; the odd CTA waits for it at the cluster barrier.
+      if (even)
+        for (int s = 0; s < STAGES; ++s)
+          if (pending & (1u << s)) wait_for(&full[s], (pend_phase >> s) & 1u, abort_flag, p, false);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (even && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int it = 0;   // accumulator uses
+      bool stop = false;
+      for (int i = 0, t; !stop && (t = tile_at(p, pair, npairs, i)) >= 0; ++i) {
+        const Tile ti = decode(p, t);
+        const Job& J = p.job[ti.job];
+        const uint32_t idesc = ptx::idesc_bf16_f32(TILE, TILE, J.a_mn, J.b_mn);
+        // K-major: 8-row groups 1024 B apart, a K step of 16 is 32 B.  MN-major: atoms of
+        // 64 rows 8 KB apart, 8-K groups 1024 B apart, a K step of 16 is 2 KB.
+        const uint32_t a_lbo = J.a_mn ? OP_BYTES / 2 : 16, a_step = J.a_mn ? 2048 : 32;
+        const uint32_t b_lbo = J.b_mn ? OP_BYTES / 2 : 16, b_step = J.b_mn ? 2048 : 32;
+        const int total = p.nterms * J.nkb;
+        int in_term = 0;
+        for (int kb = 0; kb < total && !stop;) {
+          const int run = min(J.seg_kb, J.nkb - in_term);
+          const int acc = it & 1;
+          if (!wait_for(&tempty[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, p, true)) { stop = true; break; }
+          ptx::tc_fence_after();
+          const uint32_t d = tmem_base + (uint32_t)(acc * TILE);
+          for (int q = 0; q < run; ++q) {
+            if (!wait_for(&full[stage], phase, abort_flag, p, true)) { stop = true; break; }
+            ptx::tc_fence_after();
+            const uint32_t sa = ptx::smem_addr(smem + stage * STAGE_BYTES);
+            const uint32_t sb = sa + OP_BYTES;
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              ptx::mma_bf16_pair(d, ptx::smem_desc_sw128(sa + k * a_step, a_lbo, 1024),
+                                 ptx::smem_desc_sw128(sb + k * b_step, b_lbo, 1024), idesc, (q > 0 || k > 0) ? 1u : 0u);
+            ptx::mma_commit_pair_mc(&empty[stage], 3);
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          }
+          if (stop) break;
+          ptx::mma_commit_pair_mc(&tfull[acc], 3);
+          ++it;
+          kb += run;
+          in_term += run;
+          if (in_term == J.nkb) in_term = 0;
+        }
+      }
+      // all issued MMAs complete before either CTA releases its tensor memory
+      ptx::mma_commit_pair_mc(mdone, 1);
+      wait_for(mdone, 0, abort_flag, p, false);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    int it = 0;
+    bool stop = false;
+    for (int i = 0, t; !stop && (t = tile_at(p, pair, npairs, i)) >= 0; ++i) {
+      const Tile ti = decode(p, t);
+      const Job& J = p.job[ti.job];
+      const int r = ti.tm * TILE + rank * HALF + quarter * 32 + lane;
+      const int cbase = ti.tn * TILE + half * HALF;
+      RowIn x = {};
+      if (J.kind == GRAD && r < J.m) x = row_in(p, r);
+      const int nseg = kPromote ? segments(J, p.nterms) : 1;
+      float acc[kPromote ? CHUNKS : 1][32];
+      for (int seg = 0; seg < nseg; ++seg, ++it) {
+        const int a = it & 1;
+        int ok = 1;
+        if (lane == 0) ok = wait_for(&tfull[a], (uint32_t)(it >> 1) & 1u, abort_flag, p, true) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, ok, 0)) { stop = true; break; }
+        ptx::tc_fence_after();
+        const uint32_t tb = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(a * TILE + half * HALF);
+#pragma unroll
+        for (int k = 0; k < CHUNKS; ++k) {
+          if constexpr (kPromote) {
+            ptx::tmem_add_32x32b_x16(tb + k * 32, acc[k], seg == 0);
+            ptx::tmem_add_32x32b_x16(tb + k * 32 + 16, acc[k] + 16, seg == 0);
+          } else {
+            float v[32];
+            ptx::tmem_ld_32x32b_x32(tb + k * 32, v);
+            if (J.kind == GRAD) finish_grad(p, J, r, cbase + k * 32, v, x);
+            else finish_sum(p, J, ti.split, r, cbase + k * 32, v);
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (even) ptx::mbar_arrive(&tempty[a]);
+          else ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&tempty[a]), 0));
+        }
+      }
+      if constexpr (kPromote) {
+        if (!stop && J.kind == LOGITS) {
+          finish_logits(p, J, ti, half, r, cbase, acc);
+        } else if (!stop) {
+#pragma unroll
+          for (int k = 0; k < CHUNKS; ++k) {
+            if (J.kind == GRAD) finish_grad(p, J, r, cbase + k * 32, acc[k], x);
+            else finish_sum(p, J, ti.split, r, cbase + k * 32, acc[k]);
+          }
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  ptx::cluster_sync();   // no CTA leaves while its pair may still read its shared memory
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+std::mutex g_mu;
+std::map<int, int> g_pairs;   // device -> CTA pairs that run at once
+
+}  // namespace
+
+cudaError_t prepare() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_pairs.count(dev)) return cudaSuccess;
+  if ((e = cudaFuncSetAttribute(ce_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess)
+    return e;
+  if ((e = cudaFuncSetAttribute(ce_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM;
+  int clusters = 0;
+  if ((e = cudaOccupancyMaxActiveClusters(&clusters, ce_kernel<true>, &cfg)) != cudaSuccess) return e;
+  g_pairs[dev] = clusters < MAX_PAIRS ? clusters : MAX_PAIRS;
+  return cudaSuccess;
+}
+
+int pairs() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lk(g_mu);
+  auto it = g_pairs.find(dev);
+  return it == g_pairs.end() ? 0 : it->second;
+}
+
+cudaError_t launch(const Params& p, bool promote, cudaStream_t s) {
+  if (p.tiles <= 0) return cudaSuccess;
+  const int n = pairs();
+  if (n < 1) return cudaErrorInvalidConfiguration;
+  const int grid = 2 * (p.tiles < n ? p.tiles : n);
+  if (promote) ce_kernel<true><<<grid, THREADS, SMEM, s>>>(p);
+  else ce_kernel<false><<<grid, THREADS, SMEM, s>>>(p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace ce
+}  // namespace muon

@@ -78,6 +78,19 @@ __device__ __forceinline__ void cvt4(const uint2& r, float v[4]) {
   v[3] = __uint_as_float(r.y & 0xFFFF0000u);
 }
 
+// 256-bit global accesses (32-byte aligned): a row-per-lane chunk of 64 bytes in two
+// instructions instead of four, so half the L1 requests for the same bytes.
+__device__ __forceinline__ void ld_v8(const void* src, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(src));
+}
+__device__ __forceinline__ void st_v8(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // element-wise (unaligned / ragged) access
 template <typename T> __device__ __forceinline__ float ld1(const T* p) { return to_f32(*p); }
 template <typename T> __device__ __forceinline__ void st1(T* p, float v) { *p = from_f32<T>(v); }

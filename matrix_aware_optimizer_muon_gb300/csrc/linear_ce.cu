@@ -1,167 +1,145 @@
 // Softmax cross entropy of the logits z = H W^T, without keeping the logits.
 //
-//   forward:  per piece of the vocabulary, max and sum of exponentials of each row;
-//             lse = max + log(sum), joined over the pieces; loss = lse - z[label].
+//   forward:  per row and 128 columns of the vocabulary, max and sum of exponentials
+//             (in the product's epilogue); lse = max + log(sum) joined over them;
+//             loss = lse - z[label].
 //   backward: g = c (exp(z - lse) - onehot) by pieces of the vocabulary;
 //             dH += g W_piece,  dW_piece = g^T H.
+//
+// The products run in ce_gemm.cu; here are the plan of a call, the join and the copies
+// that bring operands into a layout TMA can read.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
+#include "ce.h"
 #include "common.cuh"
-#include "internal.h"
 
 namespace muon {
 namespace ce {
+namespace {
 
-constexpr int BT = 64, BKS = 16, THREADS = 256;   // 64 x 64 tile, 4 x 4 a thread
-constexpr int64_t PIECE = 4096;                   // vocabulary columns of one backward piece
+constexpr size_t HEADER = 256;     // status word, join ticket
+constexpr int TICKET_WORD = 16;    // of the header
 
-struct Gemm {
-  // C[i, j] = sum_k A[i*sai + k*sak] * B[j*sbj + k*sbk], i < m, j < n, k < kk
-  const void *A, *B;
-  long long sai, sak, sbj, sbk;
-  long long m, n, kk;
-  // LOGITS epilogues
-  const int64_t* labels;
-  long long v0, vocab, ignore;
-  float2* part;          // FWD: [column tiles][m]
-  float* zlabel;         // FWD
-  const float *lse, *row_grad, *stats;
-  float scale;
-  void* out;             // GRAD: fp32 g; DH: fp32 running sum; DW: result
-  long long ldo;
-  void* fin;             // DH: result, on the last piece
-  int first, last;
-};
-enum { FWD = 0, GRAD = 1, DH = 2, DW = 3 };
+// A piece's g is rows x piece bf16 (three times that for 32-bit operands), twice: one
+// piece is multiplied while the next is computed.
+constexpr int64_t G_BYTES = 96 << 20;
+constexpr int64_t MIN_PIECE = 2048;
+constexpr int MAX_SPLITS = 16;
+// K steps (of 64) between take-overs of the tensor cores' sums into registers.
+constexpr int SEG_BF16 = 8, SEG_F32 = 4;
 
-template <int kEpi, typename TA, typename TB, typename TO>
-__global__ void __launch_bounds__(THREADS) gemm_kernel(const Gemm p) {
-  __shared__ float As[BKS][BT + 1], Bs[BKS][BT + 1];
-  __shared__ float2 red[BT][17];
-  const long long i0 = (long long)blockIdx.y * BT, j0 = (long long)blockIdx.x * BT;
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const TA* A = static_cast<const TA*>(p.A);
-  const TB* B = static_cast<const TB*>(p.B);
-  float acc[4][4] = {};
-  for (long long k0 = 0; k0 < p.kk; k0 += BKS) {
-    for (int t = threadIdx.x; t < BT * BKS; t += THREADS) {
-      int i, k;
-      if (p.sak == 1) { i = t / BKS; k = t % BKS; } else { i = t % BT; k = t / BT; }
-      As[k][i] = (i0 + i < p.m && k0 + k < p.kk) ? ld1(A + (i0 + i) * p.sai + (k0 + k) * p.sak) : 0.f;
-      if (p.sbk == 1) { i = t / BKS; k = t % BKS; } else { i = t % BT; k = t / BT; }
-      Bs[k][i] = (j0 + i < p.n && k0 + k < p.kk) ? ld1(B + (j0 + i) * p.sbj + (k0 + k) * p.sbk) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < BKS; ++k) {
-      float a[4], b[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) { a[u] = As[k][ty * 4 + u]; b[u] = Bs[k][tx * 4 + u]; }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) acc[u][w] = fmaf(a[u], b[w], acc[u][w]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const long long i = i0 + ty * 4 + u;
-    if (kEpi == FWD) {
-      float mx = -INFINITY, s = 0.f;
-      const long long lab = i < p.m ? p.labels[i] : -1;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const long long j = j0 + tx * 4 + w;
-        if (j < p.n) mx = fmaxf(mx, acc[u][w]);
-        if (j < p.n && i < p.m && j == lab) p.zlabel[i] = acc[u][w];
-      }
-      const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        if (j0 + tx * 4 + w < p.n) s += expf(acc[u][w] - ref);
-      red[ty * 4 + u][tx] = make_float2(mx, s);
-    } else if (kEpi == GRAD) {
-      if (i >= p.m) continue;
-      const long long lab = p.labels[i];
-      float c = p.scale;
-      if (p.row_grad) c *= p.row_grad[i];
-      if (p.stats) c /= fmaxf(p.stats[1], 1.f);
-      const bool counted = lab != p.ignore && lab >= 0 && lab < p.vocab;
-      for (int w = 0; w < 4; ++w) {
-        const long long j = j0 + tx * 4 + w;
-        if (j >= p.n) continue;
-        const float g = counted ? c * (expf(acc[u][w] - p.lse[i]) - (p.v0 + j == lab ? 1.f : 0.f)) : 0.f;
-        static_cast<float*>(p.out)[i * p.ldo + j] = g;
-      }
-    } else {
-      for (int w = 0; w < 4; ++w) {
-        const long long j = j0 + tx * 4 + w;
-        if (i >= p.m || j >= p.n) continue;
-        if (kEpi == DH) {
-          float* o = static_cast<float*>(p.out) + i * p.ldo + j;
-          const float v = acc[u][w] + (p.first ? 0.f : *o);
-          if (p.last) st1(static_cast<TO*>(p.fin) + i * p.ldo + j, v);
-          else *o = v;
-        } else {
-          st1(static_cast<TO*>(p.out) + i * p.ldo + j, acc[u][w]);
-        }
-      }
-    }
-  }
-  if (kEpi == FWD) {
-    __syncthreads();
-    if (threadIdx.x < BT && i0 + threadIdx.x < p.m) {
-      float mx = -INFINITY, s = 0.f;
-      for (int t = 0; t < 16; ++t) mx = fmaxf(mx, red[threadIdx.x][t].x);
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      for (int t = 0; t < 16; ++t) {
-        const float2 q = red[threadIdx.x][t];
-        s += q.x == -INFINITY ? q.y : q.y * expf(q.x - ref);
-      }
-      p.part[(size_t)blockIdx.x * p.m + i0 + threadIdx.x] = make_float2(mx, s);
-    }
-  }
-}
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t dt_size(int dt) { return dt == MUON_DTYPE_BF16 ? 2 : 4; }
+bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// Joins the pieces of each row; one thread a row.
-__global__ void join_kernel(const float2* part, int parts, long long rows, const int64_t* labels, long long vocab,
-                            long long ignore, const float* zlabel, float* loss, float* lse) {
-  const long long r = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+// ---------------------------------------------------------------------------
+// small kernels
+// ---------------------------------------------------------------------------
+
+// Rows of any stride and alignment to bf16 rows of ldo elements (a multiple of 8):
+// bf16 as it is, fp32 as `parts` bf16 numbers that add up to it (8 bits each).
+template <typename T>
+__global__ void __launch_bounds__(256) pack_kernel(const T* in, long long ld, long long rows, int dim, bf16* out,
+                                                   long long ldo, int parts, long long part_stride) {
+  const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (r >= rows) return;
-  float mx = -INFINITY, s = 0.f;
-  for (int t = 0; t < parts; ++t) mx = fmaxf(mx, part[(size_t)t * rows + r].x);
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  for (int t = 0; t < parts; ++t) {
-    const float2 q = part[(size_t)t * rows + r];
-    s += q.x == -INFINITY ? q.y : q.y * expf(q.x - ref);
+  const T* x = in + r * ld;
+  for (int c = (threadIdx.x & 31) * 2; c < dim; c += 64) {
+    float a = ld1(x + c), b = c + 1 < dim ? ld1(x + c + 1) : 0.f;
+    bf16* o = out + r * ldo + c;
+    for (int q = 0; q < parts; ++q) {
+      const bf16 ha = __float2bfloat16_rn(a), hb = __float2bfloat16_rn(b);
+      *reinterpret_cast<uint32_t*>(o + q * part_stride) =
+          (uint32_t)__bfloat16_as_ushort(ha) | ((uint32_t)__bfloat16_as_ushort(hb) << 16);
+      a -= __bfloat162float(ha);
+      b -= __bfloat162float(hb);
+    }
   }
-  const float l = ref + logf(s);
-  lse[r] = l;
-  const long long lab = labels[r];
-  loss[r] = lab == ignore ? 0.f : (lab < 0 || lab >= vocab) ? __int_as_float(0x7FC00000) : l - zlabel[r];
 }
 
-// Mean loss over the rows that are not ignored; one block, fixed order.
-__global__ void __launch_bounds__(1024) stats_kernel(const float* loss, const int64_t* labels, long long rows,
-                                                     long long ignore, float* stats) {
+// One warp a row: joins its partial sums, writes lse and loss; the last block to finish
+// sums the losses (each thread a fixed set of rows, then a fixed tree).
+constexpr int JOIN_WARPS = 8;
+__global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const float2* part, int parts, long long rows,
+                                                               const int64_t* labels, long long vocab, long long ignore,
+                                                               const float* zlabel, float* loss, float* lse,
+                                                               float* stats, unsigned int* ticket) {
   __shared__ float red[32];
+  __shared__ bool last;
+  const int lane = threadIdx.x & 31;
+  const long long r = (long long)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+  if (r < rows) {
+    const float2* q = part + (size_t)r * parts;
+    float mx = -INFINITY;
+    for (int t = lane; t < parts; t += 32) mx = fmaxf(mx, q[t].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float s = 0.f;
+    for (int t = lane; t < parts; t += 32) {
+      const float2 w = q[t];
+      s += w.x == -INFINITY ? w.y : w.y * expf(w.x - ref);
+    }
+    s = warp_sum(s);
+    if (lane == 0) {
+      const float l = ref + logf(s);
+      const long long lab = labels[r];
+      lse[r] = l;
+      loss[r] = lab == ignore ? 0.f : (lab < 0 || lab >= vocab) ? __int_as_float(0x7FC00000) : l - zlabel[r];
+    }
+  }
+  if (!stats) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
   float s = 0.f, c = 0.f;
-  for (long long r = threadIdx.x; r < rows; r += 1024)
-    if (labels[r] != ignore) { s += loss[r]; c += 1.f; }
+  for (long long i = threadIdx.x; i < rows; i += 32 * JOIN_WARPS)
+    if (labels[i] != ignore) { s += __ldcg(loss + i); c += 1.f; }
   s = block_sum(s, red);
   c = block_sum(c, red);
   if (threadIdx.x == 0) {
     stats[0] = s / fmaxf(c, 1.f);
     stats[1] = c;
+    *ticket = 0;
   }
 }
 
-constexpr size_t HEADER = 256;
-size_t up(size_t x) { return (x + 255) / 256 * 256; }
-size_t dt_size(int dt) { return dt == MUON_DTYPE_BF16 ? 2 : 4; }
-bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+// dH from the sums of each range of K.
+template <typename T>
+__global__ void __launch_bounds__(256) split_sum_kernel(const float* acc, int splits, long long rows, int dim,
+                                                        long long ldacc, T* out) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long r = i / dim;
+  if (r >= rows) return;
+  const int c = (int)(i - r * dim);
+  float s = 0.f;
+  for (int k = 0; k < splits; ++k) s += acc[((size_t)k * rows + r) * ldacc + c];
+  st1(out + i, s);
+}
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+struct CePlan {
+  int parts, nterms;
+  int64_t dp;                  // row length of a packed copy
+  bool pack_h, pack_w;
+  size_t hp, wp;               // packed copies
+  size_t zlabel, part;         // forward
+  int64_t piece, npieces;
+  int splits;
+  size_t g[2];
+  size_t g_part;               // elements of one part of g
+  size_t acc;
+  int64_t ldacc;
+  size_t total;
+};
 
 int check(const muon_linear_ce* a) {
   if (!a) return MUON_ERR_INVALID;
@@ -170,6 +148,11 @@ int check(const muon_linear_ce* a) {
       a->ldh < a->dim || a->ldw < a->dim)
     return MUON_ERR_INVALID;
   if (a->dtype != MUON_DTYPE_F32 && a->dtype != MUON_DTYPE_BF16) return MUON_ERR_UNSUPPORTED;
+  if (a->ldh >= (1LL << 38) || a->ldw >= (1LL << 38)) return MUON_ERR_UNSUPPORTED;
+  // tiles are counted in 31 bits
+  if (cdiv(a->rows, TILE) * cdiv(a->vocab, TILE) >= (1LL << 30) || cdiv(a->rows, TILE) * cdiv(a->dim, TILE) >= (1LL << 26) ||
+      cdiv(a->vocab, TILE) * cdiv(a->dim, TILE) >= (1LL << 30))
+    return MUON_ERR_UNSUPPORTED;
   return MUON_OK;
 }
 int check_pointers(const muon_linear_ce* a) {
@@ -179,37 +162,163 @@ int check_pointers(const muon_linear_ce* a) {
   return MUON_OK;
 }
 
-template <int kEpi, typename TA, typename TB, typename TO>
-void launch(const Gemm& p, cudaStream_t s) {
-  gemm_kernel<kEpi, TA, TB, TO><<<dim3((unsigned)((p.n + BT - 1) / BT), (unsigned)((p.m + BT - 1) / BT)), THREADS, 0,
-                                  s>>>(p);
-  count_launch();
+// Ranges the K of a dH tile is cut into: a tile over a whole piece must not outlast half
+// of a CTA pair's share of the launch (the tiles are handed out longest first).
+int split_count(int64_t rows, int64_t dim, int64_t piece, int64_t npairs) {
+  const int64_t kp = cdiv(piece, BK), mt = cdiv(rows, TILE), dt = cdiv(dim, TILE), vt = cdiv(piece, TILE);
+  const int64_t work = mt * dt * kp + vt * dt * cdiv(rows, BK) + mt * vt * cdiv(dim, BK);
+  const int64_t share = std::max<int64_t>(work / (2 * npairs), 8);
+  return (int)std::min<int64_t>(std::max<int64_t>(1, cdiv(kp, share)), MAX_SPLITS);
+}
+
+void make_plan(const muon_linear_ce* a, int backward, CePlan* P) {
+  const bool f32 = a->dtype == MUON_DTYPE_F32;
+  P->parts = f32 ? 3 : 1;
+  P->nterms = f32 ? 6 : 1;
+  P->dp = (a->dim + 7) / 8 * 8;
+  P->pack_h = f32 || a->ldh % 8 || !is_aligned(a->H, 16);
+  P->pack_w = f32 || a->ldw % 8 || !is_aligned(a->W, 16);
+  size_t at = HEADER;
+  auto take = [&](size_t bytes) { const size_t p = at; at += up(bytes); return p; };
+  // room for H's copy in any case, so that a workspace fits whatever H's alignment
+  P->hp = take((size_t)P->parts * a->rows * P->dp * 2);
+  P->wp = P->pack_w ? take((size_t)P->parts * a->vocab * P->dp * 2) : at;
+  const size_t common = at;
+  P->zlabel = take((size_t)a->rows * 4);
+  P->part = take((size_t)a->rows * 2 * cdiv(a->vocab, TILE) * sizeof(float2));
+  P->total = at;
+  if (!backward) return;
+  at = common;
+  const int64_t want = G_BYTES / (2 * P->parts * std::max<int64_t>(a->rows, 1));
+  P->piece = std::min(std::max(want / TILE * TILE, MIN_PIECE), cdiv(a->vocab, TILE) * TILE);
+  // pieces of one size, as far as tiles allow
+  P->npieces = cdiv(a->vocab, P->piece);
+  P->piece = cdiv(cdiv(a->vocab, P->npieces), TILE) * TILE;
+  P->npieces = cdiv(a->vocab, P->piece);
+  P->splits = split_count(a->rows, a->dim, P->piece, 76);
+  P->g_part = (size_t)a->rows * P->piece;
+  for (int i = 0; i < 2; ++i) P->g[i] = P->npieces > 1 || i == 0 ? take(P->parts * P->g_part * 2) : P->g[0];
+  P->ldacc = P->dp;
+  P->acc = P->npieces > 1 || P->splits > 1 ? take((size_t)P->splits * a->rows * P->ldacc * 4) : 0;
+  P->total = std::max(P->total, at);
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+struct Operand {
+  const bf16* p;
+  int64_t rows, cols, ld, part_stride;
+  int parts;
+};
+
+// box: 64 columns x box_rows rows
+bool map_of(CUtensorMap* m, const Operand& o, int box_rows) {
+  return encode_tmap_bf16(m, o.p, (uint64_t)o.cols, (uint64_t)o.rows, (uint64_t)o.parts, (uint64_t)o.ld * 2,
+                          (uint64_t)o.part_stride * 2, 64, (uint32_t)box_rows);
 }
 
 template <typename T>
-void backward(const muon_linear_ce* a, Gemm base, void* dH, void* dW, float* g, float* acc, cudaStream_t s) {
-  const size_t es = sizeof(T);
-  for (int64_t v0 = 0; v0 < a->vocab; v0 += PIECE) {
-    const int64_t c = std::min(PIECE, a->vocab - v0);
-    const char* Wp = static_cast<const char*>(a->W) + (size_t)v0 * a->ldw * es;
-    Gemm p = base;
-    p.A = a->H; p.sai = a->ldh; p.sak = 1; p.B = Wp; p.sbj = a->ldw; p.sbk = 1;
-    p.m = a->rows; p.n = c; p.kk = a->dim; p.v0 = v0; p.out = g; p.ldo = PIECE;
-    launch<GRAD, T, T, float>(p, s);
-    if (dH) {
-      p.A = g; p.sai = PIECE; p.sak = 1; p.B = Wp; p.sbj = 1; p.sbk = a->ldw;
-      p.m = a->rows; p.n = a->dim; p.kk = c; p.out = acc; p.fin = dH; p.ldo = a->dim;
-      p.first = v0 == 0; p.last = v0 + c == a->vocab;
-      launch<DH, float, T, T>(p, s);
-    }
-    if (dW) {
-      p.A = g; p.sai = 1; p.sak = PIECE; p.B = a->H; p.sbj = 1; p.sbk = a->ldh;
-      p.m = c; p.n = a->dim; p.kk = a->rows; p.out = static_cast<char*>(dW) + (size_t)v0 * a->dim * es; p.ldo = a->dim;
-      launch<DW, float, T, T>(p, s);
-    }
-  }
+void pack(const void* in, int64_t ld, int64_t rows, int64_t dim, bf16* out, int64_t ldo, int parts, cudaStream_t s) {
+  pack_kernel<T><<<(unsigned)cdiv(rows, 8), 256, 0, s>>>(static_cast<const T*>(in), ld, rows, (int)dim, out, ldo, parts,
+                                                         rows * ldo);
+  count_launch();
 }
 
+Operand operand(const muon_linear_ce* a, const CePlan& P, bool h, char* ws, cudaStream_t s) {
+  const void* src = h ? a->H : a->W;
+  const int64_t rows = h ? a->rows : a->vocab, ld = h ? a->ldh : a->ldw;
+  if (!(h ? P.pack_h : P.pack_w))
+    return Operand{static_cast<const bf16*>(src), rows, a->dim, ld, rows * ld, 1};
+  bf16* dst = reinterpret_cast<bf16*>(ws + (h ? P.hp : P.wp));
+  if (a->dtype == MUON_DTYPE_BF16) pack<bf16>(src, ld, rows, a->dim, dst, P.dp, 1, s);
+  else pack<float>(src, ld, rows, a->dim, dst, P.dp, 3, s);
+  return Operand{dst, rows, a->dim, P.dp, rows * P.dp, P.parts};
+}
+
+void common_params(Params* p, const muon_linear_ce* a, const CePlan& P, char* ws) {
+  std::memset(p, 0, offsetof(Params, order));
+  p->nterms = P.nterms;
+  p->parts = P.parts;
+  // (part of A, part of B), smallest products first
+  static const unsigned char ta[MAX_TERMS] = {2, 0, 1, 1, 0, 0}, tb[MAX_TERMS] = {0, 2, 1, 0, 1, 0};
+  if (P.nterms > 1) {
+    std::memcpy(p->ta, ta, sizeof(ta));
+    std::memcpy(p->tb, tb, sizeof(tb));
+  }
+  p->f32_out = a->dtype == MUON_DTYPE_F32;
+  p->labels = a->labels;
+  p->vocab = a->vocab;
+  p->ignore = a->ignore_index;
+  p->status = reinterpret_cast<unsigned int*>(ws);
+  p->timeout_ns = wait_limit_ns();
+  p->debug_flags = test_flags();
+}
+
+void shape(Job* j, int64_t m, int64_t n, int64_t k, int group) {
+  j->m = (int)m;
+  j->n = (int)n;
+  j->mtiles = (int)cdiv(m, TILE);
+  j->ntiles = (int)cdiv(n, TILE);
+  j->group = std::min(group, j->mtiles);
+  j->splits = 1;
+  j->nkb = (int)cdiv(k, BK);
+  j->tiles = j->mtiles * j->ntiles;
+}
+
+// Hands the launch's tiles out: each to the pair with the least work so far, jobs in
+// order of their tiles' lengths.  Launches with more tiles than the table holds go round
+// robin, where one tile more or less no longer matters.
+void lay_out(Params* p, int npairs) {
+  std::sort(p->job, p->job + p->njobs, [](const Job& x, const Job& y) { return x.nkb > y.nkb; });
+  int t = 0;
+  for (int j = 0; j < p->njobs; ++j) {
+    p->job[j].begin = t;
+    t += p->job[j].tiles;
+  }
+  p->tiles = t;
+  p->ordered = 0;
+  if (p->njobs < 2 || t > MAX_ORDER || t <= npairs) return;
+  // load[i]: work of pair i; a binary heap of pairs by (load, index)
+  long long load[MAX_PAIRS];
+  int heap[MAX_PAIRS];
+  unsigned char owner[MAX_ORDER];
+  int count[MAX_PAIRS] = {};
+  for (int i = 0; i < npairs; ++i) { load[i] = 0; heap[i] = i; }
+  auto less = [&](int x, int y) { return load[x] != load[y] ? load[x] < load[y] : x < y; };
+  t = 0;
+  for (int j = 0; j < p->njobs; ++j) {
+    const long long cost = (long long)p->job[j].nkb + 2;   // an accumulator's hand-over costs about two K steps
+    for (int i = 0; i < p->job[j].tiles; ++i, ++t) {
+      const int w = heap[0];
+      owner[t] = (unsigned char)w;
+      ++count[w];
+      load[w] += cost;
+      for (int at = 0;;) {
+        int c = 2 * at + 1;
+        if (c >= npairs) break;
+        if (c + 1 < npairs && less(heap[c + 1], heap[c])) ++c;
+        if (!less(heap[c], heap[at])) break;
+        std::swap(heap[c], heap[at]);
+        at = c;
+      }
+    }
+  }
+  p->start[0] = 0;
+  for (int i = 0; i < npairs; ++i) p->start[i + 1] = (unsigned short)(p->start[i] + count[i]);
+  int fill[MAX_PAIRS];
+  for (int i = 0; i < npairs; ++i) fill[i] = p->start[i];
+  for (t = 0; t < p->tiles; ++t) p->order[fill[owner[t]]++] = (unsigned short)t;
+  p->ordered = 1;
+}
+
+int result_vec(const void* out, int64_t ld, int dt) {
+  const size_t row = (size_t)ld * dt_size(dt);
+  if (is_aligned(out, 32) && row % 32 == 0) return 2;
+  return is_aligned(out, 16) && row % 16 == 0 ? 1 : 0;
+}
+
+}  // namespace
 }  // namespace ce
 }  // namespace muon
 
@@ -217,57 +326,66 @@ using namespace muon;
 
 extern "C" size_t muon_linear_ce_workspace_size(const muon_linear_ce* a, int backward) {
   if (ce::check(a) != MUON_OK) return (size_t)-1;
-  const size_t n = (size_t)a->rows;
-  const size_t fwd = ce::up(n * 4) + ce::up(n * ((a->vocab + ce::BT - 1) / ce::BT) * 8);
-  const size_t bwd = ce::up(n * ce::PIECE * 4) + ce::up(n * a->dim * 4);
-  return ce::HEADER + (backward ? std::max(fwd, bwd) : fwd);
+  ce::CePlan P;
+  ce::make_plan(a, backward, &P);
+  return P.total;
 }
 
 extern "C" int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, float* lse, float* stats, void* ws,
                                       size_t ws_bytes, muon_stream_t stream) {
+  using namespace ce;
   begin_launches();
-  if (int rc = ce::check(a)) return rc;
-  if (int rc = ce::check_pointers(a)) return rc;
+  if (int rc = check(a)) return rc;
+  if (int rc = check_pointers(a)) return rc;
   if (a->rows && (!loss || !lse)) return MUON_ERR_INVALID;
-  if (!ce::is_aligned(loss, 4) || !ce::is_aligned(lse, 4) || !ce::is_aligned(stats, 4)) return MUON_ERR_INVALID;
-  if (!ws || !ce::is_aligned(ws, 256) || ws_bytes < muon_linear_ce_workspace_size(a, 0)) return MUON_ERR_WORKSPACE;
+  if (!is_aligned(loss, 4) || !is_aligned(lse, 4) || !is_aligned(stats, 4)) return MUON_ERR_INVALID;
+  CePlan P = {};
+  make_plan(a, 0, &P);
+  if (!ws || !is_aligned(ws, 256) || ws_bytes < P.total) return MUON_ERR_WORKSPACE;
   int sms = 0;
   if (int rc = require_device(&sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  char* w = static_cast<char*>(ws) + ce::HEADER;
-  ce::Gemm p = {};
-  p.zlabel = reinterpret_cast<float*>(w);
-  p.part = reinterpret_cast<float2*>(w + ce::up((size_t)a->rows * 4));
-  p.labels = a->labels; p.vocab = a->vocab; p.ignore = a->ignore_index;
-  p.A = a->H; p.sai = a->ldh; p.sak = 1; p.B = a->W; p.sbj = a->ldw; p.sbk = 1;
-  p.m = a->rows; p.n = a->vocab; p.kk = a->dim;
-  if (a->rows) {
-    if (a->dtype == MUON_DTYPE_BF16) ce::launch<ce::FWD, bf16, bf16, float>(p, s);
-    else ce::launch<ce::FWD, float, float, float>(p, s);
-    ce::join_kernel<<<(unsigned)((a->rows + 127) / 128), 128, 0, s>>>(
-        p.part, (int)((a->vocab + ce::BT - 1) / ce::BT), a->rows, a->labels, a->vocab, a->ignore_index, p.zlabel, loss,
-        lse);
-    count_launch();
+  if (a->rows == 0) {
+    if (stats && cudaMemsetAsync(stats, 0, 8, s) != cudaSuccess) return MUON_ERR_CUDA;
+    return MUON_OK;
   }
-  if (stats) {
-    ce::stats_kernel<<<1, 1024, 0, s>>>(loss, a->labels, a->rows, a->ignore_index, stats);
-    count_launch();
-  }
+  if (prepare() != cudaSuccess) return MUON_ERR_CUDA;
+  char* w = static_cast<char*>(ws);
+  static thread_local Params p;
+  common_params(&p, a, P, w);
+  p.part = reinterpret_cast<float2*>(w + P.part);
+  p.zlabel = reinterpret_cast<float*>(w + P.zlabel);
+  const Operand H = operand(a, P, true, w, s), W = operand(a, P, false, w, s);
+  Job& j = p.job[0];
+  j.kind = LOGITS;
+  if (!map_of(&j.a, H, 128) || !map_of(&j.b, W, 128)) return MUON_ERR_CUDA;
+  shape(&j, a->rows, a->vocab, a->dim, 16);
+  j.seg_kb = P.nterms > 1 ? SEG_F32 : SEG_BF16;
+  p.njobs = 1;
+  p.tiles = j.tiles;
+  if (launch(p, true, s) != cudaSuccess) return MUON_ERR_CUDA;
+  join_kernel<<<(unsigned)cdiv(a->rows, JOIN_WARPS), 32 * JOIN_WARPS, 0, s>>>(
+      p.part, 2 * j.ntiles, a->rows, a->labels, a->vocab, a->ignore_index, p.zlabel, loss, lse, stats,
+      static_cast<unsigned int*>(ws) + TICKET_WORD);
+  count_launch();
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse, const float* row_grad,
                                        const float* stats, float grad_scale, void* dH, void* dW, void* ws,
                                        size_t ws_bytes, muon_stream_t stream) {
+  using namespace ce;
   begin_launches();
-  if (int rc = ce::check(a)) return rc;
-  if (int rc = ce::check_pointers(a)) return rc;
-  const size_t es = ce::dt_size(a->dtype);
+  if (int rc = check(a)) return rc;
+  if (int rc = check_pointers(a)) return rc;
+  const size_t es = dt_size(a->dtype);
   if (a->rows && !lse) return MUON_ERR_INVALID;
-  if (!ce::is_aligned(lse, 4) || !ce::is_aligned(row_grad, 4) || !ce::is_aligned(stats, 4) ||
-      !ce::is_aligned(dH, es) || !ce::is_aligned(dW, es))
+  if (!is_aligned(lse, 4) || !is_aligned(row_grad, 4) || !is_aligned(stats, 4) || !is_aligned(dH, es) ||
+      !is_aligned(dW, es))
     return MUON_ERR_INVALID;
-  if (!ws || !ce::is_aligned(ws, 256) || ws_bytes < muon_linear_ce_workspace_size(a, 1)) return MUON_ERR_WORKSPACE;
+  CePlan P = {};
+  make_plan(a, 1, &P);
+  if (!ws || !is_aligned(ws, 256) || ws_bytes < P.total) return MUON_ERR_WORKSPACE;
   if (!dH && !dW) return MUON_OK;
   int sms = 0;
   if (int rc = require_device(&sms)) return rc;
@@ -276,13 +394,79 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
     if (dW && cudaMemsetAsync(dW, 0, (size_t)a->vocab * a->dim * es, s) != cudaSuccess) return MUON_ERR_CUDA;
     return MUON_OK;
   }
-  char* w = static_cast<char*>(ws) + ce::HEADER;
-  float* g = reinterpret_cast<float*>(w);
-  float* acc = reinterpret_cast<float*>(w + ce::up((size_t)a->rows * ce::PIECE * 4));
-  ce::Gemm p = {};
-  p.labels = a->labels; p.vocab = a->vocab; p.ignore = a->ignore_index;
-  p.lse = lse; p.row_grad = row_grad; p.stats = stats; p.scale = grad_scale;
-  if (a->dtype == MUON_DTYPE_BF16) ce::backward<bf16>(a, p, dH, dW, g, acc, s);
-  else ce::backward<float>(a, p, dH, dW, g, acc, s);
+  if (prepare() != cudaSuccess) return MUON_ERR_CUDA;
+  char* w = static_cast<char*>(ws);
+  static thread_local Params p;
+  const Operand H = operand(a, P, true, w, s), W = operand(a, P, false, w, s);
+  CUtensorMap hk, hm, wk, wm;   // K-major and MN-major boxes
+  if (!map_of(&hk, H, 128) || !map_of(&hm, H, 64) || !map_of(&wk, W, 128) || !map_of(&wm, W, 64)) return MUON_ERR_CUDA;
+  const bool f32 = a->dtype == MUON_DTYPE_F32;
+  const int npairs = pairs();
+  float* acc = P.acc ? reinterpret_cast<float*>(w + P.acc) : nullptr;
+  // launch i computes g of piece i and multiplies g of piece i - 1
+  for (int64_t i = 0; i <= P.npieces; ++i) {
+    common_params(&p, a, P, w);
+    p.lse = lse;
+    p.row_grad = row_grad;
+    p.stats = stats;
+    p.scale = grad_scale;
+    if (i > 0) {
+      const int64_t v0 = (i - 1) * P.piece, c = std::min(P.piece, a->vocab - v0);
+      const Operand G{reinterpret_cast<const bf16*>(w + P.g[(i - 1) & 1]), a->rows, c, P.piece, (int64_t)P.g_part, P.parts};
+      if (dH) {
+        Job& j = p.job[p.njobs++];
+        j.kind = DH;
+        if (!map_of(&j.a, G, 128)) return MUON_ERR_CUDA;
+        j.b = wm;
+        j.b_mn = 1;
+        j.b_k0 = (int)v0;
+        shape(&j, a->rows, a->dim, c, 16);
+        j.splits = P.splits;
+        j.nkb = (int)cdiv(j.nkb, P.splits);
+        j.tiles *= P.splits;
+        j.acc = acc;
+        j.ldacc = P.ldacc;
+        j.first = i == 1;
+        j.last = i == P.npieces;
+        j.out = P.splits == 1 ? dH : nullptr;
+        j.ldo = a->dim;
+        j.vec = result_vec(dH, a->dim, a->dtype);
+        j.seg_kb = f32 ? SEG_F32 : j.nkb;
+      }
+      if (dW) {
+        Job& j = p.job[p.njobs++];
+        j.kind = DW;
+        if (!map_of(&j.a, G, 64)) return MUON_ERR_CUDA;
+        j.b = hm;
+        j.a_mn = j.b_mn = 1;
+        shape(&j, c, a->dim, a->rows, 16);
+        j.out = static_cast<char*>(dW) + (size_t)v0 * a->dim * es;
+        j.ldo = a->dim;
+        j.vec = result_vec(j.out, a->dim, a->dtype);
+        j.seg_kb = f32 ? SEG_F32 : j.nkb;
+      }
+    }
+    if (i < P.npieces) {
+      Job& j = p.job[p.njobs++];
+      j.kind = GRAD;
+      j.a = hk;
+      j.b = wk;
+      p.v0 = i * P.piece;
+      j.b_n0 = (int)p.v0;
+      shape(&j, a->rows, std::min<int64_t>(P.piece, a->vocab - p.v0), a->dim, 16);
+      j.out = w + P.g[i & 1];
+      j.ldo = P.piece;
+      j.part_stride = (long long)P.g_part;
+      j.seg_kb = f32 ? SEG_F32 : j.nkb;
+    }
+    lay_out(&p, npairs);
+    if (launch(p, f32, s) != cudaSuccess) return MUON_ERR_CUDA;
+  }
+  if (dH && P.splits > 1) {
+    const unsigned blocks = (unsigned)cdiv(a->rows * a->dim, 256);
+    if (f32) split_sum_kernel<float><<<blocks, 256, 0, s>>>(acc, P.splits, a->rows, (int)a->dim, P.ldacc, static_cast<float*>(dH));
+    else split_sum_kernel<bf16><<<blocks, 256, 0, s>>>(acc, P.splits, a->rows, (int)a->dim, P.ldacc, static_cast<bf16*>(dH));
+    count_launch();
+  }
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

@@ -117,18 +117,6 @@ __device__ __forceinline__ void store_bf16x32(bf16* dst, const float (&v)[32]) {
   }
 }
 
-// 256-bit global accesses (32-byte aligned): a row-per-lane chunk of 64 bytes in two
-// instructions instead of four, so half the L1 requests for the same bytes.
-__device__ __forceinline__ void ld_v8(const void* src, uint32_t* w) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(src));
-}
-__device__ __forceinline__ void st_v8(void* dst, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
-               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 __device__ __forceinline__ void ld_v8x2(const void* src, uint32_t* w) {
   ld_v8(src, w);
   ld_v8(reinterpret_cast<const uint8_t*>(src) + 32, w + 8);
