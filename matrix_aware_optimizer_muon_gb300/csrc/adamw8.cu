@@ -78,10 +78,64 @@ __device__ __forceinline__ uint32_t encode_v(float v, uint32_t base, uint32_t r)
   return (uint32_t)min(max(k, a ? 1 : 0), 255);
 }
 
-// One block of 128 elements per CTA, one element per thread.
+// Bandwidth-bound: 10 bytes an element for bf16 parameters and gradients (2+2 P, 2 G, 1+1
+// a moment's codes twice).  A thread owns 16 consecutive elements, so that every array is
+// read and written in whole 16- or 32-byte vectors; 8 threads make a block of 128, whose
+// two maxima take three shuffles each, and no value passes through shared memory.
+constexpr int A8_THREADS = 256;
+constexpr int A8_EACH = 16;
+constexpr int A8_CHUNK = A8_THREADS * A8_EACH;
+
+// 16 elements as loaded, converted later, so that all of a thread's loads are in flight.
+template <typename T> struct Raw16 { uint32_t w[4 * sizeof(T)]; };
+template <typename T>
+__device__ __forceinline__ void ld16(const T* p, Raw16<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) ld_v8(reinterpret_cast<const uint8_t*>(p) + 32 * i, r.w + 8 * i);
+}
+template <typename T>
+__device__ __forceinline__ void ld16_some(const T* p, int n, Raw16<T>& r) {
+#pragma unroll
+  for (int i = 0; i < A8_EACH; ++i) {
+    if (sizeof(T) == 4) {
+      r.w[i] = i < n ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+    } else {
+      const uint32_t h = i < n ? reinterpret_cast<const uint16_t*>(p)[i] : 0u;
+      r.w[i / 2] = i & 1 ? r.w[i / 2] | (h << 16) : h;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ float get16(const Raw16<T>& r, int i) {
+  if (sizeof(T) == 4) return __uint_as_float(r.w[i]);
+  return __uint_as_float(i & 1 ? r.w[i / 2] & 0xFFFF0000u : r.w[i / 2] << 16);
+}
+template <typename T>
+__device__ __forceinline__ void st16(T* p, const float (&v)[A8_EACH]) {
+  uint32_t w[4 * sizeof(T)];
+#pragma unroll
+  for (int i = 0; i < (int)(4 * sizeof(T)); ++i)
+    w[i] = sizeof(T) == 4 ? __float_as_uint(v[i % A8_EACH]) : pack_bf16x2(v[(2 * i) % A8_EACH], v[(2 * i + 1) % A8_EACH]);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) st_v8(reinterpret_cast<uint8_t*>(p) + 32 * i, w + 8 * i);
+}
+
+// Square root and quotient of the update: the hardware's approximations (2 ulp at most);
+// what they feed is lr times a number near 1, added to a parameter of 24 or 8 bits.
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t max_of_8(uint32_t x) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
 template <typename PT, typename GT>
-__global__ void __launch_bounds__(A8_BLOCK) adamw8_kernel(const __grid_constant__ Adamw8Params q) {
-  __shared__ uint32_t top[2];
+__global__ void __launch_bounds__(A8_THREADS) adamw8_kernel(const __grid_constant__ Adamw8Params q) {
   int lo = 0, hi = q.n - 1;
   const int b = blockIdx.x;
   while (lo < hi) {
@@ -89,43 +143,100 @@ __global__ void __launch_bounds__(A8_BLOCK) adamw8_kernel(const __grid_constant_
     if (q.e[mid].block_begin <= b) lo = mid; else hi = mid - 1;
   }
   const Adamw8Entry& e = q.e[lo];
-  const long long blk = b - e.block_begin;
-  const long long i = blk * A8_BLOCK + threadIdx.x;
-  if (threadIdx.x < 2) top[threadIdx.x] = 0;
-  __syncthreads();
-  const bool in = i < e.numel;
-  float m = 0.f, v = 0.f;
-  if (in) {
-    const float g = ld1(reinterpret_cast<const GT*>(e.G) + i);
-    m = q.beta1 * decode_m(e.m[i], base_m(e.ms[blk])) + q.omb1 * g;
-    v = q.beta2 * decode_v(e.v[i], base_v(e.vs[blk])) + q.omb2 * g * g;
-    PT* P = reinterpret_cast<PT*>(e.P) + i;
-    const float p = ld1(P);
-    st1(P, p - q.lr * ((m * q.inv_bc1) / (sqrtf(v) * q.inv_sqrt_bc2 + q.eps) + q.wd * p));
-    if (v != v) v = 0.f;   // the NaN is kept in m
-    v = fminf(v, FLT_MAX);
-    const uint32_t a = __float_as_uint(m) & 0x7FFFFFFFu;
-    if (a < 0x7F800000u) atomicMax(&top[0], a);
-    atomicMax(&top[1], __float_as_uint(v));
+  const long long i0 = (long long)(b - e.block_begin) * A8_CHUNK + threadIdx.x * A8_EACH;
+  const long long blk = i0 / A8_BLOCK;
+  // past the last block of codes: nothing to do, but the shuffles below need the thread
+  const bool codes = i0 < (e.numel + A8_BLOCK - 1) / A8_BLOCK * A8_BLOCK;
+  const int n = (int)min(max(e.numel - i0, 0LL), (long long)A8_EACH);
+  PT* P = reinterpret_cast<PT*>(e.P) + i0;
+  const GT* G = reinterpret_cast<const GT*>(e.G) + i0;
+  const bool whole = n == A8_EACH && e.vec;
+  Raw16<PT> pr;
+  Raw16<GT> gr;
+  uint4 mc = make_uint4(0, 0, 0, 0), vc = mc;
+  int ms = 0, vs = 0;
+  if (codes) {
+    mc = *reinterpret_cast<const uint4*>(e.m + i0);
+    vc = *reinterpret_cast<const uint4*>(e.v + i0);
+    ms = e.ms[blk];
+    vs = e.vs[blk];
   }
-  __syncthreads();
-  const int sm = scale_of(top[0]), sv = scale_of(top[1]);
-  const unsigned long long at = (unsigned long long)(e.first + i);
-  const uint32_t r = mix32((uint32_t)at ^ mix32(q.key + (uint32_t)(at >> 32)));
-  e.m[i] = (uint8_t)encode_m(m, base_m(sm), r & 0xFFFFu);
-  e.v[i] = (uint8_t)encode_v(v, base_v(sv), r >> 16);
-  if (threadIdx.x == 0) {
-    e.ms[blk] = (uint8_t)sm;
-    e.vs[blk] = (uint8_t)sv;
+  if (whole) {
+    ld16(P, pr);
+    ld16(G, gr);
+  } else {
+    ld16_some(P, n, pr);
+    ld16_some(G, n, gr);
+  }
+  float m[A8_EACH], v[A8_EACH], p[A8_EACH];
+  uint32_t mtop = 0, vtop = 0;
+  {
+    const uint32_t bm = base_m(ms), bv = base_v(vs);
+    const uint32_t mw[4] = {mc.x, mc.y, mc.z, mc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
+#pragma unroll
+    for (int i = 0; i < A8_EACH; ++i) {
+      const float g = get16(gr, i);
+      m[i] = q.beta1 * decode_m((mw[i / 4] >> (8 * (i % 4))) & 255u, bm) + q.omb1 * g;
+      v[i] = q.beta2 * decode_v((vw[i / 4] >> (8 * (i % 4))) & 255u, bv) + q.omb2 * g * g;
+      p[i] = get16(pr, i);
+      p[i] -= q.lr * (__fdividef(m[i] * q.inv_bc1, sqrt_approx(v[i]) * q.inv_sqrt_bc2 + q.eps) + q.wd * p[i]);
+      // codes past the end stay 0; a NaN is kept in m; infinite squares hold the largest code
+      if (i >= n) m[i] = v[i] = 0.f;
+      v[i] = v[i] != v[i] ? 0.f : fminf(v[i], FLT_MAX);
+      const uint32_t a = __float_as_uint(m[i]) & 0x7FFFFFFFu;
+      mtop = max(mtop, a < 0x7F800000u ? a : 0u);
+      vtop = max(vtop, __float_as_uint(v[i]));
+    }
+  }
+  if (whole) {
+    st16(P, p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < A8_EACH; ++i)
+      if (i < n) st1(P + i, p[i]);
+  }
+  ms = scale_of(max_of_8(mtop));
+  vs = scale_of(max_of_8(vtop));
+  if (!codes) return;
+  const uint32_t bm = base_m(ms), bv = base_v(vs);
+  const unsigned long long at = (unsigned long long)(e.first + i0);
+  const uint32_t key = mix32(q.key + (uint32_t)(at >> 32));
+  uint32_t mw[4] = {}, vw[4] = {};
+#pragma unroll
+  for (int i = 0; i < A8_EACH; ++i) {
+    const uint32_t r = mix32(((uint32_t)at + i) ^ key);
+    mw[i / 4] |= encode_m(m[i], bm, r & 0xFFFFu) << (8 * (i % 4));
+    vw[i / 4] |= encode_v(v[i], bv, r >> 16) << (8 * (i % 4));
+  }
+  *reinterpret_cast<uint4*>(e.m + i0) = make_uint4(mw[0], mw[1], mw[2], mw[3]);
+  *reinterpret_cast<uint4*>(e.v + i0) = make_uint4(vw[0], vw[1], vw[2], vw[3]);
+  if ((threadIdx.x & 7) == 0) {
+    e.ms[blk] = (uint8_t)ms;
+    e.vs[blk] = (uint8_t)vs;
   }
 }
 
+// 16 codes of one moment per thread: 16 bytes in, 32 out.
+template <bool kFirst>
+__device__ __forceinline__ void unpack16(const uint8_t* c, const uint8_t* s, bf16* out, long long i0) {
+  const uint4 w4 = *reinterpret_cast<const uint4*>(c + i0);
+  const int sc = s[i0 / A8_BLOCK];
+  const uint32_t base = kFirst ? base_m(sc) : base_v(sc);
+  const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+  float v[A8_EACH];
+#pragma unroll
+  for (int i = 0; i < A8_EACH; ++i) {
+    const uint32_t k = (w[i / 4] >> (8 * (i % 4))) & 255u;
+    v[i] = kFirst ? decode_m(k, base) : decode_v(k, base);
+  }
+  st16(out + i0, v);
+}
 __global__ void __launch_bounds__(256) adamw8_unpack_kernel(const uint8_t* m, const uint8_t* ms, const uint8_t* v,
                                                             const uint8_t* vs, long long numel, bf16* mo, bf16* vo) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= numel) return;
-  if (m) mo[i] = __float2bfloat16_rn(decode_m(m[i], base_m(ms[i / A8_BLOCK])));
-  if (v) vo[i] = __float2bfloat16_rn(decode_v(v[i], base_v(vs[i / A8_BLOCK])));
+  const long long i0 = ((long long)blockIdx.x * 256 + threadIdx.x) * A8_EACH;
+  if (i0 >= numel) return;
+  if (m) unpack16<true>(m, ms, mo, i0);
+  if (v) unpack16<false>(v, vs, vo, i0);
 }
 
 bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -155,7 +266,7 @@ extern "C" int muon_adamw8_step(const muon_adamw8_param* params, int n, int64_t 
     if (!is_aligned(a.P, dt_size(p_dt)) || !is_aligned(a.G, dt_size(g_dt)) || !is_aligned(a.m, 16) ||
         !is_aligned(a.v, 16))
       return MUON_ERR_INVALID;
-    if (a.numel / A8_BLOCK >= (1LL << 30)) return MUON_ERR_UNSUPPORTED;
+    if (a.numel / A8_CHUNK >= (1LL << 30)) return MUON_ERR_UNSUPPORTED;
   }
   int sms = 0;
   if (int rc = require_device(&sms)) return rc;
@@ -180,22 +291,22 @@ extern "C" int muon_adamw8_step(const muon_adamw8_param* params, int n, int64_t 
     for (; i < n && j < A8_MAX_PARAMS; ++i) {
       const muon_adamw8_param& a = params[i];
       if (a.numel == 0) continue;
-      const long long nb = (a.numel + A8_BLOCK - 1) / A8_BLOCK;
+      const long long nb = (a.numel + A8_CHUNK - 1) / A8_CHUNK;
       if (blocks + nb >= (1LL << 31)) {
         if (j == 0) return MUON_ERR_UNSUPPORTED;
         break;
       }
       q.e[j++] = Adamw8Entry{a.P, a.G, a.m, a.v, a.m_scale, a.v_scale, (long long)a.numel, (long long)a.first,
-                             (int)blocks, 0};
+                             (int)blocks, is_aligned(a.P, 32) && is_aligned(a.G, 32)};
       blocks += nb;
     }
     q.n = j;
     if (j == 0) continue;
     const bool pb = p_dt == MUON_DTYPE_BF16, gb = g_dt == MUON_DTYPE_BF16;
-    if (pb && gb) adamw8_kernel<bf16, bf16><<<(unsigned)blocks, A8_BLOCK, 0, s>>>(q);
-    else if (pb) adamw8_kernel<bf16, float><<<(unsigned)blocks, A8_BLOCK, 0, s>>>(q);
-    else if (gb) adamw8_kernel<float, bf16><<<(unsigned)blocks, A8_BLOCK, 0, s>>>(q);
-    else adamw8_kernel<float, float><<<(unsigned)blocks, A8_BLOCK, 0, s>>>(q);
+    if (pb && gb) adamw8_kernel<bf16, bf16><<<(unsigned)blocks, A8_THREADS, 0, s>>>(q);
+    else if (pb) adamw8_kernel<bf16, float><<<(unsigned)blocks, A8_THREADS, 0, s>>>(q);
+    else if (gb) adamw8_kernel<float, bf16><<<(unsigned)blocks, A8_THREADS, 0, s>>>(q);
+    else adamw8_kernel<float, float><<<(unsigned)blocks, A8_THREADS, 0, s>>>(q);
     if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
     count_launch();
   }
@@ -211,7 +322,7 @@ extern "C" int muon_adamw8_unpack(const uint8_t* m, const uint8_t* m_scale, cons
   if (!is_aligned(m, 16) || !is_aligned(v, 16) || !is_aligned(m_out, 32) || !is_aligned(v_out, 32))
     return MUON_ERR_INVALID;
   if (numel == 0 || (!m && !v)) return MUON_OK;
-  const long long blocks = (numel + 255) / 256;
+  const long long blocks = (numel / A8_EACH + 255) / 256;
   if (blocks >= (1LL << 31)) return MUON_ERR_UNSUPPORTED;
   int sms = 0;
   if (int rc = require_device(&sms)) return rc;
