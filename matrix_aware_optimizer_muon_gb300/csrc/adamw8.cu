@@ -6,6 +6,7 @@
 // update itself is adamw.cu's:
 //   m <- b1*m + (1-b1)*g;  v <- b2*v + (1-b2)*g^2;
 //   p <- p - lr*( (m/(1-b1^t)) / (sqrt(v/(1-b2^t)) + eps) + wd*p ).
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstring>
@@ -32,10 +33,11 @@ struct Adamw8Params {
   Adamw8Entry e[A8_MAX_PARAMS];
   int n;
   uint32_t key;        // from (seed, t)
-  float lr, beta1, beta2, eps, wd;
-  float omb1, omb2;    // 1 - beta1, 1 - beta2, formed in double precision on the host
-  float inv_bc1;       // 1 / (1 - beta1^t)
-  float inv_sqrt_bc2;  // 1 / sqrt(1 - beta2^t)
+  // each number twice, as the operand of a paired instruction
+  f32x2 neg_lr, beta1, beta2, eps, wd;
+  f32x2 omb1, omb2;    // 1 - beta1, 1 - beta2, formed in double precision on the host
+  f32x2 inv_bc1;       // 1 / (1 - beta1^t)
+  f32x2 root;          // 2^-12 / sqrt(1 - beta2^t)
 };
 static_assert(sizeof(Adamw8Params) < 32000, "Adamw8Params too large");
 
@@ -78,26 +80,51 @@ __device__ __forceinline__ uint32_t encode_v(float v, uint32_t base, uint32_t r)
   return (uint32_t)min(max(k, a ? 1 : 0), 255);
 }
 
-// Bandwidth-bound: 10 bytes an element for bf16 parameters and gradients (2+2 P, 2 G, 1+1
-// a moment's codes twice).  A thread owns 16 consecutive elements, so that every array is
-// read and written in whole 16- or 32-byte vectors; 8 threads make a block of 128, whose
-// two maxima take three shuffles each, and no value passes through shared memory.
+// 10 bytes an element for bf16 parameters and gradients (2+2 P, 2 G, 1+1 a moment's codes
+// twice): at HBM's rate an SM has 54 issue slots and 27 of the integer pipe an element,
+// and the coding is integer work, so instructions count.  A thread owns 16 consecutive
+// elements: whole 16- and 32-byte vectors, 8 threads a block of 128 (a maximum takes three
+// shuffles), no shared memory.  The common case is coded without selects:
+//   decoding   byte * 2^20 + base (a multiply-add), the sign as a factor +-1;
+//   encoding   |m| * 16 + random * 256 - base * 2^24 leaves the code in the top byte,
+//              which byte permutes collect;
+// zero codes, numbers below a block's least, NaN and Inf are found by a test per thread and
+// sent through the plain functions above.
 constexpr int A8_THREADS = 256;
 constexpr int A8_EACH = 16;
+constexpr int A8_WORDS = A8_EACH / 4;      // of a moment's codes
 constexpr int A8_CHUNK = A8_THREADS * A8_EACH;
 
 // 16 elements as loaded, converted later, so that all of a thread's loads are in flight.
-template <typename T> struct Raw16 { uint32_t w[4 * sizeof(T)]; };
-template <typename T>
-__device__ __forceinline__ void ld16(const T* p, Raw16<T>& r) {
+template <int kWords>
+__device__ __forceinline__ void load_words(const void* p, uint32_t* w) {
+  if constexpr (kWords == 4) {
+    const uint4 q = *static_cast<const uint4*>(p);
+    w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+  } else {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) ld_v8(reinterpret_cast<const uint8_t*>(p) + 32 * i, r.w + 8 * i);
+    for (int i = 0; i < kWords / 8; ++i) ld_v8(static_cast<const uint8_t*>(p) + 32 * i, w + 8 * i);
+  }
+}
+template <int kWords>
+__device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
+  if constexpr (kWords == 4) {
+    *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kWords / 8; ++i) st_v8(static_cast<uint8_t*>(p) + 32 * i, w + 8 * i);
+  }
+}
+template <typename T> struct RawN { uint32_t w[A8_EACH * sizeof(T) / 4]; };
+template <typename T>
+__device__ __forceinline__ void ld_all(const T* p, RawN<T>& r) {
+  load_words<A8_EACH * sizeof(T) / 4>(p, r.w);
 }
 template <typename T>
-__device__ __forceinline__ void ld16_some(const T* p, int n, Raw16<T>& r) {
+__device__ __forceinline__ void ld_some(const T* p, int n, RawN<T>& r) {
 #pragma unroll
   for (int i = 0; i < A8_EACH; ++i) {
-    if (sizeof(T) == 4) {
+    if constexpr (sizeof(T) == 4) {
       r.w[i] = i < n ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
     } else {
       const uint32_t h = i < n ? reinterpret_cast<const uint16_t*>(p)[i] : 0u;
@@ -105,140 +132,299 @@ __device__ __forceinline__ void ld16_some(const T* p, int n, Raw16<T>& r) {
     }
   }
 }
+// elements 2j and 2j + 1
 template <typename T>
-__device__ __forceinline__ float get16(const Raw16<T>& r, int i) {
-  if (sizeof(T) == 4) return __uint_as_float(r.w[i]);
-  return __uint_as_float(i & 1 ? r.w[i / 2] & 0xFFFF0000u : r.w[i / 2] << 16);
+__device__ __forceinline__ f32x2 get2(const RawN<T>& r, int j) {
+  if constexpr (sizeof(T) == 4) return make2(__uint_as_float(r.w[2 * j]), __uint_as_float(r.w[2 * j + 1]));
+  else return cvt2(r.w[j]);
 }
 template <typename T>
-__device__ __forceinline__ void st16(T* p, const float (&v)[A8_EACH]) {
-  uint32_t w[4 * sizeof(T)];
+__device__ __forceinline__ void st_all(T* p, const f32x2 (&v)[A8_EACH / 2]) {
+  uint32_t w[A8_EACH * sizeof(T) / 4];
 #pragma unroll
-  for (int i = 0; i < (int)(4 * sizeof(T)); ++i)
-    w[i] = sizeof(T) == 4 ? __float_as_uint(v[i % A8_EACH]) : pack_bf16x2(v[(2 * i) % A8_EACH], v[(2 * i + 1) % A8_EACH]);
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) st_v8(reinterpret_cast<uint8_t*>(p) + 32 * i, w + 8 * i);
+  for (int j = 0; j < A8_EACH / 2; ++j) {
+    if constexpr (sizeof(T) == 4) {
+      w[2 * j] = __float_as_uint(lo2(v[j]));
+      w[2 * j + 1] = __float_as_uint(hi2(v[j]));
+    } else {
+      w[j] = pack_bf16x2(lo2(v[j]), hi2(v[j]));
+    }
+  }
+  store_words<A8_EACH * sizeof(T) / 4>(p, w);
 }
 
-// Square root and quotient of the update: the hardware's approximations (2 ulp at most);
+// Square root and reciprocal of the update: the hardware's approximations (2 ulp at most);
 // what they feed is lr times a number near 1, added to a parameter of 24 or 8 bits.
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-__device__ __forceinline__ uint32_t max_of_8(uint32_t x) {
+// Largest and smallest magnitude of three (a NaN makes the largest NaN).
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float min3_abs(float a, float b, float c) {
+  float y;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// over the threads of a block of codes
+__device__ __forceinline__ uint32_t max_of_block(uint32_t x) {
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+  for (int o = A8_BLOCK / A8_EACH / 2; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
+// nonzero if a byte of w is zero
+__device__ __forceinline__ uint32_t zero_byte(uint32_t w) { return (w - 0x01010101u) & ~w & 0x80808080u; }
+__device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return __byte_perm(w, 0, 0x4440 | i); }
+// byte i of w as a code counted from base
+__device__ __forceinline__ float code_bits(uint32_t w, int i, uint32_t base) {
+  return __uint_as_float(byte_of(w, i) * 0x100000u + (base << 20));
+}
+// the top bytes of four words
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
 
-template <typename PT, typename GT>
-__global__ void __launch_bounds__(A8_THREADS) adamw8_kernel(const __grid_constant__ Adamw8Params q) {
-  int lo = 0, hi = q.n - 1;
-  const int b = blockIdx.x;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (q.e[mid].block_begin <= b) lo = mid; else hi = mid - 1;
-  }
-  const Adamw8Entry& e = q.e[lo];
-  const long long i0 = (long long)(b - e.block_begin) * A8_CHUNK + threadIdx.x * A8_EACH;
-  const long long blk = i0 / A8_BLOCK;
-  // past the last block of codes: nothing to do, but the shuffles below need the thread
-  const bool codes = i0 < (e.numel + A8_BLOCK - 1) / A8_BLOCK * A8_BLOCK;
-  const int n = (int)min(max(e.numel - i0, 0LL), (long long)A8_EACH);
-  PT* P = reinterpret_cast<PT*>(e.P) + i0;
-  const GT* G = reinterpret_cast<const GT*>(e.G) + i0;
-  const bool whole = n == A8_EACH && e.vec;
-  Raw16<PT> pr;
-  Raw16<GT> gr;
-  uint4 mc = make_uint4(0, 0, 0, 0), vc = mc;
-  int ms = 0, vs = 0;
-  if (codes) {
-    mc = *reinterpret_cast<const uint4*>(e.m + i0);
-    vc = *reinterpret_cast<const uint4*>(e.v + i0);
-    ms = e.ms[blk];
-    vs = e.vs[blk];
-  }
-  if (whole) {
-    ld16(P, pr);
-    ld16(G, gr);
-  } else {
-    ld16_some(P, n, pr);
-    ld16_some(G, n, gr);
-  }
-  float m[A8_EACH], v[A8_EACH], p[A8_EACH];
-  uint32_t mtop = 0, vtop = 0;
-  {
-    const uint32_t bm = base_m(ms), bv = base_v(vs);
-    const uint32_t mw[4] = {mc.x, mc.y, mc.z, mc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
+// The uncommon cases, out of line so that they hold no registers of the common one.
+struct CodesN {
+  uint32_t m[A8_WORDS], v[A8_WORDS];
+};
+struct MomentsN {
+  f32x2 m[A8_EACH / 2], v[A8_EACH / 2];
+};
+__device__ __noinline__ MomentsN decode_any(const CodesN c, uint32_t bm, uint32_t bv) {
+  MomentsN o;
 #pragma unroll
-    for (int i = 0; i < A8_EACH; ++i) {
-      const float g = get16(gr, i);
-      m[i] = q.beta1 * decode_m((mw[i / 4] >> (8 * (i % 4))) & 255u, bm) + q.omb1 * g;
-      v[i] = q.beta2 * decode_v((vw[i / 4] >> (8 * (i % 4))) & 255u, bv) + q.omb2 * g * g;
-      p[i] = get16(pr, i);
-      p[i] -= q.lr * (__fdividef(m[i] * q.inv_bc1, sqrt_approx(v[i]) * q.inv_sqrt_bc2 + q.eps) + q.wd * p[i]);
-      // codes past the end stay 0; a NaN is kept in m; infinite squares hold the largest code
-      if (i >= n) m[i] = v[i] = 0.f;
-      v[i] = v[i] != v[i] ? 0.f : fminf(v[i], FLT_MAX);
-      const uint32_t a = __float_as_uint(m[i]) & 0x7FFFFFFFu;
-      mtop = max(mtop, a < 0x7F800000u ? a : 0u);
-      vtop = max(vtop, __float_as_uint(v[i]));
-    }
+  for (int j = 0; j < A8_EACH / 2; ++j) {
+    const int i = 2 * (j % 2);
+    o.m[j] = make2(decode_m(byte_of(c.m[j / 2], i), bm), decode_m(byte_of(c.m[j / 2], i + 1), bm));
+    o.v[j] = make2(decode_v(byte_of(c.v[j / 2], i), bv), decode_v(byte_of(c.v[j / 2], i + 1), bv));
   }
-  if (whole) {
-    st16(P, p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < A8_EACH; ++i)
-      if (i < n) st1(P + i, p[i]);
-  }
-  ms = scale_of(max_of_8(mtop));
-  vs = scale_of(max_of_8(vtop));
-  if (!codes) return;
-  const uint32_t bm = base_m(ms), bv = base_v(vs);
-  const unsigned long long at = (unsigned long long)(e.first + i0);
-  const uint32_t key = mix32(q.key + (uint32_t)(at >> 32));
-  uint32_t mw[4] = {}, vw[4] = {};
+  return o;
+}
+__device__ __forceinline__ float element(const f32x2 (&a)[A8_EACH / 2], int i) {
+  return i & 1 ? hi2(a[i / 2]) : lo2(a[i / 2]);
+}
+// NaN and Inf stay out of the block's scales: a NaN is kept in m, an infinite square holds
+// the largest code.
+__device__ __forceinline__ float held(float v) { return v != v ? 0.f : fminf(v, FLT_MAX); }
+__device__ __noinline__ uint2 finite_tops(const MomentsN x) {
+  uint2 t = make_uint2(0, 0);
 #pragma unroll
   for (int i = 0; i < A8_EACH; ++i) {
-    const uint32_t r = mix32(((uint32_t)at + i) ^ key);
-    mw[i / 4] |= encode_m(m[i], bm, r & 0xFFFFu) << (8 * (i % 4));
-    vw[i / 4] |= encode_v(v[i], bv, r >> 16) << (8 * (i % 4));
+    const uint32_t a = __float_as_uint(element(x.m, i)) & 0x7FFFFFFFu;
+    t.x = max(t.x, a < 0x7F800000u ? a : 0u);
+    t.y = max(t.y, __float_as_uint(held(element(x.v, i))));
   }
-  *reinterpret_cast<uint4*>(e.m + i0) = make_uint4(mw[0], mw[1], mw[2], mw[3]);
-  *reinterpret_cast<uint4*>(e.v + i0) = make_uint4(vw[0], vw[1], vw[2], vw[3]);
-  if ((threadIdx.x & 7) == 0) {
-    e.ms[blk] = (uint8_t)ms;
-    e.vs[blk] = (uint8_t)vs;
+  return t;
+}
+__device__ __noinline__ CodesN encode_any(const MomentsN x, uint32_t bm, uint32_t bv, uint32_t x0) {
+  CodesN c = {};
+#pragma unroll
+  for (int i = 0; i < A8_EACH; ++i) {
+    uint32_t r = (x0 ^ i) * 0x9E3779B9u;
+    r = (r ^ (r >> 15)) * 0x6A09E667u;
+    r ^= r >> 16;
+    c.m[i / 4] |= encode_m(element(x.m, i), bm, r & 0xFFFFu) << (8 * (i % 4));
+    c.v[i / 4] |= encode_v(held(element(x.v, i)), bv, r >> 16) << (8 * (i % 4));
+  }
+  return c;
+}
+
+// CTAs an SM should hold.  Measured on 335 M bf16 elements (step and unpacking together):
+// four 879 us, three 967, two 1134; 8 elements a thread and six CTAs 900.
+constexpr int a8_ctas(int bytes) { return bytes == 4 ? 4 : 3; }
+template <typename PT, typename GT>
+__global__ void __launch_bounds__(A8_THREADS, a8_ctas(sizeof(PT) + sizeof(GT)))
+    adamw8_kernel(const __grid_constant__ Adamw8Params q) {
+  const int b = blockIdx.x;
+  int lo = 0;
+  if (q.n <= 4) {
+#pragma unroll
+    for (int i = 1; i < 4; ++i) lo += i < q.n && q.e[i].block_begin <= b;
+  } else {
+    int hi = q.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (q.e[mid].block_begin <= b) lo = mid; else hi = mid - 1;
+    }
+  }
+  const Adamw8Entry& e = q.e[lo];
+  // what the whole CTA shares is 64 bits wide, a thread's place in its chunk 32
+  const long long c0 = (long long)(b - e.block_begin) * A8_CHUNK;
+  const int left = (int)min(e.numel - c0, (long long)A8_CHUNK);
+  const int off = threadIdx.x * A8_EACH;
+  const int n = min(max(left - off, 0), A8_EACH);
+  // past the last block of codes: nothing to do, but the shuffles below need the thread
+  const bool codes = off < (left + A8_BLOCK - 1) / A8_BLOCK * A8_BLOCK;
+  PT* P = reinterpret_cast<PT*>(e.P) + c0;
+  const GT* G = reinterpret_cast<const GT*>(e.G) + c0;
+  uint8_t *mp = e.m + c0, *vp = e.v + c0, *msp = e.ms + c0 / A8_BLOCK, *vsp = e.vs + c0 / A8_BLOCK;
+  const bool whole = n == A8_EACH && e.vec;
+  RawN<PT> pr;
+  RawN<GT> gr;
+  CodesN codes_n = {};
+  uint32_t (&mw)[A8_WORDS] = codes_n.m, (&vw)[A8_WORDS] = codes_n.v;
+  int ms = 0, vs = 0;
+  if (codes) {
+    load_words<A8_WORDS>(mp + off, mw);
+    load_words<A8_WORDS>(vp + off, vw);
+    ms = msp[off / A8_BLOCK];
+    vs = vsp[off / A8_BLOCK];
+  }
+  if (whole) {
+    ld_all(P + off, pr);
+    ld_all(G + off, gr);
+  } else {
+    ld_some(P + off, n, pr);
+    ld_some(G + off, n, gr);
+  }
+  MomentsN now;
+  f32x2 (&m2)[A8_EACH / 2] = now.m, (&v2)[A8_EACH / 2] = now.v;
+  {
+    const uint32_t bm = base_m(ms), bv = base_v(vs);
+    uint32_t zeros = 0;
+#pragma unroll
+    for (int k = 0; k < A8_WORDS; ++k) {
+      const uint32_t mag = mw[k] & 0x7F7F7F7Fu, one = (mw[k] & 0x80808080u) | 0x3F3F3F3Fu;
+      zeros |= zero_byte(mag) | zero_byte(vw[k]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = 2 * h;
+        // +-1: top byte 0x3F or 0xBF, then 0x80
+        m2[2 * k + h] = mul2(make2(code_bits(mag, i, bm), code_bits(mag, i + 1, bm)),
+                             make2(__uint_as_float(__byte_perm(one, 0x80u, 0x0455 | (i << 12))),
+                                   __uint_as_float(__byte_perm(one, 0x80u, 0x0455 | ((i + 1) << 12)))));
+        v2[2 * k + h] = make2(code_bits(vw[k], i, bv), code_bits(vw[k], i + 1, bv));
+      }
+    }
+    if (zeros) now = decode_any(codes_n, bm, bv);
+  }
+  f32x2 p[A8_EACH / 2];
+#pragma unroll
+  for (int j = 0; j < A8_EACH / 2; ++j) {
+    const f32x2 g = get2(gr, j);
+    m2[j] = fma2(q.beta1, m2[j], mul2(q.omb1, g));
+    v2[j] = fma2(q.beta2, v2[j], mul2(mul2(q.omb2, g), g));
+    // the root of 2^24 v: the approximation flushes what is below 2^-126
+    const f32x2 x = mul2(v2[j], both(0x1p24f));
+    const f32x2 d = fma2(make2(sqrt_approx(lo2(x)), sqrt_approx(hi2(x))), q.root, q.eps);
+    p[j] = get2(pr, j);
+    const f32x2 u = mul2(mul2(m2[j], q.inv_bc1), make2(rcp_approx(lo2(d)), rcp_approx(hi2(d))));
+    p[j] = fma2(q.neg_lr, fma2(q.wd, p[j], u), p[j]);
+  }
+  if (whole) {
+    st_all(P + off, p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < A8_EACH; ++i) {
+      if (i < n) {
+        st1(P + off + i, i & 1 ? hi2(p[i / 2]) : lo2(p[i / 2]));
+      } else {   // codes past the end stay 0
+        m2[i / 2] = i & 1 ? make2(lo2(m2[i / 2]), 0.f) : make2(0.f, hi2(m2[i / 2]));
+        v2[i / 2] = i & 1 ? make2(lo2(v2[i / 2]), 0.f) : make2(0.f, hi2(v2[i / 2]));
+      }
+    }
+  }
+  float mt = 0.f, vt = 0.f, mlow = INFINITY, vlow = INFINITY;
+#pragma unroll
+  for (int j = 0; j < A8_EACH / 2; ++j) {
+    mt = max3_abs(mt, lo2(m2[j]), hi2(m2[j]));
+    vt = max3_abs(vt, lo2(v2[j]), hi2(v2[j]));
+    mlow = min3_abs(mlow, lo2(m2[j]), hi2(m2[j]));
+    vlow = min3_abs(vlow, lo2(v2[j]), hi2(v2[j]));
+  }
+  uint32_t mtop = __float_as_uint(mt), vtop = __float_as_uint(vt);
+  const bool odd = max(mtop, vtop) >= 0x7F800000u;
+  if (odd) {
+    const uint2 t = finite_tops(now);
+    mtop = t.x;
+    vtop = t.y;
+  }
+  ms = scale_of(max_of_block(mtop));
+  vs = scale_of(max_of_block(vtop));
+  if (!codes) return;
+  const uint32_t bm = base_m(ms), bv = base_v(vs);
+  const unsigned long long at = (unsigned long long)(e.first + c0);
+  // mix32 of (at + i) ^ key: i is in the lowest bits, so its first xor-shift is shared
+  uint32_t key = mix32(q.key + (uint32_t)(at >> 32));
+  const uint32_t low = (uint32_t)at + off;
+  if (low < (uint32_t)at) key = mix32(q.key + (uint32_t)(at >> 32) + 1u);
+  uint32_t x0 = low ^ key;
+  x0 ^= x0 >> 16;
+  // a block at the end of fp32's range is the one whose codes can pass the top
+  if (odd || __float_as_uint(mlow) < ((bm + 1) << 20) || __float_as_uint(vlow) < ((bv + 1) << 20) || ms == 255 || vs == 255) {
+    codes_n = encode_any(now, bm, bv, x0);
+  } else {
+    const uint32_t km = 128u - (bm << 24), kv = 128u - (bv << 24);   // half of the random bits' last place
+#pragma unroll
+    for (int k = 0; k < A8_WORDS; ++k) {
+      uint32_t a[4], c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t x = (x0 ^ (4 * k + i)) * 0x9E3779B9u;
+        x = (x ^ (x >> 15)) * 0x6A09E667u;
+        const uint32_t up = x >> 16, down = (x ^ up) & 0xFFFFu;
+        a[i] = __float_as_uint(element(m2, 4 * k + i)) * 16u + (down * 256u + km);   // the sign is shifted out
+        c[i] = __float_as_uint(element(v2, 4 * k + i)) * 16u + (up * 256u + kv);
+      }
+      const uint32_t sgn = top_bytes(__float_as_uint(lo2(m2[2 * k])), __float_as_uint(hi2(m2[2 * k])),
+                                     __float_as_uint(lo2(m2[2 * k + 1])), __float_as_uint(hi2(m2[2 * k + 1])));
+      mw[k] = top_bytes(a[0], a[1], a[2], a[3]) | (sgn & 0x80808080u);
+      vw[k] = top_bytes(c[0], c[1], c[2], c[3]);
+    }
+  }
+  store_words<A8_WORDS>(mp + off, mw);
+  store_words<A8_WORDS>(vp + off, vw);
+  if (threadIdx.x % (A8_BLOCK / A8_EACH) == 0) {
+    msp[off / A8_BLOCK] = (uint8_t)ms;
+    vsp[off / A8_BLOCK] = (uint8_t)vs;
   }
 }
 
-// 16 codes of one moment per thread: 16 bytes in, 32 out.
+// 16 codes of one moment per thread: 16 bytes in, 32 out.  The values are the top halves of
+// their fp32 bits.
 template <bool kFirst>
-__device__ __forceinline__ void unpack16(const uint8_t* c, const uint8_t* s, bf16* out, long long i0) {
-  const uint4 w4 = *reinterpret_cast<const uint4*>(c + i0);
-  const int sc = s[i0 / A8_BLOCK];
+__device__ __forceinline__ void unpack16(const uint4 w4, int sc, bf16* out) {
   const uint32_t base = kFirst ? base_m(sc) : base_v(sc);
   const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-  float v[A8_EACH];
+  uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < A8_EACH; ++i) {
-    const uint32_t k = (w[i / 4] >> (8 * (i % 4))) & 255u;
-    v[i] = kFirst ? decode_m(k, base) : decode_v(k, base);
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t c = byte_of(w[j / 2], 2 * (j % 2)), d = byte_of(w[j / 2], 2 * (j % 2) + 1);
+    o[j] = __byte_perm(__float_as_uint(kFirst ? decode_m(c, base) : decode_v(c, base)),
+                       __float_as_uint(kFirst ? decode_m(d, base) : decode_v(d, base)), 0x7632);
   }
-  st16(out + i0, v);
+  st_v8(out, o);
 }
 __global__ void __launch_bounds__(256) adamw8_unpack_kernel(const uint8_t* m, const uint8_t* ms, const uint8_t* v,
                                                             const uint8_t* vs, long long numel, bf16* mo, bf16* vo) {
-  const long long i0 = ((long long)blockIdx.x * 256 + threadIdx.x) * A8_EACH;
+  const long long i0 = ((long long)blockIdx.x * 256 + threadIdx.x) * 16;
   if (i0 >= numel) return;
-  if (m) unpack16<true>(m, ms, mo, i0);
-  if (v) unpack16<false>(v, vs, vo, i0);
+  uint4 mc = {}, vc = {};
+  int sm = 0, sv = 0;
+  if (m) { mc = *reinterpret_cast<const uint4*>(m + i0); sm = ms[i0 / A8_BLOCK]; }
+  if (v) { vc = *reinterpret_cast<const uint4*>(v + i0); sv = vs[i0 / A8_BLOCK]; }
+  if (m) unpack16<true>(mc, sm, mo + i0);
+  if (v) unpack16<false>(vc, sv, vo + i0);
 }
 
+f32x2 twice(float x) {
+  uint32_t w;
+  std::memcpy(&w, &x, 4);
+  return f32x2{(uint64_t)w << 32 | w};
+}
 bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t dt_size(int dt) { return dt == MUON_DTYPE_BF16 ? 2 : 4; }
 
@@ -277,15 +463,15 @@ extern "C" int muon_adamw8_step(const muon_adamw8_param* params, int n, int64_t 
   int i = 0;
   while (i < n) {
     q.key = mix32(seed ^ mix32((uint32_t)t));
-    q.lr = lr;
-    q.beta1 = (float)beta1;
-    q.beta2 = (float)beta2;
-    q.omb1 = (float)(1.0 - beta1);
-    q.omb2 = (float)(1.0 - beta2);
-    q.eps = eps;
-    q.wd = weight_decay;
-    q.inv_bc1 = (float)(1.0 / bc1);
-    q.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bc2));
+    q.neg_lr = twice(-lr);
+    q.beta1 = twice((float)beta1);
+    q.beta2 = twice((float)beta2);
+    q.omb1 = twice((float)(1.0 - beta1));
+    q.omb2 = twice((float)(1.0 - beta2));
+    q.eps = twice(eps);
+    q.wd = twice(weight_decay);
+    q.inv_bc1 = twice((float)(1.0 / bc1));
+    q.root = twice((float)(0x1p-12 / std::sqrt(bc2)));
     int j = 0;
     long long blocks = 0;
     for (; i < n && j < A8_MAX_PARAMS; ++i) {
@@ -322,7 +508,7 @@ extern "C" int muon_adamw8_unpack(const uint8_t* m, const uint8_t* m_scale, cons
   if (!is_aligned(m, 16) || !is_aligned(v, 16) || !is_aligned(m_out, 32) || !is_aligned(v_out, 32))
     return MUON_ERR_INVALID;
   if (numel == 0 || (!m && !v)) return MUON_OK;
-  const long long blocks = (numel / A8_EACH + 255) / 256;
+  const long long blocks = (numel / 16 + 255) / 256;
   if (blocks >= (1LL << 31)) return MUON_ERR_UNSUPPORTED;
   int sms = 0;
   if (int rc = require_device(&sms)) return rc;

@@ -47,11 +47,49 @@ __device__ __forceinline__ void ld4_stream(const bf16* p, float v[4]) {
   v[3] = __uint_as_float(x.y & 0xFFFF0000u);
 }
 
+// Two roundings in one conversion (two scalar ones take two slots of the 16-lane
+// special-function pipe).
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  uint32_t a = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
-  uint32_t b = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
-  return a | (b << 16);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
+
+// Pairs of fp32 numbers: one instruction for both (sm_100 and later).
+struct f32x2 {
+  uint64_t v;
+};
+__device__ __forceinline__ f32x2 make2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float a) { return make2(a, a); }
+__device__ __forceinline__ float lo2(f32x2 a) {
+  return __uint_as_float((uint32_t)a.v);
+}
+__device__ __forceinline__ float hi2(f32x2 a) {
+  return __uint_as_float((uint32_t)(a.v >> 32));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// the two bf16 numbers of a word
+__device__ __forceinline__ f32x2 cvt2(uint32_t w) {
+  return make2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
 __device__ __forceinline__ void st4(float* p, const float v[4]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }

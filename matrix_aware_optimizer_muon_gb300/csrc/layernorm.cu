@@ -30,50 +30,101 @@ __device__ __forceinline__ void st_w(void* w, int w_bf16, int c, float v) {
   else static_cast<float*>(w)[c] = v;
 }
 
-// kV consecutive elements: 16 bytes, or one element.
-template <typename T, int kV> struct Pack;
-template <typename T> struct Pack<T, 1> {
-  T v;
-  __device__ __forceinline__ void load(const T* p) { v = *p; }
-  __device__ __forceinline__ float get(int) const { return to_f32(v); }
-  __device__ __forceinline__ void put(const float (&x)[1]) { v = from_f32<T>(x[0]); }
-  __device__ __forceinline__ void store(T* p) const { *p = v; }
-};
-template <> struct Pack<float, 4> {
-  float4 v;
-  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
-  __device__ __forceinline__ float get(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-  __device__ __forceinline__ void put(const float (&x)[4]) { v = make_float4(x[0], x[1], x[2], x[3]); }
-  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = v; }
-};
-template <> struct Pack<bf16, 8> {
-  uint32_t w[4];
-  __device__ __forceinline__ void load(const bf16* p) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
-  }
-  __device__ __forceinline__ float get(int i) const {
-    return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-  }
-  __device__ __forceinline__ void put(const float (&x)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-  }
-  __device__ __forceinline__ void store(bf16* p) const { *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]); }
+// A thread's share of a row: kN accesses of kV elements (16 bytes, or one element),
+// `stride` elements apart, as pairs.  What lies past the row reads as zero.
+template <int kV, int kN> struct Share {
+  static constexpr int E = kV * kN;
+  static constexpr int P = (E + 1) / 2;
 };
 template <typename T> constexpr int vec_of() { return 16 / (int)sizeof(T); }
+__device__ __forceinline__ float elem(const f32x2* v, int i) { return i & 1 ? hi2(v[i / 2]) : lo2(v[i / 2]); }
 
-// kV consecutive weights (with kV > 1 their vectors are aligned too).
-template <int kV>
-__device__ __forceinline__ void ld_wv(const void* w, int w_bf16, int c, float (&o)[kV]) {
-  if (kV == 1) {
-    o[0] = ld_w(w, w_bf16, c);
-  } else if (w_bf16) {
+// 16 bytes of the row as loaded, to pairs.
+__device__ __forceinline__ void widen(const uint4& q, f32x2* v, const bf16*) {
+  v[0] = cvt2(q.x); v[1] = cvt2(q.y); v[2] = cvt2(q.z); v[3] = cvt2(q.w);
+}
+__device__ __forceinline__ void widen(const uint4& q, f32x2* v, const float*) {
+  v[0] = make2(__uint_as_float(q.x), __uint_as_float(q.y));
+  v[1] = make2(__uint_as_float(q.z), __uint_as_float(q.w));
+}
+__device__ __forceinline__ void store16(bf16* p, const f32x2* v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(lo2(v[0]), hi2(v[0])), pack_bf16x2(lo2(v[1]), hi2(v[1])),
+                                            pack_bf16x2(lo2(v[2]), hi2(v[2])), pack_bf16x2(lo2(v[3]), hi2(v[3])));
+}
+__device__ __forceinline__ void store16(float* p, const f32x2* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(lo2(v[0]), hi2(v[0]), lo2(v[1]), hi2(v[1]));
+}
+
+// The row's raw registers, all loads in flight together.
+template <typename T, int kV, int kN> struct Raw {
+  uint4 q[kN];
+  template <int kSure = 0>
+  __device__ __forceinline__ void load(const T* x, int t, int size, int dim) {
 #pragma unroll
-    for (int i = 0; i < kV / 4; ++i) ld4(static_cast<const bf16*>(w) + c + 4 * i, o + 4 * i);
+    for (int k = 0; k < kN; ++k) {
+      const int c = (k * size + t) * kV;
+      q[k] = k < kSure || c < dim ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void get(int k, f32x2* v) const { widen(q[k], v, static_cast<const T*>(nullptr)); }
+  // keeps the compiler from holding widened values across this point
+  __device__ __forceinline__ void hold() {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) asm volatile("" : "+r"(q[k].x), "+r"(q[k].y), "+r"(q[k].z), "+r"(q[k].w));
+  }
+};
+template <typename T, int kN> struct Raw<T, 1, kN> {
+  T e[kN];
+  template <int kSure = 0>
+  __device__ __forceinline__ void load(const T* x, int t, int size, int dim) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) e[k] = k * size + t < dim ? x[k * size + t] : from_f32<T>(0.f);
+  }
+  __device__ __forceinline__ void get(int k, f32x2* v) const { v[0] = make2(to_f32(e[k]), 0.f); }
+  __device__ __forceinline__ void hold() {}
+  __device__ __forceinline__ void pairs(f32x2* v) const {
+#pragma unroll
+    for (int k = 0; k < kN; k += 2) v[k / 2] = make2(to_f32(e[k]), k + 1 < kN ? to_f32(e[(k + 1) % kN]) : 0.f);
+  }
+};
+template <typename T, int kV, int kN>
+__device__ __forceinline__ void store_row(T* y, const f32x2* v, int t, int size, int dim) {
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const int c = (k * size + t) * kV;
+    if (c < dim) {
+      if constexpr (kV > 1) store16(y + c, v + k * (kV / 2));
+      else st1(y + c, elem(v, k));
+    }
+  }
+}
+
+// What the weights are: asked at run time, or known to be all there in one type (the
+// forward pass's common cases: asking costs it a sixth of its instructions).
+enum { W_ASK = 0, W_F32 = 1, W_BF16 = 2 };
+
+// The weights of access k (with kV > 1 their vectors are aligned too); `none` without any.
+template <int kV, int kW = W_ASK>
+__device__ __forceinline__ void weights(const void* w, int w_bf16, int c, int dim, float none, f32x2* v) {
+  if constexpr (kV == 1) {
+    v[0] = both(c < dim ? (w ? ld_w(w, w_bf16, c) : none) : 0.f);
+  } else if (kW == W_ASK && (c >= dim || !w)) {
+#pragma unroll
+    for (int i = 0; i < kV / 2; ++i) v[i] = both(c < dim ? none : 0.f);
+  } else if (kW == W_BF16 || (kW == W_ASK && w_bf16)) {
+#pragma unroll
+    for (int i = 0; i < kV / 4; ++i) {
+      const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(w) + c + 4 * i);
+      v[2 * i] = cvt2(q.x);
+      v[2 * i + 1] = cvt2(q.y);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < kV / 4; ++i) ld4(static_cast<const float*>(w) + c + 4 * i, o + 4 * i);
+    for (int i = 0; i < kV / 4; ++i) {
+      const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + 4 * i);
+      v[2 * i] = make2(q.x, q.y);
+      v[2 * i + 1] = make2(q.z, q.w);
+    }
   }
 }
 
@@ -82,15 +133,22 @@ struct Group {
   int t, size, id;       // thread, threads, barrier (0: the whole CTA's)
   float* red;            // 2 x 32 floats
   __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(size) : "memory"); }
+  // Sums of a and b over the group.  The halves of a warp take one of the two each after the
+  // first exchange; the warps' sums are added in order by everyone.
   __device__ __forceinline__ float2 sum(float a, float b, int parity) const {
-    a = warp_sum(a);
-    b = warp_sum(b);
+    const bool up = t & 16;
+    float v = up ? b : a;
+    v += __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (size == 32) return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
     // two buffers in turn: a warp may be one reduction ahead of the slowest
-    float2* slot = reinterpret_cast<float2*>(red) + 32 * parity;
-    if ((t & 31) == 0) slot[t >> 5] = make_float2(a, b);
+    float* slot = red + 64 * parity;
+    if ((t & 15) == 0) slot[t >> 4] = v;
     sync();
-    const float2 q = (t & 31) < (size >> 5) ? slot[t & 31] : make_float2(0.f, 0.f);
-    return make_float2(warp_sum(q.x), warp_sum(q.y));
+    f32x2 q = both(0.f);
+    for (int i = 0; i < size >> 5; ++i) q = add2(q, *reinterpret_cast<const f32x2*>(slot + 2 * i));
+    return make_float2(lo2(q), hi2(q));
   }
 };
 
@@ -103,50 +161,65 @@ struct LnFwd {
   float eps;
 };
 
-template <typename T, int kV, int kN, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * LN_WARPS : 1024) ln_forward_kernel(const LnFwd p) {
-  __shared__ float red[kWarp ? 1 : 128];
+// kSure: how many of a thread's accesses lie inside the row for every thread.
+__host__ __device__ constexpr int ln_sure(int n) { return n <= 8 ? n - 1 : n <= 12 ? n - 2 : n - 4; }
+// CTAs of a warp-a-row kernel an SM should hold: registers for the row and about 32 more.
+constexpr int ln_fwd_ctas(int n, bool warp) { return warp ? 256 / (4 * n + 32) : 1; }
+template <typename T, int kV, int kN, bool kWarp, int kW>
+__global__ void __launch_bounds__(kWarp ? 32 * LN_WARPS : 1024, ln_fwd_ctas(kN, kWarp)) ln_forward_kernel(const LnFwd p) {
+  constexpr int kSure = kWarp && kV > 1 ? ln_sure(kN) : 0;
+  __shared__ __align__(8) float red[kWarp ? 2 : 128];
   const int t = kWarp ? threadIdx.x & 31 : threadIdx.x, size = kWarp ? 32 : blockDim.x;
   const long long r = kWarp ? (long long)blockIdx.x * LN_WARPS + (threadIdx.x >> 5) : blockIdx.x;
   if (kWarp && r >= p.rows) return;
   const Group grp{t, size, 0, red};
   const T* x = static_cast<const T*>(p.x) + r * p.ldx;
   T* y = static_cast<T*>(p.y) + r * p.ldy;
-  Pack<T, kV> raw[kN];
-#pragma unroll
-  for (int k = 0; k < kN; ++k)
-    if ((k * size + t) * kV < p.dim) raw[k].load(x + (k * size + t) * kV);
+  using S = Share<kV, kN>;
+  // The row stays in registers as loaded and is widened again for each of the three
+  // passes: held as fp32 pairs it would leave room for half as many warps (measured on
+  // 32768 x 1536 bf16: 53 us instead of WIDEN).
+  Raw<T, kV, kN> raw;
+  raw.template load<kSure>(x, t, size, p.dim);
+  constexpr int C = kV == 1 ? 1 : kV / 2;   // pairs of an access
   const float inv = 1.f / (float)p.dim;
-  float s = 0.f;
+  f32x2 s = both(0.f), q = both(0.f);
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    f32x2 v[C];
+    raw.get(k, v);
+#pragma unroll
+    for (int i = 0; i < C; ++i) s = add2(s, v[i]);
+  }
+  const float sum = lo2(s) + hi2(s);
+  const float mu = (kWarp ? warp_sum(sum) : grp.sum(sum, 0.f, 0).x) * inv;
+  raw.hold();
 #pragma unroll
   for (int k = 0; k < kN; ++k)
-    if ((k * size + t) * kV < p.dim)
+    if (k < kSure || (k * size + t) * kV < p.dim) {
+      f32x2 v[C];
+      raw.get(k, v);
 #pragma unroll
-      for (int i = 0; i < kV; ++i) s += raw[k].get(i);
-  const float mu = (kWarp ? warp_sum(s) : grp.sum(s, 0.f, 0).x) * inv;
-  float q = 0.f;
-#pragma unroll
-  for (int k = 0; k < kN; ++k)
-    if ((k * size + t) * kV < p.dim)
-#pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const float d = raw[k].get(i) - mu;
-        q = fmaf(d, d, q);
+      for (int i = 0; i < C; ++i) {
+        const f32x2 d = add2(v[i], kV == 1 ? make2(-mu, 0.f) : both(-mu));
+        q = fma2(d, d, q);
       }
-  const float rs = 1.0f / sqrtf((kWarp ? warp_sum(q) : grp.sum(q, 0.f, 1).x) * inv + p.eps);
+    }
+  const float ssq = lo2(q) + hi2(q);
+  const float rs = 1.0f / sqrtf((kWarp ? warp_sum(ssq) : grp.sum(ssq, 0.f, 1).x) * inv + p.eps);
+  raw.hold();
 #pragma unroll
   for (int k = 0; k < kN; ++k) {
     const int c = (k * size + t) * kV;
-    if (c < p.dim) {
-      float w[kV], b[kV];
+    if (k < kSure || c < p.dim) {
+      f32x2 v[C], w[C], b[C];
+      raw.get(k, v);
+      weights<kV, kW>(p.w, p.w_bf16, c, p.dim, 1.f, w);
+      weights<kV, kW>(p.b, p.w_bf16, c, p.dim, 0.f, b);
 #pragma unroll
-      for (int i = 0; i < kV; ++i) { w[i] = 1.f; b[i] = 0.f; }
-      if (p.w) ld_wv<kV>(p.w, p.w_bf16, c, w);
-      if (p.b) ld_wv<kV>(p.b, p.w_bf16, c, b);
-#pragma unroll
-      for (int i = 0; i < kV; ++i) b[i] = fmaf((raw[k].get(i) - mu) * rs, w[i], b[i]);
-      raw[k].put(b);
-      raw[k].store(y + c);
+      for (int i = 0; i < C; ++i) b[i] = fma2(mul2(add2(v[i], both(-mu)), both(rs)), w[i], b[i]);
+      if constexpr (kV > 1) store16(y + c, b);
+      else st1(y + c, lo2(b[0]));
     }
   }
   if (t == 0) {
@@ -191,103 +264,149 @@ struct LnBwd {
 };
 
 // A persistent CTA of several row groups (threadIdx.y).  A thread owns the same columns of
-// every row its group takes, so the columns' sums stay in its registers; at the end the
-// groups' sums are joined in shared memory in a fixed order and the CTA writes one line.
+// every row its group takes, so the weights and the columns' sums stay in its registers; at
+// the end the groups' sums are joined in shared memory in a fixed order and the CTA writes
+// one line.  Rows come through a ring of asynchronous copies in shared memory that each
+// thread keeps for itself (it reads only what it copied: no barrier), because the registers
+// are taken: 6 KB a row of 1536 bf16 pairs, LN_RING - 1 rows ahead.  Rows that need
+// element-wise access are fetched one row ahead into registers.
 constexpr int LN_GROUPS = 8;
-constexpr int ln_bwd_ctas(int columns) { return columns > 8 ? 1 : 2; }   // CTAs of 512 threads an SM, by registers
+__host__ __device__ constexpr int ln_ring(int n) { return n <= 2 ? 4 : 3; }
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+
 template <typename T, int kV, int kN>
-__global__ void __launch_bounds__(512, ln_bwd_ctas(kV * kN)) ln_backward_kernel(const LnBwd p) {
-  extern __shared__ float sums[];               // [groups - 1][2][dim]
-  __shared__ float red[LN_GROUPS * 128];
+__global__ void __launch_bounds__(512, 1) ln_backward_kernel(const LnBwd p) {
+  extern __shared__ uint4 dyn[];
+  __shared__ __align__(8) float red[LN_GROUPS * 128];
+  using S = Share<kV, kN>;
   const int t = threadIdx.x, size = blockDim.x, grp_i = threadIdx.y, groups = blockDim.y;
+  const int nthr = size * groups, tid = grp_i * size + t;
   const Group grp{t, size, 1 + grp_i, red + 128 * grp_i};
   const float inv = 1.f / (float)p.dim;
-  float sw[kN][kV], sb[kN][kV];
+  const long long step = (long long)gridDim.x * groups;
+  long long r = (long long)blockIdx.x * groups + grp_i;
+  f32x2 w[S::P], sw[S::P], sb[S::P];
 #pragma unroll
-  for (int k = 0; k < kN; ++k)
+  for (int i = 0; i < S::P; ++i) sw[i] = sb[i] = both(0.f);
+  if constexpr (kV > 1) {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) sw[k][i] = sb[k][i] = 0.f;
-  int parity = 0;
-  for (long long r = (long long)blockIdx.x * groups + grp_i; r < p.rows; r += (long long)gridDim.x * groups) {
-    const T* x = static_cast<const T*>(p.x) + r * p.ldx;
-    const T* dy = static_cast<const T*>(p.dy) + r * p.lddy;
-    Pack<T, kV> xr[kN], gr[kN];
+    for (int k = 0; k < kN; ++k) weights<kV>(p.w, p.w_bf16, (k * size + t) * kV, p.dim, 1.f, w + k * (kV / 2));
+  } else {
+    f32x2 a[2];
 #pragma unroll
-    for (int k = 0; k < kN; ++k)
-      if ((k * size + t) * kV < p.dim) {
-        xr[k].load(x + (k * size + t) * kV);
-        gr[k].load(dy + (k * size + t) * kV);
-      }
-    const float mu = p.mean[r], rs = p.rstd[r];
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      const int c = (k * size + t) * kV;
-      if (c < p.dim) {
-        float w[kV];
-#pragma unroll
-        for (int i = 0; i < kV; ++i) w[i] = 1.f;
-        if (p.w) ld_wv<kV>(p.w, p.w_bf16, c, w);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-          const float d = gr[k].get(i), xh = (xr[k].get(i) - mu) * rs, g = d * w[i];
-          sw[k][i] = fmaf(d, xh, sw[k][i]);
-          sb[k][i] += d;
-          s1 += g;
-          s2 = fmaf(g, xh, s2);
-        }
-      }
-    }
-    const float2 c12 = grp.sum(s1, s2, parity);
-    parity ^= 1;
-    const float c1 = c12.x * inv, c2 = c12.y * inv;
-    T* dx = static_cast<T*>(p.dx) + r * p.lddx;
-#pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      const int c = (k * size + t) * kV;
-      if (c < p.dim) {
-        float w[kV];
-#pragma unroll
-        for (int i = 0; i < kV; ++i) w[i] = 1.f;
-        if (p.w) ld_wv<kV>(p.w, p.w_bf16, c, w);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-          const float xh = (xr[k].get(i) - mu) * rs;
-          w[i] = rs * (gr[k].get(i) * w[i] - c1 - xh * c2);
-        }
-        gr[k].put(w);
-        gr[k].store(dx + c);
-      }
+    for (int k = 0; k < kN; k += 2) {
+      weights<1>(p.w, p.w_bf16, k * size + t, p.dim, 1.f, a);
+      a[1] = both(0.f);
+      if (k + 1 < kN) weights<1>(p.w, p.w_bf16, (k + 1) * size + t, p.dim, 1.f, a + 1);
+      w[k / 2] = make2(lo2(a[0]), lo2(a[1]));
     }
   }
+  constexpr int R = ln_ring(kN);
+  auto slot = [&](int s, int which, int k) { return dyn + ((s * 2 + which) * kN + k) * nthr + tid; };
+  auto fetch = [&](long long row, int s) {   // one group of copies, empty past the last row
+    if constexpr (kV > 1) {
+      if (row < p.rows) {
+        const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+        const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          const int c = (k * size + t) * kV;
+          if (c < p.dim) {
+            copy16(slot(s, 0, k), x + c);
+            copy16(slot(s, 1, k), dy + c);
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  Raw<T, kV, kN> xn, gn;
+  float mu_n = 0.f, rs_n = 0.f;
+  if constexpr (kV > 1) {
+    // slots that are never copied to belong to columns past the row: zero
+#pragma unroll
+    for (int k = 0; k < kN; ++k)
+      if ((k * size + t) * kV >= p.dim)
+        for (int s = 0; s < R; ++s) *slot(s, 0, k) = *slot(s, 1, k) = make_uint4(0, 0, 0, 0);
+    for (int s = 0; s < R - 1; ++s) fetch(r + s * step, s);
+  } else if (r < p.rows) {
+    xn.load(static_cast<const T*>(p.x) + r * p.ldx, t, size, p.dim);
+    gn.load(static_cast<const T*>(p.dy) + r * p.lddy, t, size, p.dim);
+  }
+  if (r < p.rows) { mu_n = p.mean[r]; rs_n = p.rstd[r]; }
+  int parity = 0, at = 0;
+  for (; r < p.rows; r += step) {
+    f32x2 xh[S::P], g[S::P];
+    const float mu = mu_n, rs = rs_n;
+    if constexpr (kV > 1) {
+      fetch(r + (R - 1) * step, at == 0 ? R - 1 : at - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        widen(*slot(at, 0, k), xh + k * (kV / 2), static_cast<const T*>(nullptr));
+        widen(*slot(at, 1, k), g + k * (kV / 2), static_cast<const T*>(nullptr));
+      }
+      at = at + 1 == R ? 0 : at + 1;
+    } else {
+      xn.pairs(xh);
+      gn.pairs(g);
+    }
+    if (r + step < p.rows) {
+      mu_n = p.mean[r + step];
+      rs_n = p.rstd[r + step];
+      if constexpr (kV == 1) {
+        xn.load(static_cast<const T*>(p.x) + (r + step) * p.ldx, t, size, p.dim);
+        gn.load(static_cast<const T*>(p.dy) + (r + step) * p.lddy, t, size, p.dim);
+      }
+    }
+    f32x2 s1 = both(0.f), s2 = both(0.f);
+#pragma unroll
+    for (int i = 0; i < S::P; ++i) {
+      xh[i] = mul2(add2(xh[i], both(-mu)), both(rs));
+      sw[i] = fma2(g[i], xh[i], sw[i]);
+      sb[i] = add2(sb[i], g[i]);
+      g[i] = mul2(g[i], w[i]);
+      s1 = add2(s1, g[i]);
+      s2 = fma2(g[i], xh[i], s2);
+    }
+    const float2 c12 = grp.sum(lo2(s1) + hi2(s1), lo2(s2) + hi2(s2), parity);
+    parity ^= 1;
+    const f32x2 c1 = both(-rs * (c12.x * inv)), c2 = both(-rs * (c12.y * inv));
+#pragma unroll
+    for (int i = 0; i < S::P; ++i) g[i] = fma2(xh[i], c2, fma2(g[i], both(rs), c1));
+    store_row<T, kV, kN>(static_cast<T*>(p.dx) + r * p.lddx, g, t, size, p.dim);
+  }
   if (!p.part) return;
+  if constexpr (kV > 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();                              // the ring's memory is free for the sums
+  float* sums = reinterpret_cast<float*>(dyn);  // [groups - 1][2][dim]
   if (grp_i > 0) {
     float* o = sums + (size_t)(grp_i - 1) * 2 * p.dim;
 #pragma unroll
-    for (int k = 0; k < kN; ++k)
-#pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const int c = (k * size + t) * kV + i;
-        if (c < p.dim) { o[c] = sw[k][i]; o[p.dim + c] = sb[k][i]; }
-      }
+    for (int e = 0; e < S::E; ++e) {
+      const int c = ((e / kV) * size + t) * kV + e % kV;
+      if (c < p.dim) { o[c] = elem(sw, e); o[p.dim + c] = elem(sb, e); }
+    }
   }
   __syncthreads();
   if (grp_i > 0) return;
   float* o = p.part + (size_t)blockIdx.x * 2 * p.dim;
 #pragma unroll
-  for (int k = 0; k < kN; ++k)
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const int c = (k * size + t) * kV + i;
-      if (c < p.dim) {
-        for (int j = 0; j < groups - 1; ++j) {
-          sw[k][i] += sums[(size_t)j * 2 * p.dim + c];
-          sb[k][i] += sums[(size_t)j * 2 * p.dim + p.dim + c];
-        }
-        o[c] = sw[k][i];
-        o[p.dim + c] = sb[k][i];
+  for (int e = 0; e < S::E; ++e) {
+    const int c = ((e / kV) * size + t) * kV + e % kV;
+    if (c < p.dim) {
+      float a = elem(sw, e), b = elem(sb, e);
+      for (int j = 0; j < groups - 1; ++j) {
+        a += sums[(size_t)j * 2 * p.dim + c];
+        b += sums[(size_t)j * 2 * p.dim + p.dim + c];
       }
+      o[c] = a;
+      o[p.dim + c] = b;
     }
+  }
 }
 
 // Long rows: dx with the row read three times (from cache after the first), and the
@@ -358,17 +477,17 @@ bool vec_rows(const void* p, int64_t ld, int64_t rows, size_t es) {
   return is_aligned(p, 16) && (rows <= 1 || (size_t)ld * es % 16 == 0);
 }
 
-template <typename T, int kV, bool kWarp>
+template <typename T, int kV, bool kWarp, int kW>
 bool forward_n(const LnFwd& p, int need, int threads, cudaStream_t s) {
   const unsigned grid = (unsigned)(kWarp ? cdiv(p.rows, LN_WARPS) : p.rows);
 #define MUON_LN_FWD(N)                                                   \
   if (need <= N) {                                                       \
-    ln_forward_kernel<T, kV, N, kWarp><<<grid, threads, 0, s>>>(p);      \
+    ln_forward_kernel<T, kV, N, kWarp, kW><<<grid, threads, 0, s>>>(p);  \
     return true;                                                         \
   }
   if constexpr (kV > 1 && kWarp) {
-    MUON_LN_FWD(1) MUON_LN_FWD(2) MUON_LN_FWD(3) MUON_LN_FWD(4) MUON_LN_FWD(6) MUON_LN_FWD(8) MUON_LN_FWD(12)
-    MUON_LN_FWD(16)
+    MUON_LN_FWD(1) MUON_LN_FWD(2) MUON_LN_FWD(3) MUON_LN_FWD(4) MUON_LN_FWD(5) MUON_LN_FWD(6) MUON_LN_FWD(7)
+    MUON_LN_FWD(8) MUON_LN_FWD(10) MUON_LN_FWD(12) MUON_LN_FWD(16)
   } else if constexpr (kV > 1) {
     MUON_LN_FWD(1) MUON_LN_FWD(2) MUON_LN_FWD(4)
   } else if constexpr (kWarp) {
@@ -379,6 +498,14 @@ bool forward_n(const LnFwd& p, int need, int threads, cudaStream_t s) {
 #undef MUON_LN_FWD
   return false;
 }
+template <typename T, int kV, bool kWarp>
+bool forward_w(const LnFwd& p, int need, int threads, cudaStream_t s) {
+  if constexpr (kV > 1 && kWarp) {
+    if (p.w && p.b && p.w_bf16) return forward_n<T, kV, kWarp, W_BF16>(p, need, threads, s);
+    if (p.w && p.b) return forward_n<T, kV, kWarp, W_F32>(p, need, threads, s);
+  }
+  return forward_n<T, kV, kWarp, W_ASK>(p, need, threads, s);
+}
 
 // A warp per row while a lane holds its share of the row in registers (16 accesses);
 // above that a CTA per row.
@@ -387,48 +514,50 @@ void forward(const LnFwd& p, bool vec, cudaStream_t s) {
   constexpr int V = vec_of<T>();
   if (vec) {
     const int nv = p.dim / V;
-    if (forward_n<T, V, true>(p, cdiv(nv, 32), 32 * LN_WARPS, s)) return;
+    if (forward_w<T, V, true>(p, cdiv(nv, 32), 32 * LN_WARPS, s)) return;
     const int threads = 32 * cdiv(nv, 32LL * cdiv(nv, 1024));
-    if (forward_n<T, V, false>(p, cdiv(nv, threads), threads, s)) return;
+    if (forward_w<T, V, false>(p, cdiv(nv, threads), threads, s)) return;
   } else {
-    if (forward_n<T, 1, true>(p, cdiv(p.dim, 32), 32 * LN_WARPS, s)) return;
+    if (forward_w<T, 1, true>(p, cdiv(p.dim, 32), 32 * LN_WARPS, s)) return;
     const int threads = 32 * cdiv(p.dim, 32LL * std::max(8, cdiv(p.dim, 1024)));
-    if (forward_n<T, 1, false>(p, cdiv(p.dim, threads), threads, s)) return;
+    if (forward_w<T, 1, false>(p, cdiv(p.dim, threads), threads, s)) return;
   }
   ln_forward_loop_kernel<T><<<(unsigned)p.rows, LN_LOOP_THREADS, 0, s>>>(p);
 }
 
-// The backward pass's CTAs, at most two on each of 152 SMs; every CTA writes one line of
-// partial sums.
-constexpr int LN_CTAS = 304;
-constexpr int LN_MAX_SUMS = 96 * 1024;   // shared memory for the groups' sums
+// The backward pass's CTAs: one on each SM (its registers fill it); every CTA writes one
+// line of partial sums.
+constexpr int LN_CTAS = 152;
+constexpr int LN_MAX_SMEM = 200 * 1024;
 
 template <typename T, int kV, int kN>
 bool backward_n(const LnBwd& p, int threads, int* lines, cudaStream_t s, cudaError_t* err) {
   int groups = std::max(1, std::min(512 / threads, LN_GROUPS));
-  while (groups > 1 && (size_t)(groups - 1) * 2 * p.dim * 4 > LN_MAX_SUMS) --groups;
-  const int grid = (int)std::min<long long>((p.rows + groups - 1) / groups, LN_CTAS / 2 * ln_bwd_ctas(kV * kN));
-  const size_t smem = p.part ? (size_t)(groups - 1) * 2 * p.dim * 4 : 0;
-  if (smem > 32 * 1024 &&
+  auto smem_of = [&](int g) {
+    const size_t ring = kV > 1 ? (size_t)ln_ring(kN) * 2 * kN * 16 * threads * g : 0;
+    return std::max(ring, p.part ? (size_t)(g - 1) * 2 * p.dim * 4 : 0);
+  };
+  while (groups > 1 && smem_of(groups) > (size_t)LN_MAX_SMEM) --groups;
+  const int grid = (int)std::min<long long>((p.rows + groups - 1) / groups, LN_CTAS);
+  const size_t smem = smem_of(groups);
+  if (smem > 40 * 1024 &&
       (*err = cudaFuncSetAttribute(ln_backward_kernel<T, kV, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   LN_MAX_SUMS)) != cudaSuccess)
+                                   LN_MAX_SMEM)) != cudaSuccess)
     return true;
   ln_backward_kernel<T, kV, kN><<<grid, dim3(threads, groups), smem, s>>>(p);
   *lines = grid;
   return true;
 }
 
-// Threads of a row: as many as it has accesses, at most 512, then up to kN accesses each.
+// 16 columns a thread (registers hold their sums, weights and the row), 8 for rows that 16
+// would leave to less than two warps; element-wise rows 8, then 16.
 template <typename T, int kV>
 bool backward_v(const LnBwd& p, int accesses, int* lines, cudaStream_t s, cudaError_t* err) {
+  constexpr int A = kV > 1 ? 8 / kV : 4, B = kV > 1 ? 16 / kV : 8;
   auto threads = [&](int n) { return 32 * cdiv(accesses, 32LL * n); };
-  if (threads(1) <= (kV > 1 ? 512 : 128)) return backward_n<T, kV, 1>(p, threads(1), lines, s, err);
-  if (threads(2) <= (kV > 1 ? 512 : 128)) return backward_n<T, kV, 2>(p, threads(2), lines, s, err);
-  if constexpr (kV < 8) {
-    if (threads(4) <= 512) return backward_n<T, kV, 4>(p, threads(4), lines, s, err);
-  }
+  if (accesses <= 32 * B) return backward_n<T, kV, A>(p, threads(A), lines, s, err);
+  if (threads(B) <= 512) return backward_n<T, kV, B>(p, threads(B), lines, s, err);
   if constexpr (kV == 1) {
-    if (threads(8) <= 512) return backward_n<T, kV, 8>(p, threads(8), lines, s, err);
     if (threads(16) <= 512) return backward_n<T, kV, 16>(p, threads(16), lines, s, err);
   }
   return false;
