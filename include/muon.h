@@ -312,17 +312,19 @@ size_t muon_linear_ce_workspace_size(const muon_linear_ce* a, int backward);
 int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, float* lse, float* stats,
                            void* ws, size_t ws_bytes, muon_stream_t stream);
 
-/* Gradient of sum_r c_r*loss[r]:  g[r, v] = c_r*(exp(z[r, v] - lse[r]) - [v == label_r]),
- *   dH = g W  (rows x dim, leading dimension dim),  dW = g^T H  (vocab x dim, likewise),
- * both of a->dtype and overwritten; either may be NULL.  c_r = grad_scale * (row_grad ?
- * row_grad[r] : 1) * (stats ? 1/max(stats[1], 1) : 1), and 0 for an ignored row and for
- * one whose label is out of range: with the forward pass's stats this is the gradient of
- * grad_scale times the mean loss.  The logits are computed again, by pieces of the
- * vocabulary.  In bf16, g is rounded to bf16 before the two products, which are summed
- * in fp32. */
+/* Gradient of u * sum_r c_r*loss[r]:  g[r, v] = c_r*(exp(z[r, v] - lse[r]) - [v == label_r]),
+ *   dH = u g W  (rows x dim, leading dimension dim),  dW = u g^T H  (vocab x dim, likewise),
+ * both of a->dtype and overwritten; either may be NULL.  c_r = row_grad ? row_grad[r] : 1,
+ * and 0 for an ignored row and for one whose label is out of range.
+ * u = grad_scale * (upstream ? upstream[0] : 1) * (stats ? 1/max(stats[1], 1) : 1): with the
+ * forward pass's stats this is the gradient of grad_scale * upstream * the mean loss.
+ * row_grad, upstream and stats are device fp32.  The logits are computed again, by pieces
+ * of the vocabulary.  In bf16, g is rounded to bf16 before the two products, which are
+ * summed in fp32 and scaled by u before their rounding (a factor that every row shares is
+ * better there: inside g its rounding would be the same for all of them). */
 int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse, const float* row_grad,
-                            const float* stats, float grad_scale, void* dH, void* dW,
-                            void* ws, size_t ws_bytes, muon_stream_t stream);
+                            const float* stats, const float* upstream, float grad_scale, void* dH,
+                            void* dW, void* ws, size_t ws_bytes, muon_stream_t stream);
 
 /* AdamW with both moments held in 8 bits.  Blocks of MUON_ADAMW8_BLOCK consecutive
  * elements share one scale byte s per moment.  A code c stands for the fp32 number

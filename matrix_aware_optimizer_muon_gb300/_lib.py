@@ -109,7 +109,7 @@ def load_library(path: Optional[str] = None):
                                           vp]),
         "muon_linear_ce_workspace_size": (sz, [vp, i32]),
         "muon_linear_ce_forward": (i32, [vp, vp, vp, vp, vp, sz, vp]),
-        "muon_linear_ce_backward": (i32, [vp, vp, vp, vp, f32, vp, vp, vp, sz, vp]),
+        "muon_linear_ce_backward": (i32, [vp, vp, vp, vp, vp, f32, vp, vp, vp, sz, vp]),
         "muon_adamw8_step": (i32, [vp, i32, i64, f32, ctypes.c_double, ctypes.c_double, f32, f32, ctypes.c_uint32,
                                    vp]),
         "muon_adamw8_unpack": (i32, [vp, vp, vp, vp, i64, vp, vp, vp]),

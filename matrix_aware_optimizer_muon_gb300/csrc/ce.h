@@ -9,6 +9,7 @@ namespace ce {
 
 constexpr int TILE = 256;          // output tile of a CTA pair, both ways
 constexpr int BK = 64;             // K step
+constexpr int BOX = 64;            // rows of a TMA box
 constexpr int MAX_JOBS = 3;
 constexpr int MAX_PAIRS = 80;
 constexpr int MAX_ORDER = 12000;   // tiles of a launch whose order the host lays out
@@ -22,8 +23,8 @@ enum Kind : int {
 };
 
 // One product of a launch: out[m, n] = sum_k A[m, k] B[n, k].  A K-major operand's map
-// covers (k, row); an MN-major one's (row, k).  The maps' third coordinate is the bf16
-// part of a 32-bit operand.
+// covers (k, row), an MN-major one's (row, k), in boxes of 64 x 64.  The maps' third
+// coordinate is the bf16 part of a 32-bit operand.
 struct Job {
   CUtensorMap a, b;
   int kind;
@@ -56,20 +57,32 @@ struct Params {
   long long vocab, ignore, v0;   // v0: first vocabulary row of the GRAD piece
   float2* part;                  // LOGITS: [row][2 * ntiles]
   float* zlabel;
-  const float *lse, *row_grad, *stats;
+  const float *lse, *row_grad, *stats, *upstream;
   float scale;
   unsigned int* status;
   unsigned long long timeout_ns;
   int debug_flags;
-  int ordered;                   // tiles follow order[start[pair] .. start[pair + 1]), else round robin
+};
+// The same with the tiles laid out by the host: pair i takes order[start[i] .. start[i + 1]).
+// A launch whose tiles go round robin is not charged for the table.
+struct OrderedParams : Params {
   unsigned short start[MAX_PAIRS + 1];
   unsigned short order[MAX_ORDER];
 };
-static_assert(sizeof(Params) < 32000, "ce::Params too large");
+static_assert(sizeof(OrderedParams) < 32000, "ce::OrderedParams too large");
 
 cudaError_t prepare();           // kernel attributes and occupancy of the current device, once
 int pairs();                     // CTA pairs that run at once
-cudaError_t launch(const Params& p, bool promote, cudaStream_t s);
+cudaError_t launch(const OrderedParams& p, bool ordered, bool promote, cudaStream_t s);
+
+#ifdef __CUDACC__
+// The factor that all rows share.
+__device__ __forceinline__ float shared_factor(float scale, const float* upstream, const float* stats) {
+  if (upstream) scale *= *upstream;
+  if (stats) scale /= fmaxf(stats[1], 1.f);
+  return scale;
+}
+#endif
 
 }  // namespace ce
 }  // namespace muon

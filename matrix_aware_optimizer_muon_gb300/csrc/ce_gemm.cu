@@ -2,10 +2,15 @@
 // TMA), with the softmax fused into their epilogues.
 //
 // A 2-CTA cluster (cta_group::2) computes a 256 x 256 output tile; each CTA stages its
-// 128 rows of A and 128 rows of B (32 KB a K step of 64).  320 threads a CTA:
-//   warp 0      TMA producer (one lane), a ring of STAGES K steps;
+// 128 rows of A and 128 rows of B (32 KB a K step of 64).
+// 384 threads a CTA:
+//   warps 0, 2  TMA producers (one lane each) of A and of B, a ring of STAGES K steps.
+//               Two, and in boxes of 64 rows: a request takes a lane about 100 cycles
+//               to issue, and one of 128 rows 400 to serve.  Loads alone would feed
+//               1.50 PFLOP/s from one lane in boxes of 128, 1.68 in boxes of 64, 2.54
+//               from two lanes (the MMAs alone run at 2.08);
 //   warp 1      tensor-memory allocation; in the even CTA one lane issues the MMAs;
-//   warps 2..9  epilogue, two per TMEM lane quarter, 128 of the 256 columns each: a
+//   warps 4..11 epilogue, two per TMEM lane quarter, 128 of the 256 columns each: a
 //               thread owns one row, so a row's max and sum need no shuffles.
 // Two 256-column fp32 accumulators: the epilogue of a tile overlaps the next one's MMAs.
 //
@@ -16,7 +21,8 @@
 // The tensor cores add to the fp32 accumulator with truncation; its bias grows with the
 // number of K steps (measured: 2.3e-7 of a sum of 256 bf16 products, 1e-6 of 1024,
 // 9e-6 of 8192).  The kPromote form takes the accumulator over into registers every
-// seg_kb K steps and adds there with rounding to nearest.  It serves the logits of the
+// seg_kb K steps and adds there with rounding to nearest (a take-over costs about 3% of
+// 512 products' time).  It serves the logits of the
 // forward pass, whose loss is fp32, and every product of 32-bit operands; sums that
 // are rounded to bf16 (2e-3) do without.
 //
@@ -36,9 +42,10 @@ namespace {
 constexpr int HALF = TILE / 2;
 constexpr int OP_BYTES = HALF * BK * 2;        // one operand's 128 rows of a K step
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int BOX_BYTES = BOX * BK * 2;        // two boxes an operand, one above the other in either major
 constexpr int STAGES = 6;
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int CHUNKS = 4;                      // 32-column chunks of an epilogue warp
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 256;
@@ -66,11 +73,11 @@ __device__ __forceinline__ Tile decode(const Params& p, int t) {
 }
 
 // The pair's k-th tile, or -1.
+__device__ __forceinline__ int tile_at(const OrderedParams& p, int pair, int, int k) {
+  const int i = p.start[pair] + k;
+  return i < p.start[pair + 1] ? p.order[i] : -1;
+}
 __device__ __forceinline__ int tile_at(const Params& p, int pair, int npairs, int k) {
-  if (p.ordered) {
-    const int i = p.start[pair] + k;
-    return i < p.start[pair + 1] ? p.order[i] : -1;
-  }
   const int t = pair + k * npairs;
   return t < p.tiles ? t : -1;
 }
@@ -135,9 +142,7 @@ __device__ __forceinline__ RowIn row_in(const Params& p, int r) {
   RowIn x;
   x.lse = p.lse[r];
   x.label = lab - p.v0;
-  float c = p.scale;
-  if (p.row_grad) c *= p.row_grad[r];
-  if (p.stats) c /= fmaxf(p.stats[1], 1.f);
+  const float c = p.row_grad ? p.row_grad[r] : 1.f;
   x.c = (lab == p.ignore || lab < 0 || lab >= p.vocab) ? 0.f : c;
   // a row without gradient gives zeros even where its logits or lse are not finite
   if (lab == p.ignore || lab < 0 || lab >= p.vocab) x.lse = INFINITY;
@@ -164,7 +169,8 @@ __device__ __forceinline__ void finish_grad(const Params& p, const Job& J, int r
   }
 }
 
-__device__ __forceinline__ void finish_sum(const Params& p, const Job& J, int split, int r, int c0, float (&v)[32]) {
+__device__ __forceinline__ void finish_sum(const Params& p, const Job& J, int split, int r, int c0, float u,
+                                           float (&v)[32]) {
   if (r >= J.m || c0 >= J.n) return;
   const int cols = J.n - c0;
   if (J.kind == DH && J.acc) {
@@ -189,6 +195,8 @@ __device__ __forceinline__ void finish_sum(const Params& p, const Job& J, int sp
       return;
     }
   }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] *= u;
   if (p.f32_out) store_row(static_cast<float*>(J.out) + (size_t)r * J.ldo + c0, v, cols, J.vec);
   else store_row(static_cast<bf16*>(J.out) + (size_t)r * J.ldo + c0, v, cols, J.vec);
 }
@@ -227,8 +235,8 @@ __device__ __forceinline__ void finish_logits(const Params& p, const Job& J, con
   }
 }
 
-template <bool kPromote>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kernel(const __grid_constant__ Params p) {
+template <bool kPromote, class P>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kernel(const __grid_constant__ P p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
@@ -246,7 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&full[s], 2);         // the even CTA's producers of A and B
       ptx::mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -266,43 +274,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer (both CTAs)
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ producers (both CTAs)
+    const bool is_b = warp == 2;
     if (lane == 0 && !(p.debug_flags & MUON_DEBUG_STALL_PRODUCER)) {
-      for (int j = 0; j < p.njobs; ++j) {
-        ptx::prefetch_tmap(&p.job[j].a);
-        ptx::prefetch_tmap(&p.job[j].b);
-      }
+      for (int j = 0; j < p.njobs; ++j) ptx::prefetch_tmap(is_b ? &p.job[j].b : &p.job[j].a);
       int stage = 0;
       uint32_t phase = 0, pending = 0, pend_phase = 0;
       bool stop = false;
       for (int i = 0, t; !stop && (t = tile_at(p, pair, npairs, i)) >= 0; ++i) {
         const Tile ti = decode(p, t);
         const Job& J = p.job[ti.job];
-        const int m0 = ti.tm * TILE + rank * HALF;
-        const int n0 = ti.tn * TILE + rank * HALF + J.b_n0;
-        const int kbase = ti.split * J.nkb;
+        const CUtensorMap* map = is_b ? &J.b : &J.a;
+        const bool mn = is_b ? J.b_mn : J.a_mn;
+        const int r0 = is_b ? ti.tn * TILE + rank * HALF + J.b_n0 : ti.tm * TILE + rank * HALF;
+        const int k0 = ti.split * J.nkb * BK + (is_b ? J.b_k0 : 0);
         for (int term = 0; term < p.nterms && !stop; ++term) {
-          const int za = p.ta[term], zb = p.tb[term];
+          const int z = is_b ? p.tb[term] : p.ta[term];
           for (int kb = 0; kb < J.nkb; ++kb) {
             if (!wait_for(&empty[stage], phase ^ 1u, abort_flag, p, true)) { stop = true; break; }
             const uint32_t fb = ptx::mapa_shared(ptx::smem_addr(&full[stage]), 0);
-            if (even) ptx::mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
-            const uint32_t sa = ptx::smem_addr(smem + stage * STAGE_BYTES);
-            const uint32_t sb = sa + OP_BYTES;
-            const int ka = (kbase + kb) * BK, kbk = ka + J.b_k0;
-            if (J.a_mn) {
-              ptx::tma_load_3d_pair(sa, &J.a, fb, m0, ka, za);
-              ptx::tma_load_3d_pair(sa + OP_BYTES / 2, &J.a, fb, m0 + 64, ka, za);
-            } else {
-              ptx::tma_load_3d_pair(sa, &J.a, fb, ka, m0, za);
-            }
-            if (J.b_mn) {
-              ptx::tma_load_3d_pair(sb, &J.b, fb, n0, kbk, zb);
-              ptx::tma_load_3d_pair(sb + OP_BYTES / 2, &J.b, fb, n0 + 64, kbk, zb);
-            } else {
-              ptx::tma_load_3d_pair(sb, &J.b, fb, kbk, n0, zb);
-            }
+            if (even) ptx::mbar_arrive_expect_tx(&full[stage], 2 * OP_BYTES);
+            const uint32_t d = ptx::smem_addr(smem + stage * STAGE_BYTES) + (is_b ? OP_BYTES : 0);
+            const int k = k0 + kb * BK;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              ptx::tma_load_3d_pair(d + q * BOX_BYTES, map, fb, mn ? r0 + q * BOX : k, mn ? k : r0 + q * BOX, z);
             pending |= 1u << stage;
             pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -364,9 +361,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
       wait_for(mdone, 0, abort_flag, p, false);
     }
     __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (both CTAs)
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const float u = shared_factor(p.scale, p.upstream, p.stats);
     int it = 0;
     bool stop = false;
     for (int i = 0, t; !stop && (t = tile_at(p, pair, npairs, i)) >= 0; ++i) {
@@ -394,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
             float v[32];
             ptx::tmem_ld_32x32b_x32(tb + k * 32, v);
             if (J.kind == GRAD) finish_grad(p, J, r, cbase + k * 32, v, x);
-            else finish_sum(p, J, ti.split, r, cbase + k * 32, v);
+            else finish_sum(p, J, ti.split, r, cbase + k * 32, u, v);
           }
         }
         ptx::tc_fence_before();
@@ -411,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
 #pragma unroll
           for (int k = 0; k < CHUNKS; ++k) {
             if (J.kind == GRAD) finish_grad(p, J, r, cbase + k * 32, acc[k], x);
-            else finish_sum(p, J, ti.split, r, cbase + k * 32, acc[k]);
+            else finish_sum(p, J, ti.split, r, cbase + k * 32, u, acc[k]);
           }
         }
       }
@@ -424,6 +422,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
   if (warp == 1) ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
 }
 
+template <class K>
+cudaError_t allow(K kern) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+}
 std::mutex g_mu;
 std::map<int, int> g_pairs;   // device -> CTA pairs that run at once
 
@@ -435,17 +437,17 @@ cudaError_t prepare() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_pairs.count(dev)) return cudaSuccess;
-  if ((e = cudaFuncSetAttribute(ce_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess)
-    return e;
-  if ((e = cudaFuncSetAttribute(ce_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess)
+  if ((e = allow(ce_kernel<false, Params>)) != cudaSuccess || (e = allow(ce_kernel<true, Params>)) != cudaSuccess ||
+      (e = allow(ce_kernel<false, OrderedParams>)) != cudaSuccess ||
+      (e = allow(ce_kernel<true, OrderedParams>)) != cudaSuccess)
     return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM;
-  int clusters = 0;
-  if ((e = cudaOccupancyMaxActiveClusters(&clusters, ce_kernel<true>, &cfg)) != cudaSuccess) return e;
-  g_pairs[dev] = clusters < MAX_PAIRS ? clusters : MAX_PAIRS;
+  int n = 0;
+  if ((e = cudaOccupancyMaxActiveClusters(&n, ce_kernel<true, Params>, &cfg)) != cudaSuccess) return e;
+  g_pairs[dev] = n < MAX_PAIRS ? n : MAX_PAIRS;
   return cudaSuccess;
 }
 
@@ -457,13 +459,15 @@ int pairs() {
   return it == g_pairs.end() ? 0 : it->second;
 }
 
-cudaError_t launch(const Params& p, bool promote, cudaStream_t s) {
+cudaError_t launch(const OrderedParams& p, bool ordered, bool promote, cudaStream_t s) {
   if (p.tiles <= 0) return cudaSuccess;
   const int n = pairs();
   if (n < 1) return cudaErrorInvalidConfiguration;
   const int grid = 2 * (p.tiles < n ? p.tiles : n);
-  if (promote) ce_kernel<true><<<grid, THREADS, SMEM, s>>>(p);
-  else ce_kernel<false><<<grid, THREADS, SMEM, s>>>(p);
+  if (promote && ordered) ce_kernel<true, OrderedParams><<<grid, THREADS, SMEM, s>>>(p);
+  else if (promote) ce_kernel<true, Params><<<grid, THREADS, SMEM, s>>>(p);
+  else if (ordered) ce_kernel<false, OrderedParams><<<grid, THREADS, SMEM, s>>>(p);
+  else ce_kernel<false, Params><<<grid, THREADS, SMEM, s>>>(p);
   count_launch();
   return cudaGetLastError();
 }

@@ -28,7 +28,7 @@ constexpr int64_t G_BYTES = 96 << 20;
 constexpr int64_t MIN_PIECE = 2048;
 constexpr int MAX_SPLITS = 16;
 // K steps (of 64) between take-overs of the tensor cores' sums into registers.
-constexpr int SEG_BF16 = 8, SEG_F32 = 4;
+constexpr int SEG_BF16 = 20, SEG_F32 = 4;
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -113,14 +113,15 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const float2* par
 // dH from the sums of each range of K.
 template <typename T>
 __global__ void __launch_bounds__(256) split_sum_kernel(const float* acc, int splits, long long rows, int dim,
-                                                        long long ldacc, T* out) {
+                                                        long long ldacc, T* out, float scale, const float* upstream,
+                                                        const float* stats) {
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const long long r = i / dim;
   if (r >= rows) return;
   const int c = (int)(i - r * dim);
   float s = 0.f;
   for (int k = 0; k < splits; ++k) s += acc[((size_t)k * rows + r) * ldacc + c];
-  st1(out + i, s);
+  st1(out + i, s * shared_factor(scale, upstream, stats));
 }
 
 // ---------------------------------------------------------------------------
@@ -212,10 +213,9 @@ struct Operand {
   int parts;
 };
 
-// box: 64 columns x box_rows rows
-bool map_of(CUtensorMap* m, const Operand& o, int box_rows) {
+bool map_of(CUtensorMap* m, const Operand& o) {
   return encode_tmap_bf16(m, o.p, (uint64_t)o.cols, (uint64_t)o.rows, (uint64_t)o.parts, (uint64_t)o.ld * 2,
-                          (uint64_t)o.part_stride * 2, 64, (uint32_t)box_rows);
+                          (uint64_t)o.part_stride * 2, 64, BOX);
 }
 
 template <typename T>
@@ -237,7 +237,7 @@ Operand operand(const muon_linear_ce* a, const CePlan& P, bool h, char* ws, cuda
 }
 
 void common_params(Params* p, const muon_linear_ce* a, const CePlan& P, char* ws) {
-  std::memset(p, 0, offsetof(Params, order));
+  std::memset(static_cast<void*>(p), 0, sizeof(Params));
   p->nterms = P.nterms;
   p->parts = P.parts;
   // (part of A, part of B), smallest products first
@@ -255,12 +255,15 @@ void common_params(Params* p, const muon_linear_ce* a, const CePlan& P, char* ws
   p->debug_flags = test_flags();
 }
 
-void shape(Job* j, int64_t m, int64_t n, int64_t k, int group) {
+// Row tiles that are walked together for each column tile: their rows of A stay in L2.
+constexpr int GROUP = 32;
+
+void shape(Job* j, int64_t m, int64_t n, int64_t k) {
   j->m = (int)m;
   j->n = (int)n;
   j->mtiles = (int)cdiv(m, TILE);
   j->ntiles = (int)cdiv(n, TILE);
-  j->group = std::min(group, j->mtiles);
+  j->group = std::min(GROUP, j->mtiles);
   j->splits = 1;
   j->nkb = (int)cdiv(k, BK);
   j->tiles = j->mtiles * j->ntiles;
@@ -268,8 +271,8 @@ void shape(Job* j, int64_t m, int64_t n, int64_t k, int group) {
 
 // Hands the launch's tiles out: each to the pair with the least work so far, jobs in
 // order of their tiles' lengths.  Launches with more tiles than the table holds go round
-// robin, where one tile more or less no longer matters.
-void lay_out(Params* p, int npairs) {
+// robin, where one tile more or less no longer matters.  Returns whether the table is used.
+bool lay_out(OrderedParams* p, int npairs) {
   std::sort(p->job, p->job + p->njobs, [](const Job& x, const Job& y) { return x.nkb > y.nkb; });
   int t = 0;
   for (int j = 0; j < p->njobs; ++j) {
@@ -277,8 +280,7 @@ void lay_out(Params* p, int npairs) {
     t += p->job[j].tiles;
   }
   p->tiles = t;
-  p->ordered = 0;
-  if (p->njobs < 2 || t > MAX_ORDER || t <= npairs) return;
+  if (p->njobs < 2 || t > MAX_ORDER || t <= npairs) return false;
   // load[i]: work of pair i; a binary heap of pairs by (load, index)
   long long load[MAX_PAIRS];
   int heap[MAX_PAIRS];
@@ -309,7 +311,7 @@ void lay_out(Params* p, int npairs) {
   int fill[MAX_PAIRS];
   for (int i = 0; i < npairs; ++i) fill[i] = p->start[i];
   for (t = 0; t < p->tiles; ++t) p->order[fill[owner[t]]++] = (unsigned short)t;
-  p->ordered = 1;
+  return true;
 }
 
 int result_vec(const void* out, int64_t ld, int dt) {
@@ -351,19 +353,19 @@ extern "C" int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, floa
   }
   if (prepare() != cudaSuccess) return MUON_ERR_CUDA;
   char* w = static_cast<char*>(ws);
-  static thread_local Params p;
+  static thread_local OrderedParams p;
   common_params(&p, a, P, w);
   p.part = reinterpret_cast<float2*>(w + P.part);
   p.zlabel = reinterpret_cast<float*>(w + P.zlabel);
   const Operand H = operand(a, P, true, w, s), W = operand(a, P, false, w, s);
   Job& j = p.job[0];
   j.kind = LOGITS;
-  if (!map_of(&j.a, H, 128) || !map_of(&j.b, W, 128)) return MUON_ERR_CUDA;
-  shape(&j, a->rows, a->vocab, a->dim, 16);
+  if (!map_of(&j.a, H) || !map_of(&j.b, W)) return MUON_ERR_CUDA;
+  shape(&j, a->rows, a->vocab, a->dim);
   j.seg_kb = P.nterms > 1 ? SEG_F32 : SEG_BF16;
   p.njobs = 1;
   p.tiles = j.tiles;
-  if (launch(p, true, s) != cudaSuccess) return MUON_ERR_CUDA;
+  if (launch(p, false, true, s) != cudaSuccess) return MUON_ERR_CUDA;
   join_kernel<<<(unsigned)cdiv(a->rows, JOIN_WARPS), 32 * JOIN_WARPS, 0, s>>>(
       p.part, 2 * j.ntiles, a->rows, a->labels, a->vocab, a->ignore_index, p.zlabel, loss, lse, stats,
       static_cast<unsigned int*>(ws) + TICKET_WORD);
@@ -372,16 +374,16 @@ extern "C" int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, floa
 }
 
 extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse, const float* row_grad,
-                                       const float* stats, float grad_scale, void* dH, void* dW, void* ws,
-                                       size_t ws_bytes, muon_stream_t stream) {
+                                       const float* stats, const float* upstream, float grad_scale, void* dH,
+                                       void* dW, void* ws, size_t ws_bytes, muon_stream_t stream) {
   using namespace ce;
   begin_launches();
   if (int rc = check(a)) return rc;
   if (int rc = check_pointers(a)) return rc;
   const size_t es = dt_size(a->dtype);
   if (a->rows && !lse) return MUON_ERR_INVALID;
-  if (!is_aligned(lse, 4) || !is_aligned(row_grad, 4) || !is_aligned(stats, 4) || !is_aligned(dH, es) ||
-      !is_aligned(dW, es))
+  if (!is_aligned(lse, 4) || !is_aligned(row_grad, 4) || !is_aligned(stats, 4) || !is_aligned(upstream, 4) ||
+      !is_aligned(dH, es) || !is_aligned(dW, es))
     return MUON_ERR_INVALID;
   CePlan P = {};
   make_plan(a, 1, &P);
@@ -396,10 +398,10 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
   }
   if (prepare() != cudaSuccess) return MUON_ERR_CUDA;
   char* w = static_cast<char*>(ws);
-  static thread_local Params p;
+  static thread_local OrderedParams p;
   const Operand H = operand(a, P, true, w, s), W = operand(a, P, false, w, s);
-  CUtensorMap hk, hm, wk, wm;   // K-major and MN-major boxes
-  if (!map_of(&hk, H, 128) || !map_of(&hm, H, 64) || !map_of(&wk, W, 128) || !map_of(&wm, W, 64)) return MUON_ERR_CUDA;
+  CUtensorMap hmap, wmap;
+  if (!map_of(&hmap, H) || !map_of(&wmap, W)) return MUON_ERR_CUDA;
   const bool f32 = a->dtype == MUON_DTYPE_F32;
   const int npairs = pairs();
   float* acc = P.acc ? reinterpret_cast<float*>(w + P.acc) : nullptr;
@@ -409,6 +411,7 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
     p.lse = lse;
     p.row_grad = row_grad;
     p.stats = stats;
+    p.upstream = upstream;
     p.scale = grad_scale;
     if (i > 0) {
       const int64_t v0 = (i - 1) * P.piece, c = std::min(P.piece, a->vocab - v0);
@@ -416,11 +419,11 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
       if (dH) {
         Job& j = p.job[p.njobs++];
         j.kind = DH;
-        if (!map_of(&j.a, G, 128)) return MUON_ERR_CUDA;
-        j.b = wm;
+        if (!map_of(&j.a, G)) return MUON_ERR_CUDA;
+        j.b = wmap;
         j.b_mn = 1;
         j.b_k0 = (int)v0;
-        shape(&j, a->rows, a->dim, c, 16);
+        shape(&j, a->rows, a->dim, c);
         j.splits = P.splits;
         j.nkb = (int)cdiv(j.nkb, P.splits);
         j.tiles *= P.splits;
@@ -436,10 +439,10 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
       if (dW) {
         Job& j = p.job[p.njobs++];
         j.kind = DW;
-        if (!map_of(&j.a, G, 64)) return MUON_ERR_CUDA;
-        j.b = hm;
+        if (!map_of(&j.a, G)) return MUON_ERR_CUDA;
+        j.b = hmap;
         j.a_mn = j.b_mn = 1;
-        shape(&j, c, a->dim, a->rows, 16);
+        shape(&j, c, a->dim, a->rows);
         j.out = static_cast<char*>(dW) + (size_t)v0 * a->dim * es;
         j.ldo = a->dim;
         j.vec = result_vec(j.out, a->dim, a->dtype);
@@ -449,23 +452,23 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
     if (i < P.npieces) {
       Job& j = p.job[p.njobs++];
       j.kind = GRAD;
-      j.a = hk;
-      j.b = wk;
+      j.a = hmap;
+      j.b = wmap;
       p.v0 = i * P.piece;
       j.b_n0 = (int)p.v0;
-      shape(&j, a->rows, std::min<int64_t>(P.piece, a->vocab - p.v0), a->dim, 16);
+      shape(&j, a->rows, std::min<int64_t>(P.piece, a->vocab - p.v0), a->dim);
       j.out = w + P.g[i & 1];
       j.ldo = P.piece;
       j.part_stride = (long long)P.g_part;
       j.seg_kb = f32 ? SEG_F32 : j.nkb;
     }
-    lay_out(&p, npairs);
-    if (launch(p, f32, s) != cudaSuccess) return MUON_ERR_CUDA;
+    const bool ordered = lay_out(&p, npairs);
+    if (launch(p, ordered, f32, s) != cudaSuccess) return MUON_ERR_CUDA;
   }
   if (dH && P.splits > 1) {
     const unsigned blocks = (unsigned)cdiv(a->rows * a->dim, 256);
-    if (f32) split_sum_kernel<float><<<blocks, 256, 0, s>>>(acc, P.splits, a->rows, (int)a->dim, P.ldacc, static_cast<float*>(dH));
-    else split_sum_kernel<bf16><<<blocks, 256, 0, s>>>(acc, P.splits, a->rows, (int)a->dim, P.ldacc, static_cast<bf16*>(dH));
+    if (f32) split_sum_kernel<float><<<blocks, 256, 0, s>>>(acc, P.splits, a->rows, (int)a->dim, P.ldacc, static_cast<float*>(dH), grad_scale, upstream, stats);
+    else split_sum_kernel<bf16><<<blocks, 256, 0, s>>>(acc, P.splits, a->rows, (int)a->dim, P.ldacc, static_cast<bf16*>(dH), grad_scale, upstream, stats);
     count_launch();
   }
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;

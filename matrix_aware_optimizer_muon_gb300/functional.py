@@ -40,7 +40,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
         w = _plain_rows(w)
         ws = head.linear_ce_workspace_for(rows, w, labels, backward=False)
         _, lse, stats = head.muon_linear_ce_forward(rows, w, labels, ws, ignore_index)
-        ctx.save_for_backward(rows, w, labels, lse, stats)
+        ctx.save_for_backward(rows, w, labels, lse, stats)  # stats[1]: the rows that count
         ctx.shape, ctx.ignore_index = h.shape, ignore_index
         return stats[0].clone()
 
@@ -49,7 +49,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
         rows, w, labels, lse, stats = ctx.saved_tensors
         ws = head.linear_ce_workspace_for(rows, w, labels)
         dh, dw = head.muon_linear_ce_backward(
-            rows, w, labels, lse, ws, row_grad=grad.float().expand(rows.shape[0]).contiguous(), stats=stats,
+            rows, w, labels, lse, ws, stats=stats, upstream=grad.float(),
             ignore_index=ctx.ignore_index, need_dh=ctx.needs_input_grad[0], need_dw=ctx.needs_input_grad[1])
         return None if dh is None else dh.view(ctx.shape), dw, None, None
 

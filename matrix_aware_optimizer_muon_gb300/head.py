@@ -17,16 +17,26 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import _check, _dt, _stream, load_library
+from ._lib import _check, _dt, load_library
 
 ADAMW8_BLOCK = 128
+
+# The current stream's handle without building a Stream object (3 us of a small call's 12).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_here = contextlib.nullcontext()
 
 
 def _on(stream):
     """Outputs are allocated on the stream they are written on."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _here
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
+def _stream(stream, t: torch.Tensor) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _lib._stream(stream)
 
 
 def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
@@ -72,7 +82,7 @@ def muon_layernorm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = Non
         mean = torch.empty(n, dtype=torch.float32, device=x.device)
         rstd = torch.empty(n, dtype=torch.float32, device=x.device)
     _check("muon_layernorm_forward", load_library().muon_layernorm_forward(
-        px, ldx, pw, pb, n, d, _dt(x), wdt, eps, y.data_ptr(), d, mean.data_ptr(), rstd.data_ptr(), _stream(stream)))
+        px, ldx, pw, pb, n, d, _dt(x), wdt, eps, y.data_ptr(), d, mean.data_ptr(), rstd.data_ptr(), _stream(stream, x)))
     return y, mean, rstd
 
 
@@ -103,7 +113,7 @@ def muon_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[
     _check("muon_layernorm_backward", load_library().muon_layernorm_backward(
         py, ldy, px, ldx, pw, pm, pr, n, d, _dt(x), _dt(weight if weight is not None else x), dx.data_ptr(), d,
         None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), _lib._ptr(ws),
-        0 if ws is None else ws.numel(), _stream(stream)))
+        0 if ws is None else ws.numel(), _stream(stream, x)))
     return dx, dw, db
 
 
@@ -170,26 +180,29 @@ def muon_linear_ce_forward(h: torch.Tensor, w: torch.Tensor, labels: torch.Tenso
         lse = torch.empty(n, dtype=torch.float32, device=h.device)
         stats = torch.empty(2, dtype=torch.float32, device=h.device)
     _check("muon_linear_ce_forward", load_library().muon_linear_ce_forward(
-        ctypes.byref(a), loss.data_ptr(), lse.data_ptr(), stats.data_ptr(), _lib._ptr(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(a), loss.data_ptr(), lse.data_ptr(), stats.data_ptr(), _lib._ptr(ws), ws.numel(), _stream(stream, h)))
     return loss, lse, stats
 
 
 def muon_linear_ce_backward(h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor,
                             ws: torch.Tensor, row_grad: Optional[torch.Tensor] = None,
-                            stats: Optional[torch.Tensor] = None, grad_scale: float = 1.0, ignore_index: int = -100,
-                            need_dh: bool = True, need_dw: bool = True, stream=None):
-    """(dh, dw) of sum_r c_r*loss[r], c_r = grad_scale * row_grad[r] / stats[1] (each factor 1
-    where it is None): with the forward pass's stats, the gradient of the mean loss."""
+                            stats: Optional[torch.Tensor] = None, upstream: Optional[torch.Tensor] = None,
+                            grad_scale: float = 1.0, ignore_index: int = -100, need_dh: bool = True,
+                            need_dw: bool = True, stream=None):
+    """(dh, dw) of sum_r c_r*loss[r], c_r = grad_scale * upstream * row_grad[r] / stats[1] (each
+    factor 1 where it is None; upstream is one fp32 number on the device): with the forward
+    pass's stats, the gradient of the mean loss."""
     a = _ce_args(h, w, labels, ignore_index)
     n = h.shape[0]
     pl = _vector(lse, n, torch.float32, "lse")
     pg, ps = _vector(row_grad, n, torch.float32, "row_grad"), _vector(stats, 2, torch.float32, "stats")
+    pu = None if upstream is None else _vector(upstream.view(-1), 1, torch.float32, "upstream")
     with _on(stream):
         dh = torch.empty((n, h.shape[1]), dtype=h.dtype, device=h.device) if need_dh else None
         dw = torch.empty(tuple(w.shape), dtype=w.dtype, device=h.device) if need_dw else None
     _check("muon_linear_ce_backward", load_library().muon_linear_ce_backward(
-        ctypes.byref(a), pl, pg, ps, grad_scale, None if dh is None else dh.data_ptr(),
-        None if dw is None else dw.data_ptr(), _lib._ptr(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(a), pl, pg, ps, pu, grad_scale, None if dh is None else dh.data_ptr(),
+        None if dw is None else dw.data_ptr(), _lib._ptr(ws), ws.numel(), _stream(stream, h)))
     return dh, dw
 
 
@@ -217,6 +230,7 @@ class AdamW8:
         dev, total = self.params[0].device, self.starts[-1]
         self.m, self.v = (torch.zeros(total, dtype=torch.uint8, device=dev) for _ in range(2))
         self.m_scale, self.v_scale = (torch.zeros(total // ADAMW8_BLOCK, dtype=torch.uint8, device=dev) for _ in range(2))
+        self._state = (self.m.data_ptr(), self.m_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr())
         self.step_count = 0
         self._arr = np.zeros(len(self.params), dtype=_PARAM8)
         at = np.array(self.starts[:-1], dtype=np.int64)
@@ -224,38 +238,38 @@ class AdamW8:
         self._arr["m_scale"] = self.m_scale.data_ptr() + at // ADAMW8_BLOCK
         self._arr["v_scale"] = self.v_scale.data_ptr() + at // ADAMW8_BLOCK
         self._arr["numel"], self._arr["first"] = self.numels, at
-        self._arr["p_dtype"] = self._pointers(self.params, "P")
+        self._arr["p_dtype"] = self._check(self.params)
+        self._addr = self._arr.ctypes.data
 
-    def _pointers(self, tensors: Sequence[torch.Tensor], field: str) -> int:
-        """Fills one pointer column after checking the tensors; returns their dtype."""
-        if len(tensors) != len(self.numels):
-            raise ValueError("one gradient per parameter")
+    def _check(self, tensors: Sequence[torch.Tensor]) -> int:
+        """Refuses what the kernel cannot read; returns the tensors' dtype."""
+        T = torch.Tensor
+        if list(map(T.numel, tensors)) != self.numels:
+            raise ValueError("one contiguous gradient of the same size per parameter")
         dt = tensors[0].dtype
-        for t, n in zip(tensors, self.numels):
-            if t.dtype != dt:
-                raise ValueError("all parameters, and all gradients, have one dtype")
-            if t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError("parameters and gradients are contiguous CUDA tensors of the same size")
-        self._arr[field] = [t.data_ptr() for t in tensors]
+        if not all(map(T.is_contiguous, tensors)) or not all([t.is_cuda and t.dtype == dt for t in tensors]):
+            raise ValueError("parameters, and gradients, are contiguous CUDA tensors of one dtype")
         return _dt(tensors[0])
 
     def step(self, grads: Sequence[torch.Tensor], stream=None) -> None:
         """One asynchronous step."""
-        self._arr["g_dtype"] = self._pointers(grads, "G")
-        self._pointers(self.params, "P")
+        arr = self._arr
+        arr["g_dtype"] = self._check(grads)
+        arr["G"] = list(map(torch.Tensor.data_ptr, grads))
+        arr["P"] = list(map(torch.Tensor.data_ptr, self.params))
         _check("muon_adamw8_step", load_library().muon_adamw8_step(
-            self._arr.ctypes.data, len(self.params), self.step_count + 1, self.lr, self.betas[0], self.betas[1],
-            self.eps, self.weight_decay, self.seed, _stream(stream)))
+            self._addr, len(arr), self.step_count + 1, self.lr, self.betas[0], self.betas[1], self.eps,
+            self.weight_decay, self.seed, _stream(stream, self.m)))
         self.step_count += 1
 
     def moments(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """The values the codes of both moments stand for, as flat bf16 tensors (exact)."""
+        n = self.m.numel()
         with _on(stream):
-            out = torch.empty((2, self.m.numel()), dtype=torch.bfloat16, device=self.m.device)
-        m, v = out[0], out[1]
+            m = torch.empty(n, dtype=torch.bfloat16, device=self.m.device)
+            v = torch.empty(n, dtype=torch.bfloat16, device=self.m.device)
         _check("muon_adamw8_unpack", load_library().muon_adamw8_unpack(
-            self.m.data_ptr(), self.m_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr(), self.m.numel(),
-            m.data_ptr(), v.data_ptr(), _stream(stream)))
+            *self._state, n, m.data_ptr(), v.data_ptr(), _stream(stream, self.m)))
         return m, v
 
     def state_dict(self) -> Dict:

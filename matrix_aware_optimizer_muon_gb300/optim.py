@@ -54,6 +54,9 @@ class PeriodicMuon:
                 raise ValueError("W, G and M must have the same shape")
             self._arr[i].G = _lib._ptr(g)
             self._arr[i].g_dtype = _lib._dt(g)
+        if self.aux8 is not None:   # refused before anything is enqueued
+            aux_grads = [g.contiguous() for g in aux_grads]
+            self.aux8._check(aux_grads)
         br = _lib.periodic_step_prepared(self._arr, self._n, self.step_count, self.ws, self.K, self.gamma, self.mu,
                                          self.eta, self.lam, self.ns5_mode, stream=stream)
         if self.aux:
@@ -63,7 +66,7 @@ class PeriodicMuon:
             # the schedule of learning rate and decay is the caller's, as for 32 bits
             self.aux8.lr, self.aux8.betas, self.aux8.eps, self.aux8.weight_decay = self.aux_lr, self.betas, self.eps, self.lam
             self.aux8.step_count = self.step_count
-            self.aux8.step([g.contiguous() for g in aux_grads], stream=stream)
+            self.aux8.step(aux_grads, stream=stream)
         elif self.aux:
             _lib.muon_adamw_step([p.view(-1) for p in self.aux], [g.reshape(-1) for g in aux_grads], self.aux_m,
                                  self.aux_v, self.step_count + 1, self.aux_lr, self.betas[0], self.betas[1],

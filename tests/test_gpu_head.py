@@ -350,6 +350,25 @@ def test_linear_ce_large_repeats_and_other_stream():
     assert none is None and torch.equal(dw, a[1])
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_linear_ce_upstream_factor(dt):
+    """A factor on the device multiplies both gradients once, whichever way dH is summed
+    (few rows: ranges of K; more: none), and the rounding of g does not depend on it."""
+    for n, v, d in ((24, 3000, 64), (600, 700, 96)):
+        h, h64, w, w64, labels, lab = ce_case(n, v, d, dt, 77)
+        ws = mm.alloc_linear_ce_workspace(n, v, d, TYPES[dt])
+        _, lse, stats = mm.muon_linear_ce_forward(h, w, labels, ws)
+        one = mm.muon_linear_ce_backward(h, w, labels, lse, ws)
+        up = torch.tensor(0.125, device=dev())
+        a = mm.muon_linear_ce_backward(h, w, labels, lse, ws, upstream=up, grad_scale=4.0)
+        assert all(torch.equal(p * 0.5, q) for p, q in zip(one, a))
+        count = stats[1].item()
+        b = mm.muon_linear_ce_backward(h, w, labels, lse, ws, stats=stats)
+        for p, q in zip(one, b):
+            tol = (2 * BF if dt == "bf16" else 4 * U) * np.abs(num(p)) / count
+            within(num(q), num(p) / count, tol, "mean")
+
+
 def test_linear_ce_in_a_cuda_graph():
     n, v, d = 130, 1000, 64
     h, h64, w, w64, labels, lab = ce_case(n, v, d, "bf16", 31)

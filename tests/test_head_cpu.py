@@ -179,7 +179,7 @@ def test_linear_ce_refusals(lib):
         return lib.muon_linear_ce_forward(ctypes.byref(a), loss, lse, stats, ws, n, None)
 
     def bwd(a, lse=FAKE, dH=FAKE, dW=FAKE, ws=FAKE, n=1 << 40):
-        return lib.muon_linear_ce_backward(ctypes.byref(a), lse, None, None, 1.0, dH, dW, ws, n, None)
+        return lib.muon_linear_ce_backward(ctypes.byref(a), lse, None, None, None, 1.0, dH, dW, ws, n, None)
 
     for bad in (dict(rows=-1), dict(vocab=0), dict(dim=0), dict(ldh=7), dict(ldw=7), dict(rows=1 << 31)):
         assert size(_ce(**bad), 1) == big and fwd(_ce(**bad)) == -1 and bwd(_ce(**bad)) == -1, bad
