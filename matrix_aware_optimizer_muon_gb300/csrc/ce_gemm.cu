@@ -273,6 +273,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  allow_next();
+  await_previous();
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ producers (both CTAs)
@@ -287,19 +289,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
         const Job& J = p.job[ti.job];
         const CUtensorMap* map = is_b ? &J.b : &J.a;
         const bool mn = is_b ? J.b_mn : J.a_mn;
-        const int r0 = is_b ? ti.tn * TILE + rank * HALF + J.b_n0 : ti.tm * TILE + rank * HALF;
+        // boxes that lie wholly past the output's rows or columns are not fetched: what the
+        // MMAs make of stale data there is never read
+        const int t0 = is_b ? ti.tn * TILE : ti.tm * TILE, left = (is_b ? J.n : J.m) - t0;
+        const int boxes = min(max((left - rank * HALF + BOX - 1) / BOX, 0), 2);
+        const uint32_t bytes = min((left + BOX - 1) / BOX, 4) * BOX_BYTES;   // of both CTAs
+        const int r0 = t0 + rank * HALF + (is_b ? J.b_n0 : 0);
         const int k0 = ti.split * J.nkb * BK + (is_b ? J.b_k0 : 0);
         for (int term = 0; term < p.nterms && !stop; ++term) {
           const int z = is_b ? p.tb[term] : p.ta[term];
           for (int kb = 0; kb < J.nkb; ++kb) {
             if (!wait_for(&empty[stage], phase ^ 1u, abort_flag, p, true)) { stop = true; break; }
             const uint32_t fb = ptx::mapa_shared(ptx::smem_addr(&full[stage]), 0);
-            if (even) ptx::mbar_arrive_expect_tx(&full[stage], 2 * OP_BYTES);
+            if (even) ptx::mbar_arrive_expect_tx(&full[stage], bytes);
             const uint32_t d = ptx::smem_addr(smem + stage * STAGE_BYTES) + (is_b ? OP_BYTES : 0);
             const int k = k0 + kb * BK;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-              ptx::tma_load_3d_pair(d + q * BOX_BYTES, map, fb, mn ? r0 + q * BOX : k, mn ? k : r0 + q * BOX, z);
+              if (q < boxes)
+                ptx::tma_load_3d_pair(d + q * BOX_BYTES, map, fb, mn ? r0 + q * BOX : k, mn ? k : r0 + q * BOX, z);
             pending |= 1u << stage;
             pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -464,12 +472,11 @@ cudaError_t launch(const OrderedParams& p, bool ordered, bool promote, cudaStrea
   const int n = pairs();
   if (n < 1) return cudaErrorInvalidConfiguration;
   const int grid = 2 * (p.tiles < n ? p.tiles : n);
-  if (promote && ordered) ce_kernel<true, OrderedParams><<<grid, THREADS, SMEM, s>>>(p);
-  else if (promote) ce_kernel<true, Params><<<grid, THREADS, SMEM, s>>>(p);
-  else if (ordered) ce_kernel<false, OrderedParams><<<grid, THREADS, SMEM, s>>>(p);
-  else ce_kernel<false, Params><<<grid, THREADS, SMEM, s>>>(p);
   count_launch();
-  return cudaGetLastError();
+  if (promote && ordered) return launch_after(ce_kernel<true, OrderedParams>, grid, THREADS, SMEM, s, p);
+  if (promote) return launch_after(ce_kernel<true, Params>, grid, THREADS, SMEM, s, p);
+  if (ordered) return launch_after(ce_kernel<false, OrderedParams>, grid, THREADS, SMEM, s, p);
+  return launch_after(ce_kernel<false, Params>, grid, THREADS, SMEM, s, p);
 }
 
 }  // namespace ce

@@ -144,6 +144,27 @@ constexpr uint32_t DEV_TIMEOUT = 1u;
 constexpr uint32_t DEV_NONFINITE = 2u;
 
 #ifdef __CUDACC__
+// A kernel that reads what the one before it on the stream writes, launched so that its
+// CTAs may start (and set themselves up) while that one's last CTAs still run.  It calls
+// await_previous() before it touches any memory another kernel writes.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel's CTAs start where this one leaves room.
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Finite check of a sum of squares of the momentum (status null: check off).
 __device__ __forceinline__ void note_nonfinite(unsigned int* status, float ss) {
   if (status && !isfinite(ss)) atomicOr(status, DEV_NONFINITE);

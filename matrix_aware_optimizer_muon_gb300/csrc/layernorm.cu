@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(LN_SLAB_THREADS) ln_slab_kernel(const LnBwd p)
 __global__ void __launch_bounds__(1024) ln_columns_kernel(const float* part, int lines, int dim, void* dw, void* db,
                                                           int w_bf16) {
   __shared__ float tile[32][33];
+  await_previous();
   const int c = blockIdx.x * 32 + threadIdx.x, which = blockIdx.y;
   void* out = which ? db : dw;
   if (!out) return;
@@ -646,8 +647,10 @@ extern "C" int muon_layernorm_backward(const void* dy, int64_t lddy, const void*
   const cudaError_t e = x_dtype == MUON_DTYPE_BF16 ? backward<bf16>(p, vec, &lines, s) : backward<float>(p, vec, &lines, s);
   if (e != cudaSuccess) return MUON_ERR_CUDA;
   if (sums) {
-    ln_columns_kernel<<<dim3(cdiv(dim, 32), 2), dim3(32, 32), 0, s>>>(p.part, lines, (int)dim, dweight, dbias, p.w_bf16);
     count_launch();
+    if (launch_after(ln_columns_kernel, dim3(cdiv(dim, 32), 2), dim3(32, 32), 0, s, p.part, lines, (int)dim, dweight,
+                     dbias, p.w_bf16) != cudaSuccess)
+      return MUON_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

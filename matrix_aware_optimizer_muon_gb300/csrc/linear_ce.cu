@@ -24,11 +24,11 @@ constexpr int TICKET_WORD = 16;    // of the header
 
 // A piece's g is rows x piece bf16 (three times that for 32-bit operands), twice: one
 // piece is multiplied while the next is computed.
-constexpr int64_t G_BYTES = 96 << 20;
+constexpr int64_t G_BYTES = 512 << 20;
 constexpr int64_t MIN_PIECE = 2048;
 constexpr int MAX_SPLITS = 16;
 // K steps (of 64) between take-overs of the tensor cores' sums into registers.
-constexpr int SEG_BF16 = 20, SEG_F32 = 4;
+constexpr int SEG_BF16 = 20, SEG_F32 = 8;
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -60,49 +60,84 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* in, long long ld, lo
   }
 }
 
-// One warp a row: joins its partial sums, writes lse and loss; the last block to finish
-// sums the losses (each thread a fixed set of rows, then a fixed tree).
+// One warp a row: joins its partial sums (up to 32 a lane in one pass), writes lse and
+// loss.  Each block adds its rows' losses up; the last block to finish adds the blocks'.
 constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_HELD = 8;   // partial sums a lane keeps at a time
 __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const float2* part, int parts, long long rows,
                                                                const int64_t* labels, long long vocab, long long ignore,
                                                                const float* zlabel, float* loss, float* lse,
-                                                               float* stats, unsigned int* ticket) {
+                                                               float* stats, float2* sums, unsigned int* ticket) {
   __shared__ float red[32];
+  __shared__ float2 mine[JOIN_WARPS];
   __shared__ bool last;
-  const int lane = threadIdx.x & 31;
-  const long long r = (long long)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+  await_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long r = (long long)blockIdx.x * JOIN_WARPS + warp;
+  float2 sum = make_float2(0.f, 0.f);   // this row's loss, and 1 if it counts
   if (r < rows) {
     const float2* q = part + (size_t)r * parts;
-    float mx = -INFINITY;
-    for (int t = lane; t < parts; t += 32) mx = fmaxf(mx, q[t].x);
+    const long long lab = labels[r];
+    const bool counted = lab != ignore, known = counted && lab >= 0 && lab < vocab;
+    const float zl = known ? zlabel[r] : 0.f;
+    float mx = -INFINITY, s = 0.f;
+    for (int t0 = 0; t0 < parts; t0 += 32 * JOIN_HELD) {
+      float2 w[JOIN_HELD];
+      float m = mx;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    float s = 0.f;
-    for (int t = lane; t < parts; t += 32) {
-      const float2 w = q[t];
-      s += w.x == -INFINITY ? w.y : w.y * expf(w.x - ref);
+      for (int i = 0; i < JOIN_HELD; ++i) {
+        const int t = t0 + 32 * i + lane;
+        w[i] = t < parts ? q[t] : make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < JOIN_HELD; ++i) m = fmaxf(m, w[i].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+      s = mx == -INFINITY ? s : s * expf(mx - ref);
+#pragma unroll
+      for (int i = 0; i < JOIN_HELD; ++i) s += w[i].x == -INFINITY ? w[i].y : w[i].y * expf(w[i].x - ref);
+      mx = m;
     }
-    s = warp_sum(s);
+    float top = mx;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    s = warp_sum(mx == -INFINITY ? s : s * expf(mx - ref));
+    const float l = ref + logf(s);
+    const float x = known ? l - zl : counted ? __int_as_float(0x7FC00000) : 0.f;
     if (lane == 0) {
-      const float l = ref + logf(s);
-      const long long lab = labels[r];
       lse[r] = l;
-      loss[r] = lab == ignore ? 0.f : (lab < 0 || lab >= vocab) ? __int_as_float(0x7FC00000) : l - zlabel[r];
+      loss[r] = x;
     }
+    sum = make_float2(x, counted ? 1.f : 0.f);
   }
   if (!stats) return;
-  __threadfence();
+  if (lane == 0) mine[warp] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+  if (threadIdx.x == 0) {
+    float2 b = make_float2(0.f, 0.f);
+    for (int i = 0; i < JOIN_WARPS; ++i) { b.x += mine[i].x; b.y += mine[i].y; }
+    mine[0] = b;
+    last = true;
+    if (gridDim.x > 1) {
+      sums[blockIdx.x] = b;
+      __threadfence();
+      last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+    }
+  }
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  float s = 0.f, c = 0.f;
-  for (long long i = threadIdx.x; i < rows; i += 32 * JOIN_WARPS)
-    if (labels[i] != ignore) { s += __ldcg(loss + i); c += 1.f; }
-  s = block_sum(s, red);
-  c = block_sum(c, red);
+  float s = mine[0].x, c = mine[0].y;
+  if (gridDim.x > 1) {
+    __threadfence();
+    s = c = 0.f;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += 32 * JOIN_WARPS) {
+      const float2 b = __ldcg(sums + i);
+      s += b.x;
+      c += b.y;
+    }
+    s = block_sum(s, red);
+    c = block_sum(c, red);
+  }
   if (threadIdx.x == 0) {
     stats[0] = s / fmaxf(c, 1.f);
     stats[1] = c;
@@ -115,6 +150,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) split_sum_kernel(const float* acc, int splits, long long rows, int dim,
                                                         long long ldacc, T* out, float scale, const float* upstream,
                                                         const float* stats) {
+  await_previous();
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const long long r = i / dim;
   if (r >= rows) return;
@@ -132,7 +168,7 @@ struct CePlan {
   int64_t dp;                  // row length of a packed copy
   bool pack_h, pack_w;
   size_t hp, wp;               // packed copies
-  size_t zlabel, part;         // forward
+  size_t zlabel, part, sums;   // forward
   int64_t piece, npieces;
   int splits;
   size_t g[2];
@@ -187,6 +223,7 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P) {
   const size_t common = at;
   P->zlabel = take((size_t)a->rows * 4);
   P->part = take((size_t)a->rows * 2 * cdiv(a->vocab, TILE) * sizeof(float2));
+  P->sums = take((size_t)cdiv(a->rows, JOIN_WARPS) * sizeof(float2));
   P->total = at;
   if (!backward) return;
   at = common;
@@ -366,10 +403,12 @@ extern "C" int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, floa
   p.njobs = 1;
   p.tiles = j.tiles;
   if (launch(p, false, true, s) != cudaSuccess) return MUON_ERR_CUDA;
-  join_kernel<<<(unsigned)cdiv(a->rows, JOIN_WARPS), 32 * JOIN_WARPS, 0, s>>>(
-      p.part, 2 * j.ntiles, a->rows, a->labels, a->vocab, a->ignore_index, p.zlabel, loss, lse, stats,
-      static_cast<unsigned int*>(ws) + TICKET_WORD);
   count_launch();
+  if (launch_after(join_kernel, dim3((unsigned)cdiv(a->rows, JOIN_WARPS)), dim3(32 * JOIN_WARPS), 0, s, p.part,
+                   2 * j.ntiles, a->rows, a->labels, a->vocab, a->ignore_index, p.zlabel, loss, lse, stats,
+                   reinterpret_cast<float2*>(w + P.sums), reinterpret_cast<unsigned int*>(w) + TICKET_WORD) !=
+      cudaSuccess)
+    return MUON_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
@@ -466,9 +505,13 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
     if (launch(p, ordered, f32, s) != cudaSuccess) return MUON_ERR_CUDA;
   }
   if (dH && P.splits > 1) {
-    const unsigned blocks = (unsigned)cdiv(a->rows * a->dim, 256);
-    if (f32) split_sum_kernel<float><<<blocks, 256, 0, s>>>(acc, P.splits, a->rows, (int)a->dim, P.ldacc, static_cast<float*>(dH), grad_scale, upstream, stats);
-    else split_sum_kernel<bf16><<<blocks, 256, 0, s>>>(acc, P.splits, a->rows, (int)a->dim, P.ldacc, static_cast<bf16*>(dH), grad_scale, upstream, stats);
+    const dim3 blocks((unsigned)cdiv(a->rows * a->dim, 256));
+    const cudaError_t e =
+        f32 ? launch_after(split_sum_kernel<float>, blocks, dim3(256), 0, s, acc, P.splits, a->rows, a->dim, P.ldacc,
+                           static_cast<float*>(dH), grad_scale, upstream, stats)
+            : launch_after(split_sum_kernel<bf16>, blocks, dim3(256), 0, s, acc, P.splits, a->rows, a->dim, P.ldacc,
+                           static_cast<bf16*>(dH), grad_scale, upstream, stats);
+    if (e != cudaSuccess) return MUON_ERR_CUDA;
     count_launch();
   }
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
