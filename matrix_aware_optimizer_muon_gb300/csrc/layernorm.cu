@@ -6,6 +6,7 @@
 // Every sum is fp32.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -78,7 +79,7 @@ template <typename T, int kN> struct Raw<T, 1, kN> {
   template <int kSure = 0>
   __device__ __forceinline__ void load(const T* x, int t, int size, int dim) {
 #pragma unroll
-    for (int k = 0; k < kN; ++k) e[k] = k * size + t < dim ? x[k * size + t] : from_f32<T>(0.f);
+    for (int k = 0; k < kN; ++k) e[k] = k < kSure || k * size + t < dim ? x[k * size + t] : from_f32<T>(0.f);
   }
   __device__ __forceinline__ void get(int k, f32x2* v) const { v[0] = make2(to_f32(e[k]), 0.f); }
   __device__ __forceinline__ void hold() {}
@@ -87,12 +88,12 @@ template <typename T, int kN> struct Raw<T, 1, kN> {
     for (int k = 0; k < kN; k += 2) v[k / 2] = make2(to_f32(e[k]), k + 1 < kN ? to_f32(e[(k + 1) % kN]) : 0.f);
   }
 };
-template <typename T, int kV, int kN>
+template <typename T, int kV, int kN, int kSure>
 __device__ __forceinline__ void store_row(T* y, const f32x2* v, int t, int size, int dim) {
 #pragma unroll
   for (int k = 0; k < kN; ++k) {
     const int c = (k * size + t) * kV;
-    if (c < dim) {
+    if (k < kSure || c < dim) {
       if constexpr (kV > 1) store16(y + c, v + k * (kV / 2));
       else st1(y + c, elem(v, k));
     }
@@ -161,15 +162,16 @@ struct LnFwd {
   float eps;
 };
 
-// kSure: how many of a thread's accesses lie inside the row for every thread.
+// How many of a thread's n accesses lie inside the row for every thread: the launcher takes
+// the least n that covers the row out of 1 .. 8, 10, 12, 16.
 __host__ __device__ constexpr int ln_sure(int n) { return n <= 8 ? n - 1 : n <= 12 ? n - 2 : n - 4; }
 // CTAs of a warp-a-row kernel an SM should hold: registers for the row and about 32 more.
 constexpr int ln_fwd_ctas(int n, bool warp) { return warp ? 256 / (4 * n + 32) : 1; }
-template <typename T, int kV, int kN, bool kWarp, int kW>
-__global__ void __launch_bounds__(kWarp ? 32 * LN_WARPS : 1024, ln_fwd_ctas(kN, kWarp)) ln_forward_kernel(const LnFwd p) {
-  constexpr int kSure = kWarp && kV > 1 ? ln_sure(kN) : 0;
+template <typename T, int kV, int kN, bool kWarp, int kW, int kSize>
+__global__ void __launch_bounds__(kWarp ? 32 * LN_WARPS : kSize ? kSize : 1024, ln_fwd_ctas(kN, kWarp)) ln_forward_kernel(const LnFwd p) {
+  constexpr int kSure = kWarp || kSize ? ln_sure(kN) : 0;
   __shared__ __align__(8) float red[kWarp ? 2 : 128];
-  const int t = kWarp ? threadIdx.x & 31 : threadIdx.x, size = kWarp ? 32 : blockDim.x;
+  const int t = kWarp ? threadIdx.x & 31 : threadIdx.x, size = kWarp ? 32 : kSize ? kSize : blockDim.x;
   const long long r = kWarp ? (long long)blockIdx.x * LN_WARPS + (threadIdx.x >> 5) : blockIdx.x;
   if (kWarp && r >= p.rows) return;
   const Group grp{t, size, 0, red};
@@ -277,12 +279,14 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
                : "memory");
 }
 
-template <typename T, int kV, int kN>
-__global__ void __launch_bounds__(512, 1) ln_backward_kernel(const LnBwd p) {
+constexpr int LN_BWD_THREADS = 512;
+template <typename T, int kV, int kN, int kSize>
+__global__ void __launch_bounds__(LN_BWD_THREADS, 1) ln_backward_kernel(const LnBwd p) {
   extern __shared__ uint4 dyn[];
   __shared__ __align__(8) float red[LN_GROUPS * 128];
   using S = Share<kV, kN>;
-  const int t = threadIdx.x, size = blockDim.x, grp_i = threadIdx.y, groups = blockDim.y;
+  constexpr int kSure = kSize ? ln_sure(kN) : 0;
+  const int t = threadIdx.x, size = kSize ? kSize : blockDim.x, grp_i = threadIdx.y, groups = blockDim.y;
   const int nthr = size * groups, tid = grp_i * size + t;
   const Group grp{t, size, 1 + grp_i, red + 128 * grp_i};
   const float inv = 1.f / (float)p.dim;
@@ -305,49 +309,57 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const LnBwd p) {
     }
   }
   constexpr int R = ln_ring(kN);
-  auto slot = [&](int s, int which, int k) { return dyn + ((s * 2 + which) * kN + k) * nthr + tid; };
-  auto fetch = [&](long long row, int s) {   // one group of copies, empty past the last row
-    if constexpr (kV > 1) {
-      if (row < p.rows) {
-        const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-        const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+  // where the next row to be fetched lies, and the row at hand
+  const T* xf = static_cast<const T*>(p.x) + r * p.ldx;
+  const T* gf = static_cast<const T*>(p.dy) + r * p.lddy;
+  T* dx = static_cast<T*>(p.dx) + r * p.lddx;
+  const float *mean = p.mean + r, *rstd = p.rstd + r;
+  const long long sx = step * p.ldx, sg = step * p.lddy, sd = step * p.lddx;
+  long long rf = r;
+  uint4* const mine = dyn + tid;                // [slot][x, dy][access][thread]
+  auto fetch = [&](int slot) {                  // one group of copies, empty past the last row
+    if (rf < p.rows) {
+      uint4* d = mine + slot * (2 * kN) * nthr;
 #pragma unroll
-        for (int k = 0; k < kN; ++k) {
-          const int c = (k * size + t) * kV;
-          if (c < p.dim) {
-            copy16(slot(s, 0, k), x + c);
-            copy16(slot(s, 1, k), dy + c);
-          }
+      for (int k = 0; k < kN; ++k) {
+        const int c = (k * size + t) * kV;
+        if (k < kSure || c < p.dim) {
+          copy16(d + k * nthr, xf + c);
+          copy16(d + (kN + k) * nthr, gf + c);
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    rf += step;
+    xf += sx;
+    gf += sg;
   };
   Raw<T, kV, kN> xn, gn;
   float mu_n = 0.f, rs_n = 0.f;
   if constexpr (kV > 1) {
     // slots that are never copied to belong to columns past the row: zero
 #pragma unroll
-    for (int k = 0; k < kN; ++k)
+    for (int k = kSure; k < kN; ++k)
       if ((k * size + t) * kV >= p.dim)
-        for (int s = 0; s < R; ++s) *slot(s, 0, k) = *slot(s, 1, k) = make_uint4(0, 0, 0, 0);
-    for (int s = 0; s < R - 1; ++s) fetch(r + s * step, s);
+        for (int s = 0; s < 2 * R; ++s) mine[(s * kN + k) * nthr] = make_uint4(0, 0, 0, 0);
+    for (int s = 0; s < R - 1; ++s) fetch(s);
   } else if (r < p.rows) {
-    xn.load(static_cast<const T*>(p.x) + r * p.ldx, t, size, p.dim);
-    gn.load(static_cast<const T*>(p.dy) + r * p.lddy, t, size, p.dim);
+    xn.template load<kSure>(xf, t, size, p.dim);
+    gn.template load<kSure>(gf, t, size, p.dim);
   }
-  if (r < p.rows) { mu_n = p.mean[r]; rs_n = p.rstd[r]; }
+  if (r < p.rows) { mu_n = *mean; rs_n = *rstd; }
   int parity = 0, at = 0;
   for (; r < p.rows; r += step) {
     f32x2 xh[S::P], g[S::P];
     const float mu = mu_n, rs = rs_n;
     if constexpr (kV > 1) {
-      fetch(r + (R - 1) * step, at == 0 ? R - 1 : at - 1);
+      fetch(at == 0 ? R - 1 : at - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
+      const uint4* d = mine + at * (2 * kN) * nthr;
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
-        widen(*slot(at, 0, k), xh + k * (kV / 2), static_cast<const T*>(nullptr));
-        widen(*slot(at, 1, k), g + k * (kV / 2), static_cast<const T*>(nullptr));
+        widen(d[k * nthr], xh + k * (kV / 2), static_cast<const T*>(nullptr));
+        widen(d[(kN + k) * nthr], g + k * (kV / 2), static_cast<const T*>(nullptr));
       }
       at = at + 1 == R ? 0 : at + 1;
     } else {
@@ -355,11 +367,15 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const LnBwd p) {
       gn.pairs(g);
     }
     if (r + step < p.rows) {
-      mu_n = p.mean[r + step];
-      rs_n = p.rstd[r + step];
+      mean += step;
+      rstd += step;
+      mu_n = *mean;
+      rs_n = *rstd;
       if constexpr (kV == 1) {
-        xn.load(static_cast<const T*>(p.x) + (r + step) * p.ldx, t, size, p.dim);
-        gn.load(static_cast<const T*>(p.dy) + (r + step) * p.lddy, t, size, p.dim);
+        xf += sx;
+        gf += sg;
+        xn.template load<kSure>(xf, t, size, p.dim);
+        gn.template load<kSure>(gf, t, size, p.dim);
       }
     }
     f32x2 s1 = both(0.f), s2 = both(0.f);
@@ -377,7 +393,8 @@ __global__ void __launch_bounds__(512, 1) ln_backward_kernel(const LnBwd p) {
     const f32x2 c1 = both(-rs * (c12.x * inv)), c2 = both(-rs * (c12.y * inv));
 #pragma unroll
     for (int i = 0; i < S::P; ++i) g[i] = fma2(xh[i], c2, fma2(g[i], both(rs), c1));
-    store_row<T, kV, kN>(static_cast<T*>(p.dx) + r * p.lddx, g, t, size, p.dim);
+    store_row<T, kV, kN, kSure>(dx, g, t, size, p.dim);
+    dx += sd;
   }
   if (!p.part) return;
   if constexpr (kV > 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -478,52 +495,56 @@ bool vec_rows(const void* p, int64_t ld, int64_t rows, size_t es) {
   return is_aligned(p, 16) && (rows <= 1 || (size_t)ld * es % 16 == 0);
 }
 
-template <typename T, int kV, bool kWarp, int kW>
-bool forward_n(const LnFwd& p, int need, int threads, cudaStream_t s) {
-  const unsigned grid = (unsigned)(kWarp ? cdiv(p.rows, LN_WARPS) : p.rows);
-#define MUON_LN_FWD(N)                                                   \
-  if (need <= N) {                                                       \
-    ln_forward_kernel<T, kV, N, kWarp, kW><<<grid, threads, 0, s>>>(p);  \
-    return true;                                                         \
+// f(std::integral_constant<int, N>) for the least N of ln_sure's list that is >= need.
+template <class F>
+bool by_accesses(int need, F f) {
+  switch (need <= 8 ? need : need <= 10 ? 10 : need <= 12 ? 12 : 16) {
+#define MUON_LN_N(N) \
+  case N: f(std::integral_constant<int, N>()); return need <= 16;
+    MUON_LN_N(1) MUON_LN_N(2) MUON_LN_N(3) MUON_LN_N(4) MUON_LN_N(5) MUON_LN_N(6) MUON_LN_N(7) MUON_LN_N(8)
+    MUON_LN_N(10) MUON_LN_N(12) MUON_LN_N(16)
+#undef MUON_LN_N
   }
-  if constexpr (kV > 1 && kWarp) {
-    MUON_LN_FWD(1) MUON_LN_FWD(2) MUON_LN_FWD(3) MUON_LN_FWD(4) MUON_LN_FWD(5) MUON_LN_FWD(6) MUON_LN_FWD(7)
-    MUON_LN_FWD(8) MUON_LN_FWD(10) MUON_LN_FWD(12) MUON_LN_FWD(16)
-  } else if constexpr (kV > 1) {
-    MUON_LN_FWD(1) MUON_LN_FWD(2) MUON_LN_FWD(4)
-  } else if constexpr (kWarp) {
-    MUON_LN_FWD(2) MUON_LN_FWD(8) MUON_LN_FWD(16)
-  } else {
-    MUON_LN_FWD(4) MUON_LN_FWD(8) MUON_LN_FWD(16)
-  }
-#undef MUON_LN_FWD
   return false;
 }
-template <typename T, int kV, bool kWarp>
-bool forward_w(const LnFwd& p, int need, int threads, cudaStream_t s) {
+
+template <typename T, int kV, int kN, bool kWarp, int kSize>
+void forward_launch(const LnFwd& p, int threads, cudaStream_t s) {
+  const unsigned grid = (unsigned)(kWarp ? cdiv(p.rows, LN_WARPS) : p.rows);
   if constexpr (kV > 1 && kWarp) {
-    if (p.w && p.b && p.w_bf16) return forward_n<T, kV, kWarp, W_BF16>(p, need, threads, s);
-    if (p.w && p.b) return forward_n<T, kV, kWarp, W_F32>(p, need, threads, s);
+    if (p.w && p.b && p.w_bf16) { ln_forward_kernel<T, kV, kN, kWarp, W_BF16, kSize><<<grid, threads, 0, s>>>(p); return; }
+    if (p.w && p.b) { ln_forward_kernel<T, kV, kN, kWarp, W_F32, kSize><<<grid, threads, 0, s>>>(p); return; }
   }
-  return forward_n<T, kV, kWarp, W_ASK>(p, need, threads, s);
+  ln_forward_kernel<T, kV, kN, kWarp, W_ASK, kSize><<<grid, threads, 0, s>>>(p);
 }
 
-// A warp per row while a lane holds its share of the row in registers (16 accesses);
-// above that a CTA per row.
+// A warp per row while a lane holds its share of the row in registers (16 accesses, 8 of
+// single elements); above that a CTA per row.
 template <typename T>
 void forward(const LnFwd& p, bool vec, cudaStream_t s) {
   constexpr int V = vec_of<T>();
-  if (vec) {
-    const int nv = p.dim / V;
-    if (forward_w<T, V, true>(p, cdiv(nv, 32), 32 * LN_WARPS, s)) return;
-    const int threads = 32 * cdiv(nv, 32LL * cdiv(nv, 1024));
-    if (forward_w<T, V, false>(p, cdiv(nv, threads), threads, s)) return;
+  const int n = vec ? p.dim / V : p.dim;   // accesses
+  const int need = cdiv(n, 32);
+  if (vec && need <= 16) {
+    by_accesses(need, [&](auto N) { forward_launch<T, V, decltype(N)::value, true, 32>(p, 32 * LN_WARPS, s); });
+  } else if (vec && n <= 4096) {
+    const int threads = 32 * cdiv(n, 32LL * cdiv(n, 1024)), each = cdiv(n, threads);
+    if (each == 1) forward_launch<T, V, 1, false, 0>(p, threads, s);
+    else if (each == 2) forward_launch<T, V, 2, false, 0>(p, threads, s);
+    else forward_launch<T, V, 4, false, 0>(p, threads, s);
+  } else if (!vec && need <= 8) {
+    by_accesses(need, [&](auto N) {
+      if constexpr (decltype(N)::value <= 8) forward_launch<T, 1, decltype(N)::value, true, 32>(p, 32 * LN_WARPS, s);
+    });
+  } else if (!vec && n <= 256 * 16) {
+    by_accesses(cdiv(n, 256), [&](auto N) { forward_launch<T, 1, decltype(N)::value, false, 256>(p, 256, s); });
+  } else if (!vec && n <= 1024 * 16) {
+    by_accesses(cdiv(n, 1024), [&](auto N) {
+      if constexpr (decltype(N)::value >= 4) forward_launch<T, 1, decltype(N)::value, false, 1024>(p, 1024, s);
+    });
   } else {
-    if (forward_w<T, 1, true>(p, cdiv(p.dim, 32), 32 * LN_WARPS, s)) return;
-    const int threads = 32 * cdiv(p.dim, 32LL * std::max(8, cdiv(p.dim, 1024)));
-    if (forward_w<T, 1, false>(p, cdiv(p.dim, threads), threads, s)) return;
+    ln_forward_loop_kernel<T><<<(unsigned)p.rows, LN_LOOP_THREADS, 0, s>>>(p);
   }
-  ln_forward_loop_kernel<T><<<(unsigned)p.rows, LN_LOOP_THREADS, 0, s>>>(p);
 }
 
 // The backward pass's CTAs: one on each SM (its registers fill it); every CTA writes one
@@ -531,55 +552,63 @@ void forward(const LnFwd& p, bool vec, cudaStream_t s) {
 constexpr int LN_CTAS = 152;
 constexpr int LN_MAX_SMEM = 200 * 1024;
 
-template <typename T, int kV, int kN>
-bool backward_n(const LnBwd& p, int threads, int* lines, cudaStream_t s, cudaError_t* err) {
-  int groups = std::max(1, std::min(512 / threads, LN_GROUPS));
+template <typename T, int kV, int kN, int kSize>
+cudaError_t backward_launch(const LnBwd& p, int threads, int* lines, cudaStream_t s) {
+  int groups = std::max(1, std::min(LN_BWD_THREADS / threads, LN_GROUPS));
   auto smem_of = [&](int g) {
     const size_t ring = kV > 1 ? (size_t)ln_ring(kN) * 2 * kN * 16 * threads * g : 0;
     return std::max(ring, p.part ? (size_t)(g - 1) * 2 * p.dim * 4 : 0);
   };
   while (groups > 1 && smem_of(groups) > (size_t)LN_MAX_SMEM) --groups;
-  const int grid = (int)std::min<long long>((p.rows + groups - 1) / groups, LN_CTAS);
   const size_t smem = smem_of(groups);
-  if (smem > 40 * 1024 &&
-      (*err = cudaFuncSetAttribute(ln_backward_kernel<T, kV, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   LN_MAX_SMEM)) != cudaSuccess)
-    return true;
-  ln_backward_kernel<T, kV, kN><<<grid, dim3(threads, groups), smem, s>>>(p);
-  *lines = grid;
-  return true;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(ln_backward_kernel<T, kV, kN, kSize>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, LN_MAX_SMEM);
+    if (e != cudaSuccess) return e;
+  }
+  *lines = (int)std::min<long long>((p.rows + groups - 1) / groups, LN_CTAS);
+  ln_backward_kernel<T, kV, kN, kSize><<<*lines, dim3(threads, groups), smem, s>>>(p);
+  count_launch();
+  return cudaGetLastError();
 }
 
 // 16 columns a thread (registers hold their sums, weights and the row), 8 for rows that 16
-// would leave to less than two warps; element-wise rows 8, then 16.
-template <typename T, int kV>
-bool backward_v(const LnBwd& p, int accesses, int* lines, cudaStream_t s, cudaError_t* err) {
-  constexpr int A = kV > 1 ? 8 / kV : 4, B = kV > 1 ? 16 / kV : 8;
-  auto threads = [&](int n) { return 32 * cdiv(accesses, 32LL * n); };
-  if (accesses <= 32 * B) return backward_n<T, kV, A>(p, threads(A), lines, s, err);
-  if (threads(B) <= 512) return backward_n<T, kV, B>(p, threads(B), lines, s, err);
-  if constexpr (kV == 1) {
-    if (threads(16) <= 512) return backward_n<T, kV, 16>(p, threads(16), lines, s, err);
-  }
-  return false;
-}
-
+// would leave to less than two warps.  Element-wise rows: a fixed number of threads, so that
+// an access is an offset the instruction holds, and as few columns each as cover the row.
 template <typename T>
 cudaError_t backward(const LnBwd& p, bool vec, int* lines, cudaStream_t s) {
-  cudaError_t err = cudaSuccess;
+  constexpr int V = vec_of<T>();
+  cudaError_t e = cudaSuccess;
   *lines = 0;
-  if (p.rows == 0) return err;
-  bool done = vec ? backward_v<T, vec_of<T>()>(p, p.dim / vec_of<T>(), lines, s, &err)
-                  : backward_v<T, 1>(p, p.dim, lines, s, &err);
-  if (err != cudaSuccess) return err;
-  if (!done) {
-    if (p.part) {
-      *lines = (int)std::min<long long>(p.rows, LN_CTAS);
-      ln_slab_kernel<T><<<dim3(cdiv(p.dim, LN_SLAB_THREADS), *lines), LN_SLAB_THREADS, 0, s>>>(p);
-      count_launch();
-    }
-    ln_backward_loop_kernel<T><<<(unsigned)p.rows, LN_LOOP_THREADS, 0, s>>>(p);
+  if (p.rows == 0) return e;
+  const int n = vec ? p.dim / V : p.dim;
+  auto threads = [&](int each) { return 32 * cdiv(n, 32LL * each); };
+  if (vec && n <= 32 * 16 / V) return backward_launch<T, V, 8 / V, 0>(p, threads(8 / V), lines, s);
+  if (vec && threads(16 / V) <= LN_BWD_THREADS) return backward_launch<T, V, 16 / V, 0>(p, threads(16 / V), lines, s);
+  if (!vec && n <= 256) {
+    by_accesses(cdiv(n, 32), [&](auto N) {
+      if constexpr (decltype(N)::value <= 8) e = backward_launch<T, 1, decltype(N)::value, 32>(p, 32, lines, s);
+    });
+    return e;
   }
+  if (!vec && n <= 256 * 12) {
+    by_accesses(cdiv(n, 256), [&](auto N) {
+      if constexpr (decltype(N)::value <= 12) e = backward_launch<T, 1, decltype(N)::value, 256>(p, 256, lines, s);
+    });
+    return e;
+  }
+  if (!vec && n <= 512 * 16) {
+    by_accesses(cdiv(n, 512), [&](auto N) {
+      if constexpr (decltype(N)::value >= 6) e = backward_launch<T, 1, decltype(N)::value, 512>(p, 512, lines, s);
+    });
+    return e;
+  }
+  if (p.part) {
+    *lines = (int)std::min<long long>(p.rows, LN_CTAS);
+    ln_slab_kernel<T><<<dim3(cdiv(p.dim, LN_SLAB_THREADS), *lines), LN_SLAB_THREADS, 0, s>>>(p);
+    count_launch();
+  }
+  ln_backward_loop_kernel<T><<<(unsigned)p.rows, LN_LOOP_THREADS, 0, s>>>(p);
   count_launch();
   return cudaGetLastError();
 }
