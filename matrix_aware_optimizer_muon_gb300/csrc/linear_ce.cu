@@ -40,22 +40,32 @@ bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 // ---------------------------------------------------------------------------
 
 // Rows of any stride and alignment to bf16 rows of ldo elements (a multiple of 8):
-// bf16 as it is, fp32 as `parts` bf16 numbers that add up to it (8 bits each).
+// bf16 as it is, fp32 as `parts` bf16 numbers that add up to it (8 bits each).  A warp a
+// row, a lane two neighbouring columns of each 64, PACK_HELD of them in flight.
+constexpr int PACK_HELD = 8;
 template <typename T>
 __global__ void __launch_bounds__(256) pack_kernel(const T* in, long long ld, long long rows, int dim, bf16* out,
                                                    long long ldo, int parts, long long part_stride) {
   const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (r >= rows) return;
   const T* x = in + r * ld;
-  for (int c = (threadIdx.x & 31) * 2; c < dim; c += 64) {
-    float a = ld1(x + c), b = c + 1 < dim ? ld1(x + c + 1) : 0.f;
-    bf16* o = out + r * ldo + c;
-    for (int q = 0; q < parts; ++q) {
-      const bf16 ha = __float2bfloat16_rn(a), hb = __float2bfloat16_rn(b);
-      *reinterpret_cast<uint32_t*>(o + q * part_stride) =
-          (uint32_t)__bfloat16_as_ushort(ha) | ((uint32_t)__bfloat16_as_ushort(hb) << 16);
-      a -= __bfloat162float(ha);
-      b -= __bfloat162float(hb);
+  for (int c0 = (threadIdx.x & 31) * 2; c0 < dim; c0 += 64 * PACK_HELD) {
+    float a[PACK_HELD], b[PACK_HELD];
+#pragma unroll
+    for (int i = 0; i < PACK_HELD; ++i) {
+      const int c = c0 + 64 * i;
+      a[i] = c < dim ? ld1(x + c) : 0.f;
+      b[i] = c + 1 < dim ? ld1(x + c + 1) : 0.f;
+    }
+    bf16* o = out + r * ldo + c0;
+    for (int q = 0; q < parts; ++q, o += part_stride) {
+#pragma unroll
+      for (int i = 0; i < PACK_HELD; ++i) {
+        const uint32_t w = pack_bf16x2(a[i], b[i]);
+        if (c0 + 64 * i < dim) *reinterpret_cast<uint32_t*>(o + 64 * i) = w;
+        a[i] -= __uint_as_float(w << 16);
+        b[i] -= __uint_as_float(w & 0xFFFF0000u);
+      }
     }
   }
 }
@@ -145,19 +155,21 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const float2* par
   }
 }
 
-// dH from the sums of each range of K.
+// dH from the sums of each range of K; a block a row.
 template <typename T>
 __global__ void __launch_bounds__(256) split_sum_kernel(const float* acc, int splits, long long rows, int dim,
                                                         long long ldacc, T* out, float scale, const float* upstream,
                                                         const float* stats) {
   await_previous();
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long r = i / dim;
-  if (r >= rows) return;
-  const int c = (int)(i - r * dim);
-  float s = 0.f;
-  for (int k = 0; k < splits; ++k) s += acc[((size_t)k * rows + r) * ldacc + c];
-  st1(out + i, s * shared_factor(scale, upstream, stats));
+  const long long r = blockIdx.x;
+  const float u = shared_factor(scale, upstream, stats);
+  for (int c = threadIdx.x; c < dim; c += 256) {
+    const float* a = acc + r * ldacc + c;
+    float s = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) s += a[(size_t)k * rows * ldacc];
+    st1(out + r * dim + c, s * u);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -306,9 +318,11 @@ void shape(Job* j, int64_t m, int64_t n, int64_t k) {
   j->tiles = j->mtiles * j->ntiles;
 }
 
-// Hands the launch's tiles out: each to the pair with the least work so far, jobs in
-// order of their tiles' lengths.  Launches with more tiles than the table holds go round
-// robin, where one tile more or less no longer matters.  Returns whether the table is used.
+// Hands the launch's tiles out so that the pairs' work evens out: jobs in order of their
+// tiles' lengths, the tiles of each filling the pairs up to a common level, round by round
+// (so that pairs work on neighbouring tiles at a time).  Launches with more tiles than the
+// table holds go round robin, where one tile more or less no longer matters.  Returns
+// whether the table is used.
 bool lay_out(OrderedParams* p, int npairs) {
   std::sort(p->job, p->job + p->njobs, [](const Job& x, const Job& y) { return x.nkb > y.nkb; });
   int t = 0;
@@ -317,37 +331,60 @@ bool lay_out(OrderedParams* p, int npairs) {
     t += p->job[j].tiles;
   }
   p->tiles = t;
-  if (p->njobs < 2 || t > MAX_ORDER || t <= npairs) return false;
-  // load[i]: work of pair i; a binary heap of pairs by (load, index)
-  long long load[MAX_PAIRS];
-  int heap[MAX_PAIRS];
-  unsigned char owner[MAX_ORDER];
-  int count[MAX_PAIRS] = {};
-  for (int i = 0; i < npairs; ++i) { load[i] = 0; heap[i] = i; }
-  auto less = [&](int x, int y) { return load[x] != load[y] ? load[x] < load[y] : x < y; };
-  t = 0;
+  // (and what the levels are counted in has to fit 31 bits)
+  long long work = 0;
+  for (int j = 0; j < p->njobs; ++j) work += (long long)p->job[j].tiles * (p->nterms * (long long)p->job[j].nkb + 2);
+  if (p->njobs < 2 || t > MAX_ORDER || t <= npairs || work >= (1LL << 30)) return false;
+  int load[MAX_PAIRS] = {}, by_load[MAX_PAIRS];
+  int count[MAX_JOBS][MAX_PAIRS];
+  int total[MAX_PAIRS] = {};
   for (int j = 0; j < p->njobs; ++j) {
-    const long long cost = (long long)p->job[j].nkb + 2;   // an accumulator's hand-over costs about two K steps
-    for (int i = 0; i < p->job[j].tiles; ++i, ++t) {
-      const int w = heap[0];
-      owner[t] = (unsigned char)w;
-      ++count[w];
-      load[w] += cost;
-      for (int at = 0;;) {
-        int c = 2 * at + 1;
-        if (c >= npairs) break;
-        if (c + 1 < npairs && less(heap[c + 1], heap[c])) ++c;
-        if (!less(heap[c], heap[at])) break;
-        std::swap(heap[c], heap[at]);
-        at = c;
-      }
+    // what a tile costs in K steps; an accumulator's hand-over is worth about two
+    const int cost = p->nterms * p->job[j].nkb + 2;
+    const int tiles = p->job[j].tiles;
+    // the highest level up to which whole tiles can fill the pairs ...
+    auto below = [&](int level) {
+      int n = 0;
+      for (int i = 0; i < npairs; ++i) n += level > load[i] ? (level - load[i]) / cost : 0;
+      return n;
+    };
+    int most = 0;
+    long long sum = (long long)cost * tiles;
+    for (int i = 0; i < npairs; ++i) { most = std::max(most, load[i]); sum += load[i]; }
+    int lo = *std::min_element(load, load + npairs), hi = std::max<int>(most, (int)(sum / npairs)) + cost + 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (below(mid) <= tiles) lo = mid; else hi = mid - 1;
     }
+    int left = tiles;
+    for (int i = 0; i < npairs; ++i) {
+      by_load[i] = i;
+      count[j][i] = lo > load[i] ? (lo - load[i]) / cost : 0;
+      load[i] += count[j][i] * cost;
+      left -= count[j][i];
+    }
+    // ... and the rest, less than one a pair, to those with the least work
+    std::sort(by_load, by_load + npairs, [&](int x, int y) { return load[x] != load[y] ? load[x] < load[y] : x < y; });
+    for (int i = 0; i < left; ++i) {
+      ++count[j][by_load[i]];
+      load[by_load[i]] += cost;
+    }
+    for (int i = 0; i < npairs; ++i) total[i] += count[j][i];
   }
-  p->start[0] = 0;
-  for (int i = 0; i < npairs; ++i) p->start[i + 1] = (unsigned short)(p->start[i] + count[i]);
   int fill[MAX_PAIRS];
-  for (int i = 0; i < npairs; ++i) fill[i] = p->start[i];
-  for (t = 0; t < p->tiles; ++t) p->order[fill[owner[t]]++] = (unsigned short)t;
+  p->start[0] = 0;
+  for (int i = 0; i < npairs; ++i) {
+    fill[i] = p->start[i];
+    p->start[i + 1] = (unsigned short)(p->start[i] + total[i]);
+  }
+  t = 0;
+  for (int j = 0; j < p->njobs; ++j)
+    for (const int end = t + p->job[j].tiles; t < end;)
+      for (int i = 0; i < npairs; ++i)
+        if (count[j][i] > 0) {
+          --count[j][i];
+          p->order[fill[i]++] = (unsigned short)t++;
+        }
   return true;
 }
 
@@ -505,7 +542,7 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
     if (launch(p, ordered, f32, s) != cudaSuccess) return MUON_ERR_CUDA;
   }
   if (dH && P.splits > 1) {
-    const dim3 blocks((unsigned)cdiv(a->rows * a->dim, 256));
+    const dim3 blocks((unsigned)a->rows);
     const cudaError_t e =
         f32 ? launch_after(split_sum_kernel<float>, blocks, dim3(256), 0, s, acc, P.splits, a->rows, a->dim, P.ldacc,
                            static_cast<float*>(dH), grad_scale, upstream, stats)
