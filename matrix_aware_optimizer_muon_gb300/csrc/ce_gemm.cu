@@ -50,23 +50,38 @@ constexpr int CHUNKS = 4;                      // 32-column chunks of an epilogu
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 256;
 
+// A job's numbers, copied to shared memory: every role reads them for every tile, and with
+// the tile table in the parameters the constant cache does not hold them.
+struct Work {
+  int kind, a_mn, b_mn, m, n, b_n0, b_k0, mtiles, ntiles, group, begin, splits, nkb, seg_kb, first, last, vec;
+  void* out;
+  float* acc;
+  long long ldo, ldacc, part_stride;
+};
+
 struct Tile {
   int job, tm, tn, split;
 };
 
-__device__ __forceinline__ Tile decode(const Params& p, int t) {
+__device__ __forceinline__ Tile decode(const Work* jobs, int njobs, int t) {
   Tile ti;
   int j = 0;
-  while (j + 1 < p.njobs && p.job[j + 1].begin <= t) ++j;
-  const Job& J = p.job[j];
+  while (j + 1 < njobs && jobs[j + 1].begin <= t) ++j;
+  const Work& J = jobs[j];
   ti.job = j;
   int r = t - J.begin;
-  const int per = J.mtiles * J.ntiles;
-  ti.split = r / per;
-  r -= ti.split * per;
-  const int g = r / (J.group * J.ntiles);
-  const int rows = min(J.group, J.mtiles - g * J.group);
-  r -= g * J.group * J.ntiles;
+  ti.split = 0;
+  if (J.splits > 1) {
+    const int per = J.mtiles * J.ntiles;
+    ti.split = r / per;
+    r -= ti.split * per;
+  }
+  int g = 0, rows = J.mtiles;
+  if (J.group < rows) {
+    g = r / (J.group * J.ntiles);
+    r -= g * J.group * J.ntiles;
+    rows = min(J.group, J.mtiles - g * J.group);
+  }
   ti.tn = r / rows;
   ti.tm = g * J.group + (r - ti.tn * rows);
   return ti;
@@ -82,7 +97,7 @@ __device__ __forceinline__ int tile_at(const Params& p, int pair, int npairs, in
   return t < p.tiles ? t : -1;
 }
 
-__device__ __forceinline__ int segments(const Job& J, int nterms) {
+__device__ __forceinline__ int segments(const Work& J, int nterms) {
   return nterms * ((J.nkb + J.seg_kb - 1) / J.seg_kb);
 }
 
@@ -149,7 +164,7 @@ __device__ __forceinline__ RowIn row_in(const Params& p, int r) {
   return x;
 }
 
-__device__ __forceinline__ void finish_grad(const Params& p, const Job& J, int r, int c0, float (&v)[32],
+__device__ __forceinline__ void finish_grad(const Params& p, const Work& J, int r, int c0, float (&v)[32],
                                             const RowIn& x) {
   if (r >= J.m || c0 >= J.n) return;
   const bool dead = x.lse == INFINITY && x.c == 0.f;
@@ -169,7 +184,7 @@ __device__ __forceinline__ void finish_grad(const Params& p, const Job& J, int r
   }
 }
 
-__device__ __forceinline__ void finish_sum(const Params& p, const Job& J, int split, int r, int c0, float u,
+__device__ __forceinline__ void finish_sum(const Params& p, const Work& J, int split, int r, int c0, float u,
                                            float (&v)[32]) {
   if (r >= J.m || c0 >= J.n) return;
   const int cols = J.n - c0;
@@ -202,7 +217,7 @@ __device__ __forceinline__ void finish_sum(const Params& p, const Job& J, int sp
 }
 
 // Max, sum of exponentials and the label's logit over this thread's 128 columns.
-__device__ __forceinline__ void finish_logits(const Params& p, const Job& J, const Tile& ti, int half, int r, int cbase,
+__device__ __forceinline__ void finish_logits(const Params& p, const Work& J, const Tile& ti, int half, int r, int cbase,
                                               const float (&acc)[CHUNKS][32]) {
   if (r >= J.m) return;
   const int cols = J.n - cbase;
@@ -247,6 +262,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
+  __shared__ Work jobs[MAX_JOBS];
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)ptx::cluster_ctarank();
   const bool even = rank == 0;
@@ -264,6 +281,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
     ptx::mbar_init(mdone, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
+  }
+  if (warp == 2 && lane < p.njobs) {
+    const Job& J = p.job[lane];
+    jobs[lane] = Work{J.kind, J.a_mn, J.b_mn, J.m, J.n, J.b_n0, J.b_k0, J.mtiles, J.ntiles, J.group, J.begin, J.splits,
+                      J.nkb, J.seg_kb, J.first, J.last, J.vec, J.out, J.acc, J.ldo, J.ldacc, J.part_stride};
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(tmem_slot, TMEM_COLS);
@@ -285,15 +307,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
       uint32_t phase = 0, pending = 0, pend_phase = 0;
       bool stop = false;
       for (int i = 0, t; !stop && (t = tile_at(p, pair, npairs, i)) >= 0; ++i) {
-        const Tile ti = decode(p, t);
-        const Job& J = p.job[ti.job];
-        const CUtensorMap* map = is_b ? &J.b : &J.a;
+        const Tile ti = decode(jobs, p.njobs, t);
+        const Work J = jobs[ti.job];
+        const CUtensorMap* map = is_b ? &p.job[ti.job].b : &p.job[ti.job].a;
         const bool mn = is_b ? J.b_mn : J.a_mn;
-        // boxes that lie wholly past the output's rows or columns are not fetched: what the
-        // MMAs make of stale data there is never read
+        // A box that lies wholly past the output's rows or columns is not fetched (what the
+        // MMAs make of stale data there is never read), but each CTA's first always is: a
+        // producer that fetched nothing would not hold the MMAs back, and could lose count
+        // of the phases of `empty`
         const int t0 = is_b ? ti.tn * TILE : ti.tm * TILE, left = (is_b ? J.n : J.m) - t0;
-        const int boxes = min(max((left - rank * HALF + BOX - 1) / BOX, 0), 2);
-        const uint32_t bytes = min((left + BOX - 1) / BOX, 4) * BOX_BYTES;   // of both CTAs
+        const int boxes = left > rank * HALF + BOX ? 2 : 1;
+        const uint32_t bytes = ((left > BOX ? 2 : 1) + (left > HALF + BOX ? 2 : 1)) * BOX_BYTES;   // of both CTAs
         const int r0 = t0 + rank * HALF + (is_b ? J.b_n0 : 0);
         const int k0 = ti.split * J.nkb * BK + (is_b ? J.b_k0 : 0);
         for (int term = 0; term < p.nterms && !stop; ++term) {
@@ -329,8 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
       int it = 0;   // accumulator uses
       bool stop = false;
       for (int i = 0, t; !stop && (t = tile_at(p, pair, npairs, i)) >= 0; ++i) {
-        const Tile ti = decode(p, t);
-        const Job& J = p.job[ti.job];
+        const Tile ti = decode(jobs, p.njobs, t);
+        const Work J = jobs[ti.job];
         const uint32_t idesc = ptx::idesc_bf16_f32(TILE, TILE, J.a_mn, J.b_mn);
         // K-major: 8-row groups 1024 B apart, a K step of 16 is 32 B.  MN-major: atoms of
         // 64 rows 8 KB apart, 8-K groups 1024 B apart, a K step of 16 is 2 KB.
@@ -376,8 +400,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
     int it = 0;
     bool stop = false;
     for (int i = 0, t; !stop && (t = tile_at(p, pair, npairs, i)) >= 0; ++i) {
-      const Tile ti = decode(p, t);
-      const Job& J = p.job[ti.job];
+      const Tile ti = decode(jobs, p.njobs, t);
+      const Work J = jobs[ti.job];
       const int r = ti.tm * TILE + rank * HALF + quarter * 32 + lane;
       const int cbase = ti.tn * TILE + half * HALF;
       RowIn x = {};

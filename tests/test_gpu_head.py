@@ -369,6 +369,44 @@ def test_linear_ce_upstream_factor(dt):
             within(num(q), num(p) / count, tol, "mean")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_linear_ce_back_to_back(dt):
+    """Hundreds of calls queued without a wait between them, with tiles that fill only part of
+    a CTA pair: no wait in a kernel expires, every call gives the first one's bits."""
+    mm.muon_debug_set(0, 200)
+    try:
+        for n, v, d in ((300, 10007, 130), (70, 1300, 300), (8, 9000, 257)):
+            h, h64, w, w64, labels, lab = ce_case(n, v, d, dt, 5)
+            ws = mm.alloc_linear_ce_workspace(n, v, d, TYPES[dt])
+            first = mm.muon_linear_ce_forward(h, w, labels, ws)
+            first += mm.muon_linear_ce_backward(h, w, labels, first[1], ws, stats=first[2])
+            for _ in range(150):
+                out = mm.muon_linear_ce_forward(h, w, labels, ws)
+                out += mm.muon_linear_ce_backward(h, w, labels, out[1], ws, stats=out[2])
+            assert mm.muon_check_status(ws) == mm.MUON_OK
+            assert all(torch.equal(p, q) for p, q in zip(first, out))
+    finally:
+        mm.muon_debug_set(0, 0)
+
+
+def test_linear_ce_expired_wait_is_reported():
+    """A producer that issues no loads (test flag): the waits run out, the call returns, the
+    status says so, and the next call is right again."""
+    n, v, d = 40, 600, 64
+    h, h64, w, w64, labels, lab = ce_case(n, v, d, "bf16", 6)
+    ws = mm.alloc_linear_ce_workspace(n, v, d)
+    want = mm.muon_linear_ce_forward(h, w, labels, ws)
+    mm.muon_debug_set(mm.MUON_DEBUG_STALL_PRODUCER, 50)
+    try:
+        mm.muon_linear_ce_forward(h, w, labels, ws)
+        assert mm.muon_check_status(ws) == mm.MUON_ERR_TIMEOUT
+    finally:
+        mm.muon_debug_set(0, 0)
+    got = mm.muon_linear_ce_forward(h, w, labels, ws)
+    assert mm.muon_check_status(ws) == mm.MUON_OK
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
 def test_linear_ce_in_a_cuda_graph():
     n, v, d = 130, 1000, 64
     h, h64, w, w64, labels, lab = ce_case(n, v, d, "bf16", 31)
