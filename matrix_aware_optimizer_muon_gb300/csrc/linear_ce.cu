@@ -211,11 +211,15 @@ int check_pointers(const muon_linear_ce* a) {
   return MUON_OK;
 }
 
+// A tile's time in K steps: its epilogue overlaps the next tile's MMAs, and alone takes as
+// long as some 12 steps (64 rows: 3.5 us a tile of dW, one K step long).
+int64_t tile_cost(int64_t steps) { return std::max<int64_t>(steps, 12) + 2; }
+
 // Ranges the K of a dH tile is cut into: a tile over a whole piece must not outlast half
 // of a CTA pair's share of the launch (the tiles are handed out longest first).
 int split_count(int64_t rows, int64_t dim, int64_t piece, int64_t npairs) {
   const int64_t kp = cdiv(piece, BK), mt = cdiv(rows, TILE), dt = cdiv(dim, TILE), vt = cdiv(piece, TILE);
-  const int64_t work = mt * dt * kp + vt * dt * cdiv(rows, BK) + mt * vt * cdiv(dim, BK);
+  const int64_t work = mt * dt * kp + vt * dt * tile_cost(cdiv(rows, BK)) + mt * vt * tile_cost(cdiv(dim, BK));
   const int64_t share = std::max<int64_t>(work / (2 * npairs), 8);
   return (int)std::min<int64_t>(std::max<int64_t>(1, cdiv(kp, share)), MAX_SPLITS);
 }
@@ -333,14 +337,13 @@ bool lay_out(OrderedParams* p, int npairs) {
   p->tiles = t;
   // (and what the levels are counted in has to fit 31 bits)
   long long work = 0;
-  for (int j = 0; j < p->njobs; ++j) work += (long long)p->job[j].tiles * (p->nterms * (long long)p->job[j].nkb + 2);
+  for (int j = 0; j < p->njobs; ++j) work += (long long)p->job[j].tiles * tile_cost(p->nterms * (int64_t)p->job[j].nkb);
   if (p->njobs < 2 || t > MAX_ORDER || t <= npairs || work >= (1LL << 30)) return false;
   int load[MAX_PAIRS] = {}, by_load[MAX_PAIRS];
   int count[MAX_JOBS][MAX_PAIRS];
   int total[MAX_PAIRS] = {};
   for (int j = 0; j < p->njobs; ++j) {
-    // what a tile costs in K steps; an accumulator's hand-over is worth about two
-    const int cost = p->nterms * p->job[j].nkb + 2;
+    const int cost = (int)tile_cost((int64_t)p->nterms * p->job[j].nkb);
     const int tiles = p->job[j].tiles;
     // the highest level up to which whole tiles can fill the pairs ...
     auto below = [&](int level) {
