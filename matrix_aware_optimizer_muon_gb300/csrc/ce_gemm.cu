@@ -20,7 +20,8 @@
 //
 // The tensor cores add to the fp32 accumulator with truncation; its bias grows with the
 // number of K steps (measured: 2.3e-7 of a sum of 256 bf16 products, 1e-6 of 1024,
-// 9e-6 of 8192).  The kPromote form takes the accumulator over into registers every
+// 9e-6 of 8192).  Taking it over while the MMAs run is slow, for they have the tensor
+// memory's ports most of the time.  The kPromote form takes the accumulator over into registers every
 // seg_kb K steps and adds there with rounding to nearest (a take-over costs about 3% of
 // 512 products' time).  It serves the logits of the
 // forward pass, whose loss is fp32, and every product of 32-bit operands; sums that
@@ -48,7 +49,8 @@ constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int CHUNKS = 4;                      // 32-column chunks of an epilogue warp
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 256;
+constexpr int XPOSE = 32 * 17;                  // floats an epilogue warp stages: 32 rows of 16 columns
+constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 256 + EPI_WARPS * XPOSE * 4;
 
 // A job's numbers, copied to shared memory: every role reads them for every tile, and with
 // the tile table in the parameters the constant cache does not hold them.
@@ -97,8 +99,16 @@ __device__ __forceinline__ int tile_at(const Params& p, int pair, int npairs, in
   return t < p.tiles ? t : -1;
 }
 
+// A tile's K steps run through its terms, the products of the operands' leading parts
+// last.  The accumulator is taken over after each segment: SMALL_SEG steps of the other
+// terms (2^-8 of the result at most, and their truncation with them), seg_kb of the last.
+constexpr int SMALL_SEG = 256;
+__device__ __forceinline__ int segment_at(const Work& J, int nterms, int kb) {
+  const int small = (nterms - 1) * J.nkb;
+  return kb < small ? min(SMALL_SEG, small - kb) : min(J.seg_kb, nterms * J.nkb - kb);
+}
 __device__ __forceinline__ int segments(const Work& J, int nterms) {
-  return nterms * ((J.nkb + J.seg_kb - 1) / J.seg_kb);
+  return ((nterms - 1) * J.nkb + SMALL_SEG - 1) / SMALL_SEG + (J.nkb + J.seg_kb - 1) / J.seg_kb;
 }
 
 // Bounded wait: on expiry the status word and the CTA's abort flag are set and every
@@ -146,6 +156,29 @@ __device__ __forceinline__ void store_row(T* dst, const float (&v)[32], int cols
   }
 }
 
+// The same for rows that start on no vector boundary: 32 rows (row0 the first, m the
+// matrix's) by way of shared memory, so that a store covers 16 neighbouring columns of two
+// rows instead of one element of 32 (a sector each).  Called by whole warps.
+template <typename T>
+__device__ __forceinline__ void store_staged(T* out, long long ldo, int row0, int m, int c0, int cols,
+                                             const float (&v)[32], float* stage, int lane) {
+  const int cc = lane & 15, rr = lane >> 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = v[16 * h + j];
+    __syncwarp();
+    if (16 * h + cc < cols) {
+      T* o = out + (size_t)(row0 + rr) * ldo + c0 + 16 * h + cc;
+      const float* x = stage + rr * 17 + cc;
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i, o += 2 * ldo)
+        if (row0 + rr + 2 * i < m) st1(o, x[2 * i * 17]);
+    }
+  }
+}
+
 // Row constants of a GRAD tile: c (0 for a row without gradient), lse and the label's
 // column inside the piece.
 struct RowIn {
@@ -185,35 +218,42 @@ __device__ __forceinline__ void finish_grad(const Params& p, const Work& J, int 
 }
 
 __device__ __forceinline__ void finish_sum(const Params& p, const Work& J, int split, int r, int c0, float u,
-                                           float (&v)[32]) {
-  if (r >= J.m || c0 >= J.n) return;
+                                           float* stage, int lane, float (&v)[32]) {
+  if (c0 >= J.n) return;
   const int cols = J.n - c0;
   if (J.kind == DH && J.acc) {
-    float* a = J.acc + ((size_t)split * J.m + r) * J.ldacc + c0;
-    if (!J.first) {
-      if (cols >= 32) {
+    const bool more = !J.last || !J.out;
+    if (r < J.m) {
+      float* a = J.acc + ((size_t)split * J.m + r) * J.ldacc + c0;
+      if (!J.first) {
+        if (cols >= 32) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t w[8];
-          ld_v8(a + 8 * q, w);
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[8];
+            ld_v8(a + 8 * q, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[8 * q + j] += __uint_as_float(w[j]);
+            for (int j = 0; j < 8; ++j) v[8 * q + j] += __uint_as_float(w[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j < cols) v[j] += a[j];
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < cols) v[j] += a[j];
       }
+      if (more) store_row(a, v, cols, 2);
     }
-    if (!J.last || !J.out) {
-      store_row(a, v, cols, 2);
-      return;
-    }
+    if (more) return;
   }
 #pragma unroll
   for (int j = 0; j < 32; ++j) v[j] *= u;
-  if (p.f32_out) store_row(static_cast<float*>(J.out) + (size_t)r * J.ldo + c0, v, cols, J.vec);
-  else store_row(static_cast<bf16*>(J.out) + (size_t)r * J.ldo + c0, v, cols, J.vec);
+  if (J.vec) {
+    if (r >= J.m) return;
+    if (p.f32_out) store_row(static_cast<float*>(J.out) + (size_t)r * J.ldo + c0, v, cols, J.vec);
+    else store_row(static_cast<bf16*>(J.out) + (size_t)r * J.ldo + c0, v, cols, J.vec);
+  } else {
+    if (p.f32_out) store_staged(static_cast<float*>(J.out), J.ldo, r - lane, J.m, c0, cols, v, stage, lane);
+    else store_staged(static_cast<bf16*>(J.out), J.ldo, r - lane, J.m, c0, cols, v, stage, lane);
+  }
 }
 
 // Max, sum of exponentials and the label's logit over this thread's 128 columns.
@@ -361,9 +401,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
         const uint32_t a_lbo = J.a_mn ? OP_BYTES / 2 : 16, a_step = J.a_mn ? 2048 : 32;
         const uint32_t b_lbo = J.b_mn ? OP_BYTES / 2 : 16, b_step = J.b_mn ? 2048 : 32;
         const int total = p.nterms * J.nkb;
-        int in_term = 0;
         for (int kb = 0; kb < total && !stop;) {
-          const int run = min(J.seg_kb, J.nkb - in_term);
+          const int run = segment_at(J, p.nterms, kb);
           const int acc = it & 1;
           if (!wait_for(&tempty[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, p, true)) { stop = true; break; }
           ptx::tc_fence_after();
@@ -384,8 +423,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
           ptx::mma_commit_pair_mc(&tfull[acc], 3);
           ++it;
           kb += run;
-          in_term += run;
-          if (in_term == J.nkb) in_term = 0;
         }
       }
       // all issued MMAs complete before either CTA releases its tensor memory
@@ -397,11 +434,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const float u = shared_factor(p.scale, p.upstream, p.stats);
+    float* stage = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES + 256) + (warp - 4) * XPOSE;
     int it = 0;
     bool stop = false;
     for (int i = 0, t; !stop && (t = tile_at(p, pair, npairs, i)) >= 0; ++i) {
       const Tile ti = decode(jobs, p.njobs, t);
-      const Work J = jobs[ti.job];
+      const Work& J = jobs[ti.job];
       const int r = ti.tm * TILE + rank * HALF + quarter * 32 + lane;
       const int cbase = ti.tn * TILE + half * HALF;
       RowIn x = {};
@@ -424,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
             float v[32];
             ptx::tmem_ld_32x32b_x32(tb + k * 32, v);
             if (J.kind == GRAD) finish_grad(p, J, r, cbase + k * 32, v, x);
-            else finish_sum(p, J, ti.split, r, cbase + k * 32, u, v);
+            else finish_sum(p, J, ti.split, r, cbase + k * 32, u, stage, lane, v);
           }
         }
         ptx::tc_fence_before();
@@ -441,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
 #pragma unroll
           for (int k = 0; k < CHUNKS; ++k) {
             if (J.kind == GRAD) finish_grad(p, J, r, cbase + k * 32, acc[k], x);
-            else finish_sum(p, J, ti.split, r, cbase + k * 32, u, acc[k]);
+            else finish_sum(p, J, ti.split, r, cbase + k * 32, u, stage, lane, acc[k]);
           }
         }
       }

@@ -27,8 +27,11 @@ constexpr int TICKET_WORD = 16;    // of the header
 constexpr int64_t G_BYTES = 512 << 20;
 constexpr int64_t MIN_PIECE = 2048;
 constexpr int MAX_SPLITS = 16;
-// K steps (of 64) between take-overs of the tensor cores' sums into registers.
-constexpr int SEG_BF16 = 20, SEG_F32 = 8;
+// K steps (of 64) between take-overs of the tensor cores' sums into registers (for 32-bit
+// operands, of the leading parts' products).  Error against 64 bits and time: bf16 forward
+// 8192 x 2560 x 131072, 8 steps 2.5e-7 and 3.46 ms, 20 steps 3.9e-7 and 3.19, none 1e-6 and
+// 3.19; 32-bit backward 1021 x 1001 x 10007, 4 steps 4.3e-7 and 362 us, 8 steps 7.9e-7 and 350.
+constexpr int SEG_BF16 = 20, SEG_F32 = 4;
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
