@@ -90,7 +90,7 @@ __device__ __forceinline__ uint32_t encode_v(float v, uint32_t base, uint32_t r)
 //              which byte permutes collect;
 // zero codes, numbers below a block's least, NaN and Inf are found by a test per thread and
 // sent through the plain functions above.
-constexpr int A8_THREADS = 256;
+constexpr int A8_THREADS = 128;
 constexpr int A8_EACH = 16;
 constexpr int A8_WORDS = A8_EACH / 4;      // of a moment's codes
 constexpr int A8_CHUNK = A8_THREADS * A8_EACH;
@@ -242,9 +242,12 @@ __device__ __noinline__ CodesN encode_any(const MomentsN x, uint32_t bm, uint32_
   return c;
 }
 
-// CTAs an SM should hold.  Measured on 335 M bf16 elements (step and unpacking together):
-// four 879 us, three 967, two 1134; 8 elements a thread and six CTAs 900.
-constexpr int a8_ctas(int bytes) { return bytes == 4 ? 4 : 3; }
+// CTAs an SM should hold, and so registers a thread.  Each CTA takes one chunk and leaves:
+// its loads overlap the others' arithmetic.  Measured on 335 M bf16 elements (step and
+// unpacking together): 32 warps an SM 883 us, 24 967, 16 1134; in CTAs of 128 threads
+// instead of 256 868; loops over 2, 4 or 8 chunks 1035, 979, 945; a persistent kernel with
+// the next chunk's data on their way to shared memory a fifth slower than that.
+constexpr int a8_ctas(int bytes) { return bytes == 4 ? 8 : 6; }
 template <typename PT, typename GT>
 __global__ void __launch_bounds__(A8_THREADS, a8_ctas(sizeof(PT) + sizeof(GT)))
     adamw8_kernel(const __grid_constant__ Adamw8Params q) {
