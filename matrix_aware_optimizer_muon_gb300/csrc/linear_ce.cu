@@ -23,7 +23,9 @@ constexpr size_t HEADER = 256;     // status word, join ticket
 constexpr int TICKET_WORD = 16;    // of the header
 
 // A piece's g is rows x piece bf16 (three times that for 32-bit operands), twice: one
-// piece is multiplied while the next is computed.
+// piece is multiplied while the next is computed.  Every piece costs a launch and a pass
+// over dH's sums.  8192 x 2560 x 131072 backward: 48 MB 11.1 ms, 96 10.6, 192 10.5, 384
+// 10.3, 1024 10.2.
 constexpr int64_t G_BYTES = 512 << 20;
 constexpr int64_t MIN_PIECE = 2048;
 constexpr int MAX_SPLITS = 16;
@@ -311,15 +313,19 @@ void common_params(Params* p, const muon_linear_ce* a, const CePlan& P, char* ws
   p->debug_flags = test_flags();
 }
 
-// Row tiles that are walked together for each column tile: their rows of A stay in L2.
-constexpr int GROUP = 32;
+// Row tiles that are walked together for each column tile, so that their rows of A stay in
+// L2: the forward pass keeps all of 8192 rows there; the products with g, whose operands are
+// larger, and g itself beside them do better with fewer.  8192 x 2560 x 131072 in a loop:
+// forward 8 row tiles 3.46 ms, 16 3.39, 32 3.35; backward, g and its products, 32 and 32
+// 10.56 ms, 16 and 16 10.28, 32 and 12 10.37, 32 and 8 10.30, 16 and 8 10.25.
+constexpr int GROUP_FORWARD = 32, GROUP_GRAD = 16, GROUP_G = 8;
 
-void shape(Job* j, int64_t m, int64_t n, int64_t k) {
+void shape(Job* j, int64_t m, int64_t n, int64_t k, int group) {
   j->m = (int)m;
   j->n = (int)n;
   j->mtiles = (int)cdiv(m, TILE);
   j->ntiles = (int)cdiv(n, TILE);
-  j->group = std::min(GROUP, j->mtiles);
+  j->group = std::min(group, j->mtiles);
   j->splits = 1;
   j->nkb = (int)cdiv(k, BK);
   j->tiles = j->mtiles * j->ntiles;
@@ -441,7 +447,7 @@ extern "C" int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, floa
   Job& j = p.job[0];
   j.kind = LOGITS;
   if (!map_of(&j.a, H) || !map_of(&j.b, W)) return MUON_ERR_CUDA;
-  shape(&j, a->rows, a->vocab, a->dim);
+  shape(&j, a->rows, a->vocab, a->dim, GROUP_FORWARD);
   j.seg_kb = P.nterms > 1 ? SEG_F32 : SEG_BF16;
   p.njobs = 1;
   p.tiles = j.tiles;
@@ -505,7 +511,7 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
         j.b = wmap;
         j.b_mn = 1;
         j.b_k0 = (int)v0;
-        shape(&j, a->rows, a->dim, c);
+        shape(&j, a->rows, a->dim, c, GROUP_G);
         j.splits = P.splits;
         j.nkb = (int)cdiv(j.nkb, P.splits);
         j.tiles *= P.splits;
@@ -524,7 +530,7 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
         if (!map_of(&j.a, G)) return MUON_ERR_CUDA;
         j.b = hmap;
         j.a_mn = j.b_mn = 1;
-        shape(&j, c, a->dim, a->rows);
+        shape(&j, c, a->dim, a->rows, GROUP_G);
         j.out = static_cast<char*>(dW) + (size_t)v0 * a->dim * es;
         j.ldo = a->dim;
         j.vec = result_vec(j.out, a->dim, a->dtype);
@@ -538,7 +544,7 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
       j.b = wmap;
       p.v0 = i * P.piece;
       j.b_n0 = (int)p.v0;
-      shape(&j, a->rows, std::min<int64_t>(P.piece, a->vocab - p.v0), a->dim);
+      shape(&j, a->rows, std::min<int64_t>(P.piece, a->vocab - p.v0), a->dim, GROUP_GRAD);
       j.out = w + P.g[i & 1];
       j.ldo = P.piece;
       j.part_stride = (long long)P.g_part;
