@@ -298,8 +298,10 @@ typedef struct muon_linear_ce {
 
 /* Bytes of workspace for muon_linear_ce_forward (backward == 0) or for both passes
  * (backward != 0) of these sizes, strides, dtype and pointers (NULL pointers count as
- * aligned).  H or W whose rows do not start on 16-byte boundaries need room for an
- * aligned copy.  (size_t)-1 for invalid sizes. */
+ * aligned).  It holds room for a copy of H, for one of W where W's rows do not start on
+ * 16-byte boundaries (both three bf16 parts long for 32-bit operands), and for the
+ * backward pass two pieces of g (at most 512 MB each, but 2048 columns of the vocabulary
+ * at least) and fp32 sums of dH.  (size_t)-1 for invalid sizes. */
 size_t muon_linear_ce_workspace_size(const muon_linear_ce* a, int backward);
 
 /* loss[r] = lse[r] - z[r, label_r] with lse[r] = log(sum_v exp(z[r, v])); loss is 0 for

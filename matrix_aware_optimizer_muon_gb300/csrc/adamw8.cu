@@ -6,6 +6,10 @@
 // update itself is adamw.cu's:
 //   m <- b1*m + (1-b1)*g;  v <- b2*v + (1-b2)*g^2;
 //   p <- p - lr*( (m/(1-b1^t)) / (sqrt(v/(1-b2^t)) + eps) + wd*p ).
+//
+// Measured: 335.5 M bf16 parameters and gradients, step 575 us (5.9 TB/s, 86% of a copy's
+// rate; three quarters of the issue slots) and unpacking 289 us (7.0 TB/s); 38.6 M fp32
+// parameters with bf16 gradients 88 us (6.2 TB/s) and 37 us.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -246,7 +250,7 @@ __device__ __noinline__ CodesN encode_any(const MomentsN x, uint32_t bm, uint32_
 // its loads overlap the others' arithmetic.  Measured on 335 M bf16 elements (step and
 // unpacking together): 32 warps an SM 883 us, 24 967, 16 1134; in CTAs of 128 threads
 // instead of 256 868; loops over 2, 4 or 8 chunks 1035, 979, 945; a persistent kernel with
-// the next chunk's data on their way to shared memory a fifth slower than that.
+// the next chunk's data on their way to shared memory a fifth slower than one chunk a CTA.
 constexpr int a8_ctas(int bytes) { return bytes == 4 ? 8 : 6; }
 template <typename PT, typename GT>
 __global__ void __launch_bounds__(A8_THREADS, a8_ctas(sizeof(PT) + sizeof(GT)))

@@ -623,7 +623,8 @@ int muon_init(void) {
   int rc = device_info(&di);
   if (rc != MUON_OK) return rc;
   if (!aux_stream()) return MUON_ERR_CUDA;
-  if (prepare_ns_tc() != cudaSuccess || prepare_tall() != cudaSuccess) return MUON_ERR_CUDA;
+  if (prepare_ns_tc() != cudaSuccess || prepare_tall() != cudaSuccess || ce::prepare() != cudaSuccess)
+    return MUON_ERR_CUDA;
   return MUON_OK;
 }
 

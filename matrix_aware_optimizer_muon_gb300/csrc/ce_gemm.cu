@@ -22,13 +22,22 @@
 // number of K steps (measured: 2.3e-7 of a sum of 256 bf16 products, 1e-6 of 1024,
 // 9e-6 of 8192).  Taking it over while the MMAs run is slow, for they have the tensor
 // memory's ports most of the time.  The kPromote form takes the accumulator over into registers every
-// seg_kb K steps and adds there with rounding to nearest (a take-over costs about 3% of
-// 512 products' time).  It serves the logits of the
-// forward pass, whose loss is fp32, and every product of 32-bit operands; sums that
-// are rounded to bf16 (2e-3) do without.
+// seg_kb K steps and adds there with rounding to nearest (five take-overs of a tile of
+// 2560 products instead of two cost 8%).  It serves the logits of the forward pass, whose
+// loss is fp32, and every product of 32-bit operands; sums that are rounded to bf16 (2e-3)
+// do without.
 //
 // 32-bit operands come as three bf16 parts (24 bits of mantissa); the six products of
 // parts down to 2^-16 of the leading one are summed, smallest first.
+//
+// Measured (8192 rows, 2560 wide, 131072 entries, bf16, in loops of 0.1 to 0.3 s): forward
+// 3.16 to 3.34 ms (1.65 to 1.74 PFLOP/s), backward 9.9 to 11.1 ms (1.49 to 1.66); the
+// library's product of the same operands alone takes 2.65 to 2.93 ms.  The tensor pipe is
+// busy 78% (forward), 79% (g) and 89% (the products with g) of the time in single launches,
+// at 1.65 to 1.8 GHz; in loops the 1.4 kW power cap sets the clock.  Without its
+// exponentials the forward pass takes 4% less; waits that suspend the thread for longer, and
+// sharing an operand among clusters of four CTAs, change nothing.
+// 8 rows read the vocabulary matrix at 5.9 TB/s after some 11 us of launches and set-up.
 #include <map>
 #include <mutex>
 

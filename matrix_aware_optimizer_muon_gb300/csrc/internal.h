@@ -384,6 +384,9 @@ int tall_ctrl_words(int nchunks);
 cudaError_t prepare_ns_tc();
 int ns_tc_pairs();          // co-resident 2-CTA clusters of the pair kernel on the current device
 cudaError_t prepare_tall();
+namespace ce {
+cudaError_t prepare();
+}
 int cols_cluster_size();
 int cols_strip_width(int max_rows, int stage_elem_bytes);
 cudaError_t launch_fro_final(const FroFinalParams& p, cudaStream_t s);

@@ -3,7 +3,12 @@
 //   y  = (x - mean) rstd w + b,          rstd = 1/sqrt(var + eps)
 //   dx = rstd (g - sum(g)/D - xh sum(g xh)/D),   g = dy w,  xh = (x - mean) rstd
 //   dw = sum_rows dy xh,   db = sum_rows dy
-// Every sum is fp32.
+// Every sum is fp32.  Measured, of HBM's 6.79 TB/s (a copy): 32768 x 1536 bf16 forward
+// 36.7 us (5.5 TB/s), backward with both column sums 61.5 us (4.9 TB/s; 55 of them the rows'
+// kernel, 4 the column sums'); 5003 x 1537 fp32 rows of no alignment backward 25.7 us
+// (3.6 TB/s).  What is left: the forward pass and the rows' kernel wait for memory at half
+// of the issue slots; fp32 arithmetic in single instead of paired instructions takes the
+// same time.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -270,7 +275,7 @@ struct LnBwd {
 // the end the groups' sums are joined in shared memory in a fixed order and the CTA writes
 // one line.  Rows come through a ring of asynchronous copies in shared memory that each
 // thread keeps for itself (it reads only what it copied: no barrier), because the registers
-// are taken: 6 KB a row of 1536 bf16 pairs, LN_RING - 1 rows ahead.  Rows that need
+// are taken: 6 KB a row of 1536 bf16 pairs, ln_ring() - 1 rows ahead.  Rows that need
 // element-wise access are fetched one row ahead into registers.
 constexpr int LN_GROUPS = 8;
 __host__ __device__ constexpr int ln_ring(int n) { return n <= 2 ? 4 : 3; }

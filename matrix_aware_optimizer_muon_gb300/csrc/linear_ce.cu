@@ -31,8 +31,9 @@ constexpr int64_t MIN_PIECE = 2048;
 constexpr int MAX_SPLITS = 16;
 // K steps (of 64) between take-overs of the tensor cores' sums into registers (for 32-bit
 // operands, of the leading parts' products).  Error against 64 bits and time: bf16 forward
-// 8192 x 2560 x 131072, 8 steps 2.5e-7 and 3.46 ms, 20 steps 3.9e-7 and 3.19, none 1e-6 and
-// 3.19; 32-bit backward 1021 x 1001 x 10007, 4 steps 4.3e-7 and 362 us, 8 steps 7.9e-7 and 350.
+// 2560 wide, 8 steps 2.1e-7 of lse, 20 steps 5.1e-7, one take-over at the end 1.0e-6, and for
+// 8192 x 131072 3.44, 3.20 and 3.17 ms; 32-bit 1021 x 1001 x 10007 backward, 4 steps 3.9e-7
+// of dH and 314 us, 8 steps 6.9e-7 and 304, 16 steps 1.3e-6 and 302.
 constexpr int SEG_BF16 = 20, SEG_F32 = 4;
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* in, long long ld, lo
   }
 }
 
-// One warp a row: joins its partial sums (up to 32 a lane in one pass), writes lse and
+// One warp a row: joins its partial sums (JOIN_HELD a lane at a time), writes lse and
 // loss.  Each block adds its rows' losses up; the last block to finish adds the blocks'.
 constexpr int JOIN_WARPS = 8;
 constexpr int JOIN_HELD = 8;   // partial sums a lane keeps at a time
