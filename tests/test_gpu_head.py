@@ -523,6 +523,33 @@ def test_adamw8_many_tensors_resume_and_repeat():
     assert all(torch.equal(x, y) for x, y in zip(pa, P)) and torch.equal(a.m, opt.m) and torch.equal(a.v, opt.v)
 
 
+def test_adamw8_parameters_cast_or_moved_after_construction():
+    """A parameter whose data was replaced is taken as it is now, or refused, with the state
+    and the parameters unchanged."""
+    p, q = torch.zeros(300, device=dev()), torch.zeros(40, device=dev())
+    g = [torch.full((300,), 1e-3, device=dev()), torch.full((40,), 1e-3, device=dev())]
+    opt = mm.AdamW8([p, q], lr=1e-3)
+    opt.step(g)
+    guard = torch.full((900,), 7.0, dtype=torch.bfloat16, device=dev())
+    p.data = guard[300:600]                      # narrower than what the optimizer was made with
+    with pytest.raises(ValueError):              # two dtypes
+        opt.step(g)
+    q.data = q.data.bfloat16()
+    opt.step(g)
+    assert opt.step_count == 2
+    # a step of 1e-3 is below half of bf16's spacing at 7, so p's values show nothing; q's do
+    assert bool((guard == 7).all()) and bool((q < -1.5e-3).all()) and bool((q > -2.5e-3).all())
+    for bad in (p.data[:299], p.data.cpu(), torch.zeros(600, dtype=torch.bfloat16, device=dev())[::2]):
+        p.data = bad
+        with pytest.raises(ValueError):
+            opt.step(g)
+    p.data = guard[300:600]
+    for bad in ([g[0]], [g[0], g[1][:39]], [g[0].cpu(), g[1]], [g[0], g[1].bfloat16()]):
+        with pytest.raises(ValueError):
+            opt.step(bad)
+    assert opt.step_count == 2
+
+
 def test_adamw8_nonfinite_and_extreme_gradients():
     k = 300
     p = torch.zeros(k, device=dev())
