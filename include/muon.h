@@ -317,7 +317,8 @@ int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, float* lse, flo
 /* Gradient of u * sum_r c_r*loss[r]:  g[r, v] = c_r*(exp(z[r, v] - lse[r]) - [v == label_r]),
  *   dH = u g W  (rows x dim, leading dimension dim),  dW = u g^T H  (vocab x dim, likewise),
  * both of a->dtype and overwritten; either may be NULL.  c_r = row_grad ? row_grad[r] : 1,
- * and 0 for an ignored row and for one whose label is out of range.
+ * and 0 for an ignored row and for one whose label is out of range, whatever such a row
+ * of H, lse and row_grad holds (NaN and infinities included).
  * u = grad_scale * (upstream ? upstream[0] : 1) * (stats ? 1/max(stats[1], 1) : 1): with the
  * forward pass's stats this is the gradient of grad_scale * upstream * the mean loss.
  * row_grad, upstream and stats are device fp32.  The logits are computed again, by pieces

@@ -48,20 +48,36 @@ bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 // Rows of any stride and alignment to bf16 rows of ldo elements (a multiple of 8):
 // bf16 as it is, fp32 as `parts` bf16 numbers that add up to it (8 bits each).  A warp a
 // row, a lane two neighbouring columns of each 64, PACK_HELD of them in flight.
+//
+// Rows whose label carries no gradient become zeros: dW sums g^T H over all rows, and a
+// zero of g times a NaN or an infinity that such a row may hold (padding) would be NaN.
+struct RowMask {
+  const int64_t* labels;   // null: every row as it is
+  long long vocab, ignore;
+};
+__device__ __forceinline__ bool masked(const RowMask& k, long long r) {
+  if (!k.labels) return false;
+  const long long lab = k.labels[r];
+  return lab == k.ignore || lab < 0 || lab >= k.vocab;
+}
+
 constexpr int PACK_HELD = 8;
 template <typename T>
 __global__ void __launch_bounds__(256) pack_kernel(const T* in, long long ld, long long rows, int dim, bf16* out,
-                                                   long long ldo, int parts, long long part_stride) {
+                                                   long long ldo, int parts, long long part_stride, RowMask mask) {
+  allow_next();
+  await_previous();
   const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (r >= rows) return;
+  const bool zero = masked(mask, r);
   const T* x = in + r * ld;
   for (int c0 = (threadIdx.x & 31) * 2; c0 < dim; c0 += 64 * PACK_HELD) {
     float a[PACK_HELD], b[PACK_HELD];
 #pragma unroll
     for (int i = 0; i < PACK_HELD; ++i) {
       const int c = c0 + 64 * i;
-      a[i] = c < dim ? ld1(x + c) : 0.f;
-      b[i] = c + 1 < dim ? ld1(x + c + 1) : 0.f;
+      a[i] = c < dim && !zero ? ld1(x + c) : 0.f;
+      b[i] = c + 1 < dim && !zero ? ld1(x + c + 1) : 0.f;
     }
     bf16* o = out + r * ldo + c0;
     for (int q = 0; q < parts; ++q, o += part_stride) {
@@ -73,6 +89,27 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* in, long long ld, lo
         b[i] -= __uint_as_float(w & 0xFFFF0000u);
       }
     }
+  }
+}
+
+// The same for bf16 rows that are whole 16-byte vectors, ldo = dim.
+__global__ void __launch_bounds__(256) mask_kernel(const bf16* in, long long ld, long long rows, int dim, bf16* out,
+                                                   RowMask mask) {
+  allow_next();
+  await_previous();
+  const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  const bool zero = masked(mask, r);
+  const uint4* x = reinterpret_cast<const uint4*>(in + r * ld);
+  uint4* o = reinterpret_cast<uint4*>(out + r * dim);
+  for (int c0 = threadIdx.x & 31; c0 < dim / 8; c0 += 32 * PACK_HELD) {
+    uint4 v[PACK_HELD];
+#pragma unroll
+    for (int i = 0; i < PACK_HELD; ++i)
+      v[i] = c0 + 32 * i < dim / 8 && !zero ? x[c0 + 32 * i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < PACK_HELD; ++i)
+      if (c0 + 32 * i < dim / 8) o[c0 + 32 * i] = v[i];
   }
 }
 
@@ -239,7 +276,8 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P) {
   P->pack_w = f32 || a->ldw % 8 || !is_aligned(a->W, 16);
   size_t at = HEADER;
   auto take = [&](size_t bytes) { const size_t p = at; at += up(bytes); return p; };
-  // room for H's copy in any case, so that a workspace fits whatever H's alignment
+  // room for H's copy in any case: for the backward pass, and so that a workspace fits
+  // whatever H's alignment
   P->hp = take((size_t)P->parts * a->rows * P->dp * 2);
   P->wp = P->pack_w ? take((size_t)P->parts * a->vocab * P->dp * 2) : at;
   const size_t common = at;
@@ -278,21 +316,33 @@ bool map_of(CUtensorMap* m, const Operand& o) {
 }
 
 template <typename T>
-void pack(const void* in, int64_t ld, int64_t rows, int64_t dim, bf16* out, int64_t ldo, int parts, cudaStream_t s) {
-  pack_kernel<T><<<(unsigned)cdiv(rows, 8), 256, 0, s>>>(static_cast<const T*>(in), ld, rows, (int)dim, out, ldo, parts,
-                                                         rows * ldo);
+cudaError_t pack(const void* in, int64_t ld, int64_t rows, int64_t dim, bf16* out, int64_t ldo, int parts,
+                 const RowMask& mask, cudaStream_t s) {
   count_launch();
+  return launch_after(pack_kernel<T>, dim3((unsigned)cdiv(rows, 8)), dim3(256), 0, s, static_cast<const T*>(in),
+                      (long long)ld, (long long)rows, (int)dim, out, (long long)ldo, parts, (long long)(rows * ldo), mask);
 }
 
-Operand operand(const muon_linear_ce* a, const CePlan& P, bool h, char* ws, cudaStream_t s) {
+// H or W as the products read it: where it lies, or a copy of it.  mask: the rows of H that
+// carry a gradient are wanted, and zeros for the others.
+cudaError_t operand(Operand* o, const muon_linear_ce* a, const CePlan& P, bool h, bool mask, char* ws, cudaStream_t s) {
   const void* src = h ? a->H : a->W;
   const int64_t rows = h ? a->rows : a->vocab, ld = h ? a->ldh : a->ldw;
-  if (!(h ? P.pack_h : P.pack_w))
-    return Operand{static_cast<const bf16*>(src), rows, a->dim, ld, rows * ld, 1};
+  const bool copy = h ? P.pack_h : P.pack_w;
+  if (!copy && !mask) {
+    *o = Operand{static_cast<const bf16*>(src), rows, a->dim, ld, rows * ld, 1};
+    return cudaSuccess;
+  }
   bf16* dst = reinterpret_cast<bf16*>(ws + (h ? P.hp : P.wp));
-  if (a->dtype == MUON_DTYPE_BF16) pack<bf16>(src, ld, rows, a->dim, dst, P.dp, 1, s);
-  else pack<float>(src, ld, rows, a->dim, dst, P.dp, 3, s);
-  return Operand{dst, rows, a->dim, P.dp, rows * P.dp, P.parts};
+  *o = Operand{dst, rows, a->dim, P.dp, rows * P.dp, P.parts};
+  const RowMask k = {mask ? a->labels : nullptr, a->vocab, a->ignore_index};
+  if (!copy && a->dim % 8 == 0) {
+    count_launch();
+    return launch_after(mask_kernel, dim3((unsigned)cdiv(rows, 8)), dim3(256), 0, s, static_cast<const bf16*>(src),
+                        (long long)ld, (long long)rows, (int)a->dim, dst, k);
+  }
+  return a->dtype == MUON_DTYPE_BF16 ? pack<bf16>(src, ld, rows, a->dim, dst, P.dp, 1, k, s)
+                                     : pack<float>(src, ld, rows, a->dim, dst, P.dp, 3, k, s);
 }
 
 void common_params(Params* p, const muon_linear_ce* a, const CePlan& P, char* ws) {
@@ -444,7 +494,9 @@ extern "C" int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, floa
   common_params(&p, a, P, w);
   p.part = reinterpret_cast<float2*>(w + P.part);
   p.zlabel = reinterpret_cast<float*>(w + P.zlabel);
-  const Operand H = operand(a, P, true, w, s), W = operand(a, P, false, w, s);
+  Operand H, W;
+  if (operand(&H, a, P, true, false, w, s) != cudaSuccess || operand(&W, a, P, false, false, w, s) != cudaSuccess)
+    return MUON_ERR_CUDA;
   Job& j = p.job[0];
   j.kind = LOGITS;
   if (!map_of(&j.a, H) || !map_of(&j.b, W)) return MUON_ERR_CUDA;
@@ -488,7 +540,9 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
   if (prepare() != cudaSuccess) return MUON_ERR_CUDA;
   char* w = static_cast<char*>(ws);
   static thread_local OrderedParams p;
-  const Operand H = operand(a, P, true, w, s), W = operand(a, P, false, w, s);
+  Operand H, W;
+  if (operand(&H, a, P, true, dW != nullptr, w, s) != cudaSuccess || operand(&W, a, P, false, false, w, s) != cudaSuccess)
+    return MUON_ERR_CUDA;
   CUtensorMap hmap, wmap;
   if (!map_of(&hmap, H) || !map_of(&wmap, W)) return MUON_ERR_CUDA;
   const bool f32 = a->dtype == MUON_DTYPE_F32;

@@ -298,6 +298,32 @@ def test_linear_ce_labels():
     assert not loss[zero == 0].any() and stats[1].item() == (zero != 0).sum().item()
 
 
+@pytest.mark.parametrize("dt,d,pad", [("bf16", 64, 0), ("bf16", 72, 24), ("bf16", 61, 0), ("bf16", 64, 3), ("f32", 64, 0),
+                                      ("f32", 61, 2)])
+def test_linear_ce_rows_without_gradient_may_hold_anything(dt, d, pad):
+    """NaN and infinities in rows whose label is ignored or out of range change nothing: the
+    gradients are bit for bit those with zeros there."""
+    n, v = 140, 300
+    h, h64, w, w64, labels, lab = ce_case(n, v, d, dt, 12)
+    labels = labels.clone()
+    labels[::3], labels[7] = -100, v + 5
+    dead = (labels < 0) | (labels >= v)
+    big = torch.zeros(n, d + pad, dtype=h.dtype, device=dev())
+    clean = torch.where(dead[:, None], 0.0, h.float()).to(h.dtype)
+    junk = torch.tensor([float("nan"), float("inf"), float("-inf"), 3e38], device=dev()).repeat(n * d // 4 + 1)[:n * d]
+    big[:, :d] = torch.where(dead[:, None], junk.view(n, d), h.float()).to(h.dtype)
+    big = big[:, :d]
+    ws = mm.linear_ce_workspace_for(big, w, labels)
+    loss, lse, _ = mm.muon_linear_ce_forward(big, w, labels, ws)
+    want, lsew, _ = mm.muon_linear_ce_forward(clean, w, labels, ws)
+    ok = ~dead
+    assert torch.equal(loss[ok], want[ok]) and torch.equal(lse[ok], lsew[ok]) and not loss[labels == -100].any()
+    got = mm.muon_linear_ce_backward(big, w, labels, lse, ws)
+    ref_ = mm.muon_linear_ce_backward(clean, w, labels, lsew, ws)
+    assert all(torch.equal(p, q) and bool(torch.isfinite(p).all()) for p, q in zip(got, ref_))
+    assert not got[0][dead].any() and bool(got[1].any())
+
+
 def test_linear_ce_extremes():
     """Logits far apart, all equal, and not finite."""
     v, d = 500, 32
