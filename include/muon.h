@@ -263,7 +263,7 @@ int muon_adamw_step(const muon_adamw_param* params, int n, int64_t t, float lr, 
  * and rstd are fp32, one a row, and may be NULL when no backward pass follows.
  * Arithmetic is fp32 with one rounding of y; the variance is summed from the centred
  * values.  y may be x itself (same ld); other overlaps are not allowed.
- * eps >= 0; dim >= 1 (below 2^31); rows == 0 is a no-op. */
+ * eps >= 0; rows and dim at most 2^30, dim >= 1; rows == 0 is a no-op. */
 int muon_layernorm_forward(const void* x, int64_t ldx, const void* weight, const void* bias,
                            int64_t rows, int64_t dim, int x_dtype, int w_dtype, float eps,
                            void* y, int64_t ldy, float* mean, float* rstd, muon_stream_t stream);
@@ -290,7 +290,7 @@ typedef struct muon_linear_ce {
   const void* H;          /* device, rows x dim, dtype; the hidden states                      */
   const void* W;          /* device, vocab x dim, dtype; the vocabulary matrix                 */
   const int64_t* labels;  /* device, rows                                                      */
-  int64_t rows, vocab, dim; /* rows >= 0, vocab >= 1, dim >= 1, each below 2^31                */
+  int64_t rows, vocab, dim; /* rows >= 0, vocab >= 1, dim >= 1, each at most 2^30              */
   int64_t ldh, ldw;       /* elements between rows of H and of W (>= dim)                      */
   int32_t dtype;          /* of H, W and their gradients: MUON_DTYPE_F32 or MUON_DTYPE_BF16    */
   int64_t ignore_index;   /* rows with this label carry no loss and no gradient                */

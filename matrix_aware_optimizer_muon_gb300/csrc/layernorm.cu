@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(1024) ln_columns_kernel(const float* part, int
 bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t dt_size(int dt) { return dt == MUON_DTYPE_BF16 ? 2 : 4; }
 bool known(int dt) { return dt == MUON_DTYPE_F32 || dt == MUON_DTYPE_BF16; }
-bool sizes_ok(int64_t rows, int64_t dim) { return rows >= 0 && rows < (1LL << 31) && dim >= 1 && dim < (1LL << 31); }
+// (so that a column or a row past the end by a block's stride still fits an int)
+bool sizes_ok(int64_t rows, int64_t dim) { return rows >= 0 && rows <= (1LL << 30) && dim >= 1 && dim <= (1LL << 30); }
 
 int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 

@@ -235,8 +235,8 @@ struct CePlan {
 
 int check(const muon_linear_ce* a) {
   if (!a) return MUON_ERR_INVALID;
-  const int64_t lim = 1LL << 31;
-  if (a->rows < 0 || a->rows >= lim || a->vocab < 1 || a->vocab >= lim || a->dim < 1 || a->dim >= lim ||
+  const int64_t lim = 1LL << 30;   // so that a tile's rows and columns past the end still fit an int
+  if (a->rows < 0 || a->rows > lim || a->vocab < 1 || a->vocab > lim || a->dim < 1 || a->dim > lim ||
       a->ldh < a->dim || a->ldw < a->dim)
     return MUON_ERR_INVALID;
   if (a->dtype != MUON_DTYPE_F32 && a->dtype != MUON_DTYPE_BF16) return MUON_ERR_UNSUPPORTED;

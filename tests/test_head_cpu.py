@@ -193,6 +193,19 @@ def test_linear_ce_refusals(lib):
     assert fwd(_ce(), n=size(_ce(), 0) - 1) == -3 and bwd(_ce(), n=size(_ce(), 1) - 1) == -3
 
 
+def test_sizes_whose_padding_would_pass_31_bits_are_refused(lib):
+    big, top = ctypes.c_size_t(-1).value, 1 << 30
+    for k in ("rows", "vocab"):
+        a = _ce(**{k: top + 1})
+        assert lib.muon_linear_ce_workspace_size(ctypes.byref(a), 0) == big, k
+        a = _ce(**{k: top})
+        assert lib.muon_linear_ce_workspace_size(ctypes.byref(a), 0) < big, k
+    a = _ce(dim=top + 1, ldh=top + 8, ldw=top + 8)
+    assert lib.muon_linear_ce_workspace_size(ctypes.byref(a), 0) == big
+    assert lib.muon_layernorm_workspace_size(3, top + 1) == big and lib.muon_layernorm_workspace_size(3, top) < big
+    assert lib.muon_layernorm_workspace_size(top + 1, 3) == big and lib.muon_layernorm_workspace_size(top, 3) < big
+
+
 def _p8(**kw):
     from matrix_aware_optimizer_muon_gb300.head import _PARAM8
     d = dict(P=FAKE, G=FAKE, m=FAKE, v=FAKE, m_scale=FAKE, v_scale=FAKE, numel=300, first=0, p_dtype=1, g_dtype=1)
