@@ -158,7 +158,10 @@ __device__ __forceinline__ void st_all(T* p, const f32x2 (&v)[A8_EACH / 2]) {
 }
 
 // Square root and reciprocal of the update: the hardware's approximations (2 ulp at most);
-// what they feed is lr times a number near 1, added to a parameter of 24 or 8 bits.
+// what they feed is lr times a number near 1, added to a parameter of 24 or 8 bits.  They
+// flush what is below 2^-126, so the root is taken of 2^24 v; a thread that holds a v whose
+// product with 2^24 could overflow (or that is NaN) asks for each element.
+constexpr float A8_ROOT_SCALE = 0x1p24f, A8_ROOT_MAX = 0x1p103f;
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -168,6 +171,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float root_any(float v) {   // 2^12 times the root
+  return v > A8_ROOT_MAX ? 0x1p12f * sqrt_approx(v) : sqrt_approx(v * A8_ROOT_SCALE);
+}
+__device__ __forceinline__ f32x2 updated(const Adamw8Params& q, f32x2 p, f32x2 m, f32x2 root) {
+  const f32x2 d = fma2(root, q.root, q.eps);
+  const f32x2 u = mul2(mul2(m, q.inv_bc1), make2(rcp_approx(lo2(d)), rcp_approx(hi2(d))));
+  return fma2(q.neg_lr, fma2(q.wd, p, u), p);
 }
 
 // Largest and smallest magnitude of three (a NaN makes the largest NaN).
@@ -318,27 +330,16 @@ __global__ void __launch_bounds__(A8_THREADS, a8_ctas(sizeof(PT) + sizeof(GT)))
     }
     if (zeros) now = decode_any(codes_n, bm, bv);
   }
-  f32x2 p[A8_EACH / 2];
 #pragma unroll
   for (int j = 0; j < A8_EACH / 2; ++j) {
     const f32x2 g = get2(gr, j);
     m2[j] = fma2(q.beta1, m2[j], mul2(q.omb1, g));
     v2[j] = fma2(q.beta2, v2[j], mul2(mul2(q.omb2, g), g));
-    // the root of 2^24 v: the approximation flushes what is below 2^-126
-    const f32x2 x = mul2(v2[j], both(0x1p24f));
-    const f32x2 d = fma2(make2(sqrt_approx(lo2(x)), sqrt_approx(hi2(x))), q.root, q.eps);
-    p[j] = get2(pr, j);
-    const f32x2 u = mul2(mul2(m2[j], q.inv_bc1), make2(rcp_approx(lo2(d)), rcp_approx(hi2(d))));
-    p[j] = fma2(q.neg_lr, fma2(q.wd, p[j], u), p[j]);
   }
-  if (whole) {
-    st_all(P + off, p);
-  } else {
+  if (!whole) {
 #pragma unroll
     for (int i = 0; i < A8_EACH; ++i) {
-      if (i < n) {
-        st1(P + off + i, i & 1 ? hi2(p[i / 2]) : lo2(p[i / 2]));
-      } else {   // codes past the end stay 0
+      if (i >= n) {   // codes past the end stay 0
         m2[i / 2] = i & 1 ? make2(lo2(m2[i / 2]), 0.f) : make2(0.f, hi2(m2[i / 2]));
         v2[i / 2] = i & 1 ? make2(lo2(v2[i / 2]), 0.f) : make2(0.f, hi2(v2[i / 2]));
       }
@@ -351,6 +352,25 @@ __global__ void __launch_bounds__(A8_THREADS, a8_ctas(sizeof(PT) + sizeof(GT)))
     vt = max3_abs(vt, lo2(v2[j]), hi2(v2[j]));
     mlow = min3_abs(mlow, lo2(m2[j]), hi2(m2[j]));
     vlow = min3_abs(vlow, lo2(v2[j]), hi2(v2[j]));
+  }
+  f32x2 p[A8_EACH / 2];
+  if (vt <= A8_ROOT_MAX) {
+#pragma unroll
+    for (int j = 0; j < A8_EACH / 2; ++j) {
+      const f32x2 x = mul2(v2[j], both(A8_ROOT_SCALE));
+      p[j] = updated(q, get2(pr, j), m2[j], make2(sqrt_approx(lo2(x)), sqrt_approx(hi2(x))));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < A8_EACH / 2; ++j)
+      p[j] = updated(q, get2(pr, j), m2[j], make2(root_any(lo2(v2[j])), root_any(hi2(v2[j]))));
+  }
+  if (whole) {
+    st_all(P + off, p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < A8_EACH; ++i)
+      if (i < n) st1(P + off + i, element(p, i));
   }
   uint32_t mtop = __float_as_uint(mt), vtop = __float_as_uint(vt);
   const bool odd = max(mtop, vtop) >= 0x7F800000u;
