@@ -310,7 +310,9 @@ size_t muon_linear_ce_workspace_size(const muon_linear_ce* a, int backward);
  * loss over the rows that are not ignored (0 if there is none), stats[1] their count.
  * loss, lse and stats are device fp32.  Products of bf16 values are exact and summed in
  * fp32; a NaN or +Inf logit makes the row's lse and loss NaN.  Call muon_workspace_init
- * once on a fresh workspace; muon_check_status reports an expired wait. */
+ * once on a fresh workspace; muon_check_status reports an expired wait.  Until it has done
+ * so, this call and the next ones with the workspace write NaN to every output (the
+ * backward pass too), so that a caller who does not ask cannot take them for results. */
 int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, float* lse, float* stats,
                            void* ws, size_t ws_bytes, muon_stream_t stream);
 

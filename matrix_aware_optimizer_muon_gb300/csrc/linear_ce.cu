@@ -113,6 +113,18 @@ __global__ void __launch_bounds__(256) mask_kernel(const bf16* in, long long ld,
   }
 }
 
+// Whether a wait of this call's products (or of an earlier call that nobody asked about) ran
+// out: what they left unwritten must not pass for a result, so the last kernel of a call
+// writes NaN instead.  A caller without a workspace to ask sees it too.
+__device__ __forceinline__ bool is_lost(const unsigned int* status) { return __ldcg(status) & DEV_TIMEOUT; }
+__device__ __forceinline__ float not_a_number() { return __int_as_float(0x7FC00000); }
+template <typename T>
+__device__ void fill_lost(T* p, long long n) {
+  if (!p) return;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x)
+    st1(p + i, not_a_number());
+}
+
 // One warp a row: joins its partial sums (JOIN_HELD a lane at a time), writes lse and
 // loss.  Each block adds its rows' losses up; the last block to finish adds the blocks'.
 constexpr int JOIN_WARPS = 8;
@@ -120,7 +132,8 @@ constexpr int JOIN_HELD = 8;   // partial sums a lane keeps at a time
 __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const float2* part, int parts, long long rows,
                                                                const int64_t* labels, long long vocab, long long ignore,
                                                                const float* zlabel, float* loss, float* lse,
-                                                               float* stats, float2* sums, unsigned int* ticket) {
+                                                               float* stats, float2* sums, unsigned int* ticket,
+                                                               const unsigned int* status) {
   __shared__ float red[32];
   __shared__ float2 mine[JOIN_WARPS];
   __shared__ bool last;
@@ -128,7 +141,11 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const float2* par
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long r = (long long)blockIdx.x * JOIN_WARPS + warp;
   float2 sum = make_float2(0.f, 0.f);   // this row's loss, and 1 if it counts
-  if (r < rows) {
+  const bool lost = is_lost(status);
+  if (r < rows && lost) {
+    sum = make_float2(not_a_number(), not_a_number());
+    if (lane == 0) lse[r] = loss[r] = not_a_number();
+  } else if (r < rows) {
     const float2* q = part + (size_t)r * parts;
     const long long lab = labels[r];
     const bool counted = lab != ignore, known = counted && lab >= 0 && lab < vocab;
@@ -156,7 +173,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const float2* par
     const float ref = top == -INFINITY ? 0.f : top;
     s = warp_sum(mx == -INFINITY ? s : s * expf(mx - ref));
     const float l = ref + logf(s);
-    const float x = known ? l - zl : counted ? __int_as_float(0x7FC00000) : 0.f;
+    const float x = known ? l - zl : counted ? not_a_number() : 0.f;
     if (lane == 0) {
       lse[r] = l;
       loss[r] = x;
@@ -202,8 +219,14 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const float2* par
 template <typename T>
 __global__ void __launch_bounds__(256) split_sum_kernel(const float* acc, int splits, long long rows, int dim,
                                                         long long ldacc, T* out, float scale, const float* upstream,
-                                                        const float* stats) {
+                                                        const float* stats, const unsigned int* status, T* dW,
+                                                        long long vocab) {
   await_previous();
+  if (is_lost(status)) {
+    fill_lost(out, rows * dim);
+    fill_lost(dW, vocab * dim);
+    return;
+  }
   const long long r = blockIdx.x;
   const float u = shared_factor(scale, upstream, stats);
   for (int c = threadIdx.x; c < dim; c += 256) {
@@ -213,6 +236,16 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float* acc, int sp
     for (int k = 0; k < splits; ++k) s += a[(size_t)k * rows * ldacc];
     st1(out + r * dim + c, s * u);
   }
+}
+
+// The last kernel of a backward pass that sums no ranges.
+constexpr int LOST_CTAS = 32;
+template <typename T>
+__global__ void __launch_bounds__(256) lost_kernel(const unsigned int* status, T* dH, long long nh, T* dW, long long nw) {
+  await_previous();
+  if (!is_lost(status)) return;
+  fill_lost(dH, nh);
+  fill_lost(dW, nw);
 }
 
 // ---------------------------------------------------------------------------
@@ -451,6 +484,16 @@ bool lay_out(OrderedParams* p, int npairs) {
   return true;
 }
 
+template <typename T>
+cudaError_t finish(const muon_linear_ce* a, const CePlan& P, const float* acc, const Params& p, T* dH, T* dW, cudaStream_t s) {
+  count_launch();
+  if (dH && P.splits > 1)
+    return launch_after(split_sum_kernel<T>, dim3((unsigned)a->rows), dim3(256), 0, s, acc, P.splits, a->rows, a->dim,
+                        P.ldacc, dH, p.scale, p.upstream, p.stats, p.status, dW, a->vocab);
+  return launch_after(lost_kernel<T>, dim3(LOST_CTAS), dim3(256), 0, s, p.status, dH, a->rows * a->dim, dW,
+                      a->vocab * a->dim);
+}
+
 int result_vec(const void* out, int64_t ld, int dt) {
   const size_t row = (size_t)ld * dt_size(dt);
   if (is_aligned(out, 32) && row % 32 == 0) return 2;
@@ -508,7 +551,7 @@ extern "C" int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, floa
   count_launch();
   if (launch_after(join_kernel, dim3((unsigned)cdiv(a->rows, JOIN_WARPS)), dim3(32 * JOIN_WARPS), 0, s, p.part,
                    2 * j.ntiles, a->rows, a->labels, a->vocab, a->ignore_index, p.zlabel, loss, lse, stats,
-                   reinterpret_cast<float2*>(w + P.sums), reinterpret_cast<unsigned int*>(w) + TICKET_WORD) !=
+                   reinterpret_cast<float2*>(w + P.sums), reinterpret_cast<unsigned int*>(w) + TICKET_WORD, p.status) !=
       cudaSuccess)
     return MUON_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
@@ -608,15 +651,8 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
     const bool ordered = lay_out(&p, npairs);
     if (launch(p, ordered, f32, s) != cudaSuccess) return MUON_ERR_CUDA;
   }
-  if (dH && P.splits > 1) {
-    const dim3 blocks((unsigned)a->rows);
-    const cudaError_t e =
-        f32 ? launch_after(split_sum_kernel<float>, blocks, dim3(256), 0, s, acc, P.splits, a->rows, a->dim, P.ldacc,
-                           static_cast<float*>(dH), grad_scale, upstream, stats)
-            : launch_after(split_sum_kernel<bf16>, blocks, dim3(256), 0, s, acc, P.splits, a->rows, a->dim, P.ldacc,
-                           static_cast<bf16*>(dH), grad_scale, upstream, stats);
-    if (e != cudaSuccess) return MUON_ERR_CUDA;
-    count_launch();
-  }
+  const cudaError_t e = f32 ? finish<float>(a, P, acc, p, static_cast<float*>(dH), static_cast<float*>(dW), s)
+                            : finish<bf16>(a, P, acc, p, static_cast<bf16*>(dH), static_cast<bf16*>(dW), s);
+  if (e != cudaSuccess) return MUON_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

@@ -38,3 +38,33 @@ def test_adamw8_steps_for_large_gradients(pdt, gdt):
             tol = 16 * U * (np.abs(ref_p[i]) + step) + (BF * 1.01 * np.abs(p) if pdt == "bf16" else 0) + 1e-12
             within(got, p, tol, ("p", k, t))
             ref_p[i] = got
+
+
+def test_linear_ce_expired_wait_shows_in_every_output():
+    """When a wait runs out (test flag: no loads are issued) loss, lse, statistics and both
+    gradients are NaN, also for a caller that has no workspace to ask."""
+    for n, v, d in ((24, 3000, 64), (600, 700, 96)):       # dH summed over ranges of K, and not
+        h, h64, w, w64, labels, lab = ce_case(n, v, d, "bf16", 6)
+        ws = mm.alloc_linear_ce_workspace(n, v, d)
+        want = mm.muon_linear_ce_forward(h, w, labels, ws)
+        grads = mm.muon_linear_ce_backward(h, w, labels, want[1], ws, stats=want[2])
+        hr, wr = h.clone().requires_grad_(), w.clone().requires_grad_()
+        good = mm.linear_cross_entropy(hr, wr, labels)
+        mm.muon_debug_set(mm.MUON_DEBUG_STALL_PRODUCER, 20)
+        try:
+            lost = mm.muon_linear_ce_forward(h, w, labels, ws)
+            assert all(bool(torch.isnan(t).all()) for t in lost)
+            assert mm.muon_check_status(ws) == mm.MUON_ERR_TIMEOUT
+            for need in ((True, True), (True, False), (False, True)):
+                lost = mm.muon_linear_ce_backward(h, w, labels, want[1], ws, stats=want[2], need_dh=need[0], need_dw=need[1])
+                assert all(t is None or bool(torch.isnan(t).all()) for t in lost)
+                assert mm.muon_check_status(ws) == mm.MUON_ERR_TIMEOUT
+            assert torch.isnan(mm.linear_cross_entropy(hr, wr, labels))
+            good.backward()
+            assert bool(torch.isnan(hr.grad).all()) and bool(torch.isnan(wr.grad).all())
+        finally:
+            mm.muon_debug_set(0, 0)
+        got = mm.muon_linear_ce_forward(h, w, labels, ws)
+        again = mm.muon_linear_ce_backward(h, w, labels, got[1], ws, stats=got[2])
+        assert mm.muon_check_status(ws) == mm.MUON_OK
+        assert all(torch.equal(p, q) for p, q in zip(want + grads, got + again))
