@@ -24,8 +24,8 @@
 // memory's ports most of the time.  The kPromote form takes the accumulator over into registers every
 // seg_kb K steps and adds there with rounding to nearest (five take-overs of a tile of
 // 2560 products instead of two cost 8%).  It serves the logits of the forward pass, whose
-// loss is fp32, and every product of 32-bit operands; sums that are rounded to bf16 (2e-3)
-// do without.
+// loss is fp32, every product of 32-bit operands, and launches with sums of more than 2^16
+// products; shorter ones that are rounded to bf16 (4e-3) do without.
 //
 // 32-bit operands come as three bf16 parts (24 bits of mantissa); the six products of
 // parts down to 2^-16 of the leading one are summed, smallest first.

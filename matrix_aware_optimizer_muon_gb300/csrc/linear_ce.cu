@@ -35,6 +35,11 @@ constexpr int MAX_SPLITS = 16;
 // 8192 x 131072 3.44, 3.20 and 3.17 ms; 32-bit 1021 x 1001 x 10007 backward, 4 steps 3.9e-7
 // of dH and 314 us, 8 steps 6.9e-7 and 304, 16 steps 1.3e-6 and 302.
 constexpr int SEG_BF16 = 20, SEG_F32 = 4;
+// The same for bf16 products whose sums are rounded to bf16 (the backward pass).  Up to 2^16
+// products of one sign the truncation's bias is 3e-4, well below that rounding's 4e-3, and a
+// launch of no longer sums takes the form without take-overs; it grows in proportion (2^22
+// rows: 2.4e-2 of dW).
+constexpr int SEG_LONG = 1024;
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -620,7 +625,7 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
         j.out = P.splits == 1 ? dH : nullptr;
         j.ldo = a->dim;
         j.vec = result_vec(dH, a->dim, a->dtype);
-        j.seg_kb = f32 ? SEG_F32 : j.nkb;
+        j.seg_kb = f32 ? SEG_F32 : SEG_LONG;
       }
       if (dW) {
         Job& j = p.job[p.njobs++];
@@ -632,7 +637,7 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
         j.out = static_cast<char*>(dW) + (size_t)v0 * a->dim * es;
         j.ldo = a->dim;
         j.vec = result_vec(j.out, a->dim, a->dtype);
-        j.seg_kb = f32 ? SEG_F32 : j.nkb;
+        j.seg_kb = f32 ? SEG_F32 : SEG_LONG;
       }
     }
     if (i < P.npieces) {
@@ -646,10 +651,12 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
       j.out = w + P.g[i & 1];
       j.ldo = P.piece;
       j.part_stride = (long long)P.g_part;
-      j.seg_kb = f32 ? SEG_F32 : j.nkb;
+      j.seg_kb = f32 ? SEG_F32 : SEG_LONG;
     }
+    bool promote = f32;
+    for (int k = 0; k < p.njobs; ++k) promote = promote || p.job[k].nkb > SEG_LONG;
     const bool ordered = lay_out(&p, npairs);
-    if (launch(p, ordered, f32, s) != cudaSuccess) return MUON_ERR_CUDA;
+    if (launch(p, ordered, promote, s) != cudaSuccess) return MUON_ERR_CUDA;
   }
   const cudaError_t e = f32 ? finish<float>(a, P, acc, p, static_cast<float*>(dH), static_cast<float*>(dW), s)
                             : finish<bf16>(a, P, acc, p, static_cast<bf16*>(dH), static_cast<bf16*>(dW), s);

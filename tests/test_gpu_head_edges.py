@@ -68,3 +68,39 @@ def test_linear_ce_expired_wait_shows_in_every_output():
         again = mm.muon_linear_ce_backward(h, w, labels, got[1], ws, stats=got[2])
         assert mm.muon_check_status(ws) == mm.MUON_OK
         assert all(torch.equal(p, q) for p, q in zip(want + grads, got + again))
+
+
+def test_linear_ce_backward_long_sums():
+    """dW over 2^22 rows whose products all have one sign: the tensor cores' truncation must
+    not pile up.  W = 0, so every probability is 2^-8 exactly and dW[v] = 2^-8 sum_r h[r] for a
+    column that is no row's label.  Between take-overs of the sums lie 2^16 products at most,
+    2^12 additions of 16 products with an error of 2u each; then a rounding to bf16."""
+    n, v, d = 1 << 22, 256, 64
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(1)
+    h = (torch.rand(n, d, generator=gen, device=dev()) + 0.5).bfloat16()
+    w = torch.zeros(v, d, device=dev(), dtype=torch.bfloat16)
+    labels = torch.randint(0, v // 2, (n,), generator=gen, device=dev())
+    ws = mm.alloc_linear_ce_workspace(n, v, d)
+    lse = torch.full((n,), float(np.log(256.0)), device=dev())
+    _, dw = mm.muon_linear_ce_backward(h, w, labels, lse, ws, need_dh=False)
+    assert mm.muon_check_status(ws) == mm.MUON_OK
+    want = num(h.double().sum(0)) / 256
+    within(num(dw[v // 2:]), np.broadcast_to(want, (v // 2, d)), np.broadcast_to((BF + 4096 * 2 * U + 64 * U) * want, (v // 2, d)),
+           "dw")
+
+
+def test_linear_ce_backward_long_vocabulary():
+    """dH of few rows over a vocabulary of 2^21 entries, all products of one sign."""
+    n, v, d = 40, 1 << 21, 64
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(2)
+    h = torch.zeros(n, d, device=dev(), dtype=torch.bfloat16)
+    w = (torch.rand(v, d, generator=gen, device=dev()) + 0.5).bfloat16()
+    labels = torch.zeros(n, dtype=torch.int64, device=dev())
+    ws = mm.alloc_linear_ce_workspace(n, v, d)
+    lse = torch.full((n,), float(np.log(256.0)), device=dev())
+    dh, _ = mm.muon_linear_ce_backward(h, w, labels, lse, ws, need_dw=False)
+    assert mm.muon_check_status(ws) == mm.MUON_OK
+    want = num(w.double().sum(0)) / 256 - num(w[0])
+    within(num(dh), np.broadcast_to(want, (n, d)), np.broadcast_to((BF + 4096 * 2 * U + 64 * U) * want, (n, d)), "dh")
