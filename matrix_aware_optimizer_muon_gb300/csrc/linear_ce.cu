@@ -50,10 +50,6 @@ bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 // small kernels
 // ---------------------------------------------------------------------------
 
-// Rows of any stride and alignment to bf16 rows of ldo elements (a multiple of 8):
-// bf16 as it is, fp32 as `parts` bf16 numbers that add up to it (8 bits each).  A warp a
-// row, a lane two neighbouring columns of each 64, PACK_HELD of them in flight.
-//
 // Rows whose label carries no gradient become zeros: dW sums g^T H over all rows, and a
 // zero of g times a NaN or an infinity that such a row may hold (padding) would be NaN.
 struct RowMask {
@@ -66,6 +62,15 @@ __device__ __forceinline__ bool masked(const RowMask& k, long long r) {
   return lab == k.ignore || lab < 0 || lab >= k.vocab;
 }
 
+// Rows of any stride and alignment to bf16 rows of ldo elements (a multiple of 8):
+// bf16 as it is, fp32 as `parts` bf16 numbers that add up to it (8 bits each).  A warp a
+// row, a lane two neighbouring columns of each 64, PACK_HELD of them in flight.
+// A part that more parts follow stays within bf16's range: fp32's largest numbers (a mask of
+// the type's lowest value) would round to an infinity and leave a NaN for the next.  What no
+// part can hold, infinities and NaN, is left to the last one, which is multiplied with the other
+// operand's leading part alone.
+constexpr float BF16_MAX = 0x1.FEp127f;
+__device__ __forceinline__ float in_bf16_range(float x) { return fminf(fmaxf(x, -BF16_MAX), BF16_MAX); }
 constexpr int PACK_HELD = 8;
 template <typename T>
 __global__ void __launch_bounds__(256) pack_kernel(const T* in, long long ld, long long rows, int dim, bf16* out,
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* in, long long ld, lo
     for (int q = 0; q < parts; ++q, o += part_stride) {
 #pragma unroll
       for (int i = 0; i < PACK_HELD; ++i) {
-        const uint32_t w = pack_bf16x2(a[i], b[i]);
+        const uint32_t w = q + 1 < parts ? pack_bf16x2(in_bf16_range(a[i]), in_bf16_range(b[i])) : pack_bf16x2(a[i], b[i]);
         if (c0 + 64 * i < dim) *reinterpret_cast<uint32_t*>(o + 64 * i) = w;
         a[i] -= __uint_as_float(w << 16);
         b[i] -= __uint_as_float(w & 0xFFFF0000u);

@@ -104,3 +104,43 @@ def test_linear_ce_backward_long_vocabulary():
     assert mm.muon_check_status(ws) == mm.MUON_OK
     want = num(w.double().sum(0)) / 256 - num(w[0])
     within(num(dh), np.broadcast_to(want, (n, d)), np.broadcast_to((BF + 4096 * 2 * U + 64 * U) * want, (n, d)), "dh")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("mask", ["lowest", "minus infinity"])
+def test_linear_ce_vocabulary_masked_by_a_bias_column(dt, mask):
+    """Entries shut out by the type's lowest value (or minus infinity) in a column that every
+    hidden state holds 1 in: their logits vanish, the others' loss is what it is without them."""
+    n, v, d = 70, 700, 64
+    h, h64, w, w64, labels, lab = ce_case(n, v, d, dt, 12)
+    low = torch.finfo(TYPES[dt]).min if mask == "lowest" else float("-inf")
+    shut = np.arange(v) % 5 == 2
+    h[:, -1] = 1.0
+    w[:, -1] = torch.from_numpy(np.where(shut, low, 0.0)).to(dev(), w.dtype)
+    lab = np.where((lab >= 0) & shut[lab], lab - 1, lab)
+    labels = torch.from_numpy(lab).to(dev())
+    ws = mm.alloc_linear_ce_workspace(n, v, d, TYPES[dt])
+    loss, lse, stats = mm.muon_linear_ce_forward(h, w, labels, ws)
+    h64, w64 = num(h), num(w)
+    keep = np.flatnonzero(~shut)
+    place = np.where(lab >= 0, np.searchsorted(keep, np.maximum(lab, 0)), lab)
+    rloss, rlse, rmean, count = ref.linear_ce_forward(h64, w64[keep], place)
+    ez = ce_tolerances(h64, w64[keep], dt)
+    spread = np.abs(h64 @ w64[keep].T).max(1) + 1
+    elog = ez + (v / 32 + 64 + 4 * spread) * U + 4 * U * np.abs(rlse)
+    within(num(lse), rlse, elog, "lse")
+    within(num(loss), rloss, elog + ez + 2 * U * np.abs(rlse), "loss")
+    if mask == "lowest":
+        dh, dw = mm.muon_linear_ce_backward(h, w, labels, lse, ws, stats=stats)
+        assert torch.isfinite(dh).all() and torch.isfinite(dw).all() and not dw[torch.from_numpy(shut).to(dev())].any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_linear_ce_nan_and_infinite_logits_stay_nan(bad):
+    for dt in ("bf16", "f32"):
+        h, h64, w, w64, labels, lab = ce_case(20, 300, 64, dt, 13)
+        h[3, 5], w[:, 5] = bad, 1.0
+        loss, lse, _ = mm.muon_linear_ce_forward(h, w, labels.clamp(min=0), mm.alloc_linear_ce_workspace(20, 300, 64, TYPES[dt]))
+        assert torch.isnan(loss[3]) and torch.isnan(lse[3])
+        rest = torch.arange(20, device=dev()) != 3
+        assert torch.isfinite(loss[rest]).all() and torch.isfinite(lse[rest]).all()
