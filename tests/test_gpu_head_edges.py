@@ -144,3 +144,16 @@ def test_linear_ce_nan_and_infinite_logits_stay_nan(bad):
         assert torch.isnan(loss[3]) and torch.isnan(lse[3])
         rest = torch.arange(20, device=dev()) != 3
         assert torch.isfinite(loss[rest]).all() and torch.isfinite(lse[rest]).all()
+
+
+def test_second_derivatives_are_refused():
+    x = torch.randn(5, 64, device=dev(), requires_grad=True)
+    w = torch.randn(64, device=dev(), requires_grad=True)
+    g, = torch.autograd.grad(mm.layer_norm(x, w).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (g.square().sum() + x.sum()).backward()
+    v = torch.randn(100, 64, device=dev(), requires_grad=True)
+    labels = torch.arange(5, device=dev())
+    g, = torch.autograd.grad(mm.linear_cross_entropy(x, v, labels), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (g.square().sum() + x.sum()).backward()
