@@ -6,7 +6,7 @@ from typing import Dict, List, Sequence
 import torch
 
 from . import _lib
-from .head import AdamW8
+from .head import AdamW8, _on
 
 
 class PeriodicMuon:
@@ -54,8 +54,10 @@ class PeriodicMuon:
                 raise ValueError("W, G and M must have the same shape")
             self._arr[i].G = _lib._ptr(g)
             self._arr[i].g_dtype = _lib._dt(g)
-        if self.aux8 is not None:   # refused before anything is enqueued
+        # copied on the stream that reads them: in its order, and in its share of the allocator
+        with _on(stream):
             aux_grads = [g.contiguous() for g in aux_grads]
+        if self.aux8 is not None:   # refused before anything is enqueued
             self.aux8._check(aux_grads)
         br = _lib.periodic_step_prepared(self._arr, self._n, self.step_count, self.ws, self.K, self.gamma, self.mu,
                                          self.eta, self.lam, self.ns5_mode, stream=stream)

@@ -70,6 +70,34 @@ def test_linear_ce_expired_wait_shows_in_every_output():
         assert all(torch.equal(p, q) for p, q in zip(want + grads, got + again))
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_periodic_muon_copies_gradients_on_the_stream_that_reads_them(bits):
+    """Gradients that are not contiguous, and a stream of the caller's, while the current stream
+    is busy and its freed memory is written again."""
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(3)
+    W0 = torch.randn(64, 96, generator=gen, device=dev()).bfloat16()
+    A0 = [torch.randn(s, generator=gen, device=dev()) for s in ((1000, 700), (33, 65))]
+    G = [torch.randn(64, 96, generator=gen, device=dev()).bfloat16()]
+    GA = [torch.randn(*reversed(a.shape), generator=gen, device=dev()).T for a in A0]
+
+    def run(stream):
+        W, A = [W0.clone()], [a.clone() for a in A0]
+        opt = mm.PeriodicMuon(W, aux_params=A, aux_bits=bits, aux_lr=1e-2)
+        torch.cuda.synchronize()
+        if stream is None:
+            opt.step(G, [g.contiguous() for g in GA])
+        else:
+            torch.cuda._sleep(100_000_000)
+            opt.step(G, GA, stream=stream)
+            for g in GA:                          # what the step let go of is given out again
+                torch.full_like(g.contiguous(), float("nan"))
+        torch.cuda.synchronize()
+        return W + A
+
+    assert all(torch.equal(a, b) for a, b in zip(run(None), run(torch.cuda.Stream())))
+
+
 def test_linear_ce_backward_long_sums():
     """dW over 2^22 rows whose products all have one sign: the tensor cores' truncation must
     not pile up.  W = 0, so every probability is 2^-8 exactly and dW[v] = 2^-8 sum_r h[r] for a
