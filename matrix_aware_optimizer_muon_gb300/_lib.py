@@ -326,12 +326,11 @@ def muon_launch_count() -> int:
     return int(load_library().muon_launch_count())
 
 
-def muon_adamw_step(P: Sequence[torch.Tensor], G: Sequence[torch.Tensor], m: Sequence[torch.Tensor],
-                    v: Sequence[torch.Tensor], t: int, lr: float, beta1: float = 0.9, beta2: float = 0.999,
-                    eps: float = 1e-8, weight_decay: float = 0.0, stream=None):
-    """AdamW on parameters Muon does not take (any shape; m, v fp32 of the same size)."""
+def adamw_array(P: Sequence[torch.Tensor], G: Sequence[torch.Tensor], m: Sequence[torch.Tensor],
+                v: Sequence[torch.Tensor]):
+    """The parameter array of muon_adamw_step, checked."""
     n = len(P)
-    arr = (MuonAdamwParam * max(n, 1))()
+    arr = (MuonAdamwParam * n)()
     for i in range(n):
         if not (P[i].numel() == G[i].numel() == m[i].numel() == v[i].numel()):
             raise ValueError("P, G, m, v must have the same number of elements")
@@ -339,5 +338,17 @@ def muon_adamw_step(P: Sequence[torch.Tensor], G: Sequence[torch.Tensor], m: Seq
             raise ValueError("AdamW moments are fp32")
         arr[i] = MuonAdamwParam(_ptr(P[i]), _ptr(G[i]), _ptr(m[i]), _ptr(v[i]), int(P[i].numel()),
                                 _dt(P[i]), _dt(G[i]))
-    _check("muon_adamw_step", load_library().muon_adamw_step(arr, n, int(t), lr, beta1, beta2, eps,
+    return arr
+
+
+def adamw_step_prepared(arr, t: int, lr: float, beta1: float, beta2: float, eps: float, weight_decay: float,
+                        stream=None):
+    _check("muon_adamw_step", load_library().muon_adamw_step(arr, len(arr), int(t), lr, beta1, beta2, eps,
                                                              weight_decay, _stream(stream)))
+
+
+def muon_adamw_step(P: Sequence[torch.Tensor], G: Sequence[torch.Tensor], m: Sequence[torch.Tensor],
+                    v: Sequence[torch.Tensor], t: int, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+                    eps: float = 1e-8, weight_decay: float = 0.0, stream=None):
+    """AdamW on parameters Muon does not take (any shape; m, v fp32 of the same size)."""
+    adamw_step_prepared(adamw_array(P, G, m, v), t, lr, beta1, beta2, eps, weight_decay, stream)

@@ -253,17 +253,24 @@ class AdamW8:
             raise ValueError("parameters, and gradients, are contiguous and of one dtype")
         return _dt(tensors[0])
 
-    def step(self, grads: Sequence[torch.Tensor], stream=None) -> None:
-        """One asynchronous step."""
+    def _point(self, grads: Sequence[torch.Tensor]) -> None:
+        """Checks and enters the tensors of a step."""
         arr = self._arr
         # the parameters too: a model may have been cast or moved since the last step
         arr["p_dtype"], arr["g_dtype"] = self._check(self.params), self._check(grads)
         arr["G"] = list(map(torch.Tensor.data_ptr, grads))
         arr["P"] = list(map(torch.Tensor.data_ptr, self.params))
+
+    def _launch(self, stream) -> None:
         _check("muon_adamw8_step", load_library().muon_adamw8_step(
-            self._addr, len(arr), self.step_count + 1, self.lr, self.betas[0], self.betas[1], self.eps,
+            self._addr, len(self._arr), self.step_count + 1, self.lr, self.betas[0], self.betas[1], self.eps,
             self.weight_decay, self.seed, _stream(stream, self.m)))
         self.step_count += 1
+
+    def step(self, grads: Sequence[torch.Tensor], stream=None) -> None:
+        """One asynchronous step."""
+        self._point(grads)
+        self._launch(stream)
 
     def moments(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """The values the codes of both moments stand for, as flat bf16 tensors (exact)."""

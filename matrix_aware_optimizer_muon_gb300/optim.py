@@ -54,25 +54,29 @@ class PeriodicMuon:
                 raise ValueError("W, G and M must have the same shape")
             self._arr[i].G = _lib._ptr(g)
             self._arr[i].g_dtype = _lib._dt(g)
-        # copied on the stream that reads them: in its order, and in its share of the allocator
-        with _on(stream):
-            aux_grads = [g.contiguous() for g in aux_grads]
-        if self.aux8 is not None:   # refused before anything is enqueued
-            self.aux8._check(aux_grads)
-        br = _lib.periodic_step_prepared(self._arr, self._n, self.step_count, self.ws, self.K, self.gamma, self.mu,
-                                         self.eta, self.lam, self.ns5_mode, stream=stream)
+        # what cannot be read is refused before anything is enqueued
         if self.aux:
             if len(aux_grads) != len(self.aux):
                 raise ValueError("one gradient per auxiliary parameter")
+            # copied on the stream that reads them: in its order, and in its share of the allocator
+            with _on(stream):
+                aux_grads = [g.contiguous() for g in aux_grads]
+            if self.aux8 is not None:
+                self.aux8._point(aux_grads)
+            else:
+                if len({(p.dtype, g.dtype) for p, g in zip(self.aux, aux_grads)}) != 1:
+                    raise ValueError("auxiliary parameters, and their gradients, are of one dtype")
+                aux = _lib.adamw_array(self.aux, aux_grads, self.aux_m, self.aux_v)
+        br = _lib.periodic_step_prepared(self._arr, self._n, self.step_count, self.ws, self.K, self.gamma, self.mu,
+                                         self.eta, self.lam, self.ns5_mode, stream=stream)
         if self.aux8 is not None:
             # the schedule of learning rate and decay is the caller's, as for 32 bits
             self.aux8.lr, self.aux8.betas, self.aux8.eps, self.aux8.weight_decay = self.aux_lr, self.betas, self.eps, self.lam
             self.aux8.step_count = self.step_count
-            self.aux8.step(aux_grads, stream=stream)
+            self.aux8._launch(stream)
         elif self.aux:
-            _lib.muon_adamw_step([p.view(-1) for p in self.aux], [g.reshape(-1) for g in aux_grads], self.aux_m,
-                                 self.aux_v, self.step_count + 1, self.aux_lr, self.betas[0], self.betas[1],
-                                 self.eps, self.lam, stream=stream)
+            _lib.adamw_step_prepared(aux, self.step_count + 1, self.aux_lr, self.betas[0], self.betas[1], self.eps,
+                                     self.lam, stream=stream)
         self.step_count += 1
         return br
 

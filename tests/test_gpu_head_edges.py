@@ -98,6 +98,36 @@ def test_periodic_muon_copies_gradients_on_the_stream_that_reads_them(bits):
     assert all(torch.equal(a, b) for a, b in zip(run(None), run(torch.cuda.Stream())))
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_periodic_muon_refuses_before_it_changes_anything(bits):
+    W = [torch.randn(64, 96, device=dev()).bfloat16()]
+    A = [torch.randn(300, device=dev()), torch.randn(40, device=dev())]
+    opt = mm.PeriodicMuon(W, aux_params=A, aux_bits=bits)
+    g, ga = [torch.randn_like(W[0])], [torch.randn_like(a) for a in A]
+    opt.step(g, ga)
+    w, a, m = W[0].clone(), [x.clone() for x in A], opt.M[0].clone()
+
+    def refused(grads):
+        with pytest.raises((ValueError, TypeError, mm.MuonError)):
+            opt.step(g, grads)
+        torch.cuda.synchronize()
+        assert torch.equal(W[0], w) and torch.equal(opt.M[0], m) and opt.step_count == 1
+
+    refused(ga[:1])
+    refused([ga[0], ga[1][:39]])
+    refused([ga[0], ga[1].cpu()])
+    refused([ga[0], ga[1].bfloat16()])
+    refused([ga[0], ga[1].half()])
+    keep = opt.aux[1].data
+    for bad in (keep.bfloat16(), keep.cpu(), keep[:39], torch.zeros(80, device=dev())[::2]):
+        opt.aux[1].data = bad
+        refused(ga)
+    opt.aux[1].data = keep
+    assert all(torch.equal(x, y) for x, y in zip(A, a))
+    opt.step(g, ga)
+    assert opt.step_count == 2 and not torch.equal(W[0], w)
+
+
 def test_linear_ce_backward_long_sums():
     """dW over 2^22 rows whose products all have one sign: the tensor cores' truncation must
     not pile up.  W = 0, so every probability is 2^-8 exactly and dW[v] = 2^-8 sum_r h[r] for a
