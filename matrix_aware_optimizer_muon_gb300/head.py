@@ -24,6 +24,16 @@ ADAMW8_BLOCK = 128
 # The current stream's handle without building a Stream object (3 us of a small call's 12).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _here = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on_current(*tensors: Optional[torch.Tensor]) -> None:
+    """The library launches on the current device: a tensor of another one is refused, for its
+    address (and its device's stream) means something else there."""
+    here = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError("tensors must be on the current CUDA device")
 
 
 def _on(stream):
@@ -76,6 +86,7 @@ def muon_layernorm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = Non
     px, ldx = _rows(x, "x")
     n, d = x.shape
     pw, pb = _vector(weight, d, None, "weight"), _vector(bias, d, weight.dtype if weight is not None else None, "bias")
+    _on_current(x, weight, bias)
     wdt = _dt(weight if weight is not None else bias if bias is not None else x)
     with _on(stream):
         y = torch.empty((n, d), dtype=x.dtype, device=x.device)
@@ -105,6 +116,7 @@ def muon_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[
         raise ValueError("dy and x must have the same shape and dtype")
     pw = _vector(weight, d, None, "weight")
     pm, pr = _vector(mean, n, torch.float32, "mean"), _vector(rstd, n, torch.float32, "rstd")
+    _on_current(dy, x, weight, mean, rstd, ws)
     wt = weight.dtype if weight is not None else x.dtype
     with _on(stream):
         dx = torch.empty((n, d), dtype=x.dtype, device=x.device)
@@ -158,6 +170,7 @@ def _ce_workspace_size(a: MuonLinearCe, backward: bool) -> int:
 
 def linear_ce_workspace_for(h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, backward: bool = True) -> torch.Tensor:
     """Workspace for these very tensors (their strides and alignment included)."""
+    _on_current(h, w, labels)
     return _workspace(_ce_workspace_size(_ce_args(h, w, labels, -100), backward), h.device)
 
 
@@ -174,6 +187,7 @@ def muon_linear_ce_forward(h: torch.Tensor, w: torch.Tensor, labels: torch.Tenso
     without keeping the logits.  Returns (loss, lse, stats), fp32: each row's loss (0 where
     the label is ignore_index) and log-sum-exp, and [mean loss of the other rows, their count]."""
     a = _ce_args(h, w, labels, ignore_index)
+    _on_current(h, w, labels, ws)
     n = h.shape[0]
     with _on(stream):
         loss = torch.empty(n, dtype=torch.float32, device=h.device)
@@ -197,6 +211,7 @@ def muon_linear_ce_backward(h: torch.Tensor, w: torch.Tensor, labels: torch.Tens
     pl = _vector(lse, n, torch.float32, "lse")
     pg, ps = _vector(row_grad, n, torch.float32, "row_grad"), _vector(stats, 2, torch.float32, "stats")
     pu = None if upstream is None else _vector(upstream.view(-1), 1, torch.float32, "upstream")
+    _on_current(h, w, labels, lse, ws, row_grad, stats, upstream)
     with _on(stream):
         dh = torch.empty((n, h.shape[1]), dtype=h.dtype, device=h.device) if need_dh else None
         dw = torch.empty(tuple(w.shape), dtype=w.dtype, device=h.device) if need_dw else None
@@ -249,6 +264,7 @@ class AdamW8:
             raise ValueError("parameters keep their sizes, and each has one gradient of the same size")
         if not self.m.is_cuda or set(map(T.get_device, tensors)) != {self.m.get_device()}:
             raise ValueError("parameters and gradients are on one CUDA device, the state's")
+        _on_current(self.m)
         if len(set(map(T.dtype.__get__, tensors))) != 1 or not all(map(T.is_contiguous, tensors)):
             raise ValueError("parameters, and gradients, are contiguous and of one dtype")
         return _dt(tensors[0])
@@ -274,6 +290,7 @@ class AdamW8:
 
     def moments(self, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """The values the codes of both moments stand for, as flat bf16 tensors (exact)."""
+        _on_current(self.m)
         n = self.m.numel()
         with _on(stream):
             m = torch.empty(n, dtype=torch.bfloat16, device=self.m.device)

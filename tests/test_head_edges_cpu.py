@@ -73,3 +73,39 @@ def test_second_derivatives_are_refused_not_wrong(plain):
         g, = torch.autograd.grad(loss, x, create_graph=True)
         with pytest.raises(RuntimeError):
             (g.square().sum() + x.sum()).backward()
+
+
+class _Gpu(torch.Tensor):
+    """A tensor that says it lives on a GPU (the one in .gpu)."""
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.gpu
+
+
+def _on_gpu(t, gpu):
+    t = t.as_subclass(_Gpu)
+    t.gpu = gpu
+    return t
+
+
+def test_tensors_of_another_gpu_are_refused(monkeypatch):
+    """Operands on two GPUs, or all on one that is not current, never reach the library."""
+    monkeypatch.setattr(head, "_current_device", lambda: 0)
+    monkeypatch.setattr(head, "load_library", lambda: pytest.fail("reached the library"))
+    f = {"x": torch.zeros(4, 8), "w": torch.zeros(8), "b": torch.zeros(8), "mean": torch.zeros(4), "rstd": torch.zeros(4),
+         "dy": torch.zeros(4, 8), "ws": torch.zeros(512, dtype=torch.uint8), "h": torch.zeros(4, 8), "v": torch.zeros(16, 8),
+         "labels": torch.zeros(4, dtype=torch.int64), "lse": torch.zeros(4), "row_grad": torch.zeros(4),
+         "stats": torch.zeros(2), "upstream": torch.zeros(1)}
+    calls = {
+        "x w b": lambda x, w, b: head.muon_layernorm_forward(x, w, b),
+        "dy x w mean rstd ws": lambda *a: head.muon_layernorm_backward(*a),
+        "h v labels": lambda *a: head.linear_ce_workspace_for(*a),
+        "h v labels ws": lambda *a: head.muon_linear_ce_forward(*a),
+        "h v labels lse ws row_grad stats upstream": lambda *a: head.muon_linear_ce_backward(*a),
+    }
+    for names, call in calls.items():
+        names = names.split()
+        for moved in [*[{n} for n in names], set(names)]:
+            with pytest.raises(ValueError, match="current CUDA device"):
+                call(*[_on_gpu(f[n].clone(), 1 if n in moved else 0) for n in names])
