@@ -49,8 +49,8 @@ class _LayerNorm(torch.autograd.Function):
         with torch.no_grad():
             ws = head.alloc_layernorm_workspace(*rows.shape, device=rows.device)
             dx, dw, db = head.muon_layernorm_backward(_plain_rows(dy), rows, weight, mean, rstd, ws,
-                                                      bias=ctx.bias_dtype is not None)
-            dx, db = dx.view(ctx.shape), None if db is None else db.to(ctx.bias_dtype)
+                                                      bias=ctx.bias_dtype or False)
+            dx = dx.view(ctx.shape)
         return *_once((dx, dw, db), (dy, x, weight)), None
 
 

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-from typing import Dict, List, Optional, Sequence, Tuple
+from typing import Dict, List, Optional, Sequence, Tuple, Union
 
 import numpy as np
 import torch
@@ -106,9 +106,11 @@ def alloc_layernorm_workspace(rows: int, dim: int, device=None) -> torch.Tensor:
 
 
 def muon_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
-                            rstd: torch.Tensor, ws: Optional[torch.Tensor] = None, bias: bool = True, stream=None):
+                            rstd: torch.Tensor, ws: Optional[torch.Tensor] = None,
+                            bias: Union[bool, torch.dtype] = True, stream=None):
     """Gradients of muon_layernorm_forward: (dx, dweight, dbias).  dweight is None without a
-    weight; dbias is None when bias is False."""
+    weight; dbias is None when bias is False.  Without a weight, bias may be the bias's dtype
+    (x's if it is True); with one it has the weight's."""
     px, ldx = _rows(x, "x")
     py, ldy = _rows(dy, "dy")
     n, d = x.shape
@@ -117,13 +119,16 @@ def muon_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[
     pw = _vector(weight, d, None, "weight")
     pm, pr = _vector(mean, n, torch.float32, "mean"), _vector(rstd, n, torch.float32, "rstd")
     _on_current(dy, x, weight, mean, rstd, ws)
-    wt = weight.dtype if weight is not None else x.dtype
+    wt = weight.dtype if weight is not None else bias if isinstance(bias, torch.dtype) else x.dtype
+    if isinstance(bias, torch.dtype) and bias != wt:
+        raise TypeError(f"bias must be {wt}")
     with _on(stream):
         dx = torch.empty((n, d), dtype=x.dtype, device=x.device)
         dw = torch.empty(d, dtype=wt, device=x.device) if weight is not None else None
         db = torch.empty(d, dtype=wt, device=x.device) if bias else None
     _check("muon_layernorm_backward", load_library().muon_layernorm_backward(
-        py, ldy, px, ldx, pw, pm, pr, n, d, _dt(x), _dt(weight if weight is not None else x), dx.data_ptr(), d,
+        py, ldy, px, ldx, pw, pm, pr, n, d, _dt(x), _dt(weight if weight is not None else db if db is not None else x),
+        dx.data_ptr(), d,
         None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), _lib._ptr(ws),
         0 if ws is None else ws.numel(), _stream(stream, x)))
     return dx, dw, db

@@ -128,6 +128,18 @@ def test_periodic_muon_refuses_before_it_changes_anything(bits):
     assert opt.step_count == 2 and not torch.equal(W[0], w)
 
 
+def test_layer_norm_bias_without_weight_has_its_own_precision():
+    rng = np.random.default_rng(3)
+    n, d = 777, 96
+    x, _ = put(rng.standard_normal((n, d)), "bf16")
+    dy, dy64 = put(rng.standard_normal((n, d)), "bf16")
+    b, _ = put(rng.standard_normal(d), "f32")
+    x.requires_grad_(), b.requires_grad_()
+    mm.layer_norm(x, None, b).backward(dy)
+    assert b.grad.dtype == torch.float32
+    within(num(b.grad), dy64.sum(0), (n + 8) * U * np.abs(dy64).sum(0), "db")
+
+
 def test_linear_ce_backward_long_sums():
     """dW over 2^22 rows whose products all have one sign: the tensor cores' truncation must
     not pile up.  W = 0, so every probability is 2^-8 exactly and dW[v] = 2^-8 sum_r h[r] for a
