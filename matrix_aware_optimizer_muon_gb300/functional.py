@@ -47,9 +47,11 @@ class _LayerNorm(torch.autograd.Function):
     def backward(ctx, dy):
         x, rows, weight, mean, rstd = ctx.saved_tensors
         with torch.no_grad():
-            ws = head.alloc_layernorm_workspace(*rows.shape, device=rows.device)
+            # column sums only for what is trained
+            want_w, want_b = ctx.needs_input_grad[1:3]
+            ws = head.alloc_layernorm_workspace(*rows.shape, device=rows.device) if want_w or want_b else None
             dx, dw, db = head.muon_layernorm_backward(_plain_rows(dy), rows, weight, mean, rstd, ws,
-                                                      bias=ctx.bias_dtype or False)
+                                                      bias=want_b and ctx.bias_dtype, weight_grad=want_w)
             dx = dx.view(ctx.shape)
         return *_once((dx, dw, db), (dy, x, weight)), None
 

@@ -107,9 +107,9 @@ def alloc_layernorm_workspace(rows: int, dim: int, device=None) -> torch.Tensor:
 
 def muon_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
                             rstd: torch.Tensor, ws: Optional[torch.Tensor] = None,
-                            bias: Union[bool, torch.dtype] = True, stream=None):
+                            bias: Union[bool, torch.dtype] = True, stream=None, weight_grad: bool = True):
     """Gradients of muon_layernorm_forward: (dx, dweight, dbias).  dweight is None without a
-    weight; dbias is None when bias is False.  Without a weight, bias may be the bias's dtype
+    weight or weight_grad, dbias when bias is False; with neither no workspace is needed.  Without a weight, bias may be the bias's dtype
     (x's if it is True); with one it has the weight's."""
     px, ldx = _rows(x, "x")
     py, ldy = _rows(dy, "dy")
@@ -124,7 +124,7 @@ def muon_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[
         raise TypeError(f"bias must be {wt}")
     with _on(stream):
         dx = torch.empty((n, d), dtype=x.dtype, device=x.device)
-        dw = torch.empty(d, dtype=wt, device=x.device) if weight is not None else None
+        dw = torch.empty(d, dtype=wt, device=x.device) if weight is not None and weight_grad else None
         db = torch.empty(d, dtype=wt, device=x.device) if bias else None
     _check("muon_layernorm_backward", load_library().muon_layernorm_backward(
         py, ldy, px, ldx, pw, pm, pr, n, d, _dt(x), _dt(weight if weight is not None else db if db is not None else x),

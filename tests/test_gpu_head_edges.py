@@ -140,6 +140,27 @@ def test_layer_norm_bias_without_weight_has_its_own_precision():
     within(num(b.grad), dy64.sum(0), (n + 8) * U * np.abs(dy64).sum(0), "db")
 
 
+@pytest.mark.parametrize("train", [(True, False, False), (True, True, False), (True, False, True), (False, True, True)])
+def test_layer_norm_of_frozen_parameters(train):
+    """Column sums are left out where no gradient is wanted; the other gradients keep their bits."""
+    rng = np.random.default_rng(5)
+    n, d = 500, 200
+    vals = [rng.standard_normal(s) for s in ((n, d), d, d)]
+    dy, _ = put(rng.standard_normal((n, d)), "f32")
+
+    def grads(flags):
+        t = [put(a, "f32")[0].requires_grad_(f) for a, f in zip(vals, flags)]
+        mm.layer_norm(*t).backward(dy)
+        return [x.grad for x in t]
+
+    for got, want, f in zip(grads(train), grads((True, True, True)), train):
+        assert (got is None) == (not f) and (got is None or torch.equal(got, want))
+    x, w = put(vals[0], "f32")[0], put(vals[1], "f32")[0]
+    _, mean, rstd = mm.muon_layernorm_forward(x, w)
+    dx, dw, db = mm.muon_layernorm_backward(dy, x, w, mean, rstd, bias=False, weight_grad=False)
+    assert dw is None and db is None and mm.muon_launch_count() == 1
+
+
 def test_linear_ce_backward_long_sums():
     """dW over 2^22 rows whose products all have one sign: the tensor cores' truncation must
     not pile up.  W = 0, so every probability is 2^-8 exactly and dW[v] = 2^-8 sum_r h[r] for a

@@ -14,11 +14,11 @@ def _ln_forward(x, weight=None, bias=None, eps=1e-5, stream=None):
     return (y if bias is None else y + bias.float()).to(x.dtype), mean, rstd
 
 
-def _ln_backward(dy, x, weight, mean, rstd, ws=None, bias=True, stream=None):
+def _ln_backward(dy, x, weight, mean, rstd, ws=None, bias=True, stream=None, weight_grad=True):
     xh = (x.float() - mean[:, None]) * rstd[:, None]
     g = dy.float() if weight is None else dy.float() * weight.float()
     dx = rstd[:, None] * (g - g.mean(1, keepdim=True) - xh * (g * xh).mean(1, keepdim=True))
-    return (dx.to(x.dtype), None if weight is None else (dy.float() * xh).sum(0).to(weight.dtype),
+    return (dx.to(x.dtype), None if weight is None or not weight_grad else (dy.float() * xh).sum(0).to(weight.dtype),
             dy.float().sum(0) if bias else None)
 
 
@@ -63,6 +63,20 @@ def test_first_derivatives_are_the_formulas(plain):
     y = torch.nn.functional.layer_norm(x, (24,), w, b)
     want = torch.autograd.grad(torch.nn.functional.cross_entropy(y @ v.T, labels), (x, w, b, v))
     assert all(torch.allclose(p, q, atol=1e-5) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("train", [(True, False, False), (True, True, False), (True, False, True), (False, True, True)])
+def test_layer_norm_sums_columns_only_for_what_is_trained(plain, train):
+    torch.manual_seed(0)
+    t = [torch.randn(s, requires_grad=r) for s, r in zip(((6, 24), (24,), (24,)), train)]
+    functional.layer_norm(*t).square().sum().backward()
+    name, asked = plain[-1]
+    assert name == "muon_layernorm_backward" and bool(asked["weight_grad"]) == train[1] and bool(asked["bias"]) == train[2]
+    got = [x.grad for x in t]
+    t = [x.detach().requires_grad_(r) for x, r in zip(t, train)]
+    torch.nn.functional.layer_norm(t[0], (24,), t[1], t[2]).square().sum().backward()
+    for g, x in zip(got, t):
+        assert (g is None) == (x.grad is None) and (g is None or torch.allclose(g, x.grad, atol=1e-4))
 
 
 def test_second_derivatives_are_refused_not_wrong(plain):
