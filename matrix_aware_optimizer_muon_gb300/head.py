@@ -236,7 +236,9 @@ _PARAM8 = np.dtype([("P", "u8"), ("G", "u8"), ("m", "u8"), ("v", "u8"), ("m_scal
 class AdamW8:
     """AdamW over a list of parameters, both moments in 8 bits (see muon_adamw8_step in
     include/muon.h for the format).  The state is four flat byte buffers, 2 + 2/128 bytes a
-    parameter; parameter i's codes start at self.starts[i], a multiple of 128."""
+    parameter; parameter i's codes start at self.starts[i], a multiple of 128.  Parameters may be
+    of two dtypes (a bf16 matrix beside fp32 norms): those of one dtype stay of one dtype, and
+    so do their gradients; each dtype is one launch."""
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-4, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.0, seed: int = 0):
@@ -252,40 +254,58 @@ class AdamW8:
         self.m_scale, self.v_scale = (torch.zeros(total // ADAMW8_BLOCK, dtype=torch.uint8, device=dev) for _ in range(2))
         self._state = (self.m.data_ptr(), self.m_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr())
         self.step_count = 0
+        # the array's entries, parameters of one dtype next to each other
+        kinds = [p.dtype for p in self.params]
+        self._order = [i for k in dict.fromkeys(kinds) for i in range(len(kinds)) if kinds[i] == k]
+        ends = np.cumsum([kinds.count(k) for k in dict.fromkeys(kinds)]).tolist()
+        self._groups = list(zip([0, *ends], ends))
         self._arr = np.zeros(len(self.params), dtype=_PARAM8)
-        at = np.array(self.starts[:-1], dtype=np.int64)
+        at = np.array(self.starts[:-1], dtype=np.int64)[self._order]
         self._arr["m"], self._arr["v"] = self.m.data_ptr() + at, self.v.data_ptr() + at
         self._arr["m_scale"] = self.m_scale.data_ptr() + at // ADAMW8_BLOCK
         self._arr["v_scale"] = self.v_scale.data_ptr() + at // ADAMW8_BLOCK
-        self._arr["numel"], self._arr["first"] = self.numels, at
-        self._addr = self._arr.ctypes.data
+        self._arr["numel"], self._arr["first"] = [self.numels[i] for i in self._order], at
+        self._addr, self._dtypes = self._arr.ctypes.data, None
         self._check(self.params)
 
-    def _check(self, tensors: Sequence[torch.Tensor]) -> int:
-        """Refuses what the kernel cannot read; returns the tensors' dtype.  One pass of a C
-        function over the list for each property: 9 us for 48 tensors."""
+    def _check(self, tensors: Sequence[torch.Tensor]) -> Tuple[Sequence[torch.Tensor], List[int]]:
+        """Refuses what the kernel cannot read; returns the tensors in the array's order and each
+        group's dtype.  One pass of a C function over the list for each property: 9 us for 48
+        tensors."""
         T = torch.Tensor
         if list(map(T.numel, tensors)) != self.numels:
             raise ValueError("parameters keep their sizes, and each has one gradient of the same size")
         if not self.m.is_cuda or set(map(T.get_device, tensors)) != {self.m.get_device()}:
             raise ValueError("parameters and gradients are on one CUDA device, the state's")
         _on_current(self.m)
-        if len(set(map(T.dtype.__get__, tensors))) != 1 or not all(map(T.is_contiguous, tensors)):
-            raise ValueError("parameters, and gradients, are contiguous and of one dtype")
-        return _dt(tensors[0])
+        if len(self._groups) == 1:
+            one = len(set(map(T.dtype.__get__, tensors))) == 1
+        else:
+            tensors = [tensors[i] for i in self._order]
+            one = all(len(set(map(T.dtype.__get__, tensors[a:b]))) == 1 for a, b in self._groups)
+        if not one or not all(map(T.is_contiguous, tensors)):
+            raise ValueError("parameters of one dtype, and their gradients, are contiguous and of one dtype")
+        return tensors, [_dt(tensors[a]) for a, _ in self._groups]
 
     def _point(self, grads: Sequence[torch.Tensor]) -> None:
         """Checks and enters the tensors of a step."""
         arr = self._arr
         # the parameters too: a model may have been cast or moved since the last step
-        arr["p_dtype"], arr["g_dtype"] = self._check(self.params), self._check(grads)
+        params, p_dts = self._check(self.params)
+        grads, g_dts = self._check(grads)
+        if self._dtypes != (p_dts, g_dts):
+            for (a, b), p_dt, g_dt in zip(self._groups, p_dts, g_dts):
+                arr["p_dtype"][a:b], arr["g_dtype"][a:b] = p_dt, g_dt
+            self._dtypes = p_dts, g_dts
         arr["G"] = list(map(torch.Tensor.data_ptr, grads))
-        arr["P"] = list(map(torch.Tensor.data_ptr, self.params))
+        arr["P"] = list(map(torch.Tensor.data_ptr, params))
 
     def _launch(self, stream) -> None:
-        _check("muon_adamw8_step", load_library().muon_adamw8_step(
-            self._addr, len(self._arr), self.step_count + 1, self.lr, self.betas[0], self.betas[1], self.eps,
-            self.weight_decay, self.seed, _stream(stream, self.m)))
+        lib, handle = load_library(), _stream(stream, self.m)
+        for a, b in self._groups:
+            _check("muon_adamw8_step", lib.muon_adamw8_step(
+                self._addr + a * _PARAM8.itemsize, b - a, self.step_count + 1, self.lr, self.betas[0], self.betas[1],
+                self.eps, self.weight_decay, self.seed, handle))
         self.step_count += 1
 
     def step(self, grads: Sequence[torch.Tensor], stream=None) -> None:

@@ -161,6 +161,50 @@ def test_layer_norm_of_frozen_parameters(train):
     assert dw is None and db is None and mm.muon_launch_count() == 1
 
 
+def test_adamw8_parameters_of_two_types():
+    """A bf16 matrix beside fp32 vectors: each gets, bit for bit, what it gets among its like."""
+    rng = np.random.default_rng(8)
+    sizes, kinds = [5000, 300, 129, 700], ["bf16", "f32", "bf16", "f32"]
+    vals = [rng.standard_normal(k) * 0.02 for k in sizes]
+    grads = [[rng.standard_normal(k) * 1e-3 for k in sizes] for _ in range(3)]
+
+    def run(types, gtypes, resume_at=None):
+        P = [put(x, t)[0] for x, t in zip(vals, types)]
+        opt = mm.AdamW8(P, lr=1e-2, weight_decay=0.1, seed=3)
+        for s, g in enumerate(grads):
+            if s == resume_at:
+                sd = opt.state_dict()
+                opt = mm.AdamW8(P, lr=1e-2, weight_decay=0.1)
+                opt.load_state_dict(sd)
+            opt.step([put(x, t)[0] for x, t in zip(g, gtypes)])
+        return P, opt.moments()
+
+    P, (m, v) = run(kinds, kinds)
+    R, (mr, vr) = run(kinds, kinds, resume_at=2)
+    assert all(torch.equal(p, r) for p, r in zip(P, R)) and torch.equal(m, mr) and torch.equal(v, vr)
+    at = 0
+    starts = mm.AdamW8([torch.zeros(k, device=dev()) for k in sizes]).starts
+    for kind in ("bf16", "f32"):
+        Q, (mq, vq) = run([kind] * 4, [kind] * 4)
+        for i in range(4):
+            if kinds[i] == kind:
+                s = slice(starts[i], starts[i + 1])
+                assert torch.equal(P[i], Q[i]) and torch.equal(m[s], mq[s]) and torch.equal(v[s], vq[s])
+                at += 1
+    assert at == 4
+    # one type for gradients of one type of parameters
+    opt = mm.AdamW8([put(x, t)[0] for x, t in zip(vals, kinds)])
+    with pytest.raises(ValueError):
+        opt.step([put(x, t)[0] for x, t in zip(grads[0], ["bf16", "f32", "f32", "f32"])])
+    assert opt.step_count == 0
+    W = [torch.randn(64, 96, device=dev()).bfloat16()]
+    A = [put(x, t)[0] for x, t in zip(vals, kinds)]
+    both = mm.PeriodicMuon(W, aux_params=A, aux_bits=8)
+    before = [a.clone() for a in A]
+    both.step([torch.randn_like(W[0])], [put(x, t)[0] for x, t in zip(grads[0], kinds)])
+    assert all(not torch.equal(a, b) for a, b in zip(A, before))
+
+
 def test_linear_ce_backward_long_sums():
     """dW over 2^22 rows whose products all have one sign: the tensor cores' truncation must
     not pile up.  W = 0, so every probability is 2^-8 exactly and dW[v] = 2^-8 sum_r h[r] for a
