@@ -411,13 +411,17 @@ int muon_abi_version(void);
  * MUON_DEBUG_NO_OVERLAP runs the wide-row and tall-column kernels of a RowNorm
  * step one after the other on the caller's stream instead of side by side.
  * MUON_DEBUG_NO_PAIR runs the tensor-core Newton-Schulz GEMMs with one CTA per
- * 128 x 256 tile instead of 2-CTA clusters (tcgen05 cta_group::2) on 256 x 256 tiles. */
+ * 128 x 256 tile instead of 2-CTA clusters (tcgen05 cta_group::2) on 256 x 256 tiles.
+ * MUON_DEBUG_CE_PIECE times n (1 .. 255) cuts the vocabulary of the linear cross entropy's
+ * backward pass into pieces of 256 n columns, in the workspace's size and in the call, so
+ * that small cases have several. */
 enum {
   MUON_DEBUG_STALL_PRODUCER = 1,
   MUON_DEBUG_NO_CLUSTER = 2,
   MUON_DEBUG_NO_OVERLAP = 4,
   MUON_DEBUG_TALL_CLUSTER = 8,
-  MUON_DEBUG_NO_PAIR = 16
+  MUON_DEBUG_NO_PAIR = 16,
+  MUON_DEBUG_CE_PIECE = 256
 };
 int muon_debug_set(int flags, int timeout_ms);
 

@@ -37,6 +37,7 @@ MUON_DEBUG_NO_CLUSTER = 2
 MUON_DEBUG_NO_OVERLAP = 4
 MUON_DEBUG_TALL_CLUSTER = 8
 MUON_DEBUG_NO_PAIR = 16
+MUON_DEBUG_CE_PIECE = 256
 
 _NS5_MODES = {"bf16": MUON_NS5_BF16, "f32": MUON_NS5_F32}
 

@@ -332,6 +332,7 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P) {
   at = common;
   const int64_t want = G_BYTES / (2 * P->parts * std::max<int64_t>(a->rows, 1));
   P->piece = std::min(std::max(want / TILE * TILE, MIN_PIECE), cdiv(a->vocab, TILE) * TILE);
+  if (const int tiles = (test_flags() / MUON_DEBUG_CE_PIECE) & 255) P->piece = std::min<int64_t>(P->piece, (int64_t)tiles * TILE);
   // pieces of one size, as far as tiles allow
   P->npieces = cdiv(a->vocab, P->piece);
   P->piece = cdiv(cdiv(a->vocab, P->npieces), TILE) * TILE;

@@ -292,3 +292,126 @@ def test_second_derivatives_are_refused():
     g, = torch.autograd.grad(mm.linear_cross_entropy(x, v, labels), x, create_graph=True)
     with pytest.raises(RuntimeError):
         (g.square().sum() + x.sum()).backward()
+
+
+def pieces_of(v, columns):
+    """The pieces that so many columns a piece make of v entries: of one size, as far as tiles of 256 allow."""
+    n = -(-v // columns)
+    size = -(-(-(-v // n)) // 256) * 256
+    return -(-v // size)
+
+
+PIECE_SIZES = [(1, 3000, 40), (5, 3111, 65), (64, 3001, 257), (129, 3300, 96), (257, 4001, 200), (300, 3107, 321), (700, 5050, 130),
+               (1000, 3000, 32)]
+
+
+@pytest.mark.parametrize("columns", [256, 512])
+@pytest.mark.parametrize("size", PIECE_SIZES)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_linear_ce_backward_in_pieces(dt, size, columns):
+    """Six pieces of the vocabulary or more, the last one short: g in two buffers in turn, dH's
+    running sums over them, offsets into W, labels of other pieces, launches of all three
+    products, dH's ranges of K (few rows) and none."""
+    n, v, d = size
+    npieces = pieces_of(v, columns)
+    assert npieces >= 6
+    h, h64, w, w64, labels, lab = ce_case(n, v, d, dt, n + v + d)
+    plain = mm.alloc_linear_ce_workspace(n, v, d, TYPES[dt])
+    _, lse, stats = mm.muon_linear_ce_forward(h, w, labels, plain)
+    rg, rg64 = put(np.random.default_rng(3).random(n), "f32")
+    whole = mm.muon_linear_ce_backward(h, w, labels, lse, plain, row_grad=rg)
+    mm.muon_debug_set(mm.MUON_DEBUG_CE_PIECE * (columns // 256), 0)
+    try:
+        ws = mm.alloc_linear_ce_workspace(n, v, d, TYPES[dt])
+        ws[256:].fill_(255)                       # NaN in every sum that is not written first
+        dh, dw = mm.muon_linear_ce_backward(h, w, labels, lse, ws, row_grad=rg)
+        # a launch a piece and one more, the operands' copies and the last kernel
+        assert npieces + 2 <= mm.muon_launch_count() <= npieces + 4
+        assert mm.muon_check_status(ws) == mm.MUON_OK
+        again = mm.muon_linear_ce_backward(h, w, labels, lse, ws, row_grad=rg)
+        only = (mm.muon_linear_ce_backward(h, w, labels, lse, ws, row_grad=rg, need_dw=False)[0],
+                mm.muon_linear_ce_backward(h, w, labels, lse, ws, row_grad=rg, need_dh=False)[1])
+        mean = mm.muon_linear_ce_backward(h, w, labels, lse, ws, stats=stats, grad_scale=3.0)
+        assert mm.muon_check_status(ws) == mm.MUON_OK
+    finally:
+        mm.muon_debug_set(0, 0)
+    assert torch.equal(dw, whole[1])              # a column's sum over rows does not depend on the pieces
+    assert all(torch.equal(p, q) for p, q in zip((dh, dw), again)) and all(torch.equal(p, q) for p, q in zip((dh, dw), only))
+    lse64, z = num(lse), h64 @ w64.T
+    ez = ce_tolerances(h64, w64, dt)
+    spread = np.abs(z).max(1) + 1
+    count = max((lab != -100).sum(), 1)
+    for got, coef in (((dh, dw), rg64), (mean, np.full(n, 3.0 / count))):
+        g = ref.linear_ce_logit_grad(h64, w64, lab, lse64, coef)
+        counted = (lab != -100) * coef
+        eg = counted[:, None] * np.exp(z - lse64[:, None]) * (ez + (16 + 4 * spread) * U)[:, None] + 8 * U * np.abs(g) + \
+            4 * U * counted[:, None]
+        parts, one = (1, BF) if dt == "bf16" else (4, 0.0)
+        if dt == "bf16":
+            eg = eg + BF * (np.abs(g) + eg)
+        # an fp32 addition a piece on top of a whole vocabulary's sum
+        edh = eg @ np.abs(w64) + parts * (v / 16 + 64 + npieces) * 2 * U * (np.abs(g) @ np.abs(w64))
+        edw = eg.T @ np.abs(h64) + parts * (n / 16 + 64) * 2 * U * (np.abs(g).T @ np.abs(h64))
+        within(num(got[0]), g @ w64, edh + one * (np.abs(g @ w64) + edh) + 1e-30, "dh")
+        within(num(got[1]), g.T @ h64, edw + one * (np.abs(g.T @ h64) + edw) + 1e-30, "dw")
+        assert not got[0][labels == -100].any()
+
+
+def test_linear_ce_backward_in_pieces_on_their_own():
+    """The pieces of 268 million logits that a larger case makes without any flag."""
+    n, v, d = 4096, 131073, 48
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(5)
+    w = (torch.randn(v, d, generator=gen, device=dev()) * 2 / d ** 0.5).bfloat16()
+    labels = torch.randint(0, v, (n,), generator=gen, device=dev())
+    h = (torch.randn(n, d, generator=gen, device=dev()) + w[labels].float()).bfloat16()
+    labels[::7] = -100
+    ws = mm.alloc_linear_ce_workspace(n, v, d)
+    _, lse, stats = mm.muon_linear_ce_forward(h, w, labels, ws)
+    got = mm.muon_linear_ce_backward(h, w, labels, lse, ws, stats=stats)
+    # H's copy, a launch a piece and one more, the last kernel
+    assert mm.muon_launch_count() == pieces_of(v, 65536) + 3 and mm.muon_check_status(ws) == mm.MUON_OK
+    check_ce_backward_on_gpu(h, w, labels, lse, got)
+
+
+def test_linear_ce_backward_more_tiles_than_the_table_holds():
+    """A launch of two products whose 13282 and more tiles go round robin."""
+    n, v, d = 8, 1_700_003, 512
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(6)
+    w = (torch.randn(v, d, generator=gen, device=dev()) * 2 / d ** 0.5).bfloat16()
+    labels = torch.randint(0, v, (n,), generator=gen, device=dev())
+    h = (torch.randn(n, d, generator=gen, device=dev()) + 2 * w[labels].float()).bfloat16()
+    labels[3] = -100
+    ws = mm.alloc_linear_ce_workspace(n, v, d)
+    _, lse, stats = mm.muon_linear_ce_forward(h, w, labels, ws)
+    got = mm.muon_linear_ce_backward(h, w, labels, lse, ws, stats=stats)
+    assert mm.muon_check_status(ws) == mm.MUON_OK
+    check_ce_backward_on_gpu(h, w, labels, lse, got)
+
+
+def check_ce_backward_on_gpu(h, w, labels, lse, got):
+    """The mean loss's gradients against 64 bits on the GPU, bf16, the vocabulary in slices."""
+    h64, live = h.double(), (labels != -100).double()
+    n, v, c = h.shape[0], w.shape[0], live / live.sum()
+    dh, edh = torch.zeros_like(h64), torch.zeros_like(h64)
+    at = torch.arange(n, device=h.device)
+    step = (1 << 27) // n
+    for a in range(0, v, step):
+        wp = w[a:a + step].double()
+        z = h64 @ wp.T
+        p = torch.exp(z - lse.double()[:, None])
+        here = (labels >= a) & (labels < a + step)
+        g = p.clone()
+        g[at[here], labels[here] - a] -= 1
+        g *= c[:, None]
+        ez = (h.shape[1] / 16 + 16) * 2 * U * (h64.abs() @ wp.abs().T)
+        eg = c[:, None] * p * (ez + (20 + 4 * z.abs()) * U) + 8 * U * g.abs() + 4 * U * c[:, None]
+        eg += BF * (g.abs() + eg)
+        dh += g @ wp
+        edh += eg @ wp.abs() + (v / 16 + 64) * 2 * U * (g.abs() @ wp.abs())
+        dw, edw = g.T @ h64, eg.T @ h64.abs() + (n / 16 + 64) * 2 * U * (g.abs().T @ h64.abs())
+        bad = (got[1][a:a + step].double() - dw).abs() > edw + BF * (dw.abs() + edw) + 1e-30
+        assert not bad.any(), ("dw", a, int(bad.sum()))
+    bad = (got[0].double() - dh).abs() > edh + BF * (dh.abs() + edh) + 1e-30
+    assert not bad.any(), ("dh", int(bad.sum()))
