@@ -415,3 +415,66 @@ def check_ce_backward_on_gpu(h, w, labels, lse, got):
         assert not bad.any(), ("dw", a, int(bad.sum()))
     bad = (got[0].double() - dh).abs() > edh + BF * (dh.abs() + edh) + 1e-30
     assert not bad.any(), ("dh", int(bad.sum()))
+
+
+ROW_CASES = [(6000, 1536, "bf16", 0), (6000, 1544, "bf16", 0), (5000, 1540, "f32", 0), (5003, 1537, "f32", 3),
+             (6001, 1537, "bf16", 1), (2000, 8192, "bf16", 0), (1500, 8192, "f32", 0), (9000, 520, "bf16", 8), (9000, 1000, "f32", 0),
+             (12000, 300, "f32", 5), (2500, 5001, "bf16", 0), (600, 12288, "bf16", 0), (500, 9001, "f32", 1)]
+
+
+@pytest.mark.parametrize("n,d,xdt,pad", ROW_CASES)
+def test_layernorm_backward_many_rows_a_group(n, d, xdt, pad):
+    """Eight rows or more through each of the backward pass's row groups: its ring of copies
+    wraps, the barriers' buffers alternate, sums run on."""
+    rng = np.random.default_rng(n + d)
+    x, x64 = put(rng.standard_normal((n, d)) * 2 + 0.5, xdt)
+    dy, dy64 = put(rng.standard_normal((n, d)), xdt)
+    w, w64 = put(1 + 0.3 * rng.standard_normal(d), "f32")
+    xs, dys = strided(x, pad), strided(dy, pad)
+    y, mean, rstd = mm.muon_layernorm_forward(xs, w, w)
+    ws = mm.alloc_layernorm_workspace(n, d)
+    dx, dw, db = mm.muon_layernorm_backward(dys, xs, w, mean, rstd, ws)
+    ws.fill_(255)
+    again = mm.muon_layernorm_backward(dys, xs, w, mean, rstd, ws)
+    assert all(torch.equal(a, b) for a, b in zip((dx, dw, db), again))
+    check_layernorm(xdt, n, d, x64, dy64, w64, w64, (y, mean, rstd), (dx, dw, db))
+
+
+@pytest.mark.parametrize("off", [1, 2, 3, 5])
+@pytest.mark.parametrize("xdt", ["bf16", "f32"])
+def test_layernorm_unaligned_views_to_their_own_precision(xdt, off):
+    rng = np.random.default_rng(off)
+    n, d = 9, 1536
+    flat, f64 = put(rng.standard_normal(off + n * d) * 2 + 0.5, xdt)
+    dflat, d64 = put(rng.standard_normal(off + n * d), xdt)
+    wf, wf64 = put(1 + 0.3 * rng.standard_normal(off + d), "f32")
+    x, dy, w = flat[off:].view(n, d), dflat[off:].view(n, d), wf[off:]
+    y, mean, rstd = mm.muon_layernorm_forward(x, w, w)
+    got = mm.muon_layernorm_backward(dy, x, w, mean, rstd, mm.alloc_layernorm_workspace(n, d))
+    check_layernorm(xdt, n, d, f64[off:].reshape(n, d), d64[off:].reshape(n, d), wf64[off:], wf64[off:], (y, mean, rstd), got)
+
+
+def check_layernorm(xdt, n, d, x64, dy64, w64, b64, forward, backward):
+    """test_layernorm's bounds, with an fp32 weight and bias."""
+    (y, mean, rstd), (dx, dw, db) = forward, backward
+    gam, one = (d / 32 + 32) * U, BF if xdt == "bf16" else 0.0
+    ry, rmean, rrstd = ref.layernorm_forward(x64, w64, b64, 1e-5)
+    emean = gam * np.abs(x64).mean(1) + U * np.abs(rmean)
+    within(num(mean), rmean, emean, "mean")
+    cen = np.abs(x64 - rmean[:, None])
+    ev = (2 * (emean[:, None] + U * cen) * cen).mean(1) + emean ** 2 + gam * (cen ** 2).mean(1)
+    er = rrstd * (0.5 * ev * rrstd ** 2 + 8 * U)
+    within(num(rstd), rrstd, er, "rstd")
+    exh = (emean[:, None] + U * cen) * rrstd[:, None] + cen * er[:, None]
+    ey = exh * np.abs(w64) + 4 * U * (np.abs(ry) + cen * rrstd[:, None] * np.abs(w64)) + one * np.abs(ry)
+    within(num(y), ry, ey * 1.01 + 1e-30, "y")
+    m64, r64 = num(mean), num(rstd)
+    rdx, rdw, rdb = ref.layernorm_backward(dy64, x64, w64, m64, r64)
+    xh, g = (x64 - m64[:, None]) * r64[:, None], dy64 * w64
+    eg, exh = 2 * U * np.abs(g), 3 * U * np.abs(xh)
+    c1, c2 = np.abs(g).mean(1, keepdims=True), np.abs(g * xh).mean(1, keepdims=True)
+    edx = r64[:, None] * (eg + (gam + 4 * U) * c1 + np.abs(xh) * (gam + 8 * U) * c2 + exh * c2 +
+                          4 * U * (np.abs(g) + c1 + np.abs(xh) * c2)) + one * np.abs(rdx)
+    within(num(dx), rdx, edx * 1.01 + 1e-30, "dx")
+    within(num(dw), rdw, (n + 8) * U * np.abs(dy64 * xh).sum(0) + 1e-30, "dw")
+    within(num(db), rdb, (n + 8) * U * np.abs(dy64).sum(0) + 1e-30, "db")
