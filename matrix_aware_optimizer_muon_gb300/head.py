@@ -328,11 +328,14 @@ class AdamW8:
         return {"step": self.step_count, "seed": self.seed, "m": self.m.clone(), "v": self.v.clone(),
                 "m_scale": self.m_scale.clone(), "v_scale": self.v_scale.clone()}
 
-    def load_state_dict(self, sd: Dict) -> None:
-        mine = (self.m, self.v, self.m_scale, self.v_scale)
-        theirs = [sd[k] for k in ("m", "v", "m_scale", "v_scale")]
-        if any(a.shape != b.shape or b.dtype != torch.uint8 for a, b in zip(mine, theirs)):
+    def _saved(self, sd: Dict):
+        """(mine, saved) for each buffer of a state, checked."""
+        pairs = list(zip((self.m, self.v, self.m_scale, self.v_scale), [sd[k] for k in ("m", "v", "m_scale", "v_scale")]))
+        if any(a.shape != b.shape or b.dtype != torch.uint8 for a, b in pairs):
             raise ValueError("state was saved for other parameters")
-        for a, b in zip(mine, theirs):
+        return pairs
+
+    def load_state_dict(self, sd: Dict) -> None:
+        for a, b in self._saved(sd):
             a.copy_(b)
         self.step_count, self.seed = int(sd["step"]), int(sd["seed"])

@@ -105,9 +105,12 @@ class PeriodicMuon:
             raise ValueError("state has a different number of auxiliary parameters")
         if (sd.get("aux8") is None) != (self.aux8 is None):
             raise ValueError("state was saved with another aux_bits")
-        for dst, src in zip(self.M + self.aux_m + self.aux_v, list(sd["M"]) + list(aux_m) + list(aux_v)):
-            if tuple(dst.shape) != tuple(src.shape):
-                raise ValueError("state shape mismatch")
+        pairs = list(zip(self.M + self.aux_m + self.aux_v, list(sd["M"]) + list(aux_m) + list(aux_v)))
+        if any(tuple(dst.shape) != tuple(src.shape) for dst, src in pairs):
+            raise ValueError("state shape mismatch")
+        if self.aux8 is not None:   # refused before anything is copied
+            self.aux8._saved(sd["aux8"])
+        for dst, src in pairs:
             dst.copy_(src)
         if self.aux8 is not None:
             self.aux8.load_state_dict(sd["aux8"])

@@ -128,6 +128,19 @@ def test_periodic_muon_refuses_before_it_changes_anything(bits):
     assert opt.step_count == 2 and not torch.equal(W[0], w)
 
 
+def test_periodic_muon_refuses_a_state_before_it_copies_any():
+    def make(rows, k):
+        return mm.PeriodicMuon([torch.ones(rows, 96, device=dev()).bfloat16()], aux_params=[torch.ones(k, device=dev())], aux_bits=8)
+
+    opt = make(64, 300)
+    opt.step([torch.ones(64, 96, device=dev()).bfloat16()], [torch.ones(300, device=dev())])
+    m, codes = opt.M[0].clone(), opt.aux8.m.clone()
+    for other in (make(64, 700), make(65, 300)):
+        with pytest.raises(ValueError):
+            opt.load_state_dict(other.state_dict())
+        assert torch.equal(opt.M[0], m) and torch.equal(opt.aux8.m, codes) and opt.step_count == 1
+
+
 def test_layer_norm_bias_without_weight_has_its_own_precision():
     rng = np.random.default_rng(3)
     n, d = 777, 96
