@@ -40,7 +40,9 @@ def _on(stream):
     """Outputs are allocated on the stream they are written on."""
     if stream is None:
         return _here
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    if not isinstance(stream, torch.cuda.Stream):   # a handle; ExternalStream(0) would be a new stream
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _stream(stream, t: torch.Tensor) -> int:

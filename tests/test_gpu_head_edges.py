@@ -98,6 +98,23 @@ def test_periodic_muon_copies_gradients_on_the_stream_that_reads_them(bits):
     assert all(torch.equal(a, b) for a, b in zip(run(None), run(torch.cuda.Stream())))
 
 
+def test_streams_given_as_handles():
+    """0 is the default stream, any other number the stream it is the handle of: outputs and
+    copies are made on the very stream the kernels run on."""
+    from matrix_aware_optimizer_muon_gb300 import head
+    side = torch.cuda.Stream()
+    for stream, handle in ((0, 0), (side.cuda_stream, side.cuda_stream), (side, side.cuda_stream), (torch.cuda.default_stream(), 0)):
+        with torch.cuda.stream(torch.cuda.Stream()), head._on(stream):
+            assert torch.cuda.current_stream().cuda_stream == handle
+    x = torch.randn(50, 64, device=dev())
+    want = mm.muon_layernorm_forward(x)
+    torch.cuda.synchronize()
+    for stream in (0, side.cuda_stream):
+        got = mm.muon_layernorm_forward(x, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 @pytest.mark.parametrize("bits", [8, 32])
 def test_periodic_muon_refuses_before_it_changes_anything(bits):
     W = [torch.randn(64, 96, device=dev()).bfloat16()]
