@@ -9,7 +9,9 @@
 //
 // Measured: 335.5 M bf16 parameters and gradients, step 575 us (5.9 TB/s, 86% of a copy's
 // rate; three quarters of the issue slots) and unpacking 289 us (7.0 TB/s); 38.6 M fp32
-// parameters with bf16 gradients 88 us (6.2 TB/s) and 37 us.
+// parameters with bf16 gradients 88 us (6.2 TB/s) and 37 us.  A warp with a code 0 or a
+// number below its block's least takes the plain functions: 654 us where 3e-4 of the first
+// moments are 0 (gradients that change sign), 1010 us where all are (rows no token touched).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>

@@ -30,14 +30,20 @@
 // 32-bit operands come as three bf16 parts (24 bits of mantissa); the six products of
 // parts down to 2^-16 of the leading one are summed, smallest first.
 //
-// Measured (8192 rows, 2560 wide, 131072 entries, bf16, in loops of 0.1 to 0.3 s): forward
-// 3.16 to 3.34 ms (1.65 to 1.74 PFLOP/s), backward 9.9 to 11.1 ms (1.49 to 1.66); the
-// library's product of the same operands alone takes 2.65 to 2.93 ms.  The tensor pipe is
+// Measured (8192 rows, 2560 wide, 131072 entries, bf16, in loops of 0.1 to 0.3 s, several
+// GPUs): forward 3.16 to 3.45 ms (1.59 to 1.74 PFLOP/s), backward 9.9 to 11.1 ms (1.49 to
+// 1.66).  In turn on one GPU the forward pass took 3.21, 3.36 and 3.45 ms and the library's
+// product of the same operands, which writes the logits, 2.98, 3.16 and 3.11.  The tensor pipe is
 // busy 78% (forward), 79% (g) and 89% (the products with g) of the time in single launches,
 // at 1.65 to 1.8 GHz; in loops the 1.4 kW power cap sets the clock.  Without its
 // exponentials the forward pass takes 4% less; waits that suspend the thread for longer, and
 // sharing an operand among clusters of four CTAs, change nothing.
 // 8 rows read the vocabulary matrix at 5.9 TB/s after some 11 us of launches and set-up.
+//
+// Exponentials are __expf: off by 2 ulp near 0 and by 1.2 |x| ulp further down, where they
+// count less (x <= 0; at -16 they are 1e-7 of the largest and 1.2e-6 of that off).  A row's sum is
+// within some 1e-7 of itself by them, less than the sum over 2^17 entries and the logits'
+// own error (4e-7 of the loss) bring.  The bf16 gradient rounds by 4e-3.
 #include <map>
 #include <mutex>
 
@@ -206,6 +212,9 @@ __device__ __forceinline__ RowIn row_in(const Params& p, int r) {
   return x;
 }
 
+// g goes into both products as an operand of the tensor cores, so in the operands' type: bf16
+// (an error of 2.2e-3 of dH and dW with their own rounding, which alone is 1.7e-3), or three
+// bf16 parts for 32 bits.
 __device__ __forceinline__ void finish_grad(const Params& p, const Work& J, int r, int c0, float (&v)[32],
                                             const RowIn& x) {
   if (r >= J.m || c0 >= J.n) return;
