@@ -8,7 +8,7 @@ import torch
 
 import matrix_aware_optimizer_muon_gb300 as mm
 from oracle import head_ref as ref
-from test_gpu_head import BF, TYPES, U, ce_case, ce_tolerances, dev, num, put, strided, within
+from test_gpu_head import BF, TYPES, U, ce_case, ce_tolerances, compare_codes, dev, num, padded, put, strided, within
 
 pytestmark = pytest.mark.gpu
 
@@ -508,3 +508,117 @@ def check_layernorm(xdt, n, d, x64, dy64, w64, b64, forward, backward):
     within(num(dx), rdx, edx * 1.01 + 1e-30, "dx")
     within(num(dw), rdw, (n + 8) * U * np.abs(dy64 * xh).sum(0) + 1e-30, "dw")
     within(num(db), rdb, (n + 8) * U * np.abs(dy64).sum(0) + 1e-30, "db")
+
+
+def test_layernorm_past_32_bit_offsets():
+    """More than 2^31 elements: the last rows are, bit for bit, what they are by themselves."""
+    n, d, k = 2_200_003, 1024, 500
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(8)
+    x = torch.empty(n, d, device=dev(), dtype=torch.bfloat16).normal_(generator=gen)
+    w = torch.rand(d, generator=gen, device=dev()) + 0.5
+    y, mean, rstd = mm.muon_layernorm_forward(x, w, w)
+    ws = mm.alloc_layernorm_workspace(n, d)
+    dx, dw, db = mm.muon_layernorm_backward(y, x, w, mean, rstd, ws)
+    for s in (slice(0, k), slice(n - k, n)):
+        part = mm.muon_layernorm_forward(x[s], w, w)
+        assert all(torch.equal(a, b) for a, b in zip(part, (y[s], mean[s], rstd[s])))
+        assert torch.equal(mm.muon_layernorm_backward(y[s], x[s], w, mean[s], rstd[s], ws)[0], dx[s])
+    sums = [torch.zeros(d, dtype=torch.float64, device=dev()) for _ in range(4)]
+    for a in range(0, n, 1 << 18):
+        g = y[a:a + (1 << 18)].double()
+        p = g * (x[a:a + (1 << 18)].double() - mean[a:a + (1 << 18), None].double()) * rstd[a:a + (1 << 18), None].double()
+        for t, q in zip(sums, (p, p.abs(), g, g.abs())):
+            t += q.sum(0)
+    # a CTA's running sums take its share of the rows, then at most 152 lines are added
+    rows = n / 152 + 152 + 8
+    within(num(dw), num(sums[0]), rows * U * num(sums[1]), "dw")
+    within(num(db), num(sums[2]), rows * U * num(sums[3]), "db")
+
+
+def test_linear_ce_past_32_bit_offsets():
+    """H, then W, of more than 2^31 elements, and rows of H further apart than they are long."""
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(9)
+    d, k = 2048, 256
+    wide = torch.empty(1_050_003, d, device=dev(), dtype=torch.bfloat16).normal_(generator=gen)
+    few = torch.empty(300, d, device=dev(), dtype=torch.bfloat16).normal_(std=0.05, generator=gen)
+    n = wide.shape[0]
+    labels = torch.randint(0, 300, (n,), generator=gen, device=dev())
+    ws = mm.alloc_linear_ce_workspace(n, 300, d)
+    loss, lse, _ = mm.muon_linear_ce_forward(wide, few, labels, ws)
+    dh, dw = mm.muon_linear_ce_backward(wide, few, labels, lse, ws)
+    assert mm.muon_check_status(ws) == mm.MUON_OK
+    for s in (slice(0, k), slice(n - k, n)):
+        p = mm.muon_linear_ce_forward(wide[s], few, labels[s], ws)
+        assert torch.equal(p[0], loss[s]) and torch.equal(p[1], lse[s])
+        q = mm.muon_linear_ce_backward(wide[s], few, labels[s], lse[s], ws, need_dw=False)[0]
+        assert torch.linalg.norm(q.float() - dh[s].float()) <= 2 * BF * torch.linalg.norm(q.float())
+    want = torch.zeros(300, d, dtype=torch.float64, device=dev())
+    for a in range(0, n, 1 << 16):
+        h = wide[a:a + (1 << 16)].double()
+        g = torch.exp(h @ few.double().T - lse[a:a + (1 << 16), None].double())
+        g[torch.arange(len(h), device=dev()), labels[a:a + (1 << 16)]] -= 1
+        want += g.T @ h
+    assert torch.linalg.norm(dw.double() - want) <= 2 * BF * torch.linalg.norm(want)
+    del dh, dw
+    # the other way round: 300 rows against the long matrix as the vocabulary
+    labels = torch.randint(n - 1000, n, (300,), generator=gen, device=dev())
+    ws = mm.alloc_linear_ce_workspace(300, n, d)
+    loss, lse, _ = mm.muon_linear_ce_forward(few, wide, labels, ws)
+    dh, dw = mm.muon_linear_ce_backward(few, wide, labels, lse, ws)
+    assert mm.muon_check_status(ws) == mm.MUON_OK
+    z = torch.cat([few.double() @ wide[a:a + (1 << 16)].double().T for a in range(0, n, 1 << 16)], 1)
+    rl = torch.logsumexp(z, 1)
+    assert (lse - rl).abs().max() < 1e-4 and (loss - (rl - z.gather(1, labels[:, None])[:, 0])).abs().max() < 1e-4
+    g = torch.exp(z - lse.double()[:, None])
+    g[torch.arange(300, device=dev()), labels] -= 1
+    want = sum(g[:, a:a + (1 << 16)] @ wide[a:a + (1 << 16)].double() for a in range(0, n, 1 << 16))
+    assert torch.linalg.norm(dh.double() - want) <= 2 * BF * torch.linalg.norm(want)
+    for s in (slice(0, 5000), slice(n - 5000, n)):
+        want = g[:, s].T @ few.double()
+        assert torch.linalg.norm(dw[s].double() - want) <= 2 * BF * torch.linalg.norm(want)
+    # rows 2^25 elements apart
+    del wide, dh, dw, z, g, want
+    buf = torch.empty(70 << 25, device=dev(), dtype=torch.bfloat16)
+    far = buf.view(70, 1 << 25)[:, 8:8 + d]
+    far.copy_(few[:70])
+    labels = torch.randint(0, 300, (70,), generator=gen, device=dev())
+    ws = mm.linear_ce_workspace_for(far, few, labels)
+    got = mm.muon_linear_ce_forward(far, few, labels, ws)
+    got += mm.muon_linear_ce_backward(far, few, labels, got[1], ws, stats=got[2])
+    near = far.clone()
+    want = mm.muon_linear_ce_forward(near, few, labels, ws)
+    want += mm.muon_linear_ce_backward(near, few, labels, want[1], ws, stats=want[2])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_adamw8_past_32_bit_offsets():
+    """More than 2^32 elements in one parameter, and another behind it: the oracle's update and
+    its random bits at both ends and around 2^31 and 2^32."""
+    n = (1 << 32) + 70_003
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(10)
+    p = torch.full((n,), 0.5, device=dev(), dtype=torch.bfloat16)
+    g = torch.empty(n, device=dev(), dtype=torch.bfloat16).normal_(std=1e-3, generator=gen)
+    p2, g2 = p[:5000].clone(), g[:5000].clone()
+    opt = mm.AdamW8([p, p2], lr=1e-2, betas=(0.9, 0.999), seed=99)
+    opt.step([g, g2])
+    m, v = opt.moments()
+    for q, grad, first, spots in ((p, g, 0, (0, (1 << 31) - 640, (1 << 32) - 640, n - n % 128 - 1152)), (p2, g2, opt.starts[1], (0, 3712))):
+        for a in spots:
+            k = min(1280, q.numel() - a)
+            x = num(grad[a:a + k])
+            want, em, ev = ref.adamw8_update(np.full(k, 0.5), x, 0.0, 0.0, 1, 1e-2, 0.9, 0.999, 1e-8, 0.0)
+            within(num(q[a:a + k]), want, 16 * U + BF * 1.01 * np.abs(want), ("p", a))
+            blocks = -(-k // 128) * 128
+            at = first + a
+            bits = ref.random_bits(99, 1, at + np.arange(blocks)).astype(np.int64)
+            compare_codes(opt.m[at:at + blocks].cpu().numpy(), opt.m_scale[at // 128:(at + blocks) // 128].cpu().numpy(), padded(em),
+                          bits & 0xFFFF, 127, 16, 4 * U, ("m", a))
+            compare_codes(opt.v[at:at + blocks].cpu().numpy(), opt.v_scale[at // 128:(at + blocks) // 128].cpu().numpy(), padded(ev),
+                          bits >> 16, 255, 32, 8 * U, ("v", a))
+            assert np.array_equal(num(m[at:at + blocks]), ref.decode(opt.m[at:at + blocks].cpu().numpy(),
+                                                                     opt.m_scale[at // 128:(at + blocks) // 128].cpu().numpy(), True))
+            assert np.array_equal(num(v[at:at + blocks]), ref.decode(opt.v[at:at + blocks].cpu().numpy(),
+                                                                     opt.v_scale[at // 128:(at + blocks) // 128].cpu().numpy(), False))
