@@ -331,6 +331,100 @@ int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse, const flo
                             const float* stats, const float* upstream, float grad_scale, void* dH,
                             void* dW, void* ws, size_t ws_bytes, muon_stream_t stream);
 
+/* Log probabilities of given tokens, entropies and the likeliest alternatives under the
+ * softmax of the logits z = H W^T, which are never kept.  Scoring, decoding and
+ * policy-gradient training take these; a->labels holds the tokens (NULL, forward only: no
+ * token is given, every row counts).
+ *   lse[r] = log(sum_v exp(z[r, v]));  logprob[r] = z[r, token_r] - lse[r];
+ *   entropy[r] = -sum_v p log p,  p = exp(z[r, v] - lse[r]);
+ *   ids[r][0 .. top): the `top` largest logits, equal ones by the lower id;
+ *   alternatives[r][0 .. top): their log probabilities.
+ * A row with token ignore_index has logprob and entropy 0, ids -1 and alternatives minus
+ * infinity (lse is computed); a token outside [0, vocab) that is not ignore_index makes
+ * logprob and entropy NaN.  Logits of minus infinity, or below -2^120 (a mask of the type's
+ * lowest value), are masked entries: they are no alternatives, and places without one hold
+ * -1 and minus infinity.  A row of nothing but minus infinities has lse minus infinity,
+ * logprob and entropy NaN and no alternatives; a NaN or +Inf logit makes the row's lse,
+ * logprob, entropy and alternatives NaN and its ids -1.  Logits are summed as for the cross entropy; those near the top are summed
+ * again, to 2^-45 (64 bits for 32-bit operands), and ranked by that.  logprob, entropy, lse
+ * and alternatives are device fp32, ids device int64.  logprob may be NULL without tokens,
+ * ids and alternatives with top == 0. */
+#define MUON_LOGPROB_MAX_TOP 32
+int muon_linear_logprob_forward(const muon_linear_ce* a, int top, float* logprob, float* entropy, float* lse,
+                                int64_t* ids, float* alternatives, void* ws, size_t ws_bytes,
+                                muon_stream_t stream);
+
+/* Bytes of workspace for muon_linear_logprob_forward with so many alternatives (backward ==
+ * 0) or for both passes; (size_t)-1 for invalid arguments.  The rules of
+ * muon_linear_ce_workspace_size hold (initialisation, status and expired waits, too). */
+size_t muon_linear_logprob_workspace_size(const muon_linear_ce* a, int top, int backward);
+
+/* Gradient of sum_r (g_logprob[r]*logprob[r] + g_entropy[r]*entropy[r]):
+ *   g[r, v] = g_logprob[r]*([v == token_r] - p) - g_entropy[r]*p*(log p + entropy[r]),
+ *   dH = g W,  dW = g^T H, as for the cross entropy (in bf16, g is rounded to bf16).
+ * g_logprob or g_entropy may be NULL (zeros; entropy may be NULL with g_entropy).  lse and
+ * entropy are the forward pass's.  A row with token ignore_index, or with one out of range,
+ * has no gradient, whatever it holds.  Alternatives have no gradient. */
+int muon_linear_logprob_backward(const muon_linear_ce* a, const float* lse, const float* entropy,
+                                 const float* g_logprob, const float* g_entropy, void* dH, void* dW, void* ws,
+                                 size_t ws_bytes, muon_stream_t stream);
+
+/* Root-mean-square norm over the last dimension, behind a residual's addition:
+ *   t = x + residual, rounded to x_dtype (t = x without a residual);
+ *   rstd = 1/sqrt(sum(t^2)/dim + eps);  y = t*rstd*weight.
+ * x, residual, total (t) and y are x_dtype, weight (NULL: 1) is w_dtype.  total may be NULL,
+ * and is without a residual; it may be x or residual itself (same ld), y may be x itself
+ * where total is not; other overlaps are not allowed.  rstd (fp32, one a row) may be NULL.
+ * With codes, y is also written in 8 bits (y itself may then be NULL): for each row and
+ * MUON_RMS_GROUP columns (the last group may be shorter) a scale
+ *   s = max(max|y|/448, 2^-100)   (fp32, rows x ceil(dim/128), contiguous)
+ * and e4m3 codes of y/s, rounded to nearest, ties to even: code*s stands for y.  A NaN
+ * among a group's y makes its scale and codes NaN.  Arithmetic is fp32, with one rounding
+ * of y.  eps >= 0; rows and dim at most 2^30, dim >= 1; rows == 0 is a no-op. */
+#define MUON_RMS_GROUP 128
+int muon_rmsnorm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                         int64_t rows, int64_t dim, int x_dtype, int w_dtype, float eps, void* total, int64_t ldt,
+                         void* y, int64_t ldy, uint8_t* codes, int64_t ldc, float* scales, float* rstd,
+                         muon_stream_t stream);
+
+/* Bytes of workspace muon_rmsnorm_backward needs to reduce the weight's gradient;
+ * (size_t)-1 for invalid sizes. */
+size_t muon_rmsnorm_workspace_size(int64_t rows, int64_t dim);
+
+/* Gradient of y (and of total) with respect to t, which x and residual share.  With xh =
+ * t*rstd and g = dy*weight:
+ *   dx = dtotal + rstd*(g - xh*sum(g*xh)/dim);  dweight = sum over rows of dy*xh.
+ * total is the forward pass's t (x itself without a residual), dtotal the gradient that
+ * total has from elsewhere (NULL: 0).  dy, dtotal and dx are x_dtype; dweight is w_dtype,
+ * overwritten, and may be NULL (ws too then); rows == 0 writes zeros to it.  The sums over
+ * rows are fp32 in a fixed order.  dx may be dy or dtotal itself (same ld). */
+int muon_rmsnorm_backward(const void* dy, int64_t lddy, const void* total, int64_t ldt, const void* weight,
+                          const float* rstd, const void* dtotal, int64_t lddt, int64_t rows, int64_t dim,
+                          int x_dtype, int w_dtype, void* dx, int64_t lddx, void* dweight, void* ws,
+                          size_t ws_bytes, muon_stream_t stream);
+
+/* A gradient of the list that muon_clip_grad_norm takes. */
+typedef struct muon_grad {
+  void* G;           /* device, numel contiguous elements, scaled in place            */
+  int64_t numel;     /* >= 0, below 2^42                                              */
+  int32_t dtype;     /* MUON_DTYPE_F32 or MUON_DTYPE_BF16                             */
+  int32_t reserved;
+} muon_grad;
+
+/* The global norm of n gradients (host array; of both dtypes), and clipping by it:
+ *   norm = sqrt(sum of the squares of all elements);
+ *   where norm > max_norm:  g <- g*(max_norm/norm), rounded to g's dtype.
+ * norm is one device fp32 number, of the gradients as they were.  max_norm >= 0; an infinite
+ * one computes the norm alone.  Squares are added in fp32 by 64 and in 64 bits above that,
+ * with a power of two taken out where fp32 would overflow or underflow, in a fixed order.
+ * As the formula says, a norm of infinity makes finite gradients 0 and infinite ones NaN, and
+ * a NaN norm makes all of them NaN.  Tensors that are scaled must not share memory
+ * (MUON_ERR_INVALID).  ws: muon_clip_workspace_size() bytes, 8-byte aligned, no
+ * initialisation; one call at a time uses it. */
+size_t muon_clip_workspace_size(void);
+int muon_clip_grad_norm(const muon_grad* grads, int n, double max_norm, float* norm, void* ws, size_t ws_bytes,
+                        muon_stream_t stream);
+
 /* AdamW with both moments held in 8 bits.  Blocks of MUON_ADAMW8_BLOCK consecutive
  * elements share one scale byte s per moment.  A code c stands for the fp32 number
  * whose bits are (c + base) << 20, so for a float with 3 bits of mantissa:

@@ -10,11 +10,14 @@ from ._lib import (MUON_BRANCH_NS5, MUON_BRANCH_ROWNORM, MUON_DEBUG_CE_PIECE, MU
                    muon_debug_set, muon_init, muon_fro_norm, muon_fro_norm_noalloc, muon_momentum, muon_ns5_batched, muon_periodic_step,
                    muon_rownorm, muon_workspace_init, muon_workspace_size, status_str,
                    muon_profile_events, muon_launch_count, muon_adamw_step)
-from .head import (ADAMW8_BLOCK, AdamW8, MuonLinearCe, alloc_layernorm_workspace, alloc_linear_ce_workspace,
-                   linear_ce_workspace_for,
+from .head import (ADAMW8_BLOCK, LOGPROB_MAX_TOP, RMS_GROUP, AdamW8, MuonLinearCe, alloc_layernorm_workspace,
+                   alloc_linear_ce_workspace, alloc_linear_logprob_workspace, alloc_rmsnorm_workspace,
+                   linear_ce_workspace_for, linear_logprob_workspace_for, muon_linear_logprob_backward,
+                   muon_linear_logprob_forward, muon_rmsnorm_backward, muon_rmsnorm_forward, muon_rmsnorm_forward_fp8,
                    muon_layernorm_backward, muon_layernorm_forward, muon_linear_ce_backward, muon_linear_ce_forward,
                    muon_linear_ce_workspace_size)
-from .functional import layer_norm, linear_cross_entropy
+from .clip import alloc_clip_workspace, muon_clip_grad_norm
+from .functional import layer_norm, linear_cross_entropy, linear_logprobs, rms_norm
 from .optim import PeriodicMuon
 
 __all__ = [n for n in dir() if not n.startswith("_")]

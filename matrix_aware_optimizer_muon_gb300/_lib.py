@@ -111,6 +111,15 @@ def load_library(path: Optional[str] = None):
         "muon_linear_ce_workspace_size": (sz, [vp, i32]),
         "muon_linear_ce_forward": (i32, [vp, vp, vp, vp, vp, sz, vp]),
         "muon_linear_ce_backward": (i32, [vp, vp, vp, vp, vp, f32, vp, vp, vp, sz, vp]),
+        "muon_linear_logprob_workspace_size": (sz, [vp, i32, i32]),
+        "muon_linear_logprob_forward": (i32, [vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "muon_linear_logprob_backward": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "muon_rmsnorm_forward": (i32, [vp, i64, vp, i64, vp, i64, i64, i32, i32, f32, vp, i64, vp, i64, vp, i64, vp, vp,
+                                       vp]),
+        "muon_rmsnorm_workspace_size": (sz, [i64, i64]),
+        "muon_rmsnorm_backward": (i32, [vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, i32, i32, vp, i64, vp, vp, sz, vp]),
+        "muon_clip_workspace_size": (sz, []),
+        "muon_clip_grad_norm": (i32, [vp, i32, ctypes.c_double, vp, vp, sz, vp]),
         "muon_adamw8_step": (i32, [vp, i32, i64, f32, ctypes.c_double, ctypes.c_double, f32, f32, ctypes.c_uint32,
                                    vp]),
         "muon_adamw8_unpack": (i32, [vp, vp, vp, vp, i64, vp, vp, vp]),

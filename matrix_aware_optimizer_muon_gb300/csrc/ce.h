@@ -1,5 +1,5 @@
-// Linear cross entropy: what the host side (linear_ce.cu) hands to the tensor-core
-// kernel (ce_gemm.cu).
+// Linear cross entropy and log probabilities: what the host side (linear_ce.cu) hands to
+// the tensor-core kernel (ce_gemm.cu).
 #pragma once
 
 #include "internal.h"
@@ -19,8 +19,16 @@ enum Kind : int {
   LOGITS = 0,   // per row and 128 columns: max and sum of exponentials; the label's logit
   GRAD = 1,     // g = c (exp(z - lse) - onehot), in bf16 (or three bf16 parts)
   DH = 2,       // g W, summed over the pieces in fp32
-  DW = 3        // g^T H
+  DW = 3,       // g^T H
+  LOGPROB = 4,  // LOGITS, and the sum that the entropy takes and the largest of each 32 columns
+  POLICY = 5    // GRAD of log probabilities and entropies
 };
+
+// The two largest logits of 32 columns as keys: the lowest KEY_BITS bits of the number hold
+// 31 minus the column, so that two maxima a logit find them without carrying an index.
+// (An infinity becomes a NaN, which a maximum passes over.)
+constexpr int KEY_COLS = 32;
+constexpr unsigned KEY_MASK = KEY_COLS - 1;
 
 // One product of a launch: out[m, n] = sum_k A[m, k] B[n, k].  A K-major operand's map
 // covers (k, row), an MN-major one's (row, k), in boxes of 64 x 64.  The maps' third
@@ -59,6 +67,9 @@ struct Params {
   float* zlabel;
   const float *lse, *row_grad, *stats, *upstream;
   float scale;
+  float4* stat;                  // LOGPROB: [row][2 * ntiles] max m, sum of e^(z-m), sum of e^(z-m) (z-m)
+  float2* keys;                  // LOGPROB: [row][8 * ntiles], or null
+  const float *entropy, *g_logprob, *g_entropy;   // POLICY
   unsigned int* status;
   unsigned long long timeout_ns;
   int debug_flags;
@@ -73,7 +84,7 @@ static_assert(sizeof(OrderedParams) < 32000, "ce::OrderedParams too large");
 
 cudaError_t prepare();           // kernel attributes and occupancy of the current device, once
 int pairs();                     // CTA pairs that run at once
-cudaError_t launch(const OrderedParams& p, bool ordered, bool promote, cudaStream_t s);
+cudaError_t launch(const OrderedParams& p, bool ordered, bool promote, bool logprob, cudaStream_t s);
 
 #ifdef __CUDACC__
 // The factor that all rows share.

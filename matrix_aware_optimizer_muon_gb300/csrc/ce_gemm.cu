@@ -46,6 +46,7 @@
 // own error (4e-7 of the loss) bring.  The bf16 gradient rounds by 4e-3.
 #include <map>
 #include <mutex>
+#include <type_traits>
 
 #include "ce.h"
 #include "common.cuh"
@@ -235,6 +236,48 @@ __device__ __forceinline__ void finish_grad(const Params& p, const Work& J, int 
   }
 }
 
+// The same for log probabilities and entropies:
+//   g = a (onehot - p) - b p (log p + H),   p = exp(z - lse).
+// Far below lse, p is 0 and its logarithm has to stay finite.
+struct PolicyIn {
+  float a, b, lse, h;
+  long long label;
+};
+constexpr float LOG_FLOOR = -200.f;
+__device__ __forceinline__ PolicyIn policy_in(const Params& p, int r) {
+  const long long lab = p.labels[r];
+  PolicyIn x = {0.f, 0.f, INFINITY, 0.f, lab - p.v0};
+  if (lab == p.ignore || lab < 0 || lab >= p.vocab) return x;   // no gradient, whatever the row holds
+  x.lse = p.lse[r];
+  if (p.g_logprob) x.a = p.g_logprob[r];
+  if (p.g_entropy) {
+    x.b = p.g_entropy[r];
+    x.h = p.entropy[r];
+  }
+  // (a row's own lse is never +infinity: that marks the rows above)
+  if (x.lse == INFINITY) x.lse = __int_as_float(0x7FC00000);
+  return x;
+}
+__device__ __forceinline__ void finish_policy(const Params& p, const Work& J, int r, int c0, float (&v)[32],
+                                              const PolicyIn& x) {
+  if (r >= J.m || c0 >= J.n) return;
+  const bool dead = x.lse == INFINITY;
+  const int at = x.label >= c0 && x.label < c0 + 32 ? (int)(x.label - c0) : -1;
+  const float ah = fmaf(x.b, x.h, x.a);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float d = v[j] - x.lse, e = -__expf(d) * fmaf(x.b, fmaxf(d, LOG_FLOOR), ah);
+    v[j] = dead ? 0.f : j == at ? e + x.a : e;
+  }
+  bf16* dst = static_cast<bf16*>(J.out) + (size_t)r * J.ldo + c0;
+  store_row(dst, v, J.n - c0, 2);
+  for (int q = 1; q < p.parts; ++q) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+    store_row(dst + q * J.part_stride, v, J.n - c0, 2);
+  }
+}
+
 __device__ __forceinline__ void finish_sum(const Params& p, const Work& J, int split, int r, int c0, float u,
                                            float* stage, int lane, float (&v)[32]) {
   if (c0 >= J.n) return;
@@ -308,7 +351,69 @@ __device__ __forceinline__ void finish_logits(const Params& p, const Work& J, co
   }
 }
 
-template <bool kPromote, class P>
+// The statistics of the log probabilities over this thread's 128 columns: max, sum of
+// exponentials, their sum times the distance from the max (for the entropy), the token's
+// logit and, where alternatives are asked for, the two largest logits of each 32 columns.
+__device__ __forceinline__ void finish_logprob(const Params& p, const Work& J, const Tile& ti, int half, int r, int cbase,
+                                               const float (&acc)[CHUNKS][32]) {
+  if (r >= J.m) return;
+  const int cols = J.n - cbase;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k)
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (k * 32 + j < cols) mx = fmaxf(mx, acc[k][j]);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float s = 0.f, t = 0.f;
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k) {
+    float q = 0.f, u = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (k * 32 + j < cols) {
+        const float d = acc[k][j] - ref, e = __expf(d);
+        q += e;
+        u = fmaf(e, fmaxf(d, LOG_FLOOR), u);
+      }
+    s += q;
+    t += u;
+  }
+  p.stat[(size_t)r * (2 * J.ntiles) + 2 * ti.tn + half] = make_float4(mx, s, t, 0.f);
+  if (p.keys) {
+    float2 top[CHUNKS];
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) {
+      float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (k * 32 + j < cols) {
+          const float key = __uint_as_float((__float_as_uint(acc[k][j]) & ~KEY_MASK) | (KEY_MASK - j));
+          b = fmaxf(b, fminf(a, key));
+          a = fmaxf(a, key);
+        }
+      top[k] = make_float2(a, b);
+    }
+    float4* o = reinterpret_cast<float4*>(p.keys + ((size_t)r * (2 * J.ntiles) + 2 * ti.tn + half) * CHUNKS);
+#pragma unroll
+    for (int k = 0; k < CHUNKS; k += 2) o[k / 2] = make_float4(top[k].x, top[k].y, top[k + 1].x, top[k + 1].y);
+  }
+  const long long at = p.labels ? p.labels[r] - cbase : -1;
+  if (at >= 0 && at < HALF && at < cols) {
+    float z = 0.f;
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k)
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (k * 32 + j == (int)at) z = acc[k][j];
+    p.zlabel[r] = z;
+  }
+}
+
+// kLogprob: the epilogues of the log probabilities instead of the cross entropy's (kinds
+// LOGPROB and POLICY for LOGITS and GRAD); a form of its own, so that neither carries the
+// other's registers.
+template <bool kPromote, bool kLogprob, class P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kernel(const __grid_constant__ P p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -460,8 +565,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
       const Work& J = jobs[ti.job];
       const int r = ti.tm * TILE + rank * HALF + quarter * 32 + lane;
       const int cbase = ti.tn * TILE + half * HALF;
-      RowIn x = {};
-      if (J.kind == GRAD && r < J.m) x = row_in(p, r);
+      std::conditional_t<kLogprob, PolicyIn, RowIn> x = {};
+      if constexpr (kLogprob) {
+        if (J.kind == POLICY && r < J.m) x = policy_in(p, r);
+      } else {
+        if (J.kind == GRAD && r < J.m) x = row_in(p, r);
+      }
+      auto finish = [&](int c0, float (&v)[32]) {
+        if constexpr (kLogprob) {
+          if (J.kind == POLICY) { finish_policy(p, J, r, c0, v, x); return; }
+        } else {
+          if (J.kind == GRAD) { finish_grad(p, J, r, c0, v, x); return; }
+        }
+        finish_sum(p, J, ti.split, r, c0, u, stage, lane, v);
+      };
       const int nseg = kPromote ? segments(J, p.nterms) : 1;
       float acc[kPromote ? CHUNKS : 1][32];
       for (int seg = 0; seg < nseg; ++seg, ++it) {
@@ -479,8 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
           } else {
             float v[32];
             ptx::tmem_ld_32x32b_x32(tb + k * 32, v);
-            if (J.kind == GRAD) finish_grad(p, J, r, cbase + k * 32, v, x);
-            else finish_sum(p, J, ti.split, r, cbase + k * 32, u, stage, lane, v);
+            finish(cbase + k * 32, v);
           }
         }
         ptx::tc_fence_before();
@@ -491,14 +607,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
         }
       }
       if constexpr (kPromote) {
-        if (!stop && J.kind == LOGITS) {
-          finish_logits(p, J, ti, half, r, cbase, acc);
+        if (!stop && J.kind == (kLogprob ? LOGPROB : LOGITS)) {
+          if constexpr (kLogprob) finish_logprob(p, J, ti, half, r, cbase, acc);
+          else finish_logits(p, J, ti, half, r, cbase, acc);
         } else if (!stop) {
 #pragma unroll
-          for (int k = 0; k < CHUNKS; ++k) {
-            if (J.kind == GRAD) finish_grad(p, J, r, cbase + k * 32, acc[k], x);
-            else finish_sum(p, J, ti.split, r, cbase + k * 32, u, stage, lane, acc[k]);
-          }
+          for (int k = 0; k < CHUNKS; ++k) finish(cbase + k * 32, acc[k]);
         }
       }
     }
@@ -510,9 +624,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
   if (warp == 1) ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
 }
 
-template <class K>
-cudaError_t allow(K kern) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+// f(the kernel's form)
+template <bool kPromote, bool kLogprob, class F>
+cudaError_t each_order(bool ordered, F f) {
+  return ordered ? f(ce_kernel<kPromote, kLogprob, OrderedParams>) : f(ce_kernel<kPromote, kLogprob, Params>);
+}
+template <class F>
+cudaError_t each_form(bool promote, bool logprob, bool ordered, F f) {
+  if (logprob) return promote ? each_order<true, true>(ordered, f) : each_order<false, true>(ordered, f);
+  return promote ? each_order<true, false>(ordered, f) : each_order<false, false>(ordered, f);
 }
 std::mutex g_mu;
 std::map<int, int> g_pairs;   // device -> CTA pairs that run at once
@@ -525,16 +645,17 @@ cudaError_t prepare() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_pairs.count(dev)) return cudaSuccess;
-  if ((e = allow(ce_kernel<false, Params>)) != cudaSuccess || (e = allow(ce_kernel<true, Params>)) != cudaSuccess ||
-      (e = allow(ce_kernel<false, OrderedParams>)) != cudaSuccess ||
-      (e = allow(ce_kernel<true, OrderedParams>)) != cudaSuccess)
-    return e;
+  for (int f = 0; f < 8; ++f)
+    if ((e = each_form(f & 1, f & 2, f & 4, [](auto kern) {
+           return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+         })) != cudaSuccess)
+      return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM;
   int n = 0;
-  if ((e = cudaOccupancyMaxActiveClusters(&n, ce_kernel<true, Params>, &cfg)) != cudaSuccess) return e;
+  if ((e = cudaOccupancyMaxActiveClusters(&n, ce_kernel<true, false, Params>, &cfg)) != cudaSuccess) return e;
   g_pairs[dev] = n < MAX_PAIRS ? n : MAX_PAIRS;
   return cudaSuccess;
 }
@@ -547,16 +668,13 @@ int pairs() {
   return it == g_pairs.end() ? 0 : it->second;
 }
 
-cudaError_t launch(const OrderedParams& p, bool ordered, bool promote, cudaStream_t s) {
+cudaError_t launch(const OrderedParams& p, bool ordered, bool promote, bool logprob, cudaStream_t s) {
   if (p.tiles <= 0) return cudaSuccess;
   const int n = pairs();
   if (n < 1) return cudaErrorInvalidConfiguration;
   const int grid = 2 * (p.tiles < n ? p.tiles : n);
   count_launch();
-  if (promote && ordered) return launch_after(ce_kernel<true, OrderedParams>, grid, THREADS, SMEM, s, p);
-  if (promote) return launch_after(ce_kernel<true, Params>, grid, THREADS, SMEM, s, p);
-  if (ordered) return launch_after(ce_kernel<false, OrderedParams>, grid, THREADS, SMEM, s, p);
-  return launch_after(ce_kernel<false, Params>, grid, THREADS, SMEM, s, p);
+  return each_form(promote, logprob, ordered, [&](auto kern) { return launch_after(kern, grid, THREADS, SMEM, s, p); });
 }
 
 }  // namespace ce

@@ -6,6 +6,14 @@
 //   backward: g = c (exp(z - lse) - onehot) by pieces of the vocabulary;
 //             dH += g W_piece,  dW_piece = g^T H.
 //
+// Log probabilities of given tokens, entropy and the largest logits, likewise:
+//
+//   forward:  lse and z[token] as above; with S = sum e^(z-m) and T = sum e^(z-m) (z-m)
+//             (m the row's max) the entropy is log S - T/S; the two largest logits of each
+//             32 columns, from which the alternatives are chosen and ranked (top_kernel).
+//   backward: g = a (onehot - p) - b p (log p + H), a and b the gradients of log probability
+//             and entropy; the same two products.
+//
 // The products run in ce_gemm.cu; here are the plan of a call, the join and the copies
 // that bring operands into a layout TMA can read.
 #include <algorithm>
@@ -225,6 +233,319 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const float2* par
   }
 }
 
+// ---------------------------------------------------------------------------
+// log probabilities: the join and the alternatives
+// ---------------------------------------------------------------------------
+struct LogprobRows {
+  const float4* stat;        // [row][parts]
+  const float2* keys;        // [row][parts * 4], with alternatives
+  int parts;
+  long long rows;
+  const int64_t* labels;     // or null: no token is given
+  long long vocab, ignore;
+  const float* zlabel;
+  float *logprob, *entropy, *lse;
+  const unsigned int* status;
+  // alternatives
+  const void *H, *W;
+  long long ldh, ldw;
+  int dim, top, vec;
+  long long* ids;
+  float* alternatives;
+};
+
+// A running max with the sums that are relative to it.
+struct Moments {
+  float m, s, t;
+};
+// Adds sums relative to w.x, made relative to `ref` >= w.x.  A part whose max is minus
+// infinity has sums of 0, or NaN where it holds one; one far below ref adds nothing, whose
+// distance has to stay finite.
+__device__ __forceinline__ void add_moments(Moments& a, const float4& w, float ref) {
+  const float d = fmaxf(w.x - ref, -1000.f), f = expf(d);
+  const bool none = w.x == -INFINITY;
+  a.s += none ? w.y : f * w.y;
+  a.t += none ? w.z : f * fmaf(d, w.y, w.z);
+}
+__device__ __forceinline__ Moments join_moments(const float4* q, int parts, int i0, int step) {
+  Moments a = {-INFINITY, 0.f, 0.f};
+  for (int t0 = i0; t0 < parts; t0 += step * 4) {
+    float4 w[4];
+    float m = a.m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + step * i;
+      w[i] = t < parts ? q[t] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      m = fmaxf(m, w[i].x);
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    Moments b = {m, 0.f, 0.f};
+    add_moments(b, make_float4(a.m, a.s, a.t, 0.f), ref);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) add_moments(b, w[i], ref);
+    a = b;
+  }
+  return a;
+}
+__device__ __forceinline__ Moments warp_moments(const Moments& a) {
+  float top = a.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  Moments b = {top, 0.f, 0.f};
+  add_moments(b, make_float4(a.m, a.s, a.t, 0.f), top == -INFINITY ? 0.f : top);
+  b.s = warp_sum(b.s);
+  b.t = warp_sum(b.t);
+  return b;
+}
+
+// A row's results; returns its lse.  An infinite logit makes its sums NaN, and so everything.
+__device__ __forceinline__ float write_row(const LogprobRows& p, long long r, const Moments& a, bool counted, bool writes) {
+  const float ls = logf(a.s), lse = (a.m == -INFINITY ? 0.f : a.m) + ls;
+  if (writes) {
+    const long long lab = p.labels ? p.labels[r] : 0;
+    const bool known = lab >= 0 && lab < p.vocab;
+    p.lse[r] = lse;
+    if (p.labels) p.logprob[r] = !counted ? 0.f : known ? p.zlabel[r] - lse : not_a_number();
+    p.entropy[r] = !counted ? 0.f : known ? ls - a.t / a.s : not_a_number();
+  }
+  return lse;
+}
+__device__ __forceinline__ void write_lost(const LogprobRows& p, long long r) {
+  p.lse[r] = p.entropy[r] = not_a_number();
+  if (p.labels) p.logprob[r] = not_a_number();
+}
+
+// Without alternatives: a warp a row.
+__global__ void __launch_bounds__(32 * JOIN_WARPS) logprob_kernel(const LogprobRows p) {
+  await_previous();
+  const long long r = (long long)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+  if (r >= p.rows) return;
+  const int lane = threadIdx.x & 31;
+  if (is_lost(p.status)) {
+    if (lane == 0) write_lost(p, r);
+    return;
+  }
+  const Moments a = warp_moments(join_moments(p.stat + (size_t)r * p.parts, p.parts, lane, 32));
+  write_row(p, r, a, !p.labels || p.labels[r] != p.ignore, lane == 0);
+}
+
+// With alternatives: a CTA a row.  The tensor cores' logits are off by some 1e-6 of their
+// partial sums, which is enough to swap neighbours, so they only choose candidates, and the
+// candidates' logits are summed again, to 2^-45 of their largest partial sum:
+//   1. a bound from below on the top-th largest logit: the top-th of the threads' largest keys
+//      (two each where there are few);
+//   2. candidates: columns whose key is not below that by more than MARGIN of the largest
+//      logit, hundreds of times what the logits are off by; of 32 columns whose two keys both
+//      qualify, all (a third may hide behind them);
+//   3. their logits again, a warp each; 4. their ranks, ties to the lower index.
+// Where ties or a margin full of neighbours make more candidates than fit, the row's groups of
+// 32 columns are walked in order instead, against the top-th best so far.
+constexpr int TOP_THREADS = 256;
+constexpr int TOP_WARPS = TOP_THREADS / 32;
+constexpr int TOP_CANDIDATES = 512;
+constexpr int TOP_WHOLE = 8;                 // groups taken whole
+constexpr float TOP_MARGIN = 0x1p-12f;
+constexpr float MASKED = -0x1p120f;          // logits down here are masks, of the type's lowest value or less
+static_assert(TOP_WHOLE * KEY_COLS + MUON_LOGPROB_MAX_TOP <= TOP_CANDIDATES, "");
+
+// s + e <- s + e + p, exactly but for e's own rounding.
+__device__ __forceinline__ void add_exact(float& s, float& e, float p) {
+  const float t = __fadd_rn(s, p), b = __fsub_rn(t, s);
+  e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(p, b)));
+  s = t;
+}
+// Logits as sums of exact products: bf16 ones fit fp32, fp32 ones fit 64 bits.
+__device__ __forceinline__ double logit(const bf16* h, const bf16* w, int dim, int vec, int lane) {
+  float s[2] = {0.f, 0.f}, e[2] = {0.f, 0.f};
+  int c = 0;
+  if (vec) {
+    for (c = lane * 8; c + 8 <= dim; c += 256) {
+      const uint4 a = *reinterpret_cast<const uint4*>(h + c), b = *reinterpret_cast<const uint4*>(w + c);
+      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        add_exact(s[0], e[0], __fmul_rn(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16)));
+        add_exact(s[1], e[1], __fmul_rn(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u)));
+      }
+    }
+    c = dim / 8 * 8;
+  }
+  for (c += lane; c < dim; c += 32) add_exact(s[0], e[0], __fmul_rn(ld1(h + c), ld1(w + c)));
+  double v = ((double)s[0] + (double)s[1]) + ((double)e[0] + (double)e[1]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ double logit(const float* h, const float* w, int dim, int, int lane) {
+  double v = 0.0;
+  for (int c = lane; c < dim; c += 32) v = fma((double)h[c], (double)w[c], v);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct TopShared {
+  double value[TOP_CANDIDATES];
+  int id[TOP_CANDIDATES];
+  float key[2 * TOP_THREADS];
+  float4 warp[TOP_WARPS];
+  int whole[TOP_WHOLE];
+  double kept_value[MUON_LOGPROB_MAX_TOP];
+  int kept_id[MUON_LOGPROB_MAX_TOP];
+  int count, wholes;
+  float bound;
+};
+
+// The best `top` of n candidates, in order, to kept_*; the others' places hold -1.  An id of
+// -1, a masked value or a NaN is no candidate.
+__device__ __forceinline__ void rank(TopShared& sh, int n, int top) {
+  for (int i = threadIdx.x; i < top; i += TOP_THREADS) sh.kept_id[i] = -1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += TOP_THREADS) {
+    const double v = sh.value[i];
+    const int id = sh.id[i];
+    if (id < 0 || !(v > MASKED)) continue;
+    int better = 0;
+    for (int j = 0; j < n; ++j) {
+      const double u = sh.value[j];
+      better += sh.id[j] >= 0 && (u > v || (u == v && sh.id[j] < id));
+    }
+    if (better < top) {
+      sh.kept_value[better] = v;
+      sh.kept_id[better] = id;
+    }
+  }
+  __syncthreads();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(TOP_THREADS) top_kernel(const LogprobRows p) {
+  __shared__ TopShared sh;
+  await_previous();
+  const long long r = blockIdx.x;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, top = p.top;
+  long long* ids = p.ids + r * top;
+  float* alternatives = p.alternatives + r * top;
+  const bool lost = is_lost(p.status), counted = !p.labels || p.labels[r] != p.ignore;
+  // the row's sums
+  const Moments mine = warp_moments(join_moments(p.stat + (size_t)r * p.parts, p.parts, t, TOP_THREADS));
+  if (lane == 0) sh.warp[warp] = make_float4(mine.m, mine.s, mine.t, 0.f);
+  if (t == 0) sh.count = sh.wholes = 0;
+  // the thread's two largest keys
+  const int groups = p.parts * (TILE / 2 / KEY_COLS);
+  const float2* keys = p.keys + (size_t)r * groups;
+  float k1 = -INFINITY, k2 = -INFINITY;
+#pragma unroll 4
+  for (int g = t; g < groups; g += TOP_THREADS) {
+    const float2 k = keys[g];
+    k2 = fmaxf(k2, fmaxf(fminf(k1, k.x), k.y));
+    k1 = fmaxf(k1, k.x);
+  }
+  sh.key[t] = k1;
+  sh.key[TOP_THREADS + t] = k2;
+  __syncthreads();
+  Moments all = {-INFINITY, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < TOP_WARPS; ++i) all.m = fmaxf(all.m, sh.warp[i].x);
+#pragma unroll
+  for (int i = 0; i < TOP_WARPS; ++i) add_moments(all, sh.warp[i], all.m == -INFINITY ? 0.f : all.m);
+  if (lost) {
+    if (t == 0) write_lost(p, r);
+  }
+  const float lse = lost ? not_a_number() : write_row(p, r, all, counted, t == 0);
+  if (!counted || !isfinite(lse)) {
+    // nothing to rank: an ignored row, one whose logits are all minus infinity, or not numbers
+    for (int i = t; i < top; i += TOP_THREADS) {
+      ids[i] = -1;
+      alternatives[i] = counted && lse != -INFINITY ? not_a_number() : -INFINITY;
+    }
+    return;
+  }
+  // 1. the top-th largest of the threads' keys (-inf where there are fewer)
+  const int n_keys = groups >= 2 * TOP_THREADS ? TOP_THREADS : 2 * TOP_THREADS;
+  if (t == 0) sh.bound = -INFINITY;
+  __syncthreads();
+  for (int i = t; i < n_keys; i += TOP_THREADS) {
+    const float k = sh.key[i];
+    if (!(k > MASKED)) continue;
+    int better = 0;
+    for (int j = 0; j < n_keys; j += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(sh.key + j);
+      better += (q.x > k || (q.x == k && j < i)) + (q.y > k || (q.y == k && j + 1 < i)) + (q.z > k || (q.z == k && j + 2 < i)) +
+                (q.w > k || (q.w == k && j + 3 < i));
+    }
+    if (better == top - 1) sh.bound = k;
+  }
+  __syncthreads();
+  const float bound = sh.bound, margin = TOP_MARGIN * fmaxf(fabsf(all.m), bound == -INFINITY ? 0.f : fabsf(bound)) + 1e-30f;
+  const float least = bound - margin;
+  // 2. candidates
+#pragma unroll 4
+  for (int g = t; g < groups; g += TOP_THREADS) {
+    const float2 k = keys[g];
+    if (!(k.x >= least && k.x > MASKED)) continue;
+    if (k.y >= least && k.y > MASKED) {
+      const int at = atomicAdd(&sh.wholes, 1);
+      if (at < TOP_WHOLE) sh.whole[at] = g;
+    } else {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < TOP_CANDIDATES) sh.id[at] = g * KEY_COLS + (int)(KEY_MASK - (__float_as_uint(k.x) & KEY_MASK));
+    }
+  }
+  __syncthreads();
+  const T* h = static_cast<const T*>(p.H) + r * p.ldh;
+  const T* W = static_cast<const T*>(p.W);
+  const int singles = sh.count, wholes = sh.wholes;
+  if (wholes <= TOP_WHOLE && singles + wholes * KEY_COLS <= TOP_CANDIDATES) {
+    const int n = singles + wholes * KEY_COLS;
+    for (int i = singles + t; i < n; i += TOP_THREADS) {
+      const int c = sh.whole[(i - singles) / KEY_COLS] * KEY_COLS + (i - singles) % KEY_COLS;
+      sh.id[i] = c < p.vocab ? c : -1;
+    }
+    __syncthreads();
+    // 3.
+    for (int i = warp; i < n; i += TOP_WARPS) {
+      const int id = sh.id[i];
+      const double v = id < 0 ? 0.0 : logit(h, W + id * p.ldw, p.dim, p.vec, lane);
+      if (lane == 0) sh.value[i] = v;
+    }
+    __syncthreads();
+    rank(sh, n, top);
+  } else {
+    // every group against the best so far, KEY_COLS columns at a time
+    int kept = 0;
+    double worst = -INFINITY;      // of the kept, when there are `top`
+    __syncthreads();
+    for (int g = 0; g < groups; ++g) {
+      const float k = keys[g].x;   // (the same for every thread)
+      if (!(k >= least && k > MASKED) || (double)k + margin < worst) continue;
+      for (int i = warp; i < KEY_COLS; i += TOP_WARPS) {
+        const long long c = (long long)g * KEY_COLS + i;
+        const double v = c < p.vocab ? logit(h, W + c * p.ldw, p.dim, p.vec, lane) : 0.0;
+        if (lane == 0) {
+          sh.value[i] = v;
+          sh.id[i] = c < p.vocab ? (int)c : -1;
+        }
+      }
+      if (t < kept) {
+        sh.value[KEY_COLS + t] = sh.kept_value[t];
+        sh.id[KEY_COLS + t] = sh.kept_id[t];
+      }
+      __syncthreads();
+      rank(sh, KEY_COLS + kept, top);
+      kept = 0;
+      while (kept < top && sh.kept_id[kept] >= 0) ++kept;
+      if (kept == top) worst = sh.kept_value[top - 1];
+      __syncthreads();
+    }
+  }
+  for (int i = t; i < top; i += TOP_THREADS) {
+    const int id = sh.kept_id[i];
+    ids[i] = id;
+    alternatives[i] = id < 0 ? -INFINITY : (float)(sh.kept_value[i] - (double)lse);
+  }
+}
+
 // dH from the sums of each range of K; a block a row.
 template <typename T>
 __global__ void __launch_bounds__(256) split_sum_kernel(const float* acc, int splits, long long rows, int dim,
@@ -267,6 +588,7 @@ struct CePlan {
   bool pack_h, pack_w;
   size_t hp, wp;               // packed copies
   size_t zlabel, part, sums;   // forward
+  size_t stat, keys;           // forward of the log probabilities
   int64_t piece, npieces;
   int splits;
   size_t g[2];
@@ -290,9 +612,9 @@ int check(const muon_linear_ce* a) {
     return MUON_ERR_UNSUPPORTED;
   return MUON_OK;
 }
-int check_pointers(const muon_linear_ce* a) {
+int check_pointers(const muon_linear_ce* a, bool no_labels = false) {
   if (!a->W || !is_aligned(a->W, dt_size(a->dtype))) return MUON_ERR_INVALID;
-  if (a->rows && (!a->H || !a->labels || !is_aligned(a->H, dt_size(a->dtype)) || !is_aligned(a->labels, 8)))
+  if (a->rows && (!a->H || (!a->labels && !no_labels) || !is_aligned(a->H, dt_size(a->dtype)) || !is_aligned(a->labels, 8)))
     return MUON_ERR_INVALID;
   return MUON_OK;
 }
@@ -310,7 +632,9 @@ int split_count(int64_t rows, int64_t dim, int64_t piece, int64_t npairs) {
   return (int)std::min<int64_t>(std::max<int64_t>(1, cdiv(kp, share)), MAX_SPLITS);
 }
 
-void make_plan(const muon_linear_ce* a, int backward, CePlan* P) {
+// top: -1 for the cross entropy's forward pass, else the log probabilities' with so many
+// alternatives.
+void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
   const bool f32 = a->dtype == MUON_DTYPE_F32;
   P->parts = f32 ? 3 : 1;
   P->nterms = f32 ? 6 : 1;
@@ -325,8 +649,13 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P) {
   P->wp = P->pack_w ? take((size_t)P->parts * a->vocab * P->dp * 2) : at;
   const size_t common = at;
   P->zlabel = take((size_t)a->rows * 4);
-  P->part = take((size_t)a->rows * 2 * cdiv(a->vocab, TILE) * sizeof(float2));
-  P->sums = take((size_t)cdiv(a->rows, JOIN_WARPS) * sizeof(float2));
+  if (top < 0) {
+    P->part = take((size_t)a->rows * 2 * cdiv(a->vocab, TILE) * sizeof(float2));
+    P->sums = take((size_t)cdiv(a->rows, JOIN_WARPS) * sizeof(float2));
+  } else {
+    P->stat = take((size_t)a->rows * 2 * cdiv(a->vocab, TILE) * sizeof(float4));
+    P->keys = take(top ? (size_t)a->rows * (TILE / KEY_COLS) * cdiv(a->vocab, TILE) * sizeof(float2) : 0);
+  }
   P->total = at;
   if (!backward) return;
   at = common;
@@ -511,6 +840,110 @@ int result_vec(const void* out, int64_t ld, int dt) {
   return is_aligned(out, 16) && row % 16 == 0 ? 1 : 0;
 }
 
+// What g is made of in each row.
+struct RowGrads {
+  bool policy;                                             // of log probabilities and entropies
+  const float *lse, *row_grad, *stats, *upstream;          // cross entropy
+  float scale;
+  const float *entropy, *g_logprob, *g_entropy;            // log probabilities
+};
+
+int backward_pass(const muon_linear_ce* a, const RowGrads& rows, void* dH, void* dW, void* ws, size_t ws_bytes,
+                  cudaStream_t s) {
+  const size_t es = dt_size(a->dtype);
+  if (!is_aligned(dH, es) || !is_aligned(dW, es)) return MUON_ERR_INVALID;
+  CePlan P = {};
+  make_plan(a, 1, &P, rows.policy ? 0 : -1);
+  if (!ws || !is_aligned(ws, 256) || ws_bytes < P.total) return MUON_ERR_WORKSPACE;
+  if (!dH && !dW) return MUON_OK;
+  int sms = 0;
+  if (int rc = require_device(&sms)) return rc;
+  if (a->rows == 0) {
+    if (dW && cudaMemsetAsync(dW, 0, (size_t)a->vocab * a->dim * es, s) != cudaSuccess) return MUON_ERR_CUDA;
+    return MUON_OK;
+  }
+  if (prepare() != cudaSuccess) return MUON_ERR_CUDA;
+  char* w = static_cast<char*>(ws);
+  static thread_local OrderedParams p;
+  Operand H, W;
+  if (operand(&H, a, P, true, dW != nullptr, w, s) != cudaSuccess || operand(&W, a, P, false, false, w, s) != cudaSuccess)
+    return MUON_ERR_CUDA;
+  CUtensorMap hmap, wmap;
+  if (!map_of(&hmap, H) || !map_of(&wmap, W)) return MUON_ERR_CUDA;
+  const bool f32 = a->dtype == MUON_DTYPE_F32;
+  const int npairs = pairs();
+  float* acc = P.acc ? reinterpret_cast<float*>(w + P.acc) : nullptr;
+  // launch i computes g of piece i and multiplies g of piece i - 1
+  for (int64_t i = 0; i <= P.npieces; ++i) {
+    common_params(&p, a, P, w);
+    p.lse = rows.lse;
+    p.row_grad = rows.row_grad;
+    p.stats = rows.stats;
+    p.upstream = rows.upstream;
+    p.scale = rows.scale;
+    p.entropy = rows.entropy;
+    p.g_logprob = rows.g_logprob;
+    p.g_entropy = rows.g_entropy;
+    if (i > 0) {
+      const int64_t v0 = (i - 1) * P.piece, c = std::min(P.piece, a->vocab - v0);
+      const Operand G{reinterpret_cast<const bf16*>(w + P.g[(i - 1) & 1]), a->rows, c, P.piece, (int64_t)P.g_part, P.parts};
+      if (dH) {
+        Job& j = p.job[p.njobs++];
+        j.kind = DH;
+        if (!map_of(&j.a, G)) return MUON_ERR_CUDA;
+        j.b = wmap;
+        j.b_mn = 1;
+        j.b_k0 = (int)v0;
+        shape(&j, a->rows, a->dim, c, GROUP_G);
+        j.splits = P.splits;
+        j.nkb = (int)cdiv(j.nkb, P.splits);
+        j.tiles *= P.splits;
+        j.acc = acc;
+        j.ldacc = P.ldacc;
+        j.first = i == 1;
+        j.last = i == P.npieces;
+        j.out = P.splits == 1 ? dH : nullptr;
+        j.ldo = a->dim;
+        j.vec = result_vec(dH, a->dim, a->dtype);
+        j.seg_kb = f32 ? SEG_F32 : SEG_LONG;
+      }
+      if (dW) {
+        Job& j = p.job[p.njobs++];
+        j.kind = DW;
+        if (!map_of(&j.a, G)) return MUON_ERR_CUDA;
+        j.b = hmap;
+        j.a_mn = j.b_mn = 1;
+        shape(&j, c, a->dim, a->rows, GROUP_G);
+        j.out = static_cast<char*>(dW) + (size_t)v0 * a->dim * es;
+        j.ldo = a->dim;
+        j.vec = result_vec(j.out, a->dim, a->dtype);
+        j.seg_kb = f32 ? SEG_F32 : SEG_LONG;
+      }
+    }
+    if (i < P.npieces) {
+      Job& j = p.job[p.njobs++];
+      j.kind = rows.policy ? POLICY : GRAD;
+      j.a = hmap;
+      j.b = wmap;
+      p.v0 = i * P.piece;
+      j.b_n0 = (int)p.v0;
+      shape(&j, a->rows, std::min<int64_t>(P.piece, a->vocab - p.v0), a->dim, GROUP_GRAD);
+      j.out = w + P.g[i & 1];
+      j.ldo = P.piece;
+      j.part_stride = (long long)P.g_part;
+      j.seg_kb = f32 ? SEG_F32 : SEG_LONG;
+    }
+    bool promote = f32;
+    for (int k = 0; k < p.njobs; ++k) promote = promote || p.job[k].nkb > SEG_LONG;
+    const bool ordered = lay_out(&p, npairs);
+    if (launch(p, ordered, promote, rows.policy, s) != cudaSuccess) return MUON_ERR_CUDA;
+  }
+  const cudaError_t e = f32 ? finish<float>(a, P, acc, p, static_cast<float*>(dH), static_cast<float*>(dW), s)
+                            : finish<bf16>(a, P, acc, p, static_cast<bf16*>(dH), static_cast<bf16*>(dW), s);
+  if (e != cudaSuccess) return MUON_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace ce
 }  // namespace muon
@@ -558,7 +991,7 @@ extern "C" int muon_linear_ce_forward(const muon_linear_ce* a, float* loss, floa
   j.seg_kb = P.nterms > 1 ? SEG_F32 : SEG_BF16;
   p.njobs = 1;
   p.tiles = j.tiles;
-  if (launch(p, false, true, s) != cudaSuccess) return MUON_ERR_CUDA;
+  if (launch(p, false, true, false, s) != cudaSuccess) return MUON_ERR_CUDA;
   count_launch();
   if (launch_after(join_kernel, dim3((unsigned)cdiv(a->rows, JOIN_WARPS)), dim3(32 * JOIN_WARPS), 0, s, p.part,
                    2 * j.ntiles, a->rows, a->labels, a->vocab, a->ignore_index, p.zlabel, loss, lse, stats,
@@ -575,97 +1008,102 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
   begin_launches();
   if (int rc = check(a)) return rc;
   if (int rc = check_pointers(a)) return rc;
-  const size_t es = dt_size(a->dtype);
   if (a->rows && !lse) return MUON_ERR_INVALID;
-  if (!is_aligned(lse, 4) || !is_aligned(row_grad, 4) || !is_aligned(stats, 4) || !is_aligned(upstream, 4) ||
-      !is_aligned(dH, es) || !is_aligned(dW, es))
+  if (!is_aligned(lse, 4) || !is_aligned(row_grad, 4) || !is_aligned(stats, 4) || !is_aligned(upstream, 4))
+    return MUON_ERR_INVALID;
+  const RowGrads rows = {false, lse, row_grad, stats, upstream, grad_scale, nullptr, nullptr, nullptr};
+  return backward_pass(a, rows, dH, dW, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t muon_linear_logprob_workspace_size(const muon_linear_ce* a, int top, int backward) {
+  if (ce::check(a) != MUON_OK || top < 0 || top > MUON_LOGPROB_MAX_TOP) return (size_t)-1;
+  ce::CePlan P;
+  ce::make_plan(a, backward, &P, top);
+  return P.total;
+}
+
+extern "C" int muon_linear_logprob_forward(const muon_linear_ce* a, int top, float* logprob, float* entropy, float* lse,
+                                           int64_t* ids, float* alternatives, void* ws, size_t ws_bytes,
+                                           muon_stream_t stream) {
+  using namespace ce;
+  begin_launches();
+  if (int rc = check(a)) return rc;
+  if (int rc = check_pointers(a, true)) return rc;
+  if (top < 0 || top > MUON_LOGPROB_MAX_TOP) return MUON_ERR_INVALID;
+  if (a->rows && (!entropy || !lse || (a->labels && !logprob) || (top && (!ids || !alternatives)))) return MUON_ERR_INVALID;
+  if (!is_aligned(logprob, 4) || !is_aligned(entropy, 4) || !is_aligned(lse, 4) || !is_aligned(ids, 8) ||
+      !is_aligned(alternatives, 4))
     return MUON_ERR_INVALID;
   CePlan P = {};
-  make_plan(a, 1, &P);
+  make_plan(a, 0, &P, top);
   if (!ws || !is_aligned(ws, 256) || ws_bytes < P.total) return MUON_ERR_WORKSPACE;
-  if (!dH && !dW) return MUON_OK;
   int sms = 0;
   if (int rc = require_device(&sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a->rows == 0) {
-    if (dW && cudaMemsetAsync(dW, 0, (size_t)a->vocab * a->dim * es, s) != cudaSuccess) return MUON_ERR_CUDA;
-    return MUON_OK;
-  }
+  if (a->rows == 0) return MUON_OK;
   if (prepare() != cudaSuccess) return MUON_ERR_CUDA;
   char* w = static_cast<char*>(ws);
   static thread_local OrderedParams p;
+  common_params(&p, a, P, w);
+  p.stat = reinterpret_cast<float4*>(w + P.stat);
+  p.keys = top ? reinterpret_cast<float2*>(w + P.keys) : nullptr;
+  p.zlabel = reinterpret_cast<float*>(w + P.zlabel);
   Operand H, W;
-  if (operand(&H, a, P, true, dW != nullptr, w, s) != cudaSuccess || operand(&W, a, P, false, false, w, s) != cudaSuccess)
+  if (operand(&H, a, P, true, false, w, s) != cudaSuccess || operand(&W, a, P, false, false, w, s) != cudaSuccess)
     return MUON_ERR_CUDA;
-  CUtensorMap hmap, wmap;
-  if (!map_of(&hmap, H) || !map_of(&wmap, W)) return MUON_ERR_CUDA;
-  const bool f32 = a->dtype == MUON_DTYPE_F32;
-  const int npairs = pairs();
-  float* acc = P.acc ? reinterpret_cast<float*>(w + P.acc) : nullptr;
-  // launch i computes g of piece i and multiplies g of piece i - 1
-  for (int64_t i = 0; i <= P.npieces; ++i) {
-    common_params(&p, a, P, w);
-    p.lse = lse;
-    p.row_grad = row_grad;
-    p.stats = stats;
-    p.upstream = upstream;
-    p.scale = grad_scale;
-    if (i > 0) {
-      const int64_t v0 = (i - 1) * P.piece, c = std::min(P.piece, a->vocab - v0);
-      const Operand G{reinterpret_cast<const bf16*>(w + P.g[(i - 1) & 1]), a->rows, c, P.piece, (int64_t)P.g_part, P.parts};
-      if (dH) {
-        Job& j = p.job[p.njobs++];
-        j.kind = DH;
-        if (!map_of(&j.a, G)) return MUON_ERR_CUDA;
-        j.b = wmap;
-        j.b_mn = 1;
-        j.b_k0 = (int)v0;
-        shape(&j, a->rows, a->dim, c, GROUP_G);
-        j.splits = P.splits;
-        j.nkb = (int)cdiv(j.nkb, P.splits);
-        j.tiles *= P.splits;
-        j.acc = acc;
-        j.ldacc = P.ldacc;
-        j.first = i == 1;
-        j.last = i == P.npieces;
-        j.out = P.splits == 1 ? dH : nullptr;
-        j.ldo = a->dim;
-        j.vec = result_vec(dH, a->dim, a->dtype);
-        j.seg_kb = f32 ? SEG_F32 : SEG_LONG;
-      }
-      if (dW) {
-        Job& j = p.job[p.njobs++];
-        j.kind = DW;
-        if (!map_of(&j.a, G)) return MUON_ERR_CUDA;
-        j.b = hmap;
-        j.a_mn = j.b_mn = 1;
-        shape(&j, c, a->dim, a->rows, GROUP_G);
-        j.out = static_cast<char*>(dW) + (size_t)v0 * a->dim * es;
-        j.ldo = a->dim;
-        j.vec = result_vec(j.out, a->dim, a->dtype);
-        j.seg_kb = f32 ? SEG_F32 : SEG_LONG;
-      }
-    }
-    if (i < P.npieces) {
-      Job& j = p.job[p.njobs++];
-      j.kind = GRAD;
-      j.a = hmap;
-      j.b = wmap;
-      p.v0 = i * P.piece;
-      j.b_n0 = (int)p.v0;
-      shape(&j, a->rows, std::min<int64_t>(P.piece, a->vocab - p.v0), a->dim, GROUP_GRAD);
-      j.out = w + P.g[i & 1];
-      j.ldo = P.piece;
-      j.part_stride = (long long)P.g_part;
-      j.seg_kb = f32 ? SEG_F32 : SEG_LONG;
-    }
-    bool promote = f32;
-    for (int k = 0; k < p.njobs; ++k) promote = promote || p.job[k].nkb > SEG_LONG;
-    const bool ordered = lay_out(&p, npairs);
-    if (launch(p, ordered, promote, s) != cudaSuccess) return MUON_ERR_CUDA;
-  }
-  const cudaError_t e = f32 ? finish<float>(a, P, acc, p, static_cast<float*>(dH), static_cast<float*>(dW), s)
-                            : finish<bf16>(a, P, acc, p, static_cast<bf16*>(dH), static_cast<bf16*>(dW), s);
+  Job& j = p.job[0];
+  j.kind = LOGPROB;
+  if (!map_of(&j.a, H) || !map_of(&j.b, W)) return MUON_ERR_CUDA;
+  shape(&j, a->rows, a->vocab, a->dim, GROUP_FORWARD);
+  j.seg_kb = P.nterms > 1 ? SEG_F32 : SEG_BF16;
+  p.njobs = 1;
+  p.tiles = j.tiles;
+  if (launch(p, false, true, true, s) != cudaSuccess) return MUON_ERR_CUDA;
+  LogprobRows q = {};
+  q.stat = p.stat;
+  q.keys = p.keys;
+  q.parts = 2 * j.ntiles;
+  q.rows = a->rows;
+  q.labels = a->labels;
+  q.vocab = a->vocab;
+  q.ignore = a->ignore_index;
+  q.zlabel = p.zlabel;
+  q.logprob = logprob;
+  q.entropy = entropy;
+  q.lse = lse;
+  q.status = p.status;
+  q.H = a->H;
+  q.W = a->W;
+  q.ldh = a->ldh;
+  q.ldw = a->ldw;
+  q.dim = (int)a->dim;
+  q.top = top;
+  q.ids = reinterpret_cast<long long*>(ids);
+  q.alternatives = alternatives;
+  const size_t es = dt_size(a->dtype);
+  q.vec = is_aligned(a->H, 16) && is_aligned(a->W, 16) && a->ldh * es % 16 == 0 && a->ldw * es % 16 == 0;
+  count_launch();
+  cudaError_t e;
+  if (top == 0)
+    e = launch_after(logprob_kernel, dim3((unsigned)cdiv(a->rows, JOIN_WARPS)), dim3(32 * JOIN_WARPS), 0, s, q);
+  else if (a->dtype == MUON_DTYPE_BF16)
+    e = launch_after(top_kernel<bf16>, dim3((unsigned)a->rows), dim3(TOP_THREADS), 0, s, q);
+  else
+    e = launch_after(top_kernel<float>, dim3((unsigned)a->rows), dim3(TOP_THREADS), 0, s, q);
   if (e != cudaSuccess) return MUON_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+extern "C" int muon_linear_logprob_backward(const muon_linear_ce* a, const float* lse, const float* entropy,
+                                            const float* g_logprob, const float* g_entropy, void* dH, void* dW,
+                                            void* ws, size_t ws_bytes, muon_stream_t stream) {
+  using namespace ce;
+  begin_launches();
+  if (int rc = check(a)) return rc;
+  if (int rc = check_pointers(a)) return rc;
+  if (a->rows && (!lse || (g_entropy && !entropy))) return MUON_ERR_INVALID;
+  if (!is_aligned(lse, 4) || !is_aligned(entropy, 4) || !is_aligned(g_logprob, 4) || !is_aligned(g_entropy, 4))
+    return MUON_ERR_INVALID;
+  const RowGrads rows = {true, lse, nullptr, nullptr, nullptr, 1.f, entropy, g_logprob, g_entropy};
+  return backward_pass(a, rows, dH, dW, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }

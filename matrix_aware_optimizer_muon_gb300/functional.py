@@ -25,7 +25,7 @@ class _Once(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *_):
-        raise RuntimeError("layer_norm and linear_cross_entropy have no second derivatives")
+        raise RuntimeError("layer_norm, rms_norm, linear_cross_entropy and linear_logprobs have no second derivatives")
 
 
 def _once(grads, depends):
@@ -54,6 +54,68 @@ class _LayerNorm(torch.autograd.Function):
                                                       bias=want_b and ctx.bias_dtype, weight_grad=want_w)
             dx = dx.view(ctx.shape)
         return *_once((dx, dw, db), (dy, x, weight)), None
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        ctx.set_materialize_grads(False)
+        y, rstd, total = head.muon_rmsnorm_forward(_plain_rows(x), weight, None if residual is None else _plain_rows(residual), eps)
+        if residual is None:
+            ctx.save_for_backward(x, weight, total, rstd)
+            ctx.shape = x.shape
+            return y.view(x.shape)
+        ctx.shape, total = x.shape, total.view(x.shape)
+        ctx.save_for_backward(x, weight, total, rstd, residual)
+        return y.view(x.shape), total
+
+    @staticmethod
+    def backward(ctx, dy, dtotal=None):
+        x, weight, total, rstd, *residual = ctx.saved_tensors
+        dw = None
+        if dy is None:
+            dx = dtotal
+        else:
+            with torch.no_grad():
+                want_w = ctx.needs_input_grad[1]
+                rows = _plain_rows(total)
+                ws = head.alloc_rmsnorm_workspace(*rows.shape, device=rows.device) if want_w else None
+                dx, dw = head.muon_rmsnorm_backward(_plain_rows(dy), rows, weight, rstd, ws,
+                                                    None if dtotal is None else _plain_rows(dtotal), weight_grad=want_w)
+                dx = dx.view(ctx.shape)
+        dx, dw = _once((dx, dw), (dy, dtotal, x, weight, *residual))
+        return dx, dw, dx if residual else None, None
+
+
+class _LinearLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, w, tokens, ignore_index, top):
+        ctx.set_materialize_grads(False)
+        rows, flat = _plain_rows(h), tokens.reshape(-1).contiguous()
+        plain = _plain_rows(w)
+        ws = head.linear_logprob_workspace_for(rows, plain, flat, top, backward=False)
+        logprob, entropy, lse, ids, alternatives = head.muon_linear_logprob_forward(rows, plain, flat, ws, top, ignore_index)
+        ctx.save_for_backward(h, w, rows, plain, flat, lse, entropy)
+        ctx.shape, ctx.ignore_index = h.shape, ignore_index
+        out = logprob.view(tokens.shape), entropy.view(tokens.shape)
+        if top == 0:
+            return out
+        ids, alternatives = ids.view(*tokens.shape, top), alternatives.view(*tokens.shape, top)
+        ctx.mark_non_differentiable(ids, alternatives)
+        return *out, ids, alternatives
+
+    @staticmethod
+    def backward(ctx, g_logprob, g_entropy, *_):
+        h, w, rows, plain, tokens, lse, entropy = ctx.saved_tensors
+        with torch.no_grad():
+            flat = [None if g is None else g.float().reshape(-1).contiguous() for g in (g_logprob, g_entropy)]
+            ws = head.linear_logprob_workspace_for(rows, plain, tokens)
+            dh, dw = head.muon_linear_logprob_backward(
+                rows, plain, tokens, lse, entropy, ws, *flat, ignore_index=ctx.ignore_index,
+                need_dh=ctx.needs_input_grad[0], need_dw=ctx.needs_input_grad[1])
+            dh = None if dh is None else dh.view(ctx.shape)
+            dw = None if dw is None else dw.view(w.shape)
+        return *_once((dh, dw), (g_logprob, g_entropy, h, w)), None, None, None
 
 
 class _LinearCrossEntropy(torch.autograd.Function):
@@ -88,3 +150,16 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor,
     """Mean cross entropy of the logits h w^T, which are never kept (h: ... x dim, w: vocab x
     dim, labels: ... int64); 0 when every label is ignore_index."""
     return _LinearCrossEntropy.apply(h, w, labels, ignore_index)
+
+
+def rms_norm(x: torch.Tensor, weight=None, residual=None, eps: float = 1e-6):
+    """RMS norm over the last dimension (weight of that size, fp32 or bf16).  With a residual of x's
+    shape and dtype, returns (the norm of x + residual, x + residual), both differentiable."""
+    return _RmsNorm.apply(x, weight, residual, eps)
+
+
+def linear_logprobs(h: torch.Tensor, w: torch.Tensor, tokens: torch.Tensor, ignore_index: int = -100, top: int = 0):
+    """(logprob, entropy) of the softmax of the logits h w^T, which are never kept (h: ... x dim, w:
+    vocab x dim, tokens: ... int64), of the tokens' shape; both 0 where a token is ignore_index.
+    With top > 0 also (ids, alternatives) of the likeliest entries, ... x top, without gradient."""
+    return _LinearLogprobs.apply(h, w, tokens, ignore_index, top)

@@ -1,11 +1,12 @@
-"""The operators at a model's head: layer norm, linear cross entropy and AdamW with
-8-bit moments.
+"""The operators at a model's head: layer norm and RMS norm, linear cross entropy and log
+probabilities, AdamW with 8-bit moments.
 
 Muon takes the blocks' matrices; the norms and the vocabulary matrix stay on AdamW.  The
 functions here (same names as the C ABI in include/muon.h) compute the part of a training
 step those parameters belong to: the norm before the vocabulary matrix, the loss over the
-vocabulary without keeping its logits, their gradients, and the update.  Like the rest of
-the package they only marshal arguments: every computation runs in the library's kernels.
+vocabulary (or its tokens' log probabilities, entropies and alternatives) without keeping
+its logits, their gradients, and the update.  Like the rest of the package they only
+marshal arguments: every computation runs in the library's kernels.
 """
 from __future__ import annotations
 
@@ -137,6 +138,93 @@ def muon_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[
 
 
 # ---------------------------------------------------------------------------
+# RMS norm
+# ---------------------------------------------------------------------------
+RMS_GROUP = 128
+
+
+def _rms_forward(x, weight, residual, eps, need_total, eight, need_y, stream):
+    px, ldx = _rows(x, "x")
+    n, d = x.shape
+    pr, ldr = None, 0
+    if residual is not None:
+        pr, ldr = _rows(residual, "residual")
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("x and residual must have the same shape and dtype")
+    pw = _vector(weight, d, None, "weight")
+    _on_current(x, weight, residual)
+    codes = scales = y = None
+    with _on(stream):
+        rstd = torch.empty(n, dtype=torch.float32, device=x.device)
+        total = torch.empty((n, d), dtype=x.dtype, device=x.device) if residual is not None and need_total else None
+        if need_y:
+            y = torch.empty((n, d), dtype=x.dtype, device=x.device)
+        if eight:
+            codes = torch.empty((n, d), dtype=torch.float8_e4m3fn, device=x.device)
+            scales = torch.empty((n, -(-d // RMS_GROUP)), dtype=torch.float32, device=x.device)
+    _check("muon_rmsnorm_forward", load_library().muon_rmsnorm_forward(
+        px, ldx, pr, ldr, pw, n, d, _dt(x), _dt(x if weight is None else weight), eps,
+        None if total is None else total.data_ptr(), d, None if y is None else y.data_ptr(), d,
+        None if codes is None else codes.data_ptr(), d, None if scales is None else scales.data_ptr(), rstd.data_ptr(),
+        _stream(stream, x)))
+    return y, codes, scales, rstd, total if residual is not None else x
+
+
+def muon_rmsnorm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                         residual: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None,
+                         need_total: bool = True):
+    """y = total*rstd*weight over the last dimension of total = x + residual (2-D, rows may be
+    strided).  Returns (y, rstd, total): y and total contiguous in x's dtype, rstd fp32.  total is
+    x without a residual, and None with one when need_total is False."""
+    y, _, _, rstd, total = _rms_forward(x, weight, residual, eps, need_total, False, True, stream)
+    return y, rstd, total
+
+
+def muon_rmsnorm_forward_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                             residual: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None,
+                             need_total: bool = True):
+    """The same with y in 8 bits.  Returns (codes, scales, rstd, total): codes float8_e4m3fn (rows x
+    dim), scales fp32 (rows x ceil(dim/128)); codes[r, c]*scales[r, c//128] stands for y[r, c]."""
+    _, codes, scales, rstd, total = _rms_forward(x, weight, residual, eps, need_total, True, False, stream)
+    return codes, scales, rstd, total
+
+
+def alloc_rmsnorm_workspace(rows: int, dim: int, device=None) -> torch.Tensor:
+    """Workspace of muon_rmsnorm_backward for these sizes; one call at a time uses it."""
+    v = load_library().muon_rmsnorm_workspace_size(int(rows), int(dim))
+    if v == ctypes.c_size_t(-1).value:
+        raise _lib.MuonError("muon_rmsnorm_workspace_size", _lib.MUON_ERR_INVALID)
+    return torch.empty(int(v), dtype=torch.uint8, device=device or "cuda")
+
+
+def muon_rmsnorm_backward(dy: torch.Tensor, total: torch.Tensor, weight: Optional[torch.Tensor], rstd: torch.Tensor,
+                          ws: Optional[torch.Tensor] = None, dtotal: Optional[torch.Tensor] = None, stream=None,
+                          weight_grad: bool = True):
+    """Gradients of muon_rmsnorm_forward: (dx, dweight).  dx is the gradient of x and of the
+    residual alike; dtotal, if given, is the one that total has from elsewhere.  dweight is None
+    without a weight or weight_grad; then no workspace is needed."""
+    pt, ldt = _rows(total, "total")
+    py, ldy = _rows(dy, "dy")
+    n, d = total.shape
+    if tuple(dy.shape) != (n, d) or dy.dtype != total.dtype:
+        raise ValueError("dy and total must have the same shape and dtype")
+    pd, ldd = None, 0
+    if dtotal is not None:
+        pd, ldd = _rows(dtotal, "dtotal")
+        if tuple(dtotal.shape) != (n, d) or dtotal.dtype != total.dtype:
+            raise ValueError("dtotal and total must have the same shape and dtype")
+    pw, pr = _vector(weight, d, None, "weight"), _vector(rstd, n, torch.float32, "rstd")
+    _on_current(dy, total, weight, rstd, ws, dtotal)
+    with _on(stream):
+        dx = torch.empty((n, d), dtype=total.dtype, device=total.device)
+        dw = torch.empty(d, dtype=weight.dtype, device=total.device) if weight is not None and weight_grad else None
+    _check("muon_rmsnorm_backward", load_library().muon_rmsnorm_backward(
+        py, ldy, pt, ldt, pw, pr, pd, ldd, n, d, _dt(total), _dt(total if weight is None else weight), dx.data_ptr(), d,
+        None if dw is None else dw.data_ptr(), _lib._ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, total)))
+    return dx, dw
+
+
+# ---------------------------------------------------------------------------
 # linear cross entropy
 # ---------------------------------------------------------------------------
 class MuonLinearCe(ctypes.Structure):
@@ -225,6 +313,94 @@ def muon_linear_ce_backward(h: torch.Tensor, w: torch.Tensor, labels: torch.Tens
     _check("muon_linear_ce_backward", load_library().muon_linear_ce_backward(
         ctypes.byref(a), pl, pg, ps, pu, grad_scale, None if dh is None else dh.data_ptr(),
         None if dw is None else dw.data_ptr(), _lib._ptr(ws), ws.numel(), _stream(stream, h)))
+    return dh, dw
+
+
+# ---------------------------------------------------------------------------
+# log probabilities, entropies and alternatives
+# ---------------------------------------------------------------------------
+LOGPROB_MAX_TOP = 32
+
+
+def _logprob_args(h: torch.Tensor, w: torch.Tensor, tokens: Optional[torch.Tensor], ignore_index: int) -> MuonLinearCe:
+    if tokens is not None:
+        return _ce_args(h, w, tokens, ignore_index)
+    ph, ldh = _rows(h, "h")
+    pw, ldw = _rows(w, "w")
+    if h.dtype != w.dtype or h.shape[1] != w.shape[1]:
+        raise ValueError("h and w must have the same dtype and width")
+    return MuonLinearCe(ph, pw, None, h.shape[0], w.shape[0], h.shape[1], ldh, ldw, _dt(h), ignore_index)
+
+
+def _logprob_workspace_size(a: MuonLinearCe, top: int, backward: bool) -> int:
+    v = load_library().muon_linear_logprob_workspace_size(ctypes.byref(a), int(top), 1 if backward else 0)
+    if v == ctypes.c_size_t(-1).value:
+        raise _lib.MuonError("muon_linear_logprob_workspace_size", _lib.MUON_ERR_INVALID)
+    return int(v)
+
+
+def alloc_linear_logprob_workspace(rows: int, vocab: int, dim: int, dtype=torch.bfloat16, top: int = 0,
+                                   backward: bool = True, ldh: Optional[int] = None, ldw: Optional[int] = None,
+                                   device=None) -> torch.Tensor:
+    """Workspace of muon_linear_logprob_forward with up to `top` alternatives and, with backward,
+    muon_linear_logprob_backward.  ldh and ldw: elements between rows of h and w where they are
+    not contiguous."""
+    a = MuonLinearCe(None, None, None, rows, vocab, dim, ldh or dim, ldw or dim,
+                     _lib.MUON_DTYPE_F32 if dtype == torch.float32 else _lib.MUON_DTYPE_BF16, -100)
+    return _workspace(_logprob_workspace_size(a, top, backward), device)
+
+
+def linear_logprob_workspace_for(h: torch.Tensor, w: torch.Tensor, tokens: Optional[torch.Tensor], top: int = 0,
+                                 backward: bool = True) -> torch.Tensor:
+    """Workspace for these very tensors (their strides and alignment included)."""
+    a = _logprob_args(h, w, tokens, -100)
+    _on_current(h, w, tokens)
+    return _workspace(_logprob_workspace_size(a, top, backward), h.device)
+
+
+def muon_linear_logprob_forward(h: torch.Tensor, w: torch.Tensor, tokens: Optional[torch.Tensor], ws: torch.Tensor,
+                                top: int = 0, ignore_index: int = -100, stream=None):
+    """Log probabilities of int64 tokens under the softmax of the logits h w^T (h: rows x dim, w:
+    vocab x dim), the rows' entropies and their `top` (at most 32) likeliest entries, without
+    keeping the logits.  Returns (logprob, entropy, lse, ids, alternatives): fp32 but for the int64
+    ids; ids and alternatives (their log probabilities) are rows x top, or None with top == 0.
+    Rows with token ignore_index give 0, 0, their log-sum-exp, -1 and -inf.  tokens may be None:
+    every row counts, and logprob is None."""
+    a = _logprob_args(h, w, tokens, ignore_index)
+    _on_current(h, w, tokens, ws)
+    n, dev, ids, alternatives, logprob = h.shape[0], h.device, None, None, None
+    with _on(stream):
+        if tokens is not None:
+            logprob = torch.empty(n, dtype=torch.float32, device=dev)
+        entropy = torch.empty(n, dtype=torch.float32, device=dev)
+        lse = torch.empty(n, dtype=torch.float32, device=dev)
+        if top > 0:
+            ids = torch.empty((n, top), dtype=torch.int64, device=dev)
+            alternatives = torch.empty((n, top), dtype=torch.float32, device=dev)
+    _check("muon_linear_logprob_forward", load_library().muon_linear_logprob_forward(
+        ctypes.byref(a), int(top), None if logprob is None else logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+        None if ids is None else ids.data_ptr(), None if alternatives is None else alternatives.data_ptr(),
+        _lib._ptr(ws), ws.numel(), _stream(stream, h)))
+    return logprob, entropy, lse, ids, alternatives
+
+
+def muon_linear_logprob_backward(h: torch.Tensor, w: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor,
+                                 entropy: Optional[torch.Tensor], ws: torch.Tensor,
+                                 g_logprob: Optional[torch.Tensor] = None, g_entropy: Optional[torch.Tensor] = None,
+                                 ignore_index: int = -100, need_dh: bool = True, need_dw: bool = True, stream=None):
+    """(dh, dw) of sum_r g_logprob[r]*logprob[r] + g_entropy[r]*entropy[r], with the forward pass's
+    lse and entropy; a gradient that is None counts as zeros."""
+    a = _ce_args(h, w, tokens, ignore_index)
+    n = h.shape[0]
+    pl, pe = _vector(lse, n, torch.float32, "lse"), _vector(entropy, n, torch.float32, "entropy")
+    pg, ph = _vector(g_logprob, n, torch.float32, "g_logprob"), _vector(g_entropy, n, torch.float32, "g_entropy")
+    _on_current(h, w, tokens, lse, entropy, ws, g_logprob, g_entropy)
+    with _on(stream):
+        dh = torch.empty((n, h.shape[1]), dtype=h.dtype, device=h.device) if need_dh else None
+        dw = torch.empty(tuple(w.shape), dtype=w.dtype, device=h.device) if need_dw else None
+    _check("muon_linear_logprob_backward", load_library().muon_linear_logprob_backward(
+        ctypes.byref(a), pl, pe, pg, ph, None if dh is None else dh.data_ptr(), None if dw is None else dw.data_ptr(),
+        _lib._ptr(ws), ws.numel(), _stream(stream, h)))
     return dh, dw
 
 

@@ -1,11 +1,12 @@
 """Stateful wrapper: momentum buffers, workspace and step counter around muon_periodic_step."""
 from __future__ import annotations
 
-from typing import Dict, List, Sequence
+from typing import Dict, List, Optional, Sequence
 
 import torch
 
 from . import _lib
+from .clip import alloc_clip_workspace, muon_clip_grad_norm
 from .head import AdamW8, _on
 
 
@@ -19,10 +20,13 @@ class PeriodicMuon:
     def __init__(self, params: Sequence[torch.Tensor], K: int = 3, gamma: float = 0.15, mu: float = 0.95,
                  eta: float = 0.02, lam: float = 0.01, ns5_mode: str = "bf16",
                  aux_params: Sequence[torch.Tensor] = (), aux_lr: float = 1e-4, betas=(0.9, 0.999),
-                 eps: float = 1e-8, aux_bits: int = 32, aux_seed: int = 0):
+                 eps: float = 1e-8, aux_bits: int = 32, aux_seed: int = 0, max_grad_norm: Optional[float] = None):
         """aux_params: parameters Muon does not take (biases, norms, out-of-block weights);
         they are updated by AdamW with learning rate aux_lr and the shared weight decay lam.
-        aux_bits: 32, or 8 to hold AdamW's moments in 8 bits (aux_seed seeds their rounding)."""
+        aux_bits: 32, or 8 to hold AdamW's moments in 8 bits (aux_seed seeds their rounding).
+        max_grad_norm: every step first scales all gradients, the auxiliary ones among them, in
+        place so that their global norm is at most this; the norm before that is
+        self.grad_norm, one number on the device."""
         self.params: List[torch.Tensor] = list(params)
         self.aux = list(aux_params)
         self.aux_lr, self.betas, self.eps = aux_lr, betas, eps
@@ -40,6 +44,7 @@ class PeriodicMuon:
         dev = self.params[0].device
         self.M = [torch.zeros(p.shape, dtype=torch.float32, device=dev) for p in self.params]
         self.ws = _lib.alloc_workspace([tuple(p.shape) for p in self.params], ns5_mode, device=dev)
+        self.max_grad_norm, self.grad_norm, self._clip_ws = max_grad_norm, None, None
         self.step_count = 0
         # W and M never move, so the C matrix array is built once; each step only
         # points it at that step's gradients (after checking them like the array build does).
@@ -67,6 +72,11 @@ class PeriodicMuon:
                 if len({(p.dtype, g.dtype) for p, g in zip(self.aux, aux_grads)}) != 1:
                     raise ValueError("auxiliary parameters, and their gradients, are of one dtype")
                 aux = _lib.adamw_array(self.aux, aux_grads, self.aux_m, self.aux_v)
+        if self.max_grad_norm is not None:
+            if self._clip_ws is None:
+                self._clip_ws = alloc_clip_workspace(self.ws.device)
+            self.grad_norm = muon_clip_grad_norm([*grads, *(aux_grads if self.aux else ())], self.max_grad_norm,
+                                                 self._clip_ws, stream=stream)
         br = _lib.periodic_step_prepared(self._arr, self._n, self.step_count, self.ws, self.K, self.gamma, self.mu,
                                          self.eta, self.lam, self.ns5_mode, stream=stream)
         if self.aux8 is not None:

@@ -1,5 +1,6 @@
-"""Plain fp64 restatements of the head's operators: layer norm, linear cross entropy and
-AdamW with 8-bit moments.  Test infrastructure; shares no code with the CUDA path."""
+"""Plain fp64 restatements of the head's operators: layer norm and RMS norm, linear cross
+entropy and log probabilities, AdamW with 8-bit moments, clipping by the global norm.
+Test infrastructure; shares no code with the CUDA path."""
 from __future__ import annotations
 
 import numpy as np
@@ -122,3 +123,77 @@ def adamw8_update(p, g, m, v, t, lr, beta1, beta2, eps, weight_decay):
     v = beta2 * v + (1 - beta2) * g * g
     p = p - lr * ((m / (1 - beta1 ** t)) / (np.sqrt(v / (1 - beta2 ** t)) + eps) + weight_decay * p)
     return p, m, v
+
+
+def rmsnorm_forward(t, w=None, eps=1e-6):
+    t = np.asarray(t, np.float64)
+    rstd = 1.0 / np.sqrt((t * t).mean(1) + eps)
+    y = t * rstd[:, None]
+    return (y if w is None else y * np.asarray(w, np.float64)), rstd
+
+
+def rmsnorm_backward(dy, t, w, rstd, dtotal=None):
+    dy, xh = np.asarray(dy, np.float64), np.asarray(t, np.float64) * np.asarray(rstd, np.float64)[:, None]
+    g = dy if w is None else dy * np.asarray(w, np.float64)
+    dx = np.asarray(rstd, np.float64)[:, None] * (g - xh * (g * xh).mean(1, keepdims=True))
+    return (dx if dtotal is None else dx + np.asarray(dtotal, np.float64)), (dy * xh).sum(0)
+
+
+def e4m3(q):
+    """The nearest of the numbers with 4 bits of exponent and 3 of mantissa, ties to even."""
+    q = np.asarray(q, np.float64)
+    e = np.maximum(np.frexp(np.abs(q))[1], -5) - 4
+    return np.clip(np.ldexp(np.round(np.ldexp(q, -e)), e), -448.0, 448.0)
+
+
+def eight_bits(y, group=128):
+    """(codes' values, scales) of rows in groups of columns."""
+    y = np.asarray(y, np.float64)
+    k = -(-y.shape[1] // group)
+    p = np.zeros((y.shape[0], k * group))
+    p[:, :y.shape[1]] = y
+    scale = np.maximum(np.abs(p.reshape(-1, k, group)).max(2) / 448.0, 2.0 ** -100)
+    return e4m3(p / np.repeat(scale, group, 1))[:, :y.shape[1]], scale
+
+
+def logprobs(h, w, tokens, top=0, ignore_index=-100):
+    """(logprob, entropy, lse, ids, alternatives) of the logits h w^T."""
+    z = np.asarray(h, np.float64) @ np.asarray(w, np.float64).T
+    n, v = z.shape
+    m = z.max(1, keepdims=True)
+    lse = m[:, 0] + np.log(np.exp(z - m).sum(1))
+    p = np.exp(z - lse[:, None])
+    entropy = -(p * np.where(p > 0, z - lse[:, None], 0.0)).sum(1)
+    logprob = np.zeros(n)
+    ids, alternatives = np.full((n, top), -1), np.full((n, top), -np.inf)
+    for r in range(n):
+        tok = None if tokens is None else int(tokens[r])
+        if tok == ignore_index:
+            entropy[r] = 0.0
+            continue
+        if tok is not None:
+            logprob[r] = z[r, tok] - lse[r] if 0 <= tok < v else np.nan
+            entropy[r] = entropy[r] if 0 <= tok < v else np.nan
+        order = [c for c in np.argsort(-z[r], kind="stable") if z[r, c] > -np.inf][:top]
+        ids[r, :len(order)] = order
+        alternatives[r, :len(order)] = z[r, order] - lse[r]
+    return logprob, entropy, lse, ids, alternatives
+
+
+def logprob_logit_grad(h, w, tokens, lse, entropy, a, b, ignore_index=-100):
+    """Gradient of sum_r a_r logprob_r + b_r entropy_r with respect to the logits."""
+    logp = np.asarray(h, np.float64) @ np.asarray(w, np.float64).T - np.asarray(lse, np.float64)[:, None]
+    p = np.exp(logp)
+    g = np.zeros_like(p)
+    for r, tok in enumerate(np.asarray(tokens)):
+        if tok == ignore_index or not 0 <= tok < p.shape[1]:
+            continue
+        g[r] = -a[r] * p[r] - b[r] * p[r] * (np.where(p[r] > 0, logp[r], 0.0) + entropy[r])
+        g[r, tok] += a[r]
+    return g
+
+
+def clip_grad_norm(grads, max_norm):
+    norm = np.sqrt(sum(float((np.asarray(g, np.float64) ** 2).sum()) for g in grads))
+    coef = max_norm / norm if norm > max_norm else 1.0
+    return norm, [np.asarray(g, np.float64) * coef for g in grads]
