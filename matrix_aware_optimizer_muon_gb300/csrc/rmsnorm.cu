@@ -36,11 +36,257 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// The scale of a group whose largest magnitude is `most`.
-__device__ __forceinline__ float scale_of(float most) { return max_nan(most / 448.f, RMS_LEAST_SCALE); }
+// The scale of a group whose largest magnitude is `most`, and its reciprocal: both within 2 ulp
+// (a scale is what it is, and codes are of four bits).
+__device__ __forceinline__ float2 scale_of(float most) {
+  const float s = max_nan(most * (1.f / 448.f), RMS_LEAST_SCALE);
+  return make_float2(s, __fdividef(1.f, s));
+}
 // Two numbers to the nearest e4m3 codes (448 at most, NaN as NaN).
 __device__ __forceinline__ uint32_t code2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+// ---------------------------------------------------------------------------
+// forward: rows whose pointers and strides allow 16-byte vectors
+// ---------------------------------------------------------------------------
+
+// x + r, rounded to their type, over x.
+__device__ __forceinline__ void add16(uint4& x, const uint4& r, const bf16*) {
+  auto sum = [](uint32_t a, uint32_t b) {
+    const f32x2 s = add2(cvt2(a), cvt2(b));
+    return pack_bf16x2(lo2(s), hi2(s));
+  };
+  x = make_uint4(sum(x.x, r.x), sum(x.y, r.y), sum(x.z, r.z), sum(x.w, r.w));
+}
+__device__ __forceinline__ void add16(uint4& x, const uint4& r, const float*) {
+  auto sum = [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); };
+  x = make_uint4(sum(x.x, r.x), sum(x.y, r.y), sum(x.z, r.z), sum(x.w, r.w));
+}
+// A vector of y to codes; its group of 128 columns lies in 16 neighbouring lanes (bf16) or in
+// the warp (fp32).  The magnitudes' bits are compared as whole numbers: a NaN is the largest.
+template <int V>
+__device__ __forceinline__ void store_codes(const RmsFwd& p, long long row, int c, bool inside, const f32x2* y) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i)
+    most = max(most, max(__float_as_uint(lo2(y[i])) & 0x7FFFFFFFu, __float_as_uint(hi2(y[i])) & 0x7FFFFFFFu));
+#pragma unroll
+  for (int o = RMS_GROUP / V / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  const float2 scale = scale_of(__uint_as_float(most));
+  if (!inside) return;
+  uint32_t w[V / 4];
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    const f32x2 a = mul2(y[2 * i], both(scale.y)), b = mul2(y[2 * i + 1], both(scale.y));
+    w[i] = code2(lo2(a), hi2(a)) | code2(lo2(b), hi2(b)) << 16;
+  }
+  uint8_t* o = p.codes + row * p.ldc + c;
+  if constexpr (V == 8) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(o) = w[0];
+  if (c % RMS_GROUP == 0) p.scales[row * p.groups + c / RMS_GROUP] = scale.x;
+}
+
+// A warp a row (kWarp) or a CTA a row.  The row stays in registers, as loaded, between its
+// sum and its output, so that it is read once; all of a thread's loads are in flight together.
+constexpr int RMS_WARPS = 8;
+constexpr int RMS_MOST_THREADS = 512;
+template <typename T, int kN, bool kWarp, int kW, bool kEight>
+__global__ void __launch_bounds__(kWarp ? 32 * RMS_WARPS : RMS_MOST_THREADS) rms_forward_kernel(const RmsFwd p) {
+  constexpr int V = 16 / (int)sizeof(T), C = V / 2, kSure = kWarp ? sure_of(kN) : 0;
+  __shared__ __align__(8) float red[kWarp ? 2 : 128];
+  const int t = kWarp ? threadIdx.x & 31 : threadIdx.x, size = kWarp ? 32 : blockDim.x;
+  const long long r = kWarp ? (long long)blockIdx.x * RMS_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+  if (kWarp && r >= p.rows) return;
+  Raw<T, V, kN> raw;
+  raw.template load<kSure>(static_cast<const T*>(p.x) + r * p.ldx, t, size, p.dim);
+  if (p.r) {
+    Raw<T, V, kN> res;
+    res.template load<kSure>(static_cast<const T*>(p.r) + r * p.ldr, t, size, p.dim);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) add16(raw.q[k], res.q[k], static_cast<const T*>(nullptr));
+    if (p.total) {
+      T* total = static_cast<T*>(p.total) + r * p.ldt;
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int c = (k * size + t) * V;
+        if (k < kSure || c < p.dim) *reinterpret_cast<uint4*>(total + c) = raw.q[k];
+      }
+    }
+  }
+  f32x2 q = both(0.f);
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    f32x2 v[C];
+    raw.get(k, v);
+#pragma unroll
+    for (int i = 0; i < C; ++i) q = fma2(v[i], v[i], q);
+  }
+  const float ssq = lo2(q) + hi2(q);
+  const float sum = kWarp ? warp_sum(ssq) : Group{t, size, 0, red}.sum(ssq, 0.f, 0).x;
+  const float rs = 1.0f / sqrtf(sum * (1.f / (float)p.dim) + p.eps);
+  raw.hold();
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const int c = (k * size + t) * V;
+    const bool inside = k < kSure || c < p.dim;
+    f32x2 v[C], w[C];
+    raw.get(k, v);
+    if (kW == W_ASK || inside) weights<V, kW>(p.w, p.w_bf16, c, p.dim, 1.f, w);
+    else
+#pragma unroll
+      for (int i = 0; i < C; ++i) w[i] = both(0.f);
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = mul2(mul2(v[i], both(rs)), w[i]);
+    if constexpr (kEight) store_codes<V>(p, r, c, inside, v);
+    if (inside && (!kEight || p.y)) store16(static_cast<T*>(p.y) + r * p.ldy + c, v);
+  }
+  if (p.rstd && t == 0) p.rstd[r] = rs;
+}
+
+// ---------------------------------------------------------------------------
+// rows of any alignment, through shared memory
+// ---------------------------------------------------------------------------
+// A row that starts off a 16-byte boundary is fetched in whole 16-byte words, from the one
+// that holds its first element to the one that holds its last, and lies in shared memory as
+// far behind a boundary as it does in global memory; results are staged likewise, at their own
+// distance, and leave in whole words but for the ends.  (An element a thread moves 4 or 2
+// bytes where a word moves 16: LSU-bound.)
+template <typename T> __device__ __forceinline__ int behind(const T* row) {
+  return (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
+}
+template <typename T>
+__device__ __forceinline__ void fetch_row(T* slot, const T* row, int dim, int t, int size) {
+  const int off = behind(row), words = (int)(((off + dim) * sizeof(T) + 15) / 16);
+  const uint4* src = reinterpret_cast<const uint4*>(row - off);
+  for (int i = t; i < words; i += size) copy16(reinterpret_cast<uint4*>(slot) + i, src + i);
+}
+// slot holds the row from its `behind` on.
+template <typename T>
+__device__ __forceinline__ void flush_row(T* row, const T* slot, int dim, int t, int size) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const int off = behind(row), end = off + dim, words = (end + V - 1) / V;
+  T* dst = row - off;
+  for (int i = t; i < words; i += size) {
+    if (i * V >= off && i * V + V <= end) {
+      reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(slot)[i];
+    } else {
+      for (int c = max(i * V, off); c < min(i * V + V, end); ++c) dst[c] = slot[c];
+    }
+  }
+}
+template <typename T> __host__ __device__ constexpr int slot_bytes(int dim) {
+  return (int)((dim * (long long)sizeof(T) + 31 + 15) / 16 * 16);
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory"); }
+
+// The threads of a row (threadIdx.x) beside those of other rows (threadIdx.y).
+struct RowThreads {
+  int t, size, id;
+  __device__ __forceinline__ void sync() const {
+    if (size == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(size) : "memory");
+  }
+  // red: 16 floats; every thread gets the sum, in a fixed order.  A second call needs a
+  // sync() between.
+  __device__ __forceinline__ float sum(float v, float* red) const {
+    v = warp_sum(v);
+    if (size == 32) return v;
+    if ((t & 31) == 0) red[t >> 5] = v;
+    sync();
+    v = 0.f;
+    for (int i = 0; i < size >> 5; ++i) v += red[i];
+    return v;
+  }
+};
+
+constexpr int RMS_ODD_GROUPS = 8;                 // rows a CTA at most
+constexpr int RMS_ODD_SMEM = 200 * 1024;
+// Slots: x, then y (or codes); the residual, or y without one; t with one.
+template <typename T, bool kEight>
+__global__ void __launch_bounds__(512) rms_forward_odd_kernel(const RmsFwd p, int slot) {
+  extern __shared__ uint4 dyn[];
+  __shared__ float red[RMS_ODD_GROUPS][16];
+  const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= p.rows) return;
+  const RowThreads g{(int)threadIdx.x, (int)blockDim.x, 1 + (int)threadIdx.y};
+  const int slots = p.r ? 3 : 2, t = g.t, lane = t & 31, warp = t >> 5, nw = g.size >> 5;
+  uint8_t* mine = reinterpret_cast<uint8_t*>(dyn) + (size_t)threadIdx.y * slots * slot;
+  T* A = reinterpret_cast<T*>(mine);
+  T* B = reinterpret_cast<T*>(mine + slot);
+  T* D = reinterpret_cast<T*>(mine + 2 * slot);
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+  fetch_row(A, x, p.dim, t, g.size);
+  const T* a = A + behind(x);
+  const T* b = nullptr;
+  T* total = nullptr;
+  T* d = nullptr;
+  if (p.r) {
+    const T* r = static_cast<const T*>(p.r) + row * p.ldr;
+    fetch_row(B, r, p.dim, t, g.size);
+    b = B + behind(r);
+    if (p.total) total = static_cast<T*>(p.total) + row * p.ldt;
+    d = D + (total ? behind(total) : 0);
+  }
+  copies_done();
+  g.sync();
+  float q = 0.f;
+  if (p.r) {
+#pragma unroll 4
+    for (int c = t; c < p.dim; c += g.size) {
+      const T v = from_f32<T>(to_f32(a[c]) + to_f32(b[c]));
+      d[c] = v;
+      q = fmaf(to_f32(v), to_f32(v), q);
+    }
+    a = d;
+  } else {
+#pragma unroll 4
+    for (int c = t; c < p.dim; c += g.size) q = fmaf(to_f32(a[c]), to_f32(a[c]), q);
+  }
+  const float rs = 1.0f / sqrtf(g.sum(q, red[threadIdx.y]) * (1.f / (float)p.dim) + p.eps);
+  if (g.size == 32) __syncwarp();      // (with more warps the sum has waited for all of d)
+  if (total) flush_row(total, D, p.dim, t, g.size);
+  // with a residual x's slot is free, without one the residual's
+  T* Y = p.r ? A : B;
+  T* y = p.y ? static_cast<T*>(p.y) + row * p.ldy : nullptr;
+  auto norm_at = [&](int c) {
+    const float v = to_f32(a[c]) * rs;
+    return p.w ? v * ld_w(p.w, p.w_bf16, c) : v;
+  };
+  if constexpr (kEight) {
+    uint8_t* codes = p.codes + row * p.ldc;
+    uint8_t* o = reinterpret_cast<uint8_t*>(Y) + behind(codes);
+    for (int k = warp; k < p.groups; k += nw) {
+      float v[4];
+      uint32_t most = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = k * RMS_GROUP + 32 * j + lane;
+        v[j] = c < p.dim ? norm_at(c) : 0.f;
+        most = max(most, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      const float2 scale = scale_of(__uint_as_float(most));
+      if (lane == 0) p.scales[row * p.groups + k] = scale.x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = k * RMS_GROUP + 32 * j + lane;
+        if (c < p.dim) {
+          o[c] = (uint8_t)code2(v[j] * scale.y, 0.f);
+          if (y) st1(y + c, v[j]);
+        }
+      }
+    }
+    g.sync();
+    flush_row(codes, reinterpret_cast<const uint8_t*>(Y), p.dim, t, g.size);
+  } else {
+    T* o = Y + behind(y);
+#pragma unroll 4
+    for (int c = t; c < p.dim; c += g.size) o[c] = from_f32<T>(norm_at(c));
+    g.sync();
+    flush_row(y, static_cast<const T*>(Y), p.dim, t, g.size);
+  }
+  if (p.rstd && t == 0) p.rstd[row] = rs;
 }
 
 // Rows of any length: a CTA a row, three passes, the later ones from cache.
@@ -78,13 +324,13 @@ __global__ void __launch_bounds__(RMS_LOOP_THREADS) rms_forward_loop_kernel(cons
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-      const float scale = scale_of(most), inv = 1.f / scale;
-      if (lane == 0) p.scales[row * p.groups + g] = scale;
+      const float2 scale = scale_of(most);
+      if (lane == 0) p.scales[row * p.groups + g] = scale.x;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = g * RMS_GROUP + 32 * j + lane;
         if (c < p.dim) {
-          p.codes[row * p.ldc + c] = (uint8_t)code2(v[j] * inv, 0.f);
+          p.codes[row * p.ldc + c] = (uint8_t)code2(v[j] * scale.y, 0.f);
           if (p.y) st1(static_cast<T*>(p.y) + row * p.ldy + c, v[j]);
         }
       }
@@ -105,7 +351,323 @@ struct RmsBwd {
   int dim, w_bf16;
 };
 
-// Rows of any length: dx with the row read twice, and the columns' sums over slabs of rows.
+// A persistent CTA of several row groups (threadIdx.y).  A thread owns the same columns of
+// every row its group takes, so the weights and the columns' sums stay in its registers; at
+// the end the groups' sums are joined in shared memory in a fixed order and the CTA writes
+// one line.  Rows come through a ring of asynchronous copies, R - 1 rows ahead.
+constexpr int RMS_GROUPS = 8;
+constexpr int RMS_BWD_THREADS = 512;
+constexpr int RMS_RING = 3;
+
+// The groups' sums of E columns a thread, to the CTA's line.
+template <int E, class Column, class Sum>
+__device__ __forceinline__ void join_columns(const RmsBwd& p, Column column, Sum sum) {
+  extern __shared__ uint4 dyn[];
+  const int g = threadIdx.y;
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();                              // the ring's memory is free for the sums
+  float* sums = reinterpret_cast<float*>(dyn);  // [groups - 1][dim]
+  if (g > 0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (column(e) < p.dim) sums[(size_t)(g - 1) * p.dim + column(e)] = sum(e);
+  }
+  __syncthreads();
+  if (g > 0) return;
+  float* o = p.part + (size_t)blockIdx.x * p.dim;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = column(e);
+    if (c < p.dim) {
+      float a = sum(e);
+      for (int j = 0; j < (int)blockDim.y - 1; ++j) a += sums[(size_t)j * p.dim + c];
+      o[c] = a;
+    }
+  }
+}
+
+// Rows that move in 16-byte vectors: each thread reads only what it copied itself, so the
+// ring needs no barrier.
+template <typename T, int kN, bool kDt, int R>
+__global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_kernel(const RmsBwd p) {
+  extern __shared__ uint4 dyn[];
+  __shared__ float red[2][RMS_GROUPS][16];
+  constexpr int V = 16 / (int)sizeof(T), C = V / 2, P = kN * C, S = kDt ? 3 : 2;
+  const RowThreads g{(int)threadIdx.x, (int)blockDim.x, 1 + (int)threadIdx.y};
+  const int t = g.t, groups = blockDim.y, nthr = g.size * groups;
+  const float inv = 1.f / (float)p.dim;
+  const long long step = (long long)gridDim.x * groups;
+  long long r = (long long)blockIdx.x * groups + threadIdx.y, rf = r;
+  f32x2 w[P], sw[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) sw[i] = both(0.f);
+#pragma unroll
+  for (int k = 0; k < kN; ++k) weights<V>(p.w, p.w_bf16, (k * g.size + t) * V, p.dim, 1.f, w + k * C);
+  uint4* const mine = dyn + threadIdx.y * g.size + t;      // [slot][stream][access][thread]
+  const T *tf = static_cast<const T*>(p.t) + r * p.ldt, *gf = static_cast<const T*>(p.dy) + r * p.lddy;
+  const T* df = kDt ? static_cast<const T*>(p.dtotal) + r * p.lddt : nullptr;
+  auto fetch = [&](int slot) {                  // one group of copies, empty past the last row
+    if (rf < p.rows) {
+      uint4* d = mine + slot * (S * kN) * nthr;
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int c = (k * g.size + t) * V;
+        if (c < p.dim) {
+          copy16(d + k * nthr, tf + c);
+          copy16(d + (kN + k) * nthr, gf + c);
+          if (kDt) copy16(d + (2 * kN + k) * nthr, df + c);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    rf += step;
+    tf += step * p.ldt;
+    gf += step * p.lddy;
+    if (kDt) df += step * p.lddt;
+  };
+  // slots that are never copied to belong to columns past the row: zero
+#pragma unroll
+  for (int k = 0; k < kN; ++k)
+    if ((k * g.size + t) * V >= p.dim)
+      for (int s = 0; s < S * R; ++s) mine[(s * kN + k) * nthr] = make_uint4(0, 0, 0, 0);
+  for (int s = 0; s < R - 1; ++s) fetch(s);
+  float rs_n = r < p.rows ? p.rstd[r] : 0.f;
+  T* dx = static_cast<T*>(p.dx) + r * p.lddx;
+  int parity = 0, at = 0;
+  for (; r < p.rows; r += step, dx += step * p.lddx) {
+    fetch(at == 0 ? R - 1 : at - 1);
+    const float rs = rs_n;
+    if (r + step < p.rows) rs_n = p.rstd[r + step];
+    asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
+    const uint4* d = mine + at * (S * kN) * nthr;
+    at = at + 1 == R ? 0 : at + 1;
+    f32x2 xh[P], gr[P], s = both(0.f);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      widen(d[k * nthr], xh + k * C, static_cast<const T*>(nullptr));
+      widen(d[(kN + k) * nthr], gr + k * C, static_cast<const T*>(nullptr));
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      xh[i] = mul2(xh[i], both(rs));
+      sw[i] = fma2(gr[i], xh[i], sw[i]);
+      gr[i] = mul2(gr[i], w[i]);
+      s = fma2(gr[i], xh[i], s);
+    }
+    const float m = g.sum(lo2(s) + hi2(s), red[parity][threadIdx.y]) * inv;
+    parity ^= 1;
+    const f32x2 c1 = both(rs), c2 = both(-rs * m);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const int c = (k * g.size + t) * V;
+      f32x2 v[C];
+      if (kDt) widen(d[(2 * kN + k) * nthr], v, static_cast<const T*>(nullptr));
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const f32x2 a = fma2(gr[k * C + i], c1, mul2(xh[k * C + i], c2));
+        v[i] = kDt ? add2(v[i], a) : a;
+      }
+      if (c < p.dim) store16(dx + c, v);
+    }
+  }
+  if (p.part)
+    join_columns<kN * V>(p, [&](int e) { return ((e / V) * g.size + t) * V + e % V; }, [&](int e) { return elem(sw, e); });
+}
+
+// Rows of any alignment, through shared memory (fetch_row): a thread's columns are `size`
+// apart.
+template <typename T, int E>
+__global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_odd_kernel(const RmsBwd p, int slot) {
+  extern __shared__ uint4 dyn[];
+  __shared__ float red[2][RMS_GROUPS][16];
+  constexpr int R = RMS_RING;
+  const RowThreads g{(int)threadIdx.x, (int)blockDim.x, 1 + (int)threadIdx.y};
+  const int t = g.t, S = p.dtotal ? 3 : 2;
+  const float inv = 1.f / (float)p.dim;
+  const long long step = (long long)gridDim.x * blockDim.y;
+  long long r = (long long)blockIdx.x * blockDim.y + threadIdx.y, rf = r;
+  // [slot][stream], and a row that waits to be stored
+  uint8_t* mine = reinterpret_cast<uint8_t*>(dyn) + (size_t)threadIdx.y * (R * S + 1) * slot;
+  T* out = reinterpret_cast<T*>(mine + R * S * slot);
+  float w[E], sw[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = e * g.size + t;
+    w[e] = c < p.dim ? (p.w ? ld_w(p.w, p.w_bf16, c) : 1.f) : 0.f;
+    sw[e] = 0.f;
+  }
+  auto fetch = [&](int s) {
+    if (rf < p.rows) {
+      uint8_t* o = mine + s * S * slot;
+      fetch_row(reinterpret_cast<T*>(o), static_cast<const T*>(p.t) + rf * p.ldt, p.dim, t, g.size);
+      fetch_row(reinterpret_cast<T*>(o + slot), static_cast<const T*>(p.dy) + rf * p.lddy, p.dim, t, g.size);
+      if (S == 3)
+        fetch_row(reinterpret_cast<T*>(o + 2 * slot), static_cast<const T*>(p.dtotal) + rf * p.lddt, p.dim, t, g.size);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    rf += step;
+  };
+  for (int s = 0; s < R - 1; ++s) fetch(s);
+  float rs_n = r < p.rows ? p.rstd[r] : 0.f;
+  int parity = 0, at = 0;
+  for (; r < p.rows; r += step) {
+    fetch(at == 0 ? R - 1 : at - 1);
+    const float rs = rs_n;
+    if (r + step < p.rows) rs_n = p.rstd[r + step];
+    asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
+    g.sync();                                   // everyone's copies of this row are there
+    const uint8_t* o = mine + at * S * slot;
+    at = at + 1 == R ? 0 : at + 1;
+    const T* tr = reinterpret_cast<const T*>(o) + behind(static_cast<const T*>(p.t) + r * p.ldt);
+    const T* gr = reinterpret_cast<const T*>(o + slot) + behind(static_cast<const T*>(p.dy) + r * p.lddy);
+    const T* dr = reinterpret_cast<const T*>(o + 2 * slot);
+    if (S == 3) dr += behind(static_cast<const T*>(p.dtotal) + r * p.lddt);
+    float xh[E], gw[E], s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = e * g.size + t;
+      const bool in = c < p.dim;
+      xh[e] = in ? to_f32(tr[c]) * rs : 0.f;
+      gw[e] = in ? to_f32(gr[c]) : 0.f;
+      sw[e] = fmaf(gw[e], xh[e], sw[e]);
+      gw[e] *= w[e];
+      s = fmaf(gw[e], xh[e], s);
+    }
+    const float m = -rs * (g.sum(s, red[parity][threadIdx.y]) * inv);
+    parity ^= 1;
+    T* dx = static_cast<T*>(p.dx) + r * p.lddx;
+    T* to = out + behind(dx);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = e * g.size + t;
+      if (c < p.dim) {
+        const float v = fmaf(gw[e], rs, xh[e] * m);
+        to[c] = from_f32<T>(S == 3 ? to_f32(dr[c]) + v : v);
+      }
+    }
+    g.sync();
+    flush_row(dx, out, p.dim, t, g.size);
+  }
+  if (p.part) join_columns<E>(p, [&](int e) { return e * g.size + t; }, [&](int e) { return sw[e]; });
+}
+
+// Rows wider than that: dx, a CTA a row with the row in registers, and the columns' sums over
+// slabs of rows in a pass of their own.
+template <typename T, int kN>
+__global__ void __launch_bounds__(RMS_MOST_THREADS) rms_dx_kernel(const RmsBwd p) {
+  constexpr int V = 16 / (int)sizeof(T), C = V / 2;
+  __shared__ float red[16];
+  const RowThreads g{(int)threadIdx.x, (int)blockDim.x, 0};
+  const long long r = blockIdx.x;
+  Raw<T, V, kN> a, b;
+  a.load(static_cast<const T*>(p.t) + r * p.ldt, g.t, g.size, p.dim);
+  b.load(static_cast<const T*>(p.dy) + r * p.lddy, g.t, g.size, p.dim);
+  const float rs = p.rstd[r];
+  f32x2 s = both(0.f);
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    f32x2 x[C], y[C], w[C];
+    a.get(k, x);
+    b.get(k, y);
+    weights<V>(p.w, p.w_bf16, (k * g.size + g.t) * V, p.dim, 1.f, w);
+#pragma unroll
+    for (int i = 0; i < C; ++i) s = fma2(mul2(y[i], w[i]), mul2(x[i], both(rs)), s);
+  }
+  a.hold();
+  b.hold();
+  const float m = -rs * (g.sum(lo2(s) + hi2(s), red) * (1.f / (float)p.dim));
+  T* dx = static_cast<T*>(p.dx) + r * p.lddx;
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const int c = (k * g.size + g.t) * V;
+    if (c >= p.dim) continue;
+    f32x2 x[C], y[C], w[C];
+    a.get(k, x);
+    b.get(k, y);
+    weights<V>(p.w, p.w_bf16, c, p.dim, 1.f, w);
+#pragma unroll
+    for (int i = 0; i < C; ++i) y[i] = fma2(mul2(y[i], w[i]), both(rs), mul2(mul2(x[i], both(rs)), both(m)));
+    if (p.dtotal) {
+      widen(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.dtotal) + r * p.lddt + c), x, static_cast<const T*>(nullptr));
+#pragma unroll
+      for (int i = 0; i < C; ++i) y[i] = add2(x[i], y[i]);
+    }
+    store16(dx + c, y);
+  }
+}
+template <typename T>
+__global__ void __launch_bounds__(512) rms_dx_odd_kernel(const RmsBwd p, int slot) {
+  extern __shared__ uint4 dyn[];
+  __shared__ float red[16];
+  const RowThreads g{(int)threadIdx.x, (int)blockDim.x, 0};
+  const long long r = blockIdx.x;
+  uint8_t* mine = reinterpret_cast<uint8_t*>(dyn);
+  const T* src[3] = {static_cast<const T*>(p.t) + r * p.ldt, static_cast<const T*>(p.dy) + r * p.lddy,
+                     p.dtotal ? static_cast<const T*>(p.dtotal) + r * p.lddt : nullptr};
+  const T* at[3] = {};
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (src[i]) {
+      T* o = reinterpret_cast<T*>(mine + i * slot);
+      fetch_row(o, src[i], p.dim, g.t, g.size);
+      at[i] = o + behind(src[i]);
+    }
+  T* dx = static_cast<T*>(p.dx) + r * p.lddx;
+  T* out = reinterpret_cast<T*>(mine + (p.dtotal ? 3 : 2) * slot);
+  const float rs = p.rstd[r];
+  copies_done();
+  g.sync();
+  float s = 0.f;
+#pragma unroll 4
+  for (int c = g.t; c < p.dim; c += g.size)
+    s = fmaf(to_f32(at[1][c]) * (p.w ? ld_w(p.w, p.w_bf16, c) : 1.f), to_f32(at[0][c]) * rs, s);
+  const float m = -rs * (g.sum(s, red) * (1.f / (float)p.dim));
+  T* to = out + behind(dx);
+#pragma unroll 4
+  for (int c = g.t; c < p.dim; c += g.size) {
+    const float v = fmaf(to_f32(at[1][c]) * (p.w ? ld_w(p.w, p.w_bf16, c) : 1.f), rs, to_f32(at[0][c]) * rs * m);
+    to[c] = from_f32<T>(p.dtotal ? to_f32(at[2][c]) + v : v);
+  }
+  g.sync();
+  flush_row(dx, out, p.dim, g.t, g.size);
+}
+// kV columns a thread.
+constexpr int RMS_SLAB_THREADS = 128;
+template <typename T, int kV>
+__global__ void __launch_bounds__(RMS_SLAB_THREADS) rms_slab_kernel(const RmsBwd p) {
+  constexpr int P = (kV + 1) / 2;
+  const int c = (blockIdx.x * RMS_SLAB_THREADS + threadIdx.x) * kV;
+  if (c >= p.dim) return;
+  f32x2 s[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) s[i] = both(0.f);
+  constexpr int H = 4;                 // rows in flight
+  for (long long r0 = blockIdx.y; r0 < p.rows; r0 += (long long)gridDim.y * H) {
+    Raw<T, kV, 1> a[H], b[H];
+    float rs[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const long long r = r0 + (long long)gridDim.y * h, q = r < p.rows ? r : r0;
+      a[h].template load<1>(static_cast<const T*>(p.t) + q * p.ldt + c, 0, 1, p.dim);
+      b[h].template load<1>(static_cast<const T*>(p.dy) + q * p.lddy + c, 0, 1, p.dim);
+      rs[h] = r < p.rows ? p.rstd[r] : 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      if (h > 0 && r0 + (long long)gridDim.y * h >= p.rows) break;
+      f32x2 x[P], y[P];
+      a[h].get(0, x);
+      b[h].get(0, y);
+#pragma unroll
+      for (int i = 0; i < P; ++i) s[i] = fma2(y[i], mul2(x[i], both(rs[h])), s[i]);
+    }
+  }
+  float* o = p.part + (size_t)blockIdx.y * p.dim + c;
+#pragma unroll
+  for (int e = 0; e < kV; ++e) o[e] = elem(s, e);
+}
+
+// Rows of any length: dx with the row read twice.
 template <typename T>
 __global__ void __launch_bounds__(RMS_LOOP_THREADS) rms_backward_loop_kernel(const RmsBwd p) {
   __shared__ float red[32];
@@ -125,16 +687,6 @@ __global__ void __launch_bounds__(RMS_LOOP_THREADS) rms_backward_loop_kernel(con
     st1(dx + c, dt ? v + ld1(dt + c) : v);
   }
 }
-constexpr int RMS_SLAB_THREADS = 256;
-template <typename T>
-__global__ void __launch_bounds__(RMS_SLAB_THREADS) rms_slab_kernel(const RmsBwd p) {
-  const int c = blockIdx.x * RMS_SLAB_THREADS + threadIdx.x;
-  if (c >= p.dim) return;
-  float s = 0.f;
-  for (long long r = blockIdx.y; r < p.rows; r += gridDim.y)
-    s = fmaf(ld1(static_cast<const T*>(p.dy) + r * p.lddy + c), ld1(static_cast<const T*>(p.t) + r * p.ldt + c) * p.rstd[r], s);
-  p.part[(size_t)blockIdx.y * p.dim + c] = s;
-}
 
 // Column sums of the lines: 32 columns a CTA, 32 threads a column over the lines (each a
 // fixed set), then a fixed tree.
@@ -152,23 +704,142 @@ __global__ void __launch_bounds__(1024) rms_columns_kernel(const float* part, in
   if (threadIdx.x == 0 && oc < dim) st_w(dw, w_bf16, oc, s);
 }
 
-template <typename T>
-void forward(const RmsFwd& p, cudaStream_t s) {
-  count_launch();
-  rms_forward_loop_kernel<T><<<(unsigned)p.rows, RMS_LOOP_THREADS, 0, s>>>(p);
+template <typename T, int kN, bool kWarp, bool kEight>
+void forward_launch(const RmsFwd& p, int threads, cudaStream_t s) {
+  const unsigned grid = (unsigned)(kWarp ? cdiv(p.rows, RMS_WARPS) : p.rows);
+  if constexpr (kWarp) {
+    if (p.w && p.w_bf16) { rms_forward_kernel<T, kN, kWarp, W_BF16, kEight><<<grid, threads, 0, s>>>(p); return; }
+    if (p.w) { rms_forward_kernel<T, kN, kWarp, W_F32, kEight><<<grid, threads, 0, s>>>(p); return; }
+  }
+  rms_forward_kernel<T, kN, kWarp, W_ASK, kEight><<<grid, threads, 0, s>>>(p);
 }
 
+// Threads of a row of so many elements through shared memory: 16 elements each.
+int odd_threads(int dim) { return std::min(512, 32 * cdiv(dim, 512)); }
+
+// A warp a row while a lane holds its share of x and of the residual in registers (8 vectors
+// each: 2048 bf16 columns), then a CTA a row with 4 to 8 vectors a thread.
+template <typename T, bool kEight>
+cudaError_t forward(const RmsFwd& p, bool vec, cudaStream_t s) {
+  constexpr int V = vec_of<T>();
+  const int n = p.dim / V, need = cdiv(n, 32), slot = slot_bytes<T>(std::min(p.dim, 1 << 20)), slots = p.r ? 3 : 2;
+  count_launch();
+  if (vec && need <= 8) {
+    by_accesses(need, [&](auto N) {
+      if constexpr (decltype(N)::value <= 8) forward_launch<T, decltype(N)::value, true, kEight>(p, 32 * RMS_WARPS, s);
+    });
+  } else if (vec && n <= 8 * RMS_MOST_THREADS) {
+    int threads = 64;
+    while (threads * 8 < n) threads *= 2;
+    const int each = cdiv(n, threads);
+    if (each <= 5) forward_launch<T, 5, false, kEight>(p, threads, s);
+    else if (each == 6) forward_launch<T, 6, false, kEight>(p, threads, s);
+    else forward_launch<T, 8, false, kEight>(p, threads, s);
+  } else if ((long long)slots * slot <= RMS_ODD_SMEM) {
+    const int threads = odd_threads(p.dim);
+    // a few rows a CTA, as long as an SM still holds several CTAs
+    const int groups = std::max(1, std::min(std::min(256 / threads, RMS_ODD_GROUPS), 48 * 1024 / (slots * slot)));
+    const int smem = groups * slots * slot;
+    if (smem > 40 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(rms_forward_odd_kernel<T, kEight>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, RMS_ODD_SMEM);
+      if (e != cudaSuccess) return e;
+    }
+    rms_forward_odd_kernel<T, kEight><<<cdiv(p.rows, groups), dim3(threads, groups), smem, s>>>(p, slot);
+  } else {
+    rms_forward_loop_kernel<T><<<(unsigned)p.rows, RMS_LOOP_THREADS, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+template <class K>
+cudaError_t allow_smem(K kern, size_t smem) {
+  return smem <= 40 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RMS_ODD_SMEM);
+}
+
+// Row groups of a persistent CTA of so many threads a row and bytes of shared memory a group.
+int row_groups(int threads, size_t bytes, const RmsBwd& p, size_t* smem) {
+  int groups = std::max(1, std::min(RMS_BWD_THREADS / threads, RMS_GROUPS));
+  auto need = [&](int g) { return std::max(bytes * g, p.part ? (size_t)(g - 1) * p.dim * 4 : 0); };
+  while (groups > 1 && need(groups) > (size_t)RMS_ODD_SMEM) --groups;
+  *smem = need(groups);
+  return groups;
+}
+
+template <typename T, int kN>
+cudaError_t backward_vec(const RmsBwd& p, int threads, int* lines, cudaStream_t s) {
+  auto go = [&](auto kern, int ring, int streams) {
+    size_t smem = 0;
+    const int groups = row_groups(threads, (size_t)ring * streams * kN * 16 * threads, p, &smem);
+    const cudaError_t e = allow_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    *lines = (int)std::min<long long>(cdiv(p.rows, groups), RMS_CTAS);
+    count_launch();
+    kern<<<*lines, dim3(threads, groups), smem, s>>>(p);
+    return cudaGetLastError();
+  };
+  if (!p.dtotal) return go(rms_backward_kernel<T, kN, false, RMS_RING>, RMS_RING, 2);
+  // (three streams of more than 5460 fp32 columns fill the memory with a row less ahead)
+  if ((size_t)RMS_RING * 3 * kN * 16 * threads > (size_t)RMS_ODD_SMEM) return go(rms_backward_kernel<T, kN, true, 2>, 2, 3);
+  return go(rms_backward_kernel<T, kN, true, RMS_RING>, RMS_RING, 3);
+}
+template <typename T, int E>
+cudaError_t backward_odd(const RmsBwd& p, int threads, int* lines, cudaStream_t s) {
+  size_t smem = 0;
+  const int slot = slot_bytes<T>(p.dim);
+  const int groups = row_groups(threads, (size_t)(RMS_RING * (p.dtotal ? 3 : 2) + 1) * slot, p, &smem);
+  if (smem > (size_t)RMS_ODD_SMEM) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = allow_smem(rms_backward_odd_kernel<T, E>, smem);
+  if (e != cudaSuccess) return e;
+  *lines = (int)std::min<long long>(cdiv(p.rows, groups), RMS_CTAS);
+  count_launch();
+  rms_backward_odd_kernel<T, E><<<*lines, dim3(threads, groups), smem, s>>>(p, slot);
+  return cudaGetLastError();
+}
+
+// 16 columns a thread (registers hold their sums, weights and the row), 8 for rows that 16
+// would leave to less than two warps; of any alignment 8, 12 or 16, whichever leaves the
+// fewest places empty.
 template <typename T>
-cudaError_t backward(const RmsBwd& p, int* lines, cudaStream_t s) {
+cudaError_t backward(const RmsBwd& p, bool vec, int* lines, cudaStream_t s) {
+  constexpr int V = vec_of<T>();
   *lines = 0;
   if (p.rows == 0) return cudaSuccess;
-  if (p.part) {       // before dx, which may be dy itself
-    *lines = (int)std::min<long long>(p.rows, RMS_CTAS);
-    rms_slab_kernel<T><<<dim3(cdiv(p.dim, RMS_SLAB_THREADS), *lines), RMS_SLAB_THREADS, 0, s>>>(p);
-    count_launch();
+  const int n = p.dim / V;
+  auto threads = [&](int each) { return 32 * cdiv(vec ? n : p.dim, 32LL * each); };
+  if (vec && n <= 32 * 16 / V) return backward_vec<T, 8 / V>(p, threads(8 / V), lines, s);
+  if (vec && threads(16 / V) <= RMS_BWD_THREADS) return backward_vec<T, 16 / V>(p, threads(16 / V), lines, s);
+  const bool fits = (size_t)(RMS_RING * (p.dtotal ? 3 : 2) + 1) * slot_bytes<T>(std::min(p.dim, 1 << 16)) <= (size_t)RMS_ODD_SMEM;
+  if (!vec && threads(16) <= RMS_BWD_THREADS && fits) {
+    if (p.dim <= 64) return backward_odd<T, 2>(p, 32, lines, s);
+    if (p.dim <= 128) return backward_odd<T, 4>(p, 32, lines, s);
+    int best = 16;
+    for (int e : {12, 8})
+      if (threads(e) <= RMS_BWD_THREADS && threads(e) * e < threads(best) * best) best = e;
+    if (best == 8) return backward_odd<T, 8>(p, threads(8), lines, s);
+    if (best == 12) return backward_odd<T, 12>(p, threads(12), lines, s);
+    return backward_odd<T, 16>(p, threads(16), lines, s);
   }
-  rms_backward_loop_kernel<T><<<(unsigned)p.rows, RMS_LOOP_THREADS, 0, s>>>(p);
+  // the columns' sums before dx, which may be dy itself
+  if (p.part) {
+    *lines = (int)std::min<long long>(p.rows, RMS_CTAS);
+    count_launch();
+    if (vec) rms_slab_kernel<T, V><<<dim3(cdiv(n, RMS_SLAB_THREADS), *lines), RMS_SLAB_THREADS, 0, s>>>(p);
+    else rms_slab_kernel<T, 1><<<dim3(cdiv(p.dim, RMS_SLAB_THREADS), *lines), RMS_SLAB_THREADS, 0, s>>>(p);
+  }
   count_launch();
+  const size_t smem = (size_t)(p.dtotal ? 4 : 3) * slot_bytes<T>(std::min(p.dim, 1 << 20));
+  if (vec && n <= 4 * RMS_MOST_THREADS) {
+    rms_dx_kernel<T, 4><<<(unsigned)p.rows, 32 * cdiv(n, 128), 0, s>>>(p);
+  } else if (vec && n <= 8 * RMS_MOST_THREADS) {
+    rms_dx_kernel<T, 8><<<(unsigned)p.rows, 32 * cdiv(n, 256), 0, s>>>(p);
+  } else if (smem <= (size_t)RMS_ODD_SMEM) {
+    const cudaError_t e = allow_smem(rms_dx_odd_kernel<T>, smem);
+    if (e != cudaSuccess) return e;
+    rms_dx_odd_kernel<T><<<(unsigned)p.rows, odd_threads(p.dim), smem, s>>>(p, slot_bytes<T>(p.dim));
+  } else {
+    rms_backward_loop_kernel<T><<<(unsigned)p.rows, RMS_LOOP_THREADS, 0, s>>>(p);
+  }
   return cudaGetLastError();
 }
 
@@ -197,9 +868,12 @@ extern "C" int muon_rmsnorm_forward(const void* x, int64_t ldx, const void* resi
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const RmsFwd p{x, residual, weight, total, y, codes, scales, rstd, ldx, ldr, ldt, ldy, ldc, rows,
                  (int)dim, w_dtype == MUON_DTYPE_BF16, cdiv(dim, RMS_GROUP), eps};
-  if (x_dtype == MUON_DTYPE_BF16) forward<bf16>(p, s);
-  else forward<float>(p, s);
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  const bool vec = dim * xs % 16 == 0 && vec_rows(x, ldx, rows, xs) && (!residual || vec_rows(residual, ldr, rows, xs)) &&
+                   (!total || vec_rows(total, ldt, rows, xs)) && (!y || vec_rows(y, ldy, rows, xs)) &&
+                   is_aligned(weight, 16) && (!codes || (is_aligned(codes, 16 / xs) && (rows == 1 || ldc % (16 / xs) == 0)));
+  const cudaError_t e = x_dtype == MUON_DTYPE_BF16 ? (codes ? forward<bf16, true>(p, vec, s) : forward<bf16, false>(p, vec, s))
+                                                   : (codes ? forward<float, true>(p, vec, s) : forward<float, false>(p, vec, s));
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 extern "C" size_t muon_rmsnorm_workspace_size(int64_t rows, int64_t dim) {
@@ -230,8 +904,10 @@ extern "C" int muon_rmsnorm_backward(const void* dy, int64_t lddy, const void* t
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const RmsBwd p{dy, total, weight, dtotal, rstd, dx, dweight ? static_cast<float*>(ws) : nullptr, lddy, ldt, lddt, lddx,
                  rows, (int)dim, w_dtype == MUON_DTYPE_BF16};
+  const bool vec = dim * xs % 16 == 0 && vec_rows(total, ldt, rows, xs) && vec_rows(dy, lddy, rows, xs) &&
+                   vec_rows(dx, lddx, rows, xs) && (!dtotal || vec_rows(dtotal, lddt, rows, xs)) && is_aligned(weight, 16);
   int lines = 0;
-  if ((x_dtype == MUON_DTYPE_BF16 ? backward<bf16>(p, &lines, s) : backward<float>(p, &lines, s)) != cudaSuccess)
+  if ((x_dtype == MUON_DTYPE_BF16 ? backward<bf16>(p, vec, &lines, s) : backward<float>(p, vec, &lines, s)) != cudaSuccess)
     return MUON_ERR_CUDA;
   if (dweight) {
     count_launch();
