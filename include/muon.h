@@ -346,7 +346,7 @@ int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse, const flo
  * -1 and minus infinity.  A row of nothing but minus infinities has lse minus infinity,
  * logprob and entropy NaN and no alternatives; a NaN or +Inf logit makes the row's lse,
  * logprob, entropy and alternatives NaN and its ids -1.  Logits are summed as for the cross entropy; those near the top are summed
- * again, to 2^-45 (64 bits for 32-bit operands), and ranked by that.  logprob, entropy, lse
+ * again, to 2^-45, and ranked by that.  logprob, entropy, lse
  * and alternatives are device fp32, ids device int64.  logprob may be NULL without tokens,
  * ids and alternatives with top == 0. */
 #define MUON_LOGPROB_MAX_TOP 32

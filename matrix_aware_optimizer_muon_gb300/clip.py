@@ -9,10 +9,18 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import _check, _dt, load_library
+from ._lib import _check, load_library
 from .head import _on, _on_current, _stream
 
 _GRAD = np.dtype([("G", "u8"), ("numel", "i8"), ("dtype", "i4"), ("reserved", "i4")])
+
+
+def _code(dtype: torch.dtype) -> int:
+    if dtype == torch.bfloat16:
+        return _lib.MUON_DTYPE_BF16
+    if dtype == torch.float32:
+        return _lib.MUON_DTYPE_F32
+    raise TypeError(f"unsupported dtype {dtype}")
 
 
 def alloc_clip_workspace(device=None) -> torch.Tensor:
@@ -26,10 +34,9 @@ def muon_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: Optional[float]
     where it is above max_norm, they are scaled in place by max_norm/norm.  None or infinity
     computes the norm alone.  Returns the norm, one fp32 number on the device: nothing waits
     for it."""
-    grads = list(grads)
-    T = torch.Tensor
-    here = ws.get_device()
-    if not ws.is_cuda or any(d != here for d in map(T.get_device, grads)):
+    T, grads = torch.Tensor, list(grads)
+    # one pass of a C function over the list for each property
+    if not ws.is_cuda or not set(map(T.get_device, grads)) <= {ws.get_device()}:
         raise ValueError("gradients and workspace must be on one CUDA device")
     _on_current(ws)
     if not all(map(T.is_contiguous, grads)):
@@ -37,7 +44,7 @@ def muon_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: Optional[float]
     arr = np.zeros(max(len(grads), 1), dtype=_GRAD)
     if grads:
         kinds = list(map(T.dtype.__get__, grads))
-        codes = {k: _dt(g) for k, g in zip(kinds, grads)}
+        codes = {k: _code(k) for k in set(kinds)}
         arr["G"], arr["numel"] = list(map(T.data_ptr, grads)), list(map(T.numel, grads))
         arr["dtype"] = [codes[k] for k in kinds] if len(codes) > 1 else codes[kinds[0]]
     with _on(stream):

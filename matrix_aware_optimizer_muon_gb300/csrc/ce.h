@@ -24,9 +24,8 @@ enum Kind : int {
   POLICY = 5    // GRAD of log probabilities and entropies
 };
 
-// The two largest logits of 32 columns as keys: the lowest KEY_BITS bits of the number hold
+// The two largest logits of 32 columns as keys: the number's lowest 5 bits hold
 // 31 minus the column, so that two maxima a logit find them without carrying an index.
-// (An infinity becomes a NaN, which a maximum passes over.)
 constexpr int KEY_COLS = 32;
 constexpr unsigned KEY_MASK = KEY_COLS - 1;
 

@@ -351,53 +351,91 @@ __device__ __forceinline__ void finish_logits(const Params& p, const Work& J, co
   }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// The two largest of 32 columns' keys, as a tournament (77 instructions, a running pair takes
+// 96 and waits for each).
+__device__ __forceinline__ float2 largest_two(const float (&v)[32]) {
+  float a[16], b[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float x = __uint_as_float((__float_as_uint(v[2 * i]) & ~KEY_MASK) | (KEY_MASK - 2 * i));
+    const float y = __uint_as_float((__float_as_uint(v[2 * i + 1]) & ~KEY_MASK) | (KEY_MASK - 2 * i - 1));
+    a[i] = fmaxf(x, y);
+    b[i] = fminf(x, y);
+  }
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        b[i] = max3(fminf(a[i], a[i + n]), b[i], b[i + n]);
+        a[i] = fmaxf(a[i], a[i + n]);
+      }
+  return make_float2(a[0], b[0]);
+}
+
 // The statistics of the log probabilities over this thread's 128 columns: max, sum of
 // exponentials, their sum times the distance from the max (for the entropy), the token's
 // logit and, where alternatives are asked for, the two largest logits of each 32 columns.
+// Columns past the end are masked like any other.
 __device__ __forceinline__ void finish_logprob(const Params& p, const Work& J, const Tile& ti, int half, int r, int cbase,
-                                               const float (&acc)[CHUNKS][32]) {
+                                               float (&acc)[CHUNKS][32]) {
   if (r >= J.m) return;
   const int cols = J.n - cbase;
-  float mx = -INFINITY;
+  if (cols < HALF) {
 #pragma unroll
-  for (int k = 0; k < CHUNKS; ++k)
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (k * 32 + j < cols) mx = fmaxf(mx, acc[k][j]);
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  float s = 0.f, t = 0.f;
-#pragma unroll
-  for (int k = 0; k < CHUNKS; ++k) {
-    float q = 0.f, u = 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (k * 32 + j < cols) {
-        const float d = acc[k][j] - ref, e = __expf(d);
-        q += e;
-        u = fmaf(e, fmaxf(d, LOG_FLOOR), u);
-      }
-    s += q;
-    t += u;
-  }
-  p.stat[(size_t)r * (2 * J.ntiles) + 2 * ti.tn + half] = make_float4(mx, s, t, 0.f);
-  if (p.keys) {
-    float2 top[CHUNKS];
-#pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) {
-      float a = -INFINITY, b = -INFINITY;
+    for (int k = 0; k < CHUNKS; ++k)
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (k * 32 + j < cols) {
-          const float key = __uint_as_float((__float_as_uint(acc[k][j]) & ~KEY_MASK) | (KEY_MASK - j));
-          b = fmaxf(b, fminf(a, key));
-          a = fmaxf(a, key);
-        }
-      top[k] = make_float2(a, b);
-    }
-    float4* o = reinterpret_cast<float4*>(p.keys + ((size_t)r * (2 * J.ntiles) + 2 * ti.tn + half) * CHUNKS);
-#pragma unroll
-    for (int k = 0; k < CHUNKS; k += 2) o[k / 2] = make_float4(top[k].x, top[k].y, top[k + 1].x, top[k + 1].y);
+        if (k * 32 + j >= cols) acc[k][j] = -INFINITY;
   }
+  float top[CHUNKS];
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k) {
+    top[k] = fmaxf(acc[k][0], acc[k][1]);
+#pragma unroll
+    for (int j = 2; j < 32; j += 2) top[k] = max3(top[k], acc[k][j], acc[k][j + 1]);
+  }
+  const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  f32x2 s[CHUNKS], t[CHUNKS];
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k) s[k] = t[k] = both(0.f);
+#pragma unroll
+  for (int j = 0; j < 32; j += 2)
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) {
+      const f32x2 d = add2(make2(acc[k][j], acc[k][j + 1]), both(-ref));
+      const f32x2 x = mul2(d, both(1.4426950408889634f));
+      const f32x2 e = make2(exp2_approx(lo2(x)), exp2_approx(hi2(x)));
+      s[k] = add2(s[k], e);
+      t[k] = fma2(e, d, t[k]);
+    }
+  const f32x2 ss = add2(add2(s[0], s[1]), add2(s[2], s[3])), tt = add2(add2(t[0], t[1]), add2(t[2], t[3]));
+  const float sum = lo2(ss) + hi2(ss);
+  float far = lo2(tt) + hi2(tt);
+  const bool masked = far != far;   // columns of minus infinity: 0 times that
+  if (masked && sum == sum) {
+    far = 0.f;
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float d = acc[k][j] - ref;
+        far = fmaf(__expf(d), fmaxf(d, LOG_FLOOR), far);
+      }
+  }
+  const size_t at128 = (size_t)r * (2 * J.ntiles) + 2 * ti.tn + half;
+  p.stat[at128] = make_float4(mx, sum, far, 0.f);
   const long long at = p.labels ? p.labels[r] - cbase : -1;
   if (at >= 0 && at < HALF && at < cols) {
     float z = 0.f;
@@ -407,6 +445,21 @@ __device__ __forceinline__ void finish_logprob(const Params& p, const Work& J, c
       for (int j = 0; j < 32; ++j)
         if (k * 32 + j == (int)at) z = acc[k][j];
     p.zlabel[r] = z;
+  }
+  if (p.keys) {
+    // a key of minus infinity would be a NaN, which a minimum passes over too
+    if (masked) {
+#pragma unroll
+      for (int k = 0; k < CHUNKS; ++k)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[k][j] = fmaxf(acc[k][j], -0x1.fffffep127f);
+    }
+    float2 two[CHUNKS];
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) two[k] = largest_two(acc[k]);
+    float4* o = reinterpret_cast<float4*>(p.keys + at128 * CHUNKS);
+#pragma unroll
+    for (int k = 0; k < CHUNKS; k += 2) o[k / 2] = make_float4(two[k].x, two[k].y, two[k + 1].x, two[k + 1].y);
   }
 }
 

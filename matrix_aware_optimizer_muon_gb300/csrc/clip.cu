@@ -18,9 +18,12 @@ namespace {
 constexpr int CL_THREADS = 256;
 constexpr int CL_HELD = 8;                                  // 16-byte vectors a thread holds at a time
 constexpr int CL_VECS = CL_THREADS * CL_HELD;               // vectors of a chunk (32 KB)
-constexpr int CL_CTAS_PER_SM = 4;
+// CTAs an SM: registers for the vectors, and for the scaling some more.
+constexpr int CL_NORM_CTAS = 4, CL_SCALE_CTAS = 3;
 constexpr int CL_MAX_CTAS = 1024;
-constexpr int CL_ENTRIES = 1000;                            // tensors of a launch (parameter table)
+// Tensors of a launch.  The table travels in the kernel's parameters, and a launch is charged
+// for all of them (48 tensors: 8 us a call less with the small one).
+constexpr int CL_ENTRIES = 1000, CL_FEW = 64;
 
 // Chunks are counted from the 16-byte boundary at or below a tensor's first element, so that
 // tensors of any alignment move in whole vectors but for their ends.
@@ -31,6 +34,7 @@ struct ClipEntry {
   int begin;            // first chunk of the launch
   int bf16_;
 };
+template <int kEntries>
 struct ClipParams {
   int n, chunks, ctas;
   int add;                         // partial sums of an earlier launch are already there
@@ -38,12 +42,18 @@ struct ClipParams {
   double* part;
   double max_norm;
   float* norm;
-  ClipEntry e[CL_ENTRIES];
+  ClipEntry e[kEntries];
 };
-static_assert(sizeof(ClipParams) < 32700, "ClipParams too large");
+static_assert(sizeof(ClipParams<CL_ENTRIES>) < 32700, "ClipParams too large");
 
-__device__ __forceinline__ int entry_of(const ClipParams& p, int chunk) {
+// The chunk's tensor, given that of an earlier chunk: mostly the same or the next one.
+template <class P>
+__device__ __forceinline__ int entry_of(const P& p, int chunk, int from) {
   int lo = 0, hi = p.n - 1;
+  if (p.e[from].begin <= chunk) {
+    if (from == hi || p.e[from + 1].begin > chunk) return from;
+    lo = from + 1;
+  }
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.e[mid].begin <= chunk) lo = mid; else hi = mid - 1;
@@ -127,13 +137,16 @@ __device__ __forceinline__ double cta_sum(double v, double* red) {
 
 // Partial sums: a CTA's chunks are the same in every run, so the norm repeats bit for bit.
 // A thread's up to 64 squares are added in fp32, everything above in 64 bits.
-__global__ void __launch_bounds__(CL_THREADS, CL_CTAS_PER_SM) clip_norm_kernel(const __grid_constant__ ClipParams p) {
+template <class P>
+__global__ void __launch_bounds__(CL_THREADS, CL_NORM_CTAS) clip_norm_kernel(const __grid_constant__ P p) {
   __shared__ double red[CL_THREADS / 32];
   allow_next();
   await_previous();
   double acc = 0.0;
+  int at = 0;
   for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
-    const ClipEntry& e = p.e[entry_of(p, c)];
+    at = entry_of(p, c, at);
+    const ClipEntry& e = p.e[at];
     const long long v0 = (long long)(c - e.begin) * CL_VECS;
     uint4 q[CL_HELD];
     if (e.bf16_) {
@@ -181,7 +194,8 @@ __device__ __forceinline__ void scale_share(const ClipEntry& e, long long v0, fl
 
 // norm and, where it is above max_norm, the scaling.  The chunks are taken from the last to
 // the first: the norm's pass has left the last ones in L2.
-__global__ void __launch_bounds__(CL_THREADS, CL_CTAS_PER_SM) clip_scale_kernel(const __grid_constant__ ClipParams p) {
+template <class P>
+__global__ void __launch_bounds__(CL_THREADS, CL_SCALE_CTAS) clip_scale_kernel(const __grid_constant__ P p) {
   __shared__ double red[CL_THREADS / 32];
   await_previous();
   double s = 0.0;
@@ -190,8 +204,10 @@ __global__ void __launch_bounds__(CL_THREADS, CL_CTAS_PER_SM) clip_scale_kernel(
   if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
   if (p.only || norm <= p.max_norm) return;      // a NaN goes on, and makes every gradient NaN
   const float coef = (float)(p.max_norm / norm);
+  int at = p.n - 1;
   for (int c = p.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
-    const ClipEntry& e = p.e[entry_of(p, c)];
+    if (p.e[at].begin > c) at = at > 0 && p.e[at - 1].begin <= c ? at - 1 : entry_of(p, c, 0);
+    const ClipEntry& e = p.e[at];
     const long long v0 = (long long)(c - e.begin) * CL_VECS;
     if (e.bf16_) scale_share<bf16>(e, v0, coef);
     else scale_share<float>(e, v0, coef);
@@ -247,8 +263,9 @@ extern "C" int muon_clip_grad_norm(const muon_grad* grads, int n, double max_nor
   int sms = 0;
   if (int rc = require_device(&sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int most = std::min(sms * CL_CTAS_PER_SM, CL_MAX_CTAS);
-  static thread_local ClipParams p;
+  const int most = std::min(sms * CL_NORM_CTAS, CL_MAX_CTAS);
+  static thread_local ClipParams<CL_ENTRIES> p;
+  static thread_local ClipParams<CL_FEW> few;
   p.part = static_cast<double*>(ws);
   p.max_norm = max_norm;
   p.only = !std::isfinite(max_norm);
@@ -270,6 +287,23 @@ extern "C" int muon_clip_grad_norm(const muon_grad* grads, int n, double max_nor
     p.n = j;
     p.chunks = (int)chunks;
   };
+  auto launch = [&](bool scale, int grid) {
+    count_launch();
+    if (p.n > CL_FEW)
+      return scale ? launch_after(clip_scale_kernel<ClipParams<CL_ENTRIES>>, dim3(grid), dim3(CL_THREADS), 0, s, p)
+                   : launch_after(clip_norm_kernel<ClipParams<CL_ENTRIES>>, dim3(grid), dim3(CL_THREADS), 0, s, p);
+    few.n = p.n;
+    few.chunks = p.chunks;
+    few.ctas = p.ctas;
+    few.add = p.add;
+    few.only = p.only;
+    few.part = p.part;
+    few.max_norm = p.max_norm;
+    few.norm = p.norm;
+    std::copy(p.e, p.e + p.n, few.e);
+    return scale ? launch_after(clip_scale_kernel<ClipParams<CL_FEW>>, dim3(grid), dim3(CL_THREADS), 0, s, few)
+                 : launch_after(clip_norm_kernel<ClipParams<CL_FEW>>, dim3(grid), dim3(CL_THREADS), 0, s, few);
+  };
   // the norm's launches leave as many partial sums as the largest of them has CTAs
   int launches = 0, i = 0;
   fill(&i);
@@ -280,8 +314,7 @@ extern "C" int muon_clip_grad_norm(const muon_grad* grads, int n, double max_nor
     p.ctas = ctas;
     p.add = launches > 0;
     p.norm = nullptr;
-    count_launch();
-    if (launch_after(clip_norm_kernel, dim3(ctas), dim3(CL_THREADS), 0, s, p) != cudaSuccess) return MUON_ERR_CUDA;
+    if (launch(false, ctas) != cudaSuccess) return MUON_ERR_CUDA;
     ++launches;
     if (i >= n) break;
     fill(&i);
@@ -295,9 +328,8 @@ extern "C" int muon_clip_grad_norm(const muon_grad* grads, int n, double max_nor
     p.ctas = ctas;
     p.norm = k == 0 ? norm : nullptr;
     if (k > 0 && p.only) break;
-    const int grid = p.only ? 1 : std::max(1, std::min(most, p.chunks));
-    count_launch();
-    if (launch_after(clip_scale_kernel, dim3(grid), dim3(CL_THREADS), 0, s, p) != cudaSuccess) return MUON_ERR_CUDA;
+    const int grid = p.only ? 1 : std::max(1, std::min(sms * CL_SCALE_CTAS, p.chunks));
+    if (launch(true, grid) != cudaSuccess) return MUON_ERR_CUDA;
   }
   return MUON_OK;
 }

@@ -48,6 +48,10 @@ constexpr int SEG_BF16 = 20, SEG_F32 = 4;
 // launch of no longer sums takes the form without take-overs; it grows in proportion (2^22
 // rows: 2.4e-2 of dW).
 constexpr int SEG_LONG = 1024;
+// The log probabilities' products: segments of one length, SEG_BF16 steps at most; short ones
+// where a single row of tiles waits for W anyway (one row's log probability may be small against
+// its logits, and the logits' error is its own).
+constexpr int SEG_FEW = 12;
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) logprob_kernel(const LogprobR
 // partial sums, which is enough to swap neighbours, so they only choose candidates, and the
 // candidates' logits are summed again, to 2^-45 of their largest partial sum:
 //   1. a bound from below on the top-th largest logit: the top-th of the threads' largest keys
-//      (two each where there are few);
+//      (two each where there are few), each warp's in order so that few are compared;
 //   2. candidates: columns whose key is not below that by more than MARGIN of the largest
 //      logit, hundreds of times what the logits are off by; of 32 columns whose two keys both
 //      qualify, all (a third may hide behind them);
@@ -354,36 +358,82 @@ __device__ __forceinline__ void add_exact(float& s, float& e, float p) {
   e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(p, b)));
   s = t;
 }
-// Logits as sums of exact products: bf16 ones fit fp32, fp32 ones fit 64 bits.
-__device__ __forceinline__ double logit(const bf16* h, const bf16* w, int dim, int vec, int lane) {
-  float s[2] = {0.f, 0.f}, e[2] = {0.f, 0.f};
-  int c = 0;
-  if (vec) {
-    for (c = lane * 8; c + 8 <= dim; c += 256) {
-      const uint4 a = *reinterpret_cast<const uint4*>(h + c), b = *reinterpret_cast<const uint4*>(w + c);
-      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+// s + e over the warp, in every lane (64-bit additions would hold the warps up).
+__device__ __forceinline__ double warp_exact(float s, float e) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        add_exact(s[0], e[0], __fmul_rn(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16)));
-        add_exact(s[1], e[1], __fmul_rn(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u)));
+  for (int o = 16; o > 0; o >>= 1) {
+    const float so = __shfl_xor_sync(0xffffffffu, s, o), eo = __shfl_xor_sync(0xffffffffu, e, o);
+    add_exact(s, e, so);
+    e = __fadd_rn(e, eo);
+  }
+  return (double)s + (double)e;
+}
+// The logits of a row and N rows of W as sums of exact products: those of bf16 numbers are
+// exact in fp32, those of fp32 ones come in two parts.  LOGIT_HELD vectors are asked for at once.
+constexpr int LOGIT_HELD = 4;
+template <int N>
+__device__ __forceinline__ void logits(const bf16* h, const bf16* const* w, int dim, int vec, int lane, double* out) {
+  float s[N][2] = {}, e[N][2] = {};
+  const int whole = vec ? dim / 8 : 0;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  for (int c0 = lane; c0 < whole; c0 += 32 * LOGIT_HELD) {
+    uint4 a[LOGIT_HELD], b[N][LOGIT_HELD];
+#pragma unroll
+    for (int i = 0; i < LOGIT_HELD; ++i) {
+      const int c = c0 + 32 * i;
+      a[i] = c < whole ? reinterpret_cast<const uint4*>(h)[c] : none;
+#pragma unroll
+      for (int q = 0; q < N; ++q) b[q][i] = c < whole ? reinterpret_cast<const uint4*>(w[q])[c] : none;
+    }
+#pragma unroll
+    for (int i = 0; i < LOGIT_HELD; ++i) {
+      const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        const uint32_t y[4] = {b[q][i].x, b[q][i].y, b[q][i].z, b[q][i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          add_exact(s[q][0], e[q][0], __fmul_rn(__uint_as_float(x[j] << 16), __uint_as_float(y[j] << 16)));
+          add_exact(s[q][1], e[q][1], __fmul_rn(__uint_as_float(x[j] & 0xFFFF0000u), __uint_as_float(y[j] & 0xFFFF0000u)));
+        }
       }
     }
-    c = dim / 8 * 8;
   }
-  for (c += lane; c < dim; c += 32) add_exact(s[0], e[0], __fmul_rn(ld1(h + c), ld1(w + c)));
-  double v = ((double)s[0] + (double)s[1]) + ((double)e[0] + (double)e[1]);
+  for (int c = whole * 8 + lane; c < dim; c += 32)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+    for (int q = 0; q < N; ++q) add_exact(s[q][0], e[q][0], __fmul_rn(ld1(h + c), ld1(w[q] + c)));
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    add_exact(s[q][0], e[q][0], s[q][1]);
+    out[q] = warp_exact(s[q][0], __fadd_rn(e[q][0], e[q][1]));
+  }
 }
-__device__ __forceinline__ double logit(const float* h, const float* w, int dim, int, int lane) {
-  double v = 0.0;
-  for (int c = lane; c < dim; c += 32) v = fma((double)h[c], (double)w[c], v);
+template <int N>
+__device__ __forceinline__ void logits(const float* h, const float* const* w, int dim, int, int lane, double* out) {
+  float s[N] = {}, e[N] = {};
+  for (int c0 = lane; c0 < dim; c0 += 64 * LOGIT_HELD) {
+    float a[2 * LOGIT_HELD], b[N][2 * LOGIT_HELD];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+    for (int i = 0; i < 2 * LOGIT_HELD; ++i) {
+      const int c = c0 + 32 * i;
+      a[i] = c < dim ? h[c] : 0.f;
+#pragma unroll
+      for (int q = 0; q < N; ++q) b[q][i] = c < dim ? w[q][c] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * LOGIT_HELD; ++i)
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        const float x = __fmul_rn(a[i], b[q][i]);
+        e[q] = __fadd_rn(e[q], __fmaf_rn(a[i], b[q][i], -x));   // what the product's rounding dropped
+        add_exact(s[q], e[q], x);
+      }
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q) out[q] = warp_exact(s[q], e[q]);
 }
 
+constexpr int TOP_HELD = 8;                  // pairs of groups whose keys a thread keeps (131072 entries)
 struct TopShared {
   double value[TOP_CANDIDATES];
   int id[TOP_CANDIDATES];
@@ -395,6 +445,18 @@ struct TopShared {
   int count, wholes;
   float bound;
 };
+
+// The warp's numbers in descending order, one a lane.
+__device__ __forceinline__ float sort_lanes(float v, int lane) {
+#pragma unroll
+  for (int n = 2; n <= 32; n *= 2)
+#pragma unroll
+    for (int m = n / 2; m > 0; m /= 2) {
+      const float o = __shfl_xor_sync(0xffffffffu, v, m);
+      v = ((lane & n) == 0) == ((lane & m) == 0) ? fmaxf(v, o) : fminf(v, o);
+    }
+  return v;
+}
 
 // The best `top` of n candidates, in order, to kept_*; the others' places hold -1.  An id of
 // -1, a masked value or a NaN is no candidate.
@@ -418,8 +480,27 @@ __device__ __forceinline__ void rank(TopShared& sh, int n, int top) {
   __syncthreads();
 }
 
+// The values of the first n ids, two of them a warp at a time where there are as many.
 template <typename T>
-__global__ void __launch_bounds__(TOP_THREADS) top_kernel(const LogprobRows p) {
+__device__ __forceinline__ void evaluate(TopShared& sh, int n, const LogprobRows& p, const T* h) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = warp; i < n; i += 2 * TOP_WARPS) {
+    const int j = i + TOP_WARPS, a = sh.id[i], b = j < n ? sh.id[j] : -1;
+    // (an id of -1 has no row; its value is never looked at)
+    const T* w[2] = {static_cast<const T*>(p.W) + max(a, 0) * p.ldw, static_cast<const T*>(p.W) + max(b, 0) * p.ldw};
+    double v[2] = {0.0, 0.0};
+    if (b >= 0) logits<2>(h, w, p.dim, p.vec, lane, v);
+    else if (a >= 0) logits<1>(h, w, p.dim, p.vec, lane, v);
+    if (lane == 0) {
+      sh.value[i] = v[0];
+      if (j < n) sh.value[j] = v[1];
+    }
+  }
+  __syncthreads();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(TOP_THREADS, 3) top_kernel(const LogprobRows p) {
   __shared__ TopShared sh;
   await_previous();
   const long long r = blockIdx.x;
@@ -434,24 +515,35 @@ __global__ void __launch_bounds__(TOP_THREADS) top_kernel(const LogprobRows p) {
   // the thread's two largest keys
   const int groups = p.parts * (TILE / 2 / KEY_COLS);
   const float2* keys = p.keys + (size_t)r * groups;
+  const float4* pairs = reinterpret_cast<const float4*>(keys);
+  float4 held[TOP_HELD];
   float k1 = -INFINITY, k2 = -INFINITY;
-#pragma unroll 4
-  for (int g = t; g < groups; g += TOP_THREADS) {
-    const float2 k = keys[g];
+  auto take = [&](const float4& k) {
     k2 = fmaxf(k2, fmaxf(fminf(k1, k.x), k.y));
     k1 = fmaxf(k1, k.x);
+    k2 = fmaxf(k2, fmaxf(fminf(k1, k.z), k.w));
+    k1 = fmaxf(k1, k.z);
+  };
+#pragma unroll
+  for (int i = 0; i < TOP_HELD; ++i) {
+    const int g = t + i * TOP_THREADS;
+    held[i] = g < groups / 2 ? pairs[g] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
   }
-  sh.key[t] = k1;
-  sh.key[TOP_THREADS + t] = k2;
+#pragma unroll
+  for (int i = 0; i < TOP_HELD; ++i) take(held[i]);
+  for (int g = t + TOP_HELD * TOP_THREADS; g < groups / 2; g += TOP_THREADS) take(pairs[g]);
+  // (few groups: the second largest count, too)
+  const int lists = groups >= 4 * TOP_THREADS ? 1 : 2;
+  sh.key[t] = sort_lanes(k1, lane);
+  if (lists == 2) sh.key[TOP_THREADS + t] = sort_lanes(k2, lane);
+  if (t == 0) sh.bound = -INFINITY;
   __syncthreads();
   Moments all = {-INFINITY, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < TOP_WARPS; ++i) all.m = fmaxf(all.m, sh.warp[i].x);
 #pragma unroll
   for (int i = 0; i < TOP_WARPS; ++i) add_moments(all, sh.warp[i], all.m == -INFINITY ? 0.f : all.m);
-  if (lost) {
-    if (t == 0) write_lost(p, r);
-  }
+  if (lost && t == 0) write_lost(p, r);
   const float lse = lost ? not_a_number() : write_row(p, r, all, counted, t == 0);
   if (!counted || !isfinite(lse)) {
     // nothing to rank: an ignored row, one whose logits are all minus infinity, or not numbers
@@ -461,40 +553,46 @@ __global__ void __launch_bounds__(TOP_THREADS) top_kernel(const LogprobRows p) {
     }
     return;
   }
-  // 1. the top-th largest of the threads' keys (-inf where there are fewer)
-  const int n_keys = groups >= 2 * TOP_THREADS ? TOP_THREADS : 2 * TOP_THREADS;
-  if (t == 0) sh.bound = -INFINITY;
-  __syncthreads();
-  for (int i = t; i < n_keys; i += TOP_THREADS) {
+  // 1. the top-th largest of the threads' keys (-inf where there are fewer): it is among the
+  // first `top` of some warp
+  for (int l = 0; l < lists; ++l) {
+    const int i = l * TOP_THREADS + t;
     const float k = sh.key[i];
-    if (!(k > MASKED)) continue;
+    if (lane >= top || !(k > MASKED)) continue;
     int better = 0;
-    for (int j = 0; j < n_keys; j += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(sh.key + j);
-      better += (q.x > k || (q.x == k && j < i)) + (q.y > k || (q.y == k && j + 1 < i)) + (q.z > k || (q.z == k && j + 2 < i)) +
-                (q.w > k || (q.w == k && j + 3 < i));
-    }
+    for (int w = 0; w < lists * TOP_WARPS; ++w)
+      for (int j = w * 32; j < w * 32 + top; ++j) better += sh.key[j] > k || (sh.key[j] == k && j < i);
     if (better == top - 1) sh.bound = k;
   }
   __syncthreads();
   const float bound = sh.bound, margin = TOP_MARGIN * fmaxf(fabsf(all.m), bound == -INFINITY ? 0.f : fabsf(bound)) + 1e-30f;
   const float least = bound - margin;
   // 2. candidates
-#pragma unroll 4
-  for (int g = t; g < groups; g += TOP_THREADS) {
-    const float2 k = keys[g];
-    if (!(k.x >= least && k.x > MASKED)) continue;
-    if (k.y >= least && k.y > MASKED) {
+  auto choose = [&](float a, float b, int g) {
+    if (!(a >= least && a > MASKED)) return;
+    if (b >= least && b > MASKED) {
       const int at = atomicAdd(&sh.wholes, 1);
       if (at < TOP_WHOLE) sh.whole[at] = g;
     } else {
       const int at = atomicAdd(&sh.count, 1);
-      if (at < TOP_CANDIDATES) sh.id[at] = g * KEY_COLS + (int)(KEY_MASK - (__float_as_uint(k.x) & KEY_MASK));
+      if (at < TOP_CANDIDATES) sh.id[at] = g * KEY_COLS + (int)(KEY_MASK - (__float_as_uint(a) & KEY_MASK));
+    }
+  };
+  if (k1 >= least) {
+#pragma unroll
+    for (int i = 0; i < TOP_HELD; ++i) {
+      const int g = t + i * TOP_THREADS;
+      choose(held[i].x, held[i].y, 2 * g);
+      choose(held[i].z, held[i].w, 2 * g + 1);
+    }
+    for (int g = t + TOP_HELD * TOP_THREADS; g < groups / 2; g += TOP_THREADS) {
+      const float4 k = pairs[g];
+      choose(k.x, k.y, 2 * g);
+      choose(k.z, k.w, 2 * g + 1);
     }
   }
   __syncthreads();
   const T* h = static_cast<const T*>(p.H) + r * p.ldh;
-  const T* W = static_cast<const T*>(p.W);
   const int singles = sh.count, wholes = sh.wholes;
   if (wholes <= TOP_WHOLE && singles + wholes * KEY_COLS <= TOP_CANDIDATES) {
     const int n = singles + wholes * KEY_COLS;
@@ -504,12 +602,7 @@ __global__ void __launch_bounds__(TOP_THREADS) top_kernel(const LogprobRows p) {
     }
     __syncthreads();
     // 3.
-    for (int i = warp; i < n; i += TOP_WARPS) {
-      const int id = sh.id[i];
-      const double v = id < 0 ? 0.0 : logit(h, W + id * p.ldw, p.dim, p.vec, lane);
-      if (lane == 0) sh.value[i] = v;
-    }
-    __syncthreads();
+    evaluate(sh, n, p, h);
     rank(sh, n, top);
   } else {
     // every group against the best so far, KEY_COLS columns at a time
@@ -519,19 +612,14 @@ __global__ void __launch_bounds__(TOP_THREADS) top_kernel(const LogprobRows p) {
     for (int g = 0; g < groups; ++g) {
       const float k = keys[g].x;   // (the same for every thread)
       if (!(k >= least && k > MASKED) || (double)k + margin < worst) continue;
-      for (int i = warp; i < KEY_COLS; i += TOP_WARPS) {
-        const long long c = (long long)g * KEY_COLS + i;
-        const double v = c < p.vocab ? logit(h, W + c * p.ldw, p.dim, p.vec, lane) : 0.0;
-        if (lane == 0) {
-          sh.value[i] = v;
-          sh.id[i] = c < p.vocab ? (int)c : -1;
-        }
-      }
+      const long long c = (long long)g * KEY_COLS + t;
+      if (t < KEY_COLS) sh.id[t] = c < p.vocab ? (int)c : -1;
       if (t < kept) {
         sh.value[KEY_COLS + t] = sh.kept_value[t];
         sh.id[KEY_COLS + t] = sh.kept_id[t];
       }
       __syncthreads();
+      evaluate(sh, KEY_COLS, p, h);
       rank(sh, KEY_COLS + kept, top);
       kept = 0;
       while (kept < top && sh.kept_id[kept] >= 0) ++kept;
@@ -1055,7 +1143,7 @@ extern "C" int muon_linear_logprob_forward(const muon_linear_ce* a, int top, flo
   j.kind = LOGPROB;
   if (!map_of(&j.a, H) || !map_of(&j.b, W)) return MUON_ERR_CUDA;
   shape(&j, a->rows, a->vocab, a->dim, GROUP_FORWARD);
-  j.seg_kb = P.nterms > 1 ? SEG_F32 : SEG_BF16;
+  j.seg_kb = P.nterms > 1 ? SEG_F32 : j.mtiles == 1 ? SEG_FEW : (int)cdiv(j.nkb, cdiv(j.nkb, SEG_BF16));
   p.njobs = 1;
   p.tiles = j.tiles;
   if (launch(p, false, true, true, s) != cudaSuccess) return MUON_ERR_CUDA;

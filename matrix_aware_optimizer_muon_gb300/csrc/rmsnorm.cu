@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_kernel(const 
   extern __shared__ uint4 dyn[];
   __shared__ float red[2][RMS_GROUPS][16];
   constexpr int V = 16 / (int)sizeof(T), C = V / 2, P = kN * C, S = kDt ? 3 : 2;
+  allow_next();
   const RowThreads g{(int)threadIdx.x, (int)blockDim.x, 1 + (int)threadIdx.y};
   const int t = g.t, groups = blockDim.y, nthr = g.size * groups;
   const float inv = 1.f / (float)p.dim;
@@ -474,14 +475,15 @@ __global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_kernel(const 
     join_columns<kN * V>(p, [&](int e) { return ((e / V) * g.size + t) * V + e % V; }, [&](int e) { return elem(sw, e); });
 }
 
-// Rows of any alignment, through shared memory (fetch_row): a thread's columns are `size`
-// apart.
-template <typename T, int E>
+// Rows of any alignment, through shared memory (fetch_row): a thread's columns are kSize
+// apart, so that an access is an offset the instruction holds.
+template <typename T, int E, int kSize>
 __global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_odd_kernel(const RmsBwd p, int slot) {
   extern __shared__ uint4 dyn[];
   __shared__ float red[2][RMS_GROUPS][16];
-  constexpr int R = RMS_RING;
-  const RowThreads g{(int)threadIdx.x, (int)blockDim.x, 1 + (int)threadIdx.y};
+  constexpr int R = RMS_RING, P = (E + 1) / 2, kSure = sure_of(E);
+  allow_next();
+  const RowThreads g{(int)threadIdx.x, kSize, 1 + (int)threadIdx.y};
   const int t = g.t, S = p.dtotal ? 3 : 2;
   const float inv = 1.f / (float)p.dim;
   const long long step = (long long)gridDim.x * blockDim.y;
@@ -489,20 +491,22 @@ __global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_odd_kernel(co
   // [slot][stream], and a row that waits to be stored
   uint8_t* mine = reinterpret_cast<uint8_t*>(dyn) + (size_t)threadIdx.y * (R * S + 1) * slot;
   T* out = reinterpret_cast<T*>(mine + R * S * slot);
-  float w[E], sw[E];
+  auto inside = [&](int e) { return e < E && (e < kSure || e * kSize + t < p.dim); };
+  // columns e and e + 1 of the thread's as a pair
+  auto pair = [&](int i, auto get) { return make2(inside(2 * i) ? get(2 * i) : 0.f, inside(2 * i + 1) ? get(2 * i + 1) : 0.f); };
+  f32x2 w[P], sw[P];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int c = e * g.size + t;
-    w[e] = c < p.dim ? (p.w ? ld_w(p.w, p.w_bf16, c) : 1.f) : 0.f;
-    sw[e] = 0.f;
+  for (int i = 0; i < P; ++i) {
+    w[i] = pair(i, [&](int e) { return p.w ? ld_w(p.w, p.w_bf16, e * kSize + t) : 1.f; });
+    sw[i] = both(0.f);
   }
   auto fetch = [&](int s) {
     if (rf < p.rows) {
       uint8_t* o = mine + s * S * slot;
-      fetch_row(reinterpret_cast<T*>(o), static_cast<const T*>(p.t) + rf * p.ldt, p.dim, t, g.size);
-      fetch_row(reinterpret_cast<T*>(o + slot), static_cast<const T*>(p.dy) + rf * p.lddy, p.dim, t, g.size);
+      fetch_row(reinterpret_cast<T*>(o), static_cast<const T*>(p.t) + rf * p.ldt, p.dim, t, kSize);
+      fetch_row(reinterpret_cast<T*>(o + slot), static_cast<const T*>(p.dy) + rf * p.lddy, p.dim, t, kSize);
       if (S == 3)
-        fetch_row(reinterpret_cast<T*>(o + 2 * slot), static_cast<const T*>(p.dtotal) + rf * p.lddt, p.dim, t, g.size);
+        fetch_row(reinterpret_cast<T*>(o + 2 * slot), static_cast<const T*>(p.dtotal) + rf * p.lddt, p.dim, t, kSize);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     rf += step;
@@ -518,37 +522,34 @@ __global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_odd_kernel(co
     g.sync();                                   // everyone's copies of this row are there
     const uint8_t* o = mine + at * S * slot;
     at = at + 1 == R ? 0 : at + 1;
-    const T* tr = reinterpret_cast<const T*>(o) + behind(static_cast<const T*>(p.t) + r * p.ldt);
-    const T* gr = reinterpret_cast<const T*>(o + slot) + behind(static_cast<const T*>(p.dy) + r * p.lddy);
-    const T* dr = reinterpret_cast<const T*>(o + 2 * slot);
+    const T* tr = reinterpret_cast<const T*>(o) + behind(static_cast<const T*>(p.t) + r * p.ldt) + t;
+    const T* gr = reinterpret_cast<const T*>(o + slot) + behind(static_cast<const T*>(p.dy) + r * p.lddy) + t;
+    const T* dr = reinterpret_cast<const T*>(o + 2 * slot) + t;
     if (S == 3) dr += behind(static_cast<const T*>(p.dtotal) + r * p.lddt);
-    float xh[E], gw[E], s = 0.f;
+    f32x2 xh[P], gw[P], s = both(0.f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = e * g.size + t;
-      const bool in = c < p.dim;
-      xh[e] = in ? to_f32(tr[c]) * rs : 0.f;
-      gw[e] = in ? to_f32(gr[c]) : 0.f;
-      sw[e] = fmaf(gw[e], xh[e], sw[e]);
-      gw[e] *= w[e];
-      s = fmaf(gw[e], xh[e], s);
+    for (int i = 0; i < P; ++i) {
+      xh[i] = mul2(pair(i, [&](int e) { return to_f32(tr[e * kSize]); }), both(rs));
+      gw[i] = pair(i, [&](int e) { return to_f32(gr[e * kSize]); });
+      sw[i] = fma2(gw[i], xh[i], sw[i]);
+      gw[i] = mul2(gw[i], w[i]);
+      s = fma2(gw[i], xh[i], s);
     }
-    const float m = -rs * (g.sum(s, red[parity][threadIdx.y]) * inv);
+    const float m = -rs * (g.sum(lo2(s) + hi2(s), red[parity][threadIdx.y]) * inv);
     parity ^= 1;
     T* dx = static_cast<T*>(p.dx) + r * p.lddx;
-    T* to = out + behind(dx);
+    T* to = out + behind(dx) + t;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = e * g.size + t;
-      if (c < p.dim) {
-        const float v = fmaf(gw[e], rs, xh[e] * m);
-        to[c] = from_f32<T>(S == 3 ? to_f32(dr[c]) + v : v);
-      }
+    for (int i = 0; i < P; ++i) {
+      f32x2 v = fma2(gw[i], both(rs), mul2(xh[i], both(m)));
+      if (S == 3) v = add2(pair(i, [&](int e) { return to_f32(dr[e * kSize]); }), v);
+      if (inside(2 * i)) to[2 * i * kSize] = from_f32<T>(lo2(v));
+      if (inside(2 * i + 1)) to[(2 * i + 1) * kSize] = from_f32<T>(hi2(v));
     }
     g.sync();
-    flush_row(dx, out, p.dim, t, g.size);
+    flush_row(dx, out, p.dim, t, kSize);
   }
-  if (p.part) join_columns<E>(p, [&](int e) { return e * g.size + t; }, [&](int e) { return sw[e]; });
+  if (p.part) join_columns<E>(p, [&](int e) { return e * kSize + t; }, [&](int e) { return elem(sw, e); });
 }
 
 // Rows wider than that: dx, a CTA a row with the row in registers, and the columns' sums over
@@ -783,23 +784,22 @@ cudaError_t backward_vec(const RmsBwd& p, int threads, int* lines, cudaStream_t 
   if ((size_t)RMS_RING * 3 * kN * 16 * threads > (size_t)RMS_ODD_SMEM) return go(rms_backward_kernel<T, kN, true, 2>, 2, 3);
   return go(rms_backward_kernel<T, kN, true, RMS_RING>, RMS_RING, 3);
 }
-template <typename T, int E>
-cudaError_t backward_odd(const RmsBwd& p, int threads, int* lines, cudaStream_t s) {
+template <typename T, int E, int kSize>
+cudaError_t backward_odd(const RmsBwd& p, int* lines, cudaStream_t s) {
   size_t smem = 0;
   const int slot = slot_bytes<T>(p.dim);
-  const int groups = row_groups(threads, (size_t)(RMS_RING * (p.dtotal ? 3 : 2) + 1) * slot, p, &smem);
-  if (smem > (size_t)RMS_ODD_SMEM) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = allow_smem(rms_backward_odd_kernel<T, E>, smem);
+  const int groups = row_groups(kSize, (size_t)(RMS_RING * (p.dtotal ? 3 : 2) + 1) * slot, p, &smem);
+  const cudaError_t e = allow_smem(rms_backward_odd_kernel<T, E, kSize>, smem);
   if (e != cudaSuccess) return e;
   *lines = (int)std::min<long long>(cdiv(p.rows, groups), RMS_CTAS);
   count_launch();
-  rms_backward_odd_kernel<T, E><<<*lines, dim3(threads, groups), smem, s>>>(p, slot);
+  rms_backward_odd_kernel<T, E, kSize><<<*lines, dim3(kSize, groups), smem, s>>>(p, slot);
   return cudaGetLastError();
 }
 
 // 16 columns a thread (registers hold their sums, weights and the row), 8 for rows that 16
-// would leave to less than two warps; of any alignment 8, 12 or 16, whichever leaves the
-// fewest places empty.
+// would leave to less than two warps; of any alignment as few as a fixed number of threads
+// needs.
 template <typename T>
 cudaError_t backward(const RmsBwd& p, bool vec, int* lines, cudaStream_t s) {
   constexpr int V = vec_of<T>();
@@ -811,14 +811,24 @@ cudaError_t backward(const RmsBwd& p, bool vec, int* lines, cudaStream_t s) {
   if (vec && threads(16 / V) <= RMS_BWD_THREADS) return backward_vec<T, 16 / V>(p, threads(16 / V), lines, s);
   const bool fits = (size_t)(RMS_RING * (p.dtotal ? 3 : 2) + 1) * slot_bytes<T>(std::min(p.dim, 1 << 16)) <= (size_t)RMS_ODD_SMEM;
   if (!vec && threads(16) <= RMS_BWD_THREADS && fits) {
-    if (p.dim <= 64) return backward_odd<T, 2>(p, 32, lines, s);
-    if (p.dim <= 128) return backward_odd<T, 4>(p, 32, lines, s);
-    int best = 16;
-    for (int e : {12, 8})
-      if (threads(e) <= RMS_BWD_THREADS && threads(e) * e < threads(best) * best) best = e;
-    if (best == 8) return backward_odd<T, 8>(p, threads(8), lines, s);
-    if (best == 12) return backward_odd<T, 12>(p, threads(12), lines, s);
-    return backward_odd<T, 16>(p, threads(16), lines, s);
+    cudaError_t e = cudaSuccess;
+    if (p.dim <= 256)
+      by_accesses(cdiv(p.dim, 32), [&](auto N) {
+        if constexpr (decltype(N)::value <= 8) e = backward_odd<T, decltype(N)::value, 32>(p, lines, s);
+      });
+    else if (p.dim <= 1024)
+      by_accesses(cdiv(p.dim, 128), [&](auto N) {
+        if constexpr (decltype(N)::value >= 3 && decltype(N)::value <= 8) e = backward_odd<T, decltype(N)::value, 128>(p, lines, s);
+      });
+    else if (p.dim <= 4096)
+      by_accesses(cdiv(p.dim, 256), [&](auto N) {
+        if constexpr (decltype(N)::value >= 5) e = backward_odd<T, decltype(N)::value, 256>(p, lines, s);
+      });
+    else
+      by_accesses(cdiv(p.dim, 512), [&](auto N) {
+        if constexpr (decltype(N)::value >= 10) e = backward_odd<T, decltype(N)::value, 512>(p, lines, s);
+      });
+    return e;
   }
   // the columns' sums before dx, which may be dy itself
   if (p.part) {
