@@ -155,6 +155,34 @@ __global__ void __launch_bounds__(kWarp ? 32 * RMS_WARPS : RMS_MOST_THREADS) rms
 template <typename T> __device__ __forceinline__ int behind(const T* row) {
   return (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
 }
+// 16 bytes from `bytes` on (0 .. 15, a multiple of the element's size) of two words.
+template <typename T>
+__device__ __forceinline__ uint4 window(const uint4& lo, const uint4& hi, int bytes) {
+  uint32_t a[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
+  const uint32_t last = hi.w;
+  uint32_t b[5];
+  if (bytes & 8) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) a[i] = a[i + 2];
+    a[5] = last;
+  }
+#pragma unroll
+  for (int i = 0; i < 5; ++i) b[i] = bytes & 4 ? a[i + 1] : a[i];
+  if (sizeof(T) == 2 && (bytes & 2)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __funnelshift_r(b[i], b[i + 1], 16);
+  }
+  return make_uint4(b[0], b[1], b[2], b[3]);
+}
+// A word's elements outside [lo, hi) become zeros.
+template <typename T>
+__device__ __forceinline__ uint4 masked_word(uint4 q, int lo, int hi) {
+  T* x = reinterpret_cast<T*>(&q);
+#pragma unroll
+  for (int i = 0; i < 16 / (int)sizeof(T); ++i)
+    if (i < lo || i >= hi) x[i] = from_f32<T>(0.f);
+  return q;
+}
 template <typename T>
 __device__ __forceinline__ void fetch_row(T* slot, const T* row, int dim, int t, int size) {
   const int off = behind(row), words = (int)(((off + dim) * sizeof(T) + 15) / 16);
@@ -187,7 +215,7 @@ struct RowThreads {
     if (size == 32) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(size) : "memory");
   }
-  // red: 16 floats; every thread gets the sum, in a fixed order.  A second call needs a
+  // red: a float for each warp; every thread gets the sum, in a fixed order.  A second call needs a
   // sync() between.
   __device__ __forceinline__ float sum(float v, float* red) const {
     v = warp_sum(v);
@@ -199,6 +227,124 @@ struct RowThreads {
     return v;
   }
 };
+
+// Rows that start off the words' boundaries, in registers all the same, cut at the words of y
+// (and of total, which has to lie like it).  A row that lies otherwise is read as windows of
+// two words, and so are the weights; the words at the row's ends are masked, and stored by elements.
+// Columns [pos - o, ...) of a row that begins o elements behind `base`; words without any
+// element of the row are not read.
+template <typename E>
+__device__ __forceinline__ uint4 load_at(const E* base, int pos, int end) {
+  constexpr int V = 16 / (int)sizeof(E), S = sizeof(E) == 2 ? 3 : 2;
+  const int j = pos >> S, sh = pos & (V - 1);
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  const uint4* q = reinterpret_cast<const uint4*>(base);
+  const uint4 lo = j >= 0 && j * V < end ? q[j] : none;
+  if (sh == 0) return lo;
+  const uint4 hi = j + 1 >= 0 && (j + 1) * V < end ? q[j + 1] : none;
+  return window<E>(lo, hi, sh * (int)sizeof(E));
+}
+template <typename T>
+__device__ __forceinline__ void store_word(T* row, int c, int dim, const uint4& q) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (c >= 0 && c + V <= dim) {
+    *reinterpret_cast<uint4*>(row + c) = q;
+  } else {
+    const T* x = reinterpret_cast<const T*>(&q);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c + i >= 0 && c + i < dim) row[c + i] = x[i];
+  }
+}
+template <typename T, int kN, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 32 * RMS_WARPS : RMS_MOST_THREADS) rms_forward_words_kernel(const RmsFwd p) {
+  constexpr int V = 16 / (int)sizeof(T), C = V / 2;
+  __shared__ __align__(8) float red[kWarp ? 2 : 128];
+  const int t = kWarp ? threadIdx.x & 31 : threadIdx.x, size = kWarp ? 32 : blockDim.x, dim = p.dim;
+  const long long r = kWarp ? (long long)blockIdx.x * RMS_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+  if (kWarp && r >= p.rows) return;
+  T* y = static_cast<T*>(p.y) + r * p.ldy;
+  const int off = behind(y);
+  auto column = [&](int k) { return (k * size + t) * V - off; };
+  auto row_word = [&](const T* row, int k) {
+    const int c = column(k), o = behind(row);
+    const uint4 q = load_at(row - o, c + o, dim + o);
+    return c < 0 || c + V > dim ? masked_word<T>(q, -c, dim - c) : q;
+  };
+  Raw<T, V, kN> raw;
+  const T* x = static_cast<const T*>(p.x) + r * p.ldx;
+#pragma unroll
+  for (int k = 0; k < kN; ++k) raw.q[k] = row_word(x, k);
+  if (p.r) {
+    const T* res = static_cast<const T*>(p.r) + r * p.ldr;
+    Raw<T, V, kN> b;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) b.q[k] = row_word(res, k);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) add16(raw.q[k], b.q[k], static_cast<const T*>(nullptr));
+    if (p.total) {
+      T* total = static_cast<T*>(p.total) + r * p.ldt;
+#pragma unroll
+      for (int k = 0; k < kN; ++k) store_word(total, column(k), dim, raw.q[k]);
+    }
+  }
+  f32x2 q = both(0.f);
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    f32x2 v[C];
+    raw.get(k, v);
+#pragma unroll
+    for (int i = 0; i < C; ++i) q = fma2(v[i], v[i], q);
+  }
+  const float ssq = lo2(q) + hi2(q);
+  const float sum = kWarp ? warp_sum(ssq) : Group{t, size, 0, red}.sum(ssq, 0.f, 0).x;
+  const float rs = 1.0f / sqrtf(sum * (1.f / (float)dim) + p.eps);
+  raw.hold();
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const int c = column(k);
+    f32x2 v[C];
+    raw.get(k, v);
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = mul2(v[i], both(rs));
+    if (p.w && c < dim) {
+      if (p.w_bf16) {
+        const bf16* w = static_cast<const bf16*>(p.w);
+        const int o = behind(w);
+        if constexpr (V == 8) {
+          const uint4 a = load_at(w - o, c + o, dim + o);
+          v[0] = mul2(v[0], cvt2(a.x));
+          v[1] = mul2(v[1], cvt2(a.y));
+          v[2] = mul2(v[2], cvt2(a.z));
+          v[3] = mul2(v[3], cvt2(a.w));
+        } else {
+#pragma unroll
+          for (int i = 0; i < C; ++i) {
+            auto at = [&](int c) { return c >= 0 && c < dim ? to_f32(w[c]) : 0.f; };
+            v[i] = mul2(v[i], make2(at(c + 2 * i), at(c + 2 * i + 1)));
+          }
+        }
+      } else {
+        const float* w = static_cast<const float*>(p.w);
+        const int o = behind(w);
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h) {
+          const uint4 a = load_at(w - o, c + 4 * h + o, dim + o);
+          v[2 * h] = mul2(v[2 * h], make2(__uint_as_float(a.x), __uint_as_float(a.y)));
+          v[2 * h + 1] = mul2(v[2 * h + 1], make2(__uint_as_float(a.z), __uint_as_float(a.w)));
+        }
+      }
+    }
+    uint4 o;
+    if constexpr (V == 8)
+      o = make_uint4(pack_bf16x2(lo2(v[0]), hi2(v[0])), pack_bf16x2(lo2(v[1]), hi2(v[1])), pack_bf16x2(lo2(v[2]), hi2(v[2])),
+                     pack_bf16x2(lo2(v[3]), hi2(v[3])));
+    else
+      o = make_uint4(__float_as_uint(lo2(v[0])), __float_as_uint(hi2(v[0])), __float_as_uint(lo2(v[1])), __float_as_uint(hi2(v[1])));
+    store_word(y, c, dim, o);
+  }
+  if (p.rstd && t == 0) p.rstd[r] = rs;
+}
 
 constexpr int RMS_ODD_GROUPS = 8;                 // rows a CTA at most
 constexpr int RMS_ODD_SMEM = 200 * 1024;
@@ -355,9 +501,14 @@ struct RmsBwd {
 // every row its group takes, so the weights and the columns' sums stay in its registers; at
 // the end the groups' sums are joined in shared memory in a fixed order and the CTA writes
 // one line.  Rows come through a ring of asynchronous copies, R - 1 rows ahead.
-constexpr int RMS_GROUPS = 8;
-constexpr int RMS_BWD_THREADS = 512;
+constexpr int RMS_GROUPS = 16;
+// 16 columns a thread leave 512 threads of an SM 128 registers each, 8 leave 768 some 80.  Rows
+// that need windows and masks have more instructions a column to hide: 8 (32768 x 1537 bf16
+// 88 us against 93, 5003 x 1537 fp32 25.4 against 27.5); the others 16 (32768 x 1536 bf16 69.1
+// against 70.2).
+__host__ __device__ constexpr int rms_threads(int columns, bool odd) { return odd && columns <= 8 ? 768 : 512; }
 constexpr int RMS_RING = 3;
+constexpr int RMS_GUARD = 8;       // words (one would do, and leave every access across two lines)
 
 // The groups' sums of E columns a thread, to the CTA's line.
 template <int E, class Column, class Sum>
@@ -370,7 +521,7 @@ __device__ __forceinline__ void join_columns(const RmsBwd& p, Column column, Sum
   if (g > 0) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (column(e) < p.dim) sums[(size_t)(g - 1) * p.dim + column(e)] = sum(e);
+      if (column(e) >= 0 && column(e) < p.dim) sums[(size_t)(g - 1) * p.dim + column(e)] = sum(e);
   }
   __syncthreads();
   if (g > 0) return;
@@ -378,7 +529,7 @@ __device__ __forceinline__ void join_columns(const RmsBwd& p, Column column, Sum
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int c = column(e);
-    if (c < p.dim) {
+    if (c >= 0 && c < p.dim) {
       float a = sum(e);
       for (int j = 0; j < (int)blockDim.y - 1; ++j) a += sums[(size_t)j * p.dim + c];
       o[c] = a;
@@ -386,38 +537,64 @@ __device__ __forceinline__ void join_columns(const RmsBwd& p, Column column, Sum
   }
 }
 
-// Rows that move in 16-byte vectors: each thread reads only what it copied itself, so the
-// ring needs no barrier.
-template <typename T, int kN, bool kDt, int R>
-__global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_kernel(const RmsBwd p) {
+// Rows in 16-byte words.  Where all of them start on a word (!kOdd) each thread reads only what
+// it copied itself, so the ring needs no barrier.  Others (kOdd) are cut at the words of dx:
+// a group's rows lie a multiple of 16 bytes apart (a number of rows that is one of the
+// elements of a word), so the place of a row's first element in its word, and with it a
+// thread's columns, stay.  A stream that starts elsewhere in its words than dx is read through a window
+// of two words, which the threads beside have copied.
+template <typename T, int kN, bool kDt, int R, bool kOdd>
+__global__ void __launch_bounds__(rms_threads(kN * 16 / (int)sizeof(T), kOdd), 1) rms_backward_kernel(const RmsBwd p) {
   extern __shared__ uint4 dyn[];
-  __shared__ float red[2][RMS_GROUPS][16];
+  __shared__ float red[2][RMS_GROUPS][24];
   constexpr int V = 16 / (int)sizeof(T), C = V / 2, P = kN * C, S = kDt ? 3 : 2;
   allow_next();
   const RowThreads g{(int)threadIdx.x, (int)blockDim.x, 1 + (int)threadIdx.y};
-  const int t = g.t, groups = blockDim.y, nthr = g.size * groups;
+  const int t = g.t, groups = blockDim.y;
   const float inv = 1.f / (float)p.dim;
   const long long step = (long long)gridDim.x * groups;
   long long r = (long long)blockIdx.x * groups + threadIdx.y, rf = r;
+  T* dx = static_cast<T*>(p.dx) + r * p.lddx;
+  const T *tf = static_cast<const T*>(p.t) + r * p.ldt, *gf = static_cast<const T*>(p.dy) + r * p.lddy;
+  const T* df = kDt ? static_cast<const T*>(p.dtotal) + r * p.lddt : nullptr;
+  // where in its first word a row of each begins
+  const int off = kOdd ? behind(dx) : 0, ot = kOdd ? behind(tf) : 0, og = kOdd ? behind(gf) : 0, od = kOdd && kDt ? behind(df) : 0;
+  dx -= off;
+  tf -= ot;
+  gf -= og;
+  if (kDt) df -= od;
+  const bool shifted = kOdd && (ot != off || og != off || (kDt && od != off));
+  // a thread's word k begins at this column
+  auto column = [&](int k) { return (k * g.size + t) * V - off; };
   f32x2 w[P], sw[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) sw[i] = both(0.f);
 #pragma unroll
-  for (int k = 0; k < kN; ++k) weights<V>(p.w, p.w_bf16, (k * g.size + t) * V, p.dim, 1.f, w + k * C);
-  uint4* const mine = dyn + threadIdx.y * g.size + t;      // [slot][stream][access][thread]
-  const T *tf = static_cast<const T*>(p.t) + r * p.ldt, *gf = static_cast<const T*>(p.dy) + r * p.lddy;
-  const T* df = kDt ? static_cast<const T*>(p.dtotal) + r * p.lddt : nullptr;
+  for (int k = 0; k < kN; ++k) {
+    if constexpr (kOdd) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int c = column(k) + 2 * i;
+        auto at = [&](int c) { return c >= 0 && c < p.dim ? (p.w ? ld_w(p.w, p.w_bf16, c) : 1.f) : 0.f; };
+        w[k * C + i] = make2(at(c), at(c + 1));
+      }
+    } else {
+      weights<V>(p.w, p.w_bf16, column(k), p.dim, 1.f, w + k * C);
+    }
+  }
+  // [slot][stream][word], with room at either end
+  constexpr int G = kOdd ? RMS_GUARD : 0;
+  const int W = kN * g.size + 2 * G;
+  uint4* const mine = dyn + (size_t)threadIdx.y * (R * S * W) + G + t;
   auto fetch = [&](int slot) {                  // one group of copies, empty past the last row
     if (rf < p.rows) {
-      uint4* d = mine + slot * (S * kN) * nthr;
+      uint4* d = mine + slot * (S * W);
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
         const int c = (k * g.size + t) * V;
-        if (c < p.dim) {
-          copy16(d + k * nthr, tf + c);
-          copy16(d + (kN + k) * nthr, gf + c);
-          if (kDt) copy16(d + (2 * kN + k) * nthr, df + c);
-        }
+        if (c < p.dim + ot) copy16(d + k * g.size, tf + c);
+        if (c < p.dim + og) copy16(d + W + k * g.size, gf + c);
+        if (kDt && c < p.dim + od) copy16(d + 2 * W + k * g.size, df + c);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -426,27 +603,44 @@ __global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_kernel(const 
     gf += step * p.lddy;
     if (kDt) df += step * p.lddt;
   };
-  // slots that are never copied to belong to columns past the row: zero
+  if constexpr (!kOdd) {
+    // words that are never copied to belong to columns past the row: zero
 #pragma unroll
-  for (int k = 0; k < kN; ++k)
-    if ((k * g.size + t) * V >= p.dim)
-      for (int s = 0; s < S * R; ++s) mine[(s * kN + k) * nthr] = make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kN; ++k)
+      if (column(k) >= p.dim)
+        for (int s = 0; s < S * R; ++s) mine[s * W + k * g.size] = make_uint4(0, 0, 0, 0);
+  }
   for (int s = 0; s < R - 1; ++s) fetch(s);
+  // word k of a stream that begins `o` elements into its words
+  auto word = [&](const uint4* d, int k, int o) {
+    if (!shifted || o == off) return d[k * g.size];
+    const int from = o - off, back = from < 0;
+    const uint4* e = d + k * g.size - back;
+    return window<T>(e[0], e[1], (from + back * V) * (int)sizeof(T));
+  };
+  bool edge[kN];                                // words that reach past the row's ends
+#pragma unroll
+  for (int k = 0; k < kN; ++k) edge[k] = kOdd && (column(k) < 0 || column(k) + V > p.dim);
   float rs_n = r < p.rows ? p.rstd[r] : 0.f;
-  T* dx = static_cast<T*>(p.dx) + r * p.lddx;
   int parity = 0, at = 0;
   for (; r < p.rows; r += step, dx += step * p.lddx) {
     fetch(at == 0 ? R - 1 : at - 1);
     const float rs = rs_n;
     if (r + step < p.rows) rs_n = p.rstd[r + step];
     asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
-    const uint4* d = mine + at * (S * kN) * nthr;
+    if (shifted) g.sync();                      // the neighbours' copies are there
+    const uint4* d = mine + at * (S * W);
     at = at + 1 == R ? 0 : at + 1;
     f32x2 xh[P], gr[P], s = both(0.f);
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      widen(d[k * nthr], xh + k * C, static_cast<const T*>(nullptr));
-      widen(d[(kN + k) * nthr], gr + k * C, static_cast<const T*>(nullptr));
+      uint4 a = word(d, k, ot), b = word(d + W, k, og);
+      if (edge[k]) {
+        a = masked_word<T>(a, -column(k), p.dim - column(k));
+        b = masked_word<T>(b, -column(k), p.dim - column(k));
+      }
+      widen(a, xh + k * C, static_cast<const T*>(nullptr));
+      widen(b, gr + k * C, static_cast<const T*>(nullptr));
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -460,96 +654,26 @@ __global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_kernel(const 
     const f32x2 c1 = both(rs), c2 = both(-rs * m);
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      const int c = (k * g.size + t) * V;
+      const int c = column(k);
       f32x2 v[C];
-      if (kDt) widen(d[(2 * kN + k) * nthr], v, static_cast<const T*>(nullptr));
+      if (kDt) widen(word(d + 2 * W, k, od), v, static_cast<const T*>(nullptr));
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const f32x2 a = fma2(gr[k * C + i], c1, mul2(xh[k * C + i], c2));
         v[i] = kDt ? add2(v[i], a) : a;
       }
-      if (c < p.dim) store16(dx + c, v);
+      if (!edge[k]) {
+        if (kOdd || c < p.dim) store16(dx + c + off, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (c + i >= 0 && c + i < p.dim) st1(dx + off + c + i, elem(v, i));
+      }
     }
+    if (shifted) g.sync();                      // the slot is read before its next row arrives
   }
   if (p.part)
-    join_columns<kN * V>(p, [&](int e) { return ((e / V) * g.size + t) * V + e % V; }, [&](int e) { return elem(sw, e); });
-}
-
-// Rows of any alignment, through shared memory (fetch_row): a thread's columns are kSize
-// apart, so that an access is an offset the instruction holds.
-template <typename T, int E, int kSize>
-__global__ void __launch_bounds__(RMS_BWD_THREADS, 1) rms_backward_odd_kernel(const RmsBwd p, int slot) {
-  extern __shared__ uint4 dyn[];
-  __shared__ float red[2][RMS_GROUPS][16];
-  constexpr int R = RMS_RING, P = (E + 1) / 2, kSure = sure_of(E);
-  allow_next();
-  const RowThreads g{(int)threadIdx.x, kSize, 1 + (int)threadIdx.y};
-  const int t = g.t, S = p.dtotal ? 3 : 2;
-  const float inv = 1.f / (float)p.dim;
-  const long long step = (long long)gridDim.x * blockDim.y;
-  long long r = (long long)blockIdx.x * blockDim.y + threadIdx.y, rf = r;
-  // [slot][stream], and a row that waits to be stored
-  uint8_t* mine = reinterpret_cast<uint8_t*>(dyn) + (size_t)threadIdx.y * (R * S + 1) * slot;
-  T* out = reinterpret_cast<T*>(mine + R * S * slot);
-  auto inside = [&](int e) { return e < E && (e < kSure || e * kSize + t < p.dim); };
-  // columns e and e + 1 of the thread's as a pair
-  auto pair = [&](int i, auto get) { return make2(inside(2 * i) ? get(2 * i) : 0.f, inside(2 * i + 1) ? get(2 * i + 1) : 0.f); };
-  f32x2 w[P], sw[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    w[i] = pair(i, [&](int e) { return p.w ? ld_w(p.w, p.w_bf16, e * kSize + t) : 1.f; });
-    sw[i] = both(0.f);
-  }
-  auto fetch = [&](int s) {
-    if (rf < p.rows) {
-      uint8_t* o = mine + s * S * slot;
-      fetch_row(reinterpret_cast<T*>(o), static_cast<const T*>(p.t) + rf * p.ldt, p.dim, t, kSize);
-      fetch_row(reinterpret_cast<T*>(o + slot), static_cast<const T*>(p.dy) + rf * p.lddy, p.dim, t, kSize);
-      if (S == 3)
-        fetch_row(reinterpret_cast<T*>(o + 2 * slot), static_cast<const T*>(p.dtotal) + rf * p.lddt, p.dim, t, kSize);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    rf += step;
-  };
-  for (int s = 0; s < R - 1; ++s) fetch(s);
-  float rs_n = r < p.rows ? p.rstd[r] : 0.f;
-  int parity = 0, at = 0;
-  for (; r < p.rows; r += step) {
-    fetch(at == 0 ? R - 1 : at - 1);
-    const float rs = rs_n;
-    if (r + step < p.rows) rs_n = p.rstd[r + step];
-    asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
-    g.sync();                                   // everyone's copies of this row are there
-    const uint8_t* o = mine + at * S * slot;
-    at = at + 1 == R ? 0 : at + 1;
-    const T* tr = reinterpret_cast<const T*>(o) + behind(static_cast<const T*>(p.t) + r * p.ldt) + t;
-    const T* gr = reinterpret_cast<const T*>(o + slot) + behind(static_cast<const T*>(p.dy) + r * p.lddy) + t;
-    const T* dr = reinterpret_cast<const T*>(o + 2 * slot) + t;
-    if (S == 3) dr += behind(static_cast<const T*>(p.dtotal) + r * p.lddt);
-    f32x2 xh[P], gw[P], s = both(0.f);
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      xh[i] = mul2(pair(i, [&](int e) { return to_f32(tr[e * kSize]); }), both(rs));
-      gw[i] = pair(i, [&](int e) { return to_f32(gr[e * kSize]); });
-      sw[i] = fma2(gw[i], xh[i], sw[i]);
-      gw[i] = mul2(gw[i], w[i]);
-      s = fma2(gw[i], xh[i], s);
-    }
-    const float m = -rs * (g.sum(lo2(s) + hi2(s), red[parity][threadIdx.y]) * inv);
-    parity ^= 1;
-    T* dx = static_cast<T*>(p.dx) + r * p.lddx;
-    T* to = out + behind(dx) + t;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      f32x2 v = fma2(gw[i], both(rs), mul2(xh[i], both(m)));
-      if (S == 3) v = add2(pair(i, [&](int e) { return to_f32(dr[e * kSize]); }), v);
-      if (inside(2 * i)) to[2 * i * kSize] = from_f32<T>(lo2(v));
-      if (inside(2 * i + 1)) to[(2 * i + 1) * kSize] = from_f32<T>(hi2(v));
-    }
-    g.sync();
-    flush_row(dx, out, p.dim, t, kSize);
-  }
-  if (p.part) join_columns<E>(p, [&](int e) { return e * kSize + t; }, [&](int e) { return elem(sw, e); });
+    join_columns<kN * V>(p, [&](int e) { return column(e / V) + e % V; }, [&](int e) { return elem(sw, e); });
 }
 
 // Rows wider than that: dx, a CTA a row with the row in registers, and the columns' sums over
@@ -723,6 +847,9 @@ int odd_threads(int dim) { return std::min(512, 32 * cdiv(dim, 512)); }
 template <typename T, bool kEight>
 cudaError_t forward(const RmsFwd& p, bool vec, cudaStream_t s) {
   constexpr int V = vec_of<T>();
+  const int words = cdiv(p.dim - 1LL, V) + 1;       // that a row may touch
+  // whether total's rows begin where y's do in their words
+  const bool alike = !p.total || ((uintptr_t)p.total % 16 == (uintptr_t)p.y % 16 && (p.rows == 1 || (p.ldt - p.ldy) % V == 0));
   const int n = p.dim / V, need = cdiv(n, 32), slot = slot_bytes<T>(std::min(p.dim, 1 << 20)), slots = p.r ? 3 : 2;
   count_launch();
   if (vec && need <= 8) {
@@ -736,6 +863,18 @@ cudaError_t forward(const RmsFwd& p, bool vec, cudaStream_t s) {
     if (each <= 5) forward_launch<T, 5, false, kEight>(p, threads, s);
     else if (each == 6) forward_launch<T, 6, false, kEight>(p, threads, s);
     else forward_launch<T, 8, false, kEight>(p, threads, s);
+  } else if (!kEight && alike && words <= 8 * RMS_MOST_THREADS) {
+    if (words <= 256) {
+      by_accesses(cdiv(words, 32), [&](auto N) {
+        if constexpr (decltype(N)::value <= 8)
+          rms_forward_words_kernel<T, decltype(N)::value, true><<<cdiv(p.rows, RMS_WARPS), 32 * RMS_WARPS, 0, s>>>(p);
+      });
+    } else {
+      int threads = 64;
+      while (threads * 8 < words) threads *= 2;
+      if (cdiv(words, threads) <= 6) rms_forward_words_kernel<T, 6, false><<<(unsigned)p.rows, threads, 0, s>>>(p);
+      else rms_forward_words_kernel<T, 8, false><<<(unsigned)p.rows, threads, 0, s>>>(p);
+    }
   } else if ((long long)slots * slot <= RMS_ODD_SMEM) {
     const int threads = odd_threads(p.dim);
     // a few rows a CTA, as long as an SM still holds several CTAs
@@ -759,77 +898,50 @@ cudaError_t allow_smem(K kern, size_t smem) {
 }
 
 // Row groups of a persistent CTA of so many threads a row and bytes of shared memory a group.
-int row_groups(int threads, size_t bytes, const RmsBwd& p, size_t* smem) {
-  int groups = std::max(1, std::min(RMS_BWD_THREADS / threads, RMS_GROUPS));
+int row_groups(int most, int threads, size_t bytes, const RmsBwd& p, size_t* smem) {
+  int groups = std::max(1, std::min(most / threads, threads == 32 ? RMS_GROUPS : 15));   // (15 barriers)
   auto need = [&](int g) { return std::max(bytes * g, p.part ? (size_t)(g - 1) * p.dim * 4 : 0); };
   while (groups > 1 && need(groups) > (size_t)RMS_ODD_SMEM) --groups;
   *smem = need(groups);
   return groups;
 }
 
-template <typename T, int kN>
-cudaError_t backward_vec(const RmsBwd& p, int threads, int* lines, cudaStream_t s) {
-  auto go = [&](auto kern, int ring, int streams) {
+template <typename T, int kN, bool kOdd>
+cudaError_t backward_words(const RmsBwd& p, int threads, int* lines, cudaStream_t s) {
+  constexpr int V = vec_of<T>();
+  auto bytes = [&](int ring, int streams) { return (size_t)ring * streams * (kN * threads + (kOdd ? 2 * RMS_GUARD : 0)) * 16; };
+  auto go = [&](auto kern, size_t each) {
     size_t smem = 0;
-    const int groups = row_groups(threads, (size_t)ring * streams * kN * 16 * threads, p, &smem);
+    const int groups = row_groups(rms_threads(kN * V, kOdd), threads, each, p, &smem);
     const cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    *lines = (int)std::min<long long>(cdiv(p.rows, groups), RMS_CTAS);
+    int n = (int)std::min<long long>(cdiv(p.rows, groups), RMS_CTAS);
+    if (kOdd)       // a number of rows at a time that is one of a word's elements (152 are)
+      while (n * groups % V) ++n;
+    *lines = n;
     count_launch();
-    kern<<<*lines, dim3(threads, groups), smem, s>>>(p);
+    kern<<<n, dim3(threads, groups), smem, s>>>(p);
     return cudaGetLastError();
   };
-  if (!p.dtotal) return go(rms_backward_kernel<T, kN, false, RMS_RING>, RMS_RING, 2);
+  if (!p.dtotal) return go(rms_backward_kernel<T, kN, false, RMS_RING, kOdd>, bytes(RMS_RING, 2));
   // (three streams of more than 5460 fp32 columns fill the memory with a row less ahead)
-  if ((size_t)RMS_RING * 3 * kN * 16 * threads > (size_t)RMS_ODD_SMEM) return go(rms_backward_kernel<T, kN, true, 2>, 2, 3);
-  return go(rms_backward_kernel<T, kN, true, RMS_RING>, RMS_RING, 3);
-}
-template <typename T, int E, int kSize>
-cudaError_t backward_odd(const RmsBwd& p, int* lines, cudaStream_t s) {
-  size_t smem = 0;
-  const int slot = slot_bytes<T>(p.dim);
-  const int groups = row_groups(kSize, (size_t)(RMS_RING * (p.dtotal ? 3 : 2) + 1) * slot, p, &smem);
-  const cudaError_t e = allow_smem(rms_backward_odd_kernel<T, E, kSize>, smem);
-  if (e != cudaSuccess) return e;
-  *lines = (int)std::min<long long>(cdiv(p.rows, groups), RMS_CTAS);
-  count_launch();
-  rms_backward_odd_kernel<T, E, kSize><<<*lines, dim3(kSize, groups), smem, s>>>(p, slot);
-  return cudaGetLastError();
+  if (bytes(RMS_RING, 3) > (size_t)RMS_ODD_SMEM) return go(rms_backward_kernel<T, kN, true, 2, kOdd>, bytes(2, 3));
+  return go(rms_backward_kernel<T, kN, true, RMS_RING, kOdd>, bytes(RMS_RING, 3));
 }
 
-// 16 columns a thread (registers hold their sums, weights and the row), 8 for rows that 16
-// would leave to less than two warps; of any alignment as few as a fixed number of threads
-// needs.
+// A thread's columns: 16, but 8 where 16 would leave a row to less than two warps, and for rows
+// off the words' boundaries where 768 threads cover them.
 template <typename T>
 cudaError_t backward(const RmsBwd& p, bool vec, int* lines, cudaStream_t s) {
   constexpr int V = vec_of<T>();
   *lines = 0;
   if (p.rows == 0) return cudaSuccess;
-  const int n = p.dim / V;
-  auto threads = [&](int each) { return 32 * cdiv(vec ? n : p.dim, 32LL * each); };
-  if (vec && n <= 32 * 16 / V) return backward_vec<T, 8 / V>(p, threads(8 / V), lines, s);
-  if (vec && threads(16 / V) <= RMS_BWD_THREADS) return backward_vec<T, 16 / V>(p, threads(16 / V), lines, s);
-  const bool fits = (size_t)(RMS_RING * (p.dtotal ? 3 : 2) + 1) * slot_bytes<T>(std::min(p.dim, 1 << 16)) <= (size_t)RMS_ODD_SMEM;
-  if (!vec && threads(16) <= RMS_BWD_THREADS && fits) {
-    cudaError_t e = cudaSuccess;
-    if (p.dim <= 256)
-      by_accesses(cdiv(p.dim, 32), [&](auto N) {
-        if constexpr (decltype(N)::value <= 8) e = backward_odd<T, decltype(N)::value, 32>(p, lines, s);
-      });
-    else if (p.dim <= 1024)
-      by_accesses(cdiv(p.dim, 128), [&](auto N) {
-        if constexpr (decltype(N)::value >= 3 && decltype(N)::value <= 8) e = backward_odd<T, decltype(N)::value, 128>(p, lines, s);
-      });
-    else if (p.dim <= 4096)
-      by_accesses(cdiv(p.dim, 256), [&](auto N) {
-        if constexpr (decltype(N)::value >= 5) e = backward_odd<T, decltype(N)::value, 256>(p, lines, s);
-      });
-    else
-      by_accesses(cdiv(p.dim, 512), [&](auto N) {
-        if constexpr (decltype(N)::value >= 10) e = backward_odd<T, decltype(N)::value, 512>(p, lines, s);
-      });
-    return e;
-  }
+  const int n = vec ? p.dim / V : cdiv(p.dim - 1LL, V) + 1;     // words a row may touch
+  auto threads = [&](int each) { return 32 * cdiv(n, 32LL * each); };
+  if (vec && n <= 32 * 16 / V) return backward_words<T, 8 / V, false>(p, threads(8 / V), lines, s);
+  if (vec && threads(16 / V) <= rms_threads(16, false)) return backward_words<T, 16 / V, false>(p, threads(16 / V), lines, s);
+  if (!vec && threads(8 / V) <= rms_threads(8, true)) return backward_words<T, 8 / V, true>(p, threads(8 / V), lines, s);
+  if (!vec && threads(16 / V) <= rms_threads(16, true)) return backward_words<T, 16 / V, true>(p, threads(16 / V), lines, s);
   // the columns' sums before dx, which may be dy itself
   if (p.part) {
     *lines = (int)std::min<long long>(p.rows, RMS_CTAS);

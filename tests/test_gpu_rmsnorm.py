@@ -63,7 +63,10 @@ def check_forward(x, x64, w, w64, r, r64, xdt, what):
     within(num(y), ry, (rel + 3 * U + (BF if xdt == "bf16" else 0)) * np.abs(ry) * 1.01, ("y",) + what)
     # 8 bits, from the same inputs
     codes, scales, rstd8, total8 = mm.muon_rmsnorm_forward_fp8(x, w, r, eps=EPS)
-    assert torch.equal(rstd8, rstd) and torch.equal(total8, total)
+    # (rows that start off a 16-byte boundary add their squares in another order here: the bound
+    # holds for any order, so it holds for both)
+    within(num(rstd8), rrstd, rel * rrstd, ("rstd8",) + what)
+    assert torch.equal(total8, total)
     rq, rscale = ref.eight_bits(ry)
     within(num(scales), rscale, (rel + 6 * U) * rscale, ("scale",) + what)
     s = np.repeat(num(scales), 128, 1)[:, :d]
