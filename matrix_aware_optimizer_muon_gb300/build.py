@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmuon_gb300.so")
 SOURCES = ["api.cu", "ew.cu", "cols.cu", "ns_tc.cu", "ns_simt.cu", "noalloc.cu", "adamw.cu", "tall.cu",
-           "adamw8.cu", "layernorm.cu", "linear_ce.cu", "ce_gemm.cu", "rmsnorm.cu", "clip.cu"]
+           "adamw8.cu", "layernorm.cu", "linear_ce.cu", "ce_gemm.cu", "logprob_few.cu", "rmsnorm.cu", "clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

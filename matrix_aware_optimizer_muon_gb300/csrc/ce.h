@@ -85,6 +85,29 @@ cudaError_t prepare();           // kernel attributes and occupancy of the curre
 int pairs();                     // CTA pairs that run at once
 cudaError_t launch(const OrderedParams& p, bool ordered, bool promote, bool logprob, cudaStream_t s);
 
+// A call with few rows (logprob_few.cu).
+constexpr int FEW_MAX_CTAS = 608;
+struct Few {
+  const void *H, *W;
+  const int64_t* labels;
+  long long ldh, ldw, vocab, ignore;
+  int rows, dim, dp, masked;     // dp: padded row of the staged H;  masked: rows without a token count as zeros
+  const unsigned int* status;
+  // forward: as in Params, parts statistics a row
+  float4* stat;
+  float2* keys;
+  float* zlabel;
+  int parts;
+  // backward
+  const float *lse, *entropy, *g_logprob, *g_entropy;
+  float* dh_part;                // [CTA][rows, padded][dp], or null
+  void* dW;
+};
+bool few_rows(int64_t rows, int64_t dim, bool f32, bool backward);   // whether it is one
+size_t few_bytes(int64_t rows, int64_t dim);     // of dh_part
+cudaError_t few_forward(Few p, bool f32, bool vec, cudaStream_t s);
+cudaError_t few_backward(Few p, bool f32, bool vec, void* dH, cudaStream_t s);
+
 #ifdef __CUDACC__
 // The factor that all rows share.
 __device__ __forceinline__ float shared_factor(float scale, const float* upstream, const float* stats) {

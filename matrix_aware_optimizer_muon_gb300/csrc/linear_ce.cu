@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) logprob_kernel(const LogprobR
 constexpr int TOP_THREADS = 256;
 constexpr int TOP_WARPS = TOP_THREADS / 32;
 constexpr int TOP_CANDIDATES = 512;
-constexpr int TOP_WHOLE = 8;                 // groups taken whole
+constexpr int TOP_WHOLE = 14;                // groups taken whole
 constexpr float TOP_MARGIN = 0x1p-12f;
 constexpr float MASKED = -0x1p120f;          // logits down here are masks, of the type's lowest value or less
 static_assert(TOP_WHOLE * KEY_COLS + MUON_LOGPROB_MAX_TOP <= TOP_CANDIDATES, "");
@@ -524,10 +524,16 @@ __global__ void __launch_bounds__(TOP_THREADS, 3) top_kernel(const LogprobRows p
     k2 = fmaxf(k2, fmaxf(fminf(k1, k.z), k.w));
     k1 = fmaxf(k1, k.z);
   };
+  // a group a thread where that covers them (every key counts below), two otherwise
+  const bool single = groups <= TOP_THREADS;
 #pragma unroll
   for (int i = 0; i < TOP_HELD; ++i) {
-    const int g = t + i * TOP_THREADS;
+    const int g = single ? groups : t + i * TOP_THREADS;
     held[i] = g < groups / 2 ? pairs[g] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+  }
+  if (single && t < groups) {
+    const float2 k = keys[t];
+    held[0] = make_float4(k.x, k.y, -INFINITY, -INFINITY);
   }
 #pragma unroll
   for (int i = 0; i < TOP_HELD; ++i) take(held[i]);
@@ -582,7 +588,7 @@ __global__ void __launch_bounds__(TOP_THREADS, 3) top_kernel(const LogprobRows p
 #pragma unroll
     for (int i = 0; i < TOP_HELD; ++i) {
       const int g = t + i * TOP_THREADS;
-      choose(held[i].x, held[i].y, 2 * g);
+      choose(held[i].x, held[i].y, single ? t : 2 * g);
       choose(held[i].z, held[i].w, 2 * g + 1);
     }
     for (int g = t + TOP_HELD * TOP_THREADS; g < groups / 2; g += TOP_THREADS) {
@@ -677,6 +683,7 @@ struct CePlan {
   size_t hp, wp;               // packed copies
   size_t zlabel, part, sums;   // forward
   size_t stat, keys;           // forward of the log probabilities
+  size_t few;                  // their backward pass with few rows
   int64_t piece, npieces;
   int splits;
   size_t g[2];
@@ -755,6 +762,11 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
   P->piece = cdiv(cdiv(a->vocab, P->npieces), TILE) * TILE;
   P->npieces = cdiv(a->vocab, P->piece);
   P->splits = split_count(a->rows, a->dim, P->piece, 76);
+  if (top >= 0 && few_rows(a->rows, a->dim, f32, true)) {
+    P->few = take(few_bytes(a->rows, a->dim));
+    P->total = std::max(P->total, at);
+    at = common;
+  }
   P->g_part = (size_t)a->rows * P->piece;
   for (int i = 0; i < 2; ++i) P->g[i] = P->npieces > 1 || i == 0 ? take(P->parts * P->g_part * 2) : P->g[0];
   P->ldacc = P->dp;
@@ -928,6 +940,59 @@ int result_vec(const void* out, int64_t ld, int dt) {
   return is_aligned(out, 16) && row % 16 == 0 ? 1 : 0;
 }
 
+Few few_args(const muon_linear_ce* a, char* ws) {
+  Few f = {};
+  f.H = a->H;
+  f.W = a->W;
+  f.labels = a->labels;
+  f.ldh = a->ldh;
+  f.ldw = a->ldw;
+  f.vocab = a->vocab;
+  f.ignore = a->ignore_index;
+  f.rows = (int)a->rows;
+  f.dim = (int)a->dim;
+  f.status = reinterpret_cast<const unsigned int*>(ws);
+  return f;
+}
+
+// The last kernel of a forward pass.
+int join_rows(const muon_linear_ce* a, int top, const Params& p, int parts, float* logprob, float* entropy, float* lse,
+              int64_t* ids, float* alternatives, cudaStream_t s) {
+  LogprobRows q = {};
+  q.stat = p.stat;
+  q.keys = p.keys;
+  q.parts = parts;
+  q.rows = a->rows;
+  q.labels = a->labels;
+  q.vocab = a->vocab;
+  q.ignore = a->ignore_index;
+  q.zlabel = p.zlabel;
+  q.logprob = logprob;
+  q.entropy = entropy;
+  q.lse = lse;
+  q.status = p.status;
+  q.H = a->H;
+  q.W = a->W;
+  q.ldh = a->ldh;
+  q.ldw = a->ldw;
+  q.dim = (int)a->dim;
+  q.top = top;
+  q.ids = reinterpret_cast<long long*>(ids);
+  q.alternatives = alternatives;
+  const size_t es = dt_size(a->dtype);
+  q.vec = is_aligned(a->H, 16) && is_aligned(a->W, 16) && a->ldh * es % 16 == 0 && a->ldw * es % 16 == 0;
+  count_launch();
+  cudaError_t e;
+  if (top == 0)
+    e = launch_after(logprob_kernel, dim3((unsigned)cdiv(a->rows, JOIN_WARPS)), dim3(32 * JOIN_WARPS), 0, s, q);
+  else if (a->dtype == MUON_DTYPE_BF16)
+    e = launch_after(top_kernel<bf16>, dim3((unsigned)a->rows), dim3(TOP_THREADS), 0, s, q);
+  else
+    e = launch_after(top_kernel<float>, dim3((unsigned)a->rows), dim3(TOP_THREADS), 0, s, q);
+  if (e != cudaSuccess) return MUON_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
 // What g is made of in each row.
 struct RowGrads {
   bool policy;                                             // of log probabilities and entropies
@@ -952,6 +1017,17 @@ int backward_pass(const muon_linear_ce* a, const RowGrads& rows, void* dH, void*
   }
   if (prepare() != cudaSuccess) return MUON_ERR_CUDA;
   char* w = static_cast<char*>(ws);
+  if (rows.policy && P.few) {
+    Few f = few_args(a, w);
+    f.lse = rows.lse;
+    f.entropy = rows.entropy;
+    f.g_logprob = rows.g_logprob;
+    f.g_entropy = rows.g_entropy;
+    f.dh_part = reinterpret_cast<float*>(w + P.few);
+    f.dW = dW;
+    const bool vec = is_aligned(a->W, 16) && a->ldw * es % 16 == 0 && a->dim * es % 16 == 0 && is_aligned(dW, 16);
+    return few_backward(f, a->dtype == MUON_DTYPE_F32, vec, dH, s) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  }
   static thread_local OrderedParams p;
   Operand H, W;
   if (operand(&H, a, P, true, dW != nullptr, w, s) != cudaSuccess || operand(&W, a, P, false, false, w, s) != cudaSuccess)
@@ -1136,50 +1212,29 @@ extern "C" int muon_linear_logprob_forward(const muon_linear_ce* a, int top, flo
   p.stat = reinterpret_cast<float4*>(w + P.stat);
   p.keys = top ? reinterpret_cast<float2*>(w + P.keys) : nullptr;
   p.zlabel = reinterpret_cast<float*>(w + P.zlabel);
+  const size_t es = dt_size(a->dtype);
+  const bool w_vec = is_aligned(a->W, 16) && a->ldw * es % 16 == 0 && a->dim * es % 16 == 0;
+  Job& j = p.job[0];
+  shape(&j, a->rows, a->vocab, a->dim, GROUP_FORWARD);
+  if (few_rows(a->rows, a->dim, a->dtype == MUON_DTYPE_F32, false)) {
+    Few f = few_args(a, w);
+    f.stat = p.stat;
+    f.keys = p.keys;
+    f.zlabel = p.zlabel;
+    f.parts = 2 * j.ntiles;
+    if (few_forward(f, a->dtype == MUON_DTYPE_F32, w_vec, s) != cudaSuccess) return MUON_ERR_CUDA;
+    return join_rows(a, top, p, 2 * j.ntiles, logprob, entropy, lse, ids, alternatives, s);
+  }
   Operand H, W;
   if (operand(&H, a, P, true, false, w, s) != cudaSuccess || operand(&W, a, P, false, false, w, s) != cudaSuccess)
     return MUON_ERR_CUDA;
-  Job& j = p.job[0];
   j.kind = LOGPROB;
   if (!map_of(&j.a, H) || !map_of(&j.b, W)) return MUON_ERR_CUDA;
-  shape(&j, a->rows, a->vocab, a->dim, GROUP_FORWARD);
   j.seg_kb = P.nterms > 1 ? SEG_F32 : j.mtiles == 1 ? SEG_FEW : (int)cdiv(j.nkb, cdiv(j.nkb, SEG_BF16));
   p.njobs = 1;
   p.tiles = j.tiles;
   if (launch(p, false, true, true, s) != cudaSuccess) return MUON_ERR_CUDA;
-  LogprobRows q = {};
-  q.stat = p.stat;
-  q.keys = p.keys;
-  q.parts = 2 * j.ntiles;
-  q.rows = a->rows;
-  q.labels = a->labels;
-  q.vocab = a->vocab;
-  q.ignore = a->ignore_index;
-  q.zlabel = p.zlabel;
-  q.logprob = logprob;
-  q.entropy = entropy;
-  q.lse = lse;
-  q.status = p.status;
-  q.H = a->H;
-  q.W = a->W;
-  q.ldh = a->ldh;
-  q.ldw = a->ldw;
-  q.dim = (int)a->dim;
-  q.top = top;
-  q.ids = reinterpret_cast<long long*>(ids);
-  q.alternatives = alternatives;
-  const size_t es = dt_size(a->dtype);
-  q.vec = is_aligned(a->H, 16) && is_aligned(a->W, 16) && a->ldh * es % 16 == 0 && a->ldw * es % 16 == 0;
-  count_launch();
-  cudaError_t e;
-  if (top == 0)
-    e = launch_after(logprob_kernel, dim3((unsigned)cdiv(a->rows, JOIN_WARPS)), dim3(32 * JOIN_WARPS), 0, s, q);
-  else if (a->dtype == MUON_DTYPE_BF16)
-    e = launch_after(top_kernel<bf16>, dim3((unsigned)a->rows), dim3(TOP_THREADS), 0, s, q);
-  else
-    e = launch_after(top_kernel<float>, dim3((unsigned)a->rows), dim3(TOP_THREADS), 0, s, q);
-  if (e != cudaSuccess) return MUON_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  return join_rows(a, top, p, 2 * j.ntiles, logprob, entropy, lse, ids, alternatives, s);
 }
 
 extern "C" int muon_linear_logprob_backward(const muon_linear_ce* a, const float* lse, const float* entropy,

@@ -1,0 +1,390 @@
+// Log probabilities of a few rows (a decoding step, a short answer to be scored), forward and
+// backward, without the tensor cores:
+//   forward   z = H W^T and its statistics, W read once;
+//   backward  z again, g from it, dW = g^T H and dH = g W, W read and dW written once.
+//
+// With few rows a call is bound by W's bytes, and the tensor cores' tiles of 256
+// rows leave most of themselves empty; 32-bit operands would besides be written and read
+// again as three bf16 parts.  Here the rows of H lie in shared memory as fp32 numbers; a warp reads four rows
+// of W at a time, so that a word of H serves four products, and adds in fp32 (a lane dim/32
+// products, then a tree).  What a statistic of 128 columns or a key is, ce.h says: the
+// kernels that join them are those of the other path.
+#include <algorithm>
+
+#include "ce.h"
+#include "common.cuh"
+
+namespace muon {
+namespace ce {
+namespace {
+
+constexpr int FEW_THREADS = 256;
+constexpr int FEW_WARPS = FEW_THREADS / 32;
+constexpr int FEW_AT_ONCE = 4;              // rows of W a warp multiplies at a time
+constexpr int FEW_BLOCK = 128;              // columns of a statistic
+constexpr int FEW_PIECE = FEW_WARPS * FEW_AT_ONCE;   // rows of W a CTA takes at a time in the backward pass
+constexpr float FEW_FLOOR = -200.f;
+
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+size_t padded(int64_t dim) { return (size_t)(dim + 7) / 8 * 8; }
+
+// The rows of H as fp32 numbers, zeros behind them and in rows without a use.
+template <typename T, int R>
+__device__ __forceinline__ void stage_rows(const Few& p, float* h, int dp) {
+  for (int r = 0; r < R; ++r) {
+    bool live = r < p.rows;
+    if (live && p.masked) {
+      const long long lab = p.labels[r];
+      live = lab != p.ignore && lab >= 0 && lab < p.vocab;
+    }
+    const T* x = static_cast<const T*>(p.H) + r * p.ldh;
+    for (int c = threadIdx.x; c < dp; c += FEW_THREADS) h[r * dp + c] = live && c < p.dim ? ld1(x + c) : 0.f;
+  }
+}
+
+__device__ __forceinline__ void widen_word(const uint4& q, f32x2 (&v)[4], const bf16*) {
+  v[0] = cvt2(q.x); v[1] = cvt2(q.y); v[2] = cvt2(q.z); v[3] = cvt2(q.w);
+}
+__device__ __forceinline__ void widen_word(const uint4& q, f32x2 (&v)[2], const float*) {
+  v[0] = make2(__uint_as_float(q.x), __uint_as_float(q.y));
+  v[1] = make2(__uint_as_float(q.z), __uint_as_float(q.w));
+}
+
+// The products of FEW_AT_ONCE rows of W from v0 on with the R rows of H, summed over the warp:
+// lane l has product l * n / 32 (row of W times R plus row of H) of the n, the first of two
+// where n is 64.
+template <typename T, int R, bool kVec>
+__device__ __forceinline__ float2 products(const Few& p, const float* h, int dp, long long v0, int lane) {
+  constexpr int N = FEW_AT_ONCE * R;
+  float v[N];                                   // (pairs of numbers would take twice the registers)
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  const T* w[FEW_AT_ONCE];
+#pragma unroll
+  for (int i = 0; i < FEW_AT_ONCE; ++i)         // (rows behind the last are the last's; nobody looks at them)
+    w[i] = static_cast<const T*>(p.W) + min(v0 + i, p.vocab - 1) * p.ldw;
+  if constexpr (kVec) {
+    constexpr int V = 16 / (int)sizeof(T);
+#pragma unroll 2
+    for (int c = lane * V; c < p.dim; c += 32 * V) {
+      uint4 q[FEW_AT_ONCE];
+#pragma unroll
+      for (int i = 0; i < FEW_AT_ONCE; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(w[i] + c));
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        float x[FEW_AT_ONCE][4];
+#pragma unroll
+        for (int i = 0; i < FEW_AT_ONCE; ++i) {
+          f32x2 all[V / 2];
+          widen_word(q[i], all, static_cast<const T*>(nullptr));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[i][j] = j & 1 ? hi2(all[(k + j) / 2]) : lo2(all[(k + j) / 2]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float4 y = *reinterpret_cast<const float4*>(h + r * dp + c + k);
+#pragma unroll
+          for (int i = 0; i < FEW_AT_ONCE; ++i)
+            v[i * R + r] = fmaf(x[i][3], y.w, fmaf(x[i][2], y.z, fmaf(x[i][1], y.y, fmaf(x[i][0], y.x, v[i * R + r]))));
+        }
+      }
+    }
+  } else {
+    constexpr int H = 4;                        // elements in flight
+    for (int c0 = lane; c0 < p.dim; c0 += 32 * H) {
+      float x[H][FEW_AT_ONCE];
+#pragma unroll
+      for (int k = 0; k < H; ++k)
+#pragma unroll
+        for (int i = 0; i < FEW_AT_ONCE; ++i) x[k][i] = c0 + 32 * k < p.dim ? ld1(w[i] + c0 + 32 * k) : 0.f;
+#pragma unroll
+      for (int k = 0; k < H; ++k)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float y = c0 + 32 * k < p.dim ? h[r * dp + c0 + 32 * k] : 0.f;
+#pragma unroll
+          for (int i = 0; i < FEW_AT_ONCE; ++i) v[i * R + r] = fmaf(x[k][i], y, v[i * R + r]);
+        }
+    }
+  }
+  // each exchange halves what a lane holds, as long as there is more than one
+  int n = N;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n /= 2;
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i)
+        if (i < n) {
+          const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+  return make_float2(v[0], N > 32 ? v[1 % N] : 0.f);
+}
+
+template <typename T, int R, bool kVec>
+__global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
+  extern __shared__ float few_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dp = p.dp;
+  float* h = few_smem;                          // [R][dp]
+  float* z = h + R * dp;                        // [R][FEW_BLOCK]
+  allow_next();
+  await_previous();
+  stage_rows<T, R>(p, h, dp);
+  for (int blk = blockIdx.x; blk < p.parts; blk += gridDim.x) {
+    __syncthreads();                            // h is staged; the last block's z are read
+    const long long b0 = (long long)blk * FEW_BLOCK;
+    for (int i = warp * FEW_AT_ONCE; i < FEW_BLOCK; i += FEW_PIECE) {
+      if (b0 + i >= p.vocab) break;
+      const float2 v = products<T, R, kVec>(p, h, dp, b0 + i, lane);
+      constexpr int N = FEW_AT_ONCE * R;
+      if constexpr (N > 32) {
+        const int at = lane * (N / 32);
+        z[(at % R) * FEW_BLOCK + i + at / R] = v.x;
+        z[((at + 1) % R) * FEW_BLOCK + i + (at + 1) / R] = v.y;
+      } else if (lane % (32 / N) == 0) {
+        const int at = lane / (32 / N);
+        z[(at % R) * FEW_BLOCK + i + at / R] = v.x;
+      }
+    }
+    __syncthreads();
+    for (int r = warp; r < p.rows; r += FEW_WARPS) {
+      float x[4], mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = b0 + 32 * j + lane < p.vocab ? z[r * FEW_BLOCK + 32 * j + lane] : -INFINITY;
+        mx = fmaxf(mx, x[j]);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      float s = 0.f, t = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float d = x[j] - ref, e = __expf(d);
+        s += e;
+        t = fmaf(e, fmaxf(d, FEW_FLOOR), t);
+      }
+      s = warp_sum(s);
+      t = warp_sum(t);
+      if (lane == 0) p.stat[(size_t)r * p.parts + blk] = make_float4(mx, s, t, 0.f);
+      if (p.keys) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float own = __uint_as_float((__float_as_uint(fmaxf(x[j], -0x1.fffffep127f)) & ~KEY_MASK) | (KEY_MASK - lane));
+          float a = own;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          float b = own == a ? -INFINITY : own;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+          if (lane == j) p.keys[((size_t)r * p.parts + blk) * 4 + j] = make_float2(a, b);
+        }
+      }
+      const long long at = p.labels ? p.labels[r] - b0 : -1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (at == 32 * j + lane && b0 + at < p.vocab) p.zlabel[r] = x[j];
+    }
+  }
+}
+
+// The columns a thread takes at a time in the second half of a piece.
+template <typename T, bool kVec> struct Columns {
+  static constexpr int E = kVec ? 4 : 1;
+};
+__device__ __forceinline__ void load_columns(const float* p, float (&v)[4]) { ld4(p, v); }
+__device__ __forceinline__ void load_columns(const bf16* p, float (&v)[4]) { ld4(p, v); }
+template <typename T> __device__ __forceinline__ void load_columns(const T* p, float (&v)[1]) { v[0] = ld1(p); }
+template <typename T> __device__ __forceinline__ void store_columns(T* p, const float (&v)[4]) { st4(p, v); }
+template <typename T> __device__ __forceinline__ void store_columns(T* p, const float (&v)[1]) { st1(p, v[0]); }
+
+// Pieces of FEW_PIECE rows of W: their logits and g, a warp four rows; then, a thread some
+// columns, dW's rows (written) and their share of dH (kept in shared memory until the end).
+// W's second read of a piece comes from L2.
+template <typename T, int R, bool kVec>
+__global__ void __launch_bounds__(FEW_THREADS) few_backward_kernel(const Few p) {
+  extern __shared__ float few_smem[];
+  __shared__ __align__(16) float g[FEW_PIECE][R < 4 ? 4 : R];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dp = p.dp;
+  float* h = few_smem;                          // [R][dp]
+  float* dh = h + R * dp;                       // [R][dp]
+  constexpr int N = FEW_AT_ONCE * R, E = Columns<T, kVec>::E;
+  allow_next();
+  await_previous();
+  stage_rows<T, R>(p, h, dp);
+  if (p.dh_part)
+    for (int i = threadIdx.x; i < R * dp; i += FEW_THREADS) dh[i] = 0.f;
+  // what g is made of in the row of H that this lane's product belongs to
+  const int mine = lane / (N < 32 ? 32 / N : 1), row = mine % R;
+  float a = 0.f, b = 0.f, lse = 0.f, ah = 0.f;
+  long long label = -1;
+  const bool lost = __ldcg(p.status) & DEV_TIMEOUT;
+  if (row < p.rows) {
+    const long long lab = p.labels[row];
+    if (lab != p.ignore && lab >= 0 && lab < p.vocab) {
+      label = lab;
+      lse = p.lse[row];
+      if (p.g_logprob) a = p.g_logprob[row];
+      if (p.g_entropy) b = p.g_entropy[row];
+      ah = b == 0.f && !p.g_entropy ? a : fmaf(b, p.entropy[row], a);
+    }
+  }
+  for (long long v0 = (long long)blockIdx.x * FEW_PIECE; v0 < p.vocab; v0 += (long long)gridDim.x * FEW_PIECE) {
+    __syncthreads();                            // h is staged; the last piece's g are read
+    const long long w0 = v0 + warp * FEW_AT_ONCE;
+    if (w0 < p.vocab) {
+      const float z = products<T, R, kVec>(p, h, dp, w0, lane).x;
+      if (N >= 32 || lane % (32 / N) == 0) {
+        const long long v = w0 + mine / R;
+        const float d = z - lse;
+        float x = -__expf(d) * fmaf(b, fmaxf(d, FEW_FLOOR), ah);
+        if (v == label) x += a;
+        if (label < 0) x = 0.f;                 // no gradient, whatever the row holds
+        if (lost) x = __int_as_float(0x7FC00000);
+        g[warp * FEW_AT_ONCE + mine / R][row] = x;
+      }
+    }
+    __syncthreads();
+    const int n = (int)min(p.vocab - v0, (long long)FEW_PIECE);
+    for (int c = threadIdx.x * E; c < p.dim; c += FEW_THREADS * E) {
+      float hc[R][E], dc[R][E];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          hc[r][i] = h[r * dp + c + i];
+          dc[r][i] = 0.f;
+        }
+      const T* w = static_cast<const T*>(p.W) + v0 * p.ldw + c;
+      T* dw = static_cast<T*>(p.dW) + v0 * p.dim + c;
+#pragma unroll 8
+      for (int v = 0; v < n; ++v) {
+        float x[E], o[E], gv[R];
+        if (p.dh_part) load_columns(w + v * p.ldw, x);
+#pragma unroll
+        for (int r = 0; r < R; ++r) gv[r] = g[v][r];
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[i] = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            o[i] = fmaf(gv[r], hc[r][i], o[i]);
+            if (p.dh_part) dc[r][i] = fmaf(gv[r], x[i], dc[r][i]);
+          }
+        if (p.dW) store_columns(dw + (long long)v * p.dim, o);
+      }
+      if (p.dh_part)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < E; ++i) dh[r * dp + c + i] += dc[r][i];
+    }
+  }
+  if (p.dh_part) {
+    __syncthreads();
+    float* o = p.dh_part + (size_t)blockIdx.x * R * dp;
+    for (int i = threadIdx.x; i < R * dp; i += FEW_THREADS) o[i] = dh[i];
+  }
+}
+
+// dH from the CTAs' shares: 32 columns of a row a CTA, 8 threads a column over the shares
+// (each a fixed set), joined in order.
+template <typename T>
+__global__ void __launch_bounds__(256) few_join_kernel(const float* part, int ctas, int R, int dp, int dim, T* dH) {
+  __shared__ float sum[8][33];
+  await_previous();
+  const int c = blockIdx.x * 32 + threadIdx.x, r = blockIdx.y;
+  float s = 0.f;
+  if (c < dim) {
+#pragma unroll 4
+    for (int i = threadIdx.y; i < ctas; i += 8) s += part[((size_t)i * R + r) * dp + c];
+  }
+  sum[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y || c >= dim) return;
+  for (int i = 1; i < 8; ++i) s += sum[i][threadIdx.x];
+  st1(dH + (long long)r * dim + c, s);
+}
+
+int padded_rows(int64_t rows) { return rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+size_t forward_smem(int64_t rows, int64_t dim) { return padded_rows(rows) * (padded(dim) + FEW_BLOCK) * 4; }
+size_t backward_smem(int64_t rows, int64_t dim) { return padded_rows(rows) * padded(dim) * 8; }
+constexpr size_t FEW_SMEM = 200 * 1024;
+
+template <class K>
+cudaError_t run(K kern, Few& p, size_t smem, int64_t work, int most, int* grid, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FEW_SMEM);
+  if (e != cudaSuccess) return e;
+  // as many CTAs as run at once; each takes pieces in turn
+  int per_sm = 0, sms = 0;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, FEW_THREADS, smem)) != cudaSuccess) return e;
+  if (require_device(&sms) != MUON_OK) return cudaErrorNoDevice;
+  *grid = (int)std::max<int64_t>(1, std::min<int64_t>({work, (int64_t)per_sm * sms, most}));
+  count_launch();
+  return launch_after(kern, dim3(*grid), dim3(FEW_THREADS), smem, s, p);
+}
+template <typename T, bool kVec>
+cudaError_t forward_of(Few& p, cudaStream_t s) {
+  int grid = 0;
+  const size_t smem = forward_smem(p.rows, p.dim);
+  auto go = [&](auto kern) { return run(kern, p, smem, cdiv(p.vocab, FEW_BLOCK), 1 << 30, &grid, s); };
+  switch (padded_rows(p.rows)) {
+    case 1: return go(few_forward_kernel<T, 1, kVec>);
+    case 2: return go(few_forward_kernel<T, 2, kVec>);
+    case 4: return go(few_forward_kernel<T, 4, kVec>);
+    case 8: return go(few_forward_kernel<T, 8, kVec>);
+    default: return go(few_forward_kernel<T, 16, kVec>);
+  }
+}
+template <typename T, bool kVec>
+cudaError_t backward_of(Few& p, T* dH, cudaStream_t s) {
+  int grid = 0;
+  const int R = padded_rows(p.rows);
+  const size_t smem = backward_smem(p.rows, p.dim);
+  auto go = [&](auto kern) { return run(kern, p, smem, cdiv(p.vocab, FEW_PIECE), FEW_MAX_CTAS, &grid, s); };
+  const cudaError_t e = R == 1   ? go(few_backward_kernel<T, 1, kVec>)
+                        : R == 2 ? go(few_backward_kernel<T, 2, kVec>)
+                        : R == 4 ? go(few_backward_kernel<T, 4, kVec>)
+                                 : go(few_backward_kernel<T, 8, kVec>);
+  if (e != cudaSuccess || !dH) return e;
+  count_launch();
+  return launch_after(few_join_kernel<T>, dim3(cdiv(p.dim, 32), p.rows), dim3(32, 8), 0, s, p.dh_part, grid, R, p.dp, p.dim, dH);
+}
+
+}  // namespace
+
+// Up to how many rows this is the faster way (microseconds here and by tiles, 32768 x 1536):
+// fp32 forward 16 rows 98 and 203, 8 rows 58 and 199, backward 4 rows 116 and 431, 8 rows 145 and
+// 422; bf16 forward 1 row 25 and 35, 2 rows 28 and 35, 4 rows 31 and 31, backward 1 row 66 and 98,
+// 4 rows 74 and 99, 8 rows 118 and 98.
+bool few_rows(int64_t rows, int64_t dim, bool f32, bool backward) {
+  const int most = backward ? (f32 ? 8 : 4) : (f32 ? 16 : 2);
+  return rows >= 1 && rows <= most && dim < (1 << 20) &&
+         (backward ? backward_smem(rows, dim) : forward_smem(rows, dim)) <= FEW_SMEM;
+}
+size_t few_bytes(int64_t rows, int64_t dim) { return (size_t)FEW_MAX_CTAS * padded_rows(rows) * padded(dim) * 4; }
+
+cudaError_t few_forward(Few p, bool f32, bool vec, cudaStream_t s) {
+  p.dp = (int)padded(p.dim);
+  p.masked = 0;
+  if (f32) return vec ? forward_of<float, true>(p, s) : forward_of<float, false>(p, s);
+  return vec ? forward_of<bf16, true>(p, s) : forward_of<bf16, false>(p, s);
+}
+cudaError_t few_backward(Few p, bool f32, bool vec, void* dH, cudaStream_t s) {
+  p.dp = (int)padded(p.dim);
+  p.masked = 1;
+  if (!dH) p.dh_part = nullptr;
+  if (f32)
+    return vec ? backward_of<float, true>(p, static_cast<float*>(dH), s) : backward_of<float, false>(p, static_cast<float*>(dH), s);
+  return vec ? backward_of<bf16, true>(p, static_cast<bf16*>(dH), s) : backward_of<bf16, false>(p, static_cast<bf16*>(dH), s);
+}
+
+}  // namespace ce
+}  // namespace muon

@@ -345,13 +345,15 @@ def test_strides_and_alignment(dt):
         ws = mm.linear_logprob_workspace_for(hv, wv, tokens, top=6)
         packed = mm.alloc_linear_logprob_workspace(n, v, d, TYPES[dt], top=6)
         a, b = mm.muon_linear_logprob_forward(hv, wv, tokens, ws, top=6), mm.muon_linear_logprob_forward(h, w, tokens, packed, top=6)
-        assert all(torch.equal(p, q) for p, q in zip(a[:4], b[:4]))
-        # (the alternatives' sums go by other lanes)
-        assert torch.allclose(a[4], b[4], rtol=0, atol=1e-6)
+        for out in (a, b):
+            check(out, h64, w64, tok, 6, dt, (n, v, d, pad, off))
         one = torch.ones(n, device=dev())
-        a = mm.muon_linear_logprob_backward(hv, wv, tokens, b[2], b[1], ws, one, one)
-        b = mm.muon_linear_logprob_backward(h, w, tokens, b[2], b[1], packed, one, one)
-        assert all(torch.equal(p, q) for p, q in zip(a, b))
+        c = mm.muon_linear_logprob_backward(hv, wv, tokens, b[2], b[1], ws, one, one)
+        e = mm.muon_linear_logprob_backward(h, w, tokens, b[2], b[1], packed, one, one)
+        if n > 16:       # tiles of copies: the same bits (few rows are read where they lie, and summed in another order)
+            assert all(torch.equal(p, q) for p, q in zip(a[:4], b[:4])) and all(torch.equal(p, q) for p, q in zip(c, e))
+        for p, q in zip(c, e):
+            assert torch.linalg.norm((p - q).float()) <= (2 * BF if dt == "bf16" else 1e-5) * torch.linalg.norm(q.float())
 
 
 def test_repeats_other_streams_graphs_and_pieces():
