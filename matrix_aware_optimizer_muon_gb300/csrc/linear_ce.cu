@@ -337,14 +337,14 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) logprob_kernel(const LogprobR
 // partial sums, which is enough to swap neighbours, so they only choose candidates, and the
 // candidates' logits are summed again, to 2^-45 of their largest partial sum:
 //   1. a bound from below on the top-th largest logit: the top-th of the threads' largest keys
-//      (two each where there are few), each warp's in order so that few are compared;
+//      (two each where there are few), by merging the warps' lists in order;
 //   2. candidates: columns whose key is not below that by more than MARGIN of the largest
 //      logit, hundreds of times what the logits are off by; of 32 columns whose two keys both
 //      qualify, all (a third may hide behind them);
 //   3. their logits again, a warp each; 4. their ranks, ties to the lower index.
 // Where ties or a margin full of neighbours make more candidates than fit, the row's groups of
 // 32 columns are walked in order instead, against the top-th best so far.
-constexpr int TOP_THREADS = 256;
+constexpr int TOP_THREADS = 128;
 constexpr int TOP_WARPS = TOP_THREADS / 32;
 constexpr int TOP_CANDIDATES = 512;
 constexpr int TOP_WHOLE = 14;                // groups taken whole
@@ -370,7 +370,7 @@ __device__ __forceinline__ double warp_exact(float s, float e) {
 }
 // The logits of a row and N rows of W as sums of exact products: those of bf16 numbers are
 // exact in fp32, those of fp32 ones come in two parts.  LOGIT_HELD vectors are asked for at once.
-constexpr int LOGIT_HELD = 4;
+constexpr int LOGIT_HELD = 2;
 template <int N>
 __device__ __forceinline__ void logits(const bf16* h, const bf16* const* w, int dim, int vec, int lane, double* out) {
   float s[N][2] = {}, e[N][2] = {};
@@ -433,14 +433,25 @@ __device__ __forceinline__ void logits(const float* h, const float* const* w, in
   for (int q = 0; q < N; ++q) out[q] = warp_exact(s[q], e[q]);
 }
 
-constexpr int TOP_HELD = 8;                  // pairs of groups whose keys a thread keeps (131072 entries)
+// A number's place among the doubles as a whole number (comparisons of doubles take 16 cycles a
+// warp); one that is masked or not a number has none.
+constexpr long long NO_PLACE = -0x7FFFFFFFFFFFFFFFLL - 1;
+__device__ __forceinline__ long long place_of(double v) {
+  const long long b = __double_as_longlong(v + 0.0);      // (-0 is 0)
+  return v > MASKED ? b ^ ((b >> 63) & 0x7FFFFFFFFFFFFFFFLL) : NO_PLACE;
+}
+__device__ __forceinline__ double at_place(long long k) {
+  return __longlong_as_double(k ^ ((k >> 63) & 0x7FFFFFFFFFFFFFFFLL));
+}
+
+constexpr int TOP_HELD = 8;                  // pairs of groups whose keys a thread keeps (65536 entries)
 struct TopShared {
-  double value[TOP_CANDIDATES];
+  long long value[TOP_CANDIDATES];           // place_of a logit
   int id[TOP_CANDIDATES];
-  float key[2 * TOP_THREADS];
+  float key[TOP_THREADS];
   float4 warp[TOP_WARPS];
   int whole[TOP_WHOLE];
-  double kept_value[MUON_LOGPROB_MAX_TOP];
+  long long kept_value[MUON_LOGPROB_MAX_TOP];
   int kept_id[MUON_LOGPROB_MAX_TOP];
   int count, wholes;
   float bound;
@@ -458,19 +469,32 @@ __device__ __forceinline__ float sort_lanes(float v, int lane) {
   return v;
 }
 
+// The 32 largest of two warps' numbers, both in descending order, in descending order.
+__device__ __forceinline__ float merge_lanes(float a, float b, int lane) {
+  float v = fmaxf(a, __shfl_sync(0xffffffffu, b, 31 - lane));
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2) {
+    const float o = __shfl_xor_sync(0xffffffffu, v, m);
+    v = (lane & m) == 0 ? fmaxf(v, o) : fminf(v, o);
+  }
+  return v;
+}
+
 // The best `top` of n candidates, in order, to kept_*; the others' places hold -1.  An id of
 // -1, a masked value or a NaN is no candidate.
 __device__ __forceinline__ void rank(TopShared& sh, int n, int top) {
   for (int i = threadIdx.x; i < top; i += TOP_THREADS) sh.kept_id[i] = -1;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += TOP_THREADS) {
-    const double v = sh.value[i];
+    const long long v = sh.value[i];
     const int id = sh.id[i];
-    if (id < 0 || !(v > MASKED)) continue;
+    if (id < 0 || v == NO_PLACE) continue;
     int better = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
-      const double u = sh.value[j];
-      better += sh.id[j] >= 0 && (u > v || (u == v && sh.id[j] < id));
+      const long long u = sh.value[j];
+      const int other = sh.id[j];
+      better += other >= 0 && (u > v || (u == v && other < id));
     }
     if (better < top) {
       sh.kept_value[better] = v;
@@ -480,27 +504,35 @@ __device__ __forceinline__ void rank(TopShared& sh, int n, int top) {
   __syncthreads();
 }
 
-// The values of the first n ids, two of them a warp at a time where there are as many.
+// The values of N ids of a warp, TOP_WARPS apart from i on.  (An id of -1 has no row; its value
+// is never looked at.)
+template <int N, typename T>
+__device__ __forceinline__ void evaluate_some(TopShared& sh, int i, const LogprobRows& p, const T* h, int lane) {
+  const T* w[N];
+  double v[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) w[q] = static_cast<const T*>(p.W) + max(sh.id[i + q * TOP_WARPS], 0) * p.ldw;
+  logits<N>(h, w, p.dim, p.vec, lane, v);
+#pragma unroll
+  for (int q = 0; q < N; ++q)
+    if (lane == q) sh.value[i + q * TOP_WARPS] = place_of(v[q]);
+}
+// The values of the first n ids, up to four of them a warp at a time.
 template <typename T>
 __device__ __forceinline__ void evaluate(TopShared& sh, int n, const LogprobRows& p, const T* h) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = warp; i < n; i += 2 * TOP_WARPS) {
-    const int j = i + TOP_WARPS, a = sh.id[i], b = j < n ? sh.id[j] : -1;
-    // (an id of -1 has no row; its value is never looked at)
-    const T* w[2] = {static_cast<const T*>(p.W) + max(a, 0) * p.ldw, static_cast<const T*>(p.W) + max(b, 0) * p.ldw};
-    double v[2] = {0.0, 0.0};
-    if (b >= 0) logits<2>(h, w, p.dim, p.vec, lane, v);
-    else if (a >= 0) logits<1>(h, w, p.dim, p.vec, lane, v);
-    if (lane == 0) {
-      sh.value[i] = v[0];
-      if (j < n) sh.value[j] = v[1];
-    }
+  int i = warp;
+  for (; i + 3 * TOP_WARPS < n; i += 4 * TOP_WARPS) evaluate_some<4>(sh, i, p, h, lane);
+  if (i + TOP_WARPS < n) {
+    evaluate_some<2>(sh, i, p, h, lane);
+    i += 2 * TOP_WARPS;
   }
+  if (i < n) evaluate_some<1>(sh, i, p, h, lane);
   __syncthreads();
 }
 
 template <typename T>
-__global__ void __launch_bounds__(TOP_THREADS, 3) top_kernel(const LogprobRows p) {
+__global__ void __launch_bounds__(TOP_THREADS, 6) top_kernel(const LogprobRows p) {
   __shared__ TopShared sh;
   await_previous();
   const long long r = blockIdx.x;
@@ -539,9 +571,9 @@ __global__ void __launch_bounds__(TOP_THREADS, 3) top_kernel(const LogprobRows p
   for (int i = 0; i < TOP_HELD; ++i) take(held[i]);
   for (int g = t + TOP_HELD * TOP_THREADS; g < groups / 2; g += TOP_THREADS) take(pairs[g]);
   // (few groups: the second largest count, too)
-  const int lists = groups >= 4 * TOP_THREADS ? 1 : 2;
-  sh.key[t] = sort_lanes(k1, lane);
-  if (lists == 2) sh.key[TOP_THREADS + t] = sort_lanes(k2, lane);
+  float best = sort_lanes(k1, lane);
+  if (groups < 4 * TOP_THREADS) best = merge_lanes(best, sort_lanes(k2, lane), lane);
+  sh.key[t] = best;
   if (t == 0) sh.bound = -INFINITY;
   __syncthreads();
   Moments all = {-INFINITY, 0.f, 0.f};
@@ -559,16 +591,11 @@ __global__ void __launch_bounds__(TOP_THREADS, 3) top_kernel(const LogprobRows p
     }
     return;
   }
-  // 1. the top-th largest of the threads' keys (-inf where there are fewer): it is among the
-  // first `top` of some warp
-  for (int l = 0; l < lists; ++l) {
-    const int i = l * TOP_THREADS + t;
-    const float k = sh.key[i];
-    if (lane >= top || !(k > MASKED)) continue;
-    int better = 0;
-    for (int w = 0; w < lists * TOP_WARPS; ++w)
-      for (int j = w * 32; j < w * 32 + top; ++j) better += sh.key[j] > k || (sh.key[j] == k && j < i);
-    if (better == top - 1) sh.bound = k;
+  // 1. the top-th largest of the threads' keys (-inf where there are fewer)
+  if (warp == 0) {
+#pragma unroll
+    for (int w = 1; w < TOP_WARPS; ++w) best = merge_lanes(best, sh.key[32 * w + lane], lane);
+    if (lane == top - 1 && best > MASKED) sh.bound = best;
   }
   __syncthreads();
   const float bound = sh.bound, margin = TOP_MARGIN * fmaxf(fabsf(all.m), bound == -INFINITY ? 0.f : fabsf(bound)) + 1e-30f;
@@ -629,14 +656,14 @@ __global__ void __launch_bounds__(TOP_THREADS, 3) top_kernel(const LogprobRows p
       rank(sh, KEY_COLS + kept, top);
       kept = 0;
       while (kept < top && sh.kept_id[kept] >= 0) ++kept;
-      if (kept == top) worst = sh.kept_value[top - 1];
+      if (kept == top) worst = at_place(sh.kept_value[top - 1]);
       __syncthreads();
     }
   }
   for (int i = t; i < top; i += TOP_THREADS) {
     const int id = sh.kept_id[i];
     ids[i] = id;
-    alternatives[i] = id < 0 ? -INFINITY : (float)(sh.kept_value[i] - (double)lse);
+    alternatives[i] = id < 0 ? -INFINITY : (float)(at_place(sh.kept_value[i]) - (double)lse);
   }
 }
 
@@ -762,10 +789,11 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
   P->piece = cdiv(cdiv(a->vocab, P->npieces), TILE) * TILE;
   P->npieces = cdiv(a->vocab, P->piece);
   P->splits = split_count(a->rows, a->dim, P->piece, 76);
-  if (top >= 0 && few_rows(a->rows, a->dim, f32, true)) {
-    P->few = take(few_bytes(a->rows, a->dim));
-    P->total = std::max(P->total, at);
-    at = common;
+  if (top >= 0) {
+    // (for more rows too, so that their workspace serves a few of them)
+    for (int64_t n = 1; n <= 8; n *= 2)
+      if (few_rows(n, a->dim, f32, true)) P->total = std::max(P->total, common + up(few_bytes(n, a->dim)));
+    if (few_rows(a->rows, a->dim, f32, true)) P->few = common;
   }
   P->g_part = (size_t)a->rows * P->piece;
   for (int i = 0; i < 2; ++i) P->g[i] = P->npieces > 1 || i == 0 ? take(P->parts * P->g_part * 2) : P->g[0];

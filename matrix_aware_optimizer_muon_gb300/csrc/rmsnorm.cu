@@ -256,6 +256,46 @@ __device__ __forceinline__ void store_word(T* row, int c, int dim, const uint4& 
       if (c + i >= 0 && c + i < dim) row[c + i] = x[i];
   }
 }
+template <typename T>
+__device__ __forceinline__ uint4 packed(const f32x2* v) {
+  if constexpr (sizeof(T) == 2)
+    return make_uint4(pack_bf16x2(lo2(v[0]), hi2(v[0])), pack_bf16x2(lo2(v[1]), hi2(v[1])), pack_bf16x2(lo2(v[2]), hi2(v[2])),
+                      pack_bf16x2(lo2(v[3]), hi2(v[3])));
+  else
+    return make_uint4(__float_as_uint(lo2(v[0])), __float_as_uint(hi2(v[0])), __float_as_uint(lo2(v[1])), __float_as_uint(hi2(v[1])));
+}
+// The weights of V columns from any c on, 0 outside the row.
+template <int V, class P>
+__device__ __forceinline__ void weights_at(const P& p, int c, f32x2* v) {
+  if (!p.w) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = both(1.f);
+  } else if (p.w_bf16) {
+    const bf16* w = static_cast<const bf16*>(p.w);
+    const int o = behind(w);
+    const uint4 a = load_at(w - o, c + o, p.dim + o);
+    v[0] = cvt2(a.x);
+    v[1] = cvt2(a.y);
+    if constexpr (V == 8) {
+      v[2] = cvt2(a.z);
+      v[3] = cvt2(a.w);
+    }
+  } else {
+    const float* w = static_cast<const float*>(p.w);
+    const int o = behind(w);
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) {
+      const uint4 a = load_at(w - o, c + 4 * h + o, p.dim + o);
+      v[2 * h] = make2(__uint_as_float(a.x), __uint_as_float(a.y));
+      v[2 * h + 1] = make2(__uint_as_float(a.z), __uint_as_float(a.w));
+    }
+  }
+  if (c < 0 || c + V > p.dim) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c + i < 0 || c + i >= p.dim) v[i / 2] = i & 1 ? make2(lo2(v[i / 2]), 0.f) : make2(0.f, hi2(v[i / 2]));
+  }
+}
 template <typename T, int kN, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? 32 * RMS_WARPS : RMS_MOST_THREADS) rms_forward_words_kernel(const RmsFwd p) {
   constexpr int V = 16 / (int)sizeof(T), C = V / 2;
@@ -308,40 +348,12 @@ __global__ void __launch_bounds__(kWarp ? 32 * RMS_WARPS : RMS_MOST_THREADS) rms
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] = mul2(v[i], both(rs));
     if (p.w && c < dim) {
-      if (p.w_bf16) {
-        const bf16* w = static_cast<const bf16*>(p.w);
-        const int o = behind(w);
-        if constexpr (V == 8) {
-          const uint4 a = load_at(w - o, c + o, dim + o);
-          v[0] = mul2(v[0], cvt2(a.x));
-          v[1] = mul2(v[1], cvt2(a.y));
-          v[2] = mul2(v[2], cvt2(a.z));
-          v[3] = mul2(v[3], cvt2(a.w));
-        } else {
+      f32x2 w[C];
+      weights_at<V>(p, c, w);
 #pragma unroll
-          for (int i = 0; i < C; ++i) {
-            auto at = [&](int c) { return c >= 0 && c < dim ? to_f32(w[c]) : 0.f; };
-            v[i] = mul2(v[i], make2(at(c + 2 * i), at(c + 2 * i + 1)));
-          }
-        }
-      } else {
-        const float* w = static_cast<const float*>(p.w);
-        const int o = behind(w);
-#pragma unroll
-        for (int h = 0; h < V / 4; ++h) {
-          const uint4 a = load_at(w - o, c + 4 * h + o, dim + o);
-          v[2 * h] = mul2(v[2 * h], make2(__uint_as_float(a.x), __uint_as_float(a.y)));
-          v[2 * h + 1] = mul2(v[2 * h + 1], make2(__uint_as_float(a.z), __uint_as_float(a.w)));
-        }
-      }
+      for (int i = 0; i < C; ++i) v[i] = mul2(v[i], w[i]);
     }
-    uint4 o;
-    if constexpr (V == 8)
-      o = make_uint4(pack_bf16x2(lo2(v[0]), hi2(v[0])), pack_bf16x2(lo2(v[1]), hi2(v[1])), pack_bf16x2(lo2(v[2]), hi2(v[2])),
-                     pack_bf16x2(lo2(v[3]), hi2(v[3])));
-    else
-      o = make_uint4(__float_as_uint(lo2(v[0])), __float_as_uint(hi2(v[0])), __float_as_uint(lo2(v[1])), __float_as_uint(hi2(v[1])));
-    store_word(y, c, dim, o);
+    store_word(y, c, dim, packed<T>(v));
   }
   if (p.rstd && t == 0) p.rstd[r] = rs;
 }
@@ -677,16 +689,32 @@ __global__ void __launch_bounds__(rms_threads(kN * 16 / (int)sizeof(T), kOdd), 1
 }
 
 // Rows wider than that: dx, a CTA a row with the row in registers, and the columns' sums over
-// slabs of rows in a pass of their own.
-template <typename T, int kN>
-__global__ void __launch_bounds__(RMS_MOST_THREADS) rms_dx_kernel(const RmsBwd p) {
+// slabs of rows in a pass of their own.  kOdd: rows off the words' boundaries, cut at dx's.
+template <typename T, int kN, bool kOdd>
+__global__ void __launch_bounds__(kN == 4 ? 768 : RMS_MOST_THREADS) rms_dx_kernel(const RmsBwd p) {
   constexpr int V = 16 / (int)sizeof(T), C = V / 2;
-  __shared__ float red[16];
+  __shared__ float red[24];
   const RowThreads g{(int)threadIdx.x, (int)blockDim.x, 0};
   const long long r = blockIdx.x;
+  T* dx = static_cast<T*>(p.dx) + r * p.lddx;
+  const int off = kOdd ? behind(dx) : 0;
+  auto column = [&](int k) { return (k * g.size + g.t) * V - off; };
+  auto word = [&](const T* row, int k) {
+    const int c = column(k);
+    if constexpr (!kOdd) return c < p.dim ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+    const int o = behind(row);
+    const uint4 q = load_at(row - o, c + o, p.dim + o);
+    return c < 0 || c + V > p.dim ? masked_word<T>(q, -c, p.dim - c) : q;
+  };
+  auto weight = [&](int k, f32x2* w) {
+    if constexpr (!kOdd) weights<V>(p.w, p.w_bf16, column(k), p.dim, 1.f, w);
+    else weights_at<V>(p, column(k), w);
+  };
   Raw<T, V, kN> a, b;
-  a.load(static_cast<const T*>(p.t) + r * p.ldt, g.t, g.size, p.dim);
-  b.load(static_cast<const T*>(p.dy) + r * p.lddy, g.t, g.size, p.dim);
+#pragma unroll
+  for (int k = 0; k < kN; ++k) a.q[k] = word(static_cast<const T*>(p.t) + r * p.ldt, k);
+#pragma unroll
+  for (int k = 0; k < kN; ++k) b.q[k] = word(static_cast<const T*>(p.dy) + r * p.lddy, k);
   const float rs = p.rstd[r];
   f32x2 s = both(0.f);
 #pragma unroll
@@ -694,102 +722,73 @@ __global__ void __launch_bounds__(RMS_MOST_THREADS) rms_dx_kernel(const RmsBwd p
     f32x2 x[C], y[C], w[C];
     a.get(k, x);
     b.get(k, y);
-    weights<V>(p.w, p.w_bf16, (k * g.size + g.t) * V, p.dim, 1.f, w);
+    weight(k, w);
 #pragma unroll
     for (int i = 0; i < C; ++i) s = fma2(mul2(y[i], w[i]), mul2(x[i], both(rs)), s);
   }
   a.hold();
   b.hold();
   const float m = -rs * (g.sum(lo2(s) + hi2(s), red) * (1.f / (float)p.dim));
-  T* dx = static_cast<T*>(p.dx) + r * p.lddx;
 #pragma unroll
   for (int k = 0; k < kN; ++k) {
-    const int c = (k * g.size + g.t) * V;
+    const int c = column(k);
     if (c >= p.dim) continue;
     f32x2 x[C], y[C], w[C];
     a.get(k, x);
     b.get(k, y);
-    weights<V>(p.w, p.w_bf16, c, p.dim, 1.f, w);
+    weight(k, w);
 #pragma unroll
     for (int i = 0; i < C; ++i) y[i] = fma2(mul2(y[i], w[i]), both(rs), mul2(mul2(x[i], both(rs)), both(m)));
     if (p.dtotal) {
-      widen(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.dtotal) + r * p.lddt + c), x, static_cast<const T*>(nullptr));
+      widen(word(static_cast<const T*>(p.dtotal) + r * p.lddt, k), x, static_cast<const T*>(nullptr));
 #pragma unroll
       for (int i = 0; i < C; ++i) y[i] = add2(x[i], y[i]);
     }
-    store16(dx + c, y);
+    if constexpr (!kOdd) store16(dx + c, y);
+    else store_word(dx, c, p.dim, packed<T>(y));
   }
 }
-template <typename T>
-__global__ void __launch_bounds__(512) rms_dx_odd_kernel(const RmsBwd p, int slot) {
-  extern __shared__ uint4 dyn[];
-  __shared__ float red[16];
-  const RowThreads g{(int)threadIdx.x, (int)blockDim.x, 0};
-  const long long r = blockIdx.x;
-  uint8_t* mine = reinterpret_cast<uint8_t*>(dyn);
-  const T* src[3] = {static_cast<const T*>(p.t) + r * p.ldt, static_cast<const T*>(p.dy) + r * p.lddy,
-                     p.dtotal ? static_cast<const T*>(p.dtotal) + r * p.lddt : nullptr};
-  const T* at[3] = {};
-#pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (src[i]) {
-      T* o = reinterpret_cast<T*>(mine + i * slot);
-      fetch_row(o, src[i], p.dim, g.t, g.size);
-      at[i] = o + behind(src[i]);
-    }
-  T* dx = static_cast<T*>(p.dx) + r * p.lddx;
-  T* out = reinterpret_cast<T*>(mine + (p.dtotal ? 3 : 2) * slot);
-  const float rs = p.rstd[r];
-  copies_done();
-  g.sync();
-  float s = 0.f;
-#pragma unroll 4
-  for (int c = g.t; c < p.dim; c += g.size)
-    s = fmaf(to_f32(at[1][c]) * (p.w ? ld_w(p.w, p.w_bf16, c) : 1.f), to_f32(at[0][c]) * rs, s);
-  const float m = -rs * (g.sum(s, red) * (1.f / (float)p.dim));
-  T* to = out + behind(dx);
-#pragma unroll 4
-  for (int c = g.t; c < p.dim; c += g.size) {
-    const float v = fmaf(to_f32(at[1][c]) * (p.w ? ld_w(p.w, p.w_bf16, c) : 1.f), rs, to_f32(at[0][c]) * rs * m);
-    to[c] = from_f32<T>(p.dtotal ? to_f32(at[2][c]) + v : v);
-  }
-  g.sync();
-  flush_row(dx, out, p.dim, g.t, g.size);
-}
-// kV columns a thread.
+// A word of columns a thread.  Rows a number of slabs apart that is one of a word's elements
+// begin at the same place in their words (kOdd: those of t).
 constexpr int RMS_SLAB_THREADS = 128;
-template <typename T, int kV>
+template <typename T, bool kOdd>
 __global__ void __launch_bounds__(RMS_SLAB_THREADS) rms_slab_kernel(const RmsBwd p) {
-  constexpr int P = (kV + 1) / 2;
-  const int c = (blockIdx.x * RMS_SLAB_THREADS + threadIdx.x) * kV;
+  constexpr int V = 16 / (int)sizeof(T), P = V / 2, H = 4;     // H rows in flight
+  const int off = kOdd ? behind(static_cast<const T*>(p.t) + blockIdx.y * p.ldt) : 0;
+  const int og = kOdd ? behind(static_cast<const T*>(p.dy) + blockIdx.y * p.lddy) : 0;
+  const int c = (blockIdx.x * RMS_SLAB_THREADS + threadIdx.x) * V - off;
   if (c >= p.dim) return;
   f32x2 s[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) s[i] = both(0.f);
-  constexpr int H = 4;                 // rows in flight
+  auto word = [&](const T* row, int o) {
+    if constexpr (!kOdd) return *reinterpret_cast<const uint4*>(row + c);
+    return load_at(row - o, c + o, p.dim + o);
+  };
   for (long long r0 = blockIdx.y; r0 < p.rows; r0 += (long long)gridDim.y * H) {
-    Raw<T, kV, 1> a[H], b[H];
+    uint4 a[H], b[H];
     float rs[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       const long long r = r0 + (long long)gridDim.y * h, q = r < p.rows ? r : r0;
-      a[h].template load<1>(static_cast<const T*>(p.t) + q * p.ldt + c, 0, 1, p.dim);
-      b[h].template load<1>(static_cast<const T*>(p.dy) + q * p.lddy + c, 0, 1, p.dim);
+      a[h] = word(static_cast<const T*>(p.t) + q * p.ldt, off);
+      b[h] = word(static_cast<const T*>(p.dy) + q * p.lddy, og);
       rs[h] = r < p.rows ? p.rstd[r] : 0.f;
     }
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       if (h > 0 && r0 + (long long)gridDim.y * h >= p.rows) break;
       f32x2 x[P], y[P];
-      a[h].get(0, x);
-      b[h].get(0, y);
+      widen(a[h], x, static_cast<const T*>(nullptr));
+      widen(b[h], y, static_cast<const T*>(nullptr));
 #pragma unroll
       for (int i = 0; i < P; ++i) s[i] = fma2(y[i], mul2(x[i], both(rs[h])), s[i]);
     }
   }
-  float* o = p.part + (size_t)blockIdx.y * p.dim + c;
+  float* o = p.part + (size_t)blockIdx.y * p.dim;
 #pragma unroll
-  for (int e = 0; e < kV; ++e) o[e] = elem(s, e);
+  for (int e = 0; e < V; ++e)
+    if (!kOdd || (c + e >= 0 && c + e < p.dim)) o[c + e] = elem(s, e);   // (what lies outside the row was summed, too)
 }
 
 // Rows of any length: dx with the row read twice.
@@ -944,24 +943,17 @@ cudaError_t backward(const RmsBwd& p, bool vec, int* lines, cudaStream_t s) {
   if (!vec && threads(16 / V) <= rms_threads(16, true)) return backward_words<T, 16 / V, true>(p, threads(16 / V), lines, s);
   // the columns' sums before dx, which may be dy itself
   if (p.part) {
-    *lines = (int)std::min<long long>(p.rows, RMS_CTAS);
+    *lines = (int)std::min<long long>((p.rows + V - 1) / V * V, RMS_CTAS);   // (152 is a multiple of V)
+    const dim3 grid(cdiv(n, RMS_SLAB_THREADS), *lines);
     count_launch();
-    if (vec) rms_slab_kernel<T, V><<<dim3(cdiv(n, RMS_SLAB_THREADS), *lines), RMS_SLAB_THREADS, 0, s>>>(p);
-    else rms_slab_kernel<T, 1><<<dim3(cdiv(p.dim, RMS_SLAB_THREADS), *lines), RMS_SLAB_THREADS, 0, s>>>(p);
+    if (vec) rms_slab_kernel<T, false><<<grid, RMS_SLAB_THREADS, 0, s>>>(p);
+    else rms_slab_kernel<T, true><<<grid, RMS_SLAB_THREADS, 0, s>>>(p);
   }
   count_launch();
-  const size_t smem = (size_t)(p.dtotal ? 4 : 3) * slot_bytes<T>(std::min(p.dim, 1 << 20));
-  if (vec && n <= 4 * RMS_MOST_THREADS) {
-    rms_dx_kernel<T, 4><<<(unsigned)p.rows, 32 * cdiv(n, 128), 0, s>>>(p);
-  } else if (vec && n <= 8 * RMS_MOST_THREADS) {
-    rms_dx_kernel<T, 8><<<(unsigned)p.rows, 32 * cdiv(n, 256), 0, s>>>(p);
-  } else if (smem <= (size_t)RMS_ODD_SMEM) {
-    const cudaError_t e = allow_smem(rms_dx_odd_kernel<T>, smem);
-    if (e != cudaSuccess) return e;
-    rms_dx_odd_kernel<T><<<(unsigned)p.rows, odd_threads(p.dim), smem, s>>>(p, slot_bytes<T>(p.dim));
-  } else {
-    rms_backward_loop_kernel<T><<<(unsigned)p.rows, RMS_LOOP_THREADS, 0, s>>>(p);
-  }
+  auto dx = [&](auto kern, int each) { kern<<<(unsigned)p.rows, 32 * cdiv(n, 32LL * each), 0, s>>>(p); };
+  if (n <= 4 * 768) vec ? dx(rms_dx_kernel<T, 4, false>, 4) : dx(rms_dx_kernel<T, 4, true>, 4);
+  else if (n <= 8 * RMS_MOST_THREADS) vec ? dx(rms_dx_kernel<T, 8, false>, 8) : dx(rms_dx_kernel<T, 8, true>, 8);
+  else rms_backward_loop_kernel<T><<<(unsigned)p.rows, RMS_LOOP_THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
 
