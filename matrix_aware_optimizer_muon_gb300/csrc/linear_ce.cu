@@ -344,8 +344,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) logprob_kernel(const LogprobR
 //   3. their logits again, a warp each; 4. their ranks, ties to the lower index.
 // Where ties or a margin full of neighbours make more candidates than fit, the row's groups of
 // 32 columns are walked in order instead, against the top-th best so far.
-constexpr int TOP_THREADS = 128;
-constexpr int TOP_WARPS = TOP_THREADS / 32;
+// Many rows: 128 threads, so that many rows are at hand (4096 x 32000 with 8 alternatives, by 64,
+// 128 and 256 threads: 255, 237 and 349 us).  Few rows, whose every wait shows: 512, a
+// candidate a warp and a row's words asked for at once.
+constexpr int TOP_MANY = 128, TOP_FEW = 512, TOP_FEW_ROWS = 152;
 constexpr int TOP_CANDIDATES = 512;
 constexpr int TOP_WHOLE = 14;                // groups taken whole
 constexpr float TOP_MARGIN = 0x1p-12f;
@@ -369,24 +371,24 @@ __device__ __forceinline__ double warp_exact(float s, float e) {
   return (double)s + (double)e;
 }
 // The logits of a row and N rows of W as sums of exact products: those of bf16 numbers are
-// exact in fp32, those of fp32 ones come in two parts.  LOGIT_HELD vectors are asked for at once.
-constexpr int LOGIT_HELD = 2;
-template <int N>
+// exact in fp32, those of fp32 ones come in two parts.  kHeld vectors are asked for at once (the
+// order of the sums does not depend on it).
+template <int N, int kHeld>
 __device__ __forceinline__ void logits(const bf16* h, const bf16* const* w, int dim, int vec, int lane, double* out) {
   float s[N][2] = {}, e[N][2] = {};
   const int whole = vec ? dim / 8 : 0;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  for (int c0 = lane; c0 < whole; c0 += 32 * LOGIT_HELD) {
-    uint4 a[LOGIT_HELD], b[N][LOGIT_HELD];
+  for (int c0 = lane; c0 < whole; c0 += 32 * kHeld) {
+    uint4 a[kHeld], b[N][kHeld];
 #pragma unroll
-    for (int i = 0; i < LOGIT_HELD; ++i) {
+    for (int i = 0; i < kHeld; ++i) {
       const int c = c0 + 32 * i;
       a[i] = c < whole ? reinterpret_cast<const uint4*>(h)[c] : none;
 #pragma unroll
       for (int q = 0; q < N; ++q) b[q][i] = c < whole ? reinterpret_cast<const uint4*>(w[q])[c] : none;
     }
 #pragma unroll
-    for (int i = 0; i < LOGIT_HELD; ++i) {
+    for (int i = 0; i < kHeld; ++i) {
       const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
 #pragma unroll
       for (int q = 0; q < N; ++q) {
@@ -408,20 +410,20 @@ __device__ __forceinline__ void logits(const bf16* h, const bf16* const* w, int 
     out[q] = warp_exact(s[q][0], __fadd_rn(e[q][0], e[q][1]));
   }
 }
-template <int N>
+template <int N, int kHeld>
 __device__ __forceinline__ void logits(const float* h, const float* const* w, int dim, int, int lane, double* out) {
   float s[N] = {}, e[N] = {};
-  for (int c0 = lane; c0 < dim; c0 += 64 * LOGIT_HELD) {
-    float a[2 * LOGIT_HELD], b[N][2 * LOGIT_HELD];
+  for (int c0 = lane; c0 < dim; c0 += 64 * kHeld) {
+    float a[2 * kHeld], b[N][2 * kHeld];
 #pragma unroll
-    for (int i = 0; i < 2 * LOGIT_HELD; ++i) {
+    for (int i = 0; i < 2 * kHeld; ++i) {
       const int c = c0 + 32 * i;
       a[i] = c < dim ? h[c] : 0.f;
 #pragma unroll
       for (int q = 0; q < N; ++q) b[q][i] = c < dim ? w[q][c] : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 2 * LOGIT_HELD; ++i)
+    for (int i = 0; i < 2 * kHeld; ++i)
 #pragma unroll
       for (int q = 0; q < N; ++q) {
         const float x = __fmul_rn(a[i], b[q][i]);
@@ -445,11 +447,11 @@ __device__ __forceinline__ double at_place(long long k) {
 }
 
 constexpr int TOP_HELD = 8;                  // pairs of groups whose keys a thread keeps (65536 entries)
-struct TopShared {
+template <int kThreads> struct TopShared {
   long long value[TOP_CANDIDATES];           // place_of a logit
   int id[TOP_CANDIDATES];
-  float key[TOP_THREADS];
-  float4 warp[TOP_WARPS];
+  float key[kThreads];
+  float4 warp[kThreads / 32];
   int whole[TOP_WHOLE];
   long long kept_value[MUON_LOGPROB_MAX_TOP];
   int kept_id[MUON_LOGPROB_MAX_TOP];
@@ -482,10 +484,11 @@ __device__ __forceinline__ float merge_lanes(float a, float b, int lane) {
 
 // The best `top` of n candidates, in order, to kept_*; the others' places hold -1.  An id of
 // -1, a masked value or a NaN is no candidate.
-__device__ __forceinline__ void rank(TopShared& sh, int n, int top) {
-  for (int i = threadIdx.x; i < top; i += TOP_THREADS) sh.kept_id[i] = -1;
+template <int kThreads>
+__device__ __forceinline__ void rank(TopShared<kThreads>& sh, int n, int top) {
+  for (int i = threadIdx.x; i < top; i += kThreads) sh.kept_id[i] = -1;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += TOP_THREADS) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
     const long long v = sh.value[i];
     const int id = sh.id[i];
     if (id < 0 || v == NO_PLACE) continue;
@@ -504,36 +507,38 @@ __device__ __forceinline__ void rank(TopShared& sh, int n, int top) {
   __syncthreads();
 }
 
-// The values of N ids of a warp, TOP_WARPS apart from i on.  (An id of -1 has no row; its value
-// is never looked at.)
-template <int N, typename T>
-__device__ __forceinline__ void evaluate_some(TopShared& sh, int i, const LogprobRows& p, const T* h, int lane) {
+// The values of N ids of a warp, as many apart as there are warps, from i on.  (An id of -1 has
+// no row; its value is never looked at.)
+template <int N, int kHeld, typename T, int kThreads>
+__device__ __forceinline__ void evaluate_some(TopShared<kThreads>& sh, int i, const LogprobRows& p, const T* h, int lane) {
   const T* w[N];
   double v[N];
 #pragma unroll
-  for (int q = 0; q < N; ++q) w[q] = static_cast<const T*>(p.W) + max(sh.id[i + q * TOP_WARPS], 0) * p.ldw;
-  logits<N>(h, w, p.dim, p.vec, lane, v);
+  for (int q = 0; q < N; ++q) w[q] = static_cast<const T*>(p.W) + max(sh.id[i + q * (kThreads / 32)], 0) * p.ldw;
+  logits<N, kHeld>(h, w, p.dim, p.vec, lane, v);
 #pragma unroll
   for (int q = 0; q < N; ++q)
-    if (lane == q) sh.value[i + q * TOP_WARPS] = place_of(v[q]);
+    if (lane == q) sh.value[i + q * (kThreads / 32)] = place_of(v[q]);
 }
 // The values of the first n ids, up to four of them a warp at a time.
-template <typename T>
-__device__ __forceinline__ void evaluate(TopShared& sh, int n, const LogprobRows& p, const T* h) {
+template <typename T, int kThreads>
+__device__ __forceinline__ void evaluate(TopShared<kThreads>& sh, int n, const LogprobRows& p, const T* h) {
+  constexpr int W = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int i = warp;
-  for (; i + 3 * TOP_WARPS < n; i += 4 * TOP_WARPS) evaluate_some<4>(sh, i, p, h, lane);
-  if (i + TOP_WARPS < n) {
-    evaluate_some<2>(sh, i, p, h, lane);
-    i += 2 * TOP_WARPS;
+  for (; i + 3 * W < n; i += 4 * W) evaluate_some<4, 2>(sh, i, p, h, lane);
+  if (i + W < n) {
+    evaluate_some<2, 2>(sh, i, p, h, lane);
+    i += 2 * W;
   }
-  if (i < n) evaluate_some<1>(sh, i, p, h, lane);
+  if (i < n) evaluate_some<1, kThreads == TOP_FEW ? 6 : 2>(sh, i, p, h, lane);
   __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(TOP_THREADS, 6) top_kernel(const LogprobRows p) {
-  __shared__ TopShared sh;
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 6) top_kernel(const LogprobRows p) {
+  constexpr int TOP_THREADS = kThreads, TOP_WARPS = kThreads / 32;
+  __shared__ TopShared<kThreads> sh;
   await_previous();
   const long long r = blockIdx.x;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, top = p.top;
@@ -1013,10 +1018,12 @@ int join_rows(const muon_linear_ce* a, int top, const Params& p, int parts, floa
   cudaError_t e;
   if (top == 0)
     e = launch_after(logprob_kernel, dim3((unsigned)cdiv(a->rows, JOIN_WARPS)), dim3(32 * JOIN_WARPS), 0, s, q);
-  else if (a->dtype == MUON_DTYPE_BF16)
-    e = launch_after(top_kernel<bf16>, dim3((unsigned)a->rows), dim3(TOP_THREADS), 0, s, q);
+  else if (a->rows <= TOP_FEW_ROWS)
+    e = a->dtype == MUON_DTYPE_BF16 ? launch_after(top_kernel<bf16, TOP_FEW>, dim3((unsigned)a->rows), dim3(TOP_FEW), 0, s, q)
+                                    : launch_after(top_kernel<float, TOP_FEW>, dim3((unsigned)a->rows), dim3(TOP_FEW), 0, s, q);
   else
-    e = launch_after(top_kernel<float>, dim3((unsigned)a->rows), dim3(TOP_THREADS), 0, s, q);
+    e = a->dtype == MUON_DTYPE_BF16 ? launch_after(top_kernel<bf16, TOP_MANY>, dim3((unsigned)a->rows), dim3(TOP_MANY), 0, s, q)
+                                    : launch_after(top_kernel<float, TOP_MANY>, dim3((unsigned)a->rows), dim3(TOP_MANY), 0, s, q);
   if (e != cudaSuccess) return MUON_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

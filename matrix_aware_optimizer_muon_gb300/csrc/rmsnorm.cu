@@ -819,8 +819,16 @@ __global__ void __launch_bounds__(1024) rms_columns_kernel(const float* part, in
   await_previous();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
-  if (c < dim)
-    for (int i = threadIdx.y; i < lines; i += 32) s += part[(size_t)i * dim + c];
+  if (c < dim) {
+    float v[(RMS_CTAS + 31) / 32];               // all of them asked for at once
+#pragma unroll
+    for (int i = 0; i < (RMS_CTAS + 31) / 32; ++i) {
+      const int l = 32 * i + threadIdx.y;
+      v[i] = l < lines ? part[(size_t)l * dim + c] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < (RMS_CTAS + 31) / 32; ++i) s += v[i];
+  }
   tile[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   s = warp_sum(tile[threadIdx.x][threadIdx.y]);
