@@ -4,6 +4,12 @@
 // and, forward, y in 8 bits: e4m3 codes with one fp32 scale for each row and 128 columns.
 // Every sum is fp32.  t is rounded before it is normed: it is what the residual stream keeps
 // and what the backward pass reads.
+//
+// Bandwidth-bound.  Measured, of a copy's 6.68 TB/s: 32768 x 1536 bf16 with a residual, forward
+// with the output in 8 bits 59 us (6.0 TB/s), backward with the weight's gradient 68 us (5.9; the
+// column sums' kernel 4 of them); 32768 x 1537 bf16, rows off every 16-byte boundary, 85 and 87 us (4.7),
+// in 8 bits 142 (2.5); 5003 x 1537 fp32 backward 24.7 us (3.7).  What bounds the odd ones is
+// instructions: windows, masks and, in 8 bits, elements through shared memory.
 #include <algorithm>
 #include <cmath>
 #include <cuda_fp8.h>
