@@ -649,6 +649,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 6) top_ker
     evaluate(sh, n, p, h);
     rank(sh, n, top);
   } else {
+    // a row of zeros (padding): every logit is 0
+    bool zero = true;
+    for (int c = t; c < p.dim; c += TOP_THREADS) zero = zero && ld1(h + c) == 0.f;
+    if (__syncthreads_and(zero)) {
+      for (int i = t; i < top; i += TOP_THREADS) {
+        ids[i] = i < p.vocab ? i : -1;
+        alternatives[i] = i < p.vocab ? -lse : -INFINITY;
+      }
+      return;
+    }
     // every group against the best so far, KEY_COLS columns at a time
     int kept = 0;
     double worst = -INFINITY;      // of the kept, when there are `top`
