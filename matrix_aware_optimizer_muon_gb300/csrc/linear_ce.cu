@@ -542,7 +542,7 @@ __device__ __forceinline__ void evaluate(TopShared<kThreads>& sh, int n, const L
 }
 
 template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 6) top_kernel(const LogprobRows p) {
+__global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 8) top_kernel(const LogprobRows p) {
   constexpr int TOP_THREADS = kThreads, TOP_WARPS = kThreads / 32;
   __shared__ TopShared<kThreads> sh;
   await_previous();
