@@ -383,10 +383,98 @@ __device__ __forceinline__ float2 largest_two(const float (&v)[32]) {
   return make_float2(a[0], b[0]);
 }
 
-// The statistics of the log probabilities over this thread's 128 columns: max, sum of
-// exponentials, their sum times the distance from the max (for the entropy), the token's
-// logit and, where alternatives are asked for, the two largest logits of each 32 columns.
-// Columns past the end are masked like any other.
+// The statistics of the log probabilities over 128 columns of a row: max, sum of exponentials,
+// their sum times the distance from the max (for the entropy), the token's logit and, where
+// alternatives are asked for, the two largest logits of each 32 columns.  32 columns at a time
+// (the form without take-overs never holds more: the registers that 128 would take are what
+// keeps a warp's arithmetic from overlapping), joined at the end.
+struct RowStats {
+  float m[CHUNKS], s[CHUNKS], t[CHUNKS];
+  float2 two[CHUNKS];
+  float z;
+};
+// Column `at` is the token's; columns from `cols` on are masked like any other.
+__device__ __forceinline__ void take_columns(RowStats& x, int k, float (&v)[32], int cols, int at, bool keys) {
+  if (cols < 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j >= cols) v[j] = -INFINITY;
+  }
+  float top[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top[i] = fmaxf(v[8 * i], v[8 * i + 1]);
+#pragma unroll
+    for (int j = 2; j < 8; j += 2) top[i] = max3(top[i], v[8 * i + j], v[8 * i + j + 1]);
+  }
+  const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  f32x2 s[4], t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = t[i] = both(0.f);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const f32x2 d = add2(make2(v[2 * j], v[2 * j + 1]), both(-ref));
+    const f32x2 y = mul2(d, both(1.4426950408889634f));
+    const f32x2 e = make2(exp2_approx(lo2(y)), exp2_approx(hi2(y)));
+    s[j % 4] = add2(s[j % 4], e);
+    t[j % 4] = fma2(e, d, t[j % 4]);
+  }
+  const f32x2 ss = add2(add2(s[0], s[1]), add2(s[2], s[3])), tt = add2(add2(t[0], t[1]), add2(t[2], t[3]));
+  const float sum = lo2(ss) + hi2(ss);
+  float far = lo2(tt) + hi2(tt);
+  const bool masked = far != far;   // columns of minus infinity: 0 times that
+  if (masked && sum == sum) {
+    far = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float d = v[j] - ref;
+      far = fmaf(__expf(d), fmaxf(d, LOG_FLOOR), far);
+    }
+  }
+  x.m[k] = mx;
+  x.s[k] = sum;
+  x.t[k] = far;
+  if (at >= 0 && at < 32 && at < cols) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j == at) x.z = v[j];
+  }
+  if (keys) {
+    // a key of minus infinity would be a NaN, which a minimum passes over too
+    if (masked) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = fmaxf(v[j], -0x1.fffffep127f);
+    }
+    x.two[k] = largest_two(v);
+  }
+  // (what is known of these columns is computed before the next are loaded)
+  asm volatile("" : "+f"(x.m[k]), "+f"(x.s[k]), "+f"(x.t[k]), "+f"(x.two[k].x), "+f"(x.two[k].y));
+}
+// token: the token's column among the thread's, or none.
+__device__ __forceinline__ void write_stats(const Params& p, const Work& J, const Tile& ti, int half, int r, int token,
+                                            const RowStats& x) {
+  const float mx = fmaxf(max3(x.m[0], x.m[1], x.m[2]), x.m[3]), ref = mx == -INFINITY ? 0.f : mx;
+  float s = 0.f, t = 0.f;
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k) {
+    // far below the max nothing is added, and the distance has to stay finite
+    const float d = fmaxf(x.m[k] - ref, LOG_FLOOR), f = __expf(d);
+    const bool none = x.m[k] == -INFINITY;
+    s += none ? x.s[k] : f * x.s[k];
+    t += none ? x.t[k] : f * fmaf(d, x.s[k], x.t[k]);
+  }
+  const size_t at128 = (size_t)r * (2 * J.ntiles) + 2 * ti.tn + half;
+  p.stat[at128] = make_float4(mx, s, t, 0.f);
+  if (token >= 0) p.zlabel[r] = x.z;
+  if (p.keys) {
+    float4* o = reinterpret_cast<float4*>(p.keys + at128 * CHUNKS);
+#pragma unroll
+    for (int k = 0; k < CHUNKS; k += 2) o[k / 2] = make_float4(x.two[k].x, x.two[k].y, x.two[k + 1].x, x.two[k + 1].y);
+  }
+}
+
+// The same of a tile of several segments, whose 128 sums a thread holds: one max for all.
 __device__ __forceinline__ void finish_logprob(const Params& p, const Work& J, const Tile& ti, int half, int r, int cbase,
                                                float (&acc)[CHUNKS][32]) {
   if (r >= J.m) return;
@@ -633,6 +721,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
         finish_sum(p, J, ti.split, r, c0, u, stage, lane, v);
       };
       const int nseg = kPromote ? segments(J, p.nterms) : 1;
+      RowStats stats = {};                      // (a LOGPROB tile of one segment)
+      int token = -1;                           // the token's column among this thread's 128
+      if constexpr (kLogprob && !kPromote) {
+        if (J.kind == LOGPROB && p.labels && r < J.m) {
+          const long long at = p.labels[r] - cbase;
+          if (at >= 0 && at < HALF && at < J.n - cbase) token = (int)at;
+        }
+      }
       float acc[kPromote ? CHUNKS : 1][32];
       for (int seg = 0; seg < nseg; ++seg, ++it) {
         const int a = it & 1;
@@ -649,6 +745,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
           } else {
             float v[32];
             ptx::tmem_ld_32x32b_x32(tb + k * 32, v);
+            if constexpr (kLogprob) {
+              if (J.kind == LOGPROB) {
+                take_columns(stats, k, v, J.n - cbase - 32 * k, token - 32 * k, p.keys != nullptr);
+                continue;
+              }
+            }
             finish(cbase + k * 32, v);
           }
         }
@@ -658,6 +760,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
           if (even) ptx::mbar_arrive(&tempty[a]);
           else ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&tempty[a]), 0));
         }
+      }
+      if constexpr (kLogprob && !kPromote) {
+        if (!stop && J.kind == LOGPROB && r < J.m) write_stats(p, J, ti, half, r, token, stats);
       }
       if constexpr (kPromote) {
         if (!stop && J.kind == (kLogprob ? LOGPROB : LOGITS)) {

@@ -526,17 +526,13 @@ __device__ __forceinline__ void evaluate_some(TopShared<kThreads>& sh, int i, co
   for (int q = 0; q < N; ++q)
     if (lane == q) sh.value[i + q * (kThreads / 32)] = place_of(v[q]);
 }
-// The values of the first n ids, up to four of them a warp at a time.
+// The values of the first n ids, two of them a warp at a time where there are as many.
 template <typename T, int kThreads>
 __device__ __forceinline__ void evaluate(TopShared<kThreads>& sh, int n, const LogprobRows& p, const T* h) {
   constexpr int W = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int i = warp;
-  for (; i + 3 * W < n; i += 4 * W) evaluate_some<4, 2>(sh, i, p, h, lane);
-  if (i + W < n) {
-    evaluate_some<2, 2>(sh, i, p, h, lane);
-    i += 2 * W;
-  }
+  for (; i + W < n; i += 2 * W) evaluate_some<2, 2>(sh, i, p, h, lane);
   if (i < n) evaluate_some<1, kThreads == TOP_FEW ? 6 : 2>(sh, i, p, h, lane);
   __syncthreads();
 }
@@ -1284,7 +1280,8 @@ extern "C" int muon_linear_logprob_forward(const muon_linear_ce* a, int top, flo
   j.seg_kb = P.nterms > 1 ? SEG_F32 : j.mtiles == 1 ? SEG_FEW : (int)cdiv(j.nkb, cdiv(j.nkb, SEG_BF16));
   p.njobs = 1;
   p.tiles = j.tiles;
-  if (launch(p, false, true, true, s) != cudaSuccess) return MUON_ERR_CUDA;
+  const bool promote = P.nterms > 1 || j.nkb > j.seg_kb;
+  if (launch(p, false, promote, true, s) != cudaSuccess) return MUON_ERR_CUDA;
   return join_rows(a, top, p, 2 * j.ntiles, logprob, entropy, lse, ids, alternatives, s);
 }
 
