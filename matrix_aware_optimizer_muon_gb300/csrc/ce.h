@@ -97,7 +97,7 @@ struct Few {
   float4* stat;
   float2* keys;
   float* zlabel;
-  int parts;
+  int parts;                     // statistics a row
   // backward
   const float *lse, *entropy, *g_logprob, *g_entropy;
   float* dh_part;                // [CTA][rows, padded][dp], or null
@@ -105,6 +105,7 @@ struct Few {
 };
 bool few_rows(int64_t rows, int64_t dim, bool f32, bool backward);   // whether it is one
 size_t few_bytes(int64_t rows, int64_t dim);     // of dh_part
+int few_block(int64_t vocab);                    // columns of a statistic
 cudaError_t few_forward(Few p, bool f32, bool vec, cudaStream_t s);
 cudaError_t few_backward(Few p, bool f32, bool vec, void* dH, cudaStream_t s);
 

@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_kernel(const float2* par
 // ---------------------------------------------------------------------------
 struct LogprobRows {
   const float4* stat;        // [row][parts]
-  const float2* keys;        // [row][parts * 4], with alternatives
-  int parts;
+  const float2* keys;        // [row][groups], with alternatives
+  int parts, groups;
   long long rows;
   const int64_t* labels;     // or null: no token is given
   long long vocab, ignore;
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 8) top_ker
   if (lane == 0) sh.warp[warp] = make_float4(mine.m, mine.s, mine.t, 0.f);
   if (t == 0) sh.count = sh.wholes = 0;
   // the thread's two largest keys
-  const int groups = p.parts * (TILE / 2 / KEY_COLS);
+  const int groups = p.groups;
   const float2* keys = p.keys + (size_t)r * groups;
   const float4* pairs = reinterpret_cast<const float4*>(keys);
   float4 held[TOP_HELD];
@@ -792,7 +792,10 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
     P->part = take((size_t)a->rows * 2 * cdiv(a->vocab, TILE) * sizeof(float2));
     P->sums = take((size_t)cdiv(a->rows, JOIN_WARPS) * sizeof(float2));
   } else {
-    P->stat = take((size_t)a->rows * 2 * cdiv(a->vocab, TILE) * sizeof(float4));
+    int64_t stats = a->rows * 2;                // of a tile's columns; more where a few of the rows would have more
+    for (int64_t n = 1; n <= std::min<int64_t>(a->rows, 16); ++n)
+      if (few_rows(n, a->dim, f32, false)) stats = std::max(stats, n * (TILE / few_block(a->vocab)));
+    P->stat = take((size_t)stats * cdiv(a->vocab, TILE) * sizeof(float4));
     P->keys = take(top ? (size_t)a->rows * (TILE / KEY_COLS) * cdiv(a->vocab, TILE) * sizeof(float2) : 0);
   }
   P->total = at;
@@ -1007,6 +1010,7 @@ int join_rows(const muon_linear_ce* a, int top, const Params& p, int parts, floa
   q.stat = p.stat;
   q.keys = p.keys;
   q.parts = parts;
+  q.groups = (int)(TILE / KEY_COLS * cdiv(a->vocab, TILE));
   q.rows = a->rows;
   q.labels = a->labels;
   q.vocab = a->vocab;
@@ -1268,9 +1272,9 @@ extern "C" int muon_linear_logprob_forward(const muon_linear_ce* a, int top, flo
     f.stat = p.stat;
     f.keys = p.keys;
     f.zlabel = p.zlabel;
-    f.parts = 2 * j.ntiles;
+    f.parts = TILE / few_block(a->vocab) * j.ntiles;
     if (few_forward(f, a->dtype == MUON_DTYPE_F32, w_vec, s) != cudaSuccess) return MUON_ERR_CUDA;
-    return join_rows(a, top, p, 2 * j.ntiles, logprob, entropy, lse, ids, alternatives, s);
+    return join_rows(a, top, p, f.parts, logprob, entropy, lse, ids, alternatives, s);
   }
   Operand H, W;
   if (operand(&H, a, P, true, false, w, s) != cudaSuccess || operand(&W, a, P, false, false, w, s) != cudaSuccess)

@@ -7,12 +7,13 @@
 // rows leave most of themselves empty; 32-bit operands would besides be written and read
 // again as three bf16 parts.  Here the rows of H lie in shared memory as fp32 numbers; a warp reads four rows
 // of W at a time, so that a word of H serves four products, and adds in fp32 (a lane dim/32
-// products, then a tree).  What a statistic of 128 columns or a key is, ce.h says: the
-// kernels that join them are those of the other path.
+// products, then a tree).  What a statistic or a key is, ce.h says: the kernels that join them
+// are those of the other path.
 #include <algorithm>
+#include <type_traits>
 
 #include "ce.h"
-#include "common.cuh"
+#include "rows.cuh"
 
 namespace muon {
 namespace ce {
@@ -21,9 +22,18 @@ namespace {
 constexpr int FEW_THREADS = 256;
 constexpr int FEW_WARPS = FEW_THREADS / 32;
 constexpr int FEW_AT_ONCE = 4;              // rows of W a warp multiplies at a time
-constexpr int FEW_BLOCK = 128;              // columns of a statistic
+constexpr int FEW_BLOCK = 128;              // columns of a statistic; 32 where that leaves SMs without work
 constexpr int FEW_PIECE = FEW_WARPS * FEW_AT_ONCE;   // rows of W a CTA takes at a time in the backward pass
+static_assert(FEW_PIECE == KEY_COLS, "a short block is a group of the keys, a step of each warp");
 constexpr float FEW_FLOOR = -200.f;
+
+// How rows of W are read: by elements, by 16-byte words, or, where they begin off a word, by
+// words all the same, against four copies of H that lie 0 to 3 columns on.  The copies are for
+// bf16 (50257 x 2501, 1 row 57 us, by elements 127; 2 rows 111 and 146); of fp32 numbers elements are as
+// wide as lanes need them (50257 x 1001, 4 rows 48 us, by copies 72, and by windows of two
+// words 121).
+enum Read { ELEMENTS, WORDS, SHIFTED };
+constexpr int FEW_LEAD = 4, FEW_REST = 24;  // zeros in front of a copy's row, and all that it is longer than dp
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 size_t padded(int64_t dim) { return (size_t)(dim + 7) / 8 * 8; }
@@ -42,6 +52,20 @@ __device__ __forceinline__ void stage_rows(const Few& p, float* h, int dp) {
   }
 }
 
+// Its copies: column c of copy j is at FEW_LEAD + j + c.
+template <typename T, int R>
+__device__ __forceinline__ void stage_copies(const Few& p, float* h, int dq) {
+  for (int r = 0; r < R; ++r) {
+    const T* x = static_cast<const T*>(p.H) + r * p.ldh;
+    for (int i = threadIdx.x; i < dq; i += FEW_THREADS)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = i - j - FEW_LEAD;
+        h[(j * R + r) * dq + i] = r < p.rows && c >= 0 && c < p.dim ? ld1(x + c) : 0.f;
+      }
+  }
+}
+
 __device__ __forceinline__ void widen_word(const uint4& q, f32x2 (&v)[4], const bf16*) {
   v[0] = cvt2(q.x); v[1] = cvt2(q.y); v[2] = cvt2(q.z); v[3] = cvt2(q.w);
 }
@@ -50,10 +74,22 @@ __device__ __forceinline__ void widen_word(const uint4& q, f32x2 (&v)[2], const 
   v[1] = make2(__uint_as_float(q.z), __uint_as_float(q.w));
 }
 
+// Elements k to k + 3 of a word.
+template <typename T>
+__device__ __forceinline__ void four_of(const uint4& q, int k, float (&x)[4], const T* type) {
+  f32x2 all[8 / sizeof(T)];
+  widen_word(q, all, type);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = j & 1 ? hi2(all[(k + j) / 2]) : lo2(all[(k + j) / 2]);
+}
+__device__ __forceinline__ float add_four(const float (&x)[4], const float4& y, float v) {
+  return fmaf(x[3], y.w, fmaf(x[2], y.z, fmaf(x[1], y.y, fmaf(x[0], y.x, v))));
+}
+
 // The products of FEW_AT_ONCE rows of W from v0 on with the R rows of H, summed over the warp:
 // lane l has product l * n / 32 (row of W times R plus row of H) of the n, the first of two
 // where n is 64.
-template <typename T, int R, bool kVec>
+template <typename T, int R, Read kRead>
 __device__ __forceinline__ float2 products(const Few& p, const float* h, int dp, long long v0, int lane) {
   constexpr int N = FEW_AT_ONCE * R;
   float v[N];                                   // (pairs of numbers would take twice the registers)
@@ -63,8 +99,8 @@ __device__ __forceinline__ float2 products(const Few& p, const float* h, int dp,
 #pragma unroll
   for (int i = 0; i < FEW_AT_ONCE; ++i)         // (rows behind the last are the last's; nobody looks at them)
     w[i] = static_cast<const T*>(p.W) + min(v0 + i, p.vocab - 1) * p.ldw;
-  if constexpr (kVec) {
-    constexpr int V = 16 / (int)sizeof(T);
+  constexpr int V = 16 / (int)sizeof(T);
+  if constexpr (kRead == WORDS) {
 #pragma unroll 2
     for (int c = lane * V; c < p.dim; c += 32 * V) {
       uint4 q[FEW_AT_ONCE];
@@ -74,21 +110,55 @@ __device__ __forceinline__ float2 products(const Few& p, const float* h, int dp,
       for (int k = 0; k < V; k += 4) {
         float x[FEW_AT_ONCE][4];
 #pragma unroll
-        for (int i = 0; i < FEW_AT_ONCE; ++i) {
-          f32x2 all[V / 2];
-          widen_word(q[i], all, static_cast<const T*>(nullptr));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[i][j] = j & 1 ? hi2(all[(k + j) / 2]) : lo2(all[(k + j) / 2]);
-        }
+        for (int i = 0; i < FEW_AT_ONCE; ++i) four_of(q[i], k, x[i], static_cast<const T*>(nullptr));
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float4 y = *reinterpret_cast<const float4*>(h + r * dp + c + k);
 #pragma unroll
-          for (int i = 0; i < FEW_AT_ONCE; ++i)
-            v[i * R + r] = fmaf(x[i][3], y.w, fmaf(x[i][2], y.z, fmaf(x[i][1], y.y, fmaf(x[i][0], y.x, v[i * R + r]))));
+          for (int i = 0; i < FEW_AT_ONCE; ++i) v[i * R + r] = add_four(x[i], y, v[i * R + r]);
         }
       }
     }
+  } else if constexpr (kRead == SHIFTED) {
+    const int dq = dp + FEW_REST;
+    int o[FEW_AT_ONCE];                         // elements of the row's first word before it
+    const float* y0[FEW_AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < FEW_AT_ONCE; ++i) {
+      o[i] = rows::behind(w[i]);
+      w[i] -= o[i];
+      y0[i] = h + (o[i] & 3) * R * dq + FEW_LEAD - (o[i] & ~3);
+    }
+    const auto step = [&](int c, auto kind) {
+      constexpr bool edge = decltype(kind)::value;
+      if (edge && c >= p.dim + V - 1) return;   // (the copies end there)
+      uint4 q[FEW_AT_ONCE];
+#pragma unroll
+      for (int i = 0; i < FEW_AT_ONCE; ++i)
+        q[i] = !edge || c < p.dim + o[i] ? __ldg(reinterpret_cast<const uint4*>(w[i] + c)) : make_uint4(0, 0, 0, 0);
+      if constexpr (edge) {
+#pragma unroll
+        for (int i = 0; i < FEW_AT_ONCE; ++i) q[i] = rows::masked_word<T>(q[i], o[i] - c, p.dim + o[i] - c);
+      }
+#pragma unroll
+      for (int k = 0; k < V; k += 4)
+#pragma unroll
+        for (int i = 0; i < FEW_AT_ONCE; ++i) {
+          float x[4];
+          four_of(q[i], k, x, static_cast<const T*>(nullptr));
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            v[i * R + r] = add_four(x, *reinterpret_cast<const float4*>(y0[i] + r * dq + c + k), v[i * R + r]);
+        }
+    };
+    // words that reach over the row's ends are masked: in the first step and the last ones
+    constexpr int STEP = 32 * V;
+    int c = lane * V, c0 = STEP;
+    step(c, std::true_type());
+#pragma unroll 2
+    for (; c0 + STEP <= p.dim; c0 += STEP) step(c += STEP, std::false_type());
+#pragma unroll 1
+    for (; c0 < p.dim + V - 1; c0 += STEP) step(c += STEP, std::true_type());
   } else {
     constexpr int H = 4;                        // elements in flight
     for (int c0 = lane; c0 < p.dim; c0 += 32 * H) {
@@ -127,37 +197,39 @@ __device__ __forceinline__ float2 products(const Few& p, const float* h, int dp,
   return make_float2(v[0], N > 32 ? v[1 % N] : 0.f);
 }
 
-template <typename T, int R, bool kVec>
+template <typename T, int R, Read kRead, int kBlock>
 __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
   extern __shared__ float few_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dp = p.dp;
-  float* h = few_smem;                          // [R][dp]
-  float* z = h + R * dp;                        // [R][FEW_BLOCK]
+  float* h = few_smem;                          // [R][dp], or the four copies
+  float* z = h + (kRead == SHIFTED ? 4 * R * (dp + FEW_REST) : R * dp);   // [R][kBlock]
   allow_next();
   await_previous();
-  stage_rows<T, R>(p, h, dp);
+  if constexpr (kRead == SHIFTED) stage_copies<T, R>(p, h, dp + FEW_REST);
+  else stage_rows<T, R>(p, h, dp);
   for (int blk = blockIdx.x; blk < p.parts; blk += gridDim.x) {
     __syncthreads();                            // h is staged; the last block's z are read
-    const long long b0 = (long long)blk * FEW_BLOCK;
-    for (int i = warp * FEW_AT_ONCE; i < FEW_BLOCK; i += FEW_PIECE) {
+    const long long b0 = (long long)blk * kBlock;
+    for (int i = warp * FEW_AT_ONCE; i < kBlock; i += FEW_PIECE) {
       if (b0 + i >= p.vocab) break;
-      const float2 v = products<T, R, kVec>(p, h, dp, b0 + i, lane);
+      const float2 v = products<T, R, kRead>(p, h, dp, b0 + i, lane);
       constexpr int N = FEW_AT_ONCE * R;
       if constexpr (N > 32) {
         const int at = lane * (N / 32);
-        z[(at % R) * FEW_BLOCK + i + at / R] = v.x;
-        z[((at + 1) % R) * FEW_BLOCK + i + (at + 1) / R] = v.y;
+        z[(at % R) * kBlock + i + at / R] = v.x;
+        z[((at + 1) % R) * kBlock + i + (at + 1) / R] = v.y;
       } else if (lane % (32 / N) == 0) {
         const int at = lane / (32 / N);
-        z[(at % R) * FEW_BLOCK + i + at / R] = v.x;
+        z[(at % R) * kBlock + i + at / R] = v.x;
       }
     }
     __syncthreads();
     for (int r = warp; r < p.rows; r += FEW_WARPS) {
-      float x[4], mx = -INFINITY;
+      constexpr int G = kBlock / KEY_COLS;
+      float x[G], mx = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] = b0 + 32 * j + lane < p.vocab ? z[r * FEW_BLOCK + 32 * j + lane] : -INFINITY;
+      for (int j = 0; j < G; ++j) {
+        x[j] = b0 + 32 * j + lane < p.vocab ? z[r * kBlock + 32 * j + lane] : -INFINITY;
         mx = fmaxf(mx, x[j]);
       }
 #pragma unroll
@@ -165,7 +237,7 @@ __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
       const float ref = mx == -INFINITY ? 0.f : mx;
       float s = 0.f, t = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < G; ++j) {
         const float d = x[j] - ref, e = __expf(d);
         s += e;
         t = fmaf(e, fmaxf(d, FEW_FLOOR), t);
@@ -175,7 +247,7 @@ __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
       if (lane == 0) p.stat[(size_t)r * p.parts + blk] = make_float4(mx, s, t, 0.f);
       if (p.keys) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < G; ++j) {
           const float own = __uint_as_float((__float_as_uint(fmaxf(x[j], -0x1.fffffep127f)) & ~KEY_MASK) | (KEY_MASK - lane));
           float a = own;
 #pragma unroll
@@ -183,12 +255,12 @@ __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
           float b = own == a ? -INFINITY : own;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-          if (lane == j) p.keys[((size_t)r * p.parts + blk) * 4 + j] = make_float2(a, b);
+          if (lane == j) p.keys[((size_t)r * p.parts + blk) * G + j] = make_float2(a, b);
         }
       }
       const long long at = p.labels ? p.labels[r] - b0 : -1;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < G; ++j)
         if (at == 32 * j + lane && b0 + at < p.vocab) p.zlabel[r] = x[j];
     }
   }
@@ -239,7 +311,7 @@ __global__ void __launch_bounds__(FEW_THREADS) few_backward_kernel(const Few p) 
     __syncthreads();                            // h is staged; the last piece's g are read
     const long long w0 = v0 + warp * FEW_AT_ONCE;
     if (w0 < p.vocab) {
-      const float z = products<T, R, kVec>(p, h, dp, w0, lane).x;
+      const float z = products<T, R, kVec ? WORDS : ELEMENTS>(p, h, dp, w0, lane).x;
       if (N >= 32 || lane % (32 / N) == 0) {
         const long long v = w0 + mine / R;
         const float d = z - lse;
@@ -315,6 +387,7 @@ __global__ void __launch_bounds__(256) few_join_kernel(const float* part, int ct
 
 int padded_rows(int64_t rows) { return rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 size_t forward_smem(int64_t rows, int64_t dim) { return padded_rows(rows) * (padded(dim) + FEW_BLOCK) * 4; }
+size_t copies_smem(int64_t rows, int64_t dim) { return padded_rows(rows) * (4 * (padded(dim) + FEW_REST) + FEW_BLOCK) * 4; }
 size_t backward_smem(int64_t rows, int64_t dim) { return padded_rows(rows) * padded(dim) * 8; }
 constexpr size_t FEW_SMEM = 200 * 1024;
 
@@ -330,18 +403,27 @@ cudaError_t run(K kern, Few& p, size_t smem, int64_t work, int most, int* grid, 
   count_launch();
   return launch_after(kern, dim3(*grid), dim3(FEW_THREADS), smem, s, p);
 }
-template <typename T, bool kVec>
+template <typename T, Read kRead, int kBlock>
 cudaError_t forward_of(Few& p, cudaStream_t s) {
   int grid = 0;
-  const size_t smem = forward_smem(p.rows, p.dim);
-  auto go = [&](auto kern) { return run(kern, p, smem, cdiv(p.vocab, FEW_BLOCK), 1 << 30, &grid, s); };
-  switch (padded_rows(p.rows)) {
-    case 1: return go(few_forward_kernel<T, 1, kVec>);
-    case 2: return go(few_forward_kernel<T, 2, kVec>);
-    case 4: return go(few_forward_kernel<T, 4, kVec>);
-    case 8: return go(few_forward_kernel<T, 8, kVec>);
-    default: return go(few_forward_kernel<T, 16, kVec>);
+  const size_t smem = kRead == SHIFTED ? copies_smem(p.rows, p.dim) : forward_smem(p.rows, p.dim);
+  auto go = [&](auto kern) { return run(kern, p, smem, cdiv(p.vocab, kBlock), 1 << 30, &grid, s); };
+  const int R = padded_rows(p.rows);
+  if (R == 1) return go(few_forward_kernel<T, 1, kRead, kBlock>);
+  if constexpr (sizeof(T) == 4) {
+    if (R == 4) return go(few_forward_kernel<T, 4, kRead, kBlock>);
+    if (R == 8) return go(few_forward_kernel<T, 8, kRead, kBlock>);
+    if (R == 16) return go(few_forward_kernel<T, 16, kRead, kBlock>);
   }
+  return go(few_forward_kernel<T, 2, kRead, kBlock>);
+}
+template <typename T, int kBlock>
+cudaError_t forward_by(Few& p, bool vec, cudaStream_t s) {
+  if (vec) return forward_of<T, WORDS, kBlock>(p, s);
+  if constexpr (sizeof(T) == 2) {
+    if (copies_smem(p.rows, p.dim) <= FEW_SMEM / 2) return forward_of<T, SHIFTED, kBlock>(p, s);
+  }
+  return forward_of<T, ELEMENTS, kBlock>(p, s);
 }
 template <typename T, bool kVec>
 cudaError_t backward_of(Few& p, T* dH, cudaStream_t s) {
@@ -349,10 +431,11 @@ cudaError_t backward_of(Few& p, T* dH, cudaStream_t s) {
   const int R = padded_rows(p.rows);
   const size_t smem = backward_smem(p.rows, p.dim);
   auto go = [&](auto kern) { return run(kern, p, smem, cdiv(p.vocab, FEW_PIECE), FEW_MAX_CTAS, &grid, s); };
-  const cudaError_t e = R == 1   ? go(few_backward_kernel<T, 1, kVec>)
-                        : R == 2 ? go(few_backward_kernel<T, 2, kVec>)
-                        : R == 4 ? go(few_backward_kernel<T, 4, kVec>)
-                                 : go(few_backward_kernel<T, 8, kVec>);
+  cudaError_t e;
+  if (R == 1) e = go(few_backward_kernel<T, 1, kVec>);
+  else if (R == 2) e = go(few_backward_kernel<T, 2, kVec>);
+  else if (sizeof(T) == 2 || R == 4) e = go(few_backward_kernel<T, 4, kVec>);
+  else e = go(few_backward_kernel<T, sizeof(T) == 2 ? 4 : 8, kVec>);
   if (e != cudaSuccess || !dH) return e;
   count_launch();
   return launch_after(few_join_kernel<T>, dim3(cdiv(p.dim, 32), p.rows), dim3(32, 8), 0, s, p.dh_part, grid, R, p.dp, p.dim, dH);
@@ -371,11 +454,16 @@ bool few_rows(int64_t rows, int64_t dim, bool f32, bool backward) {
 }
 size_t few_bytes(int64_t rows, int64_t dim) { return (size_t)FEW_MAX_CTAS * padded_rows(rows) * padded(dim) * 4; }
 
+// Columns of a statistic: short blocks where long ones are fewer than 1.5 an SM (microseconds, short and
+// long, fp32: 1 row of 1622 x 2240 10 and 26, of 24000 x 1536 40 and 46, of 50257 x 1536 65 and 60; 8 rows of
+// 32768 x 1536 72 and 58).
+int few_block(int64_t vocab) { return 2 * vocab < 3LL * 152 * FEW_BLOCK ? KEY_COLS : FEW_BLOCK; }
+
 cudaError_t few_forward(Few p, bool f32, bool vec, cudaStream_t s) {
   p.dp = (int)padded(p.dim);
   p.masked = 0;
-  if (f32) return vec ? forward_of<float, true>(p, s) : forward_of<float, false>(p, s);
-  return vec ? forward_of<bf16, true>(p, s) : forward_of<bf16, false>(p, s);
+  if (few_block(p.vocab) == KEY_COLS) return f32 ? forward_by<float, KEY_COLS>(p, vec, s) : forward_by<bf16, KEY_COLS>(p, vec, s);
+  return f32 ? forward_by<float, FEW_BLOCK>(p, vec, s) : forward_by<bf16, FEW_BLOCK>(p, vec, s);
 }
 cudaError_t few_backward(Few p, bool f32, bool vec, void* dH, cudaStream_t s) {
   p.dp = (int)padded(p.dim);

@@ -158,9 +158,6 @@ __global__ void __launch_bounds__(kWarp ? 32 * RMS_WARPS : RMS_MOST_THREADS) rms
 // far behind a boundary as it does in global memory; results are staged likewise, at their own
 // distance, and leave in whole words but for the ends.  (An element a thread moves 4 or 2
 // bytes where a word moves 16: LSU-bound.)
-template <typename T> __device__ __forceinline__ int behind(const T* row) {
-  return (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
-}
 // 16 bytes from `bytes` on (0 .. 15, a multiple of the element's size) of two words.
 template <typename T>
 __device__ __forceinline__ uint4 window(const uint4& lo, const uint4& hi, int bytes) {
@@ -179,15 +176,6 @@ __device__ __forceinline__ uint4 window(const uint4& lo, const uint4& hi, int by
     for (int i = 0; i < 4; ++i) b[i] = __funnelshift_r(b[i], b[i + 1], 16);
   }
   return make_uint4(b[0], b[1], b[2], b[3]);
-}
-// A word's elements outside [lo, hi) become zeros.
-template <typename T>
-__device__ __forceinline__ uint4 masked_word(uint4 q, int lo, int hi) {
-  T* x = reinterpret_cast<T*>(&q);
-#pragma unroll
-  for (int i = 0; i < 16 / (int)sizeof(T); ++i)
-    if (i < lo || i >= hi) x[i] = from_f32<T>(0.f);
-  return q;
 }
 template <typename T>
 __device__ __forceinline__ void fetch_row(T* slot, const T* row, int dim, int t, int size) {

@@ -151,6 +151,20 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
                : "memory");
 }
 
+// A row that starts off a 16-byte word: elements between the word's start and the row's.
+template <typename T> __device__ __forceinline__ int behind(const T* row) {
+  return (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
+}
+// A word's elements outside [lo, hi) become zeros.
+template <typename T>
+__device__ __forceinline__ uint4 masked_word(uint4 q, int lo, int hi) {
+  T* x = reinterpret_cast<T*>(&q);
+#pragma unroll
+  for (int i = 0; i < 16 / (int)sizeof(T); ++i)
+    if (i < lo || i >= hi) x[i] = from_f32<T>(0.f);
+  return q;
+}
+
 inline bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 inline size_t dt_size(int dt) { return dt == MUON_DTYPE_BF16 ? 2 : 4; }
 inline bool known(int dt) { return dt == MUON_DTYPE_F32 || dt == MUON_DTYPE_BF16; }

@@ -126,3 +126,23 @@ def test_past_32_bit_offsets_and_unaligned(dt):
         for p, q in zip(a[5:], b[5:]):
             assert torch.linalg.norm((p - q).float()) <= (2 * BF if dt == "bf16" else 1e-5) * torch.linalg.norm(q.float())
         del big, rows, hv, wv
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("v, d, pad, shift", [(29183, 40, 0, 0), (29184, 40, 0, 0), (38913, 24, 0, 0), (1625, 2241, 0, 0),
+                                              (33, 519, 5, 0), (700, 512, 3, 1), (31, 8, 0, 3), (40001, 17, 2, 5), (150, 1001, 0, 7), (97, 768, 1, 2)])
+def test_blocks_and_alignments(dt, v, d, pad, shift):
+    """Vocabularies around the one that is read in longer blocks, and rows of W that begin anywhere."""
+    for n in (1, 2):
+        h, h64, w, w64, tokens, tok = case(n, v, d, dt, v + d + n)
+        flat = torch.full((v * (d + pad) + shift + 8,), float("nan"), dtype=w.dtype, device=dev())
+        wv = flat[shift:shift + v * (d + pad)].view(v, d + pad)[:, :d]
+        wv.copy_(w)
+        ws = mm.linear_logprob_workspace_for(h, wv, tokens, top=32)
+        one = torch.ones(n, device=dev())
+        out = both(h, wv, tokens, ws, one, top=32)
+        check(out[:5], h64, w64, tok, 32, dt, (n, v, d, pad, shift))
+        g = ref.logprob_logit_grad(h64, w64, tok, num(out[2]), num(out[1]), np.ones(n), np.ones(n))
+        tol = 3 * BF if dt == "bf16" else 1e-5
+        for got, want in ((out[5], g @ w64), (out[6], g.T @ h64)):
+            assert np.linalg.norm(num(got) - want) <= tol * np.linalg.norm(want) + 1e-30

@@ -139,6 +139,11 @@ def test_logprob_refusals(lib):
     size = lambda a, top, b: lib.muon_linear_logprob_workspace_size(ctypes.byref(a), top, b)  # noqa: E731
     assert 0 < size(_args(), 0, 0) <= size(_args(), 8, 0) and size(_args(), 8, 0) <= size(_args(), 8, 1) < big
     assert size(_args(), -1, 0) == big and size(_args(), 33, 0) == big and size(_args(), 32, 0) < big
+    for dtype in (0, 1):                       # a workspace serves fewer rows, too
+        for vocab in (1, 700, 29183, 29184, 50000):
+            for backward in (0, 1):
+                sizes = [size(_args(rows=n, vocab=vocab, dtype=dtype), 4, backward) for n in range(40)]
+                assert sizes == sorted(sizes), (dtype, vocab, backward)
 
     def fwd(a, top=3, logp=FAKE, ent=FAKE, lse=FAKE, ids=FAKE, alt=FAKE, ws=FAKE, n=1 << 40):
         return lib.muon_linear_logprob_forward(ctypes.byref(a), top, logp, ent, lse, ids, alt, ws, n, None)
