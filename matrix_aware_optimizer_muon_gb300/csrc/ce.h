@@ -103,7 +103,7 @@ struct Few {
   float* dh_part;                // [CTA][rows, padded][dp], or null
   void* dW;
 };
-bool few_rows(int64_t rows, int64_t dim, bool f32, bool backward);   // whether it is one
+bool few_rows(int64_t rows, int64_t dim, bool f32, bool backward, bool vec);   // whether it is one; vec: W in 16-byte words
 size_t few_bytes(int64_t rows, int64_t dim);     // of dh_part
 int few_block(int64_t vocab);                    // columns of a statistic
 cudaError_t few_forward(Few p, bool f32, bool vec, cudaStream_t s);

@@ -325,17 +325,26 @@ __device__ __forceinline__ void write_lost(const LogprobRows& p, long long r) {
   if (p.labels) p.logprob[r] = not_a_number();
 }
 
-// Without alternatives: a warp a row.
+// Without alternatives: a warp a row, or all of a CTA's where the rows are fewer than the SMs.
+template <bool kWide>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) logprob_kernel(const LogprobRows p) {
+  __shared__ float4 sums[JOIN_WARPS];
   await_previous();
-  const long long r = (long long)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long r = kWide ? blockIdx.x : (long long)blockIdx.x * JOIN_WARPS + warp;
   if (r >= p.rows) return;
-  const int lane = threadIdx.x & 31;
   if (is_lost(p.status)) {
-    if (lane == 0) write_lost(p, r);
+    if (kWide ? threadIdx.x == 0 : lane == 0) write_lost(p, r);
     return;
   }
-  const Moments a = warp_moments(join_moments(p.stat + (size_t)r * p.parts, p.parts, lane, 32));
+  const float4* stat = p.stat + (size_t)r * p.parts;
+  Moments a = warp_moments(join_moments(stat, p.parts, kWide ? threadIdx.x : lane, kWide ? 32 * JOIN_WARPS : 32));
+  if (kWide) {
+    if (lane == 0) sums[warp] = make_float4(a.m, a.s, a.t, 0.f);
+    __syncthreads();
+    if (warp) return;
+    a = warp_moments(join_moments(sums, JOIN_WARPS, lane, 32));
+  }
   write_row(p, r, a, !p.labels || p.labels[r] != p.ignore, lane == 0);
 }
 
@@ -794,7 +803,8 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
   } else {
     int64_t stats = a->rows * 2;                // of a tile's columns; more where a few of the rows would have more
     for (int64_t n = 1; n <= std::min<int64_t>(a->rows, 16); ++n)
-      if (few_rows(n, a->dim, f32, false)) stats = std::max(stats, n * (TILE / few_block(a->vocab)));
+      if (few_rows(n, a->dim, f32, false, false) || few_rows(n, a->dim, f32, false, true))
+        stats = std::max(stats, n * (TILE / few_block(a->vocab)));
     P->stat = take((size_t)stats * cdiv(a->vocab, TILE) * sizeof(float4));
     P->keys = take(top ? (size_t)a->rows * (TILE / KEY_COLS) * cdiv(a->vocab, TILE) * sizeof(float2) : 0);
   }
@@ -812,8 +822,8 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
   if (top >= 0) {
     // (for more rows too, so that their workspace serves a few of them)
     for (int64_t n = 1; n <= 8; n *= 2)
-      if (few_rows(n, a->dim, f32, true)) P->total = std::max(P->total, common + up(few_bytes(n, a->dim)));
-    if (few_rows(a->rows, a->dim, f32, true)) P->few = common;
+      if (few_rows(n, a->dim, f32, true, false)) P->total = std::max(P->total, common + up(few_bytes(n, a->dim)));
+    if (few_rows(a->rows, a->dim, f32, true, false)) P->few = common;
   }
   P->g_part = (size_t)a->rows * P->piece;
   for (int i = 0; i < 2; ++i) P->g[i] = P->npieces > 1 || i == 0 ? take(P->parts * P->g_part * 2) : P->g[0];
@@ -1033,7 +1043,9 @@ int join_rows(const muon_linear_ce* a, int top, const Params& p, int parts, floa
   count_launch();
   cudaError_t e;
   if (top == 0)
-    e = launch_after(logprob_kernel, dim3((unsigned)cdiv(a->rows, JOIN_WARPS)), dim3(32 * JOIN_WARPS), 0, s, q);
+    e = a->rows <= TOP_FEW_ROWS ? launch_after(logprob_kernel<true>, dim3((unsigned)a->rows), dim3(32 * JOIN_WARPS), 0, s, q)
+                                : launch_after(logprob_kernel<false>, dim3((unsigned)cdiv(a->rows, JOIN_WARPS)),
+                                               dim3(32 * JOIN_WARPS), 0, s, q);
   else if (a->rows <= TOP_FEW_ROWS)
     e = a->dtype == MUON_DTYPE_BF16 ? launch_after(top_kernel<bf16, TOP_FEW>, dim3((unsigned)a->rows), dim3(TOP_FEW), 0, s, q)
                                     : launch_after(top_kernel<float, TOP_FEW>, dim3((unsigned)a->rows), dim3(TOP_FEW), 0, s, q);
@@ -1267,7 +1279,7 @@ extern "C" int muon_linear_logprob_forward(const muon_linear_ce* a, int top, flo
   const bool w_vec = is_aligned(a->W, 16) && a->ldw * es % 16 == 0 && a->dim * es % 16 == 0;
   Job& j = p.job[0];
   shape(&j, a->rows, a->vocab, a->dim, GROUP_FORWARD);
-  if (few_rows(a->rows, a->dim, a->dtype == MUON_DTYPE_F32, false)) {
+  if (few_rows(a->rows, a->dim, a->dtype == MUON_DTYPE_F32, false, w_vec)) {
     Few f = few_args(a, w);
     f.stat = p.stat;
     f.keys = p.keys;

@@ -1,14 +1,15 @@
 // Log probabilities of a few rows (a decoding step, a short answer to be scored), forward and
-// backward, without the tensor cores:
+// backward, without the tiles of the others:
 //   forward   z = H W^T and its statistics, W read once;
 //   backward  z again, g from it, dW = g^T H and dH = g W, W read and dW written once.
 //
-// With few rows a call is bound by W's bytes, and the tensor cores' tiles of 256
-// rows leave most of themselves empty; 32-bit operands would besides be written and read
-// again as three bf16 parts.  Here the rows of H lie in shared memory as fp32 numbers; a warp reads four rows
-// of W at a time, so that a word of H serves four products, and adds in fp32 (a lane dim/32
-// products, then a tree).  What a statistic or a key is, ce.h says: the kernels that join them
-// are those of the other path.
+// With few rows a call is bound by W's bytes, and the tiles of 256 rows leave most of
+// themselves empty; 32-bit operands would besides be written and read
+// again as three bf16 parts.  fp32 products, and those of W's rows that begin off a 16-byte word: the rows of H lie
+// in shared memory as fp32 numbers; a warp reads four rows of W at a time, so that a word of H serves four
+// products, and adds in fp32 (a lane dim/32 products, then a tree).  bf16 forward: matrix instructions
+// that take W from registers.  What a statistic or a key is, ce.h says: the kernels that
+// join them are those of the other path.
 #include <algorithm>
 #include <type_traits>
 
@@ -197,6 +198,53 @@ __device__ __forceinline__ float2 products(const Few& p, const float* h, int dp,
   return make_float2(v[0], N > 32 ? v[1 % N] : 0.f);
 }
 
+// A row's statistic of a block of logits, its keys and its token's logit, by a warp.  z: the row's
+// first of kParts shares of the logits, which lie `apart`.
+template <int kBlock, int kParts>
+__device__ __forceinline__ void write_block(const Few& p, const float* z, int apart, int r, int blk, int lane) {
+  constexpr int G = kBlock / KEY_COLS;
+  const long long b0 = (long long)blk * kBlock;
+  float x[G], mx = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    float v = z[32 * j + lane];
+#pragma unroll
+    for (int i = 1; i < kParts; ++i) v += z[i * apart + 32 * j + lane];
+    x[j] = b0 + 32 * j + lane < p.vocab ? v : -INFINITY;
+    mx = fmaxf(mx, x[j]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float s = 0.f, t = 0.f;
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const float d = x[j] - ref, e = __expf(d);
+    s += e;
+    t = fmaf(e, fmaxf(d, FEW_FLOOR), t);
+  }
+  s = warp_sum(s);
+  t = warp_sum(t);
+  if (lane == 0) p.stat[(size_t)r * p.parts + blk] = make_float4(mx, s, t, 0.f);
+  if (p.keys) {
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const float own = __uint_as_float((__float_as_uint(fmaxf(x[j], -0x1.fffffep127f)) & ~KEY_MASK) | (KEY_MASK - lane));
+      float a = own;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      float b = own == a ? -INFINITY : own;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+      if (lane == j) p.keys[((size_t)r * p.parts + blk) * G + j] = make_float2(a, b);
+    }
+  }
+  const long long at = p.labels ? p.labels[r] - b0 : -1;
+#pragma unroll
+  for (int j = 0; j < G; ++j)
+    if (at == 32 * j + lane && b0 + at < p.vocab) p.zlabel[r] = x[j];
+}
+
 template <typename T, int R, Read kRead, int kBlock>
 __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
   extern __shared__ float few_smem[];
@@ -224,45 +272,95 @@ __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
       }
     }
     __syncthreads();
-    for (int r = warp; r < p.rows; r += FEW_WARPS) {
-      constexpr int G = kBlock / KEY_COLS;
-      float x[G], mx = -INFINITY;
+    for (int r = warp; r < p.rows; r += FEW_WARPS) write_block<kBlock, 1>(p, z + r * kBlock, 0, r, blk, lane);
+  }
+}
+
+// bf16 rows of W from words, by matrix instructions: 16 rows of W are one's rows and 8 rows of H its
+// columns, so that a warp takes W from global memory straight to registers, a lane 16 bytes of each of two
+// rows, and H's word with the same columns from shared memory.  (The tensor cores' larger tiles would
+// pass W through shared memory, and be filled to 1/32 by 8 rows.)  Which column of W stands at which k of an
+// instruction does not matter as long as H's stands there too: a lane's four pairs are k
+// 2t, 2t + 1 and 2t + 8, 2t + 9 of two of them.  Sums are taken over into fp32 numbers every 128 columns.
+// Short blocks: two warps take 16 of the 32 columns each, of four quarters of the row; long
+// ones: a warp takes 16 of the 128 columns.
+__device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// A row of H is an odd multiple of 64 bytes long, so that eight lanes' words lie in different banks.
+__host__ __device__ constexpr int mma_stride(int dim) { return (dim + 31) / 32 % 2 ? (dim + 31) / 32 * 32 : (dim + 63) / 32 * 32; }
+template <int R, int kBlock>
+__global__ void __launch_bounds__(FEW_THREADS) few_mma_kernel(const Few p) {
+  extern __shared__ __align__(16) float few_smem[];
+  constexpr int S = kBlock == KEY_COLS ? 4 : 1, ZS = kBlock + 4, STEPS = 4;   // STEPS of 32 columns at a time
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / 4, t = lane % 4, ds = mma_stride(p.dim);
+  bf16* h = reinterpret_cast<bf16*>(few_smem);  // [R][ds]
+  float* z = reinterpret_cast<float*>(h + R * ds);   // [S][R][ZS]
+  allow_next();
+  await_previous();
+  for (int r = 0; r < R; ++r) {
+    const bf16* x = static_cast<const bf16*>(p.H) + r * p.ldh;
+    const bool live = r < p.rows, words = rows::behind(x) == 0;   // (the number of columns is a multiple of 8)
+    for (int c = threadIdx.x * 8; c < ds; c += FEW_THREADS * 8) {
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (live && c < p.dim) {
+        if (words) {
+          q = *reinterpret_cast<const uint4*>(x + c);
+        } else {
+          bf16* e = reinterpret_cast<bf16*>(&q);
 #pragma unroll
-      for (int j = 0; j < G; ++j) {
-        x[j] = b0 + 32 * j + lane < p.vocab ? z[r * kBlock + 32 * j + lane] : -INFINITY;
-        mx = fmaxf(mx, x[j]);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      float s = 0.f, t = 0.f;
-#pragma unroll
-      for (int j = 0; j < G; ++j) {
-        const float d = x[j] - ref, e = __expf(d);
-        s += e;
-        t = fmaf(e, fmaxf(d, FEW_FLOOR), t);
-      }
-      s = warp_sum(s);
-      t = warp_sum(t);
-      if (lane == 0) p.stat[(size_t)r * p.parts + blk] = make_float4(mx, s, t, 0.f);
-      if (p.keys) {
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-          const float own = __uint_as_float((__float_as_uint(fmaxf(x[j], -0x1.fffffep127f)) & ~KEY_MASK) | (KEY_MASK - lane));
-          float a = own;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-          float b = own == a ? -INFINITY : own;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-          if (lane == j) p.keys[((size_t)r * p.parts + blk) * G + j] = make_float2(a, b);
+          for (int i = 0; i < 8; ++i) e[i] = x[c + i];
         }
       }
-      const long long at = p.labels ? p.labels[r] - b0 : -1;
-#pragma unroll
-      for (int j = 0; j < G; ++j)
-        if (at == 32 * j + lane && b0 + at < p.vocab) p.zlabel[r] = x[j];
+      *reinterpret_cast<uint4*>(h + r * ds + c) = q;
     }
+  }
+  const int group = S == 4 ? warp % 2 : warp, part = S == 4 ? warp / 2 : 0;
+  const int chunks = (p.dim + 31) / 32, lo = chunks * part / S, hi = chunks * (part + 1) / S;
+  const bf16* y = h + g * ds + t * 8;
+  for (int blk = blockIdx.x; blk < p.parts; blk += gridDim.x) {
+    __syncthreads();                            // h is staged; the last block's z are read
+    const long long v0 = (long long)blk * kBlock + group * 16;
+    if (v0 < p.vocab) {
+      // (rows behind the last are the last's; nobody looks at them)
+      const bf16* w0 = static_cast<const bf16*>(p.W) + min(v0 + g, p.vocab - 1) * p.ldw + t * 8;
+      const bf16* w1 = static_cast<const bf16*>(p.W) + min(v0 + g + 8, p.vocab - 1) * p.ldw + t * 8;
+      float sum[R / 8][4] = {};
+      for (int k = lo; k < hi; k += STEPS) {
+        uint4 a[STEPS], b[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const bool in = k + i < hi && (k + i) * 32 + t * 8 < p.dim;
+          a[i] = in ? __ldg(reinterpret_cast<const uint4*>(w0 + (k + i) * 32)) : make_uint4(0, 0, 0, 0);
+          b[i] = in ? __ldg(reinterpret_cast<const uint4*>(w1 + (k + i) * 32)) : make_uint4(0, 0, 0, 0);
+        }
+        float d[R / 8][4] = {};
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          if (k + i >= hi) break;
+#pragma unroll
+          for (int n = 0; n < R / 8; ++n) {
+            const uint4 c = *reinterpret_cast<const uint4*>(y + n * 8 * ds + (k + i) * 32);
+            mma_16x8(d[n], a[i].x, b[i].x, a[i].y, b[i].y, c.x, c.y);
+            mma_16x8(d[n], a[i].z, b[i].z, a[i].w, b[i].w, c.z, c.w);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < R / 8; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[n][i] += d[n][i];
+      }
+#pragma unroll
+      for (int n = 0; n < R / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          z[(part * R + n * 8 + 2 * t + i % 2) * ZS + group * 16 + g + i / 2 * 8] = sum[n][i];
+    }
+    __syncthreads();
+    for (int r = warp; r < p.rows; r += FEW_WARPS) write_block<kBlock, S>(p, z + r * ZS, R * ZS, r, blk, lane);
   }
 }
 
@@ -386,10 +484,14 @@ __global__ void __launch_bounds__(256) few_join_kernel(const float* part, int ct
 }
 
 int padded_rows(int64_t rows) { return rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+int mma_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
 size_t forward_smem(int64_t rows, int64_t dim) { return padded_rows(rows) * (padded(dim) + FEW_BLOCK) * 4; }
+size_t mma_smem(int64_t rows, int64_t dim) {
+  return mma_rows(rows) * ((size_t)mma_stride((int)dim) * 2 + std::max<size_t>(4 * (KEY_COLS + 4), FEW_BLOCK + 4) * 4);
+}
 size_t copies_smem(int64_t rows, int64_t dim) { return padded_rows(rows) * (4 * (padded(dim) + FEW_REST) + FEW_BLOCK) * 4; }
 size_t backward_smem(int64_t rows, int64_t dim) { return padded_rows(rows) * padded(dim) * 8; }
-constexpr size_t FEW_SMEM = 200 * 1024;
+constexpr size_t FEW_SMEM = 200 * 1024, MMA_SMEM = 60 * 1024;
 
 template <class K>
 cudaError_t run(K kern, Few& p, size_t smem, int64_t work, int most, int* grid, cudaStream_t s) {
@@ -419,8 +521,15 @@ cudaError_t forward_of(Few& p, cudaStream_t s) {
 }
 template <typename T, int kBlock>
 cudaError_t forward_by(Few& p, bool vec, cudaStream_t s) {
-  if (vec) return forward_of<T, WORDS, kBlock>(p, s);
-  if constexpr (sizeof(T) == 2) {
+  if constexpr (sizeof(T) == 4) {
+    if (vec) return forward_of<T, WORDS, kBlock>(p, s);
+  } else {
+    if (vec) {
+      int grid = 0;
+      const int R = mma_rows(p.rows);
+      auto go = [&](auto kern) { return run(kern, p, mma_smem(p.rows, p.dim), cdiv(p.vocab, kBlock), 1 << 30, &grid, s); };
+      return R == 8 ? go(few_mma_kernel<8, kBlock>) : go(few_mma_kernel<16, kBlock>);
+    }
     if (copies_smem(p.rows, p.dim) <= FEW_SMEM / 2) return forward_of<T, SHIFTED, kBlock>(p, s);
   }
   return forward_of<T, ELEMENTS, kBlock>(p, s);
@@ -445,19 +554,22 @@ cudaError_t backward_of(Few& p, T* dH, cudaStream_t s) {
 
 // Up to how many rows this is the faster way (microseconds here and by tiles, 32768 x 1536):
 // fp32 forward 16 rows 98 and 203, 8 rows 58 and 199, backward 4 rows 116 and 431, 8 rows 145 and
-// 422; bf16 forward 1 row 25 and 35, 2 rows 28 and 35, 4 rows 31 and 31, backward 1 row 66 and 98,
-// 4 rows 74 and 99, 8 rows 118 and 98.
-bool few_rows(int64_t rows, int64_t dim, bool f32, bool backward) {
-  const int most = backward ? (f32 ? 8 : 4) : (f32 ? 16 : 2);
-  return rows >= 1 && rows <= most && dim < (1 << 20) &&
-         (backward ? backward_smem(rows, dim) : forward_smem(rows, dim)) <= FEW_SMEM;
+// 422; bf16 backward 1 row 66 and 98, 4 rows 74 and 99, 8 rows 118 and 98; bf16 forward in words 8 rows 21 and
+// 29, with 8 alternatives 28 and 45, 16 rows 29 and 29, 35 and 47, 24 rows 51 and 30; of 131072 x 2560 8 rows 126 and
+// 128.  Longer rows leave an SM fewer warps (32768 x 4096, 8 rows 74 and 61): tiles.
+// bf16 rows off the words: 1 row of 50257 x 2501 57 and 150, 4 rows have no kernel here.
+bool few_rows(int64_t rows, int64_t dim, bool f32, bool backward, bool vec) {
+  if (rows < 1 || dim >= (1 << 20)) return false;
+  if (backward) return rows <= (f32 ? 8 : 4) && backward_smem(rows, dim) <= FEW_SMEM;
+  if (!f32 && vec) return rows <= 16 && mma_smem(rows, dim) <= MMA_SMEM;
+  return rows <= (f32 ? 16 : 2) && forward_smem(rows, dim) <= FEW_SMEM;
 }
 size_t few_bytes(int64_t rows, int64_t dim) { return (size_t)FEW_MAX_CTAS * padded_rows(rows) * padded(dim) * 4; }
 
-// Columns of a statistic: short blocks where long ones are fewer than 1.5 an SM (microseconds, short and
-// long, fp32: 1 row of 1622 x 2240 10 and 26, of 24000 x 1536 40 and 46, of 50257 x 1536 65 and 60; 8 rows of
-// 32768 x 1536 72 and 58).
-int few_block(int64_t vocab) { return 2 * vocab < 3LL * 152 * FEW_BLOCK ? KEY_COLS : FEW_BLOCK; }
+// Columns of a statistic: short blocks where long ones are fewer than two an SM (microseconds, short and
+// long: fp32 1 row of 1622 x 2240 10 and 26, of 32768 x 1536 43 and 49, of 50257 x 1536 62 and 58; bf16 8 rows of
+// 32768 x 1536 21 and 23, of 131072 x 512 36 and 33).
+int few_block(int64_t vocab) { return vocab < 2LL * 152 * FEW_BLOCK ? KEY_COLS : FEW_BLOCK; }
 
 cudaError_t few_forward(Few p, bool f32, bool vec, cudaStream_t s) {
   p.dp = (int)padded(p.dim);

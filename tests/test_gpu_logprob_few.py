@@ -129,7 +129,7 @@ def test_past_32_bit_offsets_and_unaligned(dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("v, d, pad, shift", [(29183, 40, 0, 0), (29184, 40, 0, 0), (38913, 24, 0, 0), (1625, 2241, 0, 0),
+@pytest.mark.parametrize("v, d, pad, shift", [(38911, 40, 0, 0), (38912, 40, 0, 0), (38913, 24, 0, 0), (1625, 2241, 0, 0),
                                               (33, 519, 5, 0), (700, 512, 3, 1), (31, 8, 0, 3), (40001, 17, 2, 5), (150, 1001, 0, 7), (97, 768, 1, 2)])
 def test_blocks_and_alignments(dt, v, d, pad, shift):
     """Vocabularies around the one that is read in longer blocks, and rows of W that begin anywhere."""
@@ -146,3 +146,21 @@ def test_blocks_and_alignments(dt, v, d, pad, shift):
         tol = 3 * BF if dt == "bf16" else 1e-5
         for got, want in ((out[5], g @ w64), (out[6], g.T @ h64)):
             assert np.linalg.norm(num(got) - want) <= tol * np.linalg.norm(want) + 1e-30
+
+
+@pytest.mark.parametrize("v, d, pad", [(300, 8, 0), (38911, 40, 8), (38912, 96, 0), (1625, 1000, 0), (17, 520, 16), (128, 2048, 0),
+                                       (31000, 136, 24), (500, 3520, 0), (500, 3560, 8)])
+@pytest.mark.parametrize("n", [1, 3, 8, 9, 16, 17, 31, 32, 33])
+def test_words_of_few_rows(n, v, d, pad):
+    """Rows of W in whole words, as matrix instructions take them: all numbers of rows, a row's ends
+    inside a step; H in words and off them."""
+    h, h64, w, w64, tokens, tok = case(n, v, d, "bf16", v + d + n)
+    wide = torch.full((v, d + pad), float("nan"), dtype=w.dtype, device=dev())
+    wide[:, :d] = w
+    odd = torch.full((n, d + 3), float("nan"), dtype=h.dtype, device=dev())
+    odd[:, :d] = h
+    for hv in (h, odd[:, :d]):
+        ws = mm.linear_logprob_workspace_for(hv, wide[:, :d], tokens, top=32)
+        out = mm.muon_linear_logprob_forward(hv, wide[:, :d], tokens, ws, top=32)
+        check(out, h64, w64, tok, 32, "bf16", (n, v, d, pad))
+        assert mm.muon_check_status(ws) == mm.MUON_OK

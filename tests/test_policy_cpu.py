@@ -140,7 +140,7 @@ def test_logprob_refusals(lib):
     assert 0 < size(_args(), 0, 0) <= size(_args(), 8, 0) and size(_args(), 8, 0) <= size(_args(), 8, 1) < big
     assert size(_args(), -1, 0) == big and size(_args(), 33, 0) == big and size(_args(), 32, 0) < big
     for dtype in (0, 1):                       # a workspace serves fewer rows, too
-        for vocab in (1, 700, 29183, 29184, 50000):
+        for vocab in (1, 700, 38911, 38912, 50000):
             for backward in (0, 1):
                 sizes = [size(_args(rows=n, vocab=vocab, dtype=dtype), 4, backward) for n in range(40)]
                 assert sizes == sorted(sizes), (dtype, vocab, backward)
