@@ -164,3 +164,50 @@ def test_words_of_few_rows(n, v, d, pad):
         out = mm.muon_linear_logprob_forward(hv, wide[:, :d], tokens, ws, top=32)
         check(out, h64, w64, tok, 32, "bf16", (n, v, d, pad))
         assert mm.muon_check_status(ws) == mm.MUON_OK
+
+
+@pytest.mark.parametrize("v", [1000, 40000])
+@pytest.mark.parametrize("n", [5, 16])
+def test_words_with_numbers_that_are_none(n, v):
+    """A NaN in a row of H is that row's alone; a row of W that the logits mask with minus infinity has
+    probability 0; the first call of a size may be a captured one; two streams at once give one's bits."""
+    d = 136
+    h, h64, w, w64, tokens, tok = case(n, v, d, "bf16", n + v)
+    h, h64 = h.abs(), np.abs(h64)                 # so that a row of W of minus infinity makes a logit of it
+    h[:, -1], h64[:, -1] = 1, 1
+    gone = np.array([0, 31, v // 2, v - 1])
+    w[torch.from_numpy(gone).to(dev())], w64[gone] = float("-inf"), -1e30
+    tok[np.isin(tok, gone)] = 1
+    tok[1] = 2
+    tokens.copy_(torch.from_numpy(tok))
+    h = h.clamp(min=2.0 ** -20)
+    h64 = num(h)
+    spaces = [mm.alloc_linear_logprob_workspace(n, v, d, top=6) for _ in range(2)]
+    torch.cuda.synchronize()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        held = mm.muon_linear_logprob_forward(h, w, tokens, spaces[0], top=6)
+    graph.replay()
+    torch.cuda.synchronize()
+    keep = np.ones(v, bool)
+    keep[gone] = False
+    back = np.flatnonzero(keep)
+    small = np.where(tok >= 0, np.searchsorted(back, np.maximum(tok, 0)), tok)
+    rlogp, rent, rlse, rids, ralt = ref.logprobs(h64, w64[keep], small, 6)
+    ids = held[3].cpu().numpy()
+    assert not np.isin(ids, gone).any()
+    ids = np.where(ids < 0, ids, np.searchsorted(back, ids))     # an ignored row has none
+    check(held[:3] + (torch.from_numpy(ids).to(dev()), held[4]), h64, w64[keep], small, 6, "bf16", (n, v, "masked"))
+    s.wait_stream(torch.cuda.current_stream())
+    one = mm.muon_linear_logprob_forward(h, w, tokens, spaces[0], top=6)
+    two = mm.muon_linear_logprob_forward(h, w, tokens, spaces[1], top=6, stream=s)
+    torch.cuda.synchronize()
+    assert same(one, held) and same(two, held)
+    bad = h.clone()
+    bad[0, 3] = float("nan")
+    out = mm.muon_linear_logprob_forward(bad, w, tokens, spaces[0], top=6)
+    assert same([x[1:] for x in out], [x[1:] for x in held])
+    assert tok[0] == -100 or bool(torch.isnan(out[0][0]) and torch.isnan(out[1][0]))
+    assert bool(torch.isnan(out[2][0]))
+    for ws in spaces:
+        assert mm.muon_check_status(ws) == mm.MUON_OK
