@@ -375,13 +375,15 @@ __device__ __forceinline__ void add_exact(float& s, float& e, float p) {
   e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(p, b)));
   s = t;
 }
-// s + e over the warp, in every lane (64-bit additions would hold the warps up).
+// s + e over the warp, in every lane (64-bit additions would hold the warps up): the same
+// number in each, for a lane and its partner round the same sums.  (What the addition of s and so
+// drops is a number of its own; e + eo comes first, which does not depend on whose is whose.)
 __device__ __forceinline__ double warp_exact(float s, float e) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float so = __shfl_xor_sync(0xffffffffu, s, o), eo = __shfl_xor_sync(0xffffffffu, e, o);
-    add_exact(s, e, so);
     e = __fadd_rn(e, eo);
+    add_exact(s, e, so);
   }
   return (double)s + (double)e;
 }
