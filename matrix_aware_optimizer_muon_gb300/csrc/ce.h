@@ -24,10 +24,16 @@ enum Kind : int {
   POLICY = 5    // GRAD of log probabilities and entropies
 };
 
-// The two largest logits of 32 columns as keys: the number's lowest 5 bits hold
-// 31 minus the column, so that two maxima a logit find them without carrying an index.
+// The two largest of 32 columns as keys: the number's lowest 5 bits hold 31 minus the
+// column, so that two maxima a logit find them without carrying an index.  The numbers are
+// upper bounds on the exact logits: a first sum is off by a share of |h||w| (the rows'
+// lengths), however small the sum itself is, and that share is added before the key is made.
 constexpr int KEY_COLS = 32;
 constexpr unsigned KEY_MASK = KEY_COLS - 1;
+// The share: a unit for each rounding that a product can pass on its way into the sum (fp32
+// additions 2^-24 each; a step of the tensor cores, which truncate, measured 2^-24 for 16 products of one
+// sign and allowed four times that), and a fiftieth for the lengths' own sums.
+constexpr float UNIT_FP32 = 0x1.05p-24f, UNIT_TENSOR = 0x1.05p-22f;
 
 // One product of a launch: out[m, n] = sum_k A[m, k] B[n, k].  A K-major operand's map
 // covers (k, row), an MN-major one's (row, k), in boxes of 64 x 64.  The maps' third
@@ -68,6 +74,9 @@ struct Params {
   float scale;
   float4* stat;                  // LOGPROB: [row][2 * ntiles] max m, sum of e^(z-m), sum of e^(z-m) (z-m)
   float2* keys;                  // LOGPROB: [row][8 * ntiles], or null
+  // with keys: [row] share of |h|, [column] length of a row of W, [32 columns] the largest, or -1 where
+  // their lengths differ (a whole tile's, with some finite length behind the vocabulary)
+  const float *hshare, *wlen, *wgroup;
   const float *entropy, *g_logprob, *g_entropy;   // POLICY
   unsigned int* status;
   unsigned long long timeout_ns;
@@ -98,6 +107,7 @@ struct Few {
   float2* keys;
   float* zlabel;
   int parts;                     // statistics a row
+  float share;                   // with keys: what a logit may be off by, over |h||w|
   // backward
   const float *lse, *entropy, *g_logprob, *g_entropy;
   float* dh_part;                // [CTA][rows, padded][dp], or null
@@ -110,6 +120,14 @@ cudaError_t few_forward(Few p, bool f32, bool vec, cudaStream_t s);
 cudaError_t few_backward(Few p, bool f32, bool vec, void* dH, cudaStream_t s);
 
 #ifdef __CUDACC__
+// A row's length from the sum of its squares, between 2^-60 and 2^63: what fp32's squares lose
+// below is too much of a bound and never too little; longer rows are masks (a product of two
+// such lengths stays away from a masked logit's 2^120).
+__device__ __forceinline__ float length_of(float squares) { return sqrtf(fminf(fmaxf(squares, 0x1p-120f), 0x1p126f)); }
+// The share of a row of H; none for a row of zeros, whose logits are exact.
+__device__ __forceinline__ float share_of(float squares, float largest, float share) {
+  return largest == 0.f ? 0.f : fminf(share * length_of(squares), 0x1p50f);
+}
 // The factor that all rows share.
 __device__ __forceinline__ float shared_factor(float scale, const float* upstream, const float* stats) {
   if (upstream) scale *= *upstream;

@@ -393,8 +393,35 @@ struct RowStats {
   float2 two[CHUNKS];
   float z;
 };
-// Column `at` is the token's; columns from `cols` on are masked like any other.
-__device__ __forceinline__ void take_columns(RowStats& x, int k, float (&v)[32], int cols, int at, bool keys) {
+__device__ __forceinline__ void prefetch(const float* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+// Logits to upper bounds: what they may be off by, added.
+__device__ __forceinline__ void raise(float (&v)[32], const float* wlen, float share) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    const float4 w = *reinterpret_cast<const float4*>(wlen + j);
+    v[j] = fmaf(share, w.x, v[j]);
+    v[j + 1] = fmaf(share, w.y, v[j + 1]);
+    v[j + 2] = fmaf(share, w.z, v[j + 2]);
+    v[j + 3] = fmaf(share, w.w, v[j + 3]);
+  }
+}
+// The two keys of 32 columns.  group: the largest length of their rows of W, by which both are
+// raised with their columns' bits kept; or -1, and every column is raised by its own.
+__device__ __forceinline__ float2 raised_keys(float (&v)[32], const float* wlen, float group, float share) {
+  if (group < 0.f) {
+    raise(v, wlen, share);
+    return largest_two(v);
+  }
+  const float2 two = largest_two(v);
+  auto up = [&](float key) {
+    return __uint_as_float((__float_as_uint(fmaf(share, group, key)) & ~KEY_MASK) | (__float_as_uint(key) & KEY_MASK));
+  };
+  return make_float2(up(two.x), up(two.y));
+}
+// Column `at` is the token's; columns from `cols` on are masked like any other.  wlen, group, share: where
+// keys are asked for.
+__device__ __forceinline__ void take_columns(RowStats& x, int k, float (&v)[32], int cols, int at, const float* wlen,
+                                             float group, float share) {
   if (cols < 32) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -440,13 +467,13 @@ __device__ __forceinline__ void take_columns(RowStats& x, int k, float (&v)[32],
     for (int j = 0; j < 32; ++j)
       if (j == at) x.z = v[j];
   }
-  if (keys) {
+  if (wlen) {
     // a key of minus infinity would be a NaN, which a minimum passes over too
     if (masked) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = fmaxf(v[j], -0x1.fffffep127f);
     }
-    x.two[k] = largest_two(v);
+    x.two[k] = raised_keys(v, wlen, group, share);
   }
   // (what is known of these columns is computed before the next are loaded)
   asm volatile("" : "+f"(x.m[k]), "+f"(x.s[k]), "+f"(x.t[k]), "+f"(x.two[k].x), "+f"(x.two[k].y));
@@ -535,16 +562,19 @@ __device__ __forceinline__ void finish_logprob(const Params& p, const Work& J, c
     p.zlabel[r] = z;
   }
   if (p.keys) {
-    // a key of minus infinity would be a NaN, which a minimum passes over too
-    if (masked) {
-#pragma unroll
-      for (int k = 0; k < CHUNKS; ++k)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) acc[k][j] = fmaxf(acc[k][j], -0x1.fffffep127f);
-    }
+    const float share = p.hshare[r];
+    const float4 group = *reinterpret_cast<const float4*>(p.wgroup + cbase / KEY_COLS);
     float2 two[CHUNKS];
 #pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) two[k] = largest_two(acc[k]);
+    for (int k = 0; k < CHUNKS; ++k) {
+      // a key of minus infinity would be a NaN, which a minimum passes over too
+      if (masked) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[k][j] = fmaxf(acc[k][j], -0x1.fffffep127f);
+      }
+      two[k] = raised_keys(acc[k], p.wlen + cbase + 32 * k, k == 0 ? group.x : k == 1 ? group.y : k == 2 ? group.z : group.w, share);
+      asm volatile("" : "+f"(two[k].x), "+f"(two[k].y)::"memory");   // (the next lengths are loaded then)
+    }
     float4* o = reinterpret_cast<float4*>(p.keys + at128 * CHUNKS);
 #pragma unroll
     for (int k = 0; k < CHUNKS; k += 2) o[k / 2] = make_float4(two[k].x, two[k].y, two[k + 1].x, two[k + 1].y);
@@ -723,6 +753,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
       const int nseg = kPromote ? segments(J, p.nterms) : 1;
       RowStats stats = {};                      // (a LOGPROB tile of one segment)
       int token = -1;                           // the token's column among this thread's 128
+      // what the keys need, asked for before the product is there
+      float share = 0.f;
+      float4 group = make_float4(0.f, 0.f, 0.f, 0.f);
+      if constexpr (kLogprob && !kPromote) {
+        if (J.kind == LOGPROB && p.keys) {
+          if (r < J.m) share = p.hshare[r];
+          group = *reinterpret_cast<const float4*>(p.wgroup + cbase / KEY_COLS);
+        }
+      } else if constexpr (kLogprob) {          // (no register is free for them)
+        if (J.kind == LOGPROB && p.keys && r < J.m) {
+          prefetch(p.hshare + r);
+          prefetch(p.wgroup + cbase / KEY_COLS);
+        }
+      }
       if constexpr (kLogprob && !kPromote) {
         if (J.kind == LOGPROB && p.labels && r < J.m) {
           const long long at = p.labels[r] - cbase;
@@ -747,7 +791,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_kerne
             ptx::tmem_ld_32x32b_x32(tb + k * 32, v);
             if constexpr (kLogprob) {
               if (J.kind == LOGPROB) {
-                take_columns(stats, k, v, J.n - cbase - 32 * k, token - 32 * k, p.keys != nullptr);
+                take_columns(stats, k, v, J.n - cbase - 32 * k, token - 32 * k, p.keys ? p.wlen + cbase + 32 * k : nullptr,
+                             k == 0 ? group.x : k == 1 ? group.y : k == 2 ? group.z : group.w, share);
                 continue;
               }
             }

@@ -141,6 +141,92 @@ __global__ void __launch_bounds__(256) mask_kernel(const bf16* in, long long ld,
   }
 }
 
+// What the keys of the log probabilities' tiles need of the operands: the lengths of W's rows, by
+// column and the largest of each KEY_COLS (minus one where one is four times as long as another: these are
+// told apart, for a few long rows would raise their neighbours' bounds too), and the shares of H's
+// rows.  A CTA has KEY_COLS rows, a warp four.  W is read once more for them, at 5 to 6 TB/s, from its end
+// on: the product starts with what was read last.
+struct Lengths {
+  const void *h, *w;
+  long long ldh, ldw, rows, vocab;
+  int dim, hvec, wvec, groups;       // vec: rows in 16-byte words
+  float share;
+  float *hshare, *wlen, *wgroup;
+};
+template <typename T>
+__global__ void __launch_bounds__(256) lengths_kernel(const Lengths p) {
+  constexpr int V = 16 / (int)sizeof(T), N = 4, HELD = 2;
+  __shared__ float all[KEY_COLS];
+  allow_next();
+  await_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool is_h = (int)blockIdx.x >= p.groups;
+  const long long block = is_h ? (long long)blockIdx.x - p.groups : p.groups - 1 - (long long)blockIdx.x;
+  const long long rows = is_h ? p.rows : p.vocab, r0 = block * KEY_COLS + warp * N;
+  const T* x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)        // (rows behind the last are the last's)
+    x[i] = static_cast<const T*>(is_h ? p.h : p.w) + min(r0 + i, rows - 1) * (is_h ? p.ldh : p.ldw);
+  f32x2 s[N];
+  float most[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    s[i] = both(0.f);
+    most[i] = 0.f;
+  }
+  auto take = [&](int i, float a, float b) {
+    s[i] = fma2(make2(a, b), make2(a, b), s[i]);
+    if (is_h) most[i] = fmaxf(most[i], fmaxf(fabsf(a), fabsf(b)));
+  };
+  const int dim = r0 < rows ? p.dim : 0, words = (is_h ? p.hvec : p.wvec) ? dim / V : 0;
+  for (int c0 = lane; c0 < words; c0 += 32 * HELD) {
+    uint4 q[N][HELD];
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        q[i][k] = c0 + 32 * k < words ? reinterpret_cast<const uint4*>(x[i])[c0 + 32 * k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t w[4] = {q[i][k].x, q[i][k].y, q[i][k].z, q[i][k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (sizeof(T) == 2) take(i, __uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+          else if (j % 2 == 0) take(i, __uint_as_float(w[j]), __uint_as_float(w[(j + 1) % 4]));
+        }
+      }
+  }
+  for (int c = words * V + lane; c < dim; c += 32)
+#pragma unroll
+    for (int i = 0; i < N; ++i) take(i, ld1(x[i] + c), 0.f);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float sum = warp_sum(lo2(s[i]) + hi2(s[i]));
+    if (is_h) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) most[i] = fmaxf(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
+      if (lane == 0 && r0 + i < rows) p.hshare[r0 + i] = share_of(sum, most[i], p.share);
+    } else if (lane == 0) {
+      all[warp * N + i] = length_of(sum);
+    }
+  }
+  if (is_h) return;
+  __syncthreads();
+  if (warp) return;
+  const long long v = block * KEY_COLS + lane;
+  const float len = all[lane];
+  float hi = len, lo = len;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+  }
+  p.wlen[v] = len;
+  if (lane == 0) p.wgroup[block] = hi > 4.f * lo ? -1.f : hi;
+}
+
 // Whether a wait of this call's products (or of an earlier call that nobody asked about) ran
 // out: what they left unwritten must not pass for a result, so the last kernel of a call
 // writes NaN instead.  A caller without a workspace to ask sees it too.
@@ -348,24 +434,28 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) logprob_kernel(const LogprobR
   write_row(p, r, a, !p.labels || p.labels[r] != p.ignore, lane == 0);
 }
 
-// With alternatives: a CTA a row.  The tensor cores' logits are off by some 1e-6 of their
-// partial sums, which is enough to swap neighbours, so they only choose candidates, and the
-// candidates' logits are summed again, to 2^-45 of their largest partial sum:
-//   1. a bound from below on the top-th largest logit: the top-th of the threads' largest keys
-//      (two each where there are few), by merging the warps' lists in order;
+// With alternatives: a CTA a row.  The products' logits are off by some 1e-6 of their
+// partial sums, which is enough to swap neighbours (and where large terms cancel, ones far apart), so
+// they only choose candidates, and the candidates' logits are summed again, to 2^-45 of their
+// largest partial sum.  The keys are upper bounds on the exact logits (ce.h):
+//   1. the top-th largest of the threads' largest keys (two each where there are few), by merging
+//      the warps' lists in order;
 //   2. candidates: columns whose key is not below that by more than MARGIN of the largest
-//      logit, hundreds of times what the logits are off by; of 32 columns whose two keys both
-//      qualify, all (a third may hide behind them);
-//   3. their logits again, a warp each; 4. their ranks, ties to the lower index.
-// Where ties or a margin full of neighbours make more candidates than fit, the row's groups of
-// 32 columns are walked in order instead, against the top-th best so far.
+//      logit; of 32 columns whose two keys both qualify, all (a third may hide behind them);
+//   3. their logits again, a warp each; 4. their ranks, ties to the lower index;
+//   5. if the top-th best of them is not below what was the least key of a candidate, nothing else
+//      can be among the best.  (MARGIN lets keys of up to some 10000 columns pass.)
+// Where it is, and where ties or bounds full of neighbours make more candidates than fit, the row's
+// groups of 32 columns are walked in order instead, against the top-th best so far.
 // Many rows: 128 threads, so that many rows are at hand (4096 x 32000 with 8 alternatives, by 64,
 // 128 and 256 threads: 255, 237 and 349 us).  Few rows, whose every wait shows: 512, a
 // candidate a warp and a row's words asked for at once.
 constexpr int TOP_MANY = 128, TOP_FEW = 512, TOP_FEW_ROWS = 152;
 constexpr int TOP_CANDIDATES = 512;
 constexpr int TOP_WHOLE = 14;                // groups taken whole
-constexpr float TOP_MARGIN = 0x1p-12f;
+constexpr float TOP_MARGIN = 0x1p-10f;
+// A bound may be above its key by this share of it (twice 31 ulp of the column's bits, a rounding).
+constexpr float KEY_SHARE = 0x1p-16f, KEY_LEAST = 1e-30f;
 constexpr float MASKED = -0x1p120f;          // logits down here are masks, of the type's lowest value or less
 static_assert(TOP_WHOLE * KEY_COLS + MUON_LOGPROB_MAX_TOP <= TOP_CANDIDATES, "");
 
@@ -616,8 +706,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 8) top_ker
     if (lane == top - 1 && best > MASKED) sh.bound = best;
   }
   __syncthreads();
-  const float bound = sh.bound, margin = TOP_MARGIN * fmaxf(fabsf(all.m), bound == -INFINITY ? 0.f : fabsf(bound)) + 1e-30f;
-  const float least = bound - margin;
+  const float bound = sh.bound;
+  float least = bound - (TOP_MARGIN * fmaxf(fabsf(all.m), bound == -INFINITY ? 0.f : fabsf(bound)) + KEY_LEAST);
+  const T* h = static_cast<const T*>(p.H) + r * p.ldh;
   // 2. candidates
   auto choose = [&](float a, float b, int g) {
     if (!(a >= least && a > MASKED)) return;
@@ -643,9 +734,19 @@ __global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 8) top_ker
     }
   }
   __syncthreads();
-  const T* h = static_cast<const T*>(p.H) + r * p.ldh;
+  // 5. what no key below `least` can reach, and the least key that can reach the top-th best
+  auto enough = [&] {
+    return least == -INFINITY || (sh.kept_id[top - 1] >= 0 && sh.kept_value[top - 1] >= place_of((double)least + (KEY_SHARE * fabsf(least) + KEY_LEAST)));
+  };
+  auto lower = [&] {
+    if (sh.kept_id[top - 1] < 0) return -INFINITY;
+    const float v = __double2float_rd(at_place(sh.kept_value[top - 1]));
+    return __fsub_rd(v, __fmaf_ru(KEY_SHARE, fabsf(v), KEY_LEAST));
+  };
   const int singles = sh.count, wholes = sh.wholes;
-  if (wholes <= TOP_WHOLE && singles + wholes * KEY_COLS <= TOP_CANDIDATES) {
+  const bool fits = wholes <= TOP_WHOLE && singles + wholes * KEY_COLS <= TOP_CANDIDATES;
+  int walks = 2;                 // the first with `least` as it is, where the candidates do not fit
+  if (fits) {
     const int n = singles + wholes * KEY_COLS;
     for (int i = singles + t; i < n; i += TOP_THREADS) {
       const int c = sh.whole[(i - singles) / KEY_COLS] * KEY_COLS + (i - singles) % KEY_COLS;
@@ -655,6 +756,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 8) top_ker
     // 3.
     evaluate(sh, n, p, h);
     rank(sh, n, top);
+    walks = 0;
+    if (!enough()) {
+      least = lower();
+      walks = 1;
+    }
   } else {
     // a row of zeros (padding): every logit is 0
     bool zero = true;
@@ -666,13 +772,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 8) top_ker
       }
       return;
     }
-    // every group against the best so far, KEY_COLS columns at a time
+  }
+  // every group against the best so far, KEY_COLS columns at a time
+  for (; walks > 0; --walks) {
     int kept = 0;
     double worst = -INFINITY;      // of the kept, when there are `top`
     __syncthreads();
     for (int g = 0; g < groups; ++g) {
       const float k = keys[g].x;   // (the same for every thread)
-      if (!(k >= least && k > MASKED) || (double)k + margin < worst) continue;
+      if (!(k >= least && k > MASKED) || (double)k + (KEY_SHARE * fabsf(k) + KEY_LEAST) < worst) continue;
       const long long c = (long long)g * KEY_COLS + t;
       if (t < KEY_COLS) sh.id[t] = c < p.vocab ? (int)c : -1;
       if (t < kept) {
@@ -687,6 +795,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 8) top_ker
       if (kept == top) worst = at_place(sh.kept_value[top - 1]);
       __syncthreads();
     }
+    if (walks == 1 || enough()) break;
+    least = lower();
   }
   for (int i = t; i < top; i += TOP_THREADS) {
     const int id = sh.kept_id[i];
@@ -737,7 +847,7 @@ struct CePlan {
   bool pack_h, pack_w;
   size_t hp, wp;               // packed copies
   size_t zlabel, part, sums;   // forward
-  size_t stat, keys;           // forward of the log probabilities
+  size_t stat, keys, hshare, wlen;   // forward of the log probabilities
   size_t few;                  // their backward pass with few rows
   int64_t piece, npieces;
   int splits;
@@ -809,6 +919,8 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
         stats = std::max(stats, n * (TILE / few_block(a->vocab)));
     P->stat = take((size_t)stats * cdiv(a->vocab, TILE) * sizeof(float4));
     P->keys = take(top ? (size_t)a->rows * (TILE / KEY_COLS) * cdiv(a->vocab, TILE) * sizeof(float2) : 0);
+    P->hshare = take(top ? (size_t)a->rows * 4 : 0);
+    P->wlen = take(top ? (size_t)cdiv(a->vocab, TILE) * (TILE + TILE / KEY_COLS) * 4 : 0);
   }
   P->total = at;
   if (!backward) return;
@@ -1013,6 +1125,32 @@ Few few_args(const muon_linear_ce* a, char* ws) {
   f.dim = (int)a->dim;
   f.status = reinterpret_cast<const unsigned int*>(ws);
   return f;
+}
+
+// The keys' shares and lengths: of bf16 operands as the products read them, of 32-bit ones as they are.
+cudaError_t lengths(const muon_linear_ce* a, const Operand& H, const Operand& W, float share, float* hshare,
+                    float* wlen, float* wgroup, cudaStream_t s) {
+  const bool f32 = a->dtype == MUON_DTYPE_F32;
+  const size_t es = dt_size(a->dtype);
+  Lengths q = {};
+  q.h = f32 ? a->H : H.p;
+  q.w = f32 ? a->W : W.p;
+  q.ldh = f32 ? a->ldh : H.ld;
+  q.ldw = f32 ? a->ldw : W.ld;
+  q.rows = a->rows;
+  q.vocab = a->vocab;
+  q.dim = (int)a->dim;
+  q.hvec = is_aligned(q.h, 16) && q.ldh * es % 16 == 0;
+  q.wvec = is_aligned(q.w, 16) && q.ldw * es % 16 == 0;
+  q.groups = (int)(cdiv(a->vocab, TILE) * (TILE / KEY_COLS));   // (of whole tiles)
+  q.share = share;
+  q.hshare = hshare;
+  q.wlen = wlen;
+  q.wgroup = wgroup;
+  count_launch();
+  const dim3 grid((unsigned)(q.groups + cdiv(a->rows, KEY_COLS)));
+  return f32 ? launch_after(lengths_kernel<float>, grid, dim3(256), 0, s, q)
+             : launch_after(lengths_kernel<bf16>, grid, dim3(256), 0, s, q);
 }
 
 // The last kernel of a forward pass.
@@ -1299,6 +1437,17 @@ extern "C" int muon_linear_logprob_forward(const muon_linear_ce* a, int top, flo
   p.njobs = 1;
   p.tiles = j.tiles;
   const bool promote = P.nterms > 1 || j.nkb > j.seg_kb;
+  if (top) {
+    // roundings on the way of one product: the segment's (four steps of 16 products a K step) and the
+    // take-overs'; for 32-bit operands also the other terms', 2^-7 of the result, and what no term holds
+    const float steps = 4.f * (float)std::min(j.seg_kb, j.nkb) + (float)cdiv(j.nkb, j.seg_kb) + (P.nterms > 1 ? 32.f : 4.f);
+    float *hshare = reinterpret_cast<float*>(w + P.hshare), *wlen = reinterpret_cast<float*>(w + P.wlen);
+    float* wgroup = wlen + (size_t)j.ntiles * TILE;
+    if (lengths(a, H, W, UNIT_TENSOR * steps, hshare, wlen, wgroup, s) != cudaSuccess) return MUON_ERR_CUDA;
+    p.hshare = hshare;
+    p.wlen = wlen;
+    p.wgroup = wgroup;
+  }
   if (launch(p, false, promote, true, s) != cudaSuccess) return MUON_ERR_CUDA;
   return join_rows(a, top, p, 2 * j.ntiles, logprob, entropy, lse, ids, alternatives, s);
 }

@@ -89,13 +89,18 @@ __device__ __forceinline__ float add_four(const float (&x)[4], const float4& y, 
 
 // The products of FEW_AT_ONCE rows of W from v0 on with the R rows of H, summed over the warp:
 // lane l has product l * n / 32 (row of W times R plus row of H) of the n, the first of two
-// where n is 64.
-template <typename T, int R, Read kRead>
-__device__ __forceinline__ float2 products(const Few& p, const float* h, int dp, long long v0, int lane) {
+// where n is 64.  kSquares: lane l also gets the squares' sum of row l / 8 of W.
+template <typename T, int R, Read kRead, bool kSquares>
+__device__ __forceinline__ float2 products(const Few& p, const float* h, int dp, long long v0, int lane, float& squares) {
   constexpr int N = FEW_AT_ONCE * R;
-  float v[N];                                   // (pairs of numbers would take twice the registers)
+  float v[N], sq[FEW_AT_ONCE];                  // (pairs of numbers would take twice the registers)
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
+#pragma unroll
+  for (int i = 0; i < FEW_AT_ONCE; ++i) sq[i] = 0.f;
+  const auto square = [&](int i, const float (&x)[4]) {
+    if constexpr (kSquares) sq[i] = add_four(x, make_float4(x[0], x[1], x[2], x[3]), sq[i]);
+  };
   const T* w[FEW_AT_ONCE];
 #pragma unroll
   for (int i = 0; i < FEW_AT_ONCE; ++i)         // (rows behind the last are the last's; nobody looks at them)
@@ -111,7 +116,10 @@ __device__ __forceinline__ float2 products(const Few& p, const float* h, int dp,
       for (int k = 0; k < V; k += 4) {
         float x[FEW_AT_ONCE][4];
 #pragma unroll
-        for (int i = 0; i < FEW_AT_ONCE; ++i) four_of(q[i], k, x[i], static_cast<const T*>(nullptr));
+        for (int i = 0; i < FEW_AT_ONCE; ++i) {
+          four_of(q[i], k, x[i], static_cast<const T*>(nullptr));
+          square(i, x[i]);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float4 y = *reinterpret_cast<const float4*>(h + r * dp + c + k);
@@ -147,6 +155,7 @@ __device__ __forceinline__ float2 products(const Few& p, const float* h, int dp,
         for (int i = 0; i < FEW_AT_ONCE; ++i) {
           float x[4];
           four_of(q[i], k, x, static_cast<const T*>(nullptr));
+          square(i, x);
 #pragma unroll
           for (int r = 0; r < R; ++r)
             v[i * R + r] = add_four(x, *reinterpret_cast<const float4*>(y0[i] + r * dq + c + k), v[i * R + r]);
@@ -169,14 +178,28 @@ __device__ __forceinline__ float2 products(const Few& p, const float* h, int dp,
 #pragma unroll
         for (int i = 0; i < FEW_AT_ONCE; ++i) x[k][i] = c0 + 32 * k < p.dim ? ld1(w[i] + c0 + 32 * k) : 0.f;
 #pragma unroll
-      for (int k = 0; k < H; ++k)
+      for (int k = 0; k < H; ++k) {
+        if constexpr (kSquares) {
+#pragma unroll
+          for (int i = 0; i < FEW_AT_ONCE; ++i) sq[i] = fmaf(x[k][i], x[k][i], sq[i]);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float y = c0 + 32 * k < p.dim ? h[r * dp + c0 + 32 * k] : 0.f;
 #pragma unroll
           for (int i = 0; i < FEW_AT_ONCE; ++i) v[i * R + r] = fmaf(x[k][i], y, v[i * R + r]);
         }
+      }
     }
+  }
+  if constexpr (kSquares) {
+    const bool a = lane & 16, b = lane & 8;
+    sq[0] = (a ? sq[2] : sq[0]) + __shfl_xor_sync(0xffffffffu, a ? sq[0] : sq[2], 16);
+    sq[1] = (a ? sq[3] : sq[1]) + __shfl_xor_sync(0xffffffffu, a ? sq[1] : sq[3], 16);
+    sq[0] = (b ? sq[1] : sq[0]) + __shfl_xor_sync(0xffffffffu, b ? sq[0] : sq[1], 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sq[0] += __shfl_xor_sync(0xffffffffu, sq[0], o);
+    squares = sq[0];
   }
   // each exchange halves what a lane holds, as long as there is more than one
   int n = N;
@@ -198,10 +221,29 @@ __device__ __forceinline__ float2 products(const Few& p, const float* h, int dp,
   return make_float2(v[0], N > 32 ? v[1 % N] : 0.f);
 }
 
+// The shares of H's rows (in shared memory, each `len` numbers with zeros behind the row's), a warp a row.
+template <typename T>
+__device__ __forceinline__ void write_shares(const Few& p, const T* h, int len, int lane, int warp, float* share) {
+  for (int r = warp; r < p.rows; r += FEW_WARPS) {
+    float s = 0.f, most = 0.f;
+    for (int c = lane; c < len; c += 32) {
+      const float x = ld1(h + (size_t)r * len + c);
+      s = fmaf(x, x, s);
+      most = fmaxf(most, fabsf(x));
+    }
+    s = warp_sum(s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) share[r] = share_of(s, most, p.share);
+  }
+}
+
 // A row's statistic of a block of logits, its keys and its token's logit, by a warp.  z: the row's
-// first of kParts shares of the logits, which lie `apart`.
-template <int kBlock, int kParts>
-__device__ __forceinline__ void write_block(const Few& p, const float* z, int apart, int r, int blk, int lane) {
+// first of kParts shares of the logits, which lie `apart`; share and squares: for the keys,
+// the row's share and kParts shares of the squares of W's rows.
+template <int kBlock, int kParts, bool kKeys>
+__device__ __forceinline__ void write_block(const Few& p, const float* z, int apart, int r, int blk, int lane, float share,
+                                            const float* squares) {
   constexpr int G = kBlock / KEY_COLS;
   const long long b0 = (long long)blk * kBlock;
   float x[G], mx = -INFINITY;
@@ -226,10 +268,14 @@ __device__ __forceinline__ void write_block(const Few& p, const float* z, int ap
   s = warp_sum(s);
   t = warp_sum(t);
   if (lane == 0) p.stat[(size_t)r * p.parts + blk] = make_float4(mx, s, t, 0.f);
-  if (p.keys) {
+  if constexpr (kKeys) {
 #pragma unroll
     for (int j = 0; j < G; ++j) {
-      const float own = __uint_as_float((__float_as_uint(fmaxf(x[j], -0x1.fffffep127f)) & ~KEY_MASK) | (KEY_MASK - lane));
+      float sq = squares[32 * j + lane];
+#pragma unroll
+      for (int i = 1; i < kParts; ++i) sq += squares[i * kBlock + 32 * j + lane];
+      const float most = fmaxf(fmaf(share, length_of(sq), x[j]), -0x1.fffffep127f);
+      const float own = __uint_as_float((__float_as_uint(most) & ~KEY_MASK) | (KEY_MASK - lane));
       float a = own;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -245,9 +291,10 @@ __device__ __forceinline__ void write_block(const Few& p, const float* z, int ap
     if (at == 32 * j + lane && b0 + at < p.vocab) p.zlabel[r] = x[j];
 }
 
-template <typename T, int R, Read kRead, int kBlock>
+template <typename T, int R, Read kRead, int kBlock, bool kKeys>
 __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
   extern __shared__ float few_smem[];
+  __shared__ float share[R], squares[kKeys ? kBlock : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dp = p.dp;
   float* h = few_smem;                          // [R][dp], or the four copies
   float* z = h + (kRead == SHIFTED ? 4 * R * (dp + FEW_REST) : R * dp);   // [R][kBlock]
@@ -255,12 +302,18 @@ __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
   await_previous();
   if constexpr (kRead == SHIFTED) stage_copies<T, R>(p, h, dp + FEW_REST);
   else stage_rows<T, R>(p, h, dp);
+  if constexpr (kKeys) {
+    __syncthreads();
+    write_shares(p, h, kRead == SHIFTED ? dp + FEW_REST : dp, lane, warp, share);
+  }
   for (int blk = blockIdx.x; blk < p.parts; blk += gridDim.x) {
     __syncthreads();                            // h is staged; the last block's z are read
     const long long b0 = (long long)blk * kBlock;
     for (int i = warp * FEW_AT_ONCE; i < kBlock; i += FEW_PIECE) {
       if (b0 + i >= p.vocab) break;
-      const float2 v = products<T, R, kRead>(p, h, dp, b0 + i, lane);
+      float sq = 0.f;
+      const float2 v = products<T, R, kRead, kKeys>(p, h, dp, b0 + i, lane, sq);
+      if (kKeys && lane % 8 == 0) squares[i + lane / 8] = sq;
       constexpr int N = FEW_AT_ONCE * R;
       if constexpr (N > 32) {
         const int at = lane * (N / 32);
@@ -272,7 +325,8 @@ __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
       }
     }
     __syncthreads();
-    for (int r = warp; r < p.rows; r += FEW_WARPS) write_block<kBlock, 1>(p, z + r * kBlock, 0, r, blk, lane);
+    for (int r = warp; r < p.rows; r += FEW_WARPS)
+      write_block<kBlock, 1, kKeys>(p, z + r * kBlock, 0, r, blk, lane, kKeys ? share[r] : 0.f, squares);
   }
 }
 
@@ -283,22 +337,39 @@ __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
 // instruction does not matter as long as H's stands there too: a lane's four pairs are k
 // 2t, 2t + 1 and 2t + 8, 2t + 9 of two of them.  Sums are taken over into fp32 numbers every 128 columns.
 // Short blocks: two warps take 16 of the 32 columns each, of four quarters of the row; long
-// ones: a warp takes 16 of the 128 columns.
+// ones: a warp takes 16 of the 128 columns.  The squares of W's rows (kKeys) are summed 16 pairs at a time in
+// bf16 (within 2^-5, which the share allows for), then in fp32.
 __device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+template <int N>
+__device__ __forceinline__ float squares_of(const uint4 (&q)[N]) {
+  __nv_bfloat162 s[2] = {__floats2bfloat162_rn(0.f, 0.f), __floats2bfloat162_rn(0.f, 0.f)};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[j]);
+      s[j & 1] = __hfma2(x, x, s[j & 1]);
+    }
+  }
+  const __nv_bfloat162 a = s[0], b = s[1];
+  return (__low2float(a) + __high2float(a)) + (__low2float(b) + __high2float(b));
+}
 // A row of H is an odd multiple of 64 bytes long, so that eight lanes' words lie in different banks.
 __host__ __device__ constexpr int mma_stride(int dim) { return (dim + 31) / 32 % 2 ? (dim + 31) / 32 * 32 : (dim + 63) / 32 * 32; }
-template <int R, int kBlock>
+template <int R, int kBlock, bool kKeys>
 __global__ void __launch_bounds__(FEW_THREADS) few_mma_kernel(const Few p) {
   extern __shared__ __align__(16) float few_smem[];
   constexpr int S = kBlock == KEY_COLS ? 4 : 1, ZS = kBlock + 4, STEPS = 4;   // STEPS of 32 columns at a time
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / 4, t = lane % 4, ds = mma_stride(p.dim);
   bf16* h = reinterpret_cast<bf16*>(few_smem);  // [R][ds]
   float* z = reinterpret_cast<float*>(h + R * ds);   // [S][R][ZS]
+  __shared__ float share[R], squares[kKeys ? S * kBlock : 1];
   allow_next();
   await_previous();
   for (int r = 0; r < R; ++r) {
@@ -321,6 +392,10 @@ __global__ void __launch_bounds__(FEW_THREADS) few_mma_kernel(const Few p) {
   const int group = S == 4 ? warp % 2 : warp, part = S == 4 ? warp / 2 : 0;
   const int chunks = (p.dim + 31) / 32, lo = chunks * part / S, hi = chunks * (part + 1) / S;
   const bf16* y = h + g * ds + t * 8;
+  if constexpr (kKeys) {
+    __syncthreads();
+    write_shares(p, h, ds, lane, warp, share);
+  }
   for (int blk = blockIdx.x; blk < p.parts; blk += gridDim.x) {
     __syncthreads();                            // h is staged; the last block's z are read
     const long long v0 = (long long)blk * kBlock + group * 16;
@@ -328,7 +403,7 @@ __global__ void __launch_bounds__(FEW_THREADS) few_mma_kernel(const Few p) {
       // (rows behind the last are the last's; nobody looks at them)
       const bf16* w0 = static_cast<const bf16*>(p.W) + min(v0 + g, p.vocab - 1) * p.ldw + t * 8;
       const bf16* w1 = static_cast<const bf16*>(p.W) + min(v0 + g + 8, p.vocab - 1) * p.ldw + t * 8;
-      float sum[R / 8][4] = {};
+      float sum[R / 8][4] = {}, first = 0.f, last = 0.f;
       for (int k = lo; k < hi; k += STEPS) {
         uint4 a[STEPS], b[STEPS];
 #pragma unroll
@@ -338,6 +413,10 @@ __global__ void __launch_bounds__(FEW_THREADS) few_mma_kernel(const Few p) {
           b[i] = in ? __ldg(reinterpret_cast<const uint4*>(w1 + (k + i) * 32)) : make_uint4(0, 0, 0, 0);
         }
         float d[R / 8][4] = {};
+        if constexpr (kKeys) {
+          first += squares_of(a);
+          last += squares_of(b);
+        }
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
           if (k + i >= hi) break;
@@ -358,9 +437,19 @@ __global__ void __launch_bounds__(FEW_THREADS) few_mma_kernel(const Few p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           z[(part * R + n * 8 + 2 * t + i % 2) * ZS + group * 16 + g + i / 2 * 8] = sum[n][i];
+      if constexpr (kKeys) {
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) {        // (the four lanes of a row)
+          first += __shfl_xor_sync(0xffffffffu, first, o);
+          last += __shfl_xor_sync(0xffffffffu, last, o);
+        }
+        if (t == 0) squares[part * kBlock + group * 16 + g] = first;
+        if (t == 1) squares[part * kBlock + group * 16 + g + 8] = last;
+      }
     }
     __syncthreads();
-    for (int r = warp; r < p.rows; r += FEW_WARPS) write_block<kBlock, S>(p, z + r * ZS, R * ZS, r, blk, lane);
+    for (int r = warp; r < p.rows; r += FEW_WARPS)
+      write_block<kBlock, S, kKeys>(p, z + r * ZS, R * ZS, r, blk, lane, kKeys ? share[r] : 0.f, squares);
   }
 }
 
@@ -409,7 +498,8 @@ __global__ void __launch_bounds__(FEW_THREADS) few_backward_kernel(const Few p) 
     __syncthreads();                            // h is staged; the last piece's g are read
     const long long w0 = v0 + warp * FEW_AT_ONCE;
     if (w0 < p.vocab) {
-      const float z = products<T, R, kVec ? WORDS : ELEMENTS>(p, h, dp, w0, lane).x;
+      float none;
+      const float z = products<T, R, kVec ? WORDS : ELEMENTS, false>(p, h, dp, w0, lane, none).x;
       if (N >= 32 || lane % (32 / N) == 0) {
         const long long v = w0 + mine / R;
         const float d = z - lse;
@@ -509,15 +599,21 @@ template <typename T, Read kRead, int kBlock>
 cudaError_t forward_of(Few& p, cudaStream_t s) {
   int grid = 0;
   const size_t smem = kRead == SHIFTED ? copies_smem(p.rows, p.dim) : forward_smem(p.rows, p.dim);
-  auto go = [&](auto kern) { return run(kern, p, smem, cdiv(p.vocab, kBlock), 1 << 30, &grid, s); };
+  // (a lane's sum of one column in 32, and the tree)
+  p.share = UNIT_FP32 * (float)(cdiv(p.dim, 32) + 16);
+  auto go = [&](auto rows) {
+    constexpr int R = decltype(rows)::value;
+    return p.keys ? run(few_forward_kernel<T, R, kRead, kBlock, true>, p, smem, cdiv(p.vocab, kBlock), 1 << 30, &grid, s)
+                  : run(few_forward_kernel<T, R, kRead, kBlock, false>, p, smem, cdiv(p.vocab, kBlock), 1 << 30, &grid, s);
+  };
   const int R = padded_rows(p.rows);
-  if (R == 1) return go(few_forward_kernel<T, 1, kRead, kBlock>);
+  if (R == 1) return go(std::integral_constant<int, 1>());
   if constexpr (sizeof(T) == 4) {
-    if (R == 4) return go(few_forward_kernel<T, 4, kRead, kBlock>);
-    if (R == 8) return go(few_forward_kernel<T, 8, kRead, kBlock>);
-    if (R == 16) return go(few_forward_kernel<T, 16, kRead, kBlock>);
+    if (R == 4) return go(std::integral_constant<int, 4>());
+    if (R == 8) return go(std::integral_constant<int, 8>());
+    if (R == 16) return go(std::integral_constant<int, 16>());
   }
-  return go(few_forward_kernel<T, 2, kRead, kBlock>);
+  return go(std::integral_constant<int, 2>());
 }
 template <typename T, int kBlock>
 cudaError_t forward_by(Few& p, bool vec, cudaStream_t s) {
@@ -527,8 +623,11 @@ cudaError_t forward_by(Few& p, bool vec, cudaStream_t s) {
     if (vec) {
       int grid = 0;
       const int R = mma_rows(p.rows);
+      // (eight instructions, and a take-over every 128 columns)
+      p.share = 1.02f * UNIT_TENSOR * (float)(cdiv(p.dim, 128) + 16);
       auto go = [&](auto kern) { return run(kern, p, mma_smem(p.rows, p.dim), cdiv(p.vocab, kBlock), 1 << 30, &grid, s); };
-      return R == 8 ? go(few_mma_kernel<8, kBlock>) : go(few_mma_kernel<16, kBlock>);
+      if (p.keys) return R == 8 ? go(few_mma_kernel<8, kBlock, true>) : go(few_mma_kernel<16, kBlock, true>);
+      return R == 8 ? go(few_mma_kernel<8, kBlock, false>) : go(few_mma_kernel<16, kBlock, false>);
     }
     if (copies_smem(p.rows, p.dim) <= FEW_SMEM / 2) return forward_of<T, SHIFTED, kBlock>(p, s);
   }

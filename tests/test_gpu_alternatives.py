@@ -1,4 +1,5 @@
-"""Alternatives where their order is hard to keep: rows of W that are copies of one another.
+"""Alternatives where their order is hard to keep: rows of W that are copies of one another, large
+terms that cancel, entries far below the others.
 
 The logits that rank them are exact to 2^-45 of their largest partial sum; the cases' other
 logits lie much farther apart than that, so that the order in 64 bits is the order."""
@@ -43,3 +44,55 @@ def test_copies_of_a_row_go_by_their_ids(dt, n, d):
         for top in (5, 20):
             ids = mm.muon_linear_logprob_forward(h, w, None, ws, top=top)[3].cpu().numpy()
             assert np.array_equal(ids, ranked(z, top)), (top, int((ids != ranked(z, top)).any(1).sum()))
+
+
+def cancelling(v, d, dt, size, rows, rng):
+    """W whose rows (those of the share `rows`) hold a pair of channels, far apart, that cancel
+    exactly for the h that has one number in both; `size` is the product of one of them."""
+    w = rng.standard_normal((v, d)) * 2 / np.sqrt(d)
+    w[:, [3, d - 5]] = 0.0
+    b = 2.0 ** rng.integers(-1, 2, v) * (1 + rng.integers(0, 64, v) / 64.0) * (rng.random(v) < rows)
+    w[:, 3], w[:, d - 5] = b * np.sqrt(size), -b * np.sqrt(size)
+    return put(w, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [2, 8, 40, 200])
+@pytest.mark.parametrize("rows", [1.0, 0.02])
+def test_terms_that_cancel(dt, n, rows):
+    """Partial sums far above the logits: the first sums' error passes the distance between
+    neighbours, in every row of W or in some of them."""
+    v, d, top = 4096, 520, 8
+    for power in (8, 14, 20):
+        rng = np.random.default_rng(n + power)
+        w, w64 = cancelling(v, d, dt, 4.0 ** (power // 2), rows, rng)
+        h = rng.standard_normal((n, d))
+        h[:, 3] = h[:, d - 5] = 2.0 ** (power // 2)
+        h, h64 = put(h, dt)
+        z = h64 @ w64.T
+        best = -np.sort(-z, 1)[:, :top + 1]
+        partial = (np.abs(h64[:, 3])[:, None] * np.abs(w64[:, 3])).max()
+        assert (best[:, :-1] - best[:, 1:]).min() > 2.0 ** -43 * partial          # (the case is one that can be ranked)
+        ws = mm.alloc_linear_logprob_workspace(n, v, d, TYPES[dt], top=top, backward=False)
+        _, _, lse, ids, alt = mm.muon_linear_logprob_forward(h, w, None, ws, top=top)
+        assert np.array_equal(ids.cpu().numpy(), ranked(z, top)), (power, int((ids.cpu().numpy() != ranked(z, top)).any(1).sum()))
+        # an alternative is its exact logit less lse, rounded once (the exact one to 2^-43 here)
+        off = np.abs(alt.double().cpu().numpy() + lse.double().cpu().numpy()[:, None] - best[:, :top])
+        assert np.all(off <= 2.0 ** -24 * np.abs(alt.double().cpu().numpy()) + 2.0 ** -42 * partial)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [3, 8, 200])
+@pytest.mark.parametrize("low", [-1e4, -1e9, -1e30])
+def test_bias_columns_far_below(dt, n, low):
+    """Entries shut by a large finite number in their row of W, longer by far than the other rows."""
+    v, d, top = 5000, 264, 10
+    rng = np.random.default_rng(n)
+    h = rng.standard_normal((n, d))
+    h[:, -1] = 1.0
+    w = rng.standard_normal((v, d)) * 2 / np.sqrt(d)
+    w[:, -1] = np.where(np.arange(v) % 5 == 2, low, 0.0)
+    (w, w64), (h, h64) = put(w, dt), put(h, dt)
+    ws = mm.alloc_linear_logprob_workspace(n, v, d, TYPES[dt], top=top, backward=False)
+    ids = mm.muon_linear_logprob_forward(h, w, None, ws, top=top)[3].cpu().numpy()
+    assert np.array_equal(ids, ranked(h64 @ w64.T, top))
