@@ -42,15 +42,53 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// The scale of a group whose largest magnitude is `most`, and its reciprocal: both within 2 ulp
-// (a scale is what it is, and codes are of four bits).
+// The scale of a group whose largest magnitude is `most`, rounded to nearest, and its reciprocal within an ulp.
+// The quotient is the product with the constant's reciprocal, corrected once by its exact remainder
+// (Markstein): right for every mantissa; a remainder of an infinity is none.
 __device__ __forceinline__ float2 scale_of(float most) {
-  const float s = max_nan(most * (1.f / 448.f), RMS_LEAST_SCALE);
-  return make_float2(s, __fdividef(1.f, s));
+  constexpr float R = 1.f / 448.f;
+  const float q = most * R, s = fmaf(fmaf(-448.f, q, most), R, q);
+  const float scale = max_nan(most <= 0x1.fffffep127f ? s : most, RMS_LEAST_SCALE);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  return make_float2(scale, inv);
 }
 // Two numbers to the nearest e4m3 codes (448 at most, NaN as NaN).
 __device__ __forceinline__ uint32_t code2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// Of two neighbouring codes (the first the smaller in magnitude) the one nearest to y/s, by the side of
+// their midpoint that y is on: the midpoint has 5 bits, and the sign of y - midpoint s is exact.
+__device__ __forceinline__ uint32_t nearer(uint32_t a, uint32_t b, float y, float s) {
+  if (a == b) return a;
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((a & 0x7Fu) | (b & 0x7Fu) << 8), __NV_E4M3);
+  const __half2 v(h);
+  const float mid = 0.5f * (__low2float(v) + __high2float(v)), d = fmaf(-mid, s, fabsf(y));
+  return d > 0.f || (d == 0.f && !(b & 1u)) ? b : a;
+}
+// The codes nearest to y/s of kPairs pairs, two bytes each, in words.  y times the reciprocal is within 2^-22 of
+// the quotient: where its neighbours 2^-21 below and above have one code, that is the code (all but some
+// 1 of 100000).
+template <int kPairs>
+__device__ __forceinline__ void codes_of(const f32x2* y, const float2& scale, uint32_t* w) {
+  static_assert(kPairs % 2 == 0, "");
+  const f32x2 below = both(scale.y * (1.f - 0x1p-21f)), above = both(scale.y * (1.f + 0x1p-21f));
+#pragma unroll
+  for (int i = 0; i < kPairs; i += 2) {
+    const f32x2 a = mul2(y[i], below), b = mul2(y[i + 1], below), c = mul2(y[i], above), d = mul2(y[i + 1], above);
+    uint32_t lo = code2(lo2(a), hi2(a)) | code2(lo2(b), hi2(b)) << 16;
+    const uint32_t hi = code2(lo2(c), hi2(c)) | code2(lo2(d), hi2(d)) << 16;
+    if (lo != hi) {
+      uint32_t out = 0;
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const f32x2 p = k < 2 ? y[i] : y[i + 1];
+        out |= nearer(lo >> 8 * k & 0xFFu, hi >> 8 * k & 0xFFu, k & 1 ? hi2(p) : lo2(p), scale.x) << 8 * k;
+      }
+      lo = out;
+    }
+    w[i / 2] = lo;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -82,11 +120,7 @@ __device__ __forceinline__ void store_codes(const RmsFwd& p, long long row, int 
   const float2 scale = scale_of(__uint_as_float(most));
   if (!inside) return;
   uint32_t w[V / 4];
-#pragma unroll
-  for (int i = 0; i < V / 4; ++i) {
-    const f32x2 a = mul2(y[2 * i], both(scale.y)), b = mul2(y[2 * i + 1], both(scale.y));
-    w[i] = code2(lo2(a), hi2(a)) | code2(lo2(b), hi2(b)) << 16;
-  }
+  codes_of<V / 2>(y, scale, w);
   uint8_t* o = p.codes + row * p.ldc + c;
   if constexpr (V == 8) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
   else *reinterpret_cast<uint32_t*>(o) = w[0];
@@ -420,11 +454,14 @@ __global__ void __launch_bounds__(512) rms_forward_odd_kernel(const RmsFwd p, in
       most = __reduce_max_sync(0xffffffffu, most);
       const float2 scale = scale_of(__uint_as_float(most));
       if (lane == 0) p.scales[row * p.groups + k] = scale.x;
+      const f32x2 pairs[2] = {make2(v[0], v[1]), make2(v[2], v[3])};
+      uint32_t code;
+      codes_of<2>(pairs, scale, &code);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = k * RMS_GROUP + 32 * j + lane;
         if (c < p.dim) {
-          o[c] = (uint8_t)code2(v[j] * scale.y, 0.f);
+          o[c] = (uint8_t)(code >> 8 * j);
           if (y) st1(y + c, v[j]);
         }
       }
@@ -478,11 +515,14 @@ __global__ void __launch_bounds__(RMS_LOOP_THREADS) rms_forward_loop_kernel(cons
       for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
       const float2 scale = scale_of(most);
       if (lane == 0) p.scales[row * p.groups + g] = scale.x;
+      const f32x2 pairs[2] = {make2(v[0], v[1]), make2(v[2], v[3])};
+      uint32_t code;
+      codes_of<2>(pairs, scale, &code);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = g * RMS_GROUP + 32 * j + lane;
         if (c < p.dim) {
-          p.codes[row * p.ldc + c] = (uint8_t)code2(v[j] * scale.y, 0.f);
+          p.codes[row * p.ldc + c] = (uint8_t)(code >> 8 * j);
           if (p.y) st1(static_cast<T*>(p.y) + row * p.ldy + c, v[j]);
         }
       }
