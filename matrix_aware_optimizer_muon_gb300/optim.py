@@ -44,7 +44,9 @@ class PeriodicMuon:
         dev = self.params[0].device
         self.M = [torch.zeros(p.shape, dtype=torch.float32, device=dev) for p in self.params]
         self.ws = _lib.alloc_workspace([tuple(p.shape) for p in self.params], ns5_mode, device=dev)
-        self.max_grad_norm, self.grad_norm, self._clip_ws = max_grad_norm, None, None
+        # (made here, like ws: a step may run on another stream than the one that is current, whose
+        # memory, freed but still in use there, a workspace made in the step could be)
+        self.max_grad_norm, self.grad_norm, self._clip_ws = max_grad_norm, None, alloc_clip_workspace(dev)
         self.step_count = 0
         # W and M never move, so the C matrix array is built once; each step only
         # points it at that step's gradients (after checking them like the array build does).
@@ -73,8 +75,6 @@ class PeriodicMuon:
                     raise ValueError("auxiliary parameters, and their gradients, are of one dtype")
                 aux = _lib.adamw_array(self.aux, aux_grads, self.aux_m, self.aux_v)
         if self.max_grad_norm is not None:
-            if self._clip_ws is None:
-                self._clip_ws = alloc_clip_workspace(self.ws.device)
             self.grad_norm = muon_clip_grad_norm([*grads, *(aux_grads if self.aux else ())], self.max_grad_norm,
                                                  self._clip_ws, stream=stream)
         br = _lib.periodic_step_prepared(self._arr, self._n, self.step_count, self.ws, self.K, self.gamma, self.mu,
