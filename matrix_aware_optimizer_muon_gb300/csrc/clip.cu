@@ -167,8 +167,21 @@ __global__ void __launch_bounds__(CL_THREADS, CL_NORM_CTAS) clip_norm_kernel(con
   if (threadIdx.x == 0) p.part[blockIdx.x] = p.add ? p.part[blockIdx.x] + acc : acc;
 }
 
+// max_norm / norm as a number that fp32 holds in full and two powers of two, 1 unless the quotient is
+// below 2^-100 (a subnormal factor would have lost its bits, not only where the results are subnormal).
+struct Factor {
+  float f, p[2];
+};
+__device__ __forceinline__ Factor factor_of(double q) {
+  if (!(q < 0x1p-100 && q > 0.0)) return {(float)q, {1.f, 1.f}};
+  int e;
+  const double m = frexp(q, &e);
+  e = max(e, -280);                       // (2^128 times that is no number of fp32 any more)
+  return {(float)m, {ldexpf(1.f, e / 2), ldexpf(1.f, e - e / 2)}};
+}
+
 template <typename T>
-__device__ __forceinline__ void scale_share(const ClipEntry& e, long long v0, float coef) {
+__device__ __forceinline__ void scale_share(const ClipEntry& e, long long v0, const Factor& coef) {
   constexpr int V = 16 / (int)sizeof(T), P = V / 2;
   uint4 q[CL_HELD];
   const bool inside = load_share<T>(e, v0, q);
@@ -178,7 +191,11 @@ __device__ __forceinline__ void scale_share(const ClipEntry& e, long long v0, fl
     f32x2 v[P];
     widen(q[k], v, static_cast<const T*>(nullptr));
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = mul2(v[i], both(coef));
+    for (int i = 0; i < P; ++i) v[i] = mul2(v[i], both(coef.f));
+    if (coef.p[0] != 1.f) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = mul2(mul2(v[i], both(coef.p[0])), both(coef.p[1]));
+    }
     uint4 o;
     if (sizeof(T) == 2)
       o = make_uint4(pack_bf16x2(lo2(v[0]), hi2(v[0])), pack_bf16x2(lo2(v[1]), hi2(v[1])),
@@ -209,7 +226,7 @@ __global__ void __launch_bounds__(CL_THREADS, CL_SCALE_CTAS) clip_scale_kernel(c
   const double norm = sqrt(cta_sum(s, red));
   if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
   if (p.only || norm <= p.max_norm) return;      // a NaN goes on, and makes every gradient NaN
-  const float coef = (float)(p.max_norm / norm);
+  const Factor coef = factor_of(p.max_norm / norm);
   int at = p.n - 1;
   for (int c = p.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
     if (p.e[at].begin > c) at = at > 0 && p.e[at - 1].begin <= c ? at - 1 : entry_of(p, c, 0);

@@ -39,3 +39,22 @@ def test_first_clipped_step_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(opt.grad_norm, one.grad_norm)
     assert all(torch.equal(a, b) for a, b in zip(weights + aux + grads, twins[0] + twins[1] + again))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("size, max_norm", [(1e38, 1.0), (1e38, 1e-3), (1e37, 1e-9), (1e20, 1e-25), (1.0, 1e-38), (1e-3, 1e-30)])
+def test_factors_below_the_smallest_normal_number(dt, size, max_norm):
+    """max_norm / norm down to 2^-150 and below keeps its bits: a clipped number is off by the norm's
+    36 roundings at most (64 squares in fp32), the factor's, the product's and its type's."""
+    rng = np.random.default_rng(1)
+    for n in (63, 4099):
+        g = torch.from_numpy(rng.uniform(-3, 3, n) * size).to(dev(), TYPES[dt])
+        before = g.double().cpu().numpy()
+        norm = np.sqrt((before ** 2).sum())
+        got = mm.muon_clip_grad_norm([g], max_norm, mm.alloc_clip_workspace())
+        assert norm > 3.4028235677973366e38 and np.isinf(got.item()) or abs(got.item() - norm) <= 36 * 2.0 ** -24 * norm
+        want = before * (max_norm / norm)
+        one = 2.0 ** -8 if dt == "bf16" else 2.0 ** -24
+        tiny = 2.0 ** -133 if dt == "bf16" else 2.0 ** -149
+        off = np.abs(g.double().cpu().numpy() - want)
+        assert np.all(off <= (one + 40 * 2.0 ** -24) * np.abs(want) + 1.01 * tiny), float((off / np.abs(want)).max())
