@@ -10,6 +10,15 @@ from .clip import alloc_clip_workspace, muon_clip_grad_norm
 from .head import AdamW8, _on
 
 
+def _write_back(to: torch.Tensor, values: torch.Tensor) -> None:
+    """values into a tensor of their shape, each element of a broadcast one once."""
+    for d in range(to.dim()):
+        if to.stride(d) == 0 and to.shape[d] > 1:
+            to, values = to.narrow(d, 0, 1), values.narrow(d, 0, 1)
+    with torch.no_grad():
+        to.copy_(values)
+
+
 class PeriodicMuon:
     """Periodic Row-wise Muon over a list of 2-D weight tensors (K = 1 is vanilla Muon).
 
@@ -62,6 +71,7 @@ class PeriodicMuon:
             self._arr[i].G = _lib._ptr(g)
             self._arr[i].g_dtype = _lib._dt(g)
         # what cannot be read is refused before anything is enqueued
+        given = aux_grads
         if self.aux:
             if len(aux_grads) != len(self.aux):
                 raise ValueError("one gradient per auxiliary parameter")
@@ -77,6 +87,10 @@ class PeriodicMuon:
         if self.max_grad_norm is not None:
             self.grad_norm = muon_clip_grad_norm([*grads, *(aux_grads if self.aux else ())], self.max_grad_norm,
                                                  self._clip_ws, stream=stream)
+            with _on(stream):
+                for g, copy in zip(given, aux_grads if self.aux else ()):
+                    if copy is not g:
+                        _write_back(g, copy)
         br = _lib.periodic_step_prepared(self._arr, self._n, self.step_count, self.ws, self.K, self.gamma, self.mu,
                                          self.eta, self.lam, self.ns5_mode, stream=stream)
         if self.aux8 is not None:

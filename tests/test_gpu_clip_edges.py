@@ -58,3 +58,23 @@ def test_factors_below_the_smallest_normal_number(dt, size, max_norm):
         tiny = 2.0 ** -133 if dt == "bf16" else 2.0 ** -149
         off = np.abs(g.double().cpu().numpy() - want)
         assert np.all(off <= (one + 40 * 2.0 ** -24) * np.abs(want) + 1.01 * tiny), float((off / np.abs(want)).max())
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_gradients_that_are_not_contiguous_are_clipped_in_place(bits):
+    torch.manual_seed(5)
+    w = [torch.randn(64, 96, device=dev())]
+    aux = [torch.randn(12, 10, device=dev()), torch.randn(40, device=dev()), torch.randn(6, 8, device=dev()), torch.randn(16, device=dev())]
+    opt = mm.PeriodicMuon(w, aux_params=aux, aux_bits=bits, max_grad_norm=0.5)
+    wide = torch.randn(40, 3, device=dev())
+    one = torch.randn(8, device=dev())
+    ga = [torch.randn(10, 12, device=dev()).t(), wide[:, 1], one.expand(6, 8), torch.randn(16, device=dev())]
+    g = [torch.randn(64, 96, device=dev())]
+    before, others = [t.double().clone() for t in g + ga], wide.clone()
+    norm = torch.sqrt(sum(t.square().sum() for t in before)).item()
+    opt.step(g, ga)
+    assert abs(opt.grad_norm.item() - norm) <= 36 * 2.0 ** -24 * norm
+    for t, b in zip(g + ga, before):
+        want = b * (0.5 / norm)
+        assert torch.all((t.double() - want).abs() <= 40 * 2.0 ** -24 * want.abs())
+    assert torch.equal(wide[:, ::2], others[:, ::2])           # its neighbours stay
