@@ -60,6 +60,8 @@ class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
         ctx.set_materialize_grads(False)
+        if residual is not None and residual.shape != x.shape:      # (as rows they might agree)
+            raise ValueError("x and residual must have the same shape and dtype")
         y, rstd, total = head.muon_rmsnorm_forward(_plain_rows(x), weight, None if residual is None else _plain_rows(residual), eps)
         if residual is None:
             ctx.save_for_backward(x, weight, total, rstd)

@@ -357,3 +357,12 @@ def test_second_derivatives_are_refused_not_wrong(plain):
         (g,) = torch.autograd.grad(out, leaf, create_graph=True)
         with pytest.raises(RuntimeError, match="second derivatives"):
             g.sum().backward()
+
+
+@pytest.mark.parametrize("shape", [(3, 2, 12), (6, 12), (1, 6, 12), (2, 3, 1, 12)])
+def test_residuals_of_other_shapes_are_refused(plain, shape):
+    """As many rows of one width are not one shape: the gradient would have x's."""
+    x = torch.randn(2, 3, 12)
+    with pytest.raises(ValueError, match="shape"):
+        functional.rms_norm(x, None, torch.randn(shape))
+    functional.rms_norm(x, None, torch.randn(2, 3, 12))
