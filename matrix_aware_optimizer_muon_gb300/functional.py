@@ -93,6 +93,8 @@ class _LinearLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, w, tokens, ignore_index, top):
         ctx.set_materialize_grads(False)
+        if tokens.shape != h.shape[:-1] and tokens.dim() > 1 and h.dim() > 2:   # (as rows they might agree)
+            raise ValueError("tokens must have h's leading shape, or one of them one dimension of rows")
         rows, flat = _plain_rows(h), tokens.reshape(-1).contiguous()
         plain = _plain_rows(w)
         ws = head.linear_logprob_workspace_for(rows, plain, flat, top, backward=False)
@@ -162,6 +164,7 @@ def rms_norm(x: torch.Tensor, weight=None, residual=None, eps: float = 1e-6):
 
 def linear_logprobs(h: torch.Tensor, w: torch.Tensor, tokens: torch.Tensor, ignore_index: int = -100, top: int = 0):
     """(logprob, entropy) of the softmax of the logits h w^T, which are never kept (h: ... x dim, w:
-    vocab x dim, tokens: ... int64), of the tokens' shape; both 0 where a token is ignore_index.
+    vocab x dim, tokens: ... int64, where either may have its rows in one dimension), of the tokens' shape;
+    both 0 where a token is ignore_index.
     With top > 0 also (ids, alternatives) of the likeliest entries, ... x top, without gradient."""
     return _LinearLogprobs.apply(h, w, tokens, ignore_index, top)

@@ -366,3 +366,17 @@ def test_residuals_of_other_shapes_are_refused(plain, shape):
     with pytest.raises(ValueError, match="shape"):
         functional.rms_norm(x, None, torch.randn(shape))
     functional.rms_norm(x, None, torch.randn(2, 3, 12))
+
+
+def test_tokens_of_another_shape_are_refused(plain):
+    """Tokens of h's leading shape, or either of them flat; as many in another order would be
+    other rows' tokens."""
+    h, w = torch.randn(2, 3, 12), torch.randn(30, 12)
+    tokens = torch.arange(6).view(2, 3)
+    for bad in (tokens.t(), tokens.view(3, 2), tokens.view(1, 6), tokens.view(2, 3, 1)):
+        with pytest.raises(ValueError, match="tokens"):
+            functional.linear_logprobs(h, w, bad)
+    want = functional.linear_logprobs(h, w, tokens)
+    for a, b in ((h.view(6, 12), tokens), (h, tokens.view(6)), (h.view(6, 12), tokens.view(6))):
+        got = functional.linear_logprobs(a, w, b)
+        assert got[0].shape == b.shape and all(torch.equal(p.reshape(-1), q.reshape(-1)) for p, q in zip(got, want))
