@@ -63,17 +63,19 @@ class _RmsNorm(torch.autograd.Function):
         if residual is not None and residual.shape != x.shape:      # (as rows they might agree)
             raise ValueError("x and residual must have the same shape and dtype")
         y, rstd, total = head.muon_rmsnorm_forward(_plain_rows(x), weight, None if residual is None else _plain_rows(residual), eps)
+        ctx.shape, ctx.behind = x.shape, residual is not None
         if residual is None:
-            ctx.save_for_backward(x, weight, total, rstd)
-            ctx.shape = x.shape
+            ctx.save_for_backward(x, weight, rstd, total)
             return y.view(x.shape)
-        ctx.shape, total = x.shape, total.view(x.shape)
-        ctx.save_for_backward(x, weight, total, rstd, residual)
+        # (total, an output, stands for x and the residual in the graph, too)
+        total = total.view(x.shape)
+        ctx.save_for_backward(total, weight, rstd)
         return y.view(x.shape), total
 
     @staticmethod
     def backward(ctx, dy, dtotal=None):
-        x, weight, total, rstd, *residual = ctx.saved_tensors
+        x, weight, rstd, *rows = ctx.saved_tensors
+        total = rows[0] if rows else x
         dw = None
         if dy is None:
             dx = dtotal
@@ -85,8 +87,8 @@ class _RmsNorm(torch.autograd.Function):
                 dx, dw = head.muon_rmsnorm_backward(_plain_rows(dy), rows, weight, rstd, ws,
                                                     None if dtotal is None else _plain_rows(dtotal), weight_grad=want_w)
                 dx = dx.view(ctx.shape)
-        dx, dw = _once((dx, dw), (dy, dtotal, x, weight, *residual))
-        return dx, dw, dx if residual else None, None
+        dx, dw = _once((dx, dw), (dy, dtotal, x, weight))
+        return dx, dw, dx if ctx.behind else None, None
 
 
 class _LinearLogprobs(torch.autograd.Function):

@@ -380,3 +380,26 @@ def test_tokens_of_another_shape_are_refused(plain):
     for a, b in ((h.view(6, 12), tokens), (h, tokens.view(6)), (h.view(6, 12), tokens.view(6))):
         got = functional.linear_logprobs(a, w, b)
         assert got[0].shape == b.shape and all(torch.equal(p.reshape(-1), q.reshape(-1)) for p, q in zip(got, want))
+
+
+def test_a_norm_behind_a_residual_keeps_their_sum_alone(plain):
+    """x and the residual are free after the forward pass: the sum is all the gradient needs."""
+    x, r, w, _, _ = _leaves()
+    kept = []
+
+    def pack(t):
+        kept.append(t)
+        return t
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        y, t = functional.rms_norm(x, w, r)
+    at = {k.untyped_storage().data_ptr() for k in kept}
+    assert not at & {x.untyped_storage().data_ptr(), r.untyped_storage().data_ptr()}
+    assert sum(k.numel() >= x.numel() for k in kept) == 1
+    # and may be written over before the backward pass
+    want = torch.autograd.grad((functional.rms_norm(x, w, r)[0] * y.detach()).sum(), (x, r, w))
+    out = (y * y.detach()).sum()
+    with torch.no_grad():
+        x.zero_(), r.zero_()
+    got = torch.autograd.grad(out, (x, r, w))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
