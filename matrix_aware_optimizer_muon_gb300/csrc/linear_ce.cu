@@ -892,6 +892,12 @@ int split_count(int64_t rows, int64_t dim, int64_t piece, int64_t npairs) {
   return (int)std::min<int64_t>(std::max<int64_t>(1, cdiv(kp, share)), MAX_SPLITS);
 }
 
+// Whether W can be read in 16-byte words.
+bool words_of_w(const muon_linear_ce* a) {
+  const size_t es = dt_size(a->dtype);
+  return is_aligned(a->W, 16) && a->ldw * es % 16 == 0 && a->dim * es % 16 == 0;
+}
+
 // top: -1 for the cross entropy's forward pass, else the log probabilities' with so many
 // alternatives.
 void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
@@ -905,9 +911,12 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
   auto take = [&](size_t bytes) { const size_t p = at; at += up(bytes); return p; };
   // room for H's copy in any case: for the backward pass, and so that a workspace fits
   // whatever H's alignment
-  P->hp = take((size_t)P->parts * a->rows * P->dp * 2);
-  P->wp = P->pack_w ? take((size_t)P->parts * a->vocab * P->dp * 2) : at;
-  const size_t common = at;
+  auto copies = [&] {
+    P->hp = take((size_t)P->parts * a->rows * P->dp * 2);
+    P->wp = P->pack_w ? take((size_t)P->parts * a->vocab * P->dp * 2) : at;
+  };
+  // (few rows' kernels read the operands where they lie, and no rows need nothing)
+  if (top < 0 || (a->rows > 0 && !few_rows(a->rows, a->dim, f32, false, words_of_w(a)))) copies();
   P->zlabel = take((size_t)a->rows * 4);
   if (top < 0) {
     P->part = take((size_t)a->rows * 2 * cdiv(a->vocab, TILE) * sizeof(float2));
@@ -924,7 +933,15 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
   }
   P->total = at;
   if (!backward) return;
-  at = common;
+  at = HEADER;
+  if (top >= 0) {
+    // (for more rows too, so that their workspace serves a few of them)
+    for (int64_t n = 1; n <= 8; n *= 2)
+      if (n < 2 * a->rows && few_rows(n, a->dim, f32, true, false)) P->total = std::max(P->total, at + up(few_bytes(n, a->dim)));
+    if (few_rows(a->rows, a->dim, f32, true, false)) P->few = at;
+    if (a->rows == 0 || P->few) return;
+  }
+  copies();
   const int64_t want = G_BYTES / (2 * P->parts * std::max<int64_t>(a->rows, 1));
   P->piece = std::min(std::max(want / TILE * TILE, MIN_PIECE), cdiv(a->vocab, TILE) * TILE);
   if (const int tiles = (test_flags() / MUON_DEBUG_CE_PIECE) & 255) P->piece = std::min<int64_t>(P->piece, (int64_t)tiles * TILE);
@@ -933,12 +950,6 @@ void make_plan(const muon_linear_ce* a, int backward, CePlan* P, int top = -1) {
   P->piece = cdiv(cdiv(a->vocab, P->npieces), TILE) * TILE;
   P->npieces = cdiv(a->vocab, P->piece);
   P->splits = split_count(a->rows, a->dim, P->piece, 76);
-  if (top >= 0) {
-    // (for more rows too, so that their workspace serves a few of them)
-    for (int64_t n = 1; n <= 8; n *= 2)
-      if (few_rows(n, a->dim, f32, true, false)) P->total = std::max(P->total, common + up(few_bytes(n, a->dim)));
-    if (few_rows(a->rows, a->dim, f32, true, false)) P->few = common;
-  }
   P->g_part = (size_t)a->rows * P->piece;
   for (int i = 0; i < 2; ++i) P->g[i] = P->npieces > 1 || i == 0 ? take(P->parts * P->g_part * 2) : P->g[0];
   P->ldacc = P->dp;
@@ -1228,7 +1239,7 @@ int backward_pass(const muon_linear_ce* a, const RowGrads& rows, void* dH, void*
     f.g_entropy = rows.g_entropy;
     f.dh_part = reinterpret_cast<float*>(w + P.few);
     f.dW = dW;
-    const bool vec = is_aligned(a->W, 16) && a->ldw * es % 16 == 0 && a->dim * es % 16 == 0 && is_aligned(dW, 16);
+    const bool vec = words_of_w(a) && is_aligned(dW, 16);
     return few_backward(f, a->dtype == MUON_DTYPE_F32, vec, dH, s) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
   }
   static thread_local OrderedParams p;
@@ -1319,7 +1330,7 @@ using namespace muon;
 
 extern "C" size_t muon_linear_ce_workspace_size(const muon_linear_ce* a, int backward) {
   if (ce::check(a) != MUON_OK) return (size_t)-1;
-  ce::CePlan P;
+  ce::CePlan P = {};
   ce::make_plan(a, backward, &P);
   return P.total;
 }
@@ -1384,7 +1395,7 @@ extern "C" int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse
 
 extern "C" size_t muon_linear_logprob_workspace_size(const muon_linear_ce* a, int top, int backward) {
   if (ce::check(a) != MUON_OK || top < 0 || top > MUON_LOGPROB_MAX_TOP) return (size_t)-1;
-  ce::CePlan P;
+  ce::CePlan P = {};
   ce::make_plan(a, backward, &P, top);
   return P.total;
 }
@@ -1415,8 +1426,7 @@ extern "C" int muon_linear_logprob_forward(const muon_linear_ce* a, int top, flo
   p.stat = reinterpret_cast<float4*>(w + P.stat);
   p.keys = top ? reinterpret_cast<float2*>(w + P.keys) : nullptr;
   p.zlabel = reinterpret_cast<float*>(w + P.zlabel);
-  const size_t es = dt_size(a->dtype);
-  const bool w_vec = is_aligned(a->W, 16) && a->ldw * es % 16 == 0 && a->dim * es % 16 == 0;
+  const bool w_vec = words_of_w(a);
   Job& j = p.job[0];
   shape(&j, a->rows, a->vocab, a->dim, GROUP_FORWARD);
   if (few_rows(a->rows, a->dim, a->dtype == MUON_DTYPE_F32, false, w_vec)) {

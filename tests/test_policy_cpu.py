@@ -403,3 +403,27 @@ def test_a_norm_behind_a_residual_keeps_their_sum_alone(plain):
         x.zero_(), r.zero_()
     got = torch.autograd.grad(out, (x, r, w))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def _workspace_size(rows, vocab, dim, f32, top, backward, ldw=None):
+    a = head.MuonLinearCe(None, None, None, rows, vocab, dim, dim, ldw or dim, 0 if f32 else 1, -100)
+    return head._logprob_workspace_size(a, top, backward)
+
+
+def test_a_few_rows_need_no_copy_of_w(lib):
+    """Their kernels read W where it lies, in any type and alignment."""
+    v, d = 32768, 1536
+    for rows in (1, 8):
+        assert _workspace_size(rows, v, d, True, 8, False) < 4 << 20 < v * d
+        assert _workspace_size(rows, v, d, True, 8, True) < 48 << 20        # shares of dH, a CTA each
+    assert _workspace_size(2, v, d, False, 8, False, ldw=d + 3) < 4 << 20
+    assert _workspace_size(40, v, d, True, 8, False) > 6 * v * d            # (by tiles: three parts of W)
+
+
+def test_a_workspace_for_more_rows_is_no_smaller(lib):
+    for f32 in (False, True):
+        for v, d in ((900, 96), (50257, 1536), (1000, 4096), (128, 40)):
+            for top in (0, 4):
+                for backward in (False, True):
+                    sizes = [_workspace_size(n, v, d, f32, top, backward) for n in (1, 2, 3, 4, 5, 8, 9, 16, 17, 33, 64)]
+                    assert sizes == sorted(sizes), (f32, v, d, top, backward, sizes)
