@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) logprob_kernel(const LogprobR
 constexpr int TOP_MANY = 128, TOP_FEW = 512, TOP_FEW_ROWS = 152;
 constexpr int TOP_CANDIDATES = 512;
 constexpr int TOP_WHOLE = 14;                // groups taken whole
-constexpr float TOP_MARGIN = 0x1p-10f;
+constexpr float TOP_MARGIN = 0x1p-10f, TOP_LEAST_MARGIN = 1e-18f;   // (rows of zeros: above what the least length makes of them)
 // A bound may be above its key by this share of it (twice 31 ulp of the column's bits, a rounding).
 constexpr float KEY_SHARE = 0x1p-16f, KEY_LEAST = 1e-30f;
 constexpr float MASKED = -0x1p120f;          // logits down here are masks, of the type's lowest value or less
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 8) top_ker
   }
   __syncthreads();
   const float bound = sh.bound;
-  float least = bound - (TOP_MARGIN * fmaxf(fabsf(all.m), bound == -INFINITY ? 0.f : fabsf(bound)) + KEY_LEAST);
+  float least = bound - (TOP_MARGIN * fmaxf(fabsf(all.m), bound == -INFINITY ? 0.f : fabsf(bound)) + TOP_LEAST_MARGIN);
   const T* h = static_cast<const T*>(p.H) + r * p.ldh;
   // 2. candidates
   auto choose = [&](float a, float b, int g) {
@@ -773,14 +773,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 8) top_ker
       return;
     }
   }
-  // every group against the best so far, KEY_COLS columns at a time
-  for (; walks > 0; --walks) {
-    int kept = 0;
-    double worst = -INFINITY;      // of the kept, when there are `top`
+  // every group against the best so far, KEY_COLS columns at a time; a second walk goes on with the
+  // keys that the first left out
+  int kept = 0;
+  double worst = -INFINITY;        // of the kept, when there are `top`
+  for (float above = INFINITY; walks > 0; --walks) {
     __syncthreads();
     for (int g = 0; g < groups; ++g) {
       const float k = keys[g].x;   // (the same for every thread)
-      if (!(k >= least && k > MASKED) || (double)k + (KEY_SHARE * fabsf(k) + KEY_LEAST) < worst) continue;
+      if (!(k >= least && k > MASKED) || k >= above || (double)k + (KEY_SHARE * fabsf(k) + KEY_LEAST) < worst) continue;
       const long long c = (long long)g * KEY_COLS + t;
       if (t < KEY_COLS) sh.id[t] = c < p.vocab ? (int)c : -1;
       if (t < kept) {
@@ -796,6 +797,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == TOP_FEW ? 1 : 8) top_ker
       __syncthreads();
     }
     if (walks == 1 || enough()) break;
+    above = least;
     least = lower();
   }
   for (int i = t; i < top; i += TOP_THREADS) {
