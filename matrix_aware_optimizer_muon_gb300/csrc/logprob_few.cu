@@ -225,13 +225,20 @@ __device__ __forceinline__ float2 products(const Few& p, const float* h, int dp,
 template <typename T>
 __device__ __forceinline__ void write_shares(const Few& p, const T* h, int len, int lane, int warp, float* share) {
   for (int r = warp; r < p.rows; r += FEW_WARPS) {
-    float s = 0.f, most = 0.f;
-    for (int c = lane; c < len; c += 32) {
-      const float x = ld1(h + (size_t)r * len + c);
-      s = fmaf(x, x, s);
-      most = fmaxf(most, fabsf(x));
+    constexpr int V = 16 / (int)sizeof(T);      // (a row's length here is a multiple of that)
+    f32x2 sums = both(0.f);
+    float most = 0.f;
+#pragma unroll 4
+    for (int c = lane * V; c < len; c += 32 * V) {
+      f32x2 x[V / 2];
+      widen_word(*reinterpret_cast<const uint4*>(h + (size_t)r * len + c), x, static_cast<const T*>(nullptr));
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        sums = fma2(x[i], x[i], sums);
+        most = fmaxf(most, fmaxf(fabsf(lo2(x[i])), fabsf(hi2(x[i]))));
+      }
     }
-    s = warp_sum(s);
+    const float s = warp_sum(lo2(sums) + hi2(sums));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     if (lane == 0) share[r] = share_of(s, most, p.share);
@@ -293,7 +300,7 @@ __device__ __forceinline__ void write_block(const Few& p, const float* z, int ap
 
 template <typename T, int R, Read kRead, int kBlock, bool kKeys>
 __global__ void __launch_bounds__(FEW_THREADS) few_forward_kernel(const Few p) {
-  extern __shared__ float few_smem[];
+  extern __shared__ __align__(16) float few_smem[];
   __shared__ float share[R], squares[kKeys ? kBlock : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dp = p.dp;
   float* h = few_smem;                          // [R][dp], or the four copies
@@ -468,7 +475,7 @@ template <typename T> __device__ __forceinline__ void store_columns(T* p, const 
 // W's second read of a piece comes from L2.
 template <typename T, int R, bool kVec>
 __global__ void __launch_bounds__(FEW_THREADS) few_backward_kernel(const Few p) {
-  extern __shared__ float few_smem[];
+  extern __shared__ __align__(16) float few_smem[];
   __shared__ __align__(16) float g[FEW_PIECE][R < 4 ? 4 : R];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dp = p.dp;
   float* h = few_smem;                          // [R][dp]
