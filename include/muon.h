@@ -345,8 +345,10 @@ int muon_linear_ce_backward(const muon_linear_ce* a, const float* lse, const flo
  * lowest value), are masked entries: they are no alternatives, and places without one hold
  * -1 and minus infinity.  A row of nothing but minus infinities has lse minus infinity,
  * logprob and entropy NaN and no alternatives; a NaN or +Inf logit makes the row's lse,
- * logprob, entropy and alternatives NaN and its ids -1.  Logits are summed as for the cross entropy; those near the top are summed
- * again, to 2^-45, and ranked by that.  logprob, entropy, lse
+ * logprob, entropy and alternatives NaN and its ids -1.  Logits are summed as for the cross
+ * entropy.  Those that can be among the largest, by a bound on their error (a share of the
+ * lengths of their rows of H and W, so that terms that cancel are allowed for), are summed again, to 2^-45 of their
+ * largest partial sum, and ranked by that.  logprob, entropy, lse
  * and alternatives are device fp32, ids device int64.  logprob may be NULL without tokens,
  * ids and alternatives with top == 0. */
 #define MUON_LOGPROB_MAX_TOP 32
@@ -377,8 +379,8 @@ int muon_linear_logprob_backward(const muon_linear_ce* a, const float* lse, cons
  * where total is not; other overlaps are not allowed.  rstd (fp32, one a row) may be NULL.
  * With codes, y is also written in 8 bits (y itself may then be NULL): for each row and
  * MUON_RMS_GROUP columns (the last group may be shorter) a scale
- *   s = max(max|y|/448, 2^-100)   (fp32, rows x ceil(dim/128), contiguous)
- * and e4m3 codes of y/s, rounded to nearest, ties to even: code*s stands for y.  A NaN
+ *   s = max(max|y|/448, 2^-100)   (fp32, rounded to nearest; rows x ceil(dim/128), contiguous)
+ * and e4m3 codes of y/s, the exact quotient rounded to nearest, ties to even: code*s stands for y.  A NaN
  * among a group's y makes its scale and codes NaN.  Arithmetic is fp32, with one rounding
  * of y.  eps >= 0; rows and dim at most 2^30, dim >= 1; rows == 0 is a no-op. */
 #define MUON_RMS_GROUP 128

@@ -7,7 +7,7 @@
 // another, and returns at once where nothing is to be scaled.
 //
 // Measured: 340 M bf16 elements in 48 tensors, clipped, 311 to 334 us (three passes over 680 MB at
-// 6.1 to 6.6 TB/s; the norm alone 115); 38.7 M fp32 and 37 k bf16 elements 73 us; 48 tensors of
+// 6.1 to 6.6 TB/s; the norm alone 115); 38.7 M fp32 and 37 k bf16 elements 73 to 78 us; 48 tensors of
 // 1536 fp32 elements 8 us on the GPU and 41 with the host's side.  Measured and not kept: loads and stores
 // marked as read once (332 to 340), CTAs of 512 threads (338), chunks of 16 KB (339), six
 // CTAs an SM; walking the second pass forwards costs 3 us.

@@ -19,9 +19,10 @@
 // that bring operands into a layout TMA can read.
 //
 // Log probabilities measured: 8192 x 2560 x 131072 bf16 forward 3.1 to 3.3 ms without
-// alternatives (1.66 to 1.77 PFLOP/s), 3.56 with 8, backward 10.6; 1021 x 1536 x 50257 bf16
-// 115 and 150 us; 8 x 1536 x 32768 bf16 21 and 28 (in a graph).  Alternatives cost the
-// product's epilogue 7% (their keys) and their kernel 8 us for 8 rows, 25 for 1021.
+// alternatives (1.66 to 1.77 PFLOP/s), 3.6 to 3.7 with 8, backward 10.5; 1021 x 1536 x 50257 bf16
+// 119 and, with 5, 178 us; 8 x 1536 x 32768 bf16 25 and 35.  Alternatives cost the product's
+// epilogue 7% (their keys), the lengths of W's rows a pass over W (26 us for 154 MB), and their
+// kernel 8 us for 8 rows, 25 for 1021.
 #include <algorithm>
 #include <cmath>
 #include <cstring>

@@ -661,8 +661,8 @@ cudaError_t backward_of(Few& p, T* dH, cudaStream_t s) {
 // Up to how many rows this is the faster way (microseconds here and by tiles, 32768 x 1536):
 // fp32 forward 16 rows 98 and 203, 8 rows 58 and 199, backward 4 rows 116 and 431, 8 rows 145 and
 // 422; bf16 backward 1 row 66 and 98, 4 rows 74 and 99, 8 rows 118 and 98; bf16 forward in words 8 rows 21 and
-// 29, with 8 alternatives 28 and 45, 16 rows 29 and 29, 35 and 47, 24 rows 51 and 30; of 131072 x 2560 8 rows 126 and
-// 128.  Longer rows leave an SM fewer warps (32768 x 4096, 8 rows 74 and 61): tiles.
+// 29, with 8 alternatives (where tiles read W once more for its rows' lengths, and these sum their squares on
+// the way) 36 and 62, 16 rows 29 and 29, 45 and 62, 24 rows 51 and 30; of 131072 x 2560 8 rows 122 and 128.  Longer rows leave an SM fewer warps (32768 x 4096, 8 rows 74 and 61): tiles.
 // bf16 rows off the words: 1 row of 50257 x 2501 57 and 150, 4 rows have no kernel here.
 bool few_rows(int64_t rows, int64_t dim, bool f32, bool backward, bool vec) {
   if (rows < 1 || dim >= (1 << 20)) return false;

@@ -8,8 +8,11 @@
 // Bandwidth-bound.  Measured, of a copy's 6.68 TB/s: 32768 x 1536 bf16 with a residual, forward
 // with the output in 8 bits 59 us (6.0 TB/s), backward with the weight's gradient 68 us (5.9; the
 // column sums' kernel 4 of them); 32768 x 1537 bf16, rows off every 16-byte boundary, 85 and 87 us (4.7),
-// in 8 bits 142 (2.5); 5003 x 1537 fp32 backward 24.7 us (3.7).  What bounds the odd ones is
-// instructions: windows, masks and, in 8 bits, elements through shared memory.
+// in 8 bits 150 (2.4); 32768 x 1536 fp32 with a residual, forward 120 us (6.7), in 8 bits 101 (6.5),
+// backward 124 (6.5); 5003 x 1537 fp32 forward 32 us (3.8), backward 24.6 (3.7).  What bounds the odd bf16
+// rows is instructions: windows, masks and, in 8 bits, elements through shared memory; the odd fp32
+// ones waits: a chain of copy, barrier and sum for each row, 8 rows a CTA, with 39% of the issue slots
+// and 37% of DRAM's time in use.
 #include <algorithm>
 #include <cmath>
 #include <cuda_fp8.h>
