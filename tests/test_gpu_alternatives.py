@@ -96,3 +96,36 @@ def test_bias_columns_far_below(dt, n, low):
     ws = mm.alloc_linear_logprob_workspace(n, v, d, TYPES[dt], top=top, backward=False)
     ids = mm.muon_linear_logprob_forward(h, w, None, ws, top=top)[3].cpu().numpy()
     assert np.array_equal(ids, ranked(h64 @ w64.T, top))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n, v, d", [(160, 70001, 40), (20, 270000, 24), (3, 270000, 24), (153, 33, 8), (200, 481, 72), (5, 481, 72)])
+def test_vocabularies_of_all_sizes(dt, n, v, d):
+    """More groups of columns than a CTA's threads hold, and fewer than it has threads; long rows, rows of
+    zeros and a padded end among W's."""
+    rng = np.random.default_rng(v + n)
+    w = rng.standard_normal((v, d)) * 2 / np.sqrt(d)
+    w[rng.integers(0, v, max(1, v // 50))] *= 30.0
+    w[rng.integers(0, v, max(1, v // 50))] = 0.0
+    w[v - v // 10:] *= 0.1
+    (w, w64), (h, h64) = put(w, dt), put(rng.standard_normal((n, d)), dt)
+    z = h64 @ w64.T
+    for top in (1, 8, 32):
+        ws = mm.alloc_linear_logprob_workspace(n, v, d, TYPES[dt], top=top, backward=False)
+        ids = mm.muon_linear_logprob_forward(h, w, None, ws, top=top)[3].cpu().numpy()
+        part = np.argpartition(-z, min(4 * top + 8, v - 1), 1)[:, :4 * top + 8]
+        part.sort(1)
+        at = ranked(np.take_along_axis(z, part, 1), top)
+        assert np.array_equal(ids, np.take_along_axis(part, at, 1))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [4, 170])
+@pytest.mark.parametrize("scale_h, scale_w", [(1e-12, 1.0), (1e12, 1e-12), (1e-9, 1e-9), (1e15, 1e10), (1.0, 1e-20)])
+def test_rows_of_all_lengths(dt, n, scale_h, scale_w):
+    v, d, top = 3000, 200, 6
+    rng = np.random.default_rng(n)
+    (w, w64), (h, h64) = put(rng.standard_normal((v, d)) * scale_w, dt), put(rng.standard_normal((n, d)) * scale_h, dt)
+    ws = mm.alloc_linear_logprob_workspace(n, v, d, TYPES[dt], top=top, backward=False)
+    _, _, lse, ids, _ = mm.muon_linear_logprob_forward(h, w, None, ws, top=top)
+    assert torch.isfinite(lse).all() and np.array_equal(ids.cpu().numpy(), ranked(h64 @ w64.T, top))
