@@ -380,7 +380,7 @@ int muon_linear_logprob_backward(const muon_linear_ce* a, const float* lse, cons
  * With codes, y is also written in 8 bits (y itself may then be NULL): for each row and
  * MUON_RMS_GROUP columns (the last group may be shorter) a scale
  *   s = max(max|y|/448, 2^-100)   (fp32, rounded to nearest; rows x ceil(dim/128), contiguous)
- * and e4m3 codes of y/s, the exact quotient rounded to nearest, ties to even: code*s stands for y.  A NaN
+ * and e4m3 codes of the fp32 quotient y/s, rounded to nearest, ties to even: code*s stands for y.  A NaN
  * among a group's y makes its scale and codes NaN.  Arithmetic is fp32, with one rounding
  * of y.  eps >= 0; rows and dim at most 2^30, dim >= 1; rows == 0 is a no-op. */
 #define MUON_RMS_GROUP 128

@@ -60,18 +60,24 @@ __device__ __forceinline__ float2 scale_of(float most) {
 __device__ __forceinline__ uint32_t code2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
-// Of two neighbouring codes (the first the smaller in magnitude) the one nearest to y/s, by the side of
-// their midpoint that y is on: the midpoint has 5 bits, and the sign of y - midpoint s is exact.
+// Of two neighbouring codes (the first the smaller in magnitude) the one nearest to the fp32 quotient y/s.  That
+// is their midpoint, and the even code is taken, where y/s is within half an ulp of it; else it is
+// on y's side.  The midpoint has 5 bits: y - midpoint s is exact, and so are the comparisons.
 __device__ __forceinline__ uint32_t nearer(uint32_t a, uint32_t b, float y, float s) {
   if (a == b) return a;
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((a & 0x7Fu) | (b & 0x7Fu) << 8), __NV_E4M3);
   const __half2 v(h);
   const float mid = 0.5f * (__low2float(v) + __high2float(v)), d = fmaf(-mid, s, fabsf(y));
-  return d > 0.f || (d == 0.f && !(b & 1u)) ? b : a;
+  const float power = __uint_as_float(__float_as_uint(mid) & 0x7F800000u), half = power * 0x1p-24f * s;
+  if (d > half) return b;
+  if (d < (mid == power ? -0.5f * half : -half)) return a;   // (numbers below a power of two lie closer)
+  return b & 1u ? a : b;
 }
-// The codes nearest to y/s of kPairs pairs, two bytes each, in words.  y times the reciprocal is within 2^-22 of
-// the quotient: where its neighbours 2^-21 below and above have one code, that is the code (all but some
-// 1 of 100000).
+// The codes nearest to y/s of kPairs pairs, two bytes each, in words; the quotient is rounded to fp32 first.  (bf16 numbers
+// and weights make quotients that are midpoints of two codes, up to the roundings of y and s, of some 1 in
+// 5000: the quotient's own rounding makes most of them midpoints again, which go to the even code.)
+// y times the reciprocal is within 2^-22 of the quotient: where its neighbours 2^-21 below and above have one
+// code, that is the code.
 template <int kPairs>
 __device__ __forceinline__ void codes_of(const f32x2* y, const float2& scale, uint32_t* w) {
   static_assert(kPairs % 2 == 0, "");

@@ -78,3 +78,36 @@ def test_gradients_that_are_not_contiguous_are_clipped_in_place(bits):
         want = b * (0.5 / norm)
         assert torch.all((t.double() - want).abs() <= 40 * 2.0 ** -24 * want.abs())
     assert torch.equal(wide[:, ::2], others[:, ::2])           # its neighbours stay
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_clipped_step_captured_first(bits):
+    """The first step of an optimizer inside a capture, its gradients changed between replays; the norm on
+    the device is the replayed step's."""
+    def fresh():
+        torch.manual_seed(6)
+        return [torch.randn(64, 96, device=dev())], [torch.randn(12, 10, device=dev()), torch.randn(40, device=dev())]
+
+    (w1, a1), (w2, a2) = fresh(), fresh()
+    one = mm.PeriodicMuon(w1, aux_params=a1, aux_bits=bits, max_grad_norm=0.5)
+    two = mm.PeriodicMuon(w2, aux_params=a2, aux_bits=bits, max_grad_norm=0.5)
+    g, ga = [torch.randn(64, 96, device=dev())], [torch.randn(10, 12, device=dev()).t(), torch.randn(40, device=dev())]
+    keep = [t.clone() for t in g + ga]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one.step(g, ga)
+    for scale in (1.0, 3.0):
+        for t, k in zip(g + ga, keep):
+            t.copy_(k * scale)
+        for p, q in zip(w1 + a1 + one.M + one.aux_m + one.aux_v, w2 + a2 + two.M + two.aux_m + two.aux_v):
+            p.copy_(q)
+        if bits == 8:
+            one.aux8.load_state_dict(two.aux8.state_dict())
+        two.step_count = 0
+        h, ha = [t.clone() for t in g], [ga[0].t().clone().t(), ga[1].clone()]
+        graph.replay()
+        two.step(h, ha)
+        torch.cuda.synchronize()
+        assert torch.equal(one.grad_norm, two.grad_norm)
+        assert all(torch.equal(p, q) for p, q in zip(w1 + a1 + g + ga, w2 + a2 + h + ha))

@@ -1,9 +1,6 @@
 """The 8-bit output of RMS norm to the last bit: given y, a scale is the fp32 number nearest to
-max|y|/448 (2^-100 at least), and a code the e4m3 number nearest to the exact quotient y/s, ties
-to even.
-
-A quotient of two numbers of 24 bits that is not itself a midpoint of two e4m3 numbers (5 bits) is
-at least 2^-30 of itself away from any, so that its rounding to 53 bits does not change its code."""
+max|y|/448 (2^-100 at least), and a code the e4m3 number nearest to the fp32 quotient y/s, ties
+to even."""
 import numpy as np
 import pytest
 import torch
@@ -26,7 +23,8 @@ def codes_of(y):
     p = np.zeros((n, k * 128))
     p[:, :d] = y
     scale = np.maximum((np.abs(p.reshape(n, k, 128)).max(2) / 448.0).astype(np.float32), np.float32(2.0 ** -100)).astype(np.float64)
-    return ref.e4m3(p / np.repeat(scale, 128, 1))[:, :d], scale
+    q = p.astype(np.float32) / np.repeat(scale, 128, 1).astype(np.float32)
+    return ref.e4m3(q)[:, :d], scale
 
 
 def next_to_midpoints(n, d, rng):
